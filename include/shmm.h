@@ -412,6 +412,90 @@ shmm_status_t shmm_layernorm_all_gather(const shmm_plan_t *plan, const void *con
                                         const float *gamma, const float *beta, float eps,
                                         void *const *full_r, void *stream);
 
+/* Layer normalisation for training: shmm_layernorm's y together with what its
+ * gradient needs, and with a residual added on the way (the step between two
+ * blocks: the running sum of the block outputs, then its normalisation).
+ *   t = x, or x + residual rounded to dtype; mean and biased variance of each
+ *   row of t in fp32; rstd = 1 / sqrt(var + eps);
+ *   y = (t - mean) * rstd * gamma + beta, rounded once to dtype.
+ * The statistics are those of the rounded sum, which is what
+ * shmm_layernorm_backward reads back.
+ *   x, y         [rows, cols], dtype, 16-byte aligned; y may be x
+ *   residual     [rows, cols] or NULL
+ *   total        out: t; required with a residual (it may be x or residual,
+ *                not y), NULL without
+ *   gamma, beta  fp32 arrays of `cols`
+ *   mean, rstd   out: fp32 arrays of `rows`
+ * Rows of up to 8192 columns stay in registers; wider ones are read three
+ * times.  No rows or no columns: nothing is written.
+ * Errors: NULL, ALIGN, SHAPE, DTYPE, UNSUPPORTED (total), CUDA. */
+shmm_status_t shmm_layernorm_forward(int64_t rows, int64_t cols, shmm_dtype_t dtype, const void *x,
+                                     const void *residual, const float *gamma, const float *beta, float eps,
+                                     void *total, void *y, float *mean, float *rstd, void *stream);
+
+/* Workspace of shmm_layernorm_backward (and, with the rows of every rank's
+ * block added up, of shmm_layernorm_all_gather_backward), in bytes: at most
+ * 304 partial rows of dgamma and dbeta.  Host only.  Errors: NULL, SHAPE. */
+shmm_status_t shmm_layernorm_backward_workspace_size(int64_t rows, int64_t cols, size_t *bytes);
+
+/* Gradient of shmm_layernorm_forward.  With xh = (x - mean) * rstd and
+ * w = dy * gamma, sums over a row's n columns, everything in fp32:
+ *   dx = rstd * (w - sum(w)/n - xh * sum(w * xh)/n) (+ residual_grad),
+ *   rounded once to dtype;
+ *   dgamma = sum over rows of dy * xh, dbeta = sum over rows of dy.
+ *   dy             [rows, cols], dtype, 16-byte aligned
+ *   x              [rows, cols]: the rows that were normalised (total, with a
+ *                  residual)
+ *   mean, rstd     as shmm_layernorm_forward left them
+ *   residual_grad  [rows, cols] or NULL: the gradient that reaches the
+ *                  normalised rows past the normalisation
+ *   dx             out; may be dy, x or residual_grad
+ *   dgamma, dbeta  out: fp32 arrays of `cols`, overwritten (zeros when there
+ *                  are no rows)
+ *   workspace      device memory of >= shmm_layernorm_backward_workspace_size
+ *                  bytes, 256-byte aligned; every byte read is written first,
+ *                  so nothing in it needs to start at zero, and calls that
+ *                  overlap on the GPU need one each
+ * The sums over rows have a fixed order: one input gives one result.
+ * Errors: NULL, ALIGN, SHAPE, DTYPE, NOMEM (workspace), CUDA. */
+shmm_status_t shmm_layernorm_backward(int64_t rows, int64_t cols, shmm_dtype_t dtype, const void *dy, const void *x,
+                                      const float *mean, const float *rstd, const float *gamma,
+                                      const void *residual_grad, void *dx, float *dgamma, float *dbeta,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* shmm_layernorm_all_gather for training: the same y on every member, and
+ * each owner block's statistics.
+ *   mean_r[N], rstd_r[N]  out: fp32 arrays of the rank's C_REDUCED rows
+ * Errors: those of shmm_layernorm_all_gather. */
+shmm_status_t shmm_layernorm_all_gather_forward(const shmm_plan_t *plan, const void *const *shard_r,
+                                                const float *gamma, const float *beta, float eps,
+                                                void *const *full_r, float *const *mean_r, float *const *rstd_r,
+                                                void *stream);
+
+/* Gradient of shmm_layernorm_all_gather_forward: the adjoint of the
+ * all-gather (a reduce-scatter of the members' gradients, each row to its
+ * owner) and of the normalisation in one pass.  Row i of an owner block takes
+ * dy = the fp32 sum, in ascending rank order, of that row in every member's
+ * dfull_r; the rest is shmm_layernorm_backward.  dgamma and dbeta are summed
+ * over the rows of every rank's block: where ranks hold copies of a block
+ * (axes the result is replicated over), each copy counts, as the sum of the
+ * ranks' own gradients does.
+ *   grad_dtype   of dfull_r: SHMM_F32 (partial sums as shmm_local_matmul
+ *                leaves them) or the plan's out_dtype
+ *   dfull_r[N]   in: box SHMM_TENSOR_C
+ *   shard_r[N]   in: box SHMM_TENSOR_C_REDUCED, the rows that were normalised
+ *   dshard_r[N]  out: box SHMM_TENSOR_C_REDUCED, out_dtype; may be shard_r
+ *   workspace    shmm_layernorm_backward_workspace_size(nranks * block rows,
+ *                cols) bytes
+ * Errors: NULL, ALIGN, SHAPE, DTYPE (grad_dtype), NOMEM, UNSUPPORTED (no row
+ * all-gather), CUDA. */
+shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_dtype_t grad_dtype,
+                                                 const void *const *dfull_r, const void *const *shard_r,
+                                                 const float *const *mean_r, const float *const *rstd_r,
+                                                 const float *gamma, void *const *dshard_r, float *dgamma,
+                                                 float *dbeta, void *workspace, size_t workspace_bytes,
+                                                 void *stream);
+
 /* ---- planner: which operand to move ("Sharded matmuls and collectives on
  * a torus", Which operand to move: the ICI roofline) ---------------------- */
 

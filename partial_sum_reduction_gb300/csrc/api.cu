@@ -635,6 +635,290 @@ shmm_status_t shmm_layernorm_all_gather(const shmm_plan_t *p, const void *const 
     return SHMM_OK;
 }
 
+// Runs an entry point's body; no C++ exception (a host allocation that
+// failed) leaves a C entry.
+extern "C++" {
+template <typename F>
+static shmm_status_t guarded(F body) {
+    try {
+        return body();
+    } catch (...) {
+        return SHMM_ERR_NOMEM;
+    }
+}
+}
+
+// Arguments that a layer normalisation's training calls share: sizes, eps
+// and alignment of what is not NULL.
+static shmm_status_t norm_sizes(const char *fn, int64_t rows, int64_t cols, shmm_dtype_t dtype) {
+    if (dtype != SHMM_F32 && dtype != SHMM_BF16) return fail(SHMM_ERR_DTYPE, std::string(fn) + ": bad dtype");
+    if (rows < 0 || cols < 0) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": negative size");
+    if (cols >= ((int64_t)1 << 31)) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": cols must be below 2^31");
+    if (rows && cols > (((int64_t)1 << 60) / rows))
+        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": rows * cols exceeds 2^60");
+    return SHMM_OK;
+}
+
+static shmm_status_t check_ptr(const char *fn, const void *p, const char *what, size_t align) {
+    if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": " + what + " is NULL");
+    if (reinterpret_cast<uintptr_t>(p) % align)
+        return fail(SHMM_ERR_ALIGN, std::string(fn) + ": " + what + " is not " + std::to_string(align) +
+                                        "-byte aligned");
+    return SHMM_OK;
+}
+
+// Statistics of a row gather's blocks: one fp32 array per rank.
+static shmm_status_t check_stats(const shmm_plan_t *p, const float *const *arr, const char *fn, const char *what) {
+    if (!arr) return fail(SHMM_ERR_NULL, std::string(fn) + ": " + what + " array is NULL");
+    for (int r = 0; r < p->nranks; ++r) {
+        if (p->boxes[SHMM_TENSOR_C_REDUCED][r].numel() == 0) continue;
+        const shmm_status_t st =
+            check_ptr(fn, arr[r], (std::string(what) + "[" + std::to_string(r) + "]").c_str(), 4);
+        if (st != SHMM_OK) return st;
+    }
+    return SHMM_OK;
+}
+
+static shmm_status_t check_norm_workspace(const char *fn, int64_t rows, int64_t cols, const void *workspace,
+                                          size_t workspace_bytes) {
+    const size_t need = shmm::norm_workspace_bytes(rows, cols);
+    if (workspace_bytes < need)
+        return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(workspace_bytes) +
+                                        " bytes, " + std::to_string(need) + " needed");
+    if (need) return check_ptr(fn, workspace, "workspace", 256);
+    return SHMM_OK;
+}
+
+shmm_status_t shmm_layernorm_forward(int64_t rows, int64_t cols, shmm_dtype_t dtype, const void *x,
+                                     const void *residual, const float *gamma, const float *beta, float eps,
+                                     void *total, void *y, float *mean, float *rstd, void *stream) {
+    static const char *fn = "shmm_layernorm_forward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+        shmm_status_t st;
+        if ((st = norm_sizes(fn, rows, cols, dtype)) != SHMM_OK) return st;
+        if (!(eps >= 0.0f)) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": eps must be >= 0");
+        if (rows == 0 || cols == 0) return SHMM_OK;
+        if ((st = check_ptr(fn, x, "x", 16)) != SHMM_OK || (st = check_ptr(fn, y, "y", 16)) != SHMM_OK ||
+            (st = check_ptr(fn, gamma, "gamma", 4)) != SHMM_OK || (st = check_ptr(fn, beta, "beta", 4)) != SHMM_OK ||
+            (st = check_ptr(fn, mean, "mean", 4)) != SHMM_OK || (st = check_ptr(fn, rstd, "rstd", 4)) != SHMM_OK)
+            return st;
+        if (residual) {
+            if ((st = check_ptr(fn, residual, "residual", 16)) != SHMM_OK ||
+                (st = check_ptr(fn, total, "total", 16)) != SHMM_OK)
+                return st;
+            if (total == y) return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": total and y are one buffer");
+        } else if (total) {
+            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": total is written only with a residual");
+        }
+        shmm::NormForwardArgs a;
+        a.brows = rows;
+        a.cols = cols;
+        a.dt = dtype;
+        a.gamma = gamma;
+        a.beta = beta;
+        a.eps = eps;
+        a.res = residual;
+        a.total = total;
+        a.src = &x;
+        a.dst = &y;
+        a.mean = &mean;
+        a.rstd = &rstd;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        const int e = shmm::launch_norm_forward(a, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_layernorm_backward_workspace_size(int64_t rows, int64_t cols, size_t *bytes) {
+    static const char *fn = "shmm_layernorm_backward_workspace_size";
+    shmm::clear_error();
+    if (!bytes) return fail(SHMM_ERR_NULL, std::string(fn) + ": bytes is NULL");
+    const shmm_status_t st = norm_sizes(fn, rows, cols, SHMM_F32);
+    if (st != SHMM_OK) return st;
+    *bytes = shmm::norm_workspace_bytes(rows, cols);
+    return SHMM_OK;
+}
+
+shmm_status_t shmm_layernorm_backward(int64_t rows, int64_t cols, shmm_dtype_t dtype, const void *dy, const void *x,
+                                      const float *mean, const float *rstd, const float *gamma,
+                                      const void *residual_grad, void *dx, float *dgamma, float *dbeta,
+                                      void *workspace, size_t workspace_bytes, void *stream) {
+    static const char *fn = "shmm_layernorm_backward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+        shmm_status_t st;
+        if ((st = norm_sizes(fn, rows, cols, dtype)) != SHMM_OK) return st;
+        if (cols == 0) return SHMM_OK;
+        if ((st = check_ptr(fn, dgamma, "dgamma", 4)) != SHMM_OK || (st = check_ptr(fn, dbeta, "dbeta", 4)) != SHMM_OK)
+            return st;
+        if (rows) {
+            if ((st = check_ptr(fn, dy, "dy", 16)) != SHMM_OK || (st = check_ptr(fn, x, "x", 16)) != SHMM_OK ||
+                (st = check_ptr(fn, dx, "dx", 16)) != SHMM_OK || (st = check_ptr(fn, mean, "mean", 4)) != SHMM_OK ||
+                (st = check_ptr(fn, rstd, "rstd", 4)) != SHMM_OK || (st = check_ptr(fn, gamma, "gamma", 4)) != SHMM_OK)
+                return st;
+            if (residual_grad && (st = check_ptr(fn, residual_grad, "residual_grad", 16)) != SHMM_OK) return st;
+        }
+        if ((st = check_norm_workspace(fn, rows, cols, workspace, workspace_bytes)) != SHMM_OK) return st;
+        shmm::NormBackwardArgs a;
+        a.brows = rows;
+        a.cols = cols;
+        a.dt = a.grad_dt = dtype;
+        a.gamma = gamma;
+        a.res = residual_grad;
+        a.grad = &dy;
+        a.src = &x;
+        a.mean = &mean;
+        a.rstd = &rstd;
+        a.dst = &dx;
+        a.dgamma = dgamma;
+        a.dbeta = dbeta;
+        a.workspace = static_cast<float *>(workspace);
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        const int e = shmm::launch_norm_backward(a, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
+// The owner blocks of a plan's row gather, in block order per group, and the
+// members' gathered buffers.
+static void row_gather_tables(const shmm_plan_t *p, const void *const *shard, const void *const *full,
+                              std::vector<const void *> *src, std::vector<const void *> *dst) {
+    const shmm::Groups &g = p->gC_groups;
+    src->resize(g.members.size());
+    dst->resize(g.members.size());
+    for (size_t i = 0; i < g.members.size(); ++i) {
+        (*src)[i] = shard[g.by_block[i]];
+        (*dst)[i] = full[g.members[i]];
+    }
+}
+
+static shmm_status_t check_row_gather(const char *fn, const shmm_plan_t *p) {
+    if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
+    if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+    if (p->gC_groups.size == 1 || p->gC_groups.blocks1 != 1)
+        return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": the plan must all-gather its result along rows");
+    return SHMM_OK;
+}
+
+shmm_status_t shmm_layernorm_all_gather_forward(const shmm_plan_t *p, const void *const *shard_r,
+                                                const float *gamma, const float *beta, float eps,
+                                                void *const *full_r, float *const *mean_r, float *const *rstd_r,
+                                                void *stream) {
+    static const char *fn = "shmm_layernorm_all_gather_forward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_row_gather(fn, p)) != SHMM_OK) return st;
+        if (!(eps >= 0.0f)) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": eps must be >= 0");
+        if ((st = check_ptr(fn, gamma, "gamma", 4)) != SHMM_OK || (st = check_ptr(fn, beta, "beta", 4)) != SHMM_OK ||
+            (st = check_ptrs(p, shard_r, SHMM_TENSOR_C_REDUCED, fn, "shard_r")) != SHMM_OK ||
+            (st = check_ptrs(p, (const void *const *)full_r, SHMM_TENSOR_C, fn, "full_r")) != SHMM_OK ||
+            (st = check_stats(p, mean_r, fn, "mean_r")) != SHMM_OK ||
+            (st = check_stats(p, rstd_r, fn, "rstd_r")) != SHMM_OK)
+            return st;
+        const shmm::Groups &g = p->gC_groups;
+        std::vector<const void *> src, dst;
+        row_gather_tables(p, shard_r, (const void *const *)full_r, &src, &dst);
+        std::vector<float *> mean(src.size()), rstd(src.size());
+        for (size_t i = 0; i < src.size(); ++i) {
+            mean[i] = mean_r[g.by_block[i]];
+            rstd[i] = rstd_r[g.by_block[i]];
+        }
+        shmm::NormForwardArgs a;
+        a.G = g.size;
+        a.ngroups = g.count;
+        a.brows = p->boxes[SHMM_TENSOR_C_REDUCED][0].ext[0];
+        a.cols = p->boxes[SHMM_TENSOR_C_REDUCED][0].ext[1];
+        if ((st = norm_sizes(fn, a.brows, a.cols, p->out_dt)) != SHMM_OK) return st;
+        a.dt = p->out_dt;
+        a.gamma = gamma;
+        a.beta = beta;
+        a.eps = eps;
+        a.src = src.data();
+        a.dst = const_cast<void *const *>(dst.data());
+        a.mean = mean.data();
+        a.rstd = rstd.data();
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        const int e = shmm::launch_norm_forward(a, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *p, shmm_dtype_t grad_dtype,
+                                                 const void *const *dfull_r, const void *const *shard_r,
+                                                 const float *const *mean_r, const float *const *rstd_r,
+                                                 const float *gamma, void *const *dshard_r, float *dgamma,
+                                                 float *dbeta, void *workspace, size_t workspace_bytes,
+                                                 void *stream) {
+    static const char *fn = "shmm_layernorm_all_gather_backward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_row_gather(fn, p)) != SHMM_OK) return st;
+        if (grad_dtype != SHMM_F32 && grad_dtype != p->out_dt)
+            return fail(SHMM_ERR_DTYPE, std::string(fn) + ": gradients are fp32 or of the plan's output dtype");
+        if ((st = check_ptr(fn, gamma, "gamma", 4)) != SHMM_OK || (st = check_ptr(fn, dgamma, "dgamma", 4)) != SHMM_OK ||
+            (st = check_ptr(fn, dbeta, "dbeta", 4)) != SHMM_OK ||
+            (st = check_ptrs(p, dfull_r, SHMM_TENSOR_C, fn, "dfull_r")) != SHMM_OK ||
+            (st = check_ptrs(p, shard_r, SHMM_TENSOR_C_REDUCED, fn, "shard_r")) != SHMM_OK ||
+            (st = check_ptrs(p, (const void *const *)dshard_r, SHMM_TENSOR_C_REDUCED, fn, "dshard_r")) != SHMM_OK ||
+            (st = check_stats(p, mean_r, fn, "mean_r")) != SHMM_OK ||
+            (st = check_stats(p, rstd_r, fn, "rstd_r")) != SHMM_OK)
+            return st;
+        const shmm::Groups &g = p->gC_groups;
+        std::vector<const void *> src, grad;
+        row_gather_tables(p, shard_r, dfull_r, &src, &grad);
+        std::vector<const float *> mean(src.size()), rstd(src.size());
+        std::vector<void *> dst(src.size());
+        for (size_t i = 0; i < src.size(); ++i) {
+            mean[i] = mean_r[g.by_block[i]];
+            rstd[i] = rstd_r[g.by_block[i]];
+            dst[i] = dshard_r[g.by_block[i]];
+        }
+        shmm::NormBackwardArgs a;
+        a.G = g.size;
+        a.ngroups = g.count;
+        a.brows = p->boxes[SHMM_TENSOR_C_REDUCED][0].ext[0];
+        a.cols = p->boxes[SHMM_TENSOR_C_REDUCED][0].ext[1];
+        const int64_t rows = a.brows * g.size * g.count;
+        if ((st = norm_sizes(fn, rows, a.cols, p->out_dt)) != SHMM_OK) return st;
+        if ((st = check_norm_workspace(fn, rows, a.cols, workspace, workspace_bytes)) != SHMM_OK) return st;
+        a.dt = p->out_dt;
+        a.grad_dt = grad_dtype;
+        a.gamma = gamma;
+        a.grad = grad.data();
+        a.src = src.data();
+        a.mean = mean.data();
+        a.rstd = rstd.data();
+        a.dst = dst.data();
+        a.dgamma = dgamma;
+        a.dbeta = dbeta;
+        a.workspace = static_cast<float *>(workspace);
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        const int e = shmm::launch_norm_backward(a, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
 shmm_status_t shmm_run_static_workspace(const shmm_plan_t *p, const void *const *A_r,
                                         const void *const *B_r, void *const *C_r, void *stream) {
     static const char *fn = "shmm_run_static_workspace";

@@ -1,0 +1,709 @@
+// Layer normalisation for training: the forward pass that keeps each row's
+// statistics (with a residual added on the way, or with the rows gathered to
+// every rank), and its gradient (with the reduce-scatter that is the adjoint
+// of that gather, and the reduction of the gain's and bias's gradient).
+//
+// For a row t of n values, with gain gamma and bias beta:
+//   mean = sum(t) / n,  rstd = 1 / sqrt(sum((t - mean)^2) / n + eps)
+//   xh   = (t - mean) rstd,  y = xh gamma + beta
+// and with dy the gradient of y, w = dy gamma:
+//   dt     = rstd (w - sum(w) / n - xh sum(w xh) / n)
+//   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+//
+// Both passes are HBM-bound (8 to 14 operations per element), so each reads
+// every element once: a CTA (or, for rows of up to 512 columns, a warp) holds
+// a row in registers between its reduction and its output, and every thread
+// keeps the same columns in every row of the CTA's walk, so gamma, beta and
+// the running dgamma, dbeta live in registers too.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "checked.cuh"
+#include "pdl.cuh"
+#include "shmm_internal.h"
+
+namespace {
+
+using shmm_dev::in_bounds;
+using shmm_pdl::launch_pdl;
+using shmm_pdl::pdl_enter;
+
+// Columns one thread of the register kernels holds, and the most threads
+// they give a row: rows of up to 8192 columns.  Wider rows take the
+// re-reading kernels at the end.
+constexpr int kCols = 16;
+constexpr int kMaxThreads = 512;
+// CTAs whose partial dgamma, dbeta rows the workspace holds: two per SM.
+constexpr int kMaxParts = 304;
+
+// Pointer tables: one entry for the plain call (a small parameter block
+// keeps its launch short), one per rank for the gathered one.
+template <int N>
+struct FwdK {
+    const void *src[N];   // [g*G + p]: block p of group g
+    void *dst[N];         // [g*G + m]: every member's gathered buffer
+    float *mean[N], *rstd[N];  // [g*G + p]
+    const void *res;      // N == 1: residual, or NULL
+    void *total;          // N == 1: x + residual, or NULL
+    const float *gamma, *beta;
+    float eps;
+    int G;
+    int64_t brows, cols, rows;  // rows over all blocks
+    int *status;
+};
+
+template <int N>
+struct BwdK {
+    const void *grad[N];  // [g*G + m]: member m's gradient of the gathered rows
+    const void *src[N];   // [g*G + p]: block p of group g
+    const float *mean[N], *rstd[N];
+    void *dst[N];
+    const void *res;      // N == 1: gradient added to dt, or NULL
+    const float *gamma;
+    float *part;          // [gridDim.x][2][cols]
+    int G;
+    int64_t brows, cols, rows;
+    int *status;
+};
+
+// VW consecutive values as they lie in memory: one access of VW * sizeof(T)
+// bytes (two for 8 fp32 values), kept packed until they are used.
+template <typename T, int VW>
+struct Raw {
+    static constexpr int W = VW * (int)sizeof(T) / 4;  // 32-bit words
+    uint32_t w[W];
+    __device__ void load(const T *p) {
+        if constexpr (W >= 4) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ void store(T *p) const {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            __stcs(reinterpret_cast<uint4 *>(p) + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+    }
+    __device__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    }
+    __device__ void set(const float *v) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VW; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VW / 2; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T v;
+    __device__ void load(const T *p) { v = *p; }
+    __device__ void store(T *p) const { *p = v; }
+    __device__ void zero() { v = T(0.0f); }
+    __device__ float get(int) const { return (float)v; }
+    __device__ void set(const float *f) {
+        if constexpr (sizeof(T) == 4) v = *f;
+        else v = __float2bfloat16_rn(*f);
+    }
+};
+
+// Where row t lives: block s = g*G + p, row rr of the block, and its row in
+// the gathered buffers of group g.
+template <int N>
+__device__ __forceinline__ void locate(int64_t t, int64_t brows, int G, int *s, int *g, int64_t *rr, int64_t *grow) {
+    if constexpr (N == 1) {
+        *s = 0;
+        *g = 0;
+        *rr = *grow = t;
+    } else {
+        int64_t q;
+        if (t < ((int64_t)1 << 31) && brows < ((int64_t)1 << 31)) q = (uint32_t)t / (uint32_t)brows;
+        else q = t / brows;
+        *s = (int)q;
+        *g = *s / G;
+        *rr = t - q * brows;
+        *grow = (int64_t)(*s - *g * G) * brows + *rr;
+    }
+}
+
+// Sum of two values over the threads of a row: shuffles, then (more than one
+// warp) the warps' sums in order.  Every thread gets the same bits.
+// `scratch` holds two float2 rows used in turn, so one barrier per sum is
+// enough: a thread that is a sum ahead writes the other row, and a thread
+// two sums ahead has passed a barrier that the slowest reader has reached.
+template <bool ONEWARP>
+__device__ __forceinline__ float2 row_sum(float2 v, float2 *scratch, int &turn) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if constexpr (ONEWARP) return v;
+    float2 *s = scratch + turn * (kMaxThreads / 32);
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x / 32] = v;
+    __syncthreads();
+    const int nw = blockDim.x / 32;
+    float2 t = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < nw; ++i) {
+        const float2 u = s[i];
+        t.x += u.x;
+        t.y += u.y;
+    }
+    return t;
+}
+
+// Thread's first column of its access j: consecutive threads read
+// consecutive accesses.
+template <int VW, bool ONEWARP>
+__device__ __forceinline__ int col_of(int j) {
+    const int th = ONEWARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int nt = ONEWARP ? 32 : blockDim.x;
+    return (th + j * nt) * VW;
+}
+
+// ---- forward ---------------------------------------------------------------
+
+template <typename T, int VW, int NV, int N, bool ONEWARP>
+__global__ void __launch_bounds__(kMaxThreads) ln_forward_kernel(const __grid_constant__ FwdK<N> k) {
+    pdl_enter();
+    __shared__ float2 scratch[2 * kMaxThreads / 32];
+    int turn = 0;
+    const int cols = (int)k.cols;
+    const float n = (float)cols;
+    const int lanes_row = ONEWARP ? threadIdx.x / 32 : 0, per_cta = ONEWARP ? blockDim.x / 32 : 1;
+    const int64_t step = (int64_t)gridDim.x * per_cta;
+    float ga[NV][VW], be[NV][VW];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = col_of<VW, ONEWARP>(j);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            ga[j][i] = c < cols ? k.gamma[c + i] : 0.0f;
+            be[j][i] = c < cols ? k.beta[c + i] : 0.0f;
+        }
+    }
+    const bool has_res = N == 1 && k.res;
+    Raw<T, VW> v[NV], r[NV];
+    auto load_row = [&](int64_t t) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        const bool ok = in_bounds(k.status, rr * cols, cols, k.brows * cols);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = col_of<VW, ONEWARP>(j);
+            v[j].zero();
+            if (c < cols && ok) v[j].load((const T *)k.src[s] + rr * cols + c);
+        }
+        if constexpr (N == 1) {
+            if (has_res) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = col_of<VW, ONEWARP>(j);
+                    r[j].zero();
+                    if (c < cols && ok) r[j].load((const T *)k.res + rr * cols + c);
+                }
+            }
+        }
+    };
+    int64_t t = (int64_t)blockIdx.x * per_cta + lanes_row;
+    if (t < k.rows) load_row(t);
+    for (; t < k.rows; t += step) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        if constexpr (N == 1) {
+            // The sum is rounded to the stored type before anything is
+            // computed from it: the backward pass reads the stored sum.
+            if (has_res) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    float f[VW];
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) f[i] = v[j].get(i) + r[j].get(i);
+                    v[j].set(f);
+                    const int c = col_of<VW, ONEWARP>(j);
+                    if (c < cols && in_bounds(k.status, rr * cols + c, VW, k.brows * cols))
+                        v[j].store((T *)k.total + rr * cols + c);
+                }
+            }
+        }
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) sum.x += v[j].get(i);
+        // Divided, not multiplied by 1 / n: a constant row whose sum is exact
+        // then has deviations of exactly zero (rstd would magnify a last bit).
+        const float mean = row_sum<ONEWARP>(sum, scratch, turn).x / n;
+        float2 sq = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (col_of<VW, ONEWARP>(j) < cols)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float d = v[j].get(i) - mean;
+                    sq.x += d * d;
+                }
+        const float rstd = 1.0f / sqrtf(row_sum<ONEWARP>(sq, scratch, turn).x / n + k.eps);
+        Raw<T, VW> y[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float f[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i) f[i] = (v[j].get(i) - mean) * rstd * ga[j][i] + be[j][i];
+            y[j].set(f);
+        }
+        if (t + step < k.rows) load_row(t + step);  // in flight while this row is written
+        if (col_of<VW, ONEWARP>(0) == 0 && in_bounds(k.status, rr, 1, k.brows)) {
+            k.mean[s][rr] = mean;
+            k.rstd[s][rr] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = col_of<VW, ONEWARP>(j);
+            if (c >= cols || !in_bounds(k.status, grow * cols + c, VW, k.G * k.brows * cols)) continue;
+            for (int m = 0; m < k.G; ++m) y[j].store((T *)k.dst[g * k.G + m] + grow * cols + c);
+        }
+    }
+}
+
+// Rows of any width: the row is read three times (from L2 after the first).
+template <typename T, int N>
+__global__ void __launch_bounds__(kMaxThreads) ln_forward_wide_kernel(const __grid_constant__ FwdK<N> k) {
+    pdl_enter();
+    __shared__ float2 scratch[2 * kMaxThreads / 32];
+    int turn = 0;
+    const float n = (float)k.cols;
+    for (int64_t t = blockIdx.x; t < k.rows; t += gridDim.x) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        if (!in_bounds(k.status, rr * k.cols, k.cols, k.brows * k.cols)) continue;  // the same for the whole CTA
+        const T *x = (const T *)k.src[s] + rr * k.cols;
+        float2 sum = make_float2(0.0f, 0.0f);
+        for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) {
+            float f = (float)x[c];
+            if (N == 1 && k.res) {
+                Raw<T, 1> o;
+                f += (float)((const T *)k.res)[rr * k.cols + c];
+                o.set(&f);
+                o.store((T *)k.total + rr * k.cols + c);
+                f = o.get(0);
+            }
+            sum.x += f;
+        }
+        if (N == 1 && k.res) x = (const T *)k.total + rr * k.cols;  // each thread reads back its own columns
+        const float mean = row_sum<false>(sum, scratch, turn).x / n;
+        float2 sq = make_float2(0.0f, 0.0f);
+        for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) {
+            const float d = (float)x[c] - mean;
+            sq.x += d * d;
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<false>(sq, scratch, turn).x / n + k.eps);
+        if (threadIdx.x == 0) {
+            k.mean[s][rr] = mean;
+            k.rstd[s][rr] = rstd;
+        }
+        for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) {
+            const float f = ((float)x[c] - mean) * rstd * k.gamma[c] + k.beta[c];
+            Raw<T, 1> o;
+            o.set(&f);
+            for (int m = 0; m < k.G; ++m) o.store((T *)k.dst[g * k.G + m] + grow * k.cols + c);
+        }
+    }
+}
+
+// ---- backward --------------------------------------------------------------
+
+template <typename T, typename GT, int VW, int NV, int N, bool ONEWARP>
+__global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_constant__ BwdK<N> k) {
+    pdl_enter();
+    __shared__ float2 scratch[2 * kMaxThreads / 32];
+    int turn = 0;
+    const int cols = (int)k.cols;
+    const float inv_n = 1.0f / (float)cols;
+    const int lanes_row = ONEWARP ? threadIdx.x / 32 : 0, per_cta = ONEWARP ? blockDim.x / 32 : 1;
+    const int64_t step = (int64_t)gridDim.x * per_cta;
+    float ga[NV][VW], dg[NV][VW], db[NV][VW];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = col_of<VW, ONEWARP>(j);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            ga[j][i] = c < cols ? k.gamma[c + i] : 0.0f;
+            dg[j][i] = db[j][i] = 0.0f;
+        }
+    }
+    Raw<T, VW> x[NV];
+    Raw<GT, VW> d0[NV];  // the first member's gradient
+    auto load_row = [&](int64_t t) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        const bool ok = in_bounds(k.status, rr * cols, cols, k.brows * cols) &&
+                        in_bounds(k.status, grow * cols, cols, k.G * k.brows * cols);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = col_of<VW, ONEWARP>(j);
+            x[j].zero();
+            d0[j].zero();
+            if (c < cols && ok) {
+                x[j].load((const T *)k.src[s] + rr * cols + c);
+                d0[j].load((const GT *)k.grad[g * k.G] + grow * cols + c);
+            }
+        }
+    };
+    int64_t t = (int64_t)blockIdx.x * per_cta + lanes_row;
+    if (t < k.rows) load_row(t);
+    for (; t < k.rows; t += step) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        const float mean = k.mean[s][rr], rstd = k.rstd[s][rr];
+        float dy[NV][VW];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) dy[j][i] = d0[j].get(i);
+        if constexpr (N > 1) {  // the members' gradients in rank order
+#pragma unroll 4
+            for (int m = 1; m < k.G; ++m) {
+                Raw<GT, VW> d[NV];
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = col_of<VW, ONEWARP>(j);
+                    d[j].zero();
+                    if (c < cols && in_bounds(k.status, grow * cols + c, VW, k.G * k.brows * cols))
+                        d[j].load((const GT *)k.grad[g * k.G + m] + grow * cols + c);
+                }
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) dy[j][i] += d[j].get(i);
+            }
+        }
+        float2 sum = make_float2(0.0f, 0.0f);  // of w and of w xh
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (col_of<VW, ONEWARP>(j) < cols)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float xh = (x[j].get(i) - mean) * rstd, w = dy[j][i] * ga[j][i];
+                    sum.x += w;
+                    sum.y += w * xh;
+                    dg[j][i] += dy[j][i] * xh;
+                    db[j][i] += dy[j][i];
+                }
+        sum = row_sum<ONEWARP>(sum, scratch, turn);
+        const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
+        float o[NV][VW];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const float xh = (x[j].get(i) - mean) * rstd;
+                o[j][i] = rstd * (dy[j][i] * ga[j][i] - c1 - xh * c2);
+            }
+        if (t + step < k.rows) load_row(t + step);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = col_of<VW, ONEWARP>(j);
+            if (c >= cols || !in_bounds(k.status, rr * cols + c, VW, k.brows * cols)) continue;
+            if constexpr (N == 1) {
+                if (k.res) {
+                    Raw<T, VW> r;
+                    r.load((const T *)k.res + rr * cols + c);
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) o[j][i] += r.get(i);
+                }
+            }
+            Raw<T, VW> y;
+            y.set(o[j]);
+            y.store((T *)k.dst[s] + rr * cols + c);
+        }
+    }
+    // This CTA's rows' sums.  One warp per row: the warps' sums in order.
+    float *part = k.part + (int64_t)blockIdx.x * 2 * cols;
+    if constexpr (ONEWARP) {
+        __shared__ float sh[(kMaxThreads / 32) * 32 * NV * VW];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, nw = blockDim.x / 32;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+                    sh[warp * 32 * NV * VW + (lane + j * 32) * VW + i] = h ? db[j][i] : dg[j][i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+                float a = 0.0f;
+                for (int w = 0; w < nw; ++w) a += sh[w * 32 * NV * VW + c];
+                part[h * cols + c] = a;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = col_of<VW, ONEWARP>(j);
+            if (c >= cols) continue;
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                part[c + i] = dg[j][i];
+                part[cols + c + i] = db[j][i];
+            }
+        }
+    }
+}
+
+// Rows of any width: the row is read twice, and each thread adds its columns
+// of dgamma and dbeta to the CTA's partial row, which it zeroes first.
+template <typename T, typename GT, int N>
+__global__ void __launch_bounds__(kMaxThreads) ln_backward_wide_kernel(const __grid_constant__ BwdK<N> k) {
+    pdl_enter();
+    __shared__ float2 scratch[2 * kMaxThreads / 32];
+    int turn = 0;
+    const float inv_n = 1.0f / (float)k.cols;
+    float *part = k.part + (int64_t)blockIdx.x * 2 * k.cols;
+    for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) part[c] = part[k.cols + c] = 0.0f;
+    for (int64_t t = blockIdx.x; t < k.rows; t += gridDim.x) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        if (!in_bounds(k.status, rr * k.cols, k.cols, k.brows * k.cols) ||
+            !in_bounds(k.status, grow * k.cols, k.cols, k.G * k.brows * k.cols))
+            continue;  // the same for the whole CTA
+        const T *x = (const T *)k.src[s] + rr * k.cols;
+        const float mean = k.mean[s][rr], rstd = k.rstd[s][rr];
+        auto grad = [&](int64_t c) {
+            float dy = (float)((const GT *)k.grad[g * k.G])[grow * k.cols + c];
+            for (int m = 1; m < k.G; ++m) dy += (float)((const GT *)k.grad[g * k.G + m])[grow * k.cols + c];
+            return dy;
+        };
+        float2 sum = make_float2(0.0f, 0.0f);
+        for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) {
+            const float dy = grad(c), xh = ((float)x[c] - mean) * rstd, w = dy * k.gamma[c];
+            sum.x += w;
+            sum.y += w * xh;
+            part[c] += dy * xh;
+            part[k.cols + c] += dy;
+        }
+        sum = row_sum<false>(sum, scratch, turn);
+        const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
+        for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) {
+            const float xh = ((float)x[c] - mean) * rstd;
+            float o = rstd * (grad(c) * k.gamma[c] - c1 - xh * c2);
+            if (N == 1 && k.res) o += (float)((const T *)k.res)[rr * k.cols + c];
+            Raw<T, 1> y;
+            y.set(&o);
+            y.store((T *)k.dst[s] + rr * k.cols + c);
+        }
+    }
+}
+
+// dgamma and dbeta: the CTAs' partial rows, column by column.  A CTA takes 32
+// columns of the [parts][2 cols] array; warp y adds rows y, y + 32, ... and
+// the 32 sums are added in order: a fixed order, so one input gives one
+// result.  parts == 0 (no rows) writes zeros.
+__global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, int parts, int64_t cols, float *dgamma,
+                                                           float *dbeta) {
+    pdl_enter();
+    __shared__ float sh[32][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float a = 0.0f;
+    if (c < 2 * cols)
+        for (int p = threadIdx.y; p < parts; p += 32) a += part[(int64_t)p * 2 * cols + c];
+    sh[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < 2 * cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int y = 0; y < 32; ++y) t += sh[y][threadIdx.x];
+        if (c < cols) dgamma[c] = t;
+        else dbeta[c - cols] = t;
+    }
+}
+
+int sms() {
+    static shmm::PerDevice<int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= shmm::kMaxDevices) return 152;
+    int n = cache.get(dev);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+        cache.set(dev, n);
+    }
+    return n;
+}
+
+// Threads per row and accesses per thread for `cols` columns in accesses of
+// VW values.  `spread` gives a row more threads with fewer columns each.
+struct Shape {
+    int nv, threads;
+    bool onewarp;
+};
+Shape shape_for(int64_t cols, int vw, int want_cols) {
+    const int nvec = (int)((cols + vw - 1) / vw);
+    if (cols <= 32 * kCols && want_cols >= kCols) return {kCols / vw, 256, true};
+    int nv = want_cols / vw;
+    if (vw == 1 && nv < 4) nv = 4;
+    while ((nvec + nv - 1) / nv > kMaxThreads) nv *= vw == 1 ? 4 : 2;
+    const int threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    return {nv, threads, false};
+}
+
+template <typename T, int VW, int N>
+cudaError_t forward_vec(const FwdK<N> &k, cudaStream_t s) {
+    const bool few = k.rows < sms();
+    const Shape h = shape_for(k.cols, VW, few ? VW : kCols);
+    const int64_t per_cta = h.onewarp ? h.threads / 32 : 1;
+    int64_t grid = (k.rows + per_cta - 1) / per_cta;
+    const int64_t cap = (int64_t)sms() * (1024 / h.threads > 0 ? 1024 / h.threads : 1);
+    if (grid > cap) grid = cap;
+    const dim3 g((unsigned)grid), b((unsigned)h.threads);
+constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
+    if (h.onewarp) return launch_pdl(ln_forward_kernel<T, VW, kMost, N, true>, g, b, 0, s, k);
+    if (h.nv == kMost) return launch_pdl(ln_forward_kernel<T, VW, kMost, N, false>, g, b, 0, s, k);
+    if (h.nv == kMost / 2 && VW > 1) return launch_pdl(ln_forward_kernel<T, VW, (VW > 1 ? kMost / 2 : kMost), N, false>, g, b, 0, s, k);
+    if (h.nv == kMost / 4 && VW < 8) return launch_pdl(ln_forward_kernel<T, VW, (VW < 8 ? kMost / 4 : kMost), N, false>, g, b, 0, s, k);
+    return cudaErrorInvalidValue;
+}
+
+template <typename T, int N>
+cudaError_t forward(const FwdK<N> &k, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    if (k.cols > (int64_t)kMaxThreads * kCols) {
+        const int64_t cap = (int64_t)sms() * 2;
+        const dim3 g((unsigned)(k.rows < cap ? k.rows : cap));
+        return launch_pdl(ln_forward_wide_kernel<T, N>, g, dim3(kMaxThreads), 0, s, k);
+    }
+    return k.cols % V == 0 ? forward_vec<T, V, N>(k, s) : forward_vec<T, 1, N>(k, s);
+}
+
+template <typename T, typename GT, int VW, int N>
+cudaError_t backward_vec(const BwdK<N> &k, int *parts, cudaStream_t s) {
+    const Shape h = shape_for(k.cols, VW, kCols);
+    const int64_t per_cta = h.onewarp ? h.threads / 32 : 1;
+    int64_t grid = (k.rows + per_cta - 1) / per_cta;
+    int64_t cap = sms() * (h.threads <= 256 ? 2 : 1);
+    if (cap > kMaxParts) cap = kMaxParts;
+    if (grid > cap) grid = cap;
+    *parts = (int)grid;
+    const dim3 g((unsigned)grid), b((unsigned)h.threads);
+constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
+    if (h.onewarp) return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, true>, g, b, 0, s, k);
+    if (h.nv == kMost) return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, false>, g, b, 0, s, k);
+    if (h.nv == kMost / 2 && VW > 1) return launch_pdl(ln_backward_kernel<T, GT, VW, (VW > 1 ? kMost / 2 : kMost), N, false>, g, b, 0, s, k);
+    if (h.nv == kMost / 4 && VW < 8) return launch_pdl(ln_backward_kernel<T, GT, VW, (VW < 8 ? kMost / 4 : kMost), N, false>, g, b, 0, s, k);
+    return cudaErrorInvalidValue;
+}
+
+template <typename T, typename GT, int N>
+cudaError_t backward(const BwdK<N> &k, int *parts, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    if (k.cols > (int64_t)kMaxThreads * kCols) {
+        int64_t cap = (int64_t)sms();
+        if (cap > kMaxParts) cap = kMaxParts;
+        *parts = (int)(k.rows < cap ? k.rows : cap);
+        return launch_pdl(ln_backward_wide_kernel<T, GT, N>, dim3((unsigned)*parts), dim3(kMaxThreads), 0, s, k);
+    }
+    return k.cols % V == 0 ? backward_vec<T, GT, V, N>(k, parts, s) : backward_vec<T, GT, 1, N>(k, parts, s);
+}
+
+template <int N>
+cudaError_t run_forward(const shmm::NormForwardArgs &a, int *status, cudaStream_t s) {
+    FwdK<N> k;
+    for (int i = 0; i < a.ngroups * a.G; ++i) {
+        k.src[i] = a.src[i];
+        k.dst[i] = a.dst[i];
+        k.mean[i] = a.mean[i];
+        k.rstd[i] = a.rstd[i];
+    }
+    k.res = a.res;
+    k.total = a.total;
+    k.gamma = a.gamma;
+    k.beta = a.beta;
+    k.eps = a.eps;
+    k.G = a.G;
+    k.brows = a.brows;
+    k.cols = a.cols;
+    k.rows = (int64_t)a.ngroups * a.G * a.brows;
+    k.status = status;
+    shmm::count_launch();
+    return a.dt == SHMM_F32 ? forward<float, N>(k, s) : forward<__nv_bfloat16, N>(k, s);
+}
+
+template <int N>
+cudaError_t run_backward(const shmm::NormBackwardArgs &a, int *status, cudaStream_t s) {
+    BwdK<N> k;
+    for (int i = 0; i < a.ngroups * a.G; ++i) {
+        k.grad[i] = a.grad[i];
+        k.src[i] = a.src[i];
+        k.dst[i] = a.dst[i];
+        k.mean[i] = a.mean[i];
+        k.rstd[i] = a.rstd[i];
+    }
+    k.res = a.res;
+    k.gamma = a.gamma;
+    k.part = a.workspace;
+    k.G = a.G;
+    k.brows = a.brows;
+    k.cols = a.cols;
+    k.rows = (int64_t)a.ngroups * a.G * a.brows;
+    k.status = status;
+    int parts = 0;
+    cudaError_t e = cudaSuccess;
+    if (k.rows > 0) {
+        shmm::count_launch();
+        if (a.dt == SHMM_F32) e = backward<float, float, N>(k, &parts, s);
+        else if (a.grad_dt == SHMM_F32) e = backward<__nv_bfloat16, float, N>(k, &parts, s);
+        else e = backward<__nv_bfloat16, __nv_bfloat16, N>(k, &parts, s);
+        if (e != cudaSuccess) return e;
+    }
+    shmm::count_launch();
+    return launch_pdl(ln_grad_sum_kernel, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(32, 32), 0, s,
+                      (const float *)a.workspace, parts, a.cols, a.dgamma, a.dbeta);
+}
+
+}  // namespace
+
+namespace shmm {
+
+size_t norm_workspace_bytes(int64_t rows, int64_t cols) {
+    const int64_t parts = rows < kMaxParts ? rows : kMaxParts;
+    return (size_t)(parts * 2 * cols * 4);
+}
+
+int launch_norm_forward(const NormForwardArgs &a, int *status, void *stream) {
+    if (a.ngroups * a.G > SHMM_MAX_RANKS) return (int)cudaErrorInvalidValue;
+    if (a.brows == 0 || a.cols == 0) return 0;
+    return (int)(a.ngroups * a.G == 1 ? run_forward<1>(a, status, (cudaStream_t)stream)
+                                      : run_forward<SHMM_MAX_RANKS>(a, status, (cudaStream_t)stream));
+}
+
+int launch_norm_backward(const NormBackwardArgs &a, int *status, void *stream) {
+    if (a.ngroups * a.G > SHMM_MAX_RANKS) return (int)cudaErrorInvalidValue;
+    if (a.cols == 0) return 0;
+    return (int)(a.ngroups * a.G == 1 ? run_backward<1>(a, status, (cudaStream_t)stream)
+                                      : run_backward<SHMM_MAX_RANKS>(a, status, (cudaStream_t)stream));
+}
+
+}  // namespace shmm

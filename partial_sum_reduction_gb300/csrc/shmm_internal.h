@@ -151,6 +151,46 @@ struct LayerNormArgs {
 };
 int launch_layernorm_gather(const LayerNormArgs &a, int *status, void *stream);
 
+// Layer normalisation for training.  Forward: block p of group g
+// (src[g*G+p], brows x cols) is normalised row by row into rows
+// [p*brows, (p+1)*brows) of every member's dst[g*G+m], and its rows'
+// statistics go to mean[g*G+p], rstd[g*G+p].  One block only: `res` (or NULL)
+// is added first and the rounded sum kept in `total`.
+struct NormForwardArgs {
+    int G = 1, ngroups = 1;
+    int64_t brows = 0, cols = 0;
+    shmm_dtype_t dt = SHMM_BF16;
+    const float *gamma = nullptr, *beta = nullptr;
+    float eps = 1e-5f;
+    const void *res = nullptr;
+    void *total = nullptr;
+    const void *const *src = nullptr;
+    void *const *dst = nullptr;
+    float *const *mean = nullptr, *const *rstd = nullptr;
+};
+int launch_norm_forward(const NormForwardArgs &a, int *status, void *stream);
+
+// Its gradient: row rr of block p takes the sum over the group's members m,
+// in ascending order, of row p*brows + rr of grad[g*G+m] (dtype grad_dt); dst
+// receives the rows' gradient (plus `res`, one block only), dgamma and dbeta
+// the sums over every block's rows.  workspace: norm_workspace_bytes(rows
+// over all blocks, cols) bytes.
+struct NormBackwardArgs {
+    int G = 1, ngroups = 1;
+    int64_t brows = 0, cols = 0;
+    shmm_dtype_t dt = SHMM_BF16, grad_dt = SHMM_BF16;
+    const float *gamma = nullptr;
+    const void *res = nullptr;
+    const void *const *grad = nullptr;
+    const void *const *src = nullptr;
+    const float *const *mean = nullptr, *const *rstd = nullptr;
+    void *const *dst = nullptr;
+    float *dgamma = nullptr, *dbeta = nullptr;
+    float *workspace = nullptr;
+};
+size_t norm_workspace_bytes(int64_t rows, int64_t cols);
+int launch_norm_backward(const NormBackwardArgs &a, int *status, void *stream);
+
 // Copies rectangles between row-major buffers: rectangle i moves h[i] rows of
 // w[i] elements of `elem` bytes from src[i] (row pitch src_ld[i] elements) to
 // dst[i] (pitch dst_ld[i]).  The reshard (all-to-all) collective.

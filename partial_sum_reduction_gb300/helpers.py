@@ -7,7 +7,7 @@ from typing import List, Optional
 
 import torch
 
-from .shmm import F32, TENSOR_P, Plan
+from .shmm import F32, TENSOR_P, Plan, shmm_layernorm_backward_workspace_size
 
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 
@@ -55,3 +55,10 @@ def workspace(plan: Plan, device="cuda") -> Optional[torch.Tensor]:
     if n == 0:
         return None
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def layernorm_workspace(rows: int, cols: int, device="cuda") -> Optional[torch.Tensor]:
+    """Workspace of a layer normalisation's gradient over `rows` rows (of
+    every rank's block, for the gathered form)."""
+    n = shmm_layernorm_backward_workspace_size(rows, cols)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None

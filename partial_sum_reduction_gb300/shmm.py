@@ -19,6 +19,8 @@ import os
 import re
 from typing import List, Optional, Sequence, Tuple
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 # SHMM_CHECKED=1 selects the bounds-checked build (build.build(checked=True)):
 # the same kernels with every global index compared with its buffer's extent.
@@ -84,7 +86,9 @@ EXPORTS = ["shmm_plan", "shmm_plan_destroy", "shmm_plan_query", "shmm_plan_rank_
            "shmm_all_reduce", "shmm_all_gather", "shmm_run", "shmm_sync_status", "shmm_last_error",
            "shmm_status_string", "shmm_version", "shmm_kernel_launches", "shmm_run_static_workspace",
            "shmm_selftest_wait_timeout", "shmm_choose_operand", "shmm_reshard", "shmm_layernorm",
-           "shmm_layernorm_all_gather", "shmm_run_host", "shmm_bounds_checked", "shmm_run_batch"]
+           "shmm_layernorm_all_gather", "shmm_run_host", "shmm_bounds_checked", "shmm_run_batch",
+           "shmm_layernorm_forward", "shmm_layernorm_backward_workspace_size", "shmm_layernorm_backward",
+           "shmm_layernorm_all_gather_forward", "shmm_layernorm_all_gather_backward"]
 
 _lib = None
 
@@ -125,6 +129,15 @@ def lib():
         L.shmm_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
         L.shmm_layernorm.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P, P, P, ctypes.c_float, P, P]
         L.shmm_layernorm_all_gather.argtypes = [P, PP, P, P, ctypes.c_float, PP, P]
+        L.shmm_layernorm_forward.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P, P, P, P, ctypes.c_float,
+                                             P, P, P, P, P]
+        L.shmm_layernorm_backward_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int64,
+                                                             ctypes.POINTER(ctypes.c_size_t)]
+        L.shmm_layernorm_backward.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P, P, P, P, P, P, P, P, P,
+                                              P, ctypes.c_size_t, P]
+        L.shmm_layernorm_all_gather_forward.argtypes = [P, PP, P, P, ctypes.c_float, PP, PP, PP, P]
+        L.shmm_layernorm_all_gather_backward.argtypes = [P, ctypes.c_int, PP, PP, PP, PP, P, PP, P, P, P,
+                                                         ctypes.c_size_t, P]
         L.shmm_reshard.argtypes = [ctypes.POINTER(shmm_mesh_t), ctypes.POINTER(shmm_spec_t),
                                    ctypes.POINTER(shmm_spec_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                    PP, PP, P]
@@ -257,6 +270,62 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _refuse(t, what: str, shape, dtype) -> None:
+    """Raises ValueError with what is wrong with tensor t (see _tensor)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if t.dtype is not dtype:
+        raise ValueError("%s is %s, expected %s" % (what, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be dense (row-major contiguous)" % what)
+    raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
+
+
+def _tensor(t, what: str, shape, dtype) -> int:
+    """Address of a dense CUDA tensor of the current device with the given
+    shape and dtype; anything else is refused before the library sees it."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == torch.cuda.current_device()):
+        _refuse(t, what, shape, dtype)
+    return t.data_ptr()
+
+
+def _tensors(ts, what: str, shapes, dtype) -> ctypes.Array:
+    """Per-rank pointer array of dense tensors (see _tensor), one per shape."""
+    if len(ts) != len(shapes):
+        raise ValueError("%s: %d tensors, the plan has %d ranks" % (what, len(ts), len(shapes)))
+    arr = (ctypes.c_void_p * len(ts))()
+    for r, t in enumerate(ts):
+        arr[r] = _tensor(t, "%s[%d]" % (what, r), shapes[r], dtype)
+    return arr
+
+
+def _rows_dtype(x, what: str = "x"):
+    """(rows, cols, torch dtype, dtype code) of a 2-D fp32 or bf16 tensor."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("%s must be a 2-D CUDA tensor" % what)
+    if x.dtype is torch.bfloat16:
+        return x.shape[0], x.shape[1], x.dtype, BF16
+    if x.dtype is torch.float32:
+        return x.shape[0], x.shape[1], x.dtype, F32
+    raise ValueError("%s is %s, expected torch.float32 or torch.bfloat16" % (what, x.dtype))
+
+
+def _workspace(ws):
+    """(address, bytes) of a workspace tensor, or of none."""
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous() \
+            or ws.get_device() != torch.cuda.current_device():
+        raise ValueError("workspace must be a dense CUDA tensor of the current device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 class Plan:
     """A shmm_plan_t handle (freed on garbage collection or close())."""
 
@@ -273,6 +342,7 @@ class Plan:
                                int(I), int(J), int(K), DTYPE_CODES[in_dtype], DTYPE_CODES[out_dtype],
                                int(flags), ctypes.byref(h)))
         self._h = h
+        self._box_shapes = {}
         self.info = self.query()
         self.nranks = self.info.nranks
 
@@ -346,6 +416,45 @@ class Plan:
         _check(lib().shmm_layernorm_all_gather(self._h, _ptr_array(shard_r, "shard"), gamma.data_ptr(),
                                                beta.data_ptr(), float(eps), _ptr_array(full_r, "full"),
                                                _stream_handle(stream)))
+
+    def _shapes(self, tensor: int):
+        """Per-rank box extents of `tensor` (kept: they never change)."""
+        got = self._box_shapes.get(tensor)
+        if got is None:
+            got = self._box_shapes[tensor] = [self.rank_box(tensor, r)[1] for r in range(self.nranks)]
+        return got
+
+    def layernorm_all_gather_forward(self, shard_r, gamma, beta, full_r, mean_r, rstd_r, eps: float = 1e-5,
+                                     stream=None):
+        """layernorm_all_gather that also leaves each owner block's row
+        statistics in mean_r, rstd_r (one fp32 [block rows] tensor per rank),
+        for layernorm_all_gather_backward."""
+        dt, f32 = TORCH_DTYPES[self.out_dtype], torch.float32
+        block = self._shapes(TENSOR_C_REDUCED)
+        rows, cols = [(e[0],) for e in block], (block[0][1],)
+        _check(lib().shmm_layernorm_all_gather_forward(
+            self._h, _tensors(shard_r, "shard", block, dt), _tensor(gamma, "gamma", cols, f32),
+            _tensor(beta, "beta", cols, f32), eps, _tensors(full_r, "full", self._shapes(TENSOR_C), dt),
+            _tensors(mean_r, "mean", rows, f32), _tensors(rstd_r, "rstd", rows, f32), _stream_handle(stream)))
+
+    def layernorm_all_gather_backward(self, dfull_r, shard_r, mean_r, rstd_r, gamma, dshard_r, dgamma, dbeta,
+                                      workspace, stream=None):
+        """Gradient of layernorm_all_gather_forward: every member's gradient
+        of the gathered rows (fp32, or the plan's output dtype), reduced to
+        the rows' owners and taken through the normalisation in one pass
+        (see include/shmm.h).  workspace: helpers.layernorm_workspace of the
+        rows of every rank's block."""
+        dt, f32 = TORCH_DTYPES[self.out_dtype], torch.float32
+        block = self._shapes(TENSOR_C_REDUCED)
+        rows, cols = [(e[0],) for e in block], (block[0][1],)
+        gdt = f32 if len(dfull_r) and getattr(dfull_r[0], "dtype", None) is f32 else dt
+        ws, ws_bytes = _workspace(workspace)
+        _check(lib().shmm_layernorm_all_gather_backward(
+            self._h, F32 if gdt is f32 else BF16, _tensors(dfull_r, "dfull", self._shapes(TENSOR_C), gdt),
+            _tensors(shard_r, "shard", block, dt), _tensors(mean_r, "mean", rows, f32),
+            _tensors(rstd_r, "rstd", rows, f32), _tensor(gamma, "gamma", cols, f32),
+            _tensors(dshard_r, "dshard", block, dt), _tensor(dgamma, "dgamma", cols, f32),
+            _tensor(dbeta, "dbeta", cols, f32), ws, ws_bytes, _stream_handle(stream)))
 
     def run_host(self, A_host, B_host, C_host, A_r, B_r, C_r, workspace=None, stream=None):
         """shmm_run_host: global A [I,J], B [J,K] (CPU tensors, pinned for
@@ -456,6 +565,40 @@ def shmm_layernorm(x, gamma, beta, y, eps: float = 1e-5, stream=None):
     dt = {"torch.float32": "f32", "torch.bfloat16": "bf16"}[str(x.dtype)]
     _check(lib().shmm_layernorm(int(rows), int(cols), DTYPE_CODES[dt], x.data_ptr(), gamma.data_ptr(),
                                 beta.data_ptr(), float(eps), y.data_ptr(), _stream_handle(stream)))
+
+
+def shmm_layernorm_forward(x, gamma, beta, y, mean, rstd, residual=None, total=None, eps: float = 1e-5, stream=None):
+    """Row-wise layer normalisation of x (+ residual, the rounded sum kept in
+    total) into y, with the rows' statistics for shmm_layernorm_backward
+    (see include/shmm.h)."""
+    rows, cols, dt, code = _rows_dtype(x)
+    f32, shape = torch.float32, (rows, cols)
+    _check(lib().shmm_layernorm_forward(
+        rows, cols, code, _tensor(x, "x", shape, dt),
+        None if residual is None else _tensor(residual, "residual", shape, dt), _tensor(gamma, "gamma", (cols,), f32),
+        _tensor(beta, "beta", (cols,), f32), eps, None if total is None else _tensor(total, "total", shape, dt),
+        _tensor(y, "y", shape, dt), _tensor(mean, "mean", (rows,), f32), _tensor(rstd, "rstd", (rows,), f32),
+        _stream_handle(stream)))
+
+
+def shmm_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().shmm_layernorm_backward_workspace_size(int(rows), int(cols), ctypes.byref(n)))
+    return n.value
+
+
+def shmm_layernorm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, workspace, residual_grad=None, stream=None):
+    """Gradient of shmm_layernorm_forward: dx (+ residual_grad), dgamma,
+    dbeta (see include/shmm.h).  workspace: helpers.layernorm_workspace."""
+    rows, cols, dt, code = _rows_dtype(x)
+    f32, shape = torch.float32, (rows, cols)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib().shmm_layernorm_backward(
+        rows, cols, code, _tensor(dy, "dy", shape, dt), _tensor(x, "x", shape, dt),
+        _tensor(mean, "mean", (rows,), f32), _tensor(rstd, "rstd", (rows,), f32), _tensor(gamma, "gamma", (cols,), f32),
+        None if residual_grad is None else _tensor(residual_grad, "residual_grad", shape, dt),
+        _tensor(dx, "dx", shape, dt), _tensor(dgamma, "dgamma", (cols,), f32), _tensor(dbeta, "dbeta", (cols,), f32),
+        ws, ws_bytes, _stream_handle(stream)))
 
 
 def shmm_reshard(mesh, spec_from, spec_to, rows: int, cols: int, dtype: str, src_r, dst_r, stream=None):
