@@ -496,6 +496,72 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_d
                                                  float *dbeta, void *workspace, size_t workspace_bytes,
                                                  void *stream);
 
+/* Low-rank adapters of many requests beside the shared projection: every row
+ * of A may have its own pair of small factors, added to the plan's product
+ * (Hu et al., "LoRA: Low-Rank Adaptation of Large Language Models", 2021).
+ * For row i with adapter a = row_adapter[i] in [0, n_adapters):
+ *   low[i] = A[i] . down[a]^T                      (fp32, `rank` values)
+ *   C[i]   = base[i] + scale[a] * low[i] . up[a]   (rounded once to out_dtype)
+ * Any other value of row_adapter[i] means no adapter: low[i] = 0 and C[i] is
+ * base[i] bit for bit.  The requests of a batch need no order: rows of one
+ * adapter may lie anywhere, several requests may share one.  Together with
+ * shmm_run: run the plan, then call this with base_r = C_r = its result.
+ *   n_adapters   1 to 65535
+ *   rank         1 to 64: the rows of each factor (adapters of lower rank: pad
+ *                with zero rows)
+ *   A_r[N]       in: box SHMM_TENSOR_A, in_dtype, as for shmm_run; read in
+ *                place, a block that several ranks hold from the lowest one
+ *   row_adapter  in: device int32 array of I entries, over the whole batch
+ *   down, up     in: [n_adapters, rank, J] and [n_adapters, rank, K], row-major,
+ *                in_dtype, 16-byte aligned (whole: the factors are not sharded)
+ *   scale        in: fp32 array of n_adapters, or NULL for 1
+ *   base_r[N]    in: box SHMM_TENSOR_C, out_dtype, or NULL for 0; may be C_r
+ *   C_r[N]       out: box SHMM_TENSOR_C
+ *   low          out: fp32 [I, rank], for shmm_adapters_backward
+ * bf16 plans use the tensor cores: products of bf16 values in fp32, low split
+ * into bf16 parts worth 16 bits (24 where C is fp32).  fp32 plans use the CUDA
+ * cores.  One row of the batch: one launch of few CTAs per factor, the same
+ * kernels.  A plan whose result GeLU finishes is refused: the adapters' part
+ * belongs before it.
+ * Errors: NULL, ALIGN, SHAPE (n_adapters, rank, an empty J or K, a size of
+ * 2^31 or more), UNSUPPORTED (rank > 64, SHMM_FLAG_GELU), CUDA. */
+shmm_status_t shmm_adapters_forward(const shmm_plan_t *plan, int n_adapters, int rank, const void *const *A_r,
+                                    const int32_t *row_adapter, const void *down, const void *up, const float *scale,
+                                    const void *const *base_r, void *const *C_r, float *low, void *stream);
+
+/* Workspace of shmm_adapters_backward in bytes.  Host only.
+ * Errors: NULL, SHAPE (n_adapters, rank), UNSUPPORTED (rank > 64). */
+shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *plan, int n_adapters, int rank,
+                                           size_t *bytes);
+
+/* Gradient of shmm_adapters_forward, for the gradient dC of its C.  With
+ * dlow[i] = scale[a] * dC[i] . up[a]^T for row i of adapter a:
+ *   dA[i]    = base[i] + dlow[i] . down[a]
+ *   ddown[a] = sum over a's rows of dlow[i]^T A[i]
+ *   dup[a]   = scale[a] * sum over a's rows of low[i]^T dC[i]
+ * Rows without an adapter: dA[i] is base[i] bit for bit.  (base is the
+ * gradient that reaches A through the shared projection, whose weights
+ * stay as they are.)
+ *   dC_r[N]      in: box SHMM_TENSOR_C, out_dtype; a block that several ranks
+ *                hold (a replicated C) is read from the lowest one and counts
+ *                once
+ *   A_r, row_adapter, down, up, scale  in: as in the forward call
+ *   low          in: as the forward call left it
+ *   base_r[N]    in: box SHMM_TENSOR_A, in_dtype, or NULL for 0; may be dA_r
+ *   dA_r[N]      out: box SHMM_TENSOR_A, in_dtype, every rank's; not A_r
+ *   ddown, dup   out: fp32, the shapes of down and up, overwritten; zeros for
+ *                an adapter without rows
+ *   workspace    device memory of >= shmm_adapters_workspace_size() bytes,
+ *                256-byte aligned; nothing in it needs to start at zero, and
+ *                calls that overlap on the GPU need one each
+ * Sums over rows have a fixed order: one input gives one result.
+ * Errors: those of shmm_adapters_forward, and NOMEM (workspace). */
+shmm_status_t shmm_adapters_backward(const shmm_plan_t *plan, int n_adapters, int rank, const void *const *dC_r,
+                                     const void *const *A_r, const int32_t *row_adapter, const void *down,
+                                     const void *up, const float *scale, const float *low, const void *const *base_r,
+                                     void *const *dA_r, float *ddown, float *dup, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* ---- planner: which operand to move ("Sharded matmuls and collectives on
  * a torus", Which operand to move: the ICI roofline) ---------------------- */
 

@@ -1,0 +1,994 @@
+// Low-rank adapters of many requests beside a shared (sharded) projection,
+// and their gradient.  Row t of the batch uses adapter a = ids[t] (none when
+// a is outside [0, n)), a pair of factors down[a] (R x J) and up[a] (R x K):
+//   low[t] = A[t] . down[a]^T,       C[t] = base[t] + scale[a] low[t] . up[a]
+// and, for the gradient dC of C,
+//   dlow[t]  = scale[a] dC[t] . up[a]^T,   dA[t] = base[t] + dlow[t] . down[a]
+//   dup[a]   = scale[a] sum over a's rows of low[t]^T dC[t]
+//   ddown[a] = sum over a's rows of dlow[t]^T A[t]
+// Both factors lie as [n][R][columns], so three kernels make all of it:
+//   project  out[t] = X[t] . W[a]^T     (low, dlow)
+//   expand   O[t] = base[t] + S[t] . W[a]   (C, dA)
+//   outer    G[a] = sum S[t]^T X[t]     (dup, ddown)
+// R is at most 64, so a row's X and O move 2 bytes per 2 R operations and all
+// three are HBM-bound (64 operations per byte at R = 64, against 280 at the
+// card's tensor rate).  They use warp matrix instructions (mma.sync, bf16
+// operands, fp32 accumulators) whose operands come straight from global
+// memory in 16-byte loads: the order of the summed index is free, so each
+// thread takes eight consecutive values where the instruction's own layout
+// would give it scattered pairs.  fp32 operands take CUDA-core kernels.
+//
+// The low-rank rows stay fp32 between the kernels.  Where they are matrix
+// operands they are split into two bf16 parts (three where the result is
+// stored in fp32), high bits first, so a product loses 2^-17 (2^-24) of
+// itself, not the 2^-9 that rounding them to bf16 would.
+//
+// Rows of other adapters never mix: a row's result takes only products with
+// its own adapter, and rows of an adapter are gathered by index for its
+// gradient, so infinities or NaN in one adapter or row stay there.
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "checked.cuh"
+#include "pdl.cuh"
+#include "shmm_internal.h"
+
+namespace {
+
+namespace cg = cooperative_groups;
+using bf16 = __nv_bfloat16;
+using shmm_dev::in_bounds;
+using shmm_pdl::launch_pdl;
+using shmm_pdl::launch_pdl_cluster;
+using shmm_pdl::pdl_enter;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// A [rows, cols] array as a grid of equal blocks (ranks' shards), row-major
+// grid of b1 blocks per row of blocks.
+struct Blocks {
+    const void *at[SHMM_MAX_RANKS];
+    int b1;
+    int64_t brows, bcols;
+};
+
+struct ProjK {
+    Blocks x;
+    const void *w;        // [n][R][cols]
+    const int *ids;
+    const float *scale;   // multiplies the result, or NULL
+    float *out;           // [rows][R]
+    int n, R;
+    int64_t rows, cols;
+    int *status;
+};
+
+struct ExpandK {
+    const void *base[SHMM_MAX_RANKS];  // or NULL: zero
+    void *out[SHMM_MAX_RANKS];
+    int row0[SHMM_MAX_RANKS], col0[SHMM_MAX_RANKS];  // the rank's box, in blocks
+    int64_t brows, bcols;
+    const void *w;        // [n][R][cols]
+    const int *ids;
+    const float *scale;   // or NULL
+    const float *s;       // [rows][R]
+    int n, R, row_tiles;
+    int64_t rows, cols;
+    int *status;
+};
+
+struct OuterJob {
+    Blocks x;
+    const float *s;       // [rows][R]
+    const float *scale;   // or NULL
+    float *out;           // [n][R][cols]
+    int64_t cols;
+    int tiles;            // column tiles of the launch
+};
+struct OuterK {
+    OuterJob job[2];
+    const int *ids;
+    int n, R;
+    int64_t rows;
+    int *status;
+};
+
+// ---- pieces shared by the kernels -------------------------------------------
+
+struct Raw8 {  // eight bf16 values as they lie in memory
+    uint32_t w[4];
+};
+
+// Values [c, c + 8) of a row, c < cols; past the row's end, zeros.  VEC: rows
+// are whole 16-byte vectors.
+template <bool VEC>
+__device__ __forceinline__ Raw8 load8(const bf16 *row, int64_t c, int64_t cols) {
+    Raw8 r;
+    if constexpr (VEC) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + c);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else {
+        const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = c + 2 * i < cols ? p[c + 2 * i] : 0, hi = c + 2 * i + 1 < cols ? p[c + 2 * i + 1] : 0;
+            r.w[i] = lo | (hi << 16);
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// High part of a split: v with its low 16 bits cut (never rounds up to
+// infinity).  The rest, v - high, is exact; it is 0 for an infinity, whose
+// own difference would be NaN.
+__device__ __forceinline__ float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+__device__ __forceinline__ float rest(float v, float high) { return v == high ? 0.0f : v - high; }
+__device__ __forceinline__ uint32_t pack_cut(float lo, float hi) {
+    return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+}
+// Part `i` of the split of (lo, hi), packed.
+template <int PARTS>
+__device__ __forceinline__ void split(float lo, float hi, uint32_t *out) {
+#pragma unroll
+    for (int i = 0; i < PARTS - 1; ++i) {
+        const float a = cut(lo), b = cut(hi);
+        out[i] = pack_cut(a, b);
+        lo = rest(lo, a);
+        hi = rest(hi, b);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    out[PARTS - 1] = *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Distinct adapters of the ROWS rows from row t0, in order of first use, into
+// list (returns how many); ids[i] = the row's adapter, -1 for none or no row.
+template <int ROWS>
+__device__ __forceinline__ int distinct(const int *gids, int64_t t0, int64_t rows, int n, int *ids, int *list,
+                                        int *count, int *status) {
+    if (threadIdx.x < ROWS) {
+        const int64_t t = t0 + threadIdx.x;
+        int a = -1;
+        if (t < rows && in_bounds(status, t, 1, rows)) a = gids[t];
+        ids[threadIdx.x] = a >= 0 && a < n ? a : -1;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int have = 0;
+#pragma unroll
+        for (int i0 = 0; i0 < ROWS; i0 += 32) {
+            const int i = i0 + threadIdx.x;
+            bool first = i < ROWS && ids[i < ROWS ? i : 0] >= 0;
+            if (first)
+                for (int j = 0; j < i; ++j)
+                    if (ids[j] == ids[i]) {
+                        first = false;
+                        break;
+                    }
+            const unsigned m = __ballot_sync(0xffffffffu, first);
+            if (first) list[have + __popc(m & ((1u << threadIdx.x) - 1))] = ids[i];
+            have += __popc(m);
+        }
+        if (threadIdx.x == 0) *count = have;
+    }
+    __syncthreads();
+    return *count;
+}
+
+// Sums `v` (N values per thread) over the CTA's warps into warp 0, halving
+// the warps per step, in a fixed order.  sh holds kWarps / 2 * N * 32 floats.
+template <int N>
+__device__ __forceinline__ void sum_warps(float *v, float *sh) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = kWarps / 2; h > 0; h /= 2) {
+        if (warp >= h && warp < 2 * h)
+#pragma unroll
+            for (int i = 0; i < N; ++i) sh[((warp - h) * N + i) * 32 + lane] = v[i];
+        __syncthreads();
+        if (warp < h)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += sh[(warp * N + i) * 32 + lane];
+        __syncthreads();
+    }
+}
+
+// ---- project ---------------------------------------------------------------
+
+// A CTA takes 16 MT rows; its warps share the columns in chunks of 64, and
+// so do the CTAs of a cluster along y when there are few rows (their sums
+// meet through distributed shared memory, so no partial sum goes to HBM).
+// blockIdx.z strides over the tile's distinct adapters.
+template <int MT, int NT, bool VEC>
+__global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_constant__ ProjK k) {
+    pdl_enter();
+    constexpr int ROWS = 16 * MT, RP = 8 * NT;
+    __shared__ int ids[ROWS], list[ROWS], count;
+    extern __shared__ float sh[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+    const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+    const int nd = distinct<ROWS>(k.ids, t0, k.rows, k.n, ids, list, &count, k.status);
+    // rows without an adapter: zeros
+    if (blockIdx.z == 0 && cr == 0)
+        for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
+            if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows) k.out[t0 * k.R + i] = 0.0f;
+    int br[2 * MT];
+    int64_t off[2 * MT];  // of the row in its block
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+        int64_t t = t0 + (i / 2) * 16 + (i & 1) * 8 + g;
+        if (t >= k.rows) t = k.rows - 1;  // never loaded: its adapter is -1
+        br[i] = (int)(t / k.x.brows) * k.x.b1;
+        off[i] = (t % k.x.brows) * k.x.bcols;
+    }
+    const int64_t per_block = (k.x.bcols + 63) / 64, chunks = per_block * k.x.b1;
+    for (int d = blockIdx.z; d < nd; d += gridDim.z) {
+        const int a = list[d];
+        const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols;
+        bool mine[2 * MT];
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) mine[i] = ids[(i / 2) * 16 + (i & 1) * 8 + g] == a;
+        float acc[MT * NT * 4];
+#pragma unroll
+        for (int i = 0; i < MT * NT * 4; ++i) acc[i] = 0.0f;
+        for (int64_t ch = warp + (int64_t)kWarps * cr; ch < chunks; ch += (int64_t)kWarps * cs) {
+            const int blk = (int)(ch / per_block);
+            const int64_t c0 = (ch - blk * per_block) * 64;
+            Raw8 x[2][2 * MT];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    const int64_t c = c0 + u * 32 + q * 8;
+                    x[u][i] = Raw8{{0, 0, 0, 0}};
+                    if (mine[i] && c < k.x.bcols && in_bounds(k.status, off[i] + c, 1, k.x.brows * k.x.bcols))
+                        x[u][i] = load8<VEC>((const bf16 *)k.x.at[br[i] + blk] + off[i], c, k.x.bcols);
+                }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t c = c0 + u * 32 + q * 8;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    Raw8 b = Raw8{{0, 0, 0, 0}};
+                    const int r = j * 8 + g;
+                    if (r < k.R && c < k.x.bcols &&
+                        in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + blk * k.x.bcols + c, 1,
+                                  (int64_t)k.n * k.R * k.cols))
+                        b = load8<VEC>(w + r * k.cols + blk * k.x.bcols, c, k.x.bcols);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        float *s = acc + (m * NT + j) * 4;
+                        const Raw8 &lo = x[u][2 * m], &hi = x[u][2 * m + 1];
+                        mma(s, lo.w[0], hi.w[0], lo.w[1], hi.w[1], b.w[0], b.w[1]);
+                        mma(s, lo.w[2], hi.w[2], lo.w[3], hi.w[3], b.w[2], b.w[3]);
+                    }
+                }
+            }
+        }
+        sum_warps<MT * NT * 4>(acc, sh);
+        if (warp == 0)
+#pragma unroll
+            for (int i = 0; i < MT * NT * 4; ++i) sh[i * 32 + lane] = acc[i];
+        if (cs > 1) cluster.sync();
+        else __syncthreads();
+        const float scale = k.scale ? k.scale[a] : 1.0f;
+        const int part = MT * NT * 4 * 32 / cs;
+        for (int e = cr * part + threadIdx.x; e < (cr + 1) * part; e += kThreads) {
+            float v = 0.0f;
+            for (int b = 0; b < cs; ++b) v += cs > 1 ? *cluster.map_shared_rank(sh + e, b) : sh[e];
+            const int i = e / 32, l = e & 31, c = i & 3, j = (i / 4) % NT, m = i / (4 * NT);
+            const int row = m * 16 + (l >> 2) + (c >> 1) * 8, r = j * 8 + (l & 3) * 2 + (c & 1);
+            if (ids[row] == a && r < k.R && in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
+                k.out[(t0 + row) * k.R + r] = k.scale ? v * scale : v;
+        }
+        if (cs > 1) cluster.sync();  // nobody overwrites, or leaves with, what another CTA still reads
+        else __syncthreads();
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float as_float(T v) { return (float)v; }
+
+// Any types, on CUDA cores: 32 rows x 16 NR adapter rows per CTA, columns in
+// chunks of 32 through shared memory, the cluster sharing the chunks.
+template <typename TX, typename TW, int NR>
+__global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_constant__ ProjK k) {
+    pdl_enter();
+    constexpr int ROWS = 32, RP = 16 * NR;
+    __shared__ int ids[ROWS], list[ROWS], count;
+    __shared__ float xs[ROWS][33], ws[RP][33], part[ROWS * RP];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+    const int nd = distinct<ROWS>(k.ids, t0, k.rows, k.n, ids, list, &count, k.status);
+    if (blockIdx.z == 0 && cr == 0)
+        for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
+            if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows) k.out[t0 * k.R + i] = 0.0f;
+    const int64_t per_block = (k.x.bcols + 31) / 32, chunks = per_block * k.x.b1;
+    for (int d = blockIdx.z; d < nd; d += gridDim.z) {
+        const int a = list[d];
+        const TW *w = (const TW *)k.w + (int64_t)a * k.R * k.cols;
+        float acc[2][NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) acc[0][i] = acc[1][i] = 0.0f;
+        for (int64_t ch = cr; ch < chunks; ch += cs) {
+            const int blk = (int)(ch / per_block);
+            const int64_t c = (ch - blk * per_block) * 32 + (threadIdx.x & 31);
+            for (int row = threadIdx.x / 32; row < ROWS; row += kWarps) {
+                const int64_t t = t0 + row;
+                float v = 0.0f;
+                if (ids[row] == a && c < k.x.bcols) {
+                    const int64_t at = (t % k.x.brows) * k.x.bcols + c;
+                    if (in_bounds(k.status, at, 1, k.x.brows * k.x.bcols))
+                        v = as_float(((const TX *)k.x.at[(t / k.x.brows) * k.x.b1 + blk])[at]);
+                }
+                xs[row][threadIdx.x & 31] = v;
+            }
+            for (int r = threadIdx.x / 32; r < RP; r += kWarps)
+                ws[r][threadIdx.x & 31] =
+                    r < k.R && c < k.x.bcols ? as_float(w[r * k.cols + blk * k.x.bcols + c]) : 0.0f;
+            __syncthreads();
+#pragma unroll
+            for (int c2 = 0; c2 < 32; ++c2) {
+                const float x0 = xs[ty][c2], x1 = xs[ty + 16][c2];
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const float v = ws[tx + 16 * i][c2];
+                    acc[0][i] = fmaf(x0, v, acc[0][i]);
+                    acc[1][i] = fmaf(x1, v, acc[1][i]);
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            part[ty * RP + tx + 16 * i] = acc[0][i];
+            part[(ty + 16) * RP + tx + 16 * i] = acc[1][i];
+        }
+        if (cs > 1) cluster.sync();
+        else __syncthreads();
+        const int share = ROWS * RP / cs;
+        for (int e = cr * share + threadIdx.x; e < (cr + 1) * share; e += kThreads) {
+            float v = 0.0f;
+            for (int b = 0; b < cs; ++b) v += cs > 1 ? *cluster.map_shared_rank(part + e, b) : part[e];
+            const int row = e / RP, r = e % RP;
+            if (ids[row] == a && r < k.R && in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
+                k.out[(t0 + row) * k.R + r] = k.scale ? v * k.scale[a] : v;
+        }
+        if (cs > 1) cluster.sync();
+        else __syncthreads();
+    }
+}
+
+// ---- expand ----------------------------------------------------------------
+
+// Eight consecutive outputs: base + v, or base alone, bit for bit (no
+// adapter).  VEC as for load8.
+template <typename T, bool VEC>
+__device__ __forceinline__ void put8(const T *base, T *out, int64_t at, int64_t left, const float *v) {
+    if constexpr (VEC) {
+        constexpr int W = sizeof(T) / 2;  // 16-byte vectors
+        uint4 b[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) b[i] = base ? reinterpret_cast<const uint4 *>(base + at)[i] : make_uint4(0, 0, 0, 0);
+        if (v) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(b);
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 h =
+                        __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + v[2 * i],
+                                              __uint_as_float(w[i] & 0xffff0000u) + v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) reinterpret_cast<uint4 *>(out + at)[i] = b[i];
+    } else {
+        for (int i = 0; i < 8 && i < left; ++i) {
+            T b = base ? base[at + i] : T(0.0f);
+            if (v) b = T(as_float(b) + v[i]);
+            out[at + i] = b;
+        }
+    }
+}
+
+// Rows of the tile without an adapter: base as it is.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const ExpandK &k, int rank, const int *ids, int nrows, int64_t l0,
+                                          int64_t lrows, int64_t c0, int64_t width) {
+    const T *base = (const T *)k.base[rank];
+    T *out = (T *)k.out[rank];
+    if (base == out) return;
+    for (int i = 0; i < nrows; ++i) {
+        if (ids[i] >= 0 || l0 + i >= lrows) continue;
+        const int64_t row = (l0 + i) * k.bcols;
+        for (int64_t c = c0 + threadIdx.x; c < c0 + width && c < k.bcols; c += kThreads)
+            if (in_bounds(k.status, row + c, 1, k.brows * k.bcols)) out[row + c] = base ? base[row + c] : T(0.0f);
+    }
+}
+
+// A CTA takes 16 MT rows of one rank's box x 512 columns (64 per warp): the
+// adapter's 16 KT x 64 piece is loaded once and stays in registers over the
+// rows.  Each thread ends with 16 consecutive columns of a row, so base and
+// output move in 16-byte vectors straight from and to registers.
+// blockIdx.x: rank x row tile; blockIdx.z strides over the tile's adapters.
+template <int MT, int KT, bool VEC, typename TO>
+__global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_constant__ ExpandK k) {
+    pdl_enter();
+    constexpr int ROWS = 16 * MT, RP = 16 * KT, PITCH = RP + 8;
+    constexpr int PARTS = sizeof(TO) == 4 ? 3 : 2;
+    __shared__ int ids[ROWS], list[ROWS], count;
+    __shared__ __align__(16) bf16 ss[PARTS][ROWS][PITCH];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+    const int rank = blockIdx.x / k.row_tiles;
+    const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;  // in the rank's box
+    const int64_t t0 = k.row0[rank] * k.brows + l0;                 // in the batch
+    const int64_t t1 = (k.row0[rank] + 1) * k.brows;
+    const int nd = distinct<ROWS>(k.ids, t0, t1 < k.rows ? t1 : k.rows, k.n, ids, list, &count, k.status);
+    if (blockIdx.z == 0) copy_rows<TO>(k, rank, ids, ROWS, l0, k.brows, (int64_t)blockIdx.y * 512, 512);
+    if ((int)blockIdx.z >= nd) return;
+    for (int i = threadIdx.x; i < ROWS * RP / 2; i += kThreads) {
+        const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
+        float lo = 0.0f, hi = 0.0f;
+        if (ids[row] >= 0) {
+            if (r < k.R) lo = k.s[(t0 + row) * k.R + r];
+            if (r + 1 < k.R) hi = k.s[(t0 + row) * k.R + r + 1];
+        }
+        uint32_t p[PARTS];
+        split<PARTS>(lo, hi, p);
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(&ss[h][row][r]) = p[h];
+    }
+    __syncthreads();
+    const int64_t c0 = (int64_t)blockIdx.y * 512 + warp * 64;
+    if (c0 >= k.bcols) return;
+    const int64_t col = k.col0[rank] * k.bcols;  // of the box in the factor
+    const TO *base = (const TO *)k.base[rank];
+    TO *out = (TO *)k.out[rank];
+    for (int d = blockIdx.z; d < nd; d += gridDim.z) {
+        const int a = list[d];
+        const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols + col;
+        uint32_t b[KT][8][2];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            Raw8 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
+                const int64_t c = c0 + g * 8;
+                v[i] = Raw8{{0, 0, 0, 0}};
+                if (r < k.R && c < k.bcols &&
+                    in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1, (int64_t)k.n * k.R * k.cols))
+                    v[i] = load8<VEC>(w + r * k.cols, c, k.bcols);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                b[kt][j][0] = __byte_perm(v[0].w[j / 2], v[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+                b[kt][j][1] = __byte_perm(v[2].w[j / 2], v[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+            }
+        }
+        const float scale = k.scale ? k.scale[a] : 1.0f;
+#pragma unroll 1
+        for (int m = 0; m < MT; ++m) {
+            const bool lo_row = ids[m * 16 + g] == a, hi_row = ids[m * 16 + 8 + g] == a;
+            if (!__any_sync(0xffffffffu, lo_row || hi_row)) continue;
+            float acc[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int h = PARTS - 1; h >= 0; --h) {
+                    uint32_t f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[i] = *reinterpret_cast<const uint32_t *>(
+                            &ss[h][m * 16 + g + (i & 1) * 8][kt * 16 + 2 * q + (i >> 1) * 8]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mma(acc[j], f[0], f[1], f[2], f[3], b[kt][j][0], b[kt][j][1]);
+                }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!(half ? hi_row : lo_row)) continue;
+                const int64_t row = (l0 + m * 16 + half * 8 + g) * k.bcols;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int64_t c = c0 + 16 * q + 8 * p;
+                    if (c >= k.bcols || !in_bounds(k.status, row + c, 1, k.brows * k.bcols)) continue;
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = acc[j][half * 2 + p] * scale;
+                    put8<TO, VEC>(base, out, row + c, k.bcols - c, v);
+                }
+            }
+        }
+    }
+}
+
+// Any types, on CUDA cores: 16 rows x 256 columns, a column per thread.
+template <typename TW, typename TO>
+__global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_constant__ ExpandK k) {
+    pdl_enter();
+    constexpr int ROWS = 16, RMAX = 64;
+    __shared__ int ids[ROWS], list[ROWS], count;
+    __shared__ float ss[RMAX][ROWS];
+    const int rank = blockIdx.x / k.row_tiles;
+    const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;
+    const int64_t t0 = k.row0[rank] * k.brows + l0, t1 = (k.row0[rank] + 1) * k.brows;
+    const int nd = distinct<ROWS>(k.ids, t0, t1 < k.rows ? t1 : k.rows, k.n, ids, list, &count, k.status);
+    if (blockIdx.z == 0) copy_rows<TO>(k, rank, ids, ROWS, l0, k.brows, (int64_t)blockIdx.y * 256, 256);
+    for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads) {
+        const int row = i / k.R, r = i % k.R;
+        ss[r][row] = ids[row] >= 0 ? k.s[(t0 + row) * k.R + r] : 0.0f;
+    }
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    if (c >= k.bcols) return;
+    const TO *base = (const TO *)k.base[rank];
+    TO *out = (TO *)k.out[rank];
+    for (int d = blockIdx.z; d < nd; d += gridDim.z) {
+        const int a = list[d];
+        const TW *w = (const TW *)k.w + (int64_t)a * k.R * k.cols + k.col0[rank] * k.bcols + c;
+        float acc[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) acc[i] = 0.0f;
+        for (int r = 0; r < k.R; ++r) {
+            const float v = as_float(w[r * k.cols]);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(ss[r][i], v, acc[i]);
+        }
+        const float scale = k.scale ? k.scale[a] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int64_t at = (l0 + i) * k.bcols + c;
+            if (ids[i] != a || !in_bounds(k.status, at, 1, k.brows * k.bcols)) continue;
+            out[at] = TO((base ? as_float(base[at]) : 0.0f) + acc[i] * scale);
+        }
+    }
+}
+
+// ---- outer -----------------------------------------------------------------
+
+constexpr int kScan = 2048;  // rows whose adapters are scanned at a time
+
+// Rows of [t0, t0 + kScan) with adapter a, ascending, into list; returns how
+// many.
+__device__ __forceinline__ int rows_of(const int *ids, int64_t t0, int64_t rows, int a, int *list, int *scratch,
+                                       int *status) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    constexpr int PER = kScan / kWarps / 32;  // rounds of 32 rows per warp
+    unsigned hit[PER];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + warp * (kScan / kWarps) + i * 32 + lane;
+        const bool ok = t < rows && in_bounds(status, t, 1, rows) && ids[t] == a;
+        hit[i] = __ballot_sync(0xffffffffu, ok);
+        mine += __popc(hit[i]);
+    }
+    __syncthreads();  // scratch and list are free
+    if (lane == 0) scratch[warp] = mine;
+    __syncthreads();
+    int at = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) at += scratch[i];
+        total += scratch[i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (hit[i] >> lane & 1)
+            list[at + __popc(hit[i] & ((1u << lane) - 1))] = (int)(t0 + warp * (kScan / kWarps) + i * 32 + lane);
+        at += __popc(hit[i]);
+    }
+    __syncthreads();
+    return total;
+}
+
+// A CTA takes one adapter and 64 columns; its warps share the adapter's rows
+// in steps of 16, each warp with the whole 16 MT x 64 result in registers,
+// summed over the warps at the end.
+template <int MT, bool VEC>
+__global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_constant__ OuterK k) {
+    pdl_enter();
+    __shared__ int list[kScan], scratch[kWarps];
+    extern __shared__ float sh[];
+    const int which = (int)blockIdx.x >= k.job[0].tiles;
+    const OuterJob &J = k.job[which];
+    const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
+    const int per_block = (int)((J.x.bcols + 63) / 64);
+    const int blk = tile / per_block;
+    const int64_t c0 = (int64_t)(tile - blk * per_block) * 64;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+    float acc[MT][8][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+    for (int64_t t0 = 0; t0 < k.rows; t0 += kScan) {
+        const int have = rows_of(k.ids, t0, k.rows, a, list, scratch, k.status);
+        for (int s = warp * 16; s < have; s += kWarps * 16) {
+            int64_t t[4];
+            Raw8 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = s + 2 * q + (i & 1) + (i >> 1) * 8;
+                t[i] = at < have ? list[at] : -1;
+                x[i] = Raw8{{0, 0, 0, 0}};
+                const int64_t c = c0 + g * 8;
+                if (t[i] >= 0 && c < J.x.bcols) {
+                    const int64_t off = (t[i] % J.x.brows) * J.x.bcols;
+                    if (in_bounds(k.status, off + c, 1, J.x.brows * J.x.bcols))
+                        x[i] = load8<VEC>((const bf16 *)J.x.at[(t[i] / J.x.brows) * J.x.b1 + blk] + off, c, J.x.bcols);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                uint32_t f[4][3];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // rows r (+8 for odd i), summed rows t (+8 for i >= 2)
+                    const int r = m * 16 + g + (i & 1) * 8;
+                    const int64_t ta = t[(i >> 1) * 2], tb = t[(i >> 1) * 2 + 1];
+                    const float lo = r < k.R && ta >= 0 ? J.s[ta * k.R + r] : 0.0f;
+                    const float hi = r < k.R && tb >= 0 ? J.s[tb * k.R + r] : 0.0f;
+                    split<3>(lo, hi, f[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t b0 = __byte_perm(x[0].w[j / 2], x[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+                    const uint32_t b1 = __byte_perm(x[2].w[j / 2], x[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+                    for (int h = 2; h >= 0; --h) mma(acc[m][j], f[0][h], f[1][h], f[2][h], f[3][h], b0, b1);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    sum_warps<MT * 32>(&acc[0][0][0], sh);
+    if (warp) return;
+    const float scale = J.scale ? J.scale[a] : 1.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = m * 16 + g + (i >> 1) * 8;
+            const int64_t c = c0 + 16 * q + 8 * (i & 1);  // and the seven after it
+            if (r >= k.R) continue;
+            float *o = J.out + ((int64_t)a * k.R + r) * J.cols + blk * J.x.bcols;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < J.x.bcols &&
+                    in_bounds(k.status, ((int64_t)a * k.R + r) * J.cols + blk * J.x.bcols + c + j, 1,
+                              (int64_t)k.n * k.R * J.cols))
+                    o[c + j] = acc[m][j][i] * scale;
+        }
+}
+
+// Any types, on CUDA cores: one adapter, 256 columns (one per thread) and 16
+// adapter rows per CTA.
+template <typename TX>
+__global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
+    pdl_enter();
+    __shared__ int list[kScan], scratch[kWarps];
+    __shared__ float ss[32][16];
+    const OuterJob &J = k.job[0];
+    const int r0 = blockIdx.z * 16, a = blockIdx.y;
+    const int per_block = (int)((J.x.bcols + 255) / 256);
+    const int blk = blockIdx.x / per_block;
+    const int64_t c = (int64_t)(blockIdx.x - blk * per_block) * 256 + threadIdx.x;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (int64_t t0 = 0; t0 < k.rows; t0 += kScan) {
+        const int have = rows_of(k.ids, t0, k.rows, a, list, scratch, k.status);
+        for (int s = 0; s < have; s += 32) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < 32 * 16; i += kThreads) {
+                const int u = i / 16, r = r0 + i % 16;
+                ss[u][i % 16] = s + u < have && r < k.R ? J.s[(int64_t)list[s + u] * k.R + r] : 0.0f;
+            }
+            __syncthreads();
+            for (int u = 0; u < 32 && s + u < have; ++u) {
+                const int64_t t = list[s + u], at = (t % J.x.brows) * J.x.bcols + c;
+                if (c >= J.x.bcols || !in_bounds(k.status, at, 1, J.x.brows * J.x.bcols)) continue;
+                const float x = as_float(((const TX *)J.x.at[(t / J.x.brows) * J.x.b1 + blk])[at]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[u][i], x, acc[i]);
+            }
+        }
+    }
+    if (c >= J.x.bcols) return;
+    const float scale = J.scale ? J.scale[a] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t at = ((int64_t)a * k.R + r0 + i) * J.cols + blk * J.x.bcols + c;
+        if (r0 + i < k.R && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols)) J.out[at] = acc[i] * scale;
+    }
+}
+
+// ---- launches --------------------------------------------------------------
+
+int sms() {
+    static shmm::PerDevice<int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= shmm::kMaxDevices) return 152;
+    int n = cache.get(dev);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+        cache.set(dev, n);
+    }
+    return n;
+}
+
+// Lets `kern` take `bytes` of dynamic shared memory on the current device.
+template <typename K>
+cudaError_t opt_in(K kern, size_t bytes, shmm::PerDevice<int> *done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= shmm::kMaxDevices) return cudaErrorInvalidDevice;
+    if (done->get(dev)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done->set(dev, 1);
+    return e;
+}
+
+void fill(Blocks *b, const shmm::BlockGrid &g) {
+    for (int i = 0; i < g.b0 * g.b1; ++i) b->at[i] = g.at[i];
+    b->b1 = g.b1;
+    b->brows = g.brows;
+    b->bcols = g.bcols;
+}
+
+// Cluster size and adapter stride of a projection whose row tiles alone are
+// `tiles` CTAs: the chunks are shared by up to 8 CTAs until every SM has one
+// or two, and the tile's adapters by up to as many CTAs as it has rows.
+void spread(int64_t tiles, int rows_per_tile, int n, int64_t chunks_per_warp, int *cluster, int *slots) {
+    const int64_t want = 2 * sms();
+    int64_t z = n < rows_per_tile ? n : rows_per_tile;
+    if (tiles * z > 8 * want) z = 8 * want / tiles > 1 ? 8 * want / tiles : 1;
+    if (tiles >= want) z = 1;
+    int c = 1;
+    while (c < 8 && tiles * c < want && chunks_per_warp > c) c *= 2;
+    *cluster = c;
+    *slots = (int)z;
+}
+
+template <int MT, int NT, bool VEC>
+cudaError_t project_mma(const ProjK &k, cudaStream_t s) {
+    constexpr size_t smem = (size_t)kWarps / 2 * MT * NT * 4 * 32 * sizeof(float);
+    auto kern = project_mma_kernel<MT, NT, VEC>;
+    static shmm::PerDevice<int> done;
+    cudaError_t e = opt_in(kern, smem, &done);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (k.rows + 16 * MT - 1) / (16 * MT);
+    int cluster, slots;
+    spread(tiles, 16 * MT, k.n, (k.cols + 64 * kWarps - 1) / (64 * kWarps), &cluster, &slots);
+    return launch_pdl_cluster(kern, dim3((unsigned)tiles, cluster, slots), dim3(1, cluster, 1), dim3(kThreads), smem,
+                              s, k);
+}
+
+template <int NT, bool VEC>
+cudaError_t project_rows(const ProjK &k, cudaStream_t s) {
+    return k.rows >= 64 * sms() ? project_mma<4, NT, VEC>(k, s) : project_mma<1, NT, VEC>(k, s);
+}
+
+template <bool VEC>
+cudaError_t project_vec(const ProjK &k, cudaStream_t s) {
+    if (k.R <= 8) return project_rows<1, VEC>(k, s);
+    if (k.R <= 16) return project_rows<2, VEC>(k, s);
+    if (k.R <= 32) return project_rows<4, VEC>(k, s);
+    return project_rows<8, VEC>(k, s);
+}
+
+template <typename TX, typename TW>
+cudaError_t project_simt(const ProjK &k, cudaStream_t s) {
+    const int64_t tiles = (k.rows + 31) / 32;
+    int cluster, slots;
+    spread(tiles, 32, k.n, (k.cols + 31) / 32, &cluster, &slots);
+    const dim3 g((unsigned)tiles, cluster, slots), c(1, cluster, 1);
+    if (k.R <= 16) return launch_pdl_cluster(project_simt_kernel<TX, TW, 1>, g, c, dim3(kThreads), 0, s, k);
+    if (k.R <= 32) return launch_pdl_cluster(project_simt_kernel<TX, TW, 2>, g, c, dim3(kThreads), 0, s, k);
+    return launch_pdl_cluster(project_simt_kernel<TX, TW, 4>, g, c, dim3(kThreads), 0, s, k);
+}
+
+cudaError_t project(const ProjK &k, shmm_dtype_t xt, shmm_dtype_t wt, cudaStream_t s) {
+    shmm::count_launch();
+    if (xt == SHMM_BF16 && wt == SHMM_BF16)
+        return k.cols % 8 == 0 && k.x.bcols % 8 == 0 ? project_vec<true>(k, s) : project_vec<false>(k, s);
+    if (xt == SHMM_F32) return wt == SHMM_F32 ? project_simt<float, float>(k, s) : project_simt<float, bf16>(k, s);
+    return project_simt<bf16, float>(k, s);
+}
+
+template <int MT, int KT, bool VEC, typename TO>
+cudaError_t expand_mma(ExpandK k, int nranks, cudaStream_t s) {
+    k.row_tiles = (int)((k.brows + 16 * MT - 1) / (16 * MT));
+    const int64_t tiles = (int64_t)k.row_tiles * nranks * ((k.bcols + 511) / 512);
+    int cluster, slots;
+    spread(tiles, 16 * MT, k.n, 1, &cluster, &slots);
+    return launch_pdl(expand_mma_kernel<MT, KT, VEC, TO>,
+                      dim3((unsigned)(k.row_tiles * nranks), (unsigned)((k.bcols + 511) / 512), slots), dim3(kThreads),
+                      0, s, k);
+}
+
+template <bool VEC, typename TO>
+cudaError_t expand_vec(const ExpandK &k, int nranks, cudaStream_t s) {
+    const bool many = k.brows >= 64 && k.brows / 64 * nranks * ((k.bcols + 511) / 512) >= sms();
+    if (k.R <= 16) return many ? expand_mma<4, 1, VEC, TO>(k, nranks, s) : expand_mma<1, 1, VEC, TO>(k, nranks, s);
+    if (k.R <= 32) return many ? expand_mma<4, 2, VEC, TO>(k, nranks, s) : expand_mma<1, 2, VEC, TO>(k, nranks, s);
+    return many ? expand_mma<4, 4, VEC, TO>(k, nranks, s) : expand_mma<1, 4, VEC, TO>(k, nranks, s);
+}
+
+template <typename TO>
+cudaError_t expand_type(ExpandK k, int nranks, shmm_dtype_t wt, cudaStream_t s) {
+    if (wt == SHMM_BF16)
+        return k.cols % 8 == 0 && k.bcols % 8 == 0 ? expand_vec<true, TO>(k, nranks, s)
+                                                   : expand_vec<false, TO>(k, nranks, s);
+    k.row_tiles = (int)((k.brows + 15) / 16);
+    const int64_t tiles = (int64_t)k.row_tiles * nranks * ((k.bcols + 255) / 256);
+    int cluster, slots;
+    spread(tiles, 16, k.n, 1, &cluster, &slots);
+    return launch_pdl(expand_simt_kernel<float, TO>,
+                      dim3((unsigned)(k.row_tiles * nranks), (unsigned)((k.bcols + 255) / 256), slots), dim3(kThreads),
+                      0, s, k);
+}
+
+cudaError_t expand(const ExpandK &k, int nranks, shmm_dtype_t wt, shmm_dtype_t ot, cudaStream_t s) {
+    shmm::count_launch();
+    return ot == SHMM_F32 ? expand_type<float>(k, nranks, wt, s) : expand_type<bf16>(k, nranks, wt, s);
+}
+
+template <int MT, bool VEC>
+cudaError_t outer_mma(const OuterK &k, cudaStream_t s) {
+    constexpr size_t smem = (size_t)kWarps / 2 * MT * 32 * 32 * sizeof(float);
+    auto kern = outer_mma_kernel<MT, VEC>;
+    static shmm::PerDevice<int> done;
+    cudaError_t e = opt_in(kern, smem, &done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)(k.job[0].tiles + k.job[1].tiles), (unsigned)k.n), dim3(kThreads), smem, s,
+                      k);
+}
+
+// One or both gradient products (job[1].cols == 0: one) of one type.
+cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
+    shmm::count_launch();
+    if (xt == SHMM_F32) {
+        const OuterJob &j = k.job[0];
+        return launch_pdl(outer_simt_kernel<float>,
+                          dim3((unsigned)((j.x.bcols + 255) / 256 * j.x.b1), (unsigned)k.n, (unsigned)((k.R + 15) / 16)),
+                          dim3(kThreads), 0, s, k);
+    }
+    bool vec = true;
+    for (OuterJob &j : k.job) {
+        if (!j.cols) continue;
+        j.tiles = (int)((j.x.bcols + 63) / 64 * j.x.b1);
+        vec = vec && j.x.bcols % 8 == 0;
+    }
+    if (k.R <= 16) return vec ? outer_mma<1, true>(k, s) : outer_mma<1, false>(k, s);
+    if (k.R <= 32) return vec ? outer_mma<2, true>(k, s) : outer_mma<2, false>(k, s);
+    return vec ? outer_mma<4, true>(k, s) : outer_mma<4, false>(k, s);
+}
+
+void fill_expand(ExpandK *k, const shmm::AdapterArgs &a, const shmm::RankBoxes &b) {
+    for (int r = 0; r < b.nranks; ++r) {
+        k->base[r] = b.base ? b.base[r] : nullptr;
+        k->out[r] = b.out[r];
+        k->row0[r] = b.row0[r];
+        k->col0[r] = b.col0[r];
+    }
+    k->brows = b.brows;
+    k->bcols = b.bcols;
+    k->ids = a.ids;
+    k->n = a.n;
+    k->R = a.R;
+    k->rows = a.rows;
+}
+
+}  // namespace
+
+namespace shmm {
+
+size_t adapters_workspace_bytes(int64_t rows, int R) { return (size_t)((rows * R * 4 + 255) / 256 * 256); }
+
+int launch_adapters_forward(const AdapterArgs &a, const BlockGrid &A, const RankBoxes &C, shmm_dtype_t in_dt,
+                            shmm_dtype_t out_dt, int *status, void *stream) {
+    if (a.rows == 0) return 0;
+    cudaStream_t s = (cudaStream_t)stream;
+    ProjK p = {};
+    fill(&p.x, A);
+    p.w = a.down;
+    p.ids = a.ids;
+    p.out = a.low;
+    p.n = a.n;
+    p.R = a.R;
+    p.rows = a.rows;
+    p.cols = a.J;
+    p.status = status;
+    cudaError_t e = project(p, in_dt, in_dt, s);
+    if (e != cudaSuccess) return (int)e;
+    ExpandK x = {};
+    fill_expand(&x, a, C);
+    x.w = a.up;
+    x.scale = a.scale;
+    x.s = a.low;
+    x.cols = a.K;
+    x.status = status;
+    return (int)expand(x, C.nranks, in_dt, out_dt, s);
+}
+
+int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const BlockGrid &A, const RankBoxes &dA,
+                             shmm_dtype_t in_dt, shmm_dtype_t out_dt, int *status, void *stream) {
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (a.rows) {
+        ProjK p = {};
+        fill(&p.x, dC);
+        p.w = a.up;
+        p.ids = a.ids;
+        p.scale = a.scale;
+        p.out = a.dlow;
+        p.n = a.n;
+        p.R = a.R;
+        p.rows = a.rows;
+        p.cols = a.K;
+        p.status = status;
+        if ((e = project(p, out_dt, in_dt, s)) != cudaSuccess) return (int)e;
+    }
+    OuterK o = {};
+    fill(&o.job[0].x, dC);
+    o.job[0].s = a.low;
+    o.job[0].scale = a.scale;
+    o.job[0].out = a.dup;
+    o.job[0].cols = a.K;
+    OuterJob down = {};
+    fill(&down.x, A);
+    down.s = a.dlow;
+    down.out = a.ddown;
+    down.cols = a.J;
+    o.ids = a.ids;
+    o.n = a.n;
+    o.R = a.R;
+    o.rows = a.rows;
+    o.status = status;
+    const bool both = in_dt == SHMM_BF16 && out_dt == SHMM_BF16;
+    if (both) o.job[1] = down;
+    if ((e = outer(o, out_dt, s)) != cudaSuccess) return (int)e;
+    if (!both) {
+        o.job[0] = down;
+        if ((e = outer(o, in_dt, s)) != cudaSuccess) return (int)e;
+    }
+    if (!a.rows) return 0;
+    ExpandK x = {};
+    fill_expand(&x, a, dA);
+    x.w = a.down;
+    x.s = a.dlow;
+    x.cols = a.J;
+    x.status = status;
+    return (int)expand(x, dA.nranks, in_dt, in_dt, s);
+}
+
+}  // namespace shmm

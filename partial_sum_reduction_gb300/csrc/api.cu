@@ -919,6 +919,161 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *p, shmm_dtyp
     });
 }
 
+// A global array held as rank boxes of `tensor`, as a grid of blocks; a block
+// that several ranks hold is read from the lowest.
+static shmm::BlockGrid block_grid(const shmm_plan_t *p, int tensor, int64_t rows, int64_t cols,
+                                  const void *const *ptrs) {
+    shmm::BlockGrid g;
+    const shmm::Box &b = p->boxes[tensor][0];
+    g.brows = b.ext[0];
+    g.bcols = b.ext[1];
+    g.b0 = rows ? (int)(rows / g.brows) : 1;
+    g.b1 = (int)(cols / g.bcols);
+    g.at.assign((size_t)g.b0 * g.b1, nullptr);
+    if (!rows) return g;
+    for (int r = p->nranks - 1; r >= 0; --r) {
+        const shmm::Box &q = p->boxes[tensor][r];
+        g.at[(size_t)(q.off[0] / g.brows * g.b1 + q.off[1] / g.bcols)] = ptrs[r];
+    }
+    return g;
+}
+
+static shmm::RankBoxes rank_boxes(const shmm_plan_t *p, int tensor, int64_t rows, const void *const *base,
+                                  void *const *out) {
+    shmm::RankBoxes b;
+    b.nranks = p->nranks;
+    b.brows = p->boxes[tensor][0].ext[0];
+    b.bcols = p->boxes[tensor][0].ext[1];
+    b.base = base;
+    b.out = out;
+    for (int r = 0; r < p->nranks && rows; ++r) {
+        b.row0.push_back((int)(p->boxes[tensor][r].off[0] / b.brows));
+        b.col0.push_back((int)(p->boxes[tensor][r].off[1] / b.bcols));
+    }
+    return b;
+}
+
+static shmm_status_t check_adapter_shape(const char *fn, int n, int R) {
+    if (n < 1 || n > 65535) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": 1 to 65535 adapters");
+    if (R < 1) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": the adapters' rank must be >= 1");
+    if (R > shmm::kMaxAdapterRank)
+        return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": adapters of rank above " +
+                                              std::to_string(shmm::kMaxAdapterRank));
+    return SHMM_OK;
+}
+
+// What the adapters' calls share: the plan and the adapters' shape.
+static shmm_status_t check_adapters(const char *fn, const shmm_plan_t *p, int n, int R, const int *ids,
+                                    const void *down, const void *up, const float *scale, const float *low) {
+    if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
+    if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+    if (p->flags & SHMM_FLAG_GELU)
+        return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": the adapters' product joins before the GeLU");
+    shmm_status_t st;
+    if ((st = check_adapter_shape(fn, n, R)) != SHMM_OK) return st;
+    if (p->J == 0 || p->K == 0) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": the plan's J or K is 0");
+    const int64_t most = (int64_t)1 << 31;
+    if (p->I >= most || p->J >= most || p->K >= most)
+        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": I, J and K must be below 2^31");
+    if ((st = check_ptr(fn, down, "down", 16)) != SHMM_OK || (st = check_ptr(fn, up, "up", 16)) != SHMM_OK) return st;
+    if (scale && (st = check_ptr(fn, scale, "scale", 4)) != SHMM_OK) return st;
+    if (p->I == 0) return SHMM_OK;
+    if ((st = check_ptr(fn, ids, "row_adapter", 4)) != SHMM_OK || (st = check_ptr(fn, low, "low", 4)) != SHMM_OK)
+        return st;
+    return SHMM_OK;
+}
+
+static shmm::AdapterArgs adapter_args(const shmm_plan_t *p, int n, int R, const int *ids, const void *down,
+                                      const void *up, const float *scale) {
+    shmm::AdapterArgs a;
+    a.n = n;
+    a.R = R;
+    a.rows = p->I;
+    a.J = p->J;
+    a.K = p->K;
+    a.ids = ids;
+    a.down = down;
+    a.up = up;
+    a.scale = scale;
+    return a;
+}
+
+shmm_status_t shmm_adapters_forward(const shmm_plan_t *p, int n_adapters, int rank, const void *const *A_r,
+                                    const int32_t *row_adapter, const void *down, const void *up, const float *scale,
+                                    const void *const *base_r, void *const *C_r, float *low, void *stream) {
+    static const char *fn = "shmm_adapters_forward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_adapters(fn, p, n_adapters, rank, row_adapter, down, up, scale, low)) != SHMM_OK ||
+            (st = check_ptrs(p, A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK ||
+            (st = check_ptrs(p, (const void *const *)C_r, SHMM_TENSOR_C, fn, "C_r")) != SHMM_OK)
+            return st;
+        if (base_r && (st = check_ptrs(p, base_r, SHMM_TENSOR_C, fn, "base_r")) != SHMM_OK) return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        shmm::AdapterArgs a = adapter_args(p, n_adapters, rank, row_adapter, down, up, scale);
+        a.low = low;
+        const int e = shmm::launch_adapters_forward(a, block_grid(p, SHMM_TENSOR_A, p->I, p->J, A_r),
+                                                    rank_boxes(p, SHMM_TENSOR_C, p->I, base_r, C_r), p->in_dt,
+                                                    p->out_dt, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *p, int n_adapters, int rank, size_t *bytes) {
+    static const char *fn = "shmm_adapters_workspace_size";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        if (!p || !bytes) return fail(SHMM_ERR_NULL, std::string(fn) + ": NULL argument");
+        const shmm_status_t st = check_adapter_shape(fn, n_adapters, rank);
+        if (st != SHMM_OK) return st;
+        *bytes = shmm::adapters_workspace_bytes(p->I, rank);
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int rank, const void *const *dC_r,
+                                     const void *const *A_r, const int32_t *row_adapter, const void *down,
+                                     const void *up, const float *scale, const float *low, const void *const *base_r,
+                                     void *const *dA_r, float *ddown, float *dup, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+    static const char *fn = "shmm_adapters_backward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_adapters(fn, p, n_adapters, rank, row_adapter, down, up, scale, low)) != SHMM_OK ||
+            (st = check_ptrs(p, dC_r, SHMM_TENSOR_C, fn, "dC_r")) != SHMM_OK ||
+            (st = check_ptrs(p, A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK ||
+            (st = check_ptrs(p, (const void *const *)dA_r, SHMM_TENSOR_A, fn, "dA_r")) != SHMM_OK ||
+            (st = check_ptr(fn, ddown, "ddown", 4)) != SHMM_OK || (st = check_ptr(fn, dup, "dup", 4)) != SHMM_OK)
+            return st;
+        if (base_r && (st = check_ptrs(p, base_r, SHMM_TENSOR_A, fn, "base_r")) != SHMM_OK) return st;
+        const size_t need = shmm::adapters_workspace_bytes(p->I, rank);
+        if (workspace_bytes < need)
+            return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(workspace_bytes) +
+                                            " bytes, " + std::to_string(need) + " needed");
+        if (need && (st = check_ptr(fn, workspace, "workspace", 256)) != SHMM_OK) return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        shmm::AdapterArgs a = adapter_args(p, n_adapters, rank, row_adapter, down, up, scale);
+        a.low = const_cast<float *>(low);
+        a.dlow = static_cast<float *>(workspace);
+        a.ddown = ddown;
+        a.dup = dup;
+        const int e = shmm::launch_adapters_backward(
+            a, block_grid(p, SHMM_TENSOR_C, p->I, p->K, dC_r), block_grid(p, SHMM_TENSOR_A, p->I, p->J, A_r),
+            rank_boxes(p, SHMM_TENSOR_A, p->I, base_r, dA_r), p->in_dt, p->out_dt, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
 shmm_status_t shmm_run_static_workspace(const shmm_plan_t *p, const void *const *A_r,
                                         const void *const *B_r, void *const *C_r, void *stream) {
     static const char *fn = "shmm_run_static_workspace";

@@ -191,6 +191,39 @@ struct NormBackwardArgs {
 size_t norm_workspace_bytes(int64_t rows, int64_t cols);
 int launch_norm_backward(const NormBackwardArgs &a, int *status, void *stream);
 
+// Low-rank adapters beside a plan's product.  BlockGrid: a global array read
+// in place as a b0 x b1 grid of equal blocks, block i at at[i] (row-major
+// grid).  RankBoxes: each rank's box of an output (and what it adds to, NULL:
+// nothing), placed at block row0[r], col0[r] of the global array.
+struct BlockGrid {
+    int b0 = 1, b1 = 1;
+    int64_t brows = 0, bcols = 0;
+    std::vector<const void *> at;
+};
+struct RankBoxes {
+    int nranks = 0;
+    int64_t brows = 0, bcols = 0;
+    const void *const *base = nullptr;
+    void *const *out = nullptr;
+    std::vector<int> row0, col0;
+};
+struct AdapterArgs {
+    int n = 0, R = 0;               // adapters, their rank (at most kMaxAdapterRank)
+    int64_t rows = 0, J = 0, K = 0;
+    const int *ids = nullptr;       // [rows]
+    const void *down = nullptr, *up = nullptr;  // [n][R][J], [n][R][K], in_dt
+    const float *scale = nullptr;   // [n]
+    float *low = nullptr;           // [rows][R]: forward out, backward in
+    float *dlow = nullptr;          // [rows][R]: backward scratch
+    float *ddown = nullptr, *dup = nullptr;     // [n][R][J], [n][R][K]
+};
+constexpr int kMaxAdapterRank = 64;
+size_t adapters_workspace_bytes(int64_t rows, int R);
+int launch_adapters_forward(const AdapterArgs &a, const BlockGrid &A, const RankBoxes &C, shmm_dtype_t in_dt,
+                            shmm_dtype_t out_dt, int *status, void *stream);
+int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const BlockGrid &A, const RankBoxes &dA,
+                             shmm_dtype_t in_dt, shmm_dtype_t out_dt, int *status, void *stream);
+
 // Copies rectangles between row-major buffers: rectangle i moves h[i] rows of
 // w[i] elements of `elem` bytes from src[i] (row pitch src_ld[i] elements) to
 // dst[i] (pitch dst_ld[i]).  The reshard (all-to-all) collective.

@@ -62,3 +62,9 @@ def layernorm_workspace(rows: int, cols: int, device="cuda") -> Optional[torch.T
     every rank's block, for the gathered form)."""
     n = shmm_layernorm_backward_workspace_size(rows, cols)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def adapters_workspace(plan: Plan, n_adapters: int, rank: int, device="cuda") -> Optional[torch.Tensor]:
+    """Workspace of plan.adapters_backward for adapters of the given rank."""
+    n = plan.adapters_workspace_size(n_adapters, rank)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None

@@ -88,7 +88,8 @@ EXPORTS = ["shmm_plan", "shmm_plan_destroy", "shmm_plan_query", "shmm_plan_rank_
            "shmm_selftest_wait_timeout", "shmm_choose_operand", "shmm_reshard", "shmm_layernorm",
            "shmm_layernorm_all_gather", "shmm_run_host", "shmm_bounds_checked", "shmm_run_batch",
            "shmm_layernorm_forward", "shmm_layernorm_backward_workspace_size", "shmm_layernorm_backward",
-           "shmm_layernorm_all_gather_forward", "shmm_layernorm_all_gather_backward"]
+           "shmm_layernorm_all_gather_forward", "shmm_layernorm_all_gather_backward",
+           "shmm_adapters_forward", "shmm_adapters_workspace_size", "shmm_adapters_backward"]
 
 _lib = None
 
@@ -138,6 +139,10 @@ def lib():
         L.shmm_layernorm_all_gather_forward.argtypes = [P, PP, P, P, ctypes.c_float, PP, PP, PP, P]
         L.shmm_layernorm_all_gather_backward.argtypes = [P, ctypes.c_int, PP, PP, PP, PP, P, PP, P, P, P,
                                                          ctypes.c_size_t, P]
+        L.shmm_adapters_forward.argtypes = [P, ctypes.c_int, ctypes.c_int, PP, P, P, P, P, PP, PP, P, P]
+        L.shmm_adapters_workspace_size.argtypes = [P, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+        L.shmm_adapters_backward.argtypes = [P, ctypes.c_int, ctypes.c_int, PP, PP, P, P, P, P, P, PP, PP, P, P, P,
+                                             ctypes.c_size_t, P]
         L.shmm_reshard.argtypes = [ctypes.POINTER(shmm_mesh_t), ctypes.POINTER(shmm_spec_t),
                                    ctypes.POINTER(shmm_spec_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                    PP, PP, P]
@@ -455,6 +460,49 @@ class Plan:
             _tensors(rstd_r, "rstd", rows, f32), _tensor(gamma, "gamma", cols, f32),
             _tensors(dshard_r, "dshard", block, dt), _tensor(dgamma, "dgamma", cols, f32),
             _tensor(dbeta, "dbeta", cols, f32), ws, ws_bytes, _stream_handle(stream)))
+
+    def adapters_workspace_size(self, n_adapters: int, rank: int) -> int:
+        n = ctypes.c_size_t()
+        _check(lib().shmm_adapters_workspace_size(self._h, int(n_adapters), int(rank), ctypes.byref(n)))
+        return n.value
+
+    def _adapters(self, row_adapter, down, up, scale):
+        """(n, rank, addresses) of the adapters' factors, checked."""
+        dt, (I, J, K) = TORCH_DTYPES[self.in_dtype], self.shape
+        if not isinstance(down, torch.Tensor) or down.dim() != 3:
+            raise ValueError("down must be a CUDA tensor [adapters, rank, J]")
+        n, rank = down.shape[0], down.shape[1]
+        return n, rank, (_tensor(row_adapter, "row_adapter", (I,), torch.int32), _tensor(down, "down", (n, rank, J), dt),
+                         _tensor(up, "up", (n, rank, K), dt),
+                         None if scale is None else _tensor(scale, "scale", (n,), torch.float32))
+
+    def adapters_forward(self, A_r, row_adapter, down, up, scale, base_r, C_r, low, stream=None):
+        """Low-rank adapters beside the plan's product: C = base + scale[a]
+        (A . down[a]^T) . up[a] for the rows of adapter a (see
+        include/shmm.h).  down [n, rank, J], up [n, rank, K]; scale [n] or
+        None; base_r: per-rank tensors (C_r itself included) or None."""
+        n, rank, ptrs = self._adapters(row_adapter, down, up, scale)
+        dt, box = TORCH_DTYPES[self.out_dtype], self._shapes(TENSOR_C)
+        _check(lib().shmm_adapters_forward(
+            self._h, n, rank, _tensors(A_r, "A", self._shapes(TENSOR_A), TORCH_DTYPES[self.in_dtype]), *ptrs,
+            None if base_r is None else _tensors(base_r, "base", box, dt), _tensors(C_r, "C", box, dt),
+            _tensor(low, "low", (self.shape[0], rank), torch.float32), _stream_handle(stream)))
+
+    def adapters_backward(self, dC_r, A_r, row_adapter, down, up, scale, low, base_r, dA_r, ddown, dup, workspace,
+                          stream=None):
+        """Gradient of adapters_forward: dA (+ base), and every adapter's
+        ddown, dup in fp32 (see include/shmm.h).  workspace:
+        helpers.adapters_workspace."""
+        n, rank, ptrs = self._adapters(row_adapter, down, up, scale)
+        dt, box, f32 = TORCH_DTYPES[self.in_dtype], self._shapes(TENSOR_A), torch.float32
+        I, J, K = self.shape
+        ws, ws_bytes = _workspace(workspace)
+        _check(lib().shmm_adapters_backward(
+            self._h, n, rank, _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype]),
+            _tensors(A_r, "A", box, dt), *ptrs, _tensor(low, "low", (I, rank), f32),
+            None if base_r is None else _tensors(base_r, "base", box, dt), _tensors(dA_r, "dA", box, dt),
+            _tensor(ddown, "ddown", (n, rank, J), f32), _tensor(dup, "dup", (n, rank, K), f32), ws, ws_bytes,
+            _stream_handle(stream)))
 
     def run_host(self, A_host, B_host, C_host, A_r, B_r, C_r, workspace=None, stream=None):
         """shmm_run_host: global A [I,J], B [J,K] (CPU tensors, pinned for
