@@ -34,6 +34,7 @@
 #include <cstdint>
 
 #include "checked.cuh"
+#include "device_wait.cuh"
 #include "pdl.cuh"
 #include "shmm_internal.h"
 
@@ -123,6 +124,24 @@ __device__ __forceinline__ Raw8 load8(const bf16 *row, int64_t c, int64_t cols) 
     return r;
 }
 
+// A thread's own queue of 16-byte pieces in shared memory, filled by
+// asynchronous copies: more loads in flight than registers would hold.  Every
+// piece is read by the thread that asked for it, at [piece][thread], so no
+// barrier is needed and no banks conflict.  ok == false: the piece is zeros.
+__device__ __forceinline__ void queue16(uint32_t at, const void *from, bool ok) {
+    const uint32_t bytes = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void queue_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>  // waits until at most LEFT of this thread's groups are in flight
+__device__ __forceinline__ void queue_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ Raw8 read16(const uint4 *p) {
+    const uint4 v = *p;
+    return Raw8{{v.x, v.y, v.z, v.w}};
+}
+
 __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
     asm volatile(
@@ -207,16 +226,30 @@ __device__ __forceinline__ void sum_warps(float *v, float *sh) {
 
 // ---- project ---------------------------------------------------------------
 
-// A CTA takes 16 MT rows; its warps share the columns in chunks of 64, and
+// A CTA takes 16 MT rows; its warps share the columns in chunks of 32 U, and
 // so do the CTAs of a cluster along y when there are few rows (their sums
 // meet through distributed shared memory, so no partial sum goes to HBM).
-// blockIdx.z strides over the tile's distinct adapters.
-template <int MT, int NT, bool VEC>
+// blockIdx.z strides over the tile's distinct adapters.  X and W pieces run
+// ST - 1 chunks ahead through the threads' queues.
+template <int MT, int NT, int U>
+struct ProjShape {
+    static constexpr int kPieces = (2 * MT + NT) * U;  // per thread and chunk
+    static constexpr int kStages = kPieces <= 6 ? 4 : kPieces <= 8 ? 3 : 2;
+    static constexpr size_t kQueue = (size_t)kStages * kPieces * kThreads * 16;
+    static constexpr size_t kSums = (size_t)kWarps / 2 * MT * NT * 4 * 32 * sizeof(float);
+    static constexpr size_t kSmem = kQueue > kSums ? kQueue : kSums;
+};
+
+template <int MT, int NT, int U, bool VEC>
 __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_constant__ ProjK k) {
     pdl_enter();
-    constexpr int ROWS = 16 * MT, RP = 8 * NT;
+    using Shape = ProjShape<MT, NT, U>;
+    constexpr int ROWS = 16 * MT, P = Shape::kPieces, ST = Shape::kStages;
     __shared__ int ids[ROWS], list[ROWS], count;
-    extern __shared__ float sh[];
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *sh = reinterpret_cast<float *>(smem);                                  // after the columns
+    const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;     // [stage * P + piece][thread]
+    const uint32_t queue_at = shmm_dev::smem_u32(smem) + threadIdx.x * 16;
     cg::cluster_group cluster = cg::this_cluster();
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
@@ -232,10 +265,11 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
     for (int i = 0; i < 2 * MT; ++i) {
         int64_t t = t0 + (i / 2) * 16 + (i & 1) * 8 + g;
         if (t >= k.rows) t = k.rows - 1;  // never loaded: its adapter is -1
-        br[i] = (int)(t / k.x.brows) * k.x.b1;
-        off[i] = (t % k.x.brows) * k.x.bcols;
+        br[i] = (int)((uint32_t)t / (uint32_t)k.x.brows) * k.x.b1;
+        off[i] = (int64_t)((uint32_t)t % (uint32_t)k.x.brows) * k.x.bcols;
     }
-    const int64_t per_block = (k.x.bcols + 63) / 64, chunks = per_block * k.x.b1;
+    const int bcols = (int)k.x.bcols, per_block = (bcols + 32 * U - 1) / (32 * U), chunks = per_block * k.x.b1;
+    const int step = kWarps * cs;
     for (int d = blockIdx.z; d < nd; d += gridDim.z) {
         const int a = list[d];
         const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols;
@@ -245,40 +279,84 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
         float acc[MT * NT * 4];
 #pragma unroll
         for (int i = 0; i < MT * NT * 4; ++i) acc[i] = 0.0f;
-        for (int64_t ch = warp + (int64_t)kWarps * cr; ch < chunks; ch += (int64_t)kWarps * cs) {
-            const int blk = (int)(ch / per_block);
-            const int64_t c0 = (ch - blk * per_block) * 64;
-            Raw8 x[2][2 * MT];
+        // Piece i of X (row i % 2 MT) and j of W for columns c.. of block blk:
+        // its address, and whether it exists.
+        auto x_piece = [&](int i, int blk, int c, bool *ok) {
+            *ok = mine[i] && c < bcols && in_bounds(k.status, off[i] + c, 1, k.x.brows * k.x.bcols);
+            return (const bf16 *)k.x.at[br[i] + blk] + off[i];
+        };
+        auto w_piece = [&](int j, int blk, int c, bool *ok) {
+            const int r = j * 8 + g;
+            const int64_t at = r * k.cols + (int64_t)blk * bcols;
+            *ok = r < k.R && c < bcols && in_bounds(k.status, (int64_t)a * k.R * k.cols + at + c, 1,
+                                                    (int64_t)k.n * k.R * k.cols);
+            return w + at;
+        };
+        auto ask = [&](int ch, int stage) {  // the chunk's pieces into the queue
+            if (VEC && ch < chunks) {
+                const int blk = k.x.b1 == 1 ? 0 : ch / per_block, c0 = (ch - blk * per_block) * 32 * U + q * 8;
+                uint32_t at = queue_at + (uint32_t)(stage * P) * kThreads * 16;
+                bool ok;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                    for (int i = 0; i < 2 * MT; ++i, at += kThreads * 16) {
+                        const bf16 *p = x_piece(i, blk, c0 + u * 32, &ok);
+                        queue16(at, ok ? p + c0 + u * 32 : w, ok);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j, at += kThreads * 16) {
+                        const bf16 *p = w_piece(j, blk, c0 + u * 32, &ok);
+                        queue16(at, ok ? p + c0 + u * 32 : w, ok);
+                    }
+                }
+            }
+            queue_commit();
+        };
+        const int ch0 = warp + kWarps * cr;
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) ask(ch0 + i * step, i);
+        int stage = 0;
+        for (int ch = ch0; ch < chunks; ch += step) {
+            ask(ch + (ST - 1) * step, stage == 0 ? ST - 1 : stage - 1);
+            queue_wait<ST - 1>();
+            const int blk = k.x.b1 == 1 ? 0 : ch / per_block, c0 = (ch - blk * per_block) * 32 * U + q * 8;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                Raw8 x[2 * MT];
+                const uint4 *from = queue + (stage * P + u * (2 * MT + NT)) * kThreads;
+                bool ok;
 #pragma unroll
                 for (int i = 0; i < 2 * MT; ++i) {
-                    const int64_t c = c0 + u * 32 + q * 8;
-                    x[u][i] = Raw8{{0, 0, 0, 0}};
-                    if (mine[i] && c < k.x.bcols && in_bounds(k.status, off[i] + c, 1, k.x.brows * k.x.bcols))
-                        x[u][i] = load8<VEC>((const bf16 *)k.x.at[br[i] + blk] + off[i], c, k.x.bcols);
+                    if constexpr (VEC) {
+                        x[i] = read16(from + i * kThreads);
+                    } else {
+                        const bf16 *p = x_piece(i, blk, c0 + u * 32, &ok);
+                        x[i] = ok ? load8<false>(p, c0 + u * 32, bcols) : Raw8{{0, 0, 0, 0}};
+                    }
                 }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int64_t c = c0 + u * 32 + q * 8;
-#pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    Raw8 b = Raw8{{0, 0, 0, 0}};
-                    const int r = j * 8 + g;
-                    if (r < k.R && c < k.x.bcols &&
-                        in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + blk * k.x.bcols + c, 1,
-                                  (int64_t)k.n * k.R * k.cols))
-                        b = load8<VEC>(w + r * k.cols + blk * k.x.bcols, c, k.x.bcols);
+                    Raw8 b;
+                    if constexpr (VEC) {
+                        b = read16(from + (2 * MT + j) * kThreads);
+                    } else {
+                        const bf16 *p = w_piece(j, blk, c0 + u * 32, &ok);
+                        b = ok ? load8<false>(p, c0 + u * 32, bcols) : Raw8{{0, 0, 0, 0}};
+                    }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         float *s = acc + (m * NT + j) * 4;
-                        const Raw8 &lo = x[u][2 * m], &hi = x[u][2 * m + 1];
+                        const Raw8 &lo = x[2 * m], &hi = x[2 * m + 1];
                         mma(s, lo.w[0], hi.w[0], lo.w[1], hi.w[1], b.w[0], b.w[1]);
                         mma(s, lo.w[2], hi.w[2], lo.w[3], hi.w[3], b.w[2], b.w[3]);
                     }
                 }
             }
+            stage = stage + 1 == ST ? 0 : stage + 1;
         }
+        queue_wait<0>();
+        __syncthreads();  // the queues' memory now takes the sums
         sum_warps<MT * NT * 4>(acc, sh);
         if (warp == 0)
 #pragma unroll
@@ -377,80 +455,102 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
 
 // ---- expand ----------------------------------------------------------------
 
-// Eight consecutive outputs: base + v, or base alone, bit for bit (no
-// adapter).  VEC as for load8.
+// Eight consecutive values of base and output, as they lie in memory.
 template <typename T, bool VEC>
-__device__ __forceinline__ void put8(const T *base, T *out, int64_t at, int64_t left, const float *v) {
-    if constexpr (VEC) {
-        constexpr int W = sizeof(T) / 2;  // 16-byte vectors
-        uint4 b[W];
+struct Out8 {
+    static constexpr int W = sizeof(T) / 2;  // 16-byte vectors
+    uint4 b[W];
+    __device__ void load(const T *p, int left) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) b[i] = base ? reinterpret_cast<const uint4 *>(base + at)[i] : make_uint4(0, 0, 0, 0);
-        if (v) {
+            for (int i = 0; i < W; ++i) b[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        } else if constexpr (sizeof(T) == 4) {
             uint32_t *w = reinterpret_cast<uint32_t *>(b);
-            if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + v[i]);
-            } else {
+            for (int i = 0; i < 8; ++i) w[i] = i < left ? __float_as_uint(p[i]) : 0;
+        } else {
+            const Raw8 r = load8<false>(p, 0, left);
+            b[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        }
+    }
+    __device__ void zero() {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 h =
-                        __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + v[2 * i],
-                                              __uint_as_float(w[i] & 0xffff0000u) + v[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
+        for (int i = 0; i < W; ++i) b[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ void add(const float *v) {  // rounds once
+        uint32_t *w = reinterpret_cast<uint32_t *>(b);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + v[2 * i],
+                                                               __uint_as_float(w[i] & 0xffff0000u) + v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
             }
         }
+    }
+    __device__ void store(T *p, int left) const {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) reinterpret_cast<uint4 *>(out + at)[i] = b[i];
-    } else {
-        for (int i = 0; i < 8 && i < left; ++i) {
-            T b = base ? base[at + i] : T(0.0f);
-            if (v) b = T(as_float(b) + v[i]);
-            out[at + i] = b;
+            for (int i = 0; i < W; ++i) __stcs(reinterpret_cast<uint4 *>(p) + i, b[i]);
+        } else {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) {
+                    if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+                    else reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)(w[i / 2] >> (i & 1) * 16);
+                }
         }
     }
-}
+};
 
-// Rows of the tile without an adapter: base as it is.
-template <typename T>
-__device__ __forceinline__ void copy_rows(const ExpandK &k, int rank, const int *ids, int nrows, int64_t l0,
-                                          int64_t lrows, int64_t c0, int64_t width) {
-    const T *base = (const T *)k.base[rank];
-    T *out = (T *)k.out[rank];
-    if (base == out) return;
-    for (int i = 0; i < nrows; ++i) {
-        if (ids[i] >= 0 || l0 + i >= lrows) continue;
-        const int64_t row = (l0 + i) * k.bcols;
-        for (int64_t c = c0 + threadIdx.x; c < c0 + width && c < k.bcols; c += kThreads)
-            if (in_bounds(k.status, row + c, 1, k.brows * k.bcols)) out[row + c] = base ? base[row + c] : T(0.0f);
-    }
-}
-
-// A CTA takes 16 MT rows of one rank's box x 512 columns (64 per warp): the
-// adapter's 16 KT x 64 piece is loaded once and stays in registers over the
-// rows.  Each thread ends with 16 consecutive columns of a row, so base and
-// output move in 16-byte vectors straight from and to registers.
-// blockIdx.x: rank x row tile; blockIdx.z strides over the tile's adapters.
+// A CTA takes 16 MT rows of one rank's box x 512 columns (64 per warp).  An
+// adapter's 16 KT x 64 piece stays in registers until a row tile needs
+// another's.  Each thread ends with 16 consecutive columns of a row, so base
+// and output move in 16-byte vectors straight from and to registers; the next
+// row tile's base is in flight while this one's products run.
+// blockIdx.x: rank x row tile; blockIdx.z strides over a row tile's adapters
+// (and z = 0 copies the rows without one).
 template <int MT, int KT, bool VEC, typename TO>
 __global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_constant__ ExpandK k) {
     pdl_enter();
     constexpr int ROWS = 16 * MT, RP = 16 * KT, PITCH = RP + 8;
     constexpr int PARTS = sizeof(TO) == 4 ? 3 : 2;
-    __shared__ int ids[ROWS], list[ROWS], count;
+    __shared__ int ids[ROWS];
     __shared__ __align__(16) bf16 ss[PARTS][ROWS][PITCH];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
     const int rank = blockIdx.x / k.row_tiles;
     const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;  // in the rank's box
     const int64_t t0 = k.row0[rank] * k.brows + l0;                 // in the batch
-    const int64_t t1 = (k.row0[rank] + 1) * k.brows;
-    const int nd = distinct<ROWS>(k.ids, t0, t1 < k.rows ? t1 : k.rows, k.n, ids, list, &count, k.status);
-    if (blockIdx.z == 0) copy_rows<TO>(k, rank, ids, ROWS, l0, k.brows, (int64_t)blockIdx.y * 512, 512);
-    if ((int)blockIdx.z >= nd) return;
+    const int nrows = (int)(k.brows - l0 < ROWS ? k.brows - l0 : ROWS);
+    const int64_t c0 = (int64_t)blockIdx.y * 512 + warp * 64;
+    const TO *base = (const TO *)k.base[rank];
+    TO *out = (TO *)k.out[rank];
+    Out8<TO, VEC> now[4], next[4];  // [row half * 2 + column half]
+    auto load_base = [&](int m, Out8<TO, VEC> *b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = m * 16 + (i >> 1) * 8 + g;
+            const int64_t c = c0 + 16 * q + 8 * (i & 1), at = (l0 + row) * k.bcols + c;
+            if (base && row < nrows && c < k.bcols && in_bounds(k.status, at, 1, k.brows * k.bcols))
+                b[i].load(base + at, (int)(k.bcols - c));
+            else
+                b[i].zero();
+        }
+    };
+    load_base(0, now);
+    if (threadIdx.x < ROWS) {
+        int a = -1;
+        if ((int)threadIdx.x < nrows && in_bounds(k.status, t0 + threadIdx.x, 1, k.rows)) a = k.ids[t0 + threadIdx.x];
+        ids[threadIdx.x] = a >= 0 && a < k.n ? a : -1;
+    }
     for (int i = threadIdx.x; i < ROWS * RP / 2; i += kThreads) {
         const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
         float lo = 0.0f, hi = 0.0f;
-        if (ids[row] >= 0) {
+        if (row < nrows) {
             if (r < k.R) lo = k.s[(t0 + row) * k.R + r];
             if (r + 1 < k.R) hi = k.s[(t0 + row) * k.R + r + 1];
         }
@@ -460,38 +560,59 @@ __global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_const
         for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(&ss[h][row][r]) = p[h];
     }
     __syncthreads();
-    const int64_t c0 = (int64_t)blockIdx.y * 512 + warp * 64;
     if (c0 >= k.bcols) return;
     const int64_t col = k.col0[rank] * k.bcols;  // of the box in the factor
-    const TO *base = (const TO *)k.base[rank];
-    TO *out = (TO *)k.out[rank];
-    for (int d = blockIdx.z; d < nd; d += gridDim.z) {
-        const int a = list[d];
-        const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols + col;
-        uint32_t b[KT][8][2];
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            Raw8 v[4];
+    int held = -1;                               // the adapter in b
+    float scale = 1.0f;
+    uint32_t b[KT][8][2];
+#pragma unroll 1
+    for (int m = 0; m < MT; ++m) {
+        if (m + 1 < MT) load_base(m + 1, next);
+        auto put = [&](int i, const float *v) {
+            const int row = m * 16 + (i >> 1) * 8 + g;
+            const int64_t c = c0 + 16 * q + 8 * (i & 1), at = (l0 + row) * k.bcols + c;
+            if (c >= k.bcols || !in_bounds(k.status, at, 1, k.brows * k.bcols)) return;
+            if (v) now[i].add(v);
+            now[i].store(out + at, (int)(k.bcols - c));
+        };
+        const int id = ids[m * 16 + (lane & 15)];
+        unsigned todo = __ballot_sync(0xffffffffu, id >= 0) & 0xffffu;
+        if (blockIdx.z == 0 && base != out) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
-                const int64_t c = c0 + g * 8;
-                v[i] = Raw8{{0, 0, 0, 0}};
-                if (r < k.R && c < k.bcols &&
-                    in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1, (int64_t)k.n * k.R * k.cols))
-                    v[i] = load8<VEC>(w + r * k.cols, c, k.bcols);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                b[kt][j][0] = __byte_perm(v[0].w[j / 2], v[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
-                b[kt][j][1] = __byte_perm(v[2].w[j / 2], v[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+                const int row = (i >> 1) * 8 + g;
+                if (!(todo >> row & 1) && m * 16 + row < nrows) put(i, nullptr);
             }
         }
-        const float scale = k.scale ? k.scale[a] : 1.0f;
-#pragma unroll 1
-        for (int m = 0; m < MT; ++m) {
-            const bool lo_row = ids[m * 16 + g] == a, hi_row = ids[m * 16 + 8 + g] == a;
-            if (!__any_sync(0xffffffffu, lo_row || hi_row)) continue;
+        for (int d = 0; todo; ++d) {
+            const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
+            const unsigned same = __ballot_sync(0xffffffffu, id == a) & 0xffffu;
+            todo &= ~same;
+            if (d % gridDim.z != blockIdx.z) continue;
+            if (a != held) {
+                held = a;
+                const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols + col;
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    Raw8 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
+                        const int64_t c = c0 + g * 8;
+                        v[i] = Raw8{{0, 0, 0, 0}};
+                        if (r < k.R && c < k.bcols &&
+                            in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1,
+                                      (int64_t)k.n * k.R * k.cols))
+                            v[i] = load8<VEC>(w + r * k.cols, c, k.bcols);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        b[kt][j][0] = __byte_perm(v[0].w[j / 2], v[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+                        b[kt][j][1] = __byte_perm(v[2].w[j / 2], v[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+                    }
+                }
+                scale = k.scale ? k.scale[a] : 1.0f;
+            }
             float acc[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -510,20 +631,38 @@ __global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_const
                     for (int j = 0; j < 8; ++j) mma(acc[j], f[0], f[1], f[2], f[3], b[kt][j][0], b[kt][j][1]);
                 }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!(half ? hi_row : lo_row)) continue;
-                const int64_t row = (l0 + m * 16 + half * 8 + g) * k.bcols;
+            for (int i = 0; i < 4; ++i) {
+                if (!(same >> ((i >> 1) * 8 + g) & 1)) continue;
+                float v[8];
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const int64_t c = c0 + 16 * q + 8 * p;
-                    if (c >= k.bcols || !in_bounds(k.status, row + c, 1, k.brows * k.bcols)) continue;
-                    float v[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = acc[j][half * 2 + p] * scale;
-                    put8<TO, VEC>(base, out, row + c, k.bcols - c, v);
-                }
+                for (int j = 0; j < 8; ++j) v[j] = acc[j][i] * scale;
+                put(i, v);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) now[i] = next[i];
+    }
+}
+
+// Rows of the tile without an adapter: base as it is.
+template <typename T, int NROWS>
+__device__ __forceinline__ void copy_rows(const ExpandK &k, int rank, const int *ids, int64_t l0, int64_t lrows,
+                                          int64_t c0) {
+    const T *base = (const T *)k.base[rank];
+    T *out = (T *)k.out[rank];
+    const int64_t c = c0 + threadIdx.x;  // width: kThreads
+    if (base == out || c >= k.bcols) return;
+    T v[NROWS];
+#pragma unroll
+    for (int i = 0; i < NROWS; ++i) {
+        const int64_t at = (l0 + i) * k.bcols + c;
+        if (ids[i] < 0 && l0 + i < lrows && in_bounds(k.status, at, 1, k.brows * k.bcols))
+            v[i] = base ? base[at] : T(0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < NROWS; ++i) {
+        const int64_t at = (l0 + i) * k.bcols + c;
+        if (ids[i] < 0 && l0 + i < lrows && in_bounds(k.status, at, 1, k.brows * k.bcols)) out[at] = v[i];
     }
 }
 
@@ -538,7 +677,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
     const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;
     const int64_t t0 = k.row0[rank] * k.brows + l0, t1 = (k.row0[rank] + 1) * k.brows;
     const int nd = distinct<ROWS>(k.ids, t0, t1 < k.rows ? t1 : k.rows, k.n, ids, list, &count, k.status);
-    if (blockIdx.z == 0) copy_rows<TO>(k, rank, ids, ROWS, l0, k.brows, (int64_t)blockIdx.y * 256, 256);
+    if (blockIdx.z == 0) copy_rows<TO, ROWS>(k, rank, ids, l0, k.brows, (int64_t)blockIdx.y * 256);
     for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads) {
         const int row = i / k.R, r = i % k.R;
         ss[r][row] = ids[row] >= 0 ? k.s[(t0 + row) * k.R + r] : 0.0f;
@@ -554,36 +693,76 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
         float acc[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) acc[i] = 0.0f;
-        for (int r = 0; r < k.R; ++r) {
-            const float v = as_float(w[r * k.cols]);
+        for (int r0 = 0; r0 < k.R; r0 += 8) {
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(ss[r][i], v, acc[i]);
+            for (int r = 0; r < 8; ++r) v[r] = r0 + r < k.R ? as_float(w[(r0 + r) * k.cols]) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (r0 + r >= k.R) break;
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(ss[r0 + r][i], v[r], acc[i]);
+            }
         }
         const float scale = k.scale ? k.scale[a] : 1.0f;
+        float old[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const int64_t at = (l0 + i) * k.bcols + c;
-            if (ids[i] != a || !in_bounds(k.status, at, 1, k.brows * k.bcols)) continue;
-            out[at] = TO((base ? as_float(base[at]) : 0.0f) + acc[i] * scale);
+            old[i] = base && ids[i] == a && in_bounds(k.status, at, 1, k.brows * k.bcols) ? as_float(base[at]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int64_t at = (l0 + i) * k.bcols + c;
+            if (ids[i] == a && in_bounds(k.status, at, 1, k.brows * k.bcols)) out[at] = TO(old[i] + acc[i] * scale);
         }
     }
 }
 
 // ---- outer -----------------------------------------------------------------
 
-constexpr int kScan = 2048;  // rows whose adapters are scanned at a time
+// Walk over the rows with adapter a, ascending, from the first'th on: fills
+// list with up to `room` of their pointers' rows.  A CTA scans kScan rows at
+// a time; `at` and `seen` (rows scanned, hits passed) carry the walk on.
+constexpr int kScan = 2048;
+struct Walk {
+    int64_t at;  // next row to scan
+    int seen;    // hits before it
+};
 
-// Rows of [t0, t0 + kScan) with adapter a, ascending, into list; returns how
-// many.
-__device__ __forceinline__ int rows_of(const int *ids, int64_t t0, int64_t rows, int a, int *list, int *scratch,
-                                       int *status) {
+// How many rows have adapter a (every thread gets it).
+__device__ __forceinline__ int count_rows(const int *ids, int64_t rows, int a, int *scratch) {
+    int mine = 0;
+    int64_t t = threadIdx.x;
+    for (; t + 7 * kThreads < rows; t += 8 * kThreads) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ids[t + i * kThreads];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine += v[i] == a;
+    }
+    for (; t < rows; t += kThreads) mine += ids[t] == a;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = mine;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) total += scratch[i];
+    __syncthreads();
+    return total;
+}
+
+// Scans rows [w.at, w.at + kScan) and lists those with adapter a whose place
+// among all of a's rows lies in [lo, hi); returns how many.
+__device__ __forceinline__ int list_rows(const int *ids, int64_t rows, int a, int lo, int hi, Walk &w, int *list,
+                                         int *scratch, int *status) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     constexpr int PER = kScan / kWarps / 32;  // rounds of 32 rows per warp
     unsigned hit[PER];
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int64_t t = t0 + warp * (kScan / kWarps) + i * 32 + lane;
+        const int64_t t = w.at + warp * (kScan / kWarps) + i * 32 + lane;
         const bool ok = t < rows && in_bounds(status, t, 1, rows) && ids[t] == a;
         hit[i] = __ballot_sync(0xffffffffu, ok);
         mine += __popc(hit[i]);
@@ -591,37 +770,61 @@ __device__ __forceinline__ int rows_of(const int *ids, int64_t t0, int64_t rows,
     __syncthreads();  // scratch and list are free
     if (lane == 0) scratch[warp] = mine;
     __syncthreads();
-    int at = 0, total = 0;
+    int place = w.seen, total = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) at += scratch[i];
+        if (i < warp) place += scratch[i];
         total += scratch[i];
     }
+    const int from = w.seen > lo ? w.seen : lo, to = w.seen + total < hi ? w.seen + total : hi;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (hit[i] >> lane & 1)
-            list[at + __popc(hit[i] & ((1u << lane) - 1))] = (int)(t0 + warp * (kScan / kWarps) + i * 32 + lane);
-        at += __popc(hit[i]);
+        const int p = place + __popc(hit[i] & ((1u << lane) - 1));
+        if ((hit[i] >> lane & 1) && p >= from && p < to)
+            list[p - from] = (int)(w.at + warp * (kScan / kWarps) + i * 32 + lane);
+        place += __popc(hit[i]);
     }
+    w.at += kScan;
+    w.seen += total;
     __syncthreads();
-    return total;
+    return to > from ? to - from : 0;
 }
 
-// A CTA takes one adapter and 64 columns; its warps share the adapter's rows
-// in steps of 16, each warp with the whole 16 MT x 64 result in registers,
-// summed over the warps at the end.
+// A CTA takes one adapter and 512 columns, 64 per warp, and a cluster along z
+// shares the adapter's rows (their sums meet through distributed shared
+// memory, in order).  Rows go in groups of 64: the CTA splits their
+// fp32 S values into bf16 operands in shared memory, in the order the matrix
+// instruction wants them (two groups' room, so one barrier per group), while
+// every thread's X pieces run ahead through its queue.
+template <int MT>
+struct OuterShape {
+    static constexpr int kStages = 5;                                       // 16-row steps of X in the queue
+    static constexpr size_t kQueue = (size_t)kStages * 4 * kThreads * 16;
+    static constexpr size_t kOperand = (size_t)4 * MT * 3 * 32 * 16;        // one group of 64 rows
+    static constexpr size_t kSums = (size_t)kThreads * MT * 32 * sizeof(float);
+    static constexpr size_t kSmem = kQueue + 2 * kOperand > kSums ? kQueue + 2 * kOperand : kSums;
+};
+
 template <int MT, bool VEC>
 __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
+    using Shape = OuterShape<MT>;
+    constexpr int ST = Shape::kStages, RP = 16 * MT;
     __shared__ int list[kScan], scratch[kWarps];
-    extern __shared__ float sh[];
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;
+    const uint32_t queue_at = shmm_dev::smem_u32(smem) + threadIdx.x * 16;
+    uint4 *operand = reinterpret_cast<uint4 *>(smem + Shape::kQueue);  // [2][(step * MT + m) * 3 + part][lane]
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
     const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
-    const int per_block = (int)((J.x.bcols + 63) / 64);
-    const int blk = tile / per_block;
-    const int64_t c0 = (int64_t)(tile - blk * per_block) * 64;
+    const int bcols = (int)J.x.bcols, per_block = (bcols + 511) / 512, blk = tile / per_block;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+    const int c0 = (tile - blk * per_block) * 512 + warp * 64;
+    const int cx = c0 + g * 8;  // this thread's columns of X
+    const float *S = J.s;
     float acc[MT][8][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -629,104 +832,198 @@ __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_consta
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-    for (int64_t t0 = 0; t0 < k.rows; t0 += kScan) {
-        const int have = rows_of(k.ids, t0, k.rows, a, list, scratch, k.status);
-        for (int s = warp * 16; s < have; s += kWarps * 16) {
-            int64_t t[4];
-            Raw8 x[4];
+    const int total = count_rows(k.ids, k.rows, a, scratch);
+    // this CTA's share of the rows, in whole groups of 64
+    const int groups = (total + 63) / 64;
+    const int lo = groups * cr / cs * 64, hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
+    Walk walk{0, 0};
+    while (walk.seen < hi && walk.at < k.rows) {
+        const int have = list_rows(k.ids, k.rows, a, lo, hi, walk, list, scratch, k.status);
+        if (!have) continue;
+        const int steps = (have + 15) / 16;
+        auto row_of = [&](int step, int i) {
+            const int at = step * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
+            return at < have ? list[at] : -1;
+        };
+        auto x_piece = [&](int t, bool *ok) {
+            const uint32_t b = (uint32_t)t / (uint32_t)J.x.brows, l = (uint32_t)t - b * (uint32_t)J.x.brows;
+            const int64_t off = (int64_t)l * bcols;
+            *ok = t >= 0 && cx < bcols && in_bounds(k.status, off + cx, 1, J.x.brows * J.x.bcols);
+            return *ok ? (const bf16 *)J.x.at[b * J.x.b1 + blk] + off : (const bf16 *)nullptr;
+        };
+        auto ask = [&](int step, int stage) {
+            if (VEC && step < steps) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = s + 2 * q + (i & 1) + (i >> 1) * 8;
-                t[i] = at < have ? list[at] : -1;
-                x[i] = Raw8{{0, 0, 0, 0}};
-                const int64_t c = c0 + g * 8;
-                if (t[i] >= 0 && c < J.x.bcols) {
-                    const int64_t off = (t[i] % J.x.brows) * J.x.bcols;
-                    if (in_bounds(k.status, off + c, 1, J.x.brows * J.x.bcols))
-                        x[i] = load8<VEC>((const bf16 *)J.x.at[(t[i] / J.x.brows) * J.x.b1 + blk] + off, c, J.x.bcols);
+                for (int i = 0; i < 4; ++i) {
+                    bool ok;
+                    const bf16 *p = x_piece(row_of(step, i), &ok);
+                    queue16(queue_at + (uint32_t)(stage * 4 + i) * kThreads * 16, ok ? (const void *)(p + cx) : S, ok);
                 }
             }
+            queue_commit();
+        };
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                uint32_t f[4][3];
+        for (int i = 0; i < ST - 1; ++i) ask(i, i);
+        int stage = 0;
+        for (int grp = 0; grp * 4 < steps; ++grp) {
+            uint4 *op = operand + (grp & 1) * (4 * MT * 3 * 32);
+            // 32 row pairs x RP: pair (t, t + 1) of r is word w of lane l
+            for (int e = threadIdx.x; e < 32 * RP; e += kThreads) {
+                const int r = e % RP, pair = e / RP, tt = (pair & 7) * 2;
+                const int at = grp * 64 + pair * 2;
+                const float x = r < k.R && at < have ? S[(int64_t)list[at] * k.R + r] : 0.0f;
+                const float y = r < k.R && at + 1 < have ? S[(int64_t)list[at + 1] * k.R + r] : 0.0f;
+                uint32_t p[3];
+                split<3>(x, y, p);
+                const int l = (r & 7) * 4 + ((tt & 7) >> 1), w = ((r >> 3) & 1) + (tt >> 3) * 2;
+                uint32_t *to = reinterpret_cast<uint32_t *>(op + (((pair >> 3) * MT + (r >> 4)) * 3) * 32 + l) + w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // rows r (+8 for odd i), summed rows t (+8 for i >= 2)
-                    const int r = m * 16 + g + (i & 1) * 8;
-                    const int64_t ta = t[(i >> 1) * 2], tb = t[(i >> 1) * 2 + 1];
-                    const float lo = r < k.R && ta >= 0 ? J.s[ta * k.R + r] : 0.0f;
-                    const float hi = r < k.R && tb >= 0 ? J.s[tb * k.R + r] : 0.0f;
-                    split<3>(lo, hi, f[i]);
+                for (int h = 0; h < 3; ++h) to[h * 32 * 4] = p[h];
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int st = 0; st < 4 && grp * 4 + st < steps; ++st) {
+                const int step = grp * 4 + st;
+                ask(step + ST - 1, stage == 0 ? ST - 1 : stage - 1);
+                queue_wait<ST - 1>();
+                Raw8 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (VEC) {
+                        x[i] = read16(queue + (stage * 4 + i) * kThreads);
+                    } else {
+                        bool ok;
+                        const bf16 *p = x_piece(row_of(step, i), &ok);
+                        x[i] = ok ? load8<false>(p, cx, bcols) : Raw8{{0, 0, 0, 0}};
+                    }
                 }
+                stage = stage + 1 == ST ? 0 : stage + 1;
+                uint32_t b[8][2];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t b0 = __byte_perm(x[0].w[j / 2], x[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
-                    const uint32_t b1 = __byte_perm(x[2].w[j / 2], x[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-                    for (int h = 2; h >= 0; --h) mma(acc[m][j], f[0][h], f[1][h], f[2][h], f[3][h], b0, b1);
+                    b[j][0] = __byte_perm(x[0].w[j / 2], x[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
+                    b[j][1] = __byte_perm(x[2].w[j / 2], x[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
                 }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 2; h >= 0; --h) {
+                        const uint4 f = op[((st * MT + m) * 3 + h) * 32 + lane];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) mma(acc[m][j], f.x, f.y, f.z, f.w, b[j][0], b[j][1]);
+                    }
             }
         }
+        queue_wait<0>();
+    }
+    const float scale = J.scale ? J.scale[a] : 1.0f;
+    // Result piece (warp w, m, i): eight columns from 16 q + 8 (i & 1) of w's
+    // 64, row m * 16 + g (+8 for i >= 2).
+    auto put = [&](int w, int m, int i, const float *v) {
+        const int r = m * 16 + g + (i >> 1) * 8, c = c0 + (w - warp) * 64 + 16 * q + 8 * (i & 1);
+        if (r >= k.R || c >= bcols) return;
+        const int64_t at = ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + c;
+        if (!in_bounds(k.status, at, c + 8 <= bcols ? 8 : bcols - c, (int64_t)k.n * k.R * J.cols)) return;
+        float *o = J.out + at;
+        if (VEC && J.cols % 4 == 0 && reinterpret_cast<uintptr_t>(J.out) % 16 == 0) {
+            reinterpret_cast<float4 *>(o)[0] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+            reinterpret_cast<float4 *>(o)[1] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < bcols) o[j] = v[j] * scale;
+        }
+    };
+    if (cs == 1) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = acc[m][j][i];
+                put(warp, m, i, v);
+            }
+        return;
     }
     __syncthreads();
-    sum_warps<MT * 32>(&acc[0][0][0], sh);
-    if (warp) return;
-    const float scale = J.scale ? J.scale[a] : 1.0f;
+    float *sums = reinterpret_cast<float *>(smem);  // [(warp * MT + m) * 4 + i][j][lane]
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = m * 16 + g + (i >> 1) * 8;
-            const int64_t c = c0 + 16 * q + 8 * (i & 1);  // and the seven after it
-            if (r >= k.R) continue;
-            float *o = J.out + ((int64_t)a * k.R + r) * J.cols + blk * J.x.bcols;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < J.x.bcols &&
-                    in_bounds(k.status, ((int64_t)a * k.R + r) * J.cols + blk * J.x.bcols + c + j, 1,
-                              (int64_t)k.n * k.R * J.cols))
-                    o[c + j] = acc[m][j][i] * scale;
+            for (int j = 0; j < 8; ++j) sums[(((warp * MT + m) * 4 + i) * 8 + j) * 32 + lane] = acc[m][j][i];
+    cluster.sync();
+    for (int u = cr + cs * warp; u < kWarps * MT * 4; u += cs * kWarps) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        for (int b = 0; b < cs; ++b) {
+            const float *from = cluster.map_shared_rank(sums + u * 8 * 32 + lane, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += from[j * 32];
         }
+        put(u / (4 * MT), u / 4 % MT, u & 3, v);
+    }
+    cluster.sync();  // nobody leaves with what another CTA still reads
 }
 
-// Any types, on CUDA cores: one adapter, 256 columns (one per thread) and 16
-// adapter rows per CTA.
+// Any types, on CUDA cores: one adapter, 128 columns and 16 adapter rows per
+// CTA; the halves of the CTA take every other group of 16 rows.
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
     __shared__ int list[kScan], scratch[kWarps];
-    __shared__ float ss[32][16];
+    __shared__ float ss[2][16][16];
+    __shared__ float sums[16][128];
     const OuterJob &J = k.job[0];
-    const int r0 = blockIdx.z * 16, a = blockIdx.y;
-    const int per_block = (int)((J.x.bcols + 255) / 256);
+    const int r0 = blockIdx.z * 16, a = blockIdx.y, half = threadIdx.x / 128, th = threadIdx.x % 128;
+    const int per_block = (int)((J.x.bcols + 127) / 128);
     const int blk = blockIdx.x / per_block;
-    const int64_t c = (int64_t)(blockIdx.x - blk * per_block) * 256 + threadIdx.x;
+    const int64_t c = (int64_t)(blockIdx.x - blk * per_block) * 128 + th;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (int64_t t0 = 0; t0 < k.rows; t0 += kScan) {
-        const int have = rows_of(k.ids, t0, k.rows, a, list, scratch, k.status);
-        for (int s = 0; s < have; s += 32) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < 32 * 16; i += kThreads) {
-                const int u = i / 16, r = r0 + i % 16;
-                ss[u][i % 16] = s + u < have && r < k.R ? J.s[(int64_t)list[s + u] * k.R + r] : 0.0f;
-            }
-            __syncthreads();
-            for (int u = 0; u < 32 && s + u < have; ++u) {
-                const int64_t t = list[s + u], at = (t % J.x.brows) * J.x.bcols + c;
-                if (c >= J.x.bcols || !in_bounds(k.status, at, 1, J.x.brows * J.x.bcols)) continue;
-                const float x = as_float(((const TX *)J.x.at[(t / J.x.brows) * J.x.b1 + blk])[at]);
+    Walk walk{0, 0};
+    while (walk.at < k.rows) {
+        const int have = list_rows(k.ids, k.rows, a, 0, 0x7fffffff, walk, list, scratch, k.status);
+        for (int s0 = 0; s0 < have; s0 += 32) {
+            const int s = s0 + half * 16;
+            float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[u][i], x, acc[i]);
+            for (int u = 0; u < 16; ++u) {
+                x[u] = 0.0f;
+                if (s + u < have && c < J.x.bcols) {
+                    const uint32_t t = list[s + u], b = t / (uint32_t)J.x.brows;
+                    const int64_t at = (int64_t)(t - b * (uint32_t)J.x.brows) * J.x.bcols + c;
+                    if (in_bounds(k.status, at, 1, J.x.brows * J.x.bcols))
+                        x[u] = as_float(((const TX *)J.x.at[b * J.x.b1 + blk])[at]);
+                }
             }
+            __syncthreads();
+            for (int i = th; i < 16 * 16; i += 128) {
+                const int u = i / 16, r = r0 + i % 16;
+                ss[half][u][i % 16] = s + u < have && r < k.R ? J.s[(int64_t)list[s + u] * k.R + r] : 0.0f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[half][u][i], x[u], acc[i]);
         }
     }
-    if (c >= J.x.bcols) return;
+    if (half)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[i][th] = acc[i];
+    __syncthreads();
+    if (half || c >= J.x.bcols) return;
     const float scale = J.scale ? J.scale[a] : 1.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int64_t at = ((int64_t)a * k.R + r0 + i) * J.cols + blk * J.x.bcols + c;
-        if (r0 + i < k.R && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols)) J.out[at] = acc[i] * scale;
+        if (r0 + i < k.R && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols))
+            J.out[at] = (acc[i] + sums[i][th]) * scale;
     }
 }
 
@@ -778,23 +1075,24 @@ void spread(int64_t tiles, int rows_per_tile, int n, int64_t chunks_per_warp, in
     *slots = (int)z;
 }
 
-template <int MT, int NT, bool VEC>
+template <int MT, int NT, int U, bool VEC>
 cudaError_t project_mma(const ProjK &k, cudaStream_t s) {
-    constexpr size_t smem = (size_t)kWarps / 2 * MT * NT * 4 * 32 * sizeof(float);
-    auto kern = project_mma_kernel<MT, NT, VEC>;
+    using Shape = ProjShape<MT, NT, U>;
+    auto kern = project_mma_kernel<MT, NT, U, VEC>;
     static shmm::PerDevice<int> done;
-    cudaError_t e = opt_in(kern, smem, &done);
+    cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (k.rows + 16 * MT - 1) / (16 * MT);
     int cluster, slots;
-    spread(tiles, 16 * MT, k.n, (k.cols + 64 * kWarps - 1) / (64 * kWarps), &cluster, &slots);
-    return launch_pdl_cluster(kern, dim3((unsigned)tiles, cluster, slots), dim3(1, cluster, 1), dim3(kThreads), smem,
-                              s, k);
+    spread(tiles, 16 * MT, k.n, (k.cols + 32 * U * kWarps - 1) / (32 * U * kWarps), &cluster, &slots);
+    return launch_pdl_cluster(kern, dim3((unsigned)tiles, cluster, slots), dim3(1, cluster, 1), dim3(kThreads),
+                              Shape::kSmem, s, k);
 }
 
 template <int NT, bool VEC>
 cudaError_t project_rows(const ProjK &k, cudaStream_t s) {
-    return k.rows >= 64 * sms() ? project_mma<4, NT, VEC>(k, s) : project_mma<1, NT, VEC>(k, s);
+    return k.rows >= 32 * sms() ? project_mma<2, NT, NT <= 2 ? 2 : 1, VEC>(k, s)
+                                : project_mma<1, NT, NT <= 2 ? 2 : 1, VEC>(k, s);
 }
 
 template <bool VEC>
@@ -864,13 +1162,16 @@ cudaError_t expand(const ExpandK &k, int nranks, shmm_dtype_t wt, shmm_dtype_t o
 
 template <int MT, bool VEC>
 cudaError_t outer_mma(const OuterK &k, cudaStream_t s) {
-    constexpr size_t smem = (size_t)kWarps / 2 * MT * 32 * 32 * sizeof(float);
+    using Shape = OuterShape<MT>;
     auto kern = outer_mma_kernel<MT, VEC>;
     static shmm::PerDevice<int> done;
-    cudaError_t e = opt_in(kern, smem, &done);
+    cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)(k.job[0].tiles + k.job[1].tiles), (unsigned)k.n), dim3(kThreads), smem, s,
-                      k);
+    const int64_t tiles = k.job[0].tiles + k.job[1].tiles;
+    int cs = 1;  // until every SM has a CTA or two, with two groups of rows each
+    while (cs < 8 && tiles * k.n * cs < 2 * sms() && k.rows / k.n >= 256 * cs) cs *= 2;
+    return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
+                              Shape::kSmem, s, k);
 }
 
 // One or both gradient products (job[1].cols == 0: one) of one type.
@@ -879,13 +1180,13 @@ cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     if (xt == SHMM_F32) {
         const OuterJob &j = k.job[0];
         return launch_pdl(outer_simt_kernel<float>,
-                          dim3((unsigned)((j.x.bcols + 255) / 256 * j.x.b1), (unsigned)k.n, (unsigned)((k.R + 15) / 16)),
+                          dim3((unsigned)((j.x.bcols + 127) / 128 * j.x.b1), (unsigned)k.n, (unsigned)((k.R + 15) / 16)),
                           dim3(kThreads), 0, s, k);
     }
     bool vec = true;
     for (OuterJob &j : k.job) {
         if (!j.cols) continue;
-        j.tiles = (int)((j.x.bcols + 63) / 64 * j.x.b1);
+        j.tiles = (int)((j.x.bcols + 511) / 512 * j.x.b1);
         vec = vec && j.x.bcols % 8 == 0;
     }
     if (k.R <= 16) return vec ? outer_mma<1, true>(k, s) : outer_mma<1, false>(k, s);
