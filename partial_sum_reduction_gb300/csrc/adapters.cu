@@ -28,15 +28,18 @@
 // gradient, so infinities or NaN in one adapter or row stay there.
 
 #include <cooperative_groups.h>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "checked.cuh"
 #include "device_wait.cuh"
 #include "pdl.cuh"
 #include "shmm_internal.h"
+#include "tcgen05.cuh"
 
 namespace {
 
@@ -66,6 +69,18 @@ struct ProjK {
     float *out;           // [rows][R]
     int n, R;
     int64_t rows, cols;
+    int *status;
+};
+
+constexpr int kMaxMaps = 16;  // blocks a tensor-memory projection takes
+struct ProjTcK {
+    CUtensorMap x[kMaxMaps];  // block i of X: boxes of 128 rows x 64 columns
+    CUtensorMap w;            // [n R][cols]: boxes of 16, 32 or 64 rows x 64 columns
+    const int *ids;
+    const float *scale;
+    float *out;
+    int n, R, b1, row_tiles, per_block, chunks;  // row tiles of a block; 64-column chunks of a block, of X
+    int64_t brows, bcols, rows;
     int *status;
 };
 
@@ -188,17 +203,19 @@ __device__ __forceinline__ int distinct(const int *gids, int64_t t0, int64_t row
         int have = 0;
 #pragma unroll
         for (int i0 = 0; i0 < ROWS; i0 += 32) {
-            const int i = i0 + threadIdx.x;
-            bool first = i < ROWS && ids[i < ROWS ? i : 0] >= 0;
+            const int i = i0 + threadIdx.x, a = i < ROWS ? ids[i < ROWS ? i : 0] : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, a);
+            bool first = a >= 0 && __ffs(same) - 1 == (int)threadIdx.x;
             if (first)
-                for (int j = 0; j < i; ++j)
-                    if (ids[j] == ids[i]) {
+                for (int j = 0; j < have; ++j)
+                    if (list[j] == a) {
                         first = false;
                         break;
                     }
             const unsigned m = __ballot_sync(0xffffffffu, first);
-            if (first) list[have + __popc(m & ((1u << threadIdx.x) - 1))] = ids[i];
+            if (first) list[have + __popc(m & ((1u << threadIdx.x) - 1))] = a;
             have += __popc(m);
+            __syncwarp();
         }
         if (threadIdx.x == 0) *count = have;
     }
@@ -226,29 +243,29 @@ __device__ __forceinline__ void sum_warps(float *v, float *sh) {
 
 // ---- project ---------------------------------------------------------------
 
-// A CTA takes 16 MT rows; its warps share the columns in chunks of 32 U, and
-// so do the CTAs of a cluster along y when there are few rows (their sums
-// meet through distributed shared memory, so no partial sum goes to HBM).
+// A CTA takes 16 MT rows; its warps share the columns in chunks of 32, and so
+// do the CTAs of a cluster along y when there are few rows (their sums meet
+// through distributed shared memory, so no partial sum goes to HBM).
 // blockIdx.z strides over the tile's distinct adapters.  X and W pieces run
-// ST - 1 chunks ahead through the threads' queues.
-template <int MT, int NT, int U>
+// ST - 1 chunks ahead through the threads' queues, across adapters too.
+template <int MT, int NT>
 struct ProjShape {
-    static constexpr int kPieces = (2 * MT + NT) * U;  // per thread and chunk
-    static constexpr int kStages = kPieces <= 6 ? 4 : kPieces <= 8 ? 3 : 2;
+    static constexpr int kPieces = 2 * MT + NT;  // per thread and chunk
+    static constexpr int kStages = kPieces <= 8 ? 3 : 2;
     static constexpr size_t kQueue = (size_t)kStages * kPieces * kThreads * 16;
     static constexpr size_t kSums = (size_t)kWarps / 2 * MT * NT * 4 * 32 * sizeof(float);
-    static constexpr size_t kSmem = kQueue > kSums ? kQueue : kSums;
+    static constexpr size_t kSmem = kQueue + kSums;
 };
 
-template <int MT, int NT, int U, bool VEC>
+template <int MT, int NT, bool VEC>
 __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_constant__ ProjK k) {
     pdl_enter();
-    using Shape = ProjShape<MT, NT, U>;
+    using Shape = ProjShape<MT, NT>;
     constexpr int ROWS = 16 * MT, P = Shape::kPieces, ST = Shape::kStages;
     __shared__ int ids[ROWS], list[ROWS], count;
     extern __shared__ __align__(16) uint8_t smem[];
-    float *sh = reinterpret_cast<float *>(smem);                                  // after the columns
-    const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;     // [stage * P + piece][thread]
+    float *sh = reinterpret_cast<float *>(smem + Shape::kQueue);
+    const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;  // [stage * P + piece][thread]
     const uint32_t queue_at = shmm_dev::smem_u32(smem) + threadIdx.x * 16;
     cg::cluster_group cluster = cg::this_cluster();
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
@@ -259,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
     if (blockIdx.z == 0 && cr == 0)
         for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
             if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows) k.out[t0 * k.R + i] = 0.0f;
-    int br[2 * MT];
+    int br[2 * MT], id[2 * MT];
     int64_t off[2 * MT];  // of the row in its block
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
@@ -267,96 +284,90 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
         if (t >= k.rows) t = k.rows - 1;  // never loaded: its adapter is -1
         br[i] = (int)((uint32_t)t / (uint32_t)k.x.brows) * k.x.b1;
         off[i] = (int64_t)((uint32_t)t % (uint32_t)k.x.brows) * k.x.bcols;
+        id[i] = ids[(i / 2) * 16 + (i & 1) * 8 + g];
     }
-    const int bcols = (int)k.x.bcols, per_block = (bcols + 32 * U - 1) / (32 * U), chunks = per_block * k.x.b1;
-    const int step = kWarps * cs;
+    const int bcols = (int)k.x.bcols, per_block = (bcols + 31) / 32, chunks = per_block * k.x.b1;
+    const int step = kWarps * cs, ch0 = warp + kWarps * cr;
+    // Piece i of X (row i % 2 MT) and j of W for columns c.. of block blk:
+    // its address, and whether it exists.
+    auto x_piece = [&](int i, int a, int blk, int c, bool *ok) {
+        *ok = id[i] == a && c < bcols && in_bounds(k.status, off[i] + c, 1, k.x.brows * k.x.bcols);
+        return (const bf16 *)k.x.at[br[i] + blk] + off[i];
+    };
+    auto w_piece = [&](int j, int a, int blk, int c, bool *ok) {
+        const int r = j * 8 + g;
+        const int64_t at = ((int64_t)a * k.R + r) * k.cols + (int64_t)blk * bcols;
+        *ok = r < k.R && c < bcols && in_bounds(k.status, at + c, 1, (int64_t)k.n * k.R * k.cols);
+        return (const bf16 *)k.w + at;
+    };
+    int ask_d = blockIdx.z, ask_ch = ch0;  // the next chunk to ask for
+    auto ask = [&](int stage) {
+        if (VEC && ch0 < chunks && ask_d < nd) {
+            const int a = list[ask_d];
+            const int blk = k.x.b1 == 1 ? 0 : ask_ch / per_block, c = (ask_ch - blk * per_block) * 32 + q * 8;
+            uint32_t at = queue_at + (uint32_t)(stage * P) * kThreads * 16;
+            bool ok;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i, at += kThreads * 16) {
+                const bf16 *p = x_piece(i, a, blk, c, &ok);
+                queue16(at, ok ? p + c : (const bf16 *)k.w, ok);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j, at += kThreads * 16) {
+                const bf16 *p = w_piece(j, a, blk, c, &ok);
+                queue16(at, ok ? p + c : (const bf16 *)k.w, ok);
+            }
+            ask_ch += step;
+            if (ask_ch >= chunks) {
+                ask_ch = ch0;
+                ask_d += gridDim.z;
+            }
+        }
+        queue_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) ask(i);
+    int stage = 0;
     for (int d = blockIdx.z; d < nd; d += gridDim.z) {
         const int a = list[d];
-        const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols;
-        bool mine[2 * MT];
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) mine[i] = ids[(i / 2) * 16 + (i & 1) * 8 + g] == a;
         float acc[MT * NT * 4];
 #pragma unroll
         for (int i = 0; i < MT * NT * 4; ++i) acc[i] = 0.0f;
-        // Piece i of X (row i % 2 MT) and j of W for columns c.. of block blk:
-        // its address, and whether it exists.
-        auto x_piece = [&](int i, int blk, int c, bool *ok) {
-            *ok = mine[i] && c < bcols && in_bounds(k.status, off[i] + c, 1, k.x.brows * k.x.bcols);
-            return (const bf16 *)k.x.at[br[i] + blk] + off[i];
-        };
-        auto w_piece = [&](int j, int blk, int c, bool *ok) {
-            const int r = j * 8 + g;
-            const int64_t at = r * k.cols + (int64_t)blk * bcols;
-            *ok = r < k.R && c < bcols && in_bounds(k.status, (int64_t)a * k.R * k.cols + at + c, 1,
-                                                    (int64_t)k.n * k.R * k.cols);
-            return w + at;
-        };
-        auto ask = [&](int ch, int stage) {  // the chunk's pieces into the queue
-            if (VEC && ch < chunks) {
-                const int blk = k.x.b1 == 1 ? 0 : ch / per_block, c0 = (ch - blk * per_block) * 32 * U + q * 8;
-                uint32_t at = queue_at + (uint32_t)(stage * P) * kThreads * 16;
-                bool ok;
+        for (int ch = ch0; ch < chunks; ch += step) {
+            ask(stage == 0 ? ST - 1 : stage - 1);
+            queue_wait<ST - 1>();
+            const int blk = k.x.b1 == 1 ? 0 : ch / per_block, c = (ch - blk * per_block) * 32 + q * 8;
+            Raw8 x[2 * MT];
+            const uint4 *from = queue + stage * P * kThreads;
+            bool ok;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-#pragma unroll
-                    for (int i = 0; i < 2 * MT; ++i, at += kThreads * 16) {
-                        const bf16 *p = x_piece(i, blk, c0 + u * 32, &ok);
-                        queue16(at, ok ? p + c0 + u * 32 : w, ok);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j, at += kThreads * 16) {
-                        const bf16 *p = w_piece(j, blk, c0 + u * 32, &ok);
-                        queue16(at, ok ? p + c0 + u * 32 : w, ok);
-                    }
+            for (int i = 0; i < 2 * MT; ++i) {
+                if constexpr (VEC) {
+                    x[i] = read16(from + i * kThreads);
+                } else {
+                    const bf16 *p = x_piece(i, a, blk, c, &ok);
+                    x[i] = ok ? load8<false>(p, c, bcols) : Raw8{{0, 0, 0, 0}};
                 }
             }
-            queue_commit();
-        };
-        const int ch0 = warp + kWarps * cr;
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) ask(ch0 + i * step, i);
-        int stage = 0;
-        for (int ch = ch0; ch < chunks; ch += step) {
-            ask(ch + (ST - 1) * step, stage == 0 ? ST - 1 : stage - 1);
-            queue_wait<ST - 1>();
-            const int blk = k.x.b1 == 1 ? 0 : ch / per_block, c0 = (ch - blk * per_block) * 32 * U + q * 8;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                Raw8 x[2 * MT];
-                const uint4 *from = queue + (stage * P + u * (2 * MT + NT)) * kThreads;
-                bool ok;
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
-                    if constexpr (VEC) {
-                        x[i] = read16(from + i * kThreads);
-                    } else {
-                        const bf16 *p = x_piece(i, blk, c0 + u * 32, &ok);
-                        x[i] = ok ? load8<false>(p, c0 + u * 32, bcols) : Raw8{{0, 0, 0, 0}};
-                    }
+            for (int j = 0; j < NT; ++j) {
+                Raw8 b;
+                if constexpr (VEC) {
+                    b = read16(from + (2 * MT + j) * kThreads);
+                } else {
+                    const bf16 *p = w_piece(j, a, blk, c, &ok);
+                    b = ok ? load8<false>(p, c, bcols) : Raw8{{0, 0, 0, 0}};
                 }
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    Raw8 b;
-                    if constexpr (VEC) {
-                        b = read16(from + (2 * MT + j) * kThreads);
-                    } else {
-                        const bf16 *p = w_piece(j, blk, c0 + u * 32, &ok);
-                        b = ok ? load8<false>(p, c0 + u * 32, bcols) : Raw8{{0, 0, 0, 0}};
-                    }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        float *s = acc + (m * NT + j) * 4;
-                        const Raw8 &lo = x[2 * m], &hi = x[2 * m + 1];
-                        mma(s, lo.w[0], hi.w[0], lo.w[1], hi.w[1], b.w[0], b.w[1]);
-                        mma(s, lo.w[2], hi.w[2], lo.w[3], hi.w[3], b.w[2], b.w[3]);
-                    }
+                for (int m = 0; m < MT; ++m) {
+                    float *s = acc + (m * NT + j) * 4;
+                    const Raw8 &lo = x[2 * m], &hi = x[2 * m + 1];
+                    mma(s, lo.w[0], hi.w[0], lo.w[1], hi.w[1], b.w[0], b.w[1]);
+                    mma(s, lo.w[2], hi.w[2], lo.w[3], hi.w[3], b.w[2], b.w[3]);
                 }
             }
             stage = stage + 1 == ST ? 0 : stage + 1;
         }
-        queue_wait<0>();
-        __syncthreads();  // the queues' memory now takes the sums
         sum_warps<MT * NT * 4>(acc, sh);
         if (warp == 0)
 #pragma unroll
@@ -376,6 +387,154 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
         if (cs > 1) cluster.sync();  // nobody overwrites, or leaves with, what another CTA still reads
         else __syncthreads();
     }
+    queue_wait<0>();
+}
+
+// Many rows: 128 rows per CTA on tcgen05.  One thread streams X in boxes of
+// 128 rows x 64 columns, with the boxes of the adapters the tile uses (up to
+// 128 factor rows per pass, each a product of its own into its own TMEM
+// columns), through a ring of shared-memory stages; one thread issues the
+// products; four warps read the result out of TMEM, a row per thread.  A
+// cluster along y shares the columns, its sums meeting through distributed
+// shared memory in order.  Beside the warp instructions above it: the factor
+// is read once per 128 rows instead of per 32, and no thread spends
+// instructions on addresses, which bounded them.
+constexpr int kTcThreads = 192, kTcStages = 5, kTcSum = 129;
+constexpr uint32_t kTcRing = 98304;  // two CTAs per SM
+constexpr size_t kTcSmem = kTcRing + 1024;
+
+template <int RP>
+__global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_constant__ ProjTcK k) {
+    pdl_enter();
+    constexpr int ROWS = 128, PER = 128 / RP, S = kTcStages;
+    __shared__ int ids[ROWS], list[ROWS], count, abort_flag;
+    __shared__ __align__(8) uint64_t bars[2 * S + 1];
+    __shared__ uint32_t tmem_at;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *tiles = raw_smem + (1024 - (shmm_dev::smem_u32(raw_smem) & 1023)) % 1024;
+    const uint32_t tiles_at = shmm_dev::smem_u32(tiles);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    auto full = [&](int s) { return shmm_dev::smem_u32(&bars[s]); };
+    auto empty = [&](int s) { return shmm_dev::smem_u32(&bars[S + s]); };
+    const uint32_t done = shmm_dev::smem_u32(&bars[2 * S]);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * S + 1; ++i) shmm_dev::mbar_init(shmm_dev::smem_u32(&bars[i]), 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        shmm_tc::fence_async();
+    }
+    if (warp == 1) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 128);
+    shmm_tc::fence_before();
+    const int brow = blockIdx.x / k.row_tiles, l0 = (int)(blockIdx.x % k.row_tiles) * ROWS;
+    const int64_t t0 = brow * k.brows + l0, t1 = (brow + 1) * k.brows;
+    const int nd = distinct<ROWS>(k.ids, t0, t1, k.n, ids, list, &count, k.status);
+    shmm_tc::fence_after();
+    const uint32_t tmem = tmem_at;
+    if (cr == 0)  // rows without an adapter: zeros
+        for (int i = threadIdx.x; i < ROWS * k.R; i += kTcThreads)
+            if (ids[i / k.R] < 0 && t0 + i / k.R < t1) k.out[t0 * k.R + i] = 0.0f;
+    // As many stages as fit with the factors a pass may bring.
+    const uint32_t stage_bytes = 16384 + (nd < PER ? nd : PER) * RP * 128;
+    const uint32_t stages = kTcRing / stage_bytes < S ? kTcRing / stage_bytes : S;
+    uint32_t it = 0;  // the producer's, and the issuer's, stages so far
+    int last[S];      // the producer: phase of its last load into each stage
+#pragma unroll
+    for (int s = 0; s < S; ++s) last[s] = -1;
+    bool ok = true;
+    for (int p0 = 0, pass = 0; p0 < nd; p0 += PER, ++pass) {
+        const int na = nd - p0 < PER ? nd - p0 : PER;
+        if (warp == 0 && lane == 0) {
+            // The cluster's CTAs take neighbouring chunks: a row's 128 bytes of
+            // each lie next to one another in DRAM.
+            for (int ch = cr; ch < k.chunks && ok; ch += cs, ++it) {
+                const int s = it % stages;
+                ok = shmm_dev::mbar_wait(empty(s), (it / stages & 1) ^ 1, &abort_flag, k.status);
+                if (!ok) break;
+                const int blk = k.b1 == 1 ? 0 : ch / k.per_block, c = (ch - blk * k.per_block) * 64;
+                const uint32_t at = tiles_at + s * stage_bytes;
+                shmm_dev::mbar_expect_tx(full(s), 16384 + na * RP * 128);
+                shmm_tc::load_box(at, &k.x[brow * k.b1 + blk], full(s), c, l0);
+                for (int i = 0; i < na; ++i)
+                    shmm_tc::load_box(at + 16384 + i * RP * 128, &k.w, full(s), (int32_t)(blk * k.bcols) + c,
+                                      list[p0 + i] * k.R);
+#pragma unroll
+                for (int j = 0; j < S; ++j)
+                    if (j == s) last[j] = it / stages & 1;
+            }
+        } else if (warp == 1 && lane == 0) {
+            for (int ch = cr; ch < k.chunks && ok; ch += cs, ++it) {
+                const int s = it % stages;
+                ok = shmm_dev::mbar_wait(full(s), it / stages & 1, &abort_flag, k.status);
+                if (!ok) break;
+                shmm_tc::fence_after();
+                const uint32_t at = tiles_at + s * stage_bytes;
+                for (int i = 0; i < na; ++i)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        shmm_tc::mma_issue(tmem + i * RP, shmm_tc::operand(at + kk * 32, 16, 1024),
+                                           shmm_tc::operand(at + 16384 + i * RP * 128 + kk * 32, 16, 1024),
+                                           shmm_tc::instruction(RP, false), ch > cr || kk > 0);
+                shmm_tc::mma_commit(empty(s));
+            }
+            shmm_tc::mma_commit(done);
+        }
+        __syncwarp();
+        float *sums = reinterpret_cast<float *>(tiles);  // [row][kTcSum], once the products are done
+        if (warp >= 2) {
+            // Not cut short by an abort: the products in flight read shared memory.
+            shmm_dev::mbar_wait(done, pass & 1, &abort_flag, k.status, false);
+            __syncwarp();
+            shmm_tc::fence_after();
+            const int quad = warp & 3, row = quad * 32 + lane;
+            for (int i = 0; i < na; ++i) {
+                const int a = list[p0 + i];
+                const float scale = k.scale ? k.scale[a] : 1.0f;
+#pragma unroll
+                for (int c = 0; c < RP; c += 16) {
+                    float v[16];
+                    shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + i * RP + c, v);
+                    if (cs > 1) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sums[row * kTcSum + i * RP + c + j] = v[j];
+                    } else if (ids[row] == a && in_bounds(k.status, (t0 + row) * k.R, k.R, k.rows * k.R)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c + j < k.R) k.out[(t0 + row) * k.R + c + j] = k.scale ? v[j] * scale : v[j];
+                    }
+                }
+            }
+            shmm_tc::fence_before();
+        }
+        if (cs > 1) {
+            cluster.sync();
+            const int r0 = ROWS * cr / cs, r1 = ROWS * (cr + 1) / cs;
+            for (int e = r0 * PER * RP + threadIdx.x; e < r1 * PER * RP; e += kTcThreads) {
+                const int row = e / (PER * RP), i = e % (PER * RP) / RP, r = e % RP;
+                if (i >= na || r >= k.R || ids[row] != list[p0 + i]) continue;
+                float v = 0.0f;
+                for (int b = 0; b < cs; ++b) v += *cluster.map_shared_rank(sums + row * kTcSum + i * RP + r, b);
+                if (in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
+                    k.out[(t0 + row) * k.R + r] = k.scale ? v * k.scale[list[p0 + i]] : v;
+            }
+            shmm_tc::fence_async();
+            cluster.sync();  // the sums are read: the stages may be filled again
+        } else {
+            __syncthreads();
+        }
+        shmm_tc::fence_after();
+    }
+    // Never leave a load into shared memory in flight.
+    if (warp == 0 && lane == 0)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (last[s] >= 0) shmm_dev::mbar_wait(full(s), (uint32_t)last[s], &abort_flag, k.status, false);
+    __syncwarp();
+    shmm_tc::fence_before();
+    __syncthreads();
+    shmm_tc::fence_after();
+    if (warp == 1) shmm_tc::tmem_free(tmem, 128);
 }
 
 template <typename T>
@@ -509,18 +668,36 @@ struct Out8 {
 
 // A CTA takes 16 MT rows of one rank's box x 512 columns (64 per warp).  An
 // adapter's 16 KT x 64 piece stays in registers until a row tile needs
-// another's.  Each thread ends with 16 consecutive columns of a row, so base
-// and output move in 16-byte vectors straight from and to registers; the next
-// row tile's base is in flight while this one's products run.
+// another's.  The product's columns are dealt out
+// so that each thread ends with two runs of eight consecutive ones, and four
+// threads with 64 bytes of a row side by side: base and output move in whole
+// sectors.  The base of up to kRing row tiles is in flight through the
+// threads' queues from the start.
 // blockIdx.x: rank x row tile; blockIdx.z strides over a row tile's adapters
 // (and z = 0 copies the rows without one).
+template <int MT, int KT, typename TO>
+struct ExpandShape {
+    static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
+    static constexpr int kPitch = 16 * KT + 8;  // bf16: a row's start moves by 4 banks, fragments do not conflict
+    static constexpr int kWords = sizeof(TO) / 2;  // 16-byte pieces of eight outputs
+    static constexpr int kRing = MT < 3 ? MT : kWords == 1 ? 3 : 2;
+    static constexpr size_t kQueue = (size_t)kRing * 4 * kWords * kThreads * 16;
+    static constexpr size_t kSmem = kQueue + (size_t)kParts * 16 * MT * kPitch * 2;
+};
+
 template <int MT, int KT, bool VEC, typename TO>
-__global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_constant__ ExpandK k) {
+__global__ void __launch_bounds__(kThreads, MT > 1 && KT <= 2 && sizeof(TO) == 2 ? 2 : 1)
+    expand_mma_kernel(const __grid_constant__ ExpandK k) {
     pdl_enter();
-    constexpr int ROWS = 16 * MT, RP = 16 * KT, PITCH = RP + 8;
-    constexpr int PARTS = sizeof(TO) == 4 ? 3 : 2;
+    using Shape = ExpandShape<MT, KT, TO>;
+    constexpr int ROWS = 16 * MT, RP = 16 * KT, PITCH = Shape::kPitch, PARTS = Shape::kParts;
+    constexpr int RING = Shape::kRing, WORDS = Shape::kWords;
+    constexpr bool AHEAD = MT == 1 && KT <= 2;  // one row tile with many adapters: the next one's factor early
     __shared__ int ids[ROWS];
-    __shared__ __align__(16) bf16 ss[PARTS][ROWS][PITCH];
+    extern __shared__ __align__(16) uint8_t smem[];
+    bf16 *ss = reinterpret_cast<bf16 *>(smem + Shape::kQueue);  // [PARTS][ROWS][PITCH]
+    const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;  // [(slot * 4 + i) * WORDS + w][thread]
+    const uint32_t queue_at = shmm_dev::smem_u32(smem) + threadIdx.x * 16;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
     const int rank = blockIdx.x / k.row_tiles;
     const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;  // in the rank's box
@@ -529,24 +706,38 @@ __global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_const
     const int64_t c0 = (int64_t)blockIdx.y * 512 + warp * 64;
     const TO *base = (const TO *)k.base[rank];
     TO *out = (TO *)k.out[rank];
-    Out8<TO, VEC> now[4], next[4];  // [row half * 2 + column half]
-    auto load_base = [&](int m, Out8<TO, VEC> *b) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = m * 16 + (i >> 1) * 8 + g;
-            const int64_t c = c0 + 16 * q + 8 * (i & 1), at = (l0 + row) * k.bcols + c;
-            if (base && row < nrows && c < k.bcols && in_bounds(k.status, at, 1, k.brows * k.bcols))
-                b[i].load(base + at, (int)(k.bcols - c));
-            else
-                b[i].zero();
-        }
+    // Piece i of row tile m: row half i / 2, columns 32 (i % 2) + 8 q of the
+    // warp's 64.  `at`: its place in the box.
+    const int64_t at0 = (l0 + g) * k.bcols + c0 + 8 * q;
+    const int left0 = (int)(k.bcols - c0 - 8 * q);
+    auto has = [&](int m, int i, int64_t *at, int *left) {
+        *at = at0 + (int64_t)(m * 16 + (i >> 1) * 8) * k.bcols + 32 * (i & 1);
+        *left = left0 - 32 * (i & 1);
+        return m * 16 + (i >> 1) * 8 + g < nrows && *left > 0 && in_bounds(k.status, *at, 1, k.brows * k.bcols);
     };
-    load_base(0, now);
+    auto ask = [&](int m) {
+        if (VEC && m < MT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int64_t at;
+                int left;
+                const bool ok = has(m, i, &at, &left) && base;
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w)
+                    queue16(queue_at + (uint32_t)(((m % RING) * 4 + i) * WORDS + w) * kThreads * 16,
+                            ok ? (const void *)(base + at + w * 8 / WORDS) : k.w, ok);
+            }
+        }
+        queue_commit();
+    };
+#pragma unroll
+    for (int m = 0; m < RING; ++m) ask(m);
     if (threadIdx.x < ROWS) {
         int a = -1;
         if ((int)threadIdx.x < nrows && in_bounds(k.status, t0 + threadIdx.x, 1, k.rows)) a = k.ids[t0 + threadIdx.x];
         ids[threadIdx.x] = a >= 0 && a < k.n ? a : -1;
     }
+#pragma unroll 4
     for (int i = threadIdx.x; i < ROWS * RP / 2; i += kThreads) {
         const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
         float lo = 0.0f, hi = 0.0f;
@@ -557,62 +748,91 @@ __global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_const
         uint32_t p[PARTS];
         split<PARTS>(lo, hi, p);
 #pragma unroll
-        for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(&ss[h][row][r]) = p[h];
+        for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(ss + (h * ROWS + row) * PITCH + r) = p[h];
     }
     __syncthreads();
-    if (c0 >= k.bcols) return;
+    if (c0 >= k.bcols) {
+        queue_wait<0>();
+        return;
+    }
     const int64_t col = k.col0[rank] * k.bcols;  // of the box in the factor
     int held = -1;                               // the adapter in b
     float scale = 1.0f;
     uint32_t b[KT][8][2];
+    Raw8 raw[KT][4];
+    auto load_w = [&](int a) {
+        const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols + col;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
+                const int64_t c = c0 + 32 * (g & 1) + 8 * (g >> 1);  // product column j of lane group g: this one + j
+                raw[kt][i] = Raw8{{0, 0, 0, 0}};
+                if (r < k.R && c < k.bcols &&
+                    in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1, (int64_t)k.n * k.R * k.cols))
+                    raw[kt][i] = load8<VEC>(w + r * k.cols, c, k.bcols);
+            }
+    };
 #pragma unroll 1
     for (int m = 0; m < MT; ++m) {
-        if (m + 1 < MT) load_base(m + 1, next);
-        auto put = [&](int i, const float *v) {
-            const int row = m * 16 + (i >> 1) * 8 + g;
-            const int64_t c = c0 + 16 * q + 8 * (i & 1), at = (l0 + row) * k.bcols + c;
-            if (c >= k.bcols || !in_bounds(k.status, at, 1, k.brows * k.bcols)) return;
-            if (v) now[i].add(v);
-            now[i].store(out + at, (int)(k.bcols - c));
-        };
         const int id = ids[m * 16 + (lane & 15)];
-        unsigned todo = __ballot_sync(0xffffffffu, id >= 0) & 0xffffu;
+        const unsigned with = __ballot_sync(0xffffffffu, id >= 0) & 0xffffu;
+        // The next of this CTA's adapters of the row tile (-1: none left)
+        // and its rows.
+        unsigned todo = with;
+        int d = 0;
+        auto advance = [&](unsigned *rows) {
+            while (todo) {
+                const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
+                *rows = __ballot_sync(0xffffffffu, id == a) & 0xffffu;
+                todo &= ~*rows;
+                if (d++ % gridDim.z == blockIdx.z) return a;
+            }
+            return -1;
+        };
+        unsigned rows = 0;
+        int a = advance(&rows);
+        if (AHEAD && a >= 0) load_w(a);
+        queue_wait<RING - 1>();
+        Out8<TO, VEC> now[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (VEC) {
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w) now[i].b[w] = queue[(((m % RING) * 4 + i) * WORDS + w) * kThreads];
+            } else {
+                int64_t at;
+                int left;
+                if (has(m, i, &at, &left) && base) now[i].load(base + at, left);
+                else now[i].zero();
+            }
+        }
         if (blockIdx.z == 0 && base != out) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = (i >> 1) * 8 + g;
-                if (!(todo >> row & 1) && m * 16 + row < nrows) put(i, nullptr);
+                int64_t at;
+                int left;
+                if (!(with >> ((i >> 1) * 8 + g) & 1) && has(m, i, &at, &left)) now[i].store(out + at, left);
             }
         }
-        for (int d = 0; todo; ++d) {
-            const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
-            const unsigned same = __ballot_sync(0xffffffffu, id == a) & 0xffffu;
-            todo &= ~same;
-            if (d % gridDim.z != blockIdx.z) continue;
+        while (a >= 0) {
             if (a != held) {
                 held = a;
-                const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols + col;
+                if (!AHEAD) load_w(a);
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    Raw8 v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
-                        const int64_t c = c0 + g * 8;
-                        v[i] = Raw8{{0, 0, 0, 0}};
-                        if (r < k.R && c < k.bcols &&
-                            in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1,
-                                      (int64_t)k.n * k.R * k.cols))
-                            v[i] = load8<VEC>(w + r * k.cols, c, k.bcols);
-                    }
+                for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
+                        const Raw8 *v = raw[kt];
                         b[kt][j][0] = __byte_perm(v[0].w[j / 2], v[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
                         b[kt][j][1] = __byte_perm(v[2].w[j / 2], v[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
                     }
-                }
                 scale = k.scale ? k.scale[a] : 1.0f;
             }
+            unsigned next_rows = 0;
+            const int next = advance(&next_rows);
+            if (AHEAD && next >= 0) load_w(next);  // in flight during this adapter's products
             float acc[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -625,23 +845,28 @@ __global__ void __launch_bounds__(kThreads) expand_mma_kernel(const __grid_const
                     uint32_t f[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        f[i] = *reinterpret_cast<const uint32_t *>(
-                            &ss[h][m * 16 + g + (i & 1) * 8][kt * 16 + 2 * q + (i >> 1) * 8]);
+                        f[i] = *reinterpret_cast<const uint32_t *>(ss + (h * ROWS + m * 16 + g + (i & 1) * 8) * PITCH +
+                                                                   kt * 16 + 2 * q + (i >> 1) * 8);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) mma(acc[j], f[0], f[1], f[2], f[3], b[kt][j][0], b[kt][j][1]);
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (!(same >> ((i >> 1) * 8 + g) & 1)) continue;
+                int64_t at;
+                int left;
+                if (!(rows >> ((i >> 1) * 8 + g) & 1) || !has(m, i, &at, &left)) continue;
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = acc[j][i] * scale;
-                put(i, v);
+                now[i].add(v);
+                now[i].store(out + at, left);
             }
+            a = next;
+            rows = next_rows;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) now[i] = next[i];
+        ask(m + RING);
     }
+    queue_wait<0>();
 }
 
 // Rows of the tile without an adapter: base as it is.
@@ -721,29 +946,32 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 
 // ---- outer -----------------------------------------------------------------
 
-// Walk over the rows with adapter a, ascending, from the first'th on: fills
-// list with up to `room` of their pointers' rows.  A CTA scans kScan rows at
-// a time; `at` and `seen` (rows scanned, hits passed) carry the walk on.
-constexpr int kScan = 2048;
-struct Walk {
-    int64_t at;  // next row to scan
-    int seen;    // hits before it
-};
+// Rows of an adapter.  A CTA marks them in a bit mask over a window of
+// kWindow rows (one read of the row adapters), then turns the marks into
+// lists of up to kList rows, ascending.
+constexpr int kWindow = 65536, kList = 1024;
 
-// How many rows have adapter a (every thread gets it).
-__device__ __forceinline__ int count_rows(const int *ids, int64_t rows, int a, int *scratch) {
+// Marks the window's rows with adapter a; returns how many.
+__device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t rows, int a, uint32_t *marks,
+                                         int *scratch, int *status) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
     int mine = 0;
-    int64_t t = threadIdx.x;
-    for (; t + 7 * kThreads < rows; t += 8 * kThreads) {
+    for (int i0 = warp; i0 < words; i0 += 8 * kWarps) {
         int v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ids[t + i * kThreads];
+        for (int i = 0; i < 8; ++i) {
+            const int64_t t = w0 + (int64_t)(i0 + i * kWarps) * 32 + lane;
+            v[i] = t < rows && in_bounds(status, t, 1, rows) ? ids[t] : -1;
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mine += v[i] == a;
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t m = __ballot_sync(0xffffffffu, v[i] == a);
+            if (lane == 0 && i0 + i * kWarps < words) marks[i0 + i * kWarps] = m;
+            mine += __popc(m);
+        }
     }
-    for (; t < rows; t += kThreads) mine += ids[t] == a;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = mine;
+    if (lane == 0) scratch[warp] = mine;
     __syncthreads();
     int total = 0;
 #pragma unroll
@@ -752,42 +980,31 @@ __device__ __forceinline__ int count_rows(const int *ids, int64_t rows, int a, i
     return total;
 }
 
-// Scans rows [w.at, w.at + kScan) and lists those with adapter a whose place
-// among all of a's rows lies in [lo, hi); returns how many.
-__device__ __forceinline__ int list_rows(const int *ids, int64_t rows, int a, int lo, int hi, Walk &w, int *list,
-                                         int *scratch, int *status) {
+// The marked rows number [from, to) of the window, at most kList, into list.
+__device__ __forceinline__ void list_rows(const uint32_t *marks, int64_t w0, int64_t rows, int from, int to, int *list,
+                                          int *scratch) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    constexpr int PER = kScan / kWarps / 32;  // rounds of 32 rows per warp
-    unsigned hit[PER];
+    const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
+    const int per = (words + kThreads - 1) / kThreads, first = threadIdx.x * per;
     int mine = 0;
+    for (int i = first; i < first + per && i < words; ++i) mine += __popc(marks[i]);
+    int upto = mine;  // inclusive over the warp
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int64_t t = w.at + warp * (kScan / kWarps) + i * 32 + lane;
-        const bool ok = t < rows && in_bounds(status, t, 1, rows) && ids[t] == a;
-        hit[i] = __ballot_sync(0xffffffffu, ok);
-        mine += __popc(hit[i]);
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
     }
     __syncthreads();  // scratch and list are free
-    if (lane == 0) scratch[warp] = mine;
+    if (lane == 31) scratch[warp] = upto;
     __syncthreads();
-    int place = w.seen, total = 0;
+    int place = upto - mine;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kWarps; ++i)
         if (i < warp) place += scratch[i];
-        total += scratch[i];
-    }
-    const int from = w.seen > lo ? w.seen : lo, to = w.seen + total < hi ? w.seen + total : hi;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int p = place + __popc(hit[i] & ((1u << lane) - 1));
-        if ((hit[i] >> lane & 1) && p >= from && p < to)
-            list[p - from] = (int)(w.at + warp * (kScan / kWarps) + i * 32 + lane);
-        place += __popc(hit[i]);
-    }
-    w.at += kScan;
-    w.seen += total;
+    for (int i = first; i < first + per && i < words; ++i)
+        for (uint32_t m = marks[i]; m; m &= m - 1, ++place)
+            if (place >= from && place < to) list[place - from] = (int)(w0 + i * 32 + __ffs(m) - 1);
     __syncthreads();
-    return to > from ? to - from : 0;
 }
 
 // A CTA takes one adapter and 512 columns, 64 per warp, and a cluster along z
@@ -798,7 +1015,7 @@ __device__ __forceinline__ int list_rows(const int *ids, int64_t rows, int a, in
 // every thread's X pieces run ahead through its queue.
 template <int MT>
 struct OuterShape {
-    static constexpr int kStages = 5;                                       // 16-row steps of X in the queue
+    static constexpr int kStages = 4;                                       // 16-row steps of X in the queue
     static constexpr size_t kQueue = (size_t)kStages * 4 * kThreads * 16;
     static constexpr size_t kOperand = (size_t)4 * MT * 3 * 32 * 16;        // one group of 64 rows
     static constexpr size_t kSums = (size_t)kThreads * MT * 32 * sizeof(float);
@@ -810,7 +1027,8 @@ __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_consta
     pdl_enter();
     using Shape = OuterShape<MT>;
     constexpr int ST = Shape::kStages, RP = 16 * MT;
-    __shared__ int list[kScan], scratch[kWarps];
+    __shared__ int list[kList], scratch[kWarps];
+    __shared__ uint32_t marks[kWindow / 32];
     extern __shared__ __align__(16) uint8_t smem[];
     const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;
     const uint32_t queue_at = shmm_dev::smem_u32(smem) + threadIdx.x * 16;
@@ -832,14 +1050,14 @@ __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_consta
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-    const int total = count_rows(k.ids, k.rows, a, scratch);
+    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
+    const int total = mark_rows(k.ids, w0, k.rows, a, marks, scratch, k.status);
     // this CTA's share of the rows, in whole groups of 64
     const int groups = (total + 63) / 64;
     const int lo = groups * cr / cs * 64, hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
-    Walk walk{0, 0};
-    while (walk.seen < hi && walk.at < k.rows) {
-        const int have = list_rows(k.ids, k.rows, a, lo, hi, walk, list, scratch, k.status);
-        if (!have) continue;
+    for (int l0 = lo; l0 < hi; l0 += kList) {
+        const int have = hi - l0 < kList ? hi - l0 : kList;
+        list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
         const int steps = (have + 15) / 16;
         auto row_of = [&](int step, int i) {
             const int at = step * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
@@ -865,21 +1083,31 @@ __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < ST - 1; ++i) ask(i, i);
         int stage = 0;
+        // S of a group: 32 row pairs x RP, this thread's pairs read ahead
+        float2 sv[2 * MT];
+        auto read_s = [&](int grp) {
+#pragma unroll
+            for (int e = 0; e < 2 * MT; ++e) {
+                const int i = threadIdx.x + e * kThreads, r = i % RP, at = grp * 64 + i / RP * 2;
+                sv[e].x = r < k.R && at < have ? S[(int64_t)list[at] * k.R + r] : 0.0f;
+                sv[e].y = r < k.R && at + 1 < have ? S[(int64_t)list[at + 1] * k.R + r] : 0.0f;
+            }
+        };
+        read_s(0);
         for (int grp = 0; grp * 4 < steps; ++grp) {
             uint4 *op = operand + (grp & 1) * (4 * MT * 3 * 32);
-            // 32 row pairs x RP: pair (t, t + 1) of r is word w of lane l
-            for (int e = threadIdx.x; e < 32 * RP; e += kThreads) {
-                const int r = e % RP, pair = e / RP, tt = (pair & 7) * 2;
-                const int at = grp * 64 + pair * 2;
-                const float x = r < k.R && at < have ? S[(int64_t)list[at] * k.R + r] : 0.0f;
-                const float y = r < k.R && at + 1 < have ? S[(int64_t)list[at + 1] * k.R + r] : 0.0f;
+            // pair (t, t + 1) of r is word w of lane l of its row step
+#pragma unroll
+            for (int e = 0; e < 2 * MT; ++e) {
+                const int i = threadIdx.x + e * kThreads, r = i % RP, pair = i / RP, tt = (pair & 7) * 2;
                 uint32_t p[3];
-                split<3>(x, y, p);
+                split<3>(sv[e].x, sv[e].y, p);
                 const int l = (r & 7) * 4 + ((tt & 7) >> 1), w = ((r >> 3) & 1) + (tt >> 3) * 2;
                 uint32_t *to = reinterpret_cast<uint32_t *>(op + (((pair >> 3) * MT + (r >> 4)) * 3) * 32 + l) + w;
 #pragma unroll
                 for (int h = 0; h < 3; ++h) to[h * 32 * 4] = p[h];
             }
+            if ((grp + 1) * 4 < steps) read_s(grp + 1);
             __syncthreads();
 #pragma unroll 1
             for (int st = 0; st < 4 && grp * 4 + st < steps; ++st) {
@@ -915,6 +1143,7 @@ __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_consta
             }
         }
         queue_wait<0>();
+    }
     }
     const float scale = J.scale ? J.scale[a] : 1.0f;
     // Result piece (warp w, m, i): eight columns from 16 q + 8 (i & 1) of w's
@@ -974,7 +1203,8 @@ __global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_consta
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
-    __shared__ int list[kScan], scratch[kWarps];
+    __shared__ int list[kList], scratch[kWarps];
+    __shared__ uint32_t marks[kWindow / 32];
     __shared__ float ss[2][16][16];
     __shared__ float sums[16][128];
     const OuterJob &J = k.job[0];
@@ -985,9 +1215,11 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    Walk walk{0, 0};
-    while (walk.at < k.rows) {
-        const int have = list_rows(k.ids, k.rows, a, 0, 0x7fffffff, walk, list, scratch, k.status);
+    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
+    const int total = mark_rows(k.ids, w0, k.rows, a, marks, scratch, k.status);
+    for (int l0 = 0; l0 < total; l0 += kList) {
+        const int have = total - l0 < kList ? total - l0 : kList;
+        list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
         for (int s0 = 0; s0 < have; s0 += 32) {
             const int s = s0 + half * 16;
             float x[16];
@@ -1012,6 +1244,7 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[half][u][i], x[u], acc[i]);
         }
+    }
     }
     if (half)
 #pragma unroll
@@ -1061,42 +1294,110 @@ void fill(Blocks *b, const shmm::BlockGrid &g) {
     b->bcols = g.bcols;
 }
 
-// Cluster size and adapter stride of a projection whose row tiles alone are
-// `tiles` CTAs: the chunks are shared by up to 8 CTAs until every SM has one
-// or two, and the tile's adapters by up to as many CTAs as it has rows.
-void spread(int64_t tiles, int rows_per_tile, int n, int64_t chunks_per_warp, int *cluster, int *slots) {
-    const int64_t want = 2 * sms();
-    int64_t z = n < rows_per_tile ? n : rows_per_tile;
-    if (tiles * z > 8 * want) z = 8 * want / tiles > 1 ? 8 * want / tiles : 1;
-    if (tiles >= want) z = 1;
-    int c = 1;
-    while (c < 8 && tiles * c < want && chunks_per_warp > c) c *= 2;
-    *cluster = c;
-    *slots = (int)z;
+// CTAs of kThreads threads and `smem` bytes of shared memory that the card
+// holds at once.
+int64_t slots_for(size_t smem) {
+    const int64_t per = (227 * 1024) / (int64_t)(smem + 3 * 1024);
+    return sms() * (per < 1 ? 1 : per > 4 ? 4 : per);
 }
 
-template <int MT, int NT, int U, bool VEC>
+// Spreads `tiles` CTAs of work over the card in one wave: a tile's adapters
+// over z CTAs (at most `most`, as many as it has rows or the call adapters),
+// then its columns over a cluster of c (at most `split`).  One wave of equal
+// CTAs ends together; two leave the second part empty.
+void spread(int64_t tiles, int64_t slots, int64_t most, int64_t split, int *c, int *z) {
+    *c = *z = 1;
+    while (*c < 8 && tiles * *c * 2 <= slots && *c * 2 <= split) *c *= 2;
+    const int64_t left = slots / (tiles * *c);
+    *z = (int)(left < 1 ? 1 : left < most ? left : most);
+}
+
+template <int MT, int NT, bool VEC>
 cudaError_t project_mma(const ProjK &k, cudaStream_t s) {
-    using Shape = ProjShape<MT, NT, U>;
-    auto kern = project_mma_kernel<MT, NT, U, VEC>;
+    using Shape = ProjShape<MT, NT>;
+    auto kern = project_mma_kernel<MT, NT, VEC>;
     static shmm::PerDevice<int> done;
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (k.rows + 16 * MT - 1) / (16 * MT);
-    int cluster, slots;
-    spread(tiles, 16 * MT, k.n, (k.cols + 32 * U * kWarps - 1) / (32 * U * kWarps), &cluster, &slots);
-    return launch_pdl_cluster(kern, dim3((unsigned)tiles, cluster, slots), dim3(1, cluster, 1), dim3(kThreads),
-                              Shape::kSmem, s, k);
+    int c, z;
+    // two chunks of 32 columns per warp at least
+    spread(tiles, slots_for(Shape::kSmem), k.n < 16 * MT ? k.n : 16 * MT, k.cols / (64 * kWarps), &c, &z);
+    return launch_pdl_cluster(kern, dim3((unsigned)tiles, c, z), dim3(1, c, 1), dim3(kThreads), Shape::kSmem, s, k);
 }
 
 template <int NT, bool VEC>
 cudaError_t project_rows(const ProjK &k, cudaStream_t s) {
-    return k.rows >= 32 * sms() ? project_mma<2, NT, NT <= 2 ? 2 : 1, VEC>(k, s)
-                                : project_mma<1, NT, NT <= 2 ? 2 : 1, VEC>(k, s);
+    // Two row tiles per warp halve the factor's share of the loads; they
+    // need rows enough to fill the card.
+    return k.rows >= 16 * sms() ? project_mma<2, NT, VEC>(k, s) : project_mma<1, NT, VEC>(k, s);
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+
+// A row-major rows x cols bf16 matrix in boxes of box_rows x 64.
+bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int RP>
+cudaError_t project_tc(const ProjK &k, int b0, cudaStream_t s) {
+    auto kern = project_tc_kernel<RP>;
+    static shmm::PerDevice<int> done;
+    cudaError_t e = opt_in(kern, kTcSmem, &done);
+    if (e != cudaSuccess) return e;
+    ProjTcK t;
+    for (int i = 0; i < b0 * k.x.b1; ++i)
+        if (!make_map(&t.x[i], k.x.at[i], k.x.brows, k.x.bcols, 128)) return cudaErrorNotSupported;
+    if (!make_map(&t.w, k.w, (int64_t)k.n * k.R, k.cols, RP)) return cudaErrorNotSupported;
+    t.ids = k.ids;
+    t.scale = k.scale;
+    t.out = k.out;
+    t.n = k.n;
+    t.R = k.R;
+    t.b1 = k.x.b1;
+    t.row_tiles = (int)((k.x.brows + 127) / 128);
+    t.per_block = (int)((k.x.bcols + 63) / 64);
+    t.chunks = t.per_block * k.x.b1;
+    t.brows = k.x.brows;
+    t.bcols = k.x.bcols;
+    t.rows = k.rows;
+    t.status = k.status;
+    const int64_t tiles = (int64_t)t.row_tiles * b0;
+    int c, z;
+    spread(tiles, slots_for(kTcSmem), 1, t.chunks / 4, &c, &z);
+    return launch_pdl_cluster(kern, dim3((unsigned)tiles, c), dim3(1, c, 1), dim3(kTcThreads), kTcSmem, s, t);
 }
 
 template <bool VEC>
 cudaError_t project_vec(const ProjK &k, cudaStream_t s) {
+    // tcgen05 from 2048 rows on: 16 row tiles, whose clusters of 8 reach most SMs.
+    const int b0 = (int)(k.rows / k.x.brows);
+    if (VEC && k.rows >= 2048 && k.x.brows >= 128 && b0 * k.x.b1 <= kMaxMaps && k.cols >= 512) {
+        if (k.R <= 16) return project_tc<16>(k, b0, s);
+        return k.R <= 32 ? project_tc<32>(k, b0, s) : project_tc<64>(k, b0, s);
+    }
     if (k.R <= 8) return project_rows<1, VEC>(k, s);
     if (k.R <= 16) return project_rows<2, VEC>(k, s);
     if (k.R <= 32) return project_rows<4, VEC>(k, s);
@@ -1106,9 +1407,9 @@ cudaError_t project_vec(const ProjK &k, cudaStream_t s) {
 template <typename TX, typename TW>
 cudaError_t project_simt(const ProjK &k, cudaStream_t s) {
     const int64_t tiles = (k.rows + 31) / 32;
-    int cluster, slots;
-    spread(tiles, 32, k.n, (k.cols + 31) / 32, &cluster, &slots);
-    const dim3 g((unsigned)tiles, cluster, slots), c(1, cluster, 1);
+    int cluster, z;
+    spread(tiles, 4 * sms(), k.n < 32 ? k.n : 32, k.cols / 64, &cluster, &z);
+    const dim3 g((unsigned)tiles, cluster, z), c(1, cluster, 1);
     if (k.R <= 16) return launch_pdl_cluster(project_simt_kernel<TX, TW, 1>, g, c, dim3(kThreads), 0, s, k);
     if (k.R <= 32) return launch_pdl_cluster(project_simt_kernel<TX, TW, 2>, g, c, dim3(kThreads), 0, s, k);
     return launch_pdl_cluster(project_simt_kernel<TX, TW, 4>, g, c, dim3(kThreads), 0, s, k);
@@ -1124,18 +1425,24 @@ cudaError_t project(const ProjK &k, shmm_dtype_t xt, shmm_dtype_t wt, cudaStream
 
 template <int MT, int KT, bool VEC, typename TO>
 cudaError_t expand_mma(ExpandK k, int nranks, cudaStream_t s) {
+    using Shape = ExpandShape<MT, KT, TO>;
+    auto kern = expand_mma_kernel<MT, KT, VEC, TO>;
+    static shmm::PerDevice<int> done;
+    cudaError_t e = opt_in(kern, Shape::kSmem, &done);
+    if (e != cudaSuccess) return e;
     k.row_tiles = (int)((k.brows + 16 * MT - 1) / (16 * MT));
-    const int64_t tiles = (int64_t)k.row_tiles * nranks * ((k.bcols + 511) / 512);
-    int cluster, slots;
-    spread(tiles, 16 * MT, k.n, 1, &cluster, &slots);
-    return launch_pdl(expand_mma_kernel<MT, KT, VEC, TO>,
-                      dim3((unsigned)(k.row_tiles * nranks), (unsigned)((k.bcols + 511) / 512), slots), dim3(kThreads),
-                      0, s, k);
+    const int64_t cols = (k.bcols + 511) / 512, tiles = (int64_t)k.row_tiles * nranks * cols;
+    int c, z;
+    spread(tiles, 3 * sms(), k.n < 16 * MT ? k.n : 16 * MT, 1, &c, &z);
+    return launch_pdl(kern, dim3((unsigned)(k.row_tiles * nranks), (unsigned)cols, z), dim3(kThreads), Shape::kSmem, s,
+                      k);
 }
 
 template <bool VEC, typename TO>
 cudaError_t expand_vec(const ExpandK &k, int nranks, cudaStream_t s) {
-    const bool many = k.brows >= 64 && k.brows / 64 * nranks * ((k.bcols + 511) / 512) >= sms();
+    // Tall row tiles load a factor's piece less often; they need rows enough
+    // to fill the card.
+    const bool many = (k.brows + 63) / 64 * nranks * ((k.bcols + 511) / 512) >= sms();
     if (k.R <= 16) return many ? expand_mma<4, 1, VEC, TO>(k, nranks, s) : expand_mma<1, 1, VEC, TO>(k, nranks, s);
     if (k.R <= 32) return many ? expand_mma<4, 2, VEC, TO>(k, nranks, s) : expand_mma<1, 2, VEC, TO>(k, nranks, s);
     return many ? expand_mma<4, 4, VEC, TO>(k, nranks, s) : expand_mma<1, 4, VEC, TO>(k, nranks, s);
@@ -1148,10 +1455,10 @@ cudaError_t expand_type(ExpandK k, int nranks, shmm_dtype_t wt, cudaStream_t s) 
                                                    : expand_vec<false, TO>(k, nranks, s);
     k.row_tiles = (int)((k.brows + 15) / 16);
     const int64_t tiles = (int64_t)k.row_tiles * nranks * ((k.bcols + 255) / 256);
-    int cluster, slots;
-    spread(tiles, 16, k.n, 1, &cluster, &slots);
+    int c, z;
+    spread(tiles, 2 * sms(), k.n < 16 ? k.n : 16, 1, &c, &z);
     return launch_pdl(expand_simt_kernel<float, TO>,
-                      dim3((unsigned)(k.row_tiles * nranks), (unsigned)((k.bcols + 255) / 256), slots), dim3(kThreads),
+                      dim3((unsigned)(k.row_tiles * nranks), (unsigned)((k.bcols + 255) / 256), z), dim3(kThreads),
                       0, s, k);
 }
 
@@ -1168,8 +1475,10 @@ cudaError_t outer_mma(const OuterK &k, cudaStream_t s) {
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = k.job[0].tiles + k.job[1].tiles;
-    int cs = 1;  // until every SM has a CTA or two, with two groups of rows each
-    while (cs < 8 && tiles * k.n * cs < 2 * sms() && k.rows / k.n >= 256 * cs) cs *= 2;
+    // Adapters differ in rows, so CTAs in time: shares of an adapter's rows
+    // until there are several waves of CTAs or only four groups of rows each.
+    int cs = 1;
+    while (cs < 8 && tiles * k.n * cs < 8 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
                               Shape::kSmem, s, k);
 }

@@ -281,6 +281,45 @@ def test_many_rows(s, I, R):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout,I,J,K,R,n,kind", [
+    ("whole", 2048, 512, 512, 16, 3, "runs"), ("whole", 2500, 520, 1000, 5, 40, "random"),
+    ("contracted", 2600, 1200, 640, 33, 4, "runs"), ("columns", 2100, 576, 4096, 64, 9, "random"),
+    ("rows", 4 * 700, 640, 520, 32, 6, "runs"), ("grid", 2 * 1100, 1160, 1040, 64, 2, "random"),
+    ("whole", 4300, 2056, 2104, 8, 300, "random"), ("scattered", 2304, 1024, 768, 16, 1, "random")])
+def test_tall_batches(s, layout, I, J, K, R, n, kind):
+    """Batches of 2048 rows and more: row tiles of 128 with one adapter and
+    with dozens (several passes over a tile), shards whose rows and columns
+    are no whole tiles."""
+    g = torch.Generator().manual_seed(I)
+    ids = torch.arange(I) // 211 % (n + 1) - 1 if kind == "runs" else torch.randint(-1, n, (I,), generator=g)
+    Case(s, layout, I, J, K, R, n, ids=ids).check()
+
+
+@pytest.mark.gpu
+def test_infinities_and_nan_stay_in_their_rows_of_a_tall_batch(s):
+    I, n = 2304, 5
+    ids = torch.arange(I, dtype=torch.int32) % (n + 1) - 1
+    c = Case(s, "whole", I, 512, 520, 16, n, ids=ids)
+    C0, low0 = c.forward()
+    dA0, dd0, du0 = c.backward(low0)
+    c.down[2, 3, 5], c.up[2, 1, 7] = float("inf"), float("nan")
+    c.A[7], c.dC[7], c.A[13] = float("nan"), float("nan"), float("inf")  # adapter 0
+    c.A[6], c.dC[6] = float("nan"), float("inf")                         # none
+    assert ids[7] == 0 and ids[13] == 0 and ids[6] == -1
+    for k in ("down", "up"):
+        c.dev[k] = getattr(c, k).cuda()
+    c.A_r = c.H.shard(c.plan, s.TENSOR_A, c.A)
+    C1, low1 = c.forward()
+    dA1, dd1, du1 = c.backward(low1)
+    clean = [i for i in range(I) if ids[i] != 2 and i not in (6, 7, 13)]
+    assert torch.equal(C0[0][clean], C1[0][clean]) and torch.equal(low0[clean], low1[clean])
+    assert torch.equal(dA0[0][clean], dA1[0][clean])
+    for a in (1, 3, 4):
+        assert torch.equal(dd0[a], dd1[a]) and torch.equal(du0[a], du1[a])
+    assert torch.equal(C1[0][6].cpu(), c.base[6]) and (low1[6] == 0).all()
+
+
+@pytest.mark.gpu
 def test_rows_past_2_to_the_32_bytes(s):
     """Offsets past 32 bits: the last rows of operands of more than 4 GiB."""
     I, J, K, R = 1 << 17, 16640, 16, 4
