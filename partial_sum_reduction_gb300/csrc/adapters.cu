@@ -49,6 +49,8 @@ using shmm_dev::in_bounds;
 using shmm_pdl::launch_pdl;
 using shmm_pdl::launch_pdl_cluster;
 using shmm_pdl::pdl_enter;
+using shmm_pdl::pdl_release;
+using shmm_pdl::pdl_wait;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -241,6 +243,19 @@ __device__ __forceinline__ void sum_warps(float *v, float *sh) {
     }
 }
 
+// Sum over the cluster's CTAs, in order, of the value at `at` in each one's
+// shared memory; the loads go out together.
+__device__ __forceinline__ float sum_cluster(cg::cluster_group &cluster, float *at, int cs) {
+    float v[8], t = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+        if (b < cs) v[b] = *cluster.map_shared_rank(at, b);
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+        if (b < cs) t += v[b];
+    return t;
+}
+
 // ---- project ---------------------------------------------------------------
 
 // A CTA takes 16 MT rows; its warps share the columns in chunks of 32, and so
@@ -377,8 +392,7 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
         const float scale = k.scale ? k.scale[a] : 1.0f;
         const int part = MT * NT * 4 * 32 / cs;
         for (int e = cr * part + threadIdx.x; e < (cr + 1) * part; e += kThreads) {
-            float v = 0.0f;
-            for (int b = 0; b < cs; ++b) v += cs > 1 ? *cluster.map_shared_rank(sh + e, b) : sh[e];
+            const float v = cs > 1 ? sum_cluster(cluster, sh + e, cs) : sh[e];
             const int i = e / 32, l = e & 31, c = i & 3, j = (i / 4) % NT, m = i / (4 * NT);
             const int row = m * 16 + (l >> 2) + (c >> 1) * 8, r = j * 8 + (l & 3) * 2 + (c & 1);
             if (ids[row] == a && r < k.R && in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
@@ -405,7 +419,7 @@ constexpr size_t kTcSmem = kTcRing + 1024;
 
 template <int RP>
 __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_constant__ ProjTcK k) {
-    pdl_enter();
+    pdl_wait();
     constexpr int ROWS = 128, PER = 128 / RP, S = kTcStages;
     __shared__ int ids[ROWS], list[ROWS], count, abort_flag;
     __shared__ __align__(8) uint64_t bars[2 * S + 1];
@@ -431,6 +445,9 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     const int64_t t0 = brow * k.brows + l0, t1 = (brow + 1) * k.brows;
     const int nd = distinct<ROWS>(k.ids, t0, t1, k.n, ids, list, &count, k.status);
     shmm_tc::fence_after();
+    // Only now may the next kernel's CTAs come: one that takes all of an SM's
+    // TMEM and then waits for this kernel must not get there first.
+    pdl_release();
     const uint32_t tmem = tmem_at;
     if (cr == 0)  // rows without an adapter: zeros
         for (int i = threadIdx.x; i < ROWS * k.R; i += kTcThreads)
@@ -438,45 +455,61 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     // As many stages as fit with the factors a pass may bring.
     const uint32_t stage_bytes = 16384 + (nd < PER ? nd : PER) * RP * 128;
     const uint32_t stages = kTcRing / stage_bytes < S ? kTcRing / stage_bytes : S;
-    uint32_t it = 0;  // the producer's, and the issuer's, stages so far
-    int last[S];      // the producer: phase of its last load into each stage
-#pragma unroll
-    for (int s = 0; s < S; ++s) last[s] = -1;
+    const int lo = (int)((int64_t)k.chunks * cr / cs), hi = (int)((int64_t)k.chunks * (cr + 1) / cs);
+    // Producer and issuer are one thread each, so their own instructions are
+    // what a chunk costs them (a division or two each made it 1500 cycles):
+    // both walk stages and blocks by counting.
+    uint32_t stage = 0, phase = 0, asked = 0;
+    const int blk0 = k.b1 == 1 ? 0 : lo / k.per_block;
     bool ok = true;
     for (int p0 = 0, pass = 0; p0 < nd; p0 += PER, ++pass) {
         const int na = nd - p0 < PER ? nd - p0 : PER;
         if (warp == 0 && lane == 0) {
-            // The cluster's CTAs take neighbouring chunks: a row's 128 bytes of
-            // each lie next to one another in DRAM.
-            for (int ch = cr; ch < k.chunks && ok; ch += cs, ++it) {
-                const int s = it % stages;
-                ok = shmm_dev::mbar_wait(empty(s), (it / stages & 1) ^ 1, &abort_flag, k.status);
+            const CUtensorMap *x = &k.x[brow * k.b1 + blk0];
+            int c = (lo - blk0 * k.per_block) * 64, wc = (int)(blk0 * k.bcols) + c;
+            const int w_row = list[p0] * k.R;
+            const uint32_t bytes = 16384 + na * RP * 128;
+            for (int ch = lo; ch < hi; ++ch) {
+                ok = ok && shmm_dev::mbar_wait(empty(stage), phase ^ 1, &abort_flag, k.status);
                 if (!ok) break;
-                const int blk = k.b1 == 1 ? 0 : ch / k.per_block, c = (ch - blk * k.per_block) * 64;
-                const uint32_t at = tiles_at + s * stage_bytes;
-                shmm_dev::mbar_expect_tx(full(s), 16384 + na * RP * 128);
-                shmm_tc::load_box(at, &k.x[brow * k.b1 + blk], full(s), c, l0);
-                for (int i = 0; i < na; ++i)
-                    shmm_tc::load_box(at + 16384 + i * RP * 128, &k.w, full(s), (int32_t)(blk * k.bcols) + c,
-                                      list[p0 + i] * k.R);
-#pragma unroll
-                for (int j = 0; j < S; ++j)
-                    if (j == s) last[j] = it / stages & 1;
+                const uint32_t at = tiles_at + stage * stage_bytes, bar = full(stage);
+                shmm_dev::mbar_expect_tx(bar, bytes);
+                shmm_tc::load_box(at, x, bar, c, l0);
+                shmm_tc::load_box(at + 16384, &k.w, bar, wc, w_row);
+                for (int i = 1; i < na; ++i)
+                    shmm_tc::load_box(at + 16384 + i * RP * 128, &k.w, bar, wc, list[p0 + i] * k.R);
+                ++asked;
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                c += 64;
+                wc += 64;
+                if (c >= k.bcols) {  // the next block
+                    wc += (int)k.bcols - c;
+                    c = 0;
+                    ++x;
+                }
             }
         } else if (warp == 1 && lane == 0) {
-            for (int ch = cr; ch < k.chunks && ok; ch += cs, ++it) {
-                const int s = it % stages;
-                ok = shmm_dev::mbar_wait(full(s), it / stages & 1, &abort_flag, k.status);
+            const uint64_t base = shmm_tc::operand(tiles_at, 16, 1024);
+            for (int ch = lo; ch < hi; ++ch) {
+                ok = ok && shmm_dev::mbar_wait(full(stage), phase, &abort_flag, k.status);
                 if (!ok) break;
                 shmm_tc::fence_after();
-                const uint32_t at = tiles_at + s * stage_bytes;
-                for (int i = 0; i < na; ++i)
+                const uint64_t xa = base + ((stage * stage_bytes) >> 4);  // addresses in units of 16 bytes
+                for (int i = 0; i < na; ++i) {
+                    const uint64_t wa = xa + 1024 + i * (RP * 8);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        shmm_tc::mma_issue(tmem + i * RP, shmm_tc::operand(at + kk * 32, 16, 1024),
-                                           shmm_tc::operand(at + 16384 + i * RP * 128 + kk * 32, 16, 1024),
-                                           shmm_tc::instruction(RP, false), ch > cr || kk > 0);
-                shmm_tc::mma_commit(empty(s));
+                        shmm_tc::mma_issue(tmem + i * RP, xa + kk * 2, wa + kk * 2, shmm_tc::instruction(RP, false),
+                                           ch > lo || kk > 0);
+                }
+                shmm_tc::mma_commit(empty(stage));
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
             shmm_tc::mma_commit(done);
         }
@@ -510,11 +543,10 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
         if (cs > 1) {
             cluster.sync();
             const int r0 = ROWS * cr / cs, r1 = ROWS * (cr + 1) / cs;
-            for (int e = r0 * PER * RP + threadIdx.x; e < r1 * PER * RP; e += kTcThreads) {
-                const int row = e / (PER * RP), i = e % (PER * RP) / RP, r = e % RP;
-                if (i >= na || r >= k.R || ids[row] != list[p0 + i]) continue;
-                float v = 0.0f;
-                for (int b = 0; b < cs; ++b) v += *cluster.map_shared_rank(sums + row * kTcSum + i * RP + r, b);
+            for (int e = threadIdx.x; e < (r1 - r0) * na * RP; e += kTcThreads) {
+                const int row = r0 + e / (na * RP), i = e % (na * RP) / RP, r = e % RP;
+                if (r >= k.R || ids[row] != list[p0 + i]) continue;
+                const float v = sum_cluster(cluster, sums + row * kTcSum + i * RP + r, cs);
                 if (in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
                     k.out[(t0 + row) * k.R + r] = k.scale ? v * k.scale[list[p0 + i]] : v;
             }
@@ -527,9 +559,8 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     }
     // Never leave a load into shared memory in flight.
     if (warp == 0 && lane == 0)
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (last[s] >= 0) shmm_dev::mbar_wait(full(s), (uint32_t)last[s], &abort_flag, k.status, false);
+        for (uint32_t u = asked > stages ? asked - stages : 0; u < asked; ++u)
+            shmm_dev::mbar_wait(full(u % stages), u / stages & 1, &abort_flag, k.status, false);
     __syncwarp();
     shmm_tc::fence_before();
     __syncthreads();
@@ -601,8 +632,7 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
         else __syncthreads();
         const int share = ROWS * RP / cs;
         for (int e = cr * share + threadIdx.x; e < (cr + 1) * share; e += kThreads) {
-            float v = 0.0f;
-            for (int b = 0; b < cs; ++b) v += cs > 1 ? *cluster.map_shared_rank(part + e, b) : part[e];
+            const float v = cs > 1 ? sum_cluster(cluster, part + e, cs) : part[e];
             const int row = e / RP, r = e % RP;
             if (ids[row] == a && r < k.R && in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
                 k.out[(t0 + row) * k.R + r] = k.scale ? v * k.scale[a] : v;
@@ -1007,195 +1037,198 @@ __device__ __forceinline__ void list_rows(const uint32_t *marks, int64_t w0, int
     __syncthreads();
 }
 
-// A CTA takes one adapter and 512 columns, 64 per warp, and a cluster along z
-// shares the adapter's rows (their sums meet through distributed shared
-// memory, in order).  Rows go in groups of 64: the CTA splits their
-// fp32 S values into bf16 operands in shared memory, in the order the matrix
-// instruction wants them (two groups' room, so one barrier per group), while
-// every thread's X pieces run ahead through its queue.
-template <int MT>
+// A CTA takes one adapter and 256 columns, and a cluster along z shares the
+// adapter's rows (its sums meet through distributed shared memory, in order).
+// Rows go in groups of 64, on tcgen05: X's rows, gathered by index, are the
+// 64 x 256 operand as they lie (MN-major boxes of 64 columns); the fp32 S
+// values' bf16 parts stand below one another in the 128 rows of the other
+// operand (three bands of RP rows; RP = 64: two, and the third part in an
+// operand tile of its own), so one product does all parts and the parts' rows
+// are added at the end.  The factor side, 3 RP columns, would be the bound of
+// warp matrix instructions at RP = 32 and above (about half their rate), and
+// its operands of their shared-memory reads.
+template <int RP>
 struct OuterShape {
-    static constexpr int kStages = 4;                                       // 16-row steps of X in the queue
-    static constexpr size_t kQueue = (size_t)kStages * 4 * kThreads * 16;
-    static constexpr size_t kOperand = (size_t)4 * MT * 3 * 32 * 16;        // one group of 64 rows
-    static constexpr size_t kSums = (size_t)kThreads * MT * 32 * sizeof(float);
-    static constexpr size_t kSmem = kQueue + 2 * kOperand > kSums ? kQueue + 2 * kOperand : kSums;
+    static constexpr int kTiles = RP == 64 ? 2 : 1;          // S operand tiles of 128 x 64
+    static constexpr int kBands = RP == 64 ? 2 : 3;
+    static constexpr uint32_t kStage = 32768 + kTiles * 16384;
+    static constexpr int kStages = 2;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static constexpr int kPairs = RP / 8;                    // row pairs of S per thread and group
+    static constexpr int kPitch = 65;                        // fp32 of a 64-column piece of the result
 };
 
-template <int MT, bool VEC>
-__global__ void __launch_bounds__(kThreads) outer_mma_kernel(const __grid_constant__ OuterK k) {
-    pdl_enter();
-    using Shape = OuterShape<MT>;
-    constexpr int ST = Shape::kStages, RP = 16 * MT;
-    __shared__ int list[kList], scratch[kWarps];
-    __shared__ uint32_t marks[kWindow / 32];
-    extern __shared__ __align__(16) uint8_t smem[];
-    const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;
-    const uint32_t queue_at = shmm_dev::smem_u32(smem) + threadIdx.x * 16;
-    uint4 *operand = reinterpret_cast<uint4 *>(smem + Shape::kQueue);  // [2][(step * MT + m) * 3 + part][lane]
+template <int RP, bool VEC>
+__global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constant__ OuterK k) {
+    pdl_wait();
+    using Shape = OuterShape<RP>;
+    constexpr int S = Shape::kStages, PAIRS = Shape::kPairs;
+    __shared__ int list[kList], scratch[kWarps], abort_flag;
+    __shared__ uint32_t marks[kWindow / 32], tmem_at;
+    __shared__ __align__(8) uint64_t bars[S];  // a stage's products are done
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *smem = raw_smem + (1024 - (shmm_dev::smem_u32(raw_smem) & 1023)) % 1024;
+    const uint32_t smem_at = shmm_dev::smem_u32(smem);
     cg::cluster_group cluster = cg::this_cluster();
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
     const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
-    const int bcols = (int)J.x.bcols, per_block = (bcols + 511) / 512, blk = tile / per_block;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
-    const int c0 = (tile - blk * per_block) * 512 + warp * 64;
-    const int cx = c0 + g * 8;  // this thread's columns of X
-    const float *S = J.s;
-    float acc[MT][8][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-    const int total = mark_rows(k.ids, w0, k.rows, a, marks, scratch, k.status);
-    // this CTA's share of the rows, in whole groups of 64
-    const int groups = (total + 63) / 64;
-    const int lo = groups * cr / cs * 64, hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
-    for (int l0 = lo; l0 < hi; l0 += kList) {
-        const int have = hi - l0 < kList ? hi - l0 : kList;
-        list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
-        const int steps = (have + 15) / 16;
-        auto row_of = [&](int step, int i) {
-            const int at = step * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
-            return at < have ? list[at] : -1;
-        };
-        auto x_piece = [&](int t, bool *ok) {
-            const uint32_t b = (uint32_t)t / (uint32_t)J.x.brows, l = (uint32_t)t - b * (uint32_t)J.x.brows;
-            const int64_t off = (int64_t)l * bcols;
-            *ok = t >= 0 && cx < bcols && in_bounds(k.status, off + cx, 1, J.x.brows * J.x.bcols);
-            return *ok ? (const bf16 *)J.x.at[b * J.x.b1 + blk] + off : (const bf16 *)nullptr;
-        };
-        auto ask = [&](int step, int stage) {
-            if (VEC && step < steps) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bool ok;
-                    const bf16 *p = x_piece(row_of(step, i), &ok);
-                    queue16(queue_at + (uint32_t)(stage * 4 + i) * kThreads * 16, ok ? (const void *)(p + cx) : S, ok);
-                }
-            }
-            queue_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < ST - 1; ++i) ask(i, i);
-        int stage = 0;
-        // S of a group: 32 row pairs x RP, this thread's pairs read ahead
-        float2 sv[2 * MT];
-        auto read_s = [&](int grp) {
-#pragma unroll
-            for (int e = 0; e < 2 * MT; ++e) {
-                const int i = threadIdx.x + e * kThreads, r = i % RP, at = grp * 64 + i / RP * 2;
-                sv[e].x = r < k.R && at < have ? S[(int64_t)list[at] * k.R + r] : 0.0f;
-                sv[e].y = r < k.R && at + 1 < have ? S[(int64_t)list[at + 1] * k.R + r] : 0.0f;
-            }
-        };
-        read_s(0);
-        for (int grp = 0; grp * 4 < steps; ++grp) {
-            uint4 *op = operand + (grp & 1) * (4 * MT * 3 * 32);
-            // pair (t, t + 1) of r is word w of lane l of its row step
-#pragma unroll
-            for (int e = 0; e < 2 * MT; ++e) {
-                const int i = threadIdx.x + e * kThreads, r = i % RP, pair = i / RP, tt = (pair & 7) * 2;
-                uint32_t p[3];
-                split<3>(sv[e].x, sv[e].y, p);
-                const int l = (r & 7) * 4 + ((tt & 7) >> 1), w = ((r >> 3) & 1) + (tt >> 3) * 2;
-                uint32_t *to = reinterpret_cast<uint32_t *>(op + (((pair >> 3) * MT + (r >> 4)) * 3) * 32 + l) + w;
-#pragma unroll
-                for (int h = 0; h < 3; ++h) to[h * 32 * 4] = p[h];
-            }
-            if ((grp + 1) * 4 < steps) read_s(grp + 1);
-            __syncthreads();
-#pragma unroll 1
-            for (int st = 0; st < 4 && grp * 4 + st < steps; ++st) {
-                const int step = grp * 4 + st;
-                ask(step + ST - 1, stage == 0 ? ST - 1 : stage - 1);
-                queue_wait<ST - 1>();
-                Raw8 x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (VEC) {
-                        x[i] = read16(queue + (stage * 4 + i) * kThreads);
-                    } else {
-                        bool ok;
-                        const bf16 *p = x_piece(row_of(step, i), &ok);
-                        x[i] = ok ? load8<false>(p, cx, bcols) : Raw8{{0, 0, 0, 0}};
-                    }
-                }
-                stage = stage + 1 == ST ? 0 : stage + 1;
-                uint32_t b[8][2];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    b[j][0] = __byte_perm(x[0].w[j / 2], x[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
-                    b[j][1] = __byte_perm(x[2].w[j / 2], x[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 2; h >= 0; --h) {
-                        const uint4 f = op[((st * MT + m) * 3 + h) * 32 + lane];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) mma(acc[m][j], f.x, f.y, f.z, f.w, b[j][0], b[j][1]);
-                    }
-            }
-        }
-        queue_wait<0>();
+    const int bcols = (int)J.x.bcols, per_block = (bcols + 255) / 256, blk = tile / per_block;
+    const int c0 = (tile - blk * per_block) * 256;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const float *Sv = J.s;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) shmm_dev::mbar_init(shmm_dev::smem_u32(&bars[i]), 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    }
-    const float scale = J.scale ? J.scale[a] : 1.0f;
-    // Result piece (warp w, m, i): eight columns from 16 q + 8 (i & 1) of w's
-    // 64, row m * 16 + g (+8 for i >= 2).
-    auto put = [&](int w, int m, int i, const float *v) {
-        const int r = m * 16 + g + (i >> 1) * 8, c = c0 + (w - warp) * 64 + 16 * q + 8 * (i & 1);
-        if (r >= k.R || c >= bcols) return;
-        const int64_t at = ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + c;
-        if (!in_bounds(k.status, at, c + 8 <= bcols ? 8 : bcols - c, (int64_t)k.n * k.R * J.cols)) return;
-        float *o = J.out + at;
-        if (VEC && J.cols % 4 == 0 && reinterpret_cast<uintptr_t>(J.out) % 16 == 0) {
-            reinterpret_cast<float4 *>(o)[0] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-            reinterpret_cast<float4 *>(o)[1] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < bcols) o[j] = v[j] * scale;
-        }
-    };
-    if (cs == 1) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = acc[m][j][i];
-                put(warp, m, i, v);
-            }
-        return;
-    }
+    if (warp == 0) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 256);
+    if constexpr (Shape::kTiles == 2)  // the third part's tile adds zeros to the second's rows
+        for (int i = threadIdx.x; i < S * 64 * 8; i += kThreads)
+            *reinterpret_cast<uint4 *>(smem + (i / 512) * Shape::kStage + 32768 + 16384 + 8192 + (i % 512) * 16) =
+                make_uint4(0, 0, 0, 0);
+    shmm_tc::fence_before();
     __syncthreads();
-    float *sums = reinterpret_cast<float *>(smem);  // [(warp * MT + m) * 4 + i][j][lane]
+    shmm_tc::fence_after();
+    pdl_release();  // after the TMEM is held (see project_tc_kernel)
+    const uint32_t tmem = tmem_at;
+    // This thread's piece of X: row `warp` + 8 i of a group, eight columns.
+    const int cx = c0 + lane * 8;
+    const uint32_t x_to = smem_at + (lane / 8) * 8192 + warp * 128 + (((lane & 7) ^ warp) * 16);
+    uint32_t fills = 0;  // groups taken so far; stage fills % S
+    bool ok = true;
+    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
+        const int total = mark_rows(k.ids, w0, k.rows, a, marks, scratch, k.status);
+        // this CTA's share of the rows, in whole groups of 64
+        const int groups = (total + 63) / 64, lo = groups * cr / cs * 64;
+        const int hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
+        for (int l0 = lo; l0 < hi; l0 += kList) {
+            const int have = hi - l0 < kList ? hi - l0 : kList, ngroups = (have + 63) / 64;
+            list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
+            float2 sv[PAIRS];
+            auto read_s = [&](int grp) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+                for (int e = 0; e < PAIRS; ++e) {
+                    const int i = threadIdx.x + e * kThreads, r = i % RP, at = grp * 64 + i / RP * 2;
+                    sv[e].x = r < k.R && at < have ? Sv[(int64_t)list[at] * k.R + r] : 0.0f;
+                    sv[e].y = r < k.R && at + 1 < have ? Sv[(int64_t)list[at + 1] * k.R + r] : 0.0f;
+                }
+            };
+            // Asks for group grp's X and writes its S parts, into the stage
+            // of fill f once that stage's products are done.
+            auto fill = [&](int grp, uint32_t f) {
+                const uint32_t s = f % S;
+                if (f >= S) ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[s]), (f / S - 1) & 1, &abort_flag, k.status) && ok;
+                const uint32_t at0 = s * Shape::kStage;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 8; ++i) {
+                    const int at = grp * 64 + i * 8 + warp;
+                    const void *from = Sv;
+                    bool has = at < have && cx < bcols;
+                    if (has) {
+                        const uint32_t t = list[at], b = t / (uint32_t)J.x.brows;
+                        const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
+                        has = in_bounds(k.status, off + cx, 1, J.x.brows * J.x.bcols);
+                        if (has) from = (const bf16 *)J.x.at[b * J.x.b1 + blk] + off + (VEC ? cx : 0);
+                    }
+                    if constexpr (VEC) {
+                        queue16(x_to + at0 + i * 1024, from, has);
+                    } else {
+                        const Raw8 v = has ? load8<false>((const bf16 *)from, cx, bcols) : Raw8{{0, 0, 0, 0}};
+                        *reinterpret_cast<uint4 *>(smem + (x_to - smem_at) + at0 + i * 1024) =
+                            make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+                    }
+                }
+                queue_commit();
+                uint8_t *op = smem + at0 + 32768;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sums[(((warp * MT + m) * 4 + i) * 8 + j) * 32 + lane] = acc[m][j][i];
-    cluster.sync();
-    for (int u = cr + cs * warp; u < kWarps * MT * 4; u += cs * kWarps) {
-        float v[8];
+                for (int e = 0; e < PAIRS; ++e) {
+                    const int i = threadIdx.x + e * kThreads, r = i % RP, t = i / RP * 2;
+                    uint32_t p[3];
+                    split<3>(sv[e].x, sv[e].y, p);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        for (int b = 0; b < cs; ++b) {
-            const float *from = cluster.map_shared_rank(sums + u * 8 * 32 + lane, b);
+                    for (int h = 0; h < 3; ++h) {
+                        const int m = RP == 64 && h == 2 ? r + 128 : h * RP + r;  // row 128: the second tile's first
+                        *reinterpret_cast<uint32_t *>(op + m * 128 + (((t >> 3) ^ (m & 7)) * 16) + (t & 7) * 2) = p[h];
+                    }
+                }
+                if (grp + 1 < ngroups) read_s(grp + 1);
+            };
+            read_s(0);
+            fill(0, fills);
+            for (int grp = 0; grp < ngroups; ++grp) {
+                if (grp + 1 < ngroups) {
+                    fill(grp + 1, fills + 1);
+                    queue_wait<1>();
+                } else {
+                    queue_wait<0>();
+                }
+                shmm_tc::fence_async();
+                shmm_tc::fence_before();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    shmm_tc::fence_after();
+                    const uint32_t at = smem_at + (fills % S) * Shape::kStage;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += from[j * 32];
+                    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                        for (int i = 0; i < Shape::kTiles; ++i)
+                            shmm_tc::mma_issue(tmem, shmm_tc::operand(at + 32768 + i * 16384 + kk * 32, 16, 1024),
+                                               shmm_tc::operand(at + kk * 2048, 8192, 1024),
+                                               shmm_tc::instruction(256, true), fills > 0 || kk > 0 || i > 0);
+                    shmm_tc::mma_commit(shmm_dev::smem_u32(&bars[fills % S]));
+                }
+                ++fills;
+            }
         }
-        put(u / (4 * MT), u / 4 % MT, u & 3, v);
     }
-    cluster.sync();  // nobody leaves with what another CTA still reads
+    // Every product is done before its operands' memory is used again.
+    for (uint32_t f = fills > S ? fills - S : 0; f < fills; ++f)
+        shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[f % S]), (f / S) & 1, &abort_flag, k.status, false);
+    __syncthreads();
+    shmm_tc::fence_after();
+    // Result: 64 columns at a time from TMEM through shared memory, the parts'
+    // rows added; whole in shared memory when the cluster shares it.
+    const float scale = J.scale ? J.scale[a] : 1.0f;
+    auto put = [&](int r, int c, float v) {
+        const int64_t at = ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + c0 + c;
+        if (c0 + c < bcols && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols)) J.out[at] = v * scale;
+    };
+    float *piece = reinterpret_cast<float *>(smem);                // [128][kPitch]
+    float *sums = piece + 128 * Shape::kPitch;                     // [RP][256]
+    for (int c = 0; c < 256; c += 64) {
+        const int quad = warp & 3, half = warp >> 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[16];
+            const int at = half * 32 + h * 16;
+            if (fills) shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + c + at, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) piece[(quad * 32 + lane) * Shape::kPitch + at + j] = fills ? v[j] : 0.0f;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < k.R * 64; e += kThreads) {
+            const int r = e / 64, j = e % 64;
+            float v = 0.0f;
+#pragma unroll
+            for (int h = Shape::kBands - 1; h >= 0; --h) v += piece[(h * RP + r) * Shape::kPitch + j];
+            if (cs > 1) sums[r * 256 + c + j] = v;
+            else put(r, c + j, v);
+        }
+        __syncthreads();
+    }
+    if (cs > 1) {
+        cluster.sync();
+        for (int e = cr * kThreads + threadIdx.x; e < k.R * 256; e += cs * kThreads) {
+            put(e / 256, e % 256, sum_cluster(cluster, sums + e, cs));
+        }
+        cluster.sync();  // nobody leaves with what another CTA still reads
+    }
+    shmm_tc::fence_before();
+    __syncthreads();
+    shmm_tc::fence_after();
+    if (warp == 0) shmm_tc::tmem_free(tmem, 256);
 }
 
 // Any types, on CUDA cores: one adapter, 128 columns and 16 adapter rows per
@@ -1467,10 +1500,10 @@ cudaError_t expand(const ExpandK &k, int nranks, shmm_dtype_t wt, shmm_dtype_t o
     return ot == SHMM_F32 ? expand_type<float>(k, nranks, wt, s) : expand_type<bf16>(k, nranks, wt, s);
 }
 
-template <int MT, bool VEC>
-cudaError_t outer_mma(const OuterK &k, cudaStream_t s) {
-    using Shape = OuterShape<MT>;
-    auto kern = outer_mma_kernel<MT, VEC>;
+template <int RP, bool VEC>
+cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
+    using Shape = OuterShape<RP>;
+    auto kern = outer_tc_kernel<RP, VEC>;
     static shmm::PerDevice<int> done;
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
@@ -1478,7 +1511,7 @@ cudaError_t outer_mma(const OuterK &k, cudaStream_t s) {
     // Adapters differ in rows, so CTAs in time: shares of an adapter's rows
     // until there are several waves of CTAs or only four groups of rows each.
     int cs = 1;
-    while (cs < 8 && tiles * k.n * cs < 8 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
+    while (cs < 8 && tiles * k.n * cs < 4 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
                               Shape::kSmem, s, k);
 }
@@ -1495,12 +1528,12 @@ cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     bool vec = true;
     for (OuterJob &j : k.job) {
         if (!j.cols) continue;
-        j.tiles = (int)((j.x.bcols + 511) / 512 * j.x.b1);
+        j.tiles = (int)((j.x.bcols + 255) / 256 * j.x.b1);
         vec = vec && j.x.bcols % 8 == 0;
     }
-    if (k.R <= 16) return vec ? outer_mma<1, true>(k, s) : outer_mma<1, false>(k, s);
-    if (k.R <= 32) return vec ? outer_mma<2, true>(k, s) : outer_mma<2, false>(k, s);
-    return vec ? outer_mma<4, true>(k, s) : outer_mma<4, false>(k, s);
+    if (k.R <= 16) return vec ? outer_tc<16, true>(k, s) : outer_tc<16, false>(k, s);
+    if (k.R <= 32) return vec ? outer_tc<32, true>(k, s) : outer_tc<32, false>(k, s);
+    return vec ? outer_tc<64, true>(k, s) : outer_tc<64, false>(k, s);
 }
 
 void fill_expand(ExpandK *k, const shmm::AdapterArgs &a, const shmm::RankBoxes &b) {
