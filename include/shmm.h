@@ -434,8 +434,8 @@ shmm_status_t shmm_layernorm_forward(int64_t rows, int64_t cols, shmm_dtype_t dt
                                      void *total, void *y, float *mean, float *rstd, void *stream);
 
 /* Workspace of shmm_layernorm_backward (and, with the rows of every rank's
- * block added up, of shmm_layernorm_all_gather_backward), in bytes: at most
- * 304 partial rows of dgamma and dbeta.  Host only.  Errors: NULL, SHAPE. */
+ * block added up, of shmm_layernorm_all_gather_backward), in bytes: a few
+ * hundred partial rows of dgamma and dbeta at most.  Host only.  Errors: NULL, SHAPE. */
 shmm_status_t shmm_layernorm_backward_workspace_size(int64_t rows, int64_t cols, size_t *bytes);
 
 /* Gradient of shmm_layernorm_forward.  With xh = (x - mean) * rstd and

@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "checked.cuh"
+#include "device_wait.cuh"
 #include "pdl.cuh"
 #include "shmm_internal.h"
 
@@ -36,8 +37,9 @@ using shmm_pdl::pdl_enter;
 // re-reading kernels at the end.
 constexpr int kCols = 16;
 constexpr int kMaxThreads = 512;
-// CTAs whose partial dgamma, dbeta rows the workspace holds: two per SM.
-constexpr int kMaxParts = 304;
+// CTAs whose partial dgamma, dbeta rows the workspace holds: two per SM, more
+// of narrower rows, whose CTAs are smaller.
+int64_t max_parts(int64_t cols) { return cols >= 4096 ? 304 : cols >= 2048 ? 608 : 912; }
 
 // Pointer tables: one entry for the plain call (a small parameter block
 // keeps its launch short), one per rank for the gathered one.
@@ -178,6 +180,116 @@ __device__ __forceinline__ int col_of(int j) {
     return (th + j * nt) * VW;
 }
 
+// ---- rows in flight ----------------------------------------------------------
+
+// Many rows: one warp keeps whole rows coming through a ring in shared memory
+// (bulk copies, an mbarrier pair per entry) while the other warps work on the
+// rows that have landed, so the loads never wait for a row's two block sums.
+// An entry is one row of one buffer: x, a residual, or a member's gradient.
+// With the rows in registers instead, what was in flight fell with every
+// register the running sums took: 63 us forward and 81 us backward at 8192 x
+// 4096 bf16 with a residual, where this takes FWD_US and BWD_US.
+constexpr int kMaxStages = 16;
+struct Ring {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int abort_flag;
+};
+
+// One side's place in the ring.
+struct Turn {
+    int stage, phase;
+    __device__ void next(int stages) {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ void ring_init(Ring &ring, int stages, int readers) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            shmm_dev::mbar_init(shmm_dev::smem_u32(&ring.full[i]), 1);
+            shmm_dev::mbar_init(shmm_dev::smem_u32(&ring.empty[i]), readers);
+        }
+        ring.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+}
+
+// The copying thread: row `from` (or nothing, if the bounds-checked build
+// found it outside its buffer) into the next entry.  False after an abort.
+__device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uint32_t entries, uint32_t entry_bytes,
+                                         const void *from, uint32_t bytes, bool ok, int *status) {
+    if (!shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.empty[turn.stage]), turn.phase ^ 1, &ring.abort_flag, status))
+        return false;
+    const uint32_t bar = shmm_dev::smem_u32(&ring.full[turn.stage]);
+    if (ok) {
+        shmm_dev::mbar_expect_tx(bar, bytes);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                entries + turn.stage * entry_bytes),
+            "l"(from), "r"(bytes), "r"(bar)
+            : "memory");
+    } else {
+        shmm_dev::mbar_arrive(bar);
+    }
+    turn.next(stages);
+    return true;
+}
+
+// The copying thread, at the end: no copy into shared memory stays in
+// flight.  `put` entries were asked for.
+__device__ __forceinline__ void ring_drain(Ring &ring, int64_t put, int stages, int *status) {
+    for (int64_t u = put > stages ? put - stages : 0; u < put; ++u)
+        shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[u % stages]), (uint32_t)(u / stages) & 1, &ring.abort_flag,
+                            status, false);
+}
+
+// A working warp: the entry it is at has landed (after an abort it returns
+// at once and what it reads is anything: the call reports the timeout) ...
+__device__ __forceinline__ void ring_wait(Ring &ring, const Turn &turn, int *status) {
+    shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[turn.stage]), turn.phase, &ring.abort_flag, status);
+}
+// ... and has been read.
+__device__ __forceinline__ void ring_free(Ring &ring, Turn &turn, int stages) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) shmm_dev::mbar_arrive(shmm_dev::smem_u32(&ring.empty[turn.stage]));
+    turn.next(stages);
+}
+
+// row_sum over the first `n` threads (the working warps).
+__device__ __forceinline__ float2 stream_sum(float2 v, float2 *scratch, int &turn, int n) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    float2 *s = scratch + turn * (kMaxThreads / 32);
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x / 32] = v;
+    asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
+    float2 t = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < n / 32; ++i) {
+        const float2 u = s[i];
+        t.x += u.x;
+        t.y += u.y;
+    }
+    return t;
+}
+
+// An access of VW values of T out of a ring entry.
+template <typename T, int VW>
+__device__ __forceinline__ void from_ring(Raw<T, VW> &r, const uint8_t *entry, int c) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(entry + (size_t)c * sizeof(T));
+#pragma unroll
+    for (int i = 0; i < Raw<T, VW>::W / 4; ++i) {
+        const uint4 v = p[i];
+        r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
+    }
+}
+
 // ---- forward ---------------------------------------------------------------
 
 template <typename T, int VW, int NV, int N, bool ONEWARP>
@@ -281,6 +393,118 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_kernel(const __grid_co
             const int c = col_of<VW, ONEWARP>(j);
             if (c >= cols || !in_bounds(k.status, grow * cols + c, VW, k.G * k.brows * cols)) continue;
             for (int m = 0; m < k.G; ++m) y[j].store((T *)k.dst[g * k.G + m] + grow * cols + c);
+        }
+    }
+}
+
+// Many rows, through the ring.  blockDim.x - 32 threads work, the last warp
+// copies.
+template <typename T, int NV, int N, bool BIG>
+__global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
+    ln_forward_stream_kernel(const __grid_constant__ FwdK<N> k, int stages) {
+    pdl_enter();
+    constexpr int VW = 16 / (int)sizeof(T);
+    extern __shared__ __align__(128) uint8_t entries[];
+    __shared__ Ring ring;
+    __shared__ float2 scratch[2 * kMaxThreads / 32];
+    const int cols = (int)k.cols, work = blockDim.x - 32;
+    const uint32_t bytes = (uint32_t)cols * sizeof(T);
+    const bool has_res = N == 1 && k.res;
+    ring_init(ring, stages, work / 32);
+    Turn turn{0, 0};
+    if ((int)threadIdx.x >= work) {
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t at = shmm_dev::smem_u32(entries);
+            int64_t put = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < k.rows && ok; t += gridDim.x) {
+                int s, g;
+                int64_t rr, grow;
+                locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+                const bool in = in_bounds(k.status, rr * cols, cols, k.brows * cols);
+                ok = ring_put(ring, turn, stages, at, bytes, (const T *)k.src[s] + rr * cols, bytes, in, k.status);
+                put += ok;
+                if (ok && has_res) {
+                    ok = ring_put(ring, turn, stages, at, bytes, (const T *)k.res + rr * cols, bytes, in, k.status);
+                    put += ok;
+                }
+            }
+            ring_drain(ring, put, stages, k.status);
+        }
+        return;
+    }
+    int sum_turn = 0;
+    const float n = (float)cols;
+    float ga[NV][VW], be[NV][VW];
+    int col[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        col[j] = (threadIdx.x + j * work) * VW;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            ga[j][i] = col[j] < cols ? k.gamma[col[j] + i] : 0.0f;
+            be[j][i] = col[j] < cols ? k.beta[col[j] + i] : 0.0f;
+        }
+    }
+    for (int64_t t = blockIdx.x; t < k.rows; t += gridDim.x) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        Raw<T, VW> v[NV];
+        ring_wait(ring, turn, k.status);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            v[j].zero();
+            if (col[j] < cols) from_ring(v[j], entries + turn.stage * bytes, col[j]);
+        }
+        ring_free(ring, turn, stages);
+        if constexpr (N == 1) {
+            if (has_res) {  // rounded before anything is computed from it
+                ring_wait(ring, turn, k.status);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    if (col[j] >= cols) continue;
+                    Raw<T, VW> r;
+                    from_ring(r, entries + turn.stage * bytes, col[j]);
+                    float f[VW];
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) f[i] = v[j].get(i) + r.get(i);
+                    v[j].set(f);
+                    if (in_bounds(k.status, rr * cols + col[j], VW, k.brows * cols))
+                        v[j].store((T *)k.total + rr * cols + col[j]);
+                }
+                ring_free(ring, turn, stages);
+            }
+        }
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) sum.x += v[j].get(i);
+        const float mean = stream_sum(sum, scratch, sum_turn, work).x / n;
+        float2 sq = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (col[j] < cols)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float d = v[j].get(i) - mean;
+                    sq.x += d * d;
+                }
+        const float rstd = 1.0f / sqrtf(stream_sum(sq, scratch, sum_turn, work).x / n + k.eps);
+        if (threadIdx.x == 0 && in_bounds(k.status, rr, 1, k.brows)) {
+            k.mean[s][rr] = mean;
+            k.rstd[s][rr] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (col[j] >= cols || !in_bounds(k.status, grow * cols + col[j], VW, k.G * k.brows * cols)) continue;
+            float f[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i) f[i] = (v[j].get(i) - mean) * rstd * ga[j][i] + be[j][i];
+            Raw<T, VW> y;
+            y.set(f);
+            for (int m = 0; m < k.G; ++m) y.store((T *)k.dst[g * k.G + m] + grow * cols + col[j]);
         }
     }
 }
@@ -474,6 +698,155 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
     }
 }
 
+// Many rows, through the ring: per row the members' gradients in rank order,
+// x, and the residual's gradient.
+template <typename T, typename GT, int NV, int N, bool BIG>
+__global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
+    ln_backward_stream_kernel(const __grid_constant__ BwdK<N> k, int stages) {
+    pdl_enter();
+    constexpr int VW = 16 / (int)sizeof(T);
+    extern __shared__ __align__(128) uint8_t entries[];
+    __shared__ Ring ring;
+    __shared__ float2 scratch[2 * kMaxThreads / 32];
+    const int cols = (int)k.cols, work = blockDim.x - 32;
+    const uint32_t bytes = (uint32_t)cols * sizeof(T), gbytes = (uint32_t)cols * sizeof(GT);
+    const uint32_t entry = gbytes > bytes ? gbytes : bytes;
+    const bool has_res = N == 1 && k.res;
+    ring_init(ring, stages, work / 32);
+    Turn turn{0, 0};
+    if ((int)threadIdx.x >= work) {
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t at = shmm_dev::smem_u32(entries);
+            int64_t put = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < k.rows && ok; t += gridDim.x) {
+                int s, g;
+                int64_t rr, grow;
+                locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+                const bool in = in_bounds(k.status, rr * cols, cols, k.brows * cols);
+                const bool gin = in_bounds(k.status, grow * cols, cols, k.G * k.brows * cols);
+                for (int m = 0; m < k.G && ok; ++m) {
+                    ok = ring_put(ring, turn, stages, at, entry, (const GT *)k.grad[g * k.G + m] + grow * cols, gbytes,
+                                  gin, k.status);
+                    put += ok;
+                }
+                if (ok) {
+                    ok = ring_put(ring, turn, stages, at, entry, (const T *)k.src[s] + rr * cols, bytes, in, k.status);
+                    put += ok;
+                }
+                if (ok && has_res) {
+                    ok = ring_put(ring, turn, stages, at, entry, (const T *)k.res + rr * cols, bytes, in, k.status);
+                    put += ok;
+                }
+            }
+            ring_drain(ring, put, stages, k.status);
+        }
+        return;
+    }
+    int sum_turn = 0;
+    const float inv_n = 1.0f / (float)cols;
+    float ga[NV][VW], dg[NV][VW], db[NV][VW];
+    int col[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        col[j] = (threadIdx.x + j * work) * VW;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            ga[j][i] = col[j] < cols ? k.gamma[col[j] + i] : 0.0f;
+            dg[j][i] = db[j][i] = 0.0f;
+        }
+    }
+    float mean = 0.0f, rstd = 0.0f;  // read a row ahead
+    auto read_stats = [&](int64_t t) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        mean = k.mean[s][rr];
+        rstd = k.rstd[s][rr];
+    };
+    if ((int64_t)blockIdx.x < k.rows) read_stats(blockIdx.x);
+    for (int64_t t = blockIdx.x; t < k.rows; t += gridDim.x) {
+        int s, g;
+        int64_t rr, grow;
+        locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        float dy[NV][VW];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) dy[j][i] = 0.0f;
+        for (int m = 0; m < k.G; ++m) {
+            ring_wait(ring, turn, k.status);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (col[j] >= cols) continue;
+                Raw<GT, VW> d;
+                from_ring(d, entries + turn.stage * entry, col[j]);
+#pragma unroll
+                for (int i = 0; i < VW; ++i) dy[j][i] = m ? dy[j][i] + d.get(i) : d.get(i);
+            }
+            ring_free(ring, turn, stages);
+        }
+        Raw<T, VW> x[NV];
+        ring_wait(ring, turn, k.status);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            x[j].zero();
+            if (col[j] < cols) from_ring(x[j], entries + turn.stage * entry, col[j]);
+        }
+        ring_free(ring, turn, stages);
+        const float mu = mean, rs = rstd;
+        if (t + gridDim.x < k.rows) read_stats(t + gridDim.x);
+        float2 sum = make_float2(0.0f, 0.0f);  // of w and of w xh
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (col[j] < cols)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float xh = (x[j].get(i) - mu) * rs, w = dy[j][i] * ga[j][i];
+                    sum.x += w;
+                    sum.y += w * xh;
+                    dg[j][i] += dy[j][i] * xh;
+                    db[j][i] += dy[j][i];
+                }
+        sum = stream_sum(sum, scratch, sum_turn, work);
+        const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
+        if (has_res) ring_wait(ring, turn, k.status);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (col[j] >= cols) continue;
+            float o[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const float xh = (x[j].get(i) - mu) * rs;
+                o[i] = rs * (dy[j][i] * ga[j][i] - c1 - xh * c2);
+            }
+            if constexpr (N == 1) {
+                if (has_res) {
+                    Raw<T, VW> r;
+                    from_ring(r, entries + turn.stage * entry, col[j]);
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) o[i] += r.get(i);
+                }
+            }
+            Raw<T, VW> y;
+            y.set(o);
+            if (in_bounds(k.status, rr * cols + col[j], VW, k.brows * cols)) y.store((T *)k.dst[s] + rr * cols + col[j]);
+        }
+        if (has_res) ring_free(ring, turn, stages);
+    }
+    float *part = k.part + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (col[j] >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < VW; i += 4) {
+            *reinterpret_cast<float4 *>(part + col[j] + i) = make_float4(dg[j][i], dg[j][i + 1], dg[j][i + 2], dg[j][i + 3]);
+            *reinterpret_cast<float4 *>(part + cols + col[j] + i) =
+                make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
+        }
+    }
+}
+
 // Rows of any width: the row is read twice, and each thread adds its columns
 // of dgamma and dbeta to the CTA's partial row, which it zeroes first.
 template <typename T, typename GT, int N>
@@ -529,8 +902,16 @@ __global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, in
     __shared__ float sh[32][33];
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float a = 0.0f;
-    if (c < 2 * cols)
-        for (int p = threadIdx.y; p < parts; p += 32) a += part[(int64_t)p * 2 * cols + c];
+    if (c < 2 * cols) {
+        constexpr int U = 10;  // loads in flight
+        for (int p0 = threadIdx.y; p0 < parts; p0 += 32 * U) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = p0 + 32 * u < parts ? part[(int64_t)(p0 + 32 * u) * 2 * cols + c] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) a += v[u];
+        }
+    }
     sh[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
     if (threadIdx.y == 0 && c < 2 * cols) {
@@ -570,6 +951,60 @@ Shape shape_for(int64_t cols, int vw, int want_cols) {
     return {nv, threads, false};
 }
 
+// Launch shape of the ring kernels: CTAs per SM for `threads` working threads,
+// and the ring's entries of `entry` bytes in each CTA's share of an SM.
+struct StreamShape {
+    int threads, per_sm, stages;
+    size_t smem;
+};
+StreamShape stream_shape(int64_t cols, int vw, int64_t entry) {
+    StreamShape h;
+    h.threads = (int)((cols + kCols * 32 - 1) / (kCols * 32)) * 32;
+    h.per_sm = h.threads > 256 ? 1 : 512 / h.threads > 6 ? 6 : 512 / h.threads;
+    const int64_t budget = (216 * 1024) / h.per_sm - 2048;
+    h.stages = (int)(budget / entry < kMaxStages ? budget / entry : kMaxStages);
+    h.smem = (size_t)(h.stages * entry);
+    return h;
+}
+
+template <typename K>
+cudaError_t launch_stream(void (*kern)(K, int), const K &k, const StreamShape &h, int64_t grid, cudaStream_t s,
+                          shmm::PerDevice<int> *done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= shmm::kMaxDevices) return cudaErrorInvalidDevice;
+    if (!done->get(dev)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
+        if (e != cudaSuccess) return e;
+        done->set(dev, 1);
+    }
+    return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)h.threads + 32), h.smem, s, k, h.stages);
+}
+
+// Rows enough for the ring kernels: every CTA has three rows or more to keep
+// in flight.
+bool stream_rows(int64_t rows, int64_t cols) { return cols > 32 * kCols && rows >= 6 * sms(); }
+
+template <typename T, int N, bool BIG>
+cudaError_t forward_stream(const FwdK<N> &k, cudaStream_t s) {
+    constexpr int VW = 16 / (int)sizeof(T);
+    static shmm::PerDevice<int> done;
+    const StreamShape h = stream_shape(k.cols, VW, k.cols * (int64_t)sizeof(T));
+    return launch_stream(ln_forward_stream_kernel<T, kCols / VW, N, BIG>, k, h, (int64_t)sms() * h.per_sm, s, &done);
+}
+
+template <typename T, typename GT, int N, bool BIG>
+cudaError_t backward_stream(const BwdK<N> &k, int *parts, cudaStream_t s) {
+    constexpr int VW = 16 / (int)sizeof(T);
+    static shmm::PerDevice<int> done;
+    const StreamShape h = stream_shape(k.cols, VW, k.cols * (int64_t)(sizeof(T) > sizeof(GT) ? sizeof(T) : sizeof(GT)));
+    int64_t grid = (int64_t)sms() * h.per_sm;
+    if (grid > max_parts(k.cols)) grid = max_parts(k.cols);
+    *parts = (int)grid;
+    return launch_stream(ln_backward_stream_kernel<T, GT, kCols / VW, N, BIG>, k, h, grid, s, &done);
+}
+
 template <typename T, int VW, int N>
 cudaError_t forward_vec(const FwdK<N> &k, cudaStream_t s) {
     const bool few = k.rows < sms();
@@ -595,7 +1030,9 @@ cudaError_t forward(const FwdK<N> &k, cudaStream_t s) {
         const dim3 g((unsigned)(k.rows < cap ? k.rows : cap));
         return launch_pdl(ln_forward_wide_kernel<T, N>, g, dim3(kMaxThreads), 0, s, k);
     }
-    return k.cols % V == 0 ? forward_vec<T, V, N>(k, s) : forward_vec<T, 1, N>(k, s);
+    if (k.cols % V) return forward_vec<T, 1, N>(k, s);
+    if (!stream_rows(k.rows, k.cols)) return forward_vec<T, V, N>(k, s);
+    return k.cols > 256 * kCols ? forward_stream<T, N, true>(k, s) : forward_stream<T, N, false>(k, s);
 }
 
 template <typename T, typename GT, int VW, int N>
@@ -603,8 +1040,8 @@ cudaError_t backward_vec(const BwdK<N> &k, int *parts, cudaStream_t s) {
     const Shape h = shape_for(k.cols, VW, kCols);
     const int64_t per_cta = h.onewarp ? h.threads / 32 : 1;
     int64_t grid = (k.rows + per_cta - 1) / per_cta;
-    int64_t cap = sms() * (h.threads <= 256 ? 2 : 1);
-    if (cap > kMaxParts) cap = kMaxParts;
+    int64_t cap = (int64_t)sms() * (h.threads > 256 ? 1 : 512 / h.threads > 6 ? 6 : 512 / h.threads);
+    if (cap > max_parts(k.cols)) cap = max_parts(k.cols);
     if (grid > cap) grid = cap;
     *parts = (int)grid;
     const dim3 g((unsigned)grid), b((unsigned)h.threads);
@@ -621,11 +1058,14 @@ cudaError_t backward(const BwdK<N> &k, int *parts, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     if (k.cols > (int64_t)kMaxThreads * kCols) {
         int64_t cap = (int64_t)sms();
-        if (cap > kMaxParts) cap = kMaxParts;
+        if (cap > max_parts(k.cols)) cap = max_parts(k.cols);
         *parts = (int)(k.rows < cap ? k.rows : cap);
         return launch_pdl(ln_backward_wide_kernel<T, GT, N>, dim3((unsigned)*parts), dim3(kMaxThreads), 0, s, k);
     }
-    return k.cols % V == 0 ? backward_vec<T, GT, V, N>(k, parts, s) : backward_vec<T, GT, 1, N>(k, parts, s);
+    if (k.cols % V) return backward_vec<T, GT, 1, N>(k, parts, s);
+    if (!stream_rows(k.rows, k.cols)) return backward_vec<T, GT, V, N>(k, parts, s);
+    return k.cols > 256 * kCols ? backward_stream<T, GT, N, true>(k, parts, s)
+                                : backward_stream<T, GT, N, false>(k, parts, s);
 }
 
 template <int N>
@@ -688,7 +1128,7 @@ cudaError_t run_backward(const shmm::NormBackwardArgs &a, int *status, cudaStrea
 namespace shmm {
 
 size_t norm_workspace_bytes(int64_t rows, int64_t cols) {
-    const int64_t parts = rows < kMaxParts ? rows : kMaxParts;
+    const int64_t most = max_parts(cols), parts = rows < most ? rows : most;
     return (size_t)(parts * 2 * cols * 4);
 }
 

@@ -88,7 +88,7 @@ SHAPES = [(1, 1), (1, 8), (3, 7), (2, 64), (9, 512), (257, 520), (5, 1001), (33,
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("rows,cols", SHAPES + [(1003, 4096), (920, 520), (950, 8192), (2500, 1544)])
 def test_forward(s, rows, cols, dtype, residual):
     x, gamma, beta, r = inputs(rows, cols, dtype)
     res = r(rows, cols).to(DT[dtype]) if residual else None
@@ -138,10 +138,10 @@ def test_forward_special_rows(s):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("cols", [512, 4096, 1001, 9000])
-def test_forward_in_place(s, cols):
-    x, gamma, beta, r = inputs(37, cols, "bf16")
-    res = r(37, cols).to(torch.bfloat16)
+@pytest.mark.parametrize("rows,cols", [(37, 512), (37, 4096), (37, 1001), (37, 9000), (1301, 4096)])
+def test_forward_in_place(s, rows, cols):
+    x, gamma, beta, r = inputs(rows, cols, "bf16")
+    res = r(rows, cols).to(torch.bfloat16)
     y, mean, rstd, total = forward(s, x, gamma, beta, res)
     xa, ra = x.cuda(), res.cuda()
     m2, r2 = torch.empty_like(mean), torch.empty_like(rstd)
@@ -168,7 +168,7 @@ def backward(s, dy, x, mean, rstd, gamma, res=None, ws=None):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("rows,cols", SHAPES + [(700, 2048), (1200, 72)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(700, 2048), (1200, 72), (1003, 4096), (920, 520), (950, 8192), (2500, 1544)])
 def test_backward(s, rows, cols, dtype, residual):
     x, gamma, beta, r = inputs(rows, cols, dtype)
     dy = r(rows, cols).to(DT[dtype])
@@ -198,12 +198,12 @@ def test_backward_without_rows_writes_zeros(s):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("cols", [96, 4096, 1001, 9000])
-def test_backward_in_place(s, cols):
-    """dx over dy, and over the residual's gradient, gives the same bits."""
+@pytest.mark.parametrize("rows,cols", [(401, 96), (401, 4096), (401, 1001), (401, 9000), (1301, 4096)])
+def test_backward_in_place(s, rows, cols):
+    """dx over dy, over x and over the residual's gradient gives the same bits."""
     from partial_sum_reduction_gb300 import helpers as H
-    x, gamma, beta, r = inputs(401, cols, "bf16")
-    dy, res = r(401, cols).bfloat16(), r(401, cols).bfloat16()
+    x, gamma, beta, r = inputs(rows, cols, "bf16")
+    dy, res = r(rows, cols).bfloat16(), r(rows, cols).bfloat16()
     _, wm, wr, _ = formula(x, gamma, beta, 1e-5)
     mean, rstd = wm.float(), wr.float()
     want = backward(s, dy, x, mean, rstd, gamma, res)
@@ -211,7 +211,7 @@ def test_backward_in_place(s, cols):
         b = {"dy": dy.cuda(), "res": res.cuda(), "x": x.cuda()}
         dg, db = torch.empty_like(want[1]), torch.empty_like(want[2])
         s.shmm_layernorm_backward(b["dy"], b["x"], mean.cuda(), rstd.cuda(), gamma.cuda(), b[which], dg, db,
-                                  H.layernorm_workspace(401, cols), residual_grad=b["res"])
+                                  H.layernorm_workspace(rows, cols), residual_grad=b["res"])
         torch.cuda.synchronize()
         assert torch.equal(b[which], want[0]) and torch.equal(dg, want[1]) and torch.equal(db, want[2])
 
@@ -264,7 +264,9 @@ GATHERS = [([("X", 2)], (("X",), ()), ((), ()), ((), ()), 1), ([("X", 8)], (("X"
 @pytest.mark.gpu
 @pytest.mark.parametrize("brows,cols,dtype,grad", [(5, 64, "bf16", "f32"), (33, 1001, "bf16", "bf16"),
                                                    (70, 4096, "bf16", "f32"), (9, 2048, "f32", "f32"),
-                                                   (1, 8192, "bf16", "bf16"), (3, 8208, "f32", "f32")])
+                                                   (1, 8192, "bf16", "bf16"), (3, 8208, "f32", "f32"),
+                                                   (479, 1032, "bf16", "f32"), (461, 4096, "bf16", "bf16"),
+                                                   (470, 8192, "f32", "f32")])
 @pytest.mark.parametrize("which", range(len(GATHERS)))
 def test_gathered_pair(s, which, brows, cols, dtype, grad):
     from partial_sum_reduction_gb300 import helpers as H
@@ -404,7 +406,8 @@ def test_refusals(monkeypatch):
     assert w(dy=None) == m.ERR_NULL and w(dg=None) == m.ERR_NULL and w(dx=odd) == m.ERR_ALIGN
     assert w(r=odd) == m.ERR_ALIGN and w(dt=7) == m.ERR_DTYPE and w(rows=-2) == m.ERR_SHAPE and w(cols=0) == m.OK
     assert s.shmm_layernorm_backward_workspace_size(4, 64) == 4 * 2 * 64 * 4
-    assert s.shmm_layernorm_backward_workspace_size(1 << 20, 64) == 304 * 2 * 64 * 4
+    big = s.shmm_layernorm_backward_workspace_size(1 << 20, 64)
+    assert big == s.shmm_layernorm_backward_workspace_size(1 << 30, 64) <= 1024 * 2 * 64 * 4
     assert L.shmm_layernorm_backward_workspace_size(1, 1, None) == m.ERR_NULL
     with pytest.raises(s.ShmmError):
         s.shmm_layernorm_backward_workspace_size(-1, 4)
