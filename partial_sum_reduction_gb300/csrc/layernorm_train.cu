@@ -71,6 +71,38 @@ struct BwdK {
     int *status;
 };
 
+// Two fp32 values in one register pair: one instruction for both (the issue
+// slots, not the memory, bound these kernels with one value each).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 split(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // VW consecutive values as they lie in memory: one access of VW * sizeof(T)
 // bytes (two for 8 fp32 values), kept packed until they are used.
 template <typename T, int VW>
@@ -98,6 +130,20 @@ struct Raw {
     __device__ float get(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    }
+    __device__ F2 get2(int i) const {  // values 2 i and 2 i + 1
+        if constexpr (sizeof(T) == 4) return pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    __device__ void set2(int i, F2 v) {
+        const float2 f = split(v);
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i] = __float_as_uint(f.x);
+            w[2 * i + 1] = __float_as_uint(f.y);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
     }
     __device__ void set(const float *v) {
         if constexpr (sizeof(T) == 4) {
@@ -144,6 +190,22 @@ __device__ __forceinline__ void locate(int64_t t, int64_t brows, int G, int *s, 
     }
 }
 
+// The warps' sums in order; the reads go out together.
+__device__ __forceinline__ float2 sum_scratch(const float2 *s, int warps) {
+    float2 t = make_float2(0.0f, 0.0f);
+    for (int i0 = 0; i0 < warps; i0 += 8) {
+        float2 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = i0 + i < warps ? s[i0 + i] : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            t.x += u[i].x;
+            t.y += u[i].y;
+        }
+    }
+    return t;
+}
+
 // Sum of two values over the threads of a row: shuffles, then (more than one
 // warp) the warps' sums in order.  Every thread gets the same bits.
 // `scratch` holds two float2 rows used in turn, so one barrier per sum is
@@ -161,14 +223,7 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2 *scratch, int &turn) 
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x / 32] = v;
     __syncthreads();
-    const int nw = blockDim.x / 32;
-    float2 t = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < nw; ++i) {
-        const float2 u = s[i];
-        t.x += u.x;
-        t.y += u.y;
-    }
-    return t;
+    return sum_scratch(s, blockDim.x / 32);
 }
 
 // Thread's first column of its access j: consecutive threads read
@@ -182,14 +237,16 @@ __device__ __forceinline__ int col_of(int j) {
 
 // ---- rows in flight ----------------------------------------------------------
 
-// Many rows: one warp keeps whole rows coming through a ring in shared memory
+// Many rows: two warps keep whole rows coming through a ring in shared memory
 // (bulk copies, an mbarrier pair per entry) while the other warps work on the
 // rows that have landed, so the loads never wait for a row's two block sums.
-// An entry is one row of one buffer: x, a residual, or a member's gradient.
+// An entry is one row of one buffer: x, a residual, or a member's gradient;
+// the copying warps (a thread of each) take every other one, because a
+// thread's own instructions per entry are what one alone was bound by.
 // With the rows in registers instead, what was in flight fell with every
 // register the running sums took: 63 us forward and 81 us backward at 8192 x
 // 4096 bf16 with a residual, where this takes FWD_US and BWD_US.
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 16, kCopiers = 2;
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort_flag;
@@ -198,9 +255,10 @@ struct Ring {
 // One side's place in the ring.
 struct Turn {
     int stage, phase;
-    __device__ void next(int stages) {
-        if (++stage == stages) {
-            stage = 0;
+    __device__ void next(int stages, int by = 1) {  // by <= stages
+        stage += by;
+        if (stage >= stages) {
+            stage -= stages;
             phase ^= 1;
         }
     }
@@ -218,8 +276,8 @@ __device__ __forceinline__ void ring_init(Ring &ring, int stages, int readers) {
     __syncthreads();
 }
 
-// The copying thread: row `from` (or nothing, if the bounds-checked build
-// found it outside its buffer) into the next entry.  False after an abort.
+// A copying thread: row `from` (or nothing, if the bounds-checked build found
+// it outside its buffer) into its next entry.  False after an abort.
 __device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uint32_t entries, uint32_t entry_bytes,
                                          const void *from, uint32_t bytes, bool ok, int *status) {
     if (!shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.empty[turn.stage]), turn.phase ^ 1, &ring.abort_flag, status))
@@ -235,16 +293,23 @@ __device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uin
     } else {
         shmm_dev::mbar_arrive(bar);
     }
-    turn.next(stages);
+    turn.next(stages, kCopiers);
     return true;
 }
 
-// The copying thread, at the end: no copy into shared memory stays in
-// flight.  `put` entries were asked for.
-__device__ __forceinline__ void ring_drain(Ring &ring, int64_t put, int stages, int *status) {
-    for (int64_t u = put > stages ? put - stages : 0; u < put; ++u)
-        shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[u % stages]), (uint32_t)(u / stages) & 1, &ring.abort_flag,
-                            status, false);
+// The end, for every thread.  The working warps have waited for every entry,
+// unless a wait was given up: then a copying thread (`put` > 0, its n-th entry
+// number `first` + n kCopiers) waits, again with a limit, for its entries of
+// the last lap, so that no copy into shared memory stays in flight.
+__device__ __forceinline__ void ring_end(Ring &ring, int first, int64_t put, int stages, int *status) {
+    __syncwarp();
+    __syncthreads();
+    if (put && *(volatile int *)&ring.abort_flag)
+        for (int64_t i = put > stages / kCopiers ? put - stages / kCopiers : 0; i < put; ++i) {
+            const int64_t u = first + i * kCopiers;
+            shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[u % stages]), (uint32_t)(u / stages) & 1,
+                                &ring.abort_flag, status, false);
+        }
 }
 
 // A working warp: the entry it is at has landed (after an abort it returns
@@ -270,13 +335,7 @@ __device__ __forceinline__ float2 stream_sum(float2 v, float2 *scratch, int &tur
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x / 32] = v;
     asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
-    float2 t = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < n / 32; ++i) {
-        const float2 u = s[i];
-        t.x += u.x;
-        t.y += u.y;
-    }
-    return t;
+    return sum_scratch(s, n / 32);
 }
 
 // An access of VW values of T out of a ring entry.
@@ -397,53 +456,56 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_kernel(const __grid_co
     }
 }
 
-// Many rows, through the ring.  blockDim.x - 32 threads work, the last warp
-// copies.
+// Many rows, through the ring.  blockDim.x - 32 kCopiers threads work, the last
+// kCopiers warps copy.
 template <typename T, int NV, int N, bool BIG>
-__global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
+__global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG ? 1 : 2)
     ln_forward_stream_kernel(const __grid_constant__ FwdK<N> k, int stages) {
     pdl_enter();
     constexpr int VW = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) uint8_t entries[];
     __shared__ Ring ring;
     __shared__ float2 scratch[2 * kMaxThreads / 32];
-    const int cols = (int)k.cols, work = blockDim.x - 32;
+    const int cols = (int)k.cols, work = blockDim.x - 32 * kCopiers;
     const uint32_t bytes = (uint32_t)cols * sizeof(T);
     const bool has_res = N == 1 && k.res;
     ring_init(ring, stages, work / 32);
-    Turn turn{0, 0};
     if ((int)threadIdx.x >= work) {
+        int64_t put = 0;
+        const int first = ((int)threadIdx.x - work) / 32;
         if ((threadIdx.x & 31) == 0) {
+            // entries of a row: x, then the residual
+            const int per_row = has_res ? 2 : 1;
             const uint32_t at = shmm_dev::smem_u32(entries);
-            int64_t put = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < k.rows && ok; t += gridDim.x) {
+            Turn turn{first, 0};
+            int64_t t = blockIdx.x + (int64_t)(first / per_row) * gridDim.x;
+            const int e = first % per_row;  // the same in every row: per_row divides kCopiers
+            const int64_t step = (int64_t)gridDim.x * (kCopiers / per_row);
+            for (bool ok = true; t < k.rows && ok; t += step) {
                 int s, g;
                 int64_t rr, grow;
                 locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-                const bool in = in_bounds(k.status, rr * cols, cols, k.brows * cols);
-                ok = ring_put(ring, turn, stages, at, bytes, (const T *)k.src[s] + rr * cols, bytes, in, k.status);
+                ok = ring_put(ring, turn, stages, at, bytes, (const T *)(e ? k.res : k.src[s]) + rr * cols, bytes,
+                              in_bounds(k.status, rr * cols, cols, k.brows * cols), k.status);
                 put += ok;
-                if (ok && has_res) {
-                    ok = ring_put(ring, turn, stages, at, bytes, (const T *)k.res + rr * cols, bytes, in, k.status);
-                    put += ok;
-                }
             }
-            ring_drain(ring, put, stages, k.status);
         }
+        ring_end(ring, first, put, stages, k.status);
         return;
     }
+    Turn turn{0, 0};
     int sum_turn = 0;
     const float n = (float)cols;
-    float ga[NV][VW], be[NV][VW];
+    F2 ga[NV][VW / 2], be[NV][VW / 2];
     int col[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         col[j] = (threadIdx.x + j * work) * VW;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            ga[j][i] = col[j] < cols ? k.gamma[col[j] + i] : 0.0f;
-            be[j][i] = col[j] < cols ? k.beta[col[j] + i] : 0.0f;
+        for (int i = 0; i < VW / 2; ++i) {
+            const bool in = col[j] < cols;
+            ga[j][i] = in ? pair(k.gamma[col[j] + 2 * i], k.gamma[col[j] + 2 * i + 1]) : both(0.0f);
+            be[j][i] = in ? pair(k.beta[col[j] + 2 * i], k.beta[col[j] + 2 * i + 1]) : both(0.0f);
         }
     }
     for (int64_t t = blockIdx.x; t < k.rows; t += gridDim.x) {
@@ -466,32 +528,35 @@ __global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
                     if (col[j] >= cols) continue;
                     Raw<T, VW> r;
                     from_ring(r, entries + turn.stage * bytes, col[j]);
-                    float f[VW];
 #pragma unroll
-                    for (int i = 0; i < VW; ++i) f[i] = v[j].get(i) + r.get(i);
-                    v[j].set(f);
+                    for (int i = 0; i < VW / 2; ++i) v[j].set2(i, v[j].get2(i) + r.get2(i));
                     if (in_bounds(k.status, rr * cols + col[j], VW, k.brows * cols))
                         v[j].store((T *)k.total + rr * cols + col[j]);
                 }
                 ring_free(ring, turn, stages);
             }
         }
-        float2 sum = make_float2(0.0f, 0.0f);
+        F2 sum = both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VW; ++i) sum.x += v[j].get(i);
-        const float mean = stream_sum(sum, scratch, sum_turn, work).x / n;
-        float2 sq = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < VW / 2; ++i) sum = sum + v[j].get2(i);
+        float2 part = split(sum);
+        const float mean = stream_sum(make_float2(part.x + part.y, 0.0f), scratch, sum_turn, work).x / n;
+        const F2 minus = both(-mean);
+        F2 sq = both(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (col[j] < cols)
 #pragma unroll
-                for (int i = 0; i < VW; ++i) {
-                    const float d = v[j].get(i) - mean;
-                    sq.x += d * d;
+                for (int i = 0; i < VW / 2; ++i) {
+                    const F2 d = v[j].get2(i) + minus;
+                    sq = fma(d, d, sq);
                 }
-        const float rstd = 1.0f / sqrtf(stream_sum(sq, scratch, sum_turn, work).x / n + k.eps);
+        part = split(sq);
+        const float rstd =
+            1.0f / sqrtf(stream_sum(make_float2(part.x + part.y, 0.0f), scratch, sum_turn, work).x / n + k.eps);
+        const F2 scale = both(rstd);
         if (threadIdx.x == 0 && in_bounds(k.status, rr, 1, k.brows)) {
             k.mean[s][rr] = mean;
             k.rstd[s][rr] = rstd;
@@ -499,14 +564,13 @@ __global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (col[j] >= cols || !in_bounds(k.status, grow * cols + col[j], VW, k.G * k.brows * cols)) continue;
-            float f[VW];
-#pragma unroll
-            for (int i = 0; i < VW; ++i) f[i] = (v[j].get(i) - mean) * rstd * ga[j][i] + be[j][i];
             Raw<T, VW> y;
-            y.set(f);
+#pragma unroll
+            for (int i = 0; i < VW / 2; ++i) y.set2(i, fma((v[j].get2(i) + minus) * scale, ga[j][i], be[j][i]));
             for (int m = 0; m < k.G; ++m) y.store((T *)k.dst[g * k.G + m] + grow * cols + col[j]);
         }
     }
+    ring_end(ring, 0, 0, stages, k.status);
 }
 
 // Rows of any width: the row is read three times (from L2 after the first).
@@ -601,7 +665,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
         int s, g;
         int64_t rr, grow;
         locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-        const float mean = k.mean[s][rr], rstd = k.rstd[s][rr];
+        const float mean = k.mean[s][rr], rstd = k.rstd[s][rr], shift = -mean * rstd;  // xh = x rstd + shift
         float dy[NV][VW];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -630,21 +694,21 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
             if (col_of<VW, ONEWARP>(j) < cols)
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
-                    const float xh = (x[j].get(i) - mean) * rstd, w = dy[j][i] * ga[j][i];
+                    const float xh = fmaf(x[j].get(i), rstd, shift), w = dy[j][i] * ga[j][i];
                     sum.x += w;
-                    sum.y += w * xh;
-                    dg[j][i] += dy[j][i] * xh;
+                    sum.y = fmaf(w, xh, sum.y);
+                    dg[j][i] = fmaf(dy[j][i], xh, dg[j][i]);
                     db[j][i] += dy[j][i];
                 }
         sum = row_sum<ONEWARP>(sum, scratch, turn);
-        const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
+        const float k1 = -rstd * (sum.x * inv_n), k2 = -rstd * (sum.y * inv_n);
         float o[NV][VW];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
-                const float xh = (x[j].get(i) - mean) * rstd;
-                o[j][i] = rstd * (dy[j][i] * ga[j][i] - c1 - xh * c2);
+                const float xh = fmaf(x[j].get(i), rstd, shift);
+                o[j][i] = fmaf(xh, k2, fmaf(dy[j][i] * ga[j][i], rstd, k1));
             }
         if (t + step < k.rows) load_row(t + step);
 #pragma unroll
@@ -701,59 +765,62 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
 // Many rows, through the ring: per row the members' gradients in rank order,
 // x, and the residual's gradient.
 template <typename T, typename GT, int NV, int N, bool BIG>
-__global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
+__global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG ? 1 : 2)
     ln_backward_stream_kernel(const __grid_constant__ BwdK<N> k, int stages) {
     pdl_enter();
     constexpr int VW = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) uint8_t entries[];
     __shared__ Ring ring;
     __shared__ float2 scratch[2 * kMaxThreads / 32];
-    const int cols = (int)k.cols, work = blockDim.x - 32;
+    const int cols = (int)k.cols, work = blockDim.x - 32 * kCopiers;
     const uint32_t bytes = (uint32_t)cols * sizeof(T), gbytes = (uint32_t)cols * sizeof(GT);
     const uint32_t entry = gbytes > bytes ? gbytes : bytes;
     const bool has_res = N == 1 && k.res;
     ring_init(ring, stages, work / 32);
-    Turn turn{0, 0};
     if ((int)threadIdx.x >= work) {
+        int64_t put = 0;
+        const int first = ((int)threadIdx.x - work) / 32;
         if ((threadIdx.x & 31) == 0) {
+            const int per_row = k.G + 1 + (has_res ? 1 : 0);
             const uint32_t at = shmm_dev::smem_u32(entries);
-            int64_t put = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < k.rows && ok; t += gridDim.x) {
-                int s, g;
-                int64_t rr, grow;
-                locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-                const bool in = in_bounds(k.status, rr * cols, cols, k.brows * cols);
-                const bool gin = in_bounds(k.status, grow * cols, cols, k.G * k.brows * cols);
-                for (int m = 0; m < k.G && ok; ++m) {
-                    ok = ring_put(ring, turn, stages, at, entry, (const GT *)k.grad[g * k.G + m] + grow * cols, gbytes,
-                                  gin, k.status);
-                    put += ok;
+            Turn turn{first, 0};
+            int64_t t = blockIdx.x;
+            int e = first, s, g;  // the next entry: number e of row t
+            int64_t rr, grow;
+            if (t < k.rows) locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+            for (bool ok = true; ok;) {
+                if (e >= per_row) {  // kCopiers <= per_row: the next row
+                    e -= per_row;
+                    t += gridDim.x;
+                    if (t < k.rows) locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
                 }
-                if (ok) {
-                    ok = ring_put(ring, turn, stages, at, entry, (const T *)k.src[s] + rr * cols, bytes, in, k.status);
-                    put += ok;
-                }
-                if (ok && has_res) {
-                    ok = ring_put(ring, turn, stages, at, entry, (const T *)k.res + rr * cols, bytes, in, k.status);
-                    put += ok;
-                }
+                if (t >= k.rows) break;
+                if (e < k.G)
+                    ok = ring_put(ring, turn, stages, at, entry, (const GT *)k.grad[g * k.G + e] + grow * cols, gbytes,
+                                  in_bounds(k.status, grow * cols, cols, k.G * k.brows * cols), k.status);
+                else
+                    ok = ring_put(ring, turn, stages, at, entry,
+                                  (const T *)(N == 1 && e > k.G ? k.res : k.src[s]) + rr * cols, bytes,
+                                  in_bounds(k.status, rr * cols, cols, k.brows * cols), k.status);
+                put += ok;
+                e += kCopiers;
             }
-            ring_drain(ring, put, stages, k.status);
         }
+        ring_end(ring, first, put, stages, k.status);
         return;
     }
+    Turn turn{0, 0};
     int sum_turn = 0;
     const float inv_n = 1.0f / (float)cols;
-    float ga[NV][VW], dg[NV][VW], db[NV][VW];
+    F2 ga[NV][VW / 2], dg[NV][VW / 2], db[NV][VW / 2];
     int col[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         col[j] = (threadIdx.x + j * work) * VW;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            ga[j][i] = col[j] < cols ? k.gamma[col[j] + i] : 0.0f;
-            dg[j][i] = db[j][i] = 0.0f;
+        for (int i = 0; i < VW / 2; ++i) {
+            ga[j][i] = col[j] < cols ? pair(k.gamma[col[j] + 2 * i], k.gamma[col[j] + 2 * i + 1]) : both(0.0f);
+            dg[j][i] = db[j][i] = both(0.0f);
         }
     }
     float mean = 0.0f, rstd = 0.0f;  // read a row ahead
@@ -769,23 +836,30 @@ __global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
         int s, g;
         int64_t rr, grow;
         locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-        float dy[NV][VW];
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < VW; ++i) dy[j][i] = 0.0f;
+        // The members' gradients.  One member's stay packed until they are used.
+        Raw<GT, VW> d0[NV];
+        F2 dys[NV][VW / 2];
         for (int m = 0; m < k.G; ++m) {
             ring_wait(ring, turn, k.status);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (col[j] >= cols) continue;
-                Raw<GT, VW> d;
-                from_ring(d, entries + turn.stage * entry, col[j]);
+                if constexpr (N == 1) d0[j].zero();
+                if (N > 1 && m == 0)
 #pragma unroll
-                for (int i = 0; i < VW; ++i) dy[j][i] = m ? dy[j][i] + d.get(i) : d.get(i);
+                    for (int i = 0; i < VW / 2; ++i) dys[j][i] = both(0.0f);
+                if (col[j] >= cols) continue;
+                if constexpr (N == 1) {
+                    from_ring(d0[j], entries + turn.stage * entry, col[j]);
+                } else {
+                    Raw<GT, VW> d;
+                    from_ring(d, entries + turn.stage * entry, col[j]);
+#pragma unroll
+                    for (int i = 0; i < VW / 2; ++i) dys[j][i] = m ? dys[j][i] + d.get2(i) : d.get2(i);
+                }
             }
             ring_free(ring, turn, stages);
         }
+        auto dy = [&](int j, int i) { return N == 1 ? d0[j].get2(i) : dys[j][i]; };
         Raw<T, VW> x[NV];
         ring_wait(ring, turn, k.status);
 #pragma unroll
@@ -794,42 +868,43 @@ __global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
             if (col[j] < cols) from_ring(x[j], entries + turn.stage * entry, col[j]);
         }
         ring_free(ring, turn, stages);
-        const float mu = mean, rs = rstd;
+        const float rs = rstd, shift = -mean * rstd;  // xh = x rstd + shift
         if (t + gridDim.x < k.rows) read_stats(t + gridDim.x);
-        float2 sum = make_float2(0.0f, 0.0f);  // of w and of w xh
+        const F2 rs2 = both(rs), shift2 = both(shift);
+        F2 sw = both(0.0f), swx = both(0.0f);  // of w and of w xh
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (col[j] < cols)
 #pragma unroll
-                for (int i = 0; i < VW; ++i) {
-                    const float xh = (x[j].get(i) - mu) * rs, w = dy[j][i] * ga[j][i];
-                    sum.x += w;
-                    sum.y += w * xh;
-                    dg[j][i] += dy[j][i] * xh;
-                    db[j][i] += dy[j][i];
+                for (int i = 0; i < VW / 2; ++i) {
+                    const F2 d = dy(j, i), xh = fma(x[j].get2(i), rs2, shift2), w = d * ga[j][i];
+                    sw = sw + w;
+                    swx = fma(w, xh, swx);
+                    dg[j][i] = fma(d, xh, dg[j][i]);
+                    db[j][i] = db[j][i] + d;
                 }
-        sum = stream_sum(sum, scratch, sum_turn, work);
-        const float c1 = sum.x * inv_n, c2 = sum.y * inv_n;
+        const float2 pw = split(sw), px = split(swx);
+        const float2 sum = stream_sum(make_float2(pw.x + pw.y, px.x + px.y), scratch, sum_turn, work);
+        const F2 k1 = both(-rs * (sum.x * inv_n)), k2 = both(-rs * (sum.y * inv_n));
         if (has_res) ring_wait(ring, turn, k.status);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (col[j] >= cols) continue;
-            float o[VW];
+            F2 o[VW / 2];
 #pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                const float xh = (x[j].get(i) - mu) * rs;
-                o[i] = rs * (dy[j][i] * ga[j][i] - c1 - xh * c2);
-            }
+            for (int i = 0; i < VW / 2; ++i)
+                o[i] = fma(fma(x[j].get2(i), rs2, shift2), k2, fma(dy(j, i) * ga[j][i], rs2, k1));
             if constexpr (N == 1) {
                 if (has_res) {
                     Raw<T, VW> r;
                     from_ring(r, entries + turn.stage * entry, col[j]);
 #pragma unroll
-                    for (int i = 0; i < VW; ++i) o[i] += r.get(i);
+                    for (int i = 0; i < VW / 2; ++i) o[i] = o[i] + r.get2(i);
                 }
             }
             Raw<T, VW> y;
-            y.set(o);
+#pragma unroll
+            for (int i = 0; i < VW / 2; ++i) y.set2(i, o[i]);
             if (in_bounds(k.status, rr * cols + col[j], VW, k.brows * cols)) y.store((T *)k.dst[s] + rr * cols + col[j]);
         }
         if (has_res) ring_free(ring, turn, stages);
@@ -839,12 +914,12 @@ __global__ void __launch_bounds__(BIG ? kMaxThreads + 32 : 288, BIG ? 1 : 2)
     for (int j = 0; j < NV; ++j) {
         if (col[j] >= cols) continue;
 #pragma unroll
-        for (int i = 0; i < VW; i += 4) {
-            *reinterpret_cast<float4 *>(part + col[j] + i) = make_float4(dg[j][i], dg[j][i + 1], dg[j][i + 2], dg[j][i + 3]);
-            *reinterpret_cast<float4 *>(part + cols + col[j] + i) =
-                make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
+        for (int i = 0; i < VW / 2; ++i) {
+            *reinterpret_cast<float2 *>(part + col[j] + 2 * i) = split(dg[j][i]);
+            *reinterpret_cast<float2 *>(part + cols + col[j] + 2 * i) = split(db[j][i]);
         }
     }
+    ring_end(ring, 0, 0, stages, k.status);
 }
 
 // Rows of any width: the row is read twice, and each thread adds its columns
@@ -979,7 +1054,7 @@ cudaError_t launch_stream(void (*kern)(K, int), const K &k, const StreamShape &h
         if (e != cudaSuccess) return e;
         done->set(dev, 1);
     }
-    return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)h.threads + 32), h.smem, s, k, h.stages);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)h.threads + 32 * kCopiers), h.smem, s, k, h.stages);
 }
 
 // Rows enough for the ring kernels: every CTA has three rows or more to keep
