@@ -716,7 +716,7 @@ struct ExpandShape {
 };
 
 template <int MT, int KT, bool VEC, typename TO>
-__global__ void __launch_bounds__(kThreads, MT > 1 && KT <= 2 && sizeof(TO) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT == 1 && KT == 1 ? 3 : 2)
     expand_mma_kernel(const __grid_constant__ ExpandK k) {
     pdl_enter();
     using Shape = ExpandShape<MT, KT, TO>;
@@ -979,7 +979,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 // Rows of an adapter.  A CTA marks them in a bit mask over a window of
 // kWindow rows (one read of the row adapters), then turns the marks into
 // lists of up to kList rows, ascending.
-constexpr int kWindow = 65536, kList = 1024;
+constexpr int kWindow = 32768, kList = 512;
 
 // Marks the window's rows with adapter a; returns how many.
 __device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t rows, int a, uint32_t *marks,
@@ -1064,6 +1064,7 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
     using Shape = OuterShape<RP>;
     constexpr int S = Shape::kStages, PAIRS = Shape::kPairs;
     __shared__ int list[kList], scratch[kWarps], abort_flag;
+    __shared__ const bf16 *row_at[kList];  // the listed rows' first columns of this tile's block
     __shared__ uint32_t marks[kWindow / 32], tmem_at;
     __shared__ __align__(8) uint64_t bars[S];  // a stage's products are done
     extern __shared__ uint8_t raw_smem[];
@@ -1106,6 +1107,14 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
         for (int l0 = lo; l0 < hi; l0 += kList) {
             const int have = hi - l0 < kList ? hi - l0 : kList, ngroups = (have + 63) / 64;
             list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
+            for (int i = threadIdx.x; i < have; i += kThreads) {
+                const uint32_t t = list[i], b = t / (uint32_t)J.x.brows;
+                const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
+                row_at[i] = in_bounds(k.status, off, bcols, J.x.brows * J.x.bcols)
+                                ? (const bf16 *)J.x.at[b * J.x.b1 + blk] + off
+                                : (const bf16 *)nullptr;
+            }
+            __syncthreads();
             float2 sv[PAIRS];
             auto read_s = [&](int grp) {
 #pragma unroll
@@ -1124,18 +1133,11 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int at = grp * 64 + i * 8 + warp;
-                    const void *from = Sv;
-                    bool has = at < have && cx < bcols;
-                    if (has) {
-                        const uint32_t t = list[at], b = t / (uint32_t)J.x.brows;
-                        const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
-                        has = in_bounds(k.status, off + cx, 1, J.x.brows * J.x.bcols);
-                        if (has) from = (const bf16 *)J.x.at[b * J.x.b1 + blk] + off + (VEC ? cx : 0);
-                    }
+                    const bf16 *row = at < have && cx < bcols ? row_at[at] : (const bf16 *)nullptr;
                     if constexpr (VEC) {
-                        queue16(x_to + at0 + i * 1024, from, has);
+                        queue16(x_to + at0 + i * 1024, row ? (const void *)(row + cx) : Sv, row != nullptr);
                     } else {
-                        const Raw8 v = has ? load8<false>((const bf16 *)from, cx, bcols) : Raw8{{0, 0, 0, 0}};
+                        const Raw8 v = row ? load8<false>(row, cx, bcols) : Raw8{{0, 0, 0, 0}};
                         *reinterpret_cast<uint4 *>(smem + (x_to - smem_at) + at0 + i * 1024) =
                             make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
                     }
@@ -1338,12 +1340,19 @@ int64_t slots_for(size_t smem) {
 // over z CTAs (at most `most`, as many as it has rows or the call adapters),
 // then its columns over a cluster of c (at most `split`).  One wave of equal
 // CTAs ends together; two leave the second part empty.
-void spread(int64_t tiles, int64_t slots, int64_t most, int64_t split, int *c, int *z) {
+// `few`: a batch of single tokens, most rows with an adapter of their own, so
+// the adapters come first; in longer ones a tile has one or two.
+void spread(int64_t tiles, int64_t slots, int64_t most, int64_t split, bool few, int *c, int *z) {
     *c = *z = 1;
-    while (*c < 8 && tiles * *c * 2 <= slots && *c * 2 <= split) *c *= 2;
-    const int64_t left = slots / (tiles * *c);
-    *z = (int)(left < 1 ? 1 : left < most ? left : most);
+    auto adapters = [&] {
+        const int64_t left = slots / (tiles * *c);
+        *z = (int)(left < 1 ? 1 : left < most ? left : most);
+    };
+    if (few) adapters();
+    while (*c < 8 && tiles * *z * *c * 2 <= slots && *c * 2 <= split) *c *= 2;
+    if (!few) adapters();
 }
+constexpr int64_t kFewRows = 256;
 
 template <int MT, int NT, bool VEC>
 cudaError_t project_mma(const ProjK &k, cudaStream_t s) {
@@ -1355,7 +1364,8 @@ cudaError_t project_mma(const ProjK &k, cudaStream_t s) {
     const int64_t tiles = (k.rows + 16 * MT - 1) / (16 * MT);
     int c, z;
     // two chunks of 32 columns per warp at least
-    spread(tiles, slots_for(Shape::kSmem), k.n < 16 * MT ? k.n : 16 * MT, k.cols / (64 * kWarps), &c, &z);
+    spread(tiles, slots_for(Shape::kSmem), k.n < 16 * MT ? k.n : 16 * MT, k.cols / (64 * kWarps),
+           k.rows < kFewRows, &c, &z);
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, c, z), dim3(1, c, 1), dim3(kThreads), Shape::kSmem, s, k);
 }
 
@@ -1419,7 +1429,7 @@ cudaError_t project_tc(const ProjK &k, int b0, cudaStream_t s) {
     t.status = k.status;
     const int64_t tiles = (int64_t)t.row_tiles * b0;
     int c, z;
-    spread(tiles, slots_for(kTcSmem), 1, t.chunks / 4, &c, &z);
+    spread(tiles, slots_for(kTcSmem), 1, t.chunks / 4, false, &c, &z);
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, c), dim3(1, c, 1), dim3(kTcThreads), kTcSmem, s, t);
 }
 
@@ -1441,7 +1451,7 @@ template <typename TX, typename TW>
 cudaError_t project_simt(const ProjK &k, cudaStream_t s) {
     const int64_t tiles = (k.rows + 31) / 32;
     int cluster, z;
-    spread(tiles, 4 * sms(), k.n < 32 ? k.n : 32, k.cols / 64, &cluster, &z);
+    spread(tiles, 4 * sms(), k.n < 32 ? k.n : 32, k.cols / 64, k.rows < kFewRows, &cluster, &z);
     const dim3 g((unsigned)tiles, cluster, z), c(1, cluster, 1);
     if (k.R <= 16) return launch_pdl_cluster(project_simt_kernel<TX, TW, 1>, g, c, dim3(kThreads), 0, s, k);
     if (k.R <= 32) return launch_pdl_cluster(project_simt_kernel<TX, TW, 2>, g, c, dim3(kThreads), 0, s, k);
@@ -1466,7 +1476,7 @@ cudaError_t expand_mma(ExpandK k, int nranks, cudaStream_t s) {
     k.row_tiles = (int)((k.brows + 16 * MT - 1) / (16 * MT));
     const int64_t cols = (k.bcols + 511) / 512, tiles = (int64_t)k.row_tiles * nranks * cols;
     int c, z;
-    spread(tiles, 3 * sms(), k.n < 16 * MT ? k.n : 16 * MT, 1, &c, &z);
+    spread(tiles, (MT == 1 && KT == 1 ? 3 : 2) * sms(), k.n < 16 * MT ? k.n : 16 * MT, 1, true, &c, &z);
     return launch_pdl(kern, dim3((unsigned)(k.row_tiles * nranks), (unsigned)cols, z), dim3(kThreads), Shape::kSmem, s,
                       k);
 }
@@ -1489,7 +1499,7 @@ cudaError_t expand_type(ExpandK k, int nranks, shmm_dtype_t wt, cudaStream_t s) 
     k.row_tiles = (int)((k.brows + 15) / 16);
     const int64_t tiles = (int64_t)k.row_tiles * nranks * ((k.bcols + 255) / 256);
     int c, z;
-    spread(tiles, 2 * sms(), k.n < 16 ? k.n : 16, 1, &c, &z);
+    spread(tiles, 2 * sms(), k.n < 16 ? k.n : 16, 1, true, &c, &z);
     return launch_pdl(expand_simt_kernel<float, TO>,
                       dim3((unsigned)(k.row_tiles * nranks), (unsigned)((k.bcols + 255) / 256), z), dim3(kThreads),
                       0, s, k);
@@ -1508,10 +1518,10 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = k.job[0].tiles + k.job[1].tiles;
-    // Adapters differ in rows, so CTAs in time: shares of an adapter's rows
-    // until there are several waves of CTAs or only four groups of rows each.
+    // Shares of an adapter's rows until the card is full (two CTAs per SM) or
+    // a share is down to four groups of rows.
     int cs = 1;
-    while (cs < 8 && tiles * k.n * cs < 4 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
+    while (cs < 8 && tiles * k.n * cs < 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
                               Shape::kSmem, s, k);
 }

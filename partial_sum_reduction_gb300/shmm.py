@@ -266,9 +266,15 @@ def _ptr_array(tensors: Sequence, what: str) -> ctypes.Array:
     return arr
 
 
+# The current stream's handle without a Stream object around it (3 us less per
+# call where this torch has it).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -278,7 +284,7 @@ def _stream_handle(stream) -> Optional[int]:
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
-def _refuse(t, what: str, shape, dtype) -> None:
+def _refuse(t, what: str, shape, dtype):
     """Raises ValueError with what is wrong with tensor t (see _tensor)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
@@ -291,23 +297,53 @@ def _refuse(t, what: str, shape, dtype) -> None:
     raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
 
 
-def _tensor(t, what: str, shape, dtype) -> int:
-    """Address of a dense CUDA tensor of the current device with the given
-    shape and dtype; anything else is refused before the library sees it."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous() and t.get_device() == torch.cuda.current_device()):
-        _refuse(t, what, shape, dtype)
-    return t.data_ptr()
+def _device() -> int:
+    """The current device; without a GPU, a number that no tensor is on (a CPU
+    tensor is on -1)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
 
 
-def _tensors(ts, what: str, shapes, dtype) -> ctypes.Array:
+def _tensor(t, what: str, shape, dtype, dev: int) -> int:
+    """Address of a dense CUDA tensor of device `dev` (the current one) with
+    the given shape and dtype; anything else is refused before the library
+    sees it."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, what, shape, dtype)
+
+
+def _tensors(ts, what: str, shapes, dtype, dev: int) -> ctypes.Array:
     """Per-rank pointer array of dense tensors (see _tensor), one per shape."""
-    if len(ts) != len(shapes):
-        raise ValueError("%s: %d tensors, the plan has %d ranks" % (what, len(ts), len(shapes)))
-    arr = (ctypes.c_void_p * len(ts))()
-    for r, t in enumerate(ts):
-        arr[r] = _tensor(t, "%s[%d]" % (what, r), shapes[r], dtype)
-    return arr
+    n = len(shapes)
+    if len(ts) != n:
+        raise ValueError("%s: %d tensors, the plan has %d ranks" % (what, len(ts), n))
+    ptrs = []
+    for t, shape in zip(ts, shapes):
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+                ptrs.append(t.data_ptr())
+                continue
+        except AttributeError:
+            pass
+        _refuse(t, "%s[%d]" % (what, len(ptrs)), shape, dtype)
+    return _pointers(n)(*ptrs)
+
+
+_pointer_types = {}
+
+
+def _pointers(n: int):
+    """The ctypes type of an array of n pointers."""
+    t = _pointer_types.get(n)
+    if t is None:
+        t = _pointer_types[n] = ctypes.c_void_p * n
+    return t
 
 
 def _rows_dtype(x, what: str = "x"):
@@ -321,14 +357,13 @@ def _rows_dtype(x, what: str = "x"):
     raise ValueError("%s is %s, expected torch.float32 or torch.bfloat16" % (what, x.dtype))
 
 
-def _workspace(ws):
+def _workspace(ws, dev: int):
     """(address, bytes) of a workspace tensor, or of none."""
     if ws is None:
         return None, 0
-    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous() \
-            or ws.get_device() != torch.cuda.current_device():
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a dense CUDA tensor of the current device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 class Plan:
@@ -429,18 +464,26 @@ class Plan:
             got = self._box_shapes[tensor] = [self.rank_box(tensor, r)[1] for r in range(self.nranks)]
         return got
 
+    def _gathered(self):
+        """(owner blocks' shapes, their row counts as shapes, (columns,))."""
+        got = self._box_shapes.get("rows")
+        if got is None:
+            block = self._shapes(TENSOR_C_REDUCED)
+            got = self._box_shapes["rows"] = (block, [(e[0],) for e in block], (block[0][1],))
+        return got
+
     def layernorm_all_gather_forward(self, shard_r, gamma, beta, full_r, mean_r, rstd_r, eps: float = 1e-5,
                                      stream=None):
         """layernorm_all_gather that also leaves each owner block's row
         statistics in mean_r, rstd_r (one fp32 [block rows] tensor per rank),
         for layernorm_all_gather_backward."""
-        dt, f32 = TORCH_DTYPES[self.out_dtype], torch.float32
-        block = self._shapes(TENSOR_C_REDUCED)
-        rows, cols = [(e[0],) for e in block], (block[0][1],)
+        dt, f32, dev = TORCH_DTYPES[self.out_dtype], torch.float32, _device()
+        block, rows, cols = self._gathered()
         _check(lib().shmm_layernorm_all_gather_forward(
-            self._h, _tensors(shard_r, "shard", block, dt), _tensor(gamma, "gamma", cols, f32),
-            _tensor(beta, "beta", cols, f32), eps, _tensors(full_r, "full", self._shapes(TENSOR_C), dt),
-            _tensors(mean_r, "mean", rows, f32), _tensors(rstd_r, "rstd", rows, f32), _stream_handle(stream)))
+            self._h, _tensors(shard_r, "shard", block, dt, dev), _tensor(gamma, "gamma", cols, f32, dev),
+            _tensor(beta, "beta", cols, f32, dev), eps, _tensors(full_r, "full", self._shapes(TENSOR_C), dt, dev),
+            _tensors(mean_r, "mean", rows, f32, dev), _tensors(rstd_r, "rstd", rows, f32, dev),
+            _stream_handle(stream)))
 
     def layernorm_all_gather_backward(self, dfull_r, shard_r, mean_r, rstd_r, gamma, dshard_r, dgamma, dbeta,
                                       workspace, stream=None):
@@ -449,59 +492,60 @@ class Plan:
         the rows' owners and taken through the normalisation in one pass
         (see include/shmm.h).  workspace: helpers.layernorm_workspace of the
         rows of every rank's block."""
-        dt, f32 = TORCH_DTYPES[self.out_dtype], torch.float32
-        block = self._shapes(TENSOR_C_REDUCED)
-        rows, cols = [(e[0],) for e in block], (block[0][1],)
+        dt, f32, dev = TORCH_DTYPES[self.out_dtype], torch.float32, _device()
+        block, rows, cols = self._gathered()
         gdt = f32 if len(dfull_r) and getattr(dfull_r[0], "dtype", None) is f32 else dt
-        ws, ws_bytes = _workspace(workspace)
+        ws, ws_bytes = _workspace(workspace, dev)
         _check(lib().shmm_layernorm_all_gather_backward(
-            self._h, F32 if gdt is f32 else BF16, _tensors(dfull_r, "dfull", self._shapes(TENSOR_C), gdt),
-            _tensors(shard_r, "shard", block, dt), _tensors(mean_r, "mean", rows, f32),
-            _tensors(rstd_r, "rstd", rows, f32), _tensor(gamma, "gamma", cols, f32),
-            _tensors(dshard_r, "dshard", block, dt), _tensor(dgamma, "dgamma", cols, f32),
-            _tensor(dbeta, "dbeta", cols, f32), ws, ws_bytes, _stream_handle(stream)))
+            self._h, F32 if gdt is f32 else BF16, _tensors(dfull_r, "dfull", self._shapes(TENSOR_C), gdt, dev),
+            _tensors(shard_r, "shard", block, dt, dev), _tensors(mean_r, "mean", rows, f32, dev),
+            _tensors(rstd_r, "rstd", rows, f32, dev), _tensor(gamma, "gamma", cols, f32, dev),
+            _tensors(dshard_r, "dshard", block, dt, dev), _tensor(dgamma, "dgamma", cols, f32, dev),
+            _tensor(dbeta, "dbeta", cols, f32, dev), ws, ws_bytes, _stream_handle(stream)))
 
     def adapters_workspace_size(self, n_adapters: int, rank: int) -> int:
         n = ctypes.c_size_t()
         _check(lib().shmm_adapters_workspace_size(self._h, int(n_adapters), int(rank), ctypes.byref(n)))
         return n.value
 
-    def _adapters(self, row_adapter, down, up, scale):
+    def _adapters(self, row_adapter, down, up, scale, dev):
         """(n, rank, addresses) of the adapters' factors, checked."""
         dt, (I, J, K) = TORCH_DTYPES[self.in_dtype], self.shape
         if not isinstance(down, torch.Tensor) or down.dim() != 3:
             raise ValueError("down must be a CUDA tensor [adapters, rank, J]")
-        n, rank = down.shape[0], down.shape[1]
-        return n, rank, (_tensor(row_adapter, "row_adapter", (I,), torch.int32), _tensor(down, "down", (n, rank, J), dt),
-                         _tensor(up, "up", (n, rank, K), dt),
-                         None if scale is None else _tensor(scale, "scale", (n,), torch.float32))
+        n, rank, _ = down.shape
+        return n, rank, (_tensor(row_adapter, "row_adapter", (I,), torch.int32, dev),
+                         _tensor(down, "down", (n, rank, J), dt, dev), _tensor(up, "up", (n, rank, K), dt, dev),
+                         None if scale is None else _tensor(scale, "scale", (n,), torch.float32, dev))
 
     def adapters_forward(self, A_r, row_adapter, down, up, scale, base_r, C_r, low, stream=None):
         """Low-rank adapters beside the plan's product: C = base + scale[a]
         (A . down[a]^T) . up[a] for the rows of adapter a (see
         include/shmm.h).  down [n, rank, J], up [n, rank, K]; scale [n] or
         None; base_r: per-rank tensors (C_r itself included) or None."""
-        n, rank, ptrs = self._adapters(row_adapter, down, up, scale)
+        dev = _device()
+        n, rank, ptrs = self._adapters(row_adapter, down, up, scale, dev)
         dt, box = TORCH_DTYPES[self.out_dtype], self._shapes(TENSOR_C)
         _check(lib().shmm_adapters_forward(
-            self._h, n, rank, _tensors(A_r, "A", self._shapes(TENSOR_A), TORCH_DTYPES[self.in_dtype]), *ptrs,
-            None if base_r is None else _tensors(base_r, "base", box, dt), _tensors(C_r, "C", box, dt),
-            _tensor(low, "low", (self.shape[0], rank), torch.float32), _stream_handle(stream)))
+            self._h, n, rank, _tensors(A_r, "A", self._shapes(TENSOR_A), TORCH_DTYPES[self.in_dtype], dev), *ptrs,
+            None if base_r is None else _tensors(base_r, "base", box, dt, dev), _tensors(C_r, "C", box, dt, dev),
+            _tensor(low, "low", (self.shape[0], rank), torch.float32, dev), _stream_handle(stream)))
 
     def adapters_backward(self, dC_r, A_r, row_adapter, down, up, scale, low, base_r, dA_r, ddown, dup, workspace,
                           stream=None):
         """Gradient of adapters_forward: dA (+ base), and every adapter's
         ddown, dup in fp32 (see include/shmm.h).  workspace:
         helpers.adapters_workspace."""
-        n, rank, ptrs = self._adapters(row_adapter, down, up, scale)
+        dev = _device()
+        n, rank, ptrs = self._adapters(row_adapter, down, up, scale, dev)
         dt, box, f32 = TORCH_DTYPES[self.in_dtype], self._shapes(TENSOR_A), torch.float32
         I, J, K = self.shape
-        ws, ws_bytes = _workspace(workspace)
+        ws, ws_bytes = _workspace(workspace, dev)
         _check(lib().shmm_adapters_backward(
-            self._h, n, rank, _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype]),
-            _tensors(A_r, "A", box, dt), *ptrs, _tensor(low, "low", (I, rank), f32),
-            None if base_r is None else _tensors(base_r, "base", box, dt), _tensors(dA_r, "dA", box, dt),
-            _tensor(ddown, "ddown", (n, rank, J), f32), _tensor(dup, "dup", (n, rank, K), f32), ws, ws_bytes,
+            self._h, n, rank, _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev),
+            _tensors(A_r, "A", box, dt, dev), *ptrs, _tensor(low, "low", (I, rank), f32, dev),
+            None if base_r is None else _tensors(base_r, "base", box, dt, dev), _tensors(dA_r, "dA", box, dt, dev),
+            _tensor(ddown, "ddown", (n, rank, J), f32, dev), _tensor(dup, "dup", (n, rank, K), f32, dev), ws, ws_bytes,
             _stream_handle(stream)))
 
     def run_host(self, A_host, B_host, C_host, A_r, B_r, C_r, workspace=None, stream=None):
@@ -620,13 +664,13 @@ def shmm_layernorm_forward(x, gamma, beta, y, mean, rstd, residual=None, total=N
     total) into y, with the rows' statistics for shmm_layernorm_backward
     (see include/shmm.h)."""
     rows, cols, dt, code = _rows_dtype(x)
-    f32, shape = torch.float32, (rows, cols)
+    f32, shape, dev = torch.float32, (rows, cols), _device()
     _check(lib().shmm_layernorm_forward(
-        rows, cols, code, _tensor(x, "x", shape, dt),
-        None if residual is None else _tensor(residual, "residual", shape, dt), _tensor(gamma, "gamma", (cols,), f32),
-        _tensor(beta, "beta", (cols,), f32), eps, None if total is None else _tensor(total, "total", shape, dt),
-        _tensor(y, "y", shape, dt), _tensor(mean, "mean", (rows,), f32), _tensor(rstd, "rstd", (rows,), f32),
-        _stream_handle(stream)))
+        rows, cols, code, _tensor(x, "x", shape, dt, dev),
+        None if residual is None else _tensor(residual, "residual", shape, dt, dev),
+        _tensor(gamma, "gamma", (cols,), f32, dev), _tensor(beta, "beta", (cols,), f32, dev), eps,
+        None if total is None else _tensor(total, "total", shape, dt, dev), _tensor(y, "y", shape, dt, dev),
+        _tensor(mean, "mean", (rows,), f32, dev), _tensor(rstd, "rstd", (rows,), f32, dev), _stream_handle(stream)))
 
 
 def shmm_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -639,14 +683,15 @@ def shmm_layernorm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, workspa
     """Gradient of shmm_layernorm_forward: dx (+ residual_grad), dgamma,
     dbeta (see include/shmm.h).  workspace: helpers.layernorm_workspace."""
     rows, cols, dt, code = _rows_dtype(x)
-    f32, shape = torch.float32, (rows, cols)
-    ws, ws_bytes = _workspace(workspace)
+    f32, shape, dev = torch.float32, (rows, cols), _device()
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(lib().shmm_layernorm_backward(
-        rows, cols, code, _tensor(dy, "dy", shape, dt), _tensor(x, "x", shape, dt),
-        _tensor(mean, "mean", (rows,), f32), _tensor(rstd, "rstd", (rows,), f32), _tensor(gamma, "gamma", (cols,), f32),
-        None if residual_grad is None else _tensor(residual_grad, "residual_grad", shape, dt),
-        _tensor(dx, "dx", shape, dt), _tensor(dgamma, "dgamma", (cols,), f32), _tensor(dbeta, "dbeta", (cols,), f32),
-        ws, ws_bytes, _stream_handle(stream)))
+        rows, cols, code, _tensor(dy, "dy", shape, dt, dev), _tensor(x, "x", shape, dt, dev),
+        _tensor(mean, "mean", (rows,), f32, dev), _tensor(rstd, "rstd", (rows,), f32, dev),
+        _tensor(gamma, "gamma", (cols,), f32, dev),
+        None if residual_grad is None else _tensor(residual_grad, "residual_grad", shape, dt, dev),
+        _tensor(dx, "dx", shape, dt, dev), _tensor(dgamma, "dgamma", (cols,), f32, dev),
+        _tensor(dbeta, "dbeta", (cols,), f32, dev), ws, ws_bytes, _stream_handle(stream)))
 
 
 def shmm_reshard(mesh, spec_from, spec_to, rows: int, cols: int, dtype: str, src_r, dst_r, stream=None):
