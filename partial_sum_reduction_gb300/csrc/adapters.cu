@@ -413,15 +413,18 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
 // shared memory in order.  Beside the warp instructions above it: the factor
 // is read once per 128 rows instead of per 32, and no thread spends
 // instructions on addresses, which bounded them.
-constexpr int kTcThreads = 192, kTcStages = 5, kTcSum = 129;
-constexpr uint32_t kTcRing = 98304;  // two CTAs per SM
+constexpr int kTcThreads = 192, kTcStages = 5;
+constexpr int kTcSum = 132;  // fp32 of a row of sums: whole 16-byte vectors
+constexpr uint32_t kTcRing = 109568;  // two CTAs per SM
 constexpr size_t kTcSmem = kTcRing + 1024;
+static_assert(128 * kTcSum * 4 <= kTcRing, "the sums take the ring's memory");
 
 template <int RP>
 __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_constant__ ProjTcK k) {
     pdl_wait();
     constexpr int ROWS = 128, PER = 128 / RP, S = kTcStages;
     __shared__ int ids[ROWS], list[ROWS], count, abort_flag;
+    __shared__ float scales[PER];
     __shared__ __align__(8) uint64_t bars[2 * S + 1];
     __shared__ uint32_t tmem_at;
     extern __shared__ uint8_t raw_smem[];
@@ -452,8 +455,11 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     if (cr == 0)  // rows without an adapter: zeros
         for (int i = threadIdx.x; i < ROWS * k.R; i += kTcThreads)
             if (ids[i / k.R] < 0 && t0 + i / k.R < t1) k.out[t0 * k.R + i] = 0.0f;
-    // As many stages as fit with the factors a pass may bring.
-    const uint32_t stage_bytes = 16384 + (nd < PER ? nd : PER) * RP * 128;
+    // As many stages as fit with the factors a pass may bring, the same number
+    // for one adapter and two: a CTA's share of the memory's bandwidth is what
+    // it has in flight, and the one with the fewest stages ends last.
+    const int most = nd < 2 ? 2 : nd < PER ? nd : PER;
+    const uint32_t stage_bytes = 16384 + most * RP * 128;
     const uint32_t stages = kTcRing / stage_bytes < S ? kTcRing / stage_bytes : S;
     const int lo = (int)((int64_t)k.chunks * cr / cs), hi = (int)((int64_t)k.chunks * (cr + 1) / cs);
     // Producer and issuer are one thread each, so their own instructions are
@@ -464,6 +470,7 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     bool ok = true;
     for (int p0 = 0, pass = 0; p0 < nd; p0 += PER, ++pass) {
         const int na = nd - p0 < PER ? nd - p0 : PER;
+        if (warp == 2 && lane < na) scales[lane] = k.scale ? k.scale[list[p0 + lane]] : 1.0f;
         if (warp == 0 && lane == 0) {
             const CUtensorMap *x = &k.x[brow * k.b1 + blk0];
             int c = (lo - blk0 * k.per_block) * 64, wc = (int)(blk0 * k.bcols) + c;
@@ -492,19 +499,19 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
                 }
             }
         } else if (warp == 1 && lane == 0) {
+            // The pass's factors lie below one another: one operand of na RP
+            // rows.  An instruction takes some 130 cycles however narrow it
+            // is, so one for all of them, not one each.
             const uint64_t base = shmm_tc::operand(tiles_at, 16, 1024);
+            const uint32_t idesc = shmm_tc::instruction(na * RP, false);
             for (int ch = lo; ch < hi; ++ch) {
                 ok = ok && shmm_dev::mbar_wait(full(stage), phase, &abort_flag, k.status);
                 if (!ok) break;
                 shmm_tc::fence_after();
                 const uint64_t xa = base + ((stage * stage_bytes) >> 4);  // addresses in units of 16 bytes
-                for (int i = 0; i < na; ++i) {
-                    const uint64_t wa = xa + 1024 + i * (RP * 8);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        shmm_tc::mma_issue(tmem + i * RP, xa + kk * 2, wa + kk * 2, shmm_tc::instruction(RP, false),
-                                           ch > lo || kk > 0);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    shmm_tc::mma_issue(tmem, xa + kk * 2, xa + 1024 + kk * 2, idesc, ch > lo || kk > 0);
                 shmm_tc::mma_commit(empty(stage));
                 if (++stage == stages) {
                     stage = 0;
@@ -518,12 +525,11 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
         if (warp >= 2) {
             // Not cut short by an abort: the products in flight read shared memory.
             shmm_dev::mbar_wait(done, pass & 1, &abort_flag, k.status, false);
-            __syncwarp();
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps; scales are written
             shmm_tc::fence_after();
             const int quad = warp & 3, row = quad * 32 + lane;
             for (int i = 0; i < na; ++i) {
                 const int a = list[p0 + i];
-                const float scale = k.scale ? k.scale[a] : 1.0f;
 #pragma unroll
                 for (int c = 0; c < RP; c += 16) {
                     float v[16];
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
                     } else if (ids[row] == a && in_bounds(k.status, (t0 + row) * k.R, k.R, k.rows * k.R)) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (c + j < k.R) k.out[(t0 + row) * k.R + c + j] = k.scale ? v[j] * scale : v[j];
+                            if (c + j < k.R) k.out[(t0 + row) * k.R + c + j] = k.scale ? v[j] * scales[i] : v[j];
                     }
                 }
             }
@@ -543,12 +549,27 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
         if (cs > 1) {
             cluster.sync();
             const int r0 = ROWS * cr / cs, r1 = ROWS * (cr + 1) / cs;
-            for (int e = threadIdx.x; e < (r1 - r0) * na * RP; e += kTcThreads) {
-                const int row = r0 + e / (na * RP), i = e % (na * RP) / RP, r = e % RP;
+            const int vecs = na * RP / 4;
+            for (int e = threadIdx.x; e < (r1 - r0) * vecs; e += kTcThreads) {
+                const int row = r0 + e / vecs, c = e % vecs * 4, i = c / RP, r = c % RP;
                 if (r >= k.R || ids[row] != list[p0 + i]) continue;
-                const float v = sum_cluster(cluster, sums + row * kTcSum + i * RP + r, cs);
-                if (in_bounds(k.status, (t0 + row) * k.R + r, 1, k.rows * k.R))
-                    k.out[(t0 + row) * k.R + r] = k.scale ? v * k.scale[list[p0 + i]] : v;
+                float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < cs) v[b] = *cluster.map_shared_rank(reinterpret_cast<float4 *>(sums + row * kTcSum + c), b);
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < cs) {
+                        t.x += v[b].x;
+                        t.y += v[b].y;
+                        t.z += v[b].z;
+                        t.w += v[b].w;
+                    }
+                const float *u = &t.x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r + j < k.R && in_bounds(k.status, (t0 + row) * k.R + r + j, 1, k.rows * k.R))
+                        k.out[(t0 + row) * k.R + r + j] = k.scale ? u[j] * scales[i] : u[j];
             }
             shmm_tc::fence_async();
             cluster.sync();  // the sums are read: the stages may be filled again
@@ -977,63 +998,63 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 // ---- outer -----------------------------------------------------------------
 
 // Rows of an adapter.  A CTA marks them in a bit mask over a window of
-// kWindow rows (one read of the row adapters), then turns the marks into
-// lists of up to kList rows, ascending.
+// kWindow rows (one read of the row adapters), with how many lie before each
+// 32-row word, then turns the marks into lists of up to kList rows, ascending.
 constexpr int kWindow = 32768, kList = 512;
+struct Marks {
+    uint32_t bits[kWindow / 32];
+    int before[kWindow / 32];
+    int warp_sum[kWarps];
+};
 
-// Marks the window's rows with adapter a; returns how many.
-__device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t rows, int a, uint32_t *marks,
-                                         int *scratch, int *status) {
+// Marks the window's rows with adapter a; returns how many.  A warp takes
+// consecutive words.
+__device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t rows, int a, Marks &marks, int *status) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
+    const int per = (words + kWarps - 1) / kWarps, first = warp * per, last = first + per < words ? first + per : words;
     int mine = 0;
-    for (int i0 = warp; i0 < words; i0 += 8 * kWarps) {
+    for (int i0 = first; i0 < last; i0 += 8) {
         int v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t t = w0 + (int64_t)(i0 + i * kWarps) * 32 + lane;
-            v[i] = t < rows && in_bounds(status, t, 1, rows) ? ids[t] : -1;
+            const int64_t t = w0 + (int64_t)(i0 + i) * 32 + lane;
+            v[i] = i0 + i < last && t < rows && in_bounds(status, t, 1, rows) ? ids[t] : -1;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t m = __ballot_sync(0xffffffffu, v[i] == a);
-            if (lane == 0 && i0 + i * kWarps < words) marks[i0 + i * kWarps] = m;
+            if (lane == 0 && i0 + i < last) {
+                marks.bits[i0 + i] = m;
+                marks.before[i0 + i] = mine;  // of the warp's words
+            }
             mine += __popc(m);
         }
     }
-    if (lane == 0) scratch[warp] = mine;
+    if (lane == 0) marks.warp_sum[warp] = mine;
     __syncthreads();
-    int total = 0;
+    int total = 0, before = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += scratch[i];
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += marks.warp_sum[i];
+        total += marks.warp_sum[i];
+    }
+    for (int i = first + lane; i < last; i += 32) marks.before[i] += before;
     __syncthreads();
     return total;
 }
 
 // The marked rows number [from, to) of the window, at most kList, into list.
-__device__ __forceinline__ void list_rows(const uint32_t *marks, int64_t w0, int64_t rows, int from, int to, int *list,
-                                          int *scratch) {
+__device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_t rows, int from, int to, int *list) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
-    const int per = (words + kThreads - 1) / kThreads, first = threadIdx.x * per;
-    int mine = 0;
-    for (int i = first; i < first + per && i < words; ++i) mine += __popc(marks[i]);
-    int upto = mine;  // inclusive over the warp
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+    __syncthreads();  // list is free
+#pragma unroll 4
+    for (int i = warp; i < words; i += kWarps) {
+        const uint32_t m = marks.bits[i];
+        const int place = marks.before[i] + __popc(m & ((1u << lane) - 1));
+        if ((m >> lane & 1) && place >= from && place < to) list[place - from] = (int)(w0 + i * 32 + lane);
     }
-    __syncthreads();  // scratch and list are free
-    if (lane == 31) scratch[warp] = upto;
-    __syncthreads();
-    int place = upto - mine;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i)
-        if (i < warp) place += scratch[i];
-    for (int i = first; i < first + per && i < words; ++i)
-        for (uint32_t m = marks[i]; m; m &= m - 1, ++place)
-            if (place >= from && place < to) list[place - from] = (int)(w0 + i * 32 + __ffs(m) - 1);
     __syncthreads();
 }
 
@@ -1053,9 +1074,11 @@ struct OuterShape {
     static constexpr int kBands = RP == 64 ? 2 : 3;
     static constexpr uint32_t kStage = 32768 + kTiles * 16384;
     static constexpr int kStages = 2;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
     static constexpr int kPairs = RP / 8;                    // row pairs of S per thread and group
-    static constexpr int kPitch = 65;                        // fp32 of a 64-column piece of the result
+    static constexpr int kPitch = 132;                       // fp32 of a 128-column piece of the result
+    static constexpr int kRows = kBands * RP;                // rows of it that hold something
+    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * 256 * 4;  // that piece, the whole sum
+    static constexpr size_t kSmem = (kResult > (size_t)kStages * kStage ? kResult : (size_t)kStages * kStage) + 1024;
 };
 
 template <int RP, bool VEC>
@@ -1063,9 +1086,10 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
     pdl_wait();
     using Shape = OuterShape<RP>;
     constexpr int S = Shape::kStages, PAIRS = Shape::kPairs;
-    __shared__ int list[kList], scratch[kWarps], abort_flag;
+    __shared__ int list[kList], abort_flag;
     __shared__ const bf16 *row_at[kList];  // the listed rows' first columns of this tile's block
-    __shared__ uint32_t marks[kWindow / 32], tmem_at;
+    __shared__ Marks marks;
+    __shared__ uint32_t tmem_at;
     __shared__ __align__(8) uint64_t bars[S];  // a stage's products are done
     extern __shared__ uint8_t raw_smem[];
     uint8_t *smem = raw_smem + (1024 - (shmm_dev::smem_u32(raw_smem) & 1023)) % 1024;
@@ -1100,13 +1124,13 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
     uint32_t fills = 0;  // groups taken so far; stage fills % S
     bool ok = true;
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-        const int total = mark_rows(k.ids, w0, k.rows, a, marks, scratch, k.status);
+        const int total = mark_rows(k.ids, w0, k.rows, a, marks, k.status);
         // this CTA's share of the rows, in whole groups of 64
         const int groups = (total + 63) / 64, lo = groups * cr / cs * 64;
         const int hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
         for (int l0 = lo; l0 < hi; l0 += kList) {
             const int have = hi - l0 < kList ? hi - l0 : kList, ngroups = (have + 63) / 64;
-            list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
+            list_rows(marks, w0, k.rows, l0, l0 + have, list);
             for (int i = threadIdx.x; i < have; i += kThreads) {
                 const uint32_t t = list[i], b = t / (uint32_t)J.x.brows;
                 const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
@@ -1190,40 +1214,74 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
         shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[f % S]), (f / S) & 1, &abort_flag, k.status, false);
     __syncthreads();
     shmm_tc::fence_after();
-    // Result: 64 columns at a time from TMEM through shared memory, the parts'
-    // rows added; whole in shared memory when the cluster shares it.
+    // Result: 128 columns at a time from TMEM through shared memory, the
+    // parts' rows added; whole in shared memory when the cluster shares it.
     const float scale = J.scale ? J.scale[a] : 1.0f;
-    auto put = [&](int r, int c, float v) {
-        const int64_t at = ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + c0 + c;
-        if (c0 + c < bcols && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols)) J.out[at] = v * scale;
+    float *out = J.out + (int64_t)a * k.R * J.cols + (int64_t)blk * bcols + c0;
+    const bool whole = (J.cols & 3) == 0 && (bcols & 3) == 0 && (reinterpret_cast<uintptr_t>(J.out) & 15) == 0;
+    auto put = [&](int r, int c, float4 v) {  // four columns from c of row r
+        const int left = bcols - c0 - c;
+        if (left <= 0 || !in_bounds(k.status, ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + c0 + c,
+                                    left < 4 ? left : 4, (int64_t)k.n * k.R * J.cols))
+            return;
+        float *o = out + (int64_t)r * J.cols + c;
+        v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+        if (whole) {
+            *reinterpret_cast<float4 *>(o) = v;
+        } else {
+            o[0] = v.x;
+            if (left > 1) o[1] = v.y;
+            if (left > 2) o[2] = v.z;
+            if (left > 3) o[3] = v.w;
+        }
     };
-    float *piece = reinterpret_cast<float *>(smem);                // [128][kPitch]
-    float *sums = piece + 128 * Shape::kPitch;                     // [RP][256]
-    for (int c = 0; c < 256; c += 64) {
-        const int quad = warp & 3, half = warp >> 2;
+    float *piece = reinterpret_cast<float *>(smem);                // [kRows][kPitch]
+    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][256]
+    auto add = [](float4 &t, const float4 &v) {
+        t.x += v.x;
+        t.y += v.y;
+        t.z += v.z;
+        t.w += v.w;
+    };
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 128) {
+        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+        if (quad * 32 < Shape::kRows) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[16];
-            const int at = half * 32 + h * 16;
-            if (fills) shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + c + at, v);
+            for (int h = 0; h < 4; ++h) {
+                float v[16];
+                const int at = half * 64 + h * 16;
+                if (fills) shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + c + at, v);
+                if (row < Shape::kRows)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) piece[(quad * 32 + lane) * Shape::kPitch + at + j] = fills ? v[j] : 0.0f;
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(piece + row * Shape::kPitch + at + j) =
+                            fills ? make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < k.R * 64; e += kThreads) {
-            const int r = e / 64, j = e % 64;
-            float v = 0.0f;
+        for (int e = threadIdx.x; e < k.R * 32; e += kThreads) {
+            const int r = e / 32, j = e % 32 * 4;
+            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int h = Shape::kBands - 1; h >= 0; --h) v += piece[(h * RP + r) * Shape::kPitch + j];
-            if (cs > 1) sums[r * 256 + c + j] = v;
-            else put(r, c + j, v);
+            for (int h = Shape::kBands - 1; h >= 0; --h)
+                add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
+            if (cs > 1) *reinterpret_cast<float4 *>(sums + r * 256 + c + j) = t;
+            else put(r, c + j, t);
         }
         __syncthreads();
     }
     if (cs > 1) {
         cluster.sync();
-        for (int e = cr * kThreads + threadIdx.x; e < k.R * 256; e += cs * kThreads) {
-            put(e / 256, e % 256, sum_cluster(cluster, sums + e, cs));
+        for (int e = cr * kThreads + threadIdx.x; e < k.R * 64; e += cs * kThreads) {
+            float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                if (b < cs) v[b] = *cluster.map_shared_rank(reinterpret_cast<float4 *>(sums) + e, b);
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                if (b < cs) add(t, v[b]);
+            put(e / 64, e % 64 * 4, t);
         }
         cluster.sync();  // nobody leaves with what another CTA still reads
     }
@@ -1238,8 +1296,8 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
-    __shared__ int list[kList], scratch[kWarps];
-    __shared__ uint32_t marks[kWindow / 32];
+    __shared__ int list[kList];
+    __shared__ Marks marks;
     __shared__ float ss[2][16][16];
     __shared__ float sums[16][128];
     const OuterJob &J = k.job[0];
@@ -1251,10 +1309,10 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-    const int total = mark_rows(k.ids, w0, k.rows, a, marks, scratch, k.status);
+    const int total = mark_rows(k.ids, w0, k.rows, a, marks, k.status);
     for (int l0 = 0; l0 < total; l0 += kList) {
         const int have = total - l0 < kList ? total - l0 : kList;
-        list_rows(marks, w0, k.rows, l0, l0 + have, list, scratch);
+        list_rows(marks, w0, k.rows, l0, l0 + have, list);
         for (int s0 = 0; s0 < have; s0 += 32) {
             const int s = s0 + half * 16;
             float x[16];
@@ -1521,7 +1579,7 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     // Shares of an adapter's rows until the card is full (two CTAs per SM) or
     // a share is down to four groups of rows.
     int cs = 1;
-    while (cs < 8 && tiles * k.n * cs < 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
+    while (cs < 8 && tiles * k.n * cs * 2 <= 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
                               Shape::kSmem, s, k);
 }
