@@ -95,7 +95,7 @@ struct ExpandK {
     const int *ids;
     const float *scale;   // or NULL
     const float *s;       // [rows][R]
-    int n, R, row_tiles;
+    int n, R, row_tiles, mt;  // CTAs per box's rows; 16-row tiles of a CTA
     int64_t rows, cols;
     int *status;
 };
@@ -717,7 +717,8 @@ struct Out8 {
     }
 };
 
-// A CTA takes 16 MT rows of one rank's box x 512 columns (64 per warp).  An
+// A CTA takes k.mt row tiles of 16 of one rank's box x 512 columns (64 per
+// warp; FEW: one row tile, many adapters).  An
 // adapter's 16 KT x 64 piece stays in registers until a row tile needs
 // another's.  The product's columns are dealt out
 // so that each thread ends with two runs of eight consecutive ones, and four
@@ -726,25 +727,31 @@ struct Out8 {
 // threads' queues from the start.
 // blockIdx.x: rank x row tile; blockIdx.z strides over a row tile's adapters
 // (and z = 0 copies the rows without one).
-template <int MT, int KT, typename TO>
+constexpr int kMaxRowTiles = 16;
+template <bool FEW, int KT, typename TO>
 struct ExpandShape {
     static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
     static constexpr int kPitch = 16 * KT + 8;  // bf16: a row's start moves by 4 banks, fragments do not conflict
     static constexpr int kWords = sizeof(TO) / 2;  // 16-byte pieces of eight outputs
-    static constexpr int kRing = MT < 3 ? MT : kWords == 1 ? 3 : 2;
-    static constexpr size_t kQueue = (size_t)kRing * 4 * kWords * kThreads * 16;
-    static constexpr size_t kSmem = kQueue + (size_t)kParts * 16 * MT * kPitch * 2;
+    static constexpr int kRing = FEW ? 1 : kWords == 1 ? 3 : 2;
+    static constexpr size_t kBase = (size_t)kRing * 4 * kWords * kThreads * 16;
+    // FEW: factor pieces of the next kAhead adapters queued too.
+    static constexpr int kAhead = !FEW ? 0 : KT == 1 ? 4 : 2;
+    static constexpr size_t kQueue = kBase + (size_t)kAhead * 4 * KT * kThreads * 16;
+    static size_t smem(int row_tiles) { return kQueue + (size_t)kParts * 16 * row_tiles * kPitch * 2; }
 };
 
-template <int MT, int KT, bool VEC, typename TO>
-__global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT == 1 && KT == 1 ? 3 : 2)
+template <bool FEW, int KT, bool VEC, typename TO>
+__global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     expand_mma_kernel(const __grid_constant__ ExpandK k) {
     pdl_enter();
-    using Shape = ExpandShape<MT, KT, TO>;
-    constexpr int ROWS = 16 * MT, RP = 16 * KT, PITCH = Shape::kPitch, PARTS = Shape::kParts;
+    using Shape = ExpandShape<FEW, KT, TO>;
+    constexpr int RP = 16 * KT, PITCH = Shape::kPitch, PARTS = Shape::kParts;
     constexpr int RING = Shape::kRing, WORDS = Shape::kWords;
-    constexpr bool AHEAD = MT == 1 && KT <= 2;  // one row tile with many adapters: the next one's factor early
-    __shared__ int ids[ROWS];
+    constexpr int AHEAD = FEW && VEC ? Shape::kAhead : 0;
+    const int MT = FEW ? 1 : k.mt, ROWS = 16 * MT;
+    __shared__ int ids[16 * kMaxRowTiles];
+    __shared__ float row_scale[16 * kMaxRowTiles];
     extern __shared__ __align__(16) uint8_t smem[];
     bf16 *ss = reinterpret_cast<bf16 *>(smem + Shape::kQueue);  // [PARTS][ROWS][PITCH]
     const uint4 *queue = reinterpret_cast<const uint4 *>(smem) + threadIdx.x;  // [(slot * 4 + i) * WORDS + w][thread]
@@ -766,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
         *left = left0 - 32 * (i & 1);
         return m * 16 + (i >> 1) * 8 + g < nrows && *left > 0 && in_bounds(k.status, *at, 1, k.brows * k.bcols);
     };
-    auto ask = [&](int m) {
+    auto ask = [&](int m, int slot) {  // row tile m into a slot of the queue
         if (VEC && m < MT) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -775,19 +782,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
                 const bool ok = has(m, i, &at, &left) && base;
 #pragma unroll
                 for (int w = 0; w < WORDS; ++w)
-                    queue16(queue_at + (uint32_t)(((m % RING) * 4 + i) * WORDS + w) * kThreads * 16,
+                    queue16(queue_at + (uint32_t)((slot * 4 + i) * WORDS + w) * kThreads * 16,
                             ok ? (const void *)(base + at + w * 8 / WORDS) : k.w, ok);
             }
         }
         queue_commit();
     };
 #pragma unroll
-    for (int m = 0; m < RING; ++m) ask(m);
-    if (threadIdx.x < ROWS) {
-        int a = -1;
-        if ((int)threadIdx.x < nrows && in_bounds(k.status, t0 + threadIdx.x, 1, k.rows)) a = k.ids[t0 + threadIdx.x];
-        ids[threadIdx.x] = a >= 0 && a < k.n ? a : -1;
-    }
+    for (int m = 0; m < RING; ++m) ask(m, m);
+    int my_id = -1;  // of row threadIdx.x; on its way while the low rows are split
+    if ((int)threadIdx.x < nrows && in_bounds(k.status, t0 + threadIdx.x, 1, k.rows)) my_id = k.ids[t0 + threadIdx.x];
 #pragma unroll 4
     for (int i = threadIdx.x; i < ROWS * RP / 2; i += kThreads) {
         const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
@@ -801,6 +805,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(ss + (h * ROWS + row) * PITCH + r) = p[h];
     }
+    if ((int)threadIdx.x < ROWS) {
+        my_id = my_id >= 0 && my_id < k.n ? my_id : -1;
+        ids[threadIdx.x] = my_id;
+        row_scale[threadIdx.x] = k.scale && my_id >= 0 ? k.scale[my_id] : 1.0f;
+    }
     __syncthreads();
     if (c0 >= k.bcols) {
         queue_wait<0>();
@@ -808,10 +817,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
     }
     const int64_t col = k.col0[rank] * k.bcols;  // of the box in the factor
     int held = -1;                               // the adapter in b
-    float scale = 1.0f;
     uint32_t b[KT][8][2];
     Raw8 raw[KT][4];
-    auto load_w = [&](int a) {
+    const uint4 *w_queue = queue + Shape::kBase / 16;
+    // Adapter a's pieces, into registers or (to >= 0) into place `to` of the
+    // queue.
+    auto load_w = [&](int a, int to = -1) {
         const bf16 *w = (const bf16 *)k.w + (int64_t)a * k.R * k.cols + col;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
@@ -819,39 +830,57 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
             for (int i = 0; i < 4; ++i) {
                 const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
                 const int64_t c = c0 + 32 * (g & 1) + 8 * (g >> 1);  // product column j of lane group g: this one + j
-                raw[kt][i] = Raw8{{0, 0, 0, 0}};
-                if (r < k.R && c < k.bcols &&
-                    in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1, (int64_t)k.n * k.R * k.cols))
-                    raw[kt][i] = load8<VEC>(w + r * k.cols, c, k.bcols);
+                const bool ok = r < k.R && c < k.bcols &&
+                                in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1,
+                                          (int64_t)k.n * k.R * k.cols);
+                if (AHEAD && to >= 0) {
+                    queue16(queue_at + (uint32_t)Shape::kBase + (uint32_t)((to * KT + kt) * 4 + i) * kThreads * 16,
+                            ok ? (const void *)(w + r * k.cols + c) : k.w, ok);
+                } else {
+                    raw[kt][i] = Raw8{{0, 0, 0, 0}};
+                    if (ok) raw[kt][i] = load8<VEC>(w + r * k.cols, c, k.bcols);
+                }
             }
     };
+    int slot = 0;
 #pragma unroll 1
     for (int m = 0; m < MT; ++m) {
         const int id = ids[m * 16 + (lane & 15)];
         const unsigned with = __ballot_sync(0xffffffffu, id >= 0) & 0xffffu;
         // The next of this CTA's adapters of the row tile (-1: none left)
         // and its rows.
-        unsigned todo = with;
-        int d = 0;
-        auto advance = [&](unsigned *rows) {
-            while (todo) {
-                const int a = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
+        struct Left {
+            unsigned todo;
+            int d;
+        };
+        auto advance = [&](Left &left, unsigned *rows) {
+            while (left.todo) {
+                const int a = __shfl_sync(0xffffffffu, id, __ffs(left.todo) - 1);
                 *rows = __ballot_sync(0xffffffffu, id == a) & 0xffffu;
-                todo &= ~*rows;
-                if (d++ % gridDim.z == blockIdx.z) return a;
+                left.todo &= ~*rows;
+                if (left.d++ % gridDim.z == blockIdx.z) return a;
             }
             return -1;
         };
-        unsigned rows = 0;
-        int a = advance(&rows);
-        if (AHEAD && a >= 0) load_w(a);
-        queue_wait<RING - 1>();
+        Left left{with, 0}, ahead{with, 0};
+        int w_at = 0;  // the place of the next adapter in the queue
+        auto ask_w = [&](int to) {
+            unsigned rows;
+            const int a = advance(ahead, &rows);
+            if (a >= 0) load_w(a, to);
+            queue_commit();
+        };
+        if constexpr (AHEAD > 0) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) ask_w(i);
+        }
+        queue_wait<RING - 1 + AHEAD>();
         Out8<TO, VEC> now[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (VEC) {
 #pragma unroll
-                for (int w = 0; w < WORDS; ++w) now[i].b[w] = queue[(((m % RING) * 4 + i) * WORDS + w) * kThreads];
+                for (int w = 0; w < WORDS; ++w) now[i].b[w] = queue[((slot * 4 + i) * WORDS + w) * kThreads];
             } else {
                 int64_t at;
                 int left;
@@ -867,8 +896,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
                 if (!(with >> ((i >> 1) * 8 + g) & 1) && has(m, i, &at, &left)) now[i].store(out + at, left);
             }
         }
-        while (a >= 0) {
-            if (a != held) {
+        unsigned rows = 0;
+        for (int a = advance(left, &rows); a >= 0; a = advance(left, &rows)) {
+            if constexpr (AHEAD > 0) {
+                queue_wait<AHEAD - 1>();
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) raw[kt][i] = read16(w_queue + ((w_at * KT + kt) * 4 + i) * kThreads);
+            }
+            if (AHEAD || a != held) {
                 held = a;
                 if (!AHEAD) load_w(a);
 #pragma unroll
@@ -879,11 +916,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
                         b[kt][j][0] = __byte_perm(v[0].w[j / 2], v[1].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
                         b[kt][j][1] = __byte_perm(v[2].w[j / 2], v[3].w[j / 2], (j & 1) ? 0x7632 : 0x5410);
                     }
-                scale = k.scale ? k.scale[a] : 1.0f;
             }
-            unsigned next_rows = 0;
-            const int next = advance(&next_rows);
-            if (AHEAD && next >= 0) load_w(next);  // in flight during this adapter's products
             float acc[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -906,16 +939,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : MT =
                 int64_t at;
                 int left;
                 if (!(rows >> ((i >> 1) * 8 + g) & 1) || !has(m, i, &at, &left)) continue;
+                const float scale = row_scale[m * 16 + (i >> 1) * 8 + g];
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = acc[j][i] * scale;
                 now[i].add(v);
                 now[i].store(out + at, left);
             }
-            a = next;
-            rows = next_rows;
+            if constexpr (AHEAD > 0) {
+                ask_w(w_at);
+                w_at = w_at + 1 == AHEAD ? 0 : w_at + 1;
+            }
         }
-        ask(m + RING);
+        ask(m + RING, slot);
+        slot = slot + 1 == RING ? 0 : slot + 1;
     }
     queue_wait<0>();
 }
@@ -1524,29 +1561,37 @@ cudaError_t project(const ProjK &k, shmm_dtype_t xt, shmm_dtype_t wt, cudaStream
     return project_simt<bf16, float>(k, s);
 }
 
-template <int MT, int KT, bool VEC, typename TO>
+template <bool FEW, int KT, bool VEC, typename TO>
 cudaError_t expand_mma(ExpandK k, int nranks, cudaStream_t s) {
-    using Shape = ExpandShape<MT, KT, TO>;
-    auto kern = expand_mma_kernel<MT, KT, VEC, TO>;
+    using Shape = ExpandShape<FEW, KT, TO>;
+    auto kern = expand_mma_kernel<FEW, KT, VEC, TO>;
     static shmm::PerDevice<int> done;
-    cudaError_t e = opt_in(kern, Shape::kSmem, &done);
+    cudaError_t e = opt_in(kern, Shape::smem(FEW ? 1 : kMaxRowTiles), &done);
     if (e != cudaSuccess) return e;
-    k.row_tiles = (int)((k.brows + 16 * MT - 1) / (16 * MT));
-    const int64_t cols = (k.bcols + 511) / 512, tiles = (int64_t)k.row_tiles * nranks * cols;
-    int c, z;
-    spread(tiles, (MT == 1 && KT == 1 ? 3 : 2) * sms(), k.n < 16 * MT ? k.n : 16 * MT, 1, true, &c, &z);
-    return launch_pdl(kern, dim3((unsigned)(k.row_tiles * nranks), (unsigned)cols, z), dim3(kThreads), Shape::kSmem, s,
-                      k);
+    const int64_t cols = (k.bcols + 511) / 512;
+    k.row_tiles = (int)((k.brows + 16 * k.mt - 1) / (16 * k.mt));
+    int c, z = 1;
+    if (FEW) spread((int64_t)k.row_tiles * nranks * cols, 2 * sms(), k.n < 16 ? k.n : 16, 1, true, &c, &z);
+    return launch_pdl(kern, dim3((unsigned)(k.row_tiles * nranks), (unsigned)cols, z), dim3(kThreads),
+                      Shape::smem(k.mt), s, k);
 }
 
 template <bool VEC, typename TO>
-cudaError_t expand_vec(const ExpandK &k, int nranks, cudaStream_t s) {
-    // Tall row tiles load a factor's piece less often; they need rows enough
-    // to fill the card.
-    const bool many = (k.brows + 63) / 64 * nranks * ((k.bcols + 511) / 512) >= sms();
-    if (k.R <= 16) return many ? expand_mma<4, 1, VEC, TO>(k, nranks, s) : expand_mma<1, 1, VEC, TO>(k, nranks, s);
-    if (k.R <= 32) return many ? expand_mma<4, 2, VEC, TO>(k, nranks, s) : expand_mma<1, 2, VEC, TO>(k, nranks, s);
-    return many ? expand_mma<4, 4, VEC, TO>(k, nranks, s) : expand_mma<1, 4, VEC, TO>(k, nranks, s);
+cudaError_t expand_vec(ExpandK k, int nranks, cudaStream_t s) {
+    // A CTA of more row tiles reads a factor's piece and the low rows' split
+    // less often (its start costs some 3 us), while the last wave of CTAs
+    // leaves less of the card empty the more of them there are: 16 row tiles
+    // where that makes six waves of two CTAs per SM, 8 for three, else 4.
+    auto waves = [&](int mt) {
+        return (double)((k.brows + 16 * mt - 1) / (16 * mt) * nranks * ((k.bcols + 511) / 512)) / (2 * sms());
+    };
+    k.mt = waves(16) >= 6 ? 16 : waves(8) >= 3 ? 8 : waves(4) >= 0.5 ? 4 : 1;
+    if (k.mt == 1) {
+        if (k.R <= 16) return expand_mma<true, 1, VEC, TO>(k, nranks, s);
+        return k.R <= 32 ? expand_mma<true, 2, VEC, TO>(k, nranks, s) : expand_mma<true, 4, VEC, TO>(k, nranks, s);
+    }
+    if (k.R <= 16) return expand_mma<false, 1, VEC, TO>(k, nranks, s);
+    return k.R <= 32 ? expand_mma<false, 2, VEC, TO>(k, nranks, s) : expand_mma<false, 4, VEC, TO>(k, nranks, s);
 }
 
 template <typename TO>
