@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from array import array
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -136,12 +137,12 @@ def lib():
                                                              ctypes.POINTER(ctypes.c_size_t)]
         L.shmm_layernorm_backward.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P, P, P, P, P, P, P, P, P,
                                               P, ctypes.c_size_t, P]
-        L.shmm_layernorm_all_gather_forward.argtypes = [P, PP, P, P, ctypes.c_float, PP, PP, PP, P]
-        L.shmm_layernorm_all_gather_backward.argtypes = [P, ctypes.c_int, PP, PP, PP, PP, P, PP, P, P, P,
-                                                         ctypes.c_size_t, P]
-        L.shmm_adapters_forward.argtypes = [P, ctypes.c_int, ctypes.c_int, PP, P, P, P, P, PP, PP, P, P]
+        L.shmm_layernorm_all_gather_forward.argtypes = [P, P, P, P, ctypes.c_float, P, P, P, P]
+        L.shmm_layernorm_all_gather_backward.argtypes = [P, ctypes.c_int, P, P, P, P, P, P, P, P, P, ctypes.c_size_t,
+                                                         P]
+        L.shmm_adapters_forward.argtypes = [P, ctypes.c_int, ctypes.c_int, P, P, P, P, P, P, P, P, P]
         L.shmm_adapters_workspace_size.argtypes = [P, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
-        L.shmm_adapters_backward.argtypes = [P, ctypes.c_int, ctypes.c_int, PP, PP, P, P, P, P, P, PP, PP, P, P, P,
+        L.shmm_adapters_backward.argtypes = [P, ctypes.c_int, ctypes.c_int, P, P, P, P, P, P, P, P, P, P, P, P,
                                              ctypes.c_size_t, P]
         L.shmm_reshard.argtypes = [ctypes.POINTER(shmm_mesh_t), ctypes.POINTER(shmm_spec_t),
                                    ctypes.POINTER(shmm_spec_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
@@ -318,12 +319,13 @@ def _tensor(t, what: str, shape, dtype, dev: int) -> int:
     return _refuse(t, what, shape, dtype)
 
 
-def _tensors(ts, what: str, shapes, dtype, dev: int) -> ctypes.Array:
-    """Per-rank pointer array of dense tensors (see _tensor), one per shape."""
-    n = len(shapes)
-    if len(ts) != n:
-        raise ValueError("%s: %d tensors, the plan has %d ranks" % (what, len(ts), n))
-    ptrs = []
+def _tensors(ts, what: str, shapes, dtype, dev: int) -> array:
+    """Addresses of dense tensors (see _tensor), one per shape, as an array of
+    pointers; its _at() goes to the library (a ctypes array costs ten times
+    as much to make)."""
+    if len(ts) != len(shapes):
+        raise ValueError("%s: %d tensors, the plan has %d ranks" % (what, len(ts), len(shapes)))
+    ptrs = array("Q")
     for t, shape in zip(ts, shapes):
         try:
             if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
@@ -332,18 +334,11 @@ def _tensors(ts, what: str, shapes, dtype, dev: int) -> ctypes.Array:
         except AttributeError:
             pass
         _refuse(t, "%s[%d]" % (what, len(ptrs)), shape, dtype)
-    return _pointers(n)(*ptrs)
+    return ptrs
 
 
-_pointer_types = {}
-
-
-def _pointers(n: int):
-    """The ctypes type of an array of n pointers."""
-    t = _pointer_types.get(n)
-    if t is None:
-        t = _pointer_types[n] = ctypes.c_void_p * n
-    return t
+def _at(ptrs: Optional[array]) -> Optional[int]:
+    return None if ptrs is None else ptrs.buffer_info()[0]
 
 
 def _rows_dtype(x, what: str = "x"):
@@ -479,11 +474,12 @@ class Plan:
         for layernorm_all_gather_backward."""
         dt, f32, dev = TORCH_DTYPES[self.out_dtype], torch.float32, _device()
         block, rows, cols = self._gathered()
+        shard = _tensors(shard_r, "shard", block, dt, dev)
+        full = _tensors(full_r, "full", self._shapes(TENSOR_C), dt, dev)
+        mean, rstd = _tensors(mean_r, "mean", rows, f32, dev), _tensors(rstd_r, "rstd", rows, f32, dev)
         _check(lib().shmm_layernorm_all_gather_forward(
-            self._h, _tensors(shard_r, "shard", block, dt, dev), _tensor(gamma, "gamma", cols, f32, dev),
-            _tensor(beta, "beta", cols, f32, dev), eps, _tensors(full_r, "full", self._shapes(TENSOR_C), dt, dev),
-            _tensors(mean_r, "mean", rows, f32, dev), _tensors(rstd_r, "rstd", rows, f32, dev),
-            _stream_handle(stream)))
+            self._h, _at(shard), _tensor(gamma, "gamma", cols, f32, dev), _tensor(beta, "beta", cols, f32, dev), eps,
+            _at(full), _at(mean), _at(rstd), _stream_handle(stream)))
 
     def layernorm_all_gather_backward(self, dfull_r, shard_r, mean_r, rstd_r, gamma, dshard_r, dgamma, dbeta,
                                       workspace, stream=None):
@@ -496,11 +492,12 @@ class Plan:
         block, rows, cols = self._gathered()
         gdt = f32 if len(dfull_r) and getattr(dfull_r[0], "dtype", None) is f32 else dt
         ws, ws_bytes = _workspace(workspace, dev)
+        dfull = _tensors(dfull_r, "dfull", self._shapes(TENSOR_C), gdt, dev)
+        shard, dshard = _tensors(shard_r, "shard", block, dt, dev), _tensors(dshard_r, "dshard", block, dt, dev)
+        mean, rstd = _tensors(mean_r, "mean", rows, f32, dev), _tensors(rstd_r, "rstd", rows, f32, dev)
         _check(lib().shmm_layernorm_all_gather_backward(
-            self._h, F32 if gdt is f32 else BF16, _tensors(dfull_r, "dfull", self._shapes(TENSOR_C), gdt, dev),
-            _tensors(shard_r, "shard", block, dt, dev), _tensors(mean_r, "mean", rows, f32, dev),
-            _tensors(rstd_r, "rstd", rows, f32, dev), _tensor(gamma, "gamma", cols, f32, dev),
-            _tensors(dshard_r, "dshard", block, dt, dev), _tensor(dgamma, "dgamma", cols, f32, dev),
+            self._h, F32 if gdt is f32 else BF16, _at(dfull), _at(shard), _at(mean), _at(rstd),
+            _tensor(gamma, "gamma", cols, f32, dev), _at(dshard), _tensor(dgamma, "dgamma", cols, f32, dev),
             _tensor(dbeta, "dbeta", cols, f32, dev), ws, ws_bytes, _stream_handle(stream)))
 
     def adapters_workspace_size(self, n_adapters: int, rank: int) -> int:
@@ -526,9 +523,11 @@ class Plan:
         dev = _device()
         n, rank, ptrs = self._adapters(row_adapter, down, up, scale, dev)
         dt, box = TORCH_DTYPES[self.out_dtype], self._shapes(TENSOR_C)
+        A = _tensors(A_r, "A", self._shapes(TENSOR_A), TORCH_DTYPES[self.in_dtype], dev)
+        base = None if base_r is None else _tensors(base_r, "base", box, dt, dev)
+        C = _tensors(C_r, "C", box, dt, dev)
         _check(lib().shmm_adapters_forward(
-            self._h, n, rank, _tensors(A_r, "A", self._shapes(TENSOR_A), TORCH_DTYPES[self.in_dtype], dev), *ptrs,
-            None if base_r is None else _tensors(base_r, "base", box, dt, dev), _tensors(C_r, "C", box, dt, dev),
+            self._h, n, rank, _at(A), *ptrs, _at(base), _at(C),
             _tensor(low, "low", (self.shape[0], rank), torch.float32, dev), _stream_handle(stream)))
 
     def adapters_backward(self, dC_r, A_r, row_adapter, down, up, scale, low, base_r, dA_r, ddown, dup, workspace,
@@ -541,10 +540,11 @@ class Plan:
         dt, box, f32 = TORCH_DTYPES[self.in_dtype], self._shapes(TENSOR_A), torch.float32
         I, J, K = self.shape
         ws, ws_bytes = _workspace(workspace, dev)
+        dC = _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev)
+        A, dA = _tensors(A_r, "A", box, dt, dev), _tensors(dA_r, "dA", box, dt, dev)
+        base = None if base_r is None else _tensors(base_r, "base", box, dt, dev)
         _check(lib().shmm_adapters_backward(
-            self._h, n, rank, _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev),
-            _tensors(A_r, "A", box, dt, dev), *ptrs, _tensor(low, "low", (I, rank), f32, dev),
-            None if base_r is None else _tensors(base_r, "base", box, dt, dev), _tensors(dA_r, "dA", box, dt, dev),
+            self._h, n, rank, _at(dC), _at(A), *ptrs, _tensor(low, "low", (I, rank), f32, dev), _at(base), _at(dA),
             _tensor(ddown, "ddown", (n, rank, J), f32, dev), _tensor(dup, "dup", (n, rank, K), f32, dev), ws, ws_bytes,
             _stream_handle(stream)))
 
