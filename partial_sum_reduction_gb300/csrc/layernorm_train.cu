@@ -237,16 +237,21 @@ __device__ __forceinline__ int col_of(int j) {
 
 // ---- rows in flight ----------------------------------------------------------
 
-// Many rows: two warps keep whole rows coming through a ring in shared memory
-// (bulk copies, an mbarrier pair per entry) while the other warps work on the
-// rows that have landed, so the loads never wait for a row's two block sums.
-// An entry is one row of one buffer: x, a residual, or a member's gradient;
-// the copying warps (a thread of each) take every other one, because a
-// thread's own instructions per entry are what one alone was bound by.
+// Many rows: a warp or two keep whole rows coming through a ring in shared
+// memory (bulk copies, an mbarrier pair per entry) while the other warps work
+// on the rows that have landed, so the loads never wait for a row's two block
+// sums.  An entry is one row of one buffer: x, a residual, or a member's
+// gradient; copying warp i (one thread of it) takes entries i, i + COPIERS, ...
 // With the rows in registers instead, what was in flight fell with every
 // register the running sums took: 63 us forward and 81 us backward at 8192 x
 // 4096 bf16 with a residual, where this takes FWD_US and BWD_US.
-constexpr int kMaxStages = 16, kCopiers = 2;
+constexpr int kMaxStages = 16;
+// Forward, one block: three CTAs per SM under one another's chains of sums and
+// barriers (54 -> 49 us at 8192 x 4096 bf16 with a residual; with a second
+// copying warp they do not fit); gathered: two (98 against 101 us, 8 ranks).
+// Backward: two, the third's registers would spill (57 against 77 us), and a
+// second copying warp for its three entries a row.
+constexpr int kForwardCopiers = 1, kBackwardCopiers = 2;
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort_flag;
@@ -278,6 +283,7 @@ __device__ __forceinline__ void ring_init(Ring &ring, int stages, int readers) {
 
 // A copying thread: row `from` (or nothing, if the bounds-checked build found
 // it outside its buffer) into its next entry.  False after an abort.
+template <int COPIERS>
 __device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uint32_t entries, uint32_t entry_bytes,
                                          const void *from, uint32_t bytes, bool ok, int *status) {
     if (!shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.empty[turn.stage]), turn.phase ^ 1, &ring.abort_flag, status))
@@ -293,20 +299,21 @@ __device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uin
     } else {
         shmm_dev::mbar_arrive(bar);
     }
-    turn.next(stages, kCopiers);
+    turn.next(stages, COPIERS);
     return true;
 }
 
 // The end, for every thread.  The working warps have waited for every entry,
 // unless a wait was given up: then a copying thread (`put` > 0, its n-th entry
-// number `first` + n kCopiers) waits, again with a limit, for its entries of
+// number `first` + n COPIERS) waits, again with a limit, for its entries of
 // the last lap, so that no copy into shared memory stays in flight.
+template <int COPIERS>
 __device__ __forceinline__ void ring_end(Ring &ring, int first, int64_t put, int stages, int *status) {
     __syncwarp();
     __syncthreads();
     if (put && *(volatile int *)&ring.abort_flag)
-        for (int64_t i = put > stages / kCopiers ? put - stages / kCopiers : 0; i < put; ++i) {
-            const int64_t u = first + i * kCopiers;
+        for (int64_t i = put > stages / COPIERS ? put - stages / COPIERS : 0; i < put; ++i) {
+            const int64_t u = first + i * COPIERS;
             shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[u % stages]), (uint32_t)(u / stages) & 1,
                                 &ring.abort_flag, status, false);
         }
@@ -456,17 +463,17 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_kernel(const __grid_co
     }
 }
 
-// Many rows, through the ring.  blockDim.x - 32 kCopiers threads work, the last
-// kCopiers warps copy.
+// Many rows, through the ring.  blockDim.x - 32 kForwardCopiers threads work, the
+// last warps copy.
 template <typename T, int NV, int N, bool BIG>
-__global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG ? 1 : 2)
+__global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kForwardCopiers, BIG ? 1 : N == 1 ? 3 : 2)
     ln_forward_stream_kernel(const __grid_constant__ FwdK<N> k, int stages) {
     pdl_enter();
     constexpr int VW = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) uint8_t entries[];
     __shared__ Ring ring;
     __shared__ float2 scratch[2 * kMaxThreads / 32];
-    const int cols = (int)k.cols, work = blockDim.x - 32 * kCopiers;
+    const int cols = (int)k.cols, work = blockDim.x - 32 * kForwardCopiers;
     const uint32_t bytes = (uint32_t)cols * sizeof(T);
     const bool has_res = N == 1 && k.res;
     ring_init(ring, stages, work / 32);
@@ -475,22 +482,27 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG
         const int first = ((int)threadIdx.x - work) / 32;
         if ((threadIdx.x & 31) == 0) {
             // entries of a row: x, then the residual
-            const int per_row = has_res ? 2 : 1;
             const uint32_t at = shmm_dev::smem_u32(entries);
             Turn turn{first, 0};
-            int64_t t = blockIdx.x + (int64_t)(first / per_row) * gridDim.x;
-            const int e = first % per_row;  // the same in every row: per_row divides kCopiers
-            const int64_t step = (int64_t)gridDim.x * (kCopiers / per_row);
-            for (bool ok = true; t < k.rows && ok; t += step) {
+            int64_t t = blockIdx.x;
+            int e = first;
+            for (bool ok = true; ok;) {
+                const int per_row = has_res ? 2 : 1;
+                while (e >= per_row) {
+                    e -= per_row;
+                    t += gridDim.x;
+                }
+                if (t >= k.rows) break;
                 int s, g;
                 int64_t rr, grow;
                 locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-                ok = ring_put(ring, turn, stages, at, bytes, (const T *)(e ? k.res : k.src[s]) + rr * cols, bytes,
+                ok = ring_put<kForwardCopiers>(ring, turn, stages, at, bytes, (const T *)(e ? k.res : k.src[s]) + rr * cols, bytes,
                               in_bounds(k.status, rr * cols, cols, k.brows * cols), k.status);
                 put += ok;
+                e += kForwardCopiers;
             }
         }
-        ring_end(ring, first, put, stages, k.status);
+        ring_end<kForwardCopiers>(ring, first, put, stages, k.status);
         return;
     }
     Turn turn{0, 0};
@@ -570,7 +582,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG
             for (int m = 0; m < k.G; ++m) y.store((T *)k.dst[g * k.G + m] + grow * cols + col[j]);
         }
     }
-    ring_end(ring, 0, 0, stages, k.status);
+    ring_end<kForwardCopiers>(ring, 0, 0, stages, k.status);
 }
 
 // Rows of any width: the row is read three times (from L2 after the first).
@@ -765,17 +777,22 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
 // Many rows, through the ring: per row the members' gradients in rank order,
 // x, and the residual's gradient.
 template <typename T, typename GT, int NV, int N, bool BIG>
-__global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG ? 1 : 2)
+__global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopiers, BIG ? 1 : 2)
     ln_backward_stream_kernel(const __grid_constant__ BwdK<N> k, int stages) {
     pdl_enter();
     constexpr int VW = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) uint8_t entries[];
     __shared__ Ring ring;
     __shared__ float2 scratch[2 * kMaxThreads / 32];
-    const int cols = (int)k.cols, work = blockDim.x - 32 * kCopiers;
+    const int cols = (int)k.cols, work = blockDim.x - 32 * kBackwardCopiers;
     const uint32_t bytes = (uint32_t)cols * sizeof(T), gbytes = (uint32_t)cols * sizeof(GT);
     const uint32_t entry = gbytes > bytes ? gbytes : bytes;
     const bool has_res = N == 1 && k.res;
+    // gamma: with one member in registers, with several, whose sum takes the
+    // registers, in shared memory (8 fp32 members: 184 against 198 us; one
+    // member: 57 in registers against 64).
+    float *gains = reinterpret_cast<float *>(entries + (size_t)stages * entry);
+    F2 gr[N == 1 ? NV : 1][VW / 2];
     ring_init(ring, stages, work / 32);
     if ((int)threadIdx.x >= work) {
         int64_t put = 0;
@@ -789,40 +806,47 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG
             int64_t rr, grow;
             if (t < k.rows) locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
             for (bool ok = true; ok;) {
-                if (e >= per_row) {  // kCopiers <= per_row: the next row
+                if (e >= per_row) {  // kBackwardCopiers <= per_row: the next row
                     e -= per_row;
                     t += gridDim.x;
                     if (t < k.rows) locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
                 }
                 if (t >= k.rows) break;
                 if (e < k.G)
-                    ok = ring_put(ring, turn, stages, at, entry, (const GT *)k.grad[g * k.G + e] + grow * cols, gbytes,
+                    ok = ring_put<kBackwardCopiers>(ring, turn, stages, at, entry, (const GT *)k.grad[g * k.G + e] + grow * cols, gbytes,
                                   in_bounds(k.status, grow * cols, cols, k.G * k.brows * cols), k.status);
                 else
-                    ok = ring_put(ring, turn, stages, at, entry,
+                    ok = ring_put<kBackwardCopiers>(ring, turn, stages, at, entry,
                                   (const T *)(N == 1 && e > k.G ? k.res : k.src[s]) + rr * cols, bytes,
                                   in_bounds(k.status, rr * cols, cols, k.brows * cols), k.status);
                 put += ok;
-                e += kCopiers;
+                e += kBackwardCopiers;
             }
         }
-        ring_end(ring, first, put, stages, k.status);
+        ring_end<kBackwardCopiers>(ring, first, put, stages, k.status);
         return;
     }
     Turn turn{0, 0};
     int sum_turn = 0;
     const float inv_n = 1.0f / (float)cols;
-    F2 ga[NV][VW / 2], dg[NV][VW / 2], db[NV][VW / 2];
+    F2 dg[NV][VW / 2], db[NV][VW / 2];
     int col[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         col[j] = (threadIdx.x + j * work) * VW;
 #pragma unroll
         for (int i = 0; i < VW / 2; ++i) {
-            ga[j][i] = col[j] < cols ? pair(k.gamma[col[j] + 2 * i], k.gamma[col[j] + 2 * i + 1]) : both(0.0f);
             dg[j][i] = db[j][i] = both(0.0f);
+            const float2 two = col[j] < cols ? make_float2(k.gamma[col[j] + 2 * i], k.gamma[col[j] + 2 * i + 1])
+                                             : make_float2(0.0f, 0.0f);
+            if constexpr (N == 1) gr[j][i] = pair(two.x, two.y);
+            else if (col[j] < cols) *reinterpret_cast<float2 *>(gains + col[j] + 2 * i) = two;
         }
     }
+    auto ga = [&](int j, int i) {
+        if constexpr (N == 1) return gr[j][i];
+        else return F2{*reinterpret_cast<const uint64_t *>(gains + col[j] + 2 * i)};
+    };
     float mean = 0.0f, rstd = 0.0f;  // read a row ahead
     auto read_stats = [&](int64_t t) {
         int s, g;
@@ -877,7 +901,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG
             if (col[j] < cols)
 #pragma unroll
                 for (int i = 0; i < VW / 2; ++i) {
-                    const F2 d = dy(j, i), xh = fma(x[j].get2(i), rs2, shift2), w = d * ga[j][i];
+                    const F2 d = dy(j, i), xh = fma(x[j].get2(i), rs2, shift2), w = d * ga(j, i);
                     sw = sw + w;
                     swx = fma(w, xh, swx);
                     dg[j][i] = fma(d, xh, dg[j][i]);
@@ -893,7 +917,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG
             F2 o[VW / 2];
 #pragma unroll
             for (int i = 0; i < VW / 2; ++i)
-                o[i] = fma(fma(x[j].get2(i), rs2, shift2), k2, fma(dy(j, i) * ga[j][i], rs2, k1));
+                o[i] = fma(fma(x[j].get2(i), rs2, shift2), k2, fma(dy(j, i) * ga(j, i), rs2, k1));
             if constexpr (N == 1) {
                 if (has_res) {
                     Raw<T, VW> r;
@@ -919,7 +943,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kCopiers, BIG
             *reinterpret_cast<float2 *>(part + cols + col[j] + 2 * i) = split(db[j][i]);
         }
     }
-    ring_end(ring, 0, 0, stages, k.status);
+    ring_end<kBackwardCopiers>(ring, 0, 0, stages, k.status);
 }
 
 // Rows of any width: the row is read twice, and each thread adds its columns
@@ -1032,29 +1056,29 @@ struct StreamShape {
     int threads, per_sm, stages;
     size_t smem;
 };
-StreamShape stream_shape(int64_t cols, int vw, int64_t entry) {
+StreamShape stream_shape(int64_t cols, int64_t entry, int64_t extra, int most) {  // most: CTAs of 256 threads
     StreamShape h;
     h.threads = (int)((cols + kCols * 32 - 1) / (kCols * 32)) * 32;
-    h.per_sm = h.threads > 256 ? 1 : 512 / h.threads > 6 ? 6 : 512 / h.threads;
-    const int64_t budget = (216 * 1024) / h.per_sm - 2048;
+    h.per_sm = h.threads > 256 ? 1 : most * 256 / h.threads > 6 ? 6 : most * 256 / h.threads;
+    const int64_t budget = (220 * 1024) / h.per_sm - 2048 - extra;
     h.stages = (int)(budget / entry < kMaxStages ? budget / entry : kMaxStages);
-    h.smem = (size_t)(h.stages * entry);
+    h.smem = (size_t)(h.stages * entry + extra);
     return h;
 }
 
 template <typename K>
-cudaError_t launch_stream(void (*kern)(K, int), const K &k, const StreamShape &h, int64_t grid, cudaStream_t s,
+cudaError_t launch_stream(void (*kern)(K, int), const K &k, const StreamShape &h, int copiers, int64_t grid, cudaStream_t s,
                           shmm::PerDevice<int> *done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= shmm::kMaxDevices) return cudaErrorInvalidDevice;
     if (!done->get(dev)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
         if (e != cudaSuccess) return e;
         done->set(dev, 1);
     }
-    return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)h.threads + 32 * kCopiers), h.smem, s, k, h.stages);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)h.threads + 32 * copiers), h.smem, s, k, h.stages);
 }
 
 // Rows enough for the ring kernels: every CTA has three rows or more to keep
@@ -1065,19 +1089,21 @@ template <typename T, int N, bool BIG>
 cudaError_t forward_stream(const FwdK<N> &k, cudaStream_t s) {
     constexpr int VW = 16 / (int)sizeof(T);
     static shmm::PerDevice<int> done;
-    const StreamShape h = stream_shape(k.cols, VW, k.cols * (int64_t)sizeof(T));
-    return launch_stream(ln_forward_stream_kernel<T, kCols / VW, N, BIG>, k, h, (int64_t)sms() * h.per_sm, s, &done);
+    const StreamShape h = stream_shape(k.cols, k.cols * (int64_t)sizeof(T), 0, N == 1 ? 3 : 2);
+    return launch_stream(ln_forward_stream_kernel<T, kCols / VW, N, BIG>, k, h, kForwardCopiers,
+                         (int64_t)sms() * h.per_sm, s, &done);
 }
 
 template <typename T, typename GT, int N, bool BIG>
 cudaError_t backward_stream(const BwdK<N> &k, int *parts, cudaStream_t s) {
     constexpr int VW = 16 / (int)sizeof(T);
     static shmm::PerDevice<int> done;
-    const StreamShape h = stream_shape(k.cols, VW, k.cols * (int64_t)(sizeof(T) > sizeof(GT) ? sizeof(T) : sizeof(GT)));
+    const StreamShape h = stream_shape(k.cols, k.cols * (int64_t)(sizeof(T) > sizeof(GT) ? sizeof(T) : sizeof(GT)),
+                                       N == 1 ? 0 : k.cols * 4, 2);
     int64_t grid = (int64_t)sms() * h.per_sm;
     if (grid > max_parts(k.cols)) grid = max_parts(k.cols);
     *parts = (int)grid;
-    return launch_stream(ln_backward_stream_kernel<T, GT, kCols / VW, N, BIG>, k, h, grid, s, &done);
+    return launch_stream(ln_backward_stream_kernel<T, GT, kCols / VW, N, BIG>, k, h, kBackwardCopiers, grid, s, &done);
 }
 
 template <typename T, int VW, int N>
