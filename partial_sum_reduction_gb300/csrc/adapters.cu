@@ -405,27 +405,36 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
 }
 
 // Many rows: 128 rows per CTA on tcgen05.  One thread streams X in boxes of
-// 128 rows x 64 columns, with the boxes of the adapters the tile uses (up to
-// 128 factor rows per pass, each a product of its own into its own TMEM
+// 128 rows x 64 columns, with the boxes of the adapters the tile uses (128
+// factor rows per pass, each a product of its own into its own TMEM
 // columns), through a ring of shared-memory stages; one thread issues the
-// products; four warps read the result out of TMEM, a row per thread.  A
+// products; eight warps read the result out of TMEM, a row per thread.  A
 // cluster along y shares the columns, its sums meeting through distributed
 // shared memory in order.  Beside the warp instructions above it: the factor
 // is read once per 128 rows instead of per 32, and no thread spends
 // instructions on addresses, which bounded them.
-constexpr int kTcThreads = 192, kTcStages = 5;
+constexpr int kTcThreads = 320, kTcStages = 6;
+// Chunks summed in the tensor memory before their sum is added in registers:
+// 16 instructions.  The tensor core's own fp32 additions cut instead of
+// rounding, so their error grows with their number (some 4e-8 of the sum per
+// instruction: 1e-5 over a 7168-column share); in registers they round.
+constexpr int kTcSegment = 4;
 constexpr int kTcSum = 132;  // fp32 of a row of sums: whole 16-byte vectors
-constexpr uint32_t kTcRing = 109568;  // two CTAs per SM
+// One CTA per SM: the reading warps' sums of a pass take 64 registers a
+// thread, and a smaller pass would make the tile with the most adapters, which
+// then streams X twice, the one that ends last.
+constexpr int kTcCols = 128;  // factor rows of a pass
+constexpr uint32_t kTcStage = 16384 + kTcCols * 128, kTcRing = kTcStages * kTcStage;
 constexpr size_t kTcSmem = kTcRing + 1024;
 static_assert(128 * kTcSum * 4 <= kTcRing, "the sums take the ring's memory");
 
 template <int RP>
 __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_constant__ ProjTcK k) {
     pdl_wait();
-    constexpr int ROWS = 128, PER = 128 / RP, S = kTcStages;
+    constexpr int ROWS = 128, PER = kTcCols / RP, S = kTcStages, MINE = kTcCols / 2;  // MINE: of a reading warp
     __shared__ int ids[ROWS], list[ROWS], count, abort_flag;
     __shared__ float scales[PER];
-    __shared__ __align__(8) uint64_t bars[2 * S + 1];
+    __shared__ __align__(8) uint64_t bars[2 * S + 5];
     __shared__ uint32_t tmem_at;
     extern __shared__ uint8_t raw_smem[];
     uint8_t *tiles = raw_smem + (1024 - (shmm_dev::smem_u32(raw_smem) & 1023)) % 1024;
@@ -435,14 +444,17 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     auto full = [&](int s) { return shmm_dev::smem_u32(&bars[s]); };
     auto empty = [&](int s) { return shmm_dev::smem_u32(&bars[S + s]); };
-    const uint32_t done = shmm_dev::smem_u32(&bars[2 * S]);
+    auto done = [&](int b) { return shmm_dev::smem_u32(&bars[2 * S + b]); };         // a segment is in buffer b
+    auto drained = [&](int b) { return shmm_dev::smem_u32(&bars[2 * S + 2 + b]); };  // and has been read (8 warps)
+    const uint32_t finished = shmm_dev::smem_u32(&bars[2 * S + 4]);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2 * S + 1; ++i) shmm_dev::mbar_init(shmm_dev::smem_u32(&bars[i]), 1);
+        for (int i = 0; i < 2 * S + 5; ++i)
+            shmm_dev::mbar_init(shmm_dev::smem_u32(&bars[i]), i == 2 * S + 2 || i == 2 * S + 3 ? 8 : 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         shmm_tc::fence_async();
     }
-    if (warp == 1) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 128);
+    if (warp == 1) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 256);
     shmm_tc::fence_before();
     const int brow = blockIdx.x / k.row_tiles, l0 = (int)(blockIdx.x % k.row_tiles) * ROWS;
     const int64_t t0 = brow * k.brows + l0, t1 = (brow + 1) * k.brows;
@@ -455,17 +467,12 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     if (cr == 0)  // rows without an adapter: zeros
         for (int i = threadIdx.x; i < ROWS * k.R; i += kTcThreads)
             if (ids[i / k.R] < 0 && t0 + i / k.R < t1) k.out[t0 * k.R + i] = 0.0f;
-    // As many stages as fit with the factors a pass may bring, the same number
-    // for one adapter and two: a CTA's share of the memory's bandwidth is what
-    // it has in flight, and the one with the fewest stages ends last.
-    const int most = nd < 2 ? 2 : nd < PER ? nd : PER;
-    const uint32_t stage_bytes = 16384 + most * RP * 128;
-    const uint32_t stages = kTcRing / stage_bytes < S ? kTcRing / stage_bytes : S;
     const int lo = (int)((int64_t)k.chunks * cr / cs), hi = (int)((int64_t)k.chunks * (cr + 1) / cs);
     // Producer and issuer are one thread each, so their own instructions are
     // what a chunk costs them (a division or two each made it 1500 cycles):
     // both walk stages and blocks by counting.
     uint32_t stage = 0, phase = 0, asked = 0;
+    uint32_t uses = 0;  // segments so far; segment u is the (u / 2)-th in buffer u % 2
     const int blk0 = k.b1 == 1 ? 0 : lo / k.per_block;
     bool ok = true;
     for (int p0 = 0, pass = 0; p0 < nd; p0 += PER, ++pass) {
@@ -479,14 +486,14 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
             for (int ch = lo; ch < hi; ++ch) {
                 ok = ok && shmm_dev::mbar_wait(empty(stage), phase ^ 1, &abort_flag, k.status);
                 if (!ok) break;
-                const uint32_t at = tiles_at + stage * stage_bytes, bar = full(stage);
+                const uint32_t at = tiles_at + stage * kTcStage, bar = full(stage);
                 shmm_dev::mbar_expect_tx(bar, bytes);
                 shmm_tc::load_box(at, x, bar, c, l0);
                 shmm_tc::load_box(at + 16384, &k.w, bar, wc, w_row);
                 for (int i = 1; i < na; ++i)
                     shmm_tc::load_box(at + 16384 + i * RP * 128, &k.w, bar, wc, list[p0 + i] * k.R);
                 ++asked;
-                if (++stage == stages) {
+                if (++stage == S) {
                     stage = 0;
                     phase ^= 1;
                 }
@@ -504,47 +511,80 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
             // is, so one for all of them, not one each.
             const uint64_t base = shmm_tc::operand(tiles_at, 16, 1024);
             const uint32_t idesc = shmm_tc::instruction(na * RP, false);
+            int left = 0;  // chunks of the segment still to come
             for (int ch = lo; ch < hi; ++ch) {
+                const uint32_t buf = uses & 1;
+                const bool start = left == 0;
+                if (start) {
+                    left = kTcSegment;
+                    if (uses >= 2) ok = ok && shmm_dev::mbar_wait(drained(buf), (uses / 2 - 1) & 1, &abort_flag, k.status);
+                }
                 ok = ok && shmm_dev::mbar_wait(full(stage), phase, &abort_flag, k.status);
                 if (!ok) break;
                 shmm_tc::fence_after();
-                const uint64_t xa = base + ((stage * stage_bytes) >> 4);  // addresses in units of 16 bytes
+                const uint64_t xa = base + ((stage * kTcStage) >> 4);  // addresses in units of 16 bytes
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    shmm_tc::mma_issue(tmem, xa + kk * 2, xa + 1024 + kk * 2, idesc, ch > lo || kk > 0);
+                    shmm_tc::mma_issue(tmem + buf * 128, xa + kk * 2, xa + 1024 + kk * 2, idesc, !start || kk > 0);
                 shmm_tc::mma_commit(empty(stage));
-                if (++stage == stages) {
+                if (++stage == S) {
                     stage = 0;
                     phase ^= 1;
                 }
+                if (--left == 0 || ch + 1 == hi) {
+                    left = 0;
+                    shmm_tc::mma_commit(done(buf));
+                    ++uses;
+                }
             }
-            shmm_tc::mma_commit(done);
+            // Not cut short by an abort: the products in flight read shared memory.
+            shmm_tc::mma_commit(finished);
+            shmm_dev::mbar_wait(finished, pass & 1, &abort_flag, k.status, false);
         }
         __syncwarp();
         float *sums = reinterpret_cast<float *>(tiles);  // [row][kTcSum], once the products are done
         if (warp >= 2) {
-            // Not cut short by an abort: the products in flight read shared memory.
-            shmm_dev::mbar_wait(done, pass & 1, &abort_flag, k.status, false);
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps; scales are written
-            shmm_tc::fence_after();
-            const int quad = warp & 3, row = quad * 32 + lane;
-            for (int i = 0; i < na; ++i) {
-                const int a = list[p0 + i];
+            // Warp: 32 rows, half of the columns, from c0 on.
+            const int quad = warp & 3, row = quad * 32 + lane, c0 = (warp - 2) / 4 * MINE;
+            float acc[MINE];
 #pragma unroll
-                for (int c = 0; c < RP; c += 16) {
+            for (int c = 0; c < MINE; ++c) acc[c] = 0.0f;
+            for (int ch = lo; ch < hi; ch += kTcSegment, ++uses) {
+                const uint32_t buf = uses & 1;
+                ok = ok && shmm_dev::mbar_wait(done(buf), uses / 2 & 1, &abort_flag, k.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                shmm_tc::fence_after();
+#pragma unroll
+                for (int c = 0; c < MINE; c += 16) {
+                    if (c0 + c >= na * RP) continue;
                     float v[16];
-                    shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + i * RP + c, v);
-                    if (cs > 1) {
+                    shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 + c0 + c, v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) sums[row * kTcSum + i * RP + c + j] = v[j];
-                    } else if (ids[row] == a && in_bounds(k.status, (t0 + row) * k.R, k.R, k.rows * k.R)) {
+                    for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                }
+                shmm_tc::fence_before();
+                __syncwarp();
+                if (lane == 0) shmm_dev::mbar_arrive(drained(buf));
+            }
+            // The ring's memory takes the sums once every warp's last segment
+            // is done, which the last product is part of.
+            asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j < k.R) k.out[(t0 + row) * k.R + c + j] = k.scale ? v[j] * scales[i] : v[j];
-                    }
+            for (int c = 0; c < MINE; c += 16) {
+                if (c0 + c >= na * RP) continue;
+                const int i = (c0 + c) / RP, r = (c0 + c) % RP;
+                if (cs > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(sums + row * kTcSum + c0 + c + j) =
+                            make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
+                } else if (ids[row] == list[p0 + i] && in_bounds(k.status, (t0 + row) * k.R, k.R, k.rows * k.R)) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (r + j < k.R) k.out[(t0 + row) * k.R + r + j] = k.scale ? acc[c + j] * scales[i] : acc[c + j];
                 }
             }
-            shmm_tc::fence_before();
         }
         if (cs > 1) {
             cluster.sync();
@@ -580,13 +620,13 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
     }
     // Never leave a load into shared memory in flight.
     if (warp == 0 && lane == 0)
-        for (uint32_t u = asked > stages ? asked - stages : 0; u < asked; ++u)
-            shmm_dev::mbar_wait(full(u % stages), u / stages & 1, &abort_flag, k.status, false);
+        for (uint32_t u = asked > S ? asked - S : 0; u < asked; ++u)
+            shmm_dev::mbar_wait(full(u % S), u / S & 1, &abort_flag, k.status, false);
     __syncwarp();
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
-    if (warp == 1) shmm_tc::tmem_free(tmem, 128);
+    if (warp == 1) shmm_tc::tmem_free(tmem, 256);
 }
 
 template <typename T>
@@ -1037,19 +1077,20 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 // Rows of an adapter.  A CTA marks them in a bit mask over a window of
 // kWindow rows (one read of the row adapters), with how many lie before each
 // 32-row word, then turns the marks into lists of up to kList rows, ascending.
-constexpr int kWindow = 32768, kList = 512;
+constexpr int kWindow = 16384, kList = 512;
 struct Marks {
     uint32_t bits[kWindow / 32];
     int before[kWindow / 32];
-    int warp_sum[kWarps];
+    int warp_sum[16];
 };
 
 // Marks the window's rows with adapter a; returns how many.  A warp takes
 // consecutive words.
+template <int WARPS>
 __device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t rows, int a, Marks &marks, int *status) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
-    const int per = (words + kWarps - 1) / kWarps, first = warp * per, last = first + per < words ? first + per : words;
+    const int per = (words + WARPS - 1) / WARPS, first = warp * per, last = first + per < words ? first + per : words;
     int mine = 0;
     for (int i0 = first; i0 < last; i0 += 8) {
         int v[8];
@@ -1072,7 +1113,7 @@ __device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t row
     __syncthreads();
     int total = 0, before = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         if (i < warp) before += marks.warp_sum[i];
         total += marks.warp_sum[i];
     }
@@ -1082,12 +1123,13 @@ __device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t row
 }
 
 // The marked rows number [from, to) of the window, at most kList, into list.
+template <int WARPS>
 __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_t rows, int from, int to, int *list) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
     __syncthreads();  // list is free
 #pragma unroll 4
-    for (int i = warp; i < words; i += kWarps) {
+    for (int i = warp; i < words; i += WARPS) {
         const uint32_t m = marks.bits[i];
         const int place = marks.before[i] + __popc(m & ((1u << lane) - 1));
         if ((m >> lane & 1) && place >= from && place < to) list[place - from] = (int)(w0 + i * 32 + lane);
@@ -1095,10 +1137,10 @@ __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_
     __syncthreads();
 }
 
-// A CTA takes one adapter and 256 columns, and a cluster along z shares the
+// A CTA takes one adapter and 128 columns, and a cluster along z shares the
 // adapter's rows (its sums meet through distributed shared memory, in order).
 // Rows go in groups of 64, on tcgen05: X's rows, gathered by index, are the
-// 64 x 256 operand as they lie (MN-major boxes of 64 columns); the fp32 S
+// 64 x 128 operand as they lie (MN-major boxes of 64 columns); the fp32 S
 // values' bf16 parts stand below one another in the 128 rows of the other
 // operand (three bands of RP rows; RP = 64: two, and the third part in an
 // operand tile of its own), so one product does all parts and the parts' rows
@@ -1109,20 +1151,25 @@ template <int RP>
 struct OuterShape {
     static constexpr int kTiles = RP == 64 ? 2 : 1;          // S operand tiles of 128 x 64
     static constexpr int kBands = RP == 64 ? 2 : 3;
-    static constexpr uint32_t kStage = 32768 + kTiles * 16384;
-    static constexpr int kStages = 2;
+    static constexpr int kRows = kBands * RP;                // operand rows (and TMEM lanes) that hold something
+    // The operand's other rows are whatever follows it: they make other lanes.
+    static constexpr uint32_t kOperand = RP == 64 ? 32768 : kRows * 128;
+    static constexpr uint32_t kStage = 16384 + kOperand;
+    static constexpr int kStages = RP == 16 ? 4 : RP == 32 ? 3 : 2;
+    static constexpr uint32_t kRing = kStages * kStage + (16384 * kTiles - kOperand);
     static constexpr int kPairs = RP / 8;                    // row pairs of S per thread and group
-    static constexpr int kPitch = 132;                       // fp32 of a 128-column piece of the result
-    static constexpr int kRows = kBands * RP;                // rows of it that hold something
-    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * 256 * 4;  // that piece, the whole sum
-    static constexpr size_t kSmem = (kResult > (size_t)kStages * kStage ? kResult : (size_t)kStages * kStage) + 1024;
+    static constexpr int kPitch = 132;                       // fp32 of a row of the result
+    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * 128 * 4;  // the parts, their sum
+    static constexpr size_t kSmem = (kResult > kRing ? kResult : kRing) + 1024;
 };
+constexpr int kOuterSegment = 4;  // groups summed in the tensor memory before registers take them (see kTcSegment)
 
 template <int RP, bool VEC>
-__global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constant__ OuterK k) {
+__global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_constant__ OuterK k) {
     pdl_wait();
     using Shape = OuterShape<RP>;
     constexpr int S = Shape::kStages, PAIRS = Shape::kPairs;
+    constexpr int AHEAD = S - 1;  // groups asked for early
     __shared__ int list[kList], abort_flag;
     __shared__ const bf16 *row_at[kList];  // the listed rows' first columns of this tile's block
     __shared__ Marks marks;
@@ -1136,8 +1183,8 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
     const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
-    const int bcols = (int)J.x.bcols, per_block = (bcols + 255) / 256, blk = tile / per_block;
-    const int c0 = (tile - blk * per_block) * 256;
+    const int bcols = (int)J.x.bcols, per_block = (bcols + 127) / 128, blk = tile / per_block;
+    const int c0 = (tile - blk * per_block) * 128;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const float *Sv = J.s;
     if (threadIdx.x == 0) {
@@ -1148,26 +1195,47 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
     if (warp == 0) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 256);
     if constexpr (Shape::kTiles == 2)  // the third part's tile adds zeros to the second's rows
         for (int i = threadIdx.x; i < S * 64 * 8; i += kThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / 512) * Shape::kStage + 32768 + 16384 + 8192 + (i % 512) * 16) =
+            *reinterpret_cast<uint4 *>(smem + (i / 512) * Shape::kStage + 16384 + 16384 + 8192 + (i % 512) * 16) =
                 make_uint4(0, 0, 0, 0);
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
     pdl_release();  // after the TMEM is held (see project_tc_kernel)
     const uint32_t tmem = tmem_at;
-    // This thread's piece of X: row `warp` + 8 i of a group, eight columns.
-    const int cx = c0 + lane * 8;
-    const uint32_t x_to = smem_at + (lane / 8) * 8192 + warp * 128 + (((lane & 7) ^ warp) * 16);
+    // This thread's piece of X: row 2 warp + lane / 16 + 16 i of a group, eight
+    // columns.
+    const int row0 = warp * 2 + lane / 16, piece_of = lane & 15, cx = c0 + piece_of * 8;
+    const uint32_t x_to = smem_at + (piece_of / 8) * 8192 + row0 * 128 + (((piece_of & 7) ^ (row0 & 7)) * 16);
     uint32_t fills = 0;  // groups taken so far; stage fills % S
     bool ok = true;
+    // The sums so far: TMEM lane 32 (warp % 4) + lane, columns 64 (warp / 4)..
+    const int quad = warp & 3, part = warp >> 2;
+    float acc[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+    // Adds segment q (fill `last` its last) from its buffer.
+    auto drain = [&](uint32_t q, uint32_t last) {
+        ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[last % S]), (last / S) & 1, &abort_flag, k.status) && ok;
+        __syncwarp();
+        shmm_tc::fence_after();
+        if (quad * 32 >= Shape::kRows) return;
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
+            float v[16];
+            shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + (q & 1) * 128 + part * 64 + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+        }
+        shmm_tc::fence_before();  // the barrier before the next product into this buffer follows
+    };
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-        const int total = mark_rows(k.ids, w0, k.rows, a, marks, k.status);
+        const int total = mark_rows<kWarps>(k.ids, w0, k.rows, a, marks, k.status);
         // this CTA's share of the rows, in whole groups of 64
         const int groups = (total + 63) / 64, lo = groups * cr / cs * 64;
         const int hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
         for (int l0 = lo; l0 < hi; l0 += kList) {
             const int have = hi - l0 < kList ? hi - l0 : kList, ngroups = (have + 63) / 64;
-            list_rows(marks, w0, k.rows, l0, l0 + have, list);
+            list_rows<kWarps>(marks, w0, k.rows, l0, l0 + have, list);
             for (int i = threadIdx.x; i < have; i += kThreads) {
                 const uint32_t t = list[i], b = t / (uint32_t)J.x.brows;
                 const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
@@ -1192,19 +1260,19 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
                 if (f >= S) ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[s]), (f / S - 1) & 1, &abort_flag, k.status) && ok;
                 const uint32_t at0 = s * Shape::kStage;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int at = grp * 64 + i * 8 + warp;
+                for (int i = 0; i < 4; ++i) {
+                    const int at = grp * 64 + i * 16 + row0;
                     const bf16 *row = at < have && cx < bcols ? row_at[at] : (const bf16 *)nullptr;
                     if constexpr (VEC) {
-                        queue16(x_to + at0 + i * 1024, row ? (const void *)(row + cx) : Sv, row != nullptr);
+                        queue16(x_to + at0 + i * 2048, row ? (const void *)(row + cx) : Sv, row != nullptr);
                     } else {
                         const Raw8 v = row ? load8<false>(row, cx, bcols) : Raw8{{0, 0, 0, 0}};
-                        *reinterpret_cast<uint4 *>(smem + (x_to - smem_at) + at0 + i * 1024) =
+                        *reinterpret_cast<uint4 *>(smem + (x_to - smem_at) + at0 + i * 2048) =
                             make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
                     }
                 }
                 queue_commit();
-                uint8_t *op = smem + at0 + 32768;
+                uint8_t *op = smem + at0 + 16384;
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
                     const int i = threadIdx.x + e * kThreads, r = i % RP, t = i / RP * 2;
@@ -1219,17 +1287,17 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
                 if (grp + 1 < ngroups) read_s(grp + 1);
             };
             read_s(0);
-            fill(0, fills);
+#pragma unroll 1
+            for (int g = 0; g < AHEAD; ++g) {
+                if (g < ngroups) fill(g, fills + g);
+                else queue_commit();
+            }
             for (int grp = 0; grp < ngroups; ++grp) {
-                if (grp + 1 < ngroups) {
-                    fill(grp + 1, fills + 1);
-                    queue_wait<1>();
-                } else {
-                    queue_wait<0>();
-                }
+                queue_wait<AHEAD - 1>();
                 shmm_tc::fence_async();
                 shmm_tc::fence_before();
                 __syncthreads();
+                const uint32_t q = fills / kOuterSegment;
                 if (threadIdx.x == 0) {
                     shmm_tc::fence_after();
                     const uint32_t at = smem_at + (fills % S) * Shape::kStage;
@@ -1237,22 +1305,31 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int i = 0; i < Shape::kTiles; ++i)
-                            shmm_tc::mma_issue(tmem, shmm_tc::operand(at + 32768 + i * 16384 + kk * 32, 16, 1024),
+                            shmm_tc::mma_issue(tmem + (q & 1) * 128,
+                                               shmm_tc::operand(at + 16384 + i * 16384 + kk * 32, 16, 1024),
                                                shmm_tc::operand(at + kk * 2048, 8192, 1024),
-                                               shmm_tc::instruction(256, true), fills > 0 || kk > 0 || i > 0);
+                                               shmm_tc::instruction(128, true),
+                                               fills % kOuterSegment > 0 || kk > 0 || i > 0);
                     shmm_tc::mma_commit(shmm_dev::smem_u32(&bars[fills % S]));
                 }
+                // Into the stage of the group before this one, whose products
+                // have had the wait above to end.
+                if (grp + AHEAD < ngroups) fill(grp + AHEAD, fills + AHEAD);
+                else queue_commit();
+                // The segment before this one, while its successor's first
+                // products run (they go into the other buffer).
+                if (fills % kOuterSegment == 0 && fills > 0) drain(q - 1, fills - 1);
                 ++fills;
             }
         }
     }
+    if (fills > 0) drain((fills - 1) / kOuterSegment, fills - 1);
     // Every product is done before its operands' memory is used again.
     for (uint32_t f = fills > S ? fills - S : 0; f < fills; ++f)
         shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[f % S]), (f / S) & 1, &abort_flag, k.status, false);
     __syncthreads();
-    shmm_tc::fence_after();
-    // Result: 128 columns at a time from TMEM through shared memory, the
-    // parts' rows added; whole in shared memory when the cluster shares it.
+    // Result through shared memory, the parts' rows added there; the cluster's
+    // sums then meet.
     const float scale = J.scale ? J.scale[a] : 1.0f;
     float *out = J.out + (int64_t)a * k.R * J.cols + (int64_t)blk * bcols + c0;
     const bool whole = (J.cols & 3) == 0 && (bcols & 3) == 0 && (reinterpret_cast<uintptr_t>(J.out) & 15) == 0;
@@ -1273,44 +1350,32 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
         }
     };
     float *piece = reinterpret_cast<float *>(smem);                // [kRows][kPitch]
-    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][256]
+    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][128]
     auto add = [](float4 &t, const float4 &v) {
         t.x += v.x;
         t.y += v.y;
         t.z += v.z;
         t.w += v.w;
     };
-#pragma unroll 1
-    for (int c = 0; c < 256; c += 128) {
-        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
-        if (quad * 32 < Shape::kRows) {
+    const int my_row = quad * 32 + lane;
+    if (my_row < Shape::kRows)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                float v[16];
-                const int at = half * 64 + h * 16;
-                if (fills) shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + c + at, v);
-                if (row < Shape::kRows)
+        for (int j = 0; j < 64; j += 4)
+            *reinterpret_cast<float4 *>(piece + my_row * Shape::kPitch + part * 64 + j) =
+                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < k.R * 32; e += kThreads) {
+        const int r = e / 32, j = e % 32 * 4;
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<float4 *>(piece + row * Shape::kPitch + at + j) =
-                            fills ? make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < k.R * 32; e += kThreads) {
-            const int r = e / 32, j = e % 32 * 4;
-            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int h = Shape::kBands - 1; h >= 0; --h)
-                add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
-            if (cs > 1) *reinterpret_cast<float4 *>(sums + r * 256 + c + j) = t;
-            else put(r, c + j, t);
-        }
-        __syncthreads();
+        for (int h = Shape::kBands - 1; h >= 0; --h)
+            add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
+        if (cs > 1) *reinterpret_cast<float4 *>(sums + r * 128 + j) = t;
+        else put(r, j, t);
     }
     if (cs > 1) {
         cluster.sync();
-        for (int e = cr * kThreads + threadIdx.x; e < k.R * 64; e += cs * kThreads) {
+        for (int e = cr * kThreads + threadIdx.x; e < k.R * 32; e += cs * kThreads) {
             float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int b = 0; b < 8; ++b)
@@ -1318,7 +1383,7 @@ __global__ void __launch_bounds__(kThreads) outer_tc_kernel(const __grid_constan
 #pragma unroll
             for (int b = 0; b < 8; ++b)
                 if (b < cs) add(t, v[b]);
-            put(e / 64, e % 64 * 4, t);
+            put(e / 32, e % 32 * 4, t);
         }
         cluster.sync();  // nobody leaves with what another CTA still reads
     }
@@ -1346,10 +1411,10 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-    const int total = mark_rows(k.ids, w0, k.rows, a, marks, k.status);
+    const int total = mark_rows<kWarps>(k.ids, w0, k.rows, a, marks, k.status);
     for (int l0 = 0; l0 < total; l0 += kList) {
         const int have = total - l0 < kList ? total - l0 : kList;
-        list_rows(marks, w0, k.rows, l0, l0 + have, list);
+        list_rows<kWarps>(marks, w0, k.rows, l0, l0 + have, list);
         for (int s0 = 0; s0 < have; s0 += 32) {
             const int s = s0 + half * 16;
             float x[16];
@@ -1524,7 +1589,7 @@ cudaError_t project_tc(const ProjK &k, int b0, cudaStream_t s) {
     t.status = k.status;
     const int64_t tiles = (int64_t)t.row_tiles * b0;
     int c, z;
-    spread(tiles, slots_for(kTcSmem), 1, t.chunks / 4, false, &c, &z);
+    spread(tiles, sms(), 1, t.chunks / 4, false, &c, &z);
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, c), dim3(1, c, 1), dim3(kTcThreads), kTcSmem, s, t);
 }
 
@@ -1621,8 +1686,8 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = k.job[0].tiles + k.job[1].tiles;
-    // Shares of an adapter's rows until the card is full (two CTAs per SM) or
-    // a share is down to four groups of rows.
+    // Shares of an adapter's rows until the card is full (two CTAs per SM) or a
+    // share is down to four groups of rows.
     int cs = 1;
     while (cs < 8 && tiles * k.n * cs * 2 <= 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
@@ -1641,7 +1706,7 @@ cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     bool vec = true;
     for (OuterJob &j : k.job) {
         if (!j.cols) continue;
-        j.tiles = (int)((j.x.bcols + 255) / 256 * j.x.b1);
+        j.tiles = (int)((j.x.bcols + 127) / 128 * j.x.b1);
         vec = vec && j.x.bcols % 8 == 0;
     }
     if (k.R <= 16) return vec ? outer_tc<16, true>(k, s) : outer_tc<16, false>(k, s);
