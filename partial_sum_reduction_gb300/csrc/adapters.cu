@@ -1077,36 +1077,54 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 // Rows of an adapter.  A CTA marks them in a bit mask over a window of
 // kWindow rows (one read of the row adapters), with how many lie before each
 // 32-row word, then turns the marks into lists of up to kList rows, ascending.
-constexpr int kWindow = 16384, kList = 512;
+constexpr int kWindow = 16384, kList = 1024;
 struct Marks {
     uint32_t bits[kWindow / 32];
     int before[kWindow / 32];
     int warp_sum[16];
 };
 
-// Marks the window's rows with adapter a; returns how many.  A warp takes
-// consecutive words.
+// Marks the window's rows with adapter a; returns how many.  A lane reads four
+// rows, eight lanes make a word, a warp 128 rows at a time; all of a warp's
+// rows of a window of 8 * 128 WARPS are asked for before any is looked at.
 template <int WARPS>
 __device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t rows, int a, Marks &marks, int *status) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int words = (int)((rows - w0 < kWindow ? rows - w0 : kWindow) + 31) / 32;
-    const int per = (words + WARPS - 1) / WARPS, first = warp * per, last = first + per < words ? first + per : words;
+    const int n = (int)(rows - w0 < kWindow ? rows - w0 : kWindow), words = (n + 31) / 32;
+    const int per = (words + 4 * WARPS - 1) / (4 * WARPS), first = warp * per;  // in units of 128 rows
+    const bool whole = (reinterpret_cast<uintptr_t>(ids + w0) & 15) == 0;
     int mine = 0;
-    for (int i0 = first; i0 < last; i0 += 8) {
-        int v[8];
+    for (int u0 = 0; u0 < per; u0 += 8) {
+        int4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t t = w0 + (int64_t)(i0 + i) * 32 + lane;
-            v[i] = i0 + i < last && t < rows && in_bounds(status, t, 1, rows) ? ids[t] : -1;
+        for (int u = 0; u < 8; ++u) {
+            const int t = (first + u0 + u) * 128 + lane * 4;
+            v[u] = make_int4(-1, -1, -1, -1);
+            if (u0 + u >= per || t >= n || !in_bounds(status, w0 + t, n - t < 4 ? n - t : 4, rows)) continue;
+            if (whole && t + 4 <= n) {
+                v[u] = *reinterpret_cast<const int4 *>(ids + w0 + t);
+            } else {
+                v[u].x = ids[w0 + t];
+                if (t + 1 < n) v[u].y = ids[w0 + t + 1];
+                if (t + 2 < n) v[u].z = ids[w0 + t + 2];
+                if (t + 3 < n) v[u].w = ids[w0 + t + 3];
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t m = __ballot_sync(0xffffffffu, v[i] == a);
-            if (lane == 0 && i0 + i < last) {
-                marks.bits[i0 + i] = m;
-                marks.before[i0 + i] = mine;  // of the warp's words
+        for (int u = 0; u < 8; ++u) {
+            if (u0 + u >= per) break;
+            uint32_t m = (uint32_t)((v[u].x == a) | (v[u].y == a) << 1 | (v[u].z == a) << 2 | (v[u].w == a) << 3)
+                         << (lane & 7) * 4;
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) m |= __shfl_xor_sync(0xffffffffu, m, o);
+            const int c0 = __popc(__shfl_sync(0xffffffffu, m, 0)), c1 = __popc(__shfl_sync(0xffffffffu, m, 8)),
+                      c2 = __popc(__shfl_sync(0xffffffffu, m, 16)), c3 = __popc(__shfl_sync(0xffffffffu, m, 24));
+            const int word = (first + u0 + u) * 4 + lane / 8;
+            if ((lane & 7) == 0 && word < words) {
+                marks.bits[word] = m;
+                marks.before[word] = mine + (lane > 0 ? c0 : 0) + (lane > 8 ? c1 : 0) + (lane > 16 ? c2 : 0);
             }
-            mine += __popc(m);
+            mine += c0 + c1 + c2 + c3;
         }
     }
     if (lane == 0) marks.warp_sum[warp] = mine;
@@ -1117,7 +1135,7 @@ __device__ __forceinline__ int mark_rows(const int *ids, int64_t w0, int64_t row
         if (i < warp) before += marks.warp_sum[i];
         total += marks.warp_sum[i];
     }
-    for (int i = first + lane; i < last; i += 32) marks.before[i] += before;
+    for (int i = first * 4 + lane; i < (first + per) * 4 && i < words; i += 32) marks.before[i] += before;
     __syncthreads();
     return total;
 }
@@ -1137,35 +1155,34 @@ __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_
     __syncthreads();
 }
 
-// A CTA takes one adapter and 128 columns, and a cluster along z shares the
+// A CTA takes one adapter and 256 columns, and a cluster along z shares the
 // adapter's rows (its sums meet through distributed shared memory, in order).
 // Rows go in groups of 64, on tcgen05: X's rows, gathered by index, are the
-// 64 x 128 operand as they lie (MN-major boxes of 64 columns); the fp32 S
+// 64 x 256 operand as they lie (MN-major boxes of 64 columns); the fp32 S
 // values' bf16 parts stand below one another in the 128 rows of the other
 // operand (three bands of RP rows; RP = 64: two, and the third part in an
 // operand tile of its own), so one product does all parts and the parts' rows
 // are added at the end.  The factor side, 3 RP columns, would be the bound of
 // warp matrix instructions at RP = 32 and above (about half their rate), and
 // its operands of their shared-memory reads.
+constexpr int kOuterThreads = 512, kOuterWarps = kOuterThreads / 32;  // one CTA per SM
 template <int RP>
 struct OuterShape {
     static constexpr int kTiles = RP == 64 ? 2 : 1;          // S operand tiles of 128 x 64
     static constexpr int kBands = RP == 64 ? 2 : 3;
     static constexpr int kRows = kBands * RP;                // operand rows (and TMEM lanes) that hold something
-    // The operand's other rows are whatever follows it: they make other lanes.
-    static constexpr uint32_t kOperand = RP == 64 ? 32768 : kRows * 128;
-    static constexpr uint32_t kStage = 16384 + kOperand;
-    static constexpr int kStages = RP == 16 ? 4 : RP == 32 ? 3 : 2;
-    static constexpr uint32_t kRing = kStages * kStage + (16384 * kTiles - kOperand);
-    static constexpr int kPairs = RP / 8;                    // row pairs of S per thread and group
-    static constexpr int kPitch = 132;                       // fp32 of a row of the result
-    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * 128 * 4;  // the parts, their sum
+    static constexpr uint32_t kStage = 32768 + kTiles * 16384;
+    static constexpr int kStages = RP == 64 ? 3 : 4;
+    static constexpr uint32_t kRing = kStages * kStage;
+    static constexpr int kPairs = RP / 16;                   // row pairs of S per thread and group
+    static constexpr int kPitch = 132;                       // fp32 of a 128-column piece of the result
+    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * 256 * 4;  // a piece, the whole sum
     static constexpr size_t kSmem = (kResult > kRing ? kResult : kRing) + 1024;
 };
 constexpr int kOuterSegment = 4;  // groups summed in the tensor memory before registers take them (see kTcSegment)
 
 template <int RP, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_constant__ OuterK k) {
+__global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_constant__ OuterK k) {
     pdl_wait();
     using Shape = OuterShape<RP>;
     constexpr int S = Shape::kStages, PAIRS = Shape::kPairs;
@@ -1183,8 +1200,8 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
     const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
-    const int bcols = (int)J.x.bcols, per_block = (bcols + 127) / 128, blk = tile / per_block;
-    const int c0 = (tile - blk * per_block) * 128;
+    const int bcols = (int)J.x.bcols, per_block = (bcols + 255) / 256, blk = tile / per_block;
+    const int c0 = (tile - blk * per_block) * 256;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const float *Sv = J.s;
     if (threadIdx.x == 0) {
@@ -1192,20 +1209,19 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 256);
+    if (warp == 0) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 512);
     if constexpr (Shape::kTiles == 2)  // the third part's tile adds zeros to the second's rows
-        for (int i = threadIdx.x; i < S * 64 * 8; i += kThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / 512) * Shape::kStage + 16384 + 16384 + 8192 + (i % 512) * 16) =
+        for (int i = threadIdx.x; i < S * 64 * 8; i += kOuterThreads)
+            *reinterpret_cast<uint4 *>(smem + (i / 512) * Shape::kStage + 32768 + 16384 + 8192 + (i % 512) * 16) =
                 make_uint4(0, 0, 0, 0);
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
     pdl_release();  // after the TMEM is held (see project_tc_kernel)
     const uint32_t tmem = tmem_at;
-    // This thread's piece of X: row 2 warp + lane / 16 + 16 i of a group, eight
-    // columns.
-    const int row0 = warp * 2 + lane / 16, piece_of = lane & 15, cx = c0 + piece_of * 8;
-    const uint32_t x_to = smem_at + (piece_of / 8) * 8192 + row0 * 128 + (((piece_of & 7) ^ (row0 & 7)) * 16);
+    // This thread's piece of X: row `warp` + 16 i of a group, eight columns.
+    const int cx = c0 + lane * 8;
+    const uint32_t x_to = smem_at + (lane / 8) * 8192 + warp * 128 + (((lane & 7) ^ (warp & 7)) * 16);
     uint32_t fills = 0;  // groups taken so far; stage fills % S
     bool ok = true;
     // The sums so far: TMEM lane 32 (warp % 4) + lane, columns 64 (warp / 4)..
@@ -1222,21 +1238,21 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < 64; c += 16) {
             float v[16];
-            shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + (q & 1) * 128 + part * 64 + c, v);
+            shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + (q & 1) * 256 + part * 64 + c, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
         }
         shmm_tc::fence_before();  // the barrier before the next product into this buffer follows
     };
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-        const int total = mark_rows<kWarps>(k.ids, w0, k.rows, a, marks, k.status);
+        const int total = mark_rows<kOuterWarps>(k.ids, w0, k.rows, a, marks, k.status);
         // this CTA's share of the rows, in whole groups of 64
         const int groups = (total + 63) / 64, lo = groups * cr / cs * 64;
         const int hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
         for (int l0 = lo; l0 < hi; l0 += kList) {
             const int have = hi - l0 < kList ? hi - l0 : kList, ngroups = (have + 63) / 64;
-            list_rows<kWarps>(marks, w0, k.rows, l0, l0 + have, list);
-            for (int i = threadIdx.x; i < have; i += kThreads) {
+            list_rows<kOuterWarps>(marks, w0, k.rows, l0, l0 + have, list);
+            for (int i = threadIdx.x; i < have; i += kOuterThreads) {
                 const uint32_t t = list[i], b = t / (uint32_t)J.x.brows;
                 const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
                 row_at[i] = in_bounds(k.status, off, bcols, J.x.brows * J.x.bcols)
@@ -1244,24 +1260,23 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
                                 : (const bf16 *)nullptr;
             }
             __syncthreads();
-            float2 sv[PAIRS];
-            auto read_s = [&](int grp) {
+            auto read_s = [&](int grp, float2 *sv) {  // this thread's row pairs of a group's S
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
-                    const int i = threadIdx.x + e * kThreads, r = i % RP, at = grp * 64 + i / RP * 2;
+                    const int i = threadIdx.x + e * kOuterThreads, r = i % RP, at = grp * 64 + i / RP * 2;
                     sv[e].x = r < k.R && at < have ? Sv[(int64_t)list[at] * k.R + r] : 0.0f;
                     sv[e].y = r < k.R && at + 1 < have ? Sv[(int64_t)list[at + 1] * k.R + r] : 0.0f;
                 }
             };
-            // Asks for group grp's X and writes its S parts, into the stage
-            // of fill f once that stage's products are done.
-            auto fill = [&](int grp, uint32_t f) {
+            // Asks for group grp's X, into the stage of fill f once that
+            // stage's products are done.
+            auto ask = [&](int grp, uint32_t f) {
                 const uint32_t s = f % S;
                 if (f >= S) ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[s]), (f / S - 1) & 1, &abort_flag, k.status) && ok;
                 const uint32_t at0 = s * Shape::kStage;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int at = grp * 64 + i * 16 + row0;
+                    const int at = grp * 64 + i * 16 + warp;
                     const bf16 *row = at < have && cx < bcols ? row_at[at] : (const bf16 *)nullptr;
                     if constexpr (VEC) {
                         queue16(x_to + at0 + i * 2048, row ? (const void *)(row + cx) : Sv, row != nullptr);
@@ -1272,10 +1287,13 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
                     }
                 }
                 queue_commit();
-                uint8_t *op = smem + at0 + 16384;
+            };
+            // The parts of a group's S into the same stage.
+            auto put_s = [&](uint32_t f, const float2 *sv) {
+                uint8_t *op = smem + (f % S) * Shape::kStage + 32768;
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
-                    const int i = threadIdx.x + e * kThreads, r = i % RP, t = i / RP * 2;
+                    const int i = threadIdx.x + e * kOuterThreads, r = i % RP, t = i / RP * 2;
                     uint32_t p[3];
                     split<3>(sv[e].x, sv[e].y, p);
 #pragma unroll
@@ -1284,13 +1302,23 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
                         *reinterpret_cast<uint32_t *>(op + m * 128 + (((t >> 3) ^ (m & 7)) * 16) + (t & 7) * 2) = p[h];
                     }
                 }
-                if (grp + 1 < ngroups) read_s(grp + 1);
             };
-            read_s(0);
-#pragma unroll 1
-            for (int g = 0; g < AHEAD; ++g) {
-                if (g < ngroups) fill(g, fills + g);
-                else queue_commit();
+            float2 sv[PAIRS];
+            {
+                float2 first[AHEAD][PAIRS];
+#pragma unroll
+                for (int g = 0; g < AHEAD; ++g) {
+                    if (g < ngroups) {
+                        read_s(g, first[g]);
+                        ask(g, fills + g);
+                    } else {
+                        queue_commit();
+                    }
+                }
+                if (AHEAD < ngroups) read_s(AHEAD, sv);
+#pragma unroll
+                for (int g = 0; g < AHEAD; ++g)
+                    if (g < ngroups) put_s(fills + g, first[g]);
             }
             for (int grp = 0; grp < ngroups; ++grp) {
                 queue_wait<AHEAD - 1>();
@@ -1305,17 +1333,22 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int i = 0; i < Shape::kTiles; ++i)
-                            shmm_tc::mma_issue(tmem + (q & 1) * 128,
-                                               shmm_tc::operand(at + 16384 + i * 16384 + kk * 32, 16, 1024),
+                            shmm_tc::mma_issue(tmem + (q & 1) * 256,
+                                               shmm_tc::operand(at + 32768 + i * 16384 + kk * 32, 16, 1024),
                                                shmm_tc::operand(at + kk * 2048, 8192, 1024),
-                                               shmm_tc::instruction(128, true),
+                                               shmm_tc::instruction(256, true),
                                                fills % kOuterSegment > 0 || kk > 0 || i > 0);
                     shmm_tc::mma_commit(shmm_dev::smem_u32(&bars[fills % S]));
                 }
                 // Into the stage of the group before this one, whose products
                 // have had the wait above to end.
-                if (grp + AHEAD < ngroups) fill(grp + AHEAD, fills + AHEAD);
-                else queue_commit();
+                if (grp + AHEAD < ngroups) {
+                    ask(grp + AHEAD, fills + AHEAD);
+                    put_s(fills + AHEAD, sv);
+                    if (grp + AHEAD + 1 < ngroups) read_s(grp + AHEAD + 1, sv);
+                } else {
+                    queue_commit();
+                }
                 // The segment before this one, while its successor's first
                 // products run (they go into the other buffer).
                 if (fills % kOuterSegment == 0 && fills > 0) drain(q - 1, fills - 1);
@@ -1350,7 +1383,7 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
         }
     };
     float *piece = reinterpret_cast<float *>(smem);                // [kRows][kPitch]
-    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][128]
+    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][256]
     auto add = [](float4 &t, const float4 &v) {
         t.x += v.x;
         t.y += v.y;
@@ -1358,24 +1391,28 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
         t.w += v.w;
     };
     const int my_row = quad * 32 + lane;
-    if (my_row < Shape::kRows)
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 128) {
+        if (part / 2 == c / 128 && my_row < Shape::kRows)
 #pragma unroll
-        for (int j = 0; j < 64; j += 4)
-            *reinterpret_cast<float4 *>(piece + my_row * Shape::kPitch + part * 64 + j) =
-                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-    __syncthreads();
-    for (int e = threadIdx.x; e < k.R * 32; e += kThreads) {
-        const int r = e / 32, j = e % 32 * 4;
-        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j = 0; j < 64; j += 4)
+                *reinterpret_cast<float4 *>(piece + my_row * Shape::kPitch + (part & 1) * 64 + j) =
+                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        __syncthreads();
+        for (int e = threadIdx.x; e < k.R * 32; e += kOuterThreads) {
+            const int r = e / 32, j = e % 32 * 4;
+            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int h = Shape::kBands - 1; h >= 0; --h)
-            add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
-        if (cs > 1) *reinterpret_cast<float4 *>(sums + r * 128 + j) = t;
-        else put(r, j, t);
+            for (int h = Shape::kBands - 1; h >= 0; --h)
+                add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
+            if (cs > 1) *reinterpret_cast<float4 *>(sums + r * 256 + c + j) = t;
+            else put(r, c + j, t);
+        }
+        __syncthreads();
     }
     if (cs > 1) {
         cluster.sync();
-        for (int e = cr * kThreads + threadIdx.x; e < k.R * 32; e += cs * kThreads) {
+        for (int e = cr * kOuterThreads + threadIdx.x; e < k.R * 64; e += cs * kOuterThreads) {
             float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int b = 0; b < 8; ++b)
@@ -1383,14 +1420,14 @@ __global__ void __launch_bounds__(kThreads, 2) outer_tc_kernel(const __grid_cons
 #pragma unroll
             for (int b = 0; b < 8; ++b)
                 if (b < cs) add(t, v[b]);
-            put(e / 32, e % 32 * 4, t);
+            put(e / 64, e % 64 * 4, t);
         }
         cluster.sync();  // nobody leaves with what another CTA still reads
     }
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
-    if (warp == 0) shmm_tc::tmem_free(tmem, 256);
+    if (warp == 0) shmm_tc::tmem_free(tmem, 512);
 }
 
 // Any types, on CUDA cores: one adapter, 128 columns and 16 adapter rows per
@@ -1686,11 +1723,11 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = k.job[0].tiles + k.job[1].tiles;
-    // Shares of an adapter's rows until the card is full (two CTAs per SM) or a
-    // share is down to four groups of rows.
+    // Shares of an adapter's rows until the card is full or a share is down to
+    // four groups of rows.
     int cs = 1;
     while (cs < 8 && tiles * k.n * cs * 2 <= 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
-    return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kThreads),
+    return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kOuterThreads),
                               Shape::kSmem, s, k);
 }
 
@@ -1706,7 +1743,7 @@ cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     bool vec = true;
     for (OuterJob &j : k.job) {
         if (!j.cols) continue;
-        j.tiles = (int)((j.x.bcols + 127) / 128 * j.x.b1);
+        j.tiles = (int)((j.x.bcols + 255) / 256 * j.x.b1);
         vec = vec && j.x.bcols % 8 == 0;
     }
     if (k.R <= 16) return vec ? outer_tc<16, true>(k, s) : outer_tc<16, false>(k, s);
