@@ -103,6 +103,7 @@ struct ExpandK {
 struct OuterJob {
     Blocks x;
     const float *s;       // [rows][R]
+    const bf16 *parts;    // s by adapter, in parts: [rows][3 RP] (see arrange_kernel)
     const float *scale;   // or NULL
     float *out;           // [n][R][cols]
     int64_t cols;
@@ -110,7 +111,17 @@ struct OuterJob {
 };
 struct OuterK {
     OuterJob job[2];
+    const int *order;     // [rows]: the rows with an adapter, by adapter, each one's ascending
+    const int *start;     // [n + 1]: adapter a's are order[start[a]] .. order[start[a + 1] - 1]
+    int n, R;
+    int64_t rows;
+    int *status;
+};
+struct ArrangeK {
     const int *ids;
+    const float *s[2];    // either may be NULL
+    bf16 *parts[2];
+    int *order, *start;
     int n, R;
     int64_t rows;
     int *status;
@@ -510,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
             // rows.  An instruction takes some 130 cycles however narrow it
             // is, so one for all of them, not one each.
             const uint64_t base = shmm_tc::operand(tiles_at, 16, 1024);
-            const uint32_t idesc = shmm_tc::instruction(na * RP, false);
+            const uint32_t idesc = shmm_tc::instruction(na * RP, false, false);
             int left = 0;  // chunks of the segment still to come
             for (int ch = lo; ch < hi; ++ch) {
                 const uint32_t buf = uses & 1;
@@ -1155,41 +1166,104 @@ __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_
     __syncthreads();
 }
 
-// A CTA takes one adapter and 256 columns, and a cluster along z shares the
+// Sorts the rows by adapter for the kernels that sum over an adapter's rows,
+// and lays their low-rank values down in that order as those kernels' operand:
+// three bf16 parts of RP values each (zeros past R), per row.  A CTA takes one
+// adapter, and CTAs along y share its rows; every CTA counts for itself, from
+// the ids alone, so that they need nothing of one another.
+template <int RP>
+__global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ ArrangeK k) {
+    pdl_enter();
+    __shared__ Marks marks;
+    __shared__ int list[kList], sum[16];
+    const int a = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    // rows of the adapters below this one: where its own begin
+    int below = 0;
+    if (a > 0) {
+        const int64_t n4 = (reinterpret_cast<uintptr_t>(k.ids) & 15) ? 0 : k.rows / 4;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < n4; i += 512) {
+            const int4 v = in_bounds(k.status, i * 4, 4, k.rows) ? reinterpret_cast<const int4 *>(k.ids)[i] : make_int4(a, a, a, a);
+            below += ((unsigned)v.x < (unsigned)a) + ((unsigned)v.y < (unsigned)a) + ((unsigned)v.z < (unsigned)a) +
+                     ((unsigned)v.w < (unsigned)a);
+        }
+        for (int64_t i = n4 * 4 + threadIdx.x; i < k.rows; i += 512) below += (unsigned)k.ids[i] < (unsigned)a;
+        below = __reduce_add_sync(0xffffffffu, below);
+    }
+    if (lane == 0) sum[warp] = below;
+    __syncthreads();
+    below = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) below += sum[i];
+    int at = below;  // place of the window's first row
+    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
+        const int total = mark_rows<16>(k.ids, w0, k.rows, a, marks, k.status);
+        const int lo = (int)((int64_t)total * blockIdx.y / gridDim.y), hi = (int)((int64_t)total * (blockIdx.y + 1) / gridDim.y);
+        for (int l0 = lo; l0 < hi; l0 += kList) {
+            const int have = hi - l0 < kList ? hi - l0 : kList;
+            list_rows<16>(marks, w0, k.rows, l0, l0 + have, list);
+            for (int i = threadIdx.x; i < have; i += 512)
+                if (in_bounds(k.status, at + l0 + i, 1, k.rows)) k.order[at + l0 + i] = list[i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (!k.s[j]) continue;
+#pragma unroll 2
+                for (int e = threadIdx.x; e < have * (RP / 2); e += 512) {
+                    const int i = e / (RP / 2), r = e % (RP / 2) * 2;
+                    const float *v = k.s[j] + (int64_t)list[i] * k.R;
+                    uint32_t p[3];
+                    split<3>(r < k.R ? v[r] : 0.0f, r + 1 < k.R ? v[r + 1] : 0.0f, p);
+                    const int64_t to = ((int64_t)at + l0 + i) * (3 * RP) + r;
+                    if (!in_bounds(k.status, to, 2 * RP + 2, k.rows * 3 * RP)) continue;
+#pragma unroll
+                    for (int h = 0; h < 3; ++h) *reinterpret_cast<uint32_t *>(k.parts[j] + to + h * RP) = p[h];
+                }
+            }
+        }
+        at += total;
+    }
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        k.start[a] = below;
+        if (a == k.n - 1) k.start[k.n] = at;
+    }
+}
+
+// A CTA takes one adapter and 128 columns, and a cluster along z shares the
 // adapter's rows (its sums meet through distributed shared memory, in order).
-// Rows go in groups of 64, on tcgen05: X's rows, gathered by index, are the
-// 64 x 256 operand as they lie (MN-major boxes of 64 columns); the fp32 S
-// values' bf16 parts stand below one another in the 128 rows of the other
-// operand (three bands of RP rows; RP = 64: two, and the third part in an
-// operand tile of its own), so one product does all parts and the parts' rows
-// are added at the end.  The factor side, 3 RP columns, would be the bound of
-// warp matrix instructions at RP = 32 and above (about half their rate), and
-// its operands of their shared-memory reads.
-constexpr int kOuterThreads = 512, kOuterWarps = kOuterThreads / 32;  // one CTA per SM
+// Rows go in groups of 64, on tcgen05.  Both operands are MN-major, as their
+// rows lie in memory: X's, gathered by index, 64 x 128; and the arranged low
+// values', whose three parts stand beside one another, 64 x 3 RP, so that one
+// product of 128 rows does all parts (RP = 64: a second one the third) and the
+// parts' rows are added at the end.  The factor side, 3 RP columns, would be
+// the bound of warp matrix instructions at RP = 32 and above (about half their
+// rate), and its operands of their shared-memory reads.
+constexpr int kOuterThreads = 256, kOuterCols = 128;  // two CTAs per SM
 template <int RP>
 struct OuterShape {
-    static constexpr int kTiles = RP == 64 ? 2 : 1;          // S operand tiles of 128 x 64
-    static constexpr int kBands = RP == 64 ? 2 : 3;
-    static constexpr int kRows = kBands * RP;                // operand rows (and TMEM lanes) that hold something
-    static constexpr uint32_t kStage = 32768 + kTiles * 16384;
-    static constexpr int kStages = RP == 64 ? 3 : 4;
+    static constexpr int kWidth = 3 * RP;                    // parts of a row
+    static constexpr int kBoxes = (kWidth + 63) / 64;        // 64 x 64 boxes of them
+    static constexpr int kRows = RP == 64 ? 128 : kWidth;    // TMEM lanes that hold something
+    static constexpr int kBands = kRows / RP;
+    static constexpr uint32_t kX = kBoxes * 8192;            // X's place in a stage, behind them
+    static constexpr uint32_t kStage = kX + 16384;
+    static constexpr int kStages = RP == 16 ? 4 : RP == 32 ? 3 : 2;
     static constexpr uint32_t kRing = kStages * kStage;
-    static constexpr int kPairs = RP / 16;                   // row pairs of S per thread and group
-    static constexpr int kPitch = 132;                       // fp32 of a 128-column piece of the result
-    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * 256 * 4;  // a piece, the whole sum
-    static constexpr size_t kSmem = (kResult > kRing ? kResult : kRing) + 1024;
+    static constexpr uint32_t kZeros = RP == 64 ? 8192 : 0;  // the lower half of the third part's product
+    static constexpr int kPitch = 132;                       // fp32
+    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * kOuterCols * 4;  // product, sum
+    static constexpr size_t kSmem = (kResult > kRing + kZeros ? kResult : kRing + kZeros) + 1024;
 };
 constexpr int kOuterSegment = 4;  // groups summed in the tensor memory before registers take them (see kTcSegment)
+constexpr int kOuterList = 1024;  // row addresses at hand: 16 groups, half of them ahead
 
 template <int RP, bool VEC>
-__global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_constant__ OuterK k) {
+__global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid_constant__ OuterK k) {
     pdl_wait();
     using Shape = OuterShape<RP>;
-    constexpr int S = Shape::kStages, PAIRS = Shape::kPairs;
+    constexpr int S = Shape::kStages;
     constexpr int AHEAD = S - 1;  // groups asked for early
-    __shared__ int list[kList], abort_flag;
-    __shared__ const bf16 *row_at[kList];  // the listed rows' first columns of this tile's block
-    __shared__ Marks marks;
+    __shared__ int abort_flag;
+    __shared__ const bf16 *row_at[kOuterList];  // rows' first values of this tile's block, by place in the share
     __shared__ uint32_t tmem_at;
     __shared__ __align__(8) uint64_t bars[S];  // a stage's products are done
     extern __shared__ uint8_t raw_smem[];
@@ -1200,36 +1274,54 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_co
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
     const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
-    const int bcols = (int)J.x.bcols, per_block = (bcols + 255) / 256, blk = tile / per_block;
-    const int c0 = (tile - blk * per_block) * 256;
+    const int bcols = (int)J.x.bcols, per_block = (bcols + kOuterCols - 1) / kOuterCols, blk = tile / per_block;
+    const int c0 = (tile - blk * per_block) * kOuterCols;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const float *Sv = J.s;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) shmm_dev::mbar_init(shmm_dev::smem_u32(&bars[i]), 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 512);
-    if constexpr (Shape::kTiles == 2)  // the third part's tile adds zeros to the second's rows
-        for (int i = threadIdx.x; i < S * 64 * 8; i += kOuterThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / 512) * Shape::kStage + 32768 + 16384 + 8192 + (i % 512) * 16) =
-                make_uint4(0, 0, 0, 0);
+    if (warp == 0) shmm_tc::tmem_alloc(shmm_dev::smem_u32(&tmem_at), 2 * kOuterCols);
+    if constexpr (Shape::kZeros > 0)
+        for (int i = threadIdx.x; i < (int)Shape::kZeros / 16; i += kOuterThreads)
+            *reinterpret_cast<uint4 *>(smem + Shape::kRing + i * 16) = make_uint4(0, 0, 0, 0);
+    // This CTA's share of the adapter's rows, in whole groups of 64.
+    const int first = k.start[a], total = k.start[a + 1] - first, groups = (total + 63) / 64;
+    const int lo = (int)((int64_t)groups * cr / cs) * 64, end = (int)((int64_t)groups * (cr + 1) / cs) * 64;
+    const int have = (end < total ? end : total) - lo, ngroups = (have + 63) / 64;
+    const int *order = k.order + first + lo;
+    const bf16 *parts = J.parts + (int64_t)(first + lo) * Shape::kWidth;
+    auto find_rows = [&](int i0) {  // the addresses of 512 rows from i0 on
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u * kOuterThreads + threadIdx.x;
+            if (i >= have) continue;
+            const uint32_t t = in_bounds(k.status, first + lo + i, 1, k.rows) ? order[i] : 0, b = t / (uint32_t)J.x.brows;
+            const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
+            row_at[i % kOuterList] = in_bounds(k.status, off, bcols, J.x.brows * J.x.bcols)
+                                         ? (const bf16 *)J.x.at[b * J.x.b1 + blk] + off
+                                         : (const bf16 *)nullptr;
+        }
+    };
+    find_rows(0);
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
     pdl_release();  // after the TMEM is held (see project_tc_kernel)
     const uint32_t tmem = tmem_at;
-    // This thread's piece of X: row `warp` + 16 i of a group, eight columns.
-    const int cx = c0 + lane * 8;
-    const uint32_t x_to = smem_at + (lane / 8) * 8192 + warp * 128 + (((lane & 7) ^ (warp & 7)) * 16);
-    uint32_t fills = 0;  // groups taken so far; stage fills % S
+    // This thread's pieces of a group: of X, eight columns of the rows xr + 16 i;
+    // of the parts, every fourth eight of row pr.
+    const int xr = threadIdx.x / 16, cx = c0 + (threadIdx.x & 15) * 8;
+    const uint32_t x_to = Shape::kX + (threadIdx.x & 15) / 8 * 8192 + xr * 128 + (((threadIdx.x & 7) ^ (xr & 7)) * 16);
+    const int pr = threadIdx.x / 4, pc = threadIdx.x & 3;
     bool ok = true;
     // The sums so far: TMEM lane 32 (warp % 4) + lane, columns 64 (warp / 4)..
     const int quad = warp & 3, part = warp >> 2;
     float acc[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-    // Adds segment q (fill `last` its last) from its buffer.
+    // Adds segment q (group `last` its last) from its buffer.
     auto drain = [&](uint32_t q, uint32_t last) {
         ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[last % S]), (last / S) & 1, &abort_flag, k.status) && ok;
         __syncwarp();
@@ -1238,127 +1330,76 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_co
 #pragma unroll
         for (int c = 0; c < 64; c += 16) {
             float v[16];
-            shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + (q & 1) * 256 + part * 64 + c, v);
+            shmm_tc::tmem_read16(tmem + ((uint32_t)(quad * 32) << 16) + (q & 1) * kOuterCols + part * 64 + c, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
         }
         shmm_tc::fence_before();  // the barrier before the next product into this buffer follows
     };
-    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-        const int total = mark_rows<kOuterWarps>(k.ids, w0, k.rows, a, marks, k.status);
-        // this CTA's share of the rows, in whole groups of 64
-        const int groups = (total + 63) / 64, lo = groups * cr / cs * 64;
-        const int hi = groups * (cr + 1) / cs * 64 < total ? groups * (cr + 1) / cs * 64 : total;
-        for (int l0 = lo; l0 < hi; l0 += kList) {
-            const int have = hi - l0 < kList ? hi - l0 : kList, ngroups = (have + 63) / 64;
-            list_rows<kOuterWarps>(marks, w0, k.rows, l0, l0 + have, list);
-            for (int i = threadIdx.x; i < have; i += kOuterThreads) {
-                const uint32_t t = list[i], b = t / (uint32_t)J.x.brows;
-                const int64_t off = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols;
-                row_at[i] = in_bounds(k.status, off, bcols, J.x.brows * J.x.bcols)
-                                ? (const bf16 *)J.x.at[b * J.x.b1 + blk] + off
-                                : (const bf16 *)nullptr;
-            }
-            __syncthreads();
-            auto read_s = [&](int grp, float2 *sv) {  // this thread's row pairs of a group's S
+    // Asks for group f, once the products of the stage's last one are done.
+    auto ask = [&](uint32_t f) {
+        const uint32_t s = f % S;
+        if (f >= S) ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[s]), (f / S - 1) & 1, &abort_flag, k.status) && ok;
+        const uint32_t at0 = s * Shape::kStage;
 #pragma unroll
-                for (int e = 0; e < PAIRS; ++e) {
-                    const int i = threadIdx.x + e * kOuterThreads, r = i % RP, at = grp * 64 + i / RP * 2;
-                    sv[e].x = r < k.R && at < have ? Sv[(int64_t)list[at] * k.R + r] : 0.0f;
-                    sv[e].y = r < k.R && at + 1 < have ? Sv[(int64_t)list[at + 1] * k.R + r] : 0.0f;
-                }
-            };
-            // Asks for group grp's X, into the stage of fill f once that
-            // stage's products are done.
-            auto ask = [&](int grp, uint32_t f) {
-                const uint32_t s = f % S;
-                if (f >= S) ok = shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[s]), (f / S - 1) & 1, &abort_flag, k.status) && ok;
-                const uint32_t at0 = s * Shape::kStage;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = grp * 64 + i * 16 + warp;
-                    const bf16 *row = at < have && cx < bcols ? row_at[at] : (const bf16 *)nullptr;
-                    if constexpr (VEC) {
-                        queue16(x_to + at0 + i * 2048, row ? (const void *)(row + cx) : Sv, row != nullptr);
-                    } else {
-                        const Raw8 v = row ? load8<false>(row, cx, bcols) : Raw8{{0, 0, 0, 0}};
-                        *reinterpret_cast<uint4 *>(smem + (x_to - smem_at) + at0 + i * 2048) =
-                            make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-                    }
-                }
-                queue_commit();
-            };
-            // The parts of a group's S into the same stage.
-            auto put_s = [&](uint32_t f, const float2 *sv) {
-                uint8_t *op = smem + (f % S) * Shape::kStage + 32768;
-#pragma unroll
-                for (int e = 0; e < PAIRS; ++e) {
-                    const int i = threadIdx.x + e * kOuterThreads, r = i % RP, t = i / RP * 2;
-                    uint32_t p[3];
-                    split<3>(sv[e].x, sv[e].y, p);
-#pragma unroll
-                    for (int h = 0; h < 3; ++h) {
-                        const int m = RP == 64 && h == 2 ? r + 128 : h * RP + r;  // row 128: the second tile's first
-                        *reinterpret_cast<uint32_t *>(op + m * 128 + (((t >> 3) ^ (m & 7)) * 16) + (t & 7) * 2) = p[h];
-                    }
-                }
-            };
-            float2 sv[PAIRS];
-            {
-                float2 first[AHEAD][PAIRS];
-#pragma unroll
-                for (int g = 0; g < AHEAD; ++g) {
-                    if (g < ngroups) {
-                        read_s(g, first[g]);
-                        ask(g, fills + g);
-                    } else {
-                        queue_commit();
-                    }
-                }
-                if (AHEAD < ngroups) read_s(AHEAD, sv);
-#pragma unroll
-                for (int g = 0; g < AHEAD; ++g)
-                    if (g < ngroups) put_s(fills + g, first[g]);
-            }
-            for (int grp = 0; grp < ngroups; ++grp) {
-                queue_wait<AHEAD - 1>();
-                shmm_tc::fence_async();
-                shmm_tc::fence_before();
-                __syncthreads();
-                const uint32_t q = fills / kOuterSegment;
-                if (threadIdx.x == 0) {
-                    shmm_tc::fence_after();
-                    const uint32_t at = smem_at + (fills % S) * Shape::kStage;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                        for (int i = 0; i < Shape::kTiles; ++i)
-                            shmm_tc::mma_issue(tmem + (q & 1) * 256,
-                                               shmm_tc::operand(at + 32768 + i * 16384 + kk * 32, 16, 1024),
-                                               shmm_tc::operand(at + kk * 2048, 8192, 1024),
-                                               shmm_tc::instruction(256, true),
-                                               fills % kOuterSegment > 0 || kk > 0 || i > 0);
-                    shmm_tc::mma_commit(shmm_dev::smem_u32(&bars[fills % S]));
-                }
-                // Into the stage of the group before this one, whose products
-                // have had the wait above to end.
-                if (grp + AHEAD < ngroups) {
-                    ask(grp + AHEAD, fills + AHEAD);
-                    put_s(fills + AHEAD, sv);
-                    if (grp + AHEAD + 1 < ngroups) read_s(grp + AHEAD + 1, sv);
-                } else {
-                    queue_commit();
-                }
-                // The segment before this one, while its successor's first
-                // products run (they go into the other buffer).
-                if (fills % kOuterSegment == 0 && fills > 0) drain(q - 1, fills - 1);
-                ++fills;
+        for (int i = 0; i < 4; ++i) {
+            const int at = f * 64 + i * 16 + xr;
+            const bf16 *row = at < have && cx < bcols ? row_at[at % kOuterList] : (const bf16 *)nullptr;
+            if constexpr (VEC) {
+                queue16(smem_at + x_to + at0 + i * 2048, row ? (const void *)(row + cx) : parts, row != nullptr);
+            } else {
+                const Raw8 v = row ? load8<false>(row, cx, bcols) : Raw8{{0, 0, 0, 0}};
+                *reinterpret_cast<uint4 *>(smem + x_to + at0 + i * 2048) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
             }
         }
+        const bool real = (int)f * 64 + pr < have;
+        const bf16 *from = parts + (int64_t)(real ? f * 64 + pr : 0) * Shape::kWidth + pc * 8;
+#pragma unroll
+        for (int i = 0; i < (Shape::kWidth + 31) / 32; ++i) {
+            const int c = pc + 4 * i;
+            if (c < Shape::kWidth / 8)
+                queue16(smem_at + at0 + (c / 8) * 8192 + pr * 128 + (((c & 7) ^ (pr & 7)) * 16), from + i * 32, real);
+        }
+        queue_commit();
+    };
+#pragma unroll 1
+    for (int f = 0; f < AHEAD; ++f) {
+        if (f < ngroups) ask(f);
+        else queue_commit();
     }
-    if (fills > 0) drain((fills - 1) / kOuterSegment, fills - 1);
+    for (int f = 0; f < ngroups; ++f) {
+        queue_wait<AHEAD - 1>();
+        shmm_tc::fence_async();
+        shmm_tc::fence_before();
+        __syncthreads();
+        const uint32_t q = f / kOuterSegment;
+        if (threadIdx.x == 0) {
+            shmm_tc::fence_after();
+            const uint32_t at = smem_at + (f % S) * Shape::kStage, zeros = smem_at + Shape::kRing;  // RP = 64
+            constexpr uint32_t idesc = shmm_tc::instruction(kOuterCols, true, true);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t x = shmm_tc::operand(at + Shape::kX + kk * 2048, 8192, 1024);
+                // RP = 16 has one box: X's first one fills the 64 rows that nobody reads
+                shmm_tc::mma_issue(tmem + (q & 1) * kOuterCols, shmm_tc::operand(at + kk * 2048, 8192, 1024), x, idesc,
+                                   f % kOuterSegment > 0 || kk > 0);
+                if constexpr (RP == 64)
+                    shmm_tc::mma_issue(tmem + (q & 1) * kOuterCols,
+                                       shmm_tc::operand(at + 16384 + kk * 2048, zeros - at - 16384 - kk * 2048, 1024), x,
+                                       idesc, true);
+            }
+            shmm_tc::mma_commit(shmm_dev::smem_u32(&bars[f % S]));
+        }
+        if (f % 8 == 0) find_rows((f + 8) * 64);  // asked for after the next barrier at the earliest
+        if (f + AHEAD < ngroups) ask(f + AHEAD);
+        else queue_commit();
+        // The segment before this one, while its successor's first products
+        // run (they go into the other buffer).
+        if (f % kOuterSegment == 0 && f > 0) drain(q - 1, f - 1);
+    }
+    if (ngroups > 0) drain((ngroups - 1) / kOuterSegment, ngroups - 1);
     // Every product is done before its operands' memory is used again.
-    for (uint32_t f = fills > S ? fills - S : 0; f < fills; ++f)
+    for (int f = ngroups > S ? ngroups - S : 0; f < ngroups; ++f)
         shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[f % S]), (f / S) & 1, &abort_flag, k.status, false);
     __syncthreads();
     // Result through shared memory, the parts' rows added there; the cluster's
@@ -1383,7 +1424,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_co
         }
     };
     float *piece = reinterpret_cast<float *>(smem);                // [kRows][kPitch]
-    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][256]
+    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][128]
     auto add = [](float4 &t, const float4 &v) {
         t.x += v.x;
         t.y += v.y;
@@ -1391,28 +1432,24 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_co
         t.w += v.w;
     };
     const int my_row = quad * 32 + lane;
-#pragma unroll 1
-    for (int c = 0; c < 256; c += 128) {
-        if (part / 2 == c / 128 && my_row < Shape::kRows)
+    if (my_row < Shape::kRows)
 #pragma unroll
-            for (int j = 0; j < 64; j += 4)
-                *reinterpret_cast<float4 *>(piece + my_row * Shape::kPitch + (part & 1) * 64 + j) =
-                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-        __syncthreads();
-        for (int e = threadIdx.x; e < k.R * 32; e += kOuterThreads) {
-            const int r = e / 32, j = e % 32 * 4;
-            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < 64; j += 4)
+            *reinterpret_cast<float4 *>(piece + my_row * Shape::kPitch + part * 64 + j) =
+                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < k.R * 32; e += kOuterThreads) {
+        const int r = e / 32, j = e % 32 * 4;
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int h = Shape::kBands - 1; h >= 0; --h)
-                add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
-            if (cs > 1) *reinterpret_cast<float4 *>(sums + r * 256 + c + j) = t;
-            else put(r, c + j, t);
-        }
-        __syncthreads();
+        for (int h = Shape::kBands - 1; h >= 0; --h)
+            add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
+        if (cs > 1) *reinterpret_cast<float4 *>(sums + r * kOuterCols + j) = t;
+        else put(r, j, t);
     }
     if (cs > 1) {
         cluster.sync();
-        for (int e = cr * kOuterThreads + threadIdx.x; e < k.R * 64; e += cs * kOuterThreads) {
+        for (int e = cr * kOuterThreads + threadIdx.x; e < k.R * 32; e += cs * kOuterThreads) {
             float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int b = 0; b < 8; ++b)
@@ -1420,14 +1457,14 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_co
 #pragma unroll
             for (int b = 0; b < 8; ++b)
                 if (b < cs) add(t, v[b]);
-            put(e / 64, e % 64 * 4, t);
+            put(e / 32, e % 32 * 4, t);
         }
         cluster.sync();  // nobody leaves with what another CTA still reads
     }
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
-    if (warp == 0) shmm_tc::tmem_free(tmem, 512);
+    if (warp == 0) shmm_tc::tmem_free(tmem, 2 * kOuterCols);
 }
 
 // Any types, on CUDA cores: one adapter, 128 columns and 16 adapter rows per
@@ -1435,8 +1472,6 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(const __grid_co
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
-    __shared__ int list[kList];
-    __shared__ Marks marks;
     __shared__ float ss[2][16][16];
     __shared__ float sums[16][128];
     const OuterJob &J = k.job[0];
@@ -1447,36 +1482,31 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
-    const int total = mark_rows<kWarps>(k.ids, w0, k.rows, a, marks, k.status);
-    for (int l0 = 0; l0 < total; l0 += kList) {
-        const int have = total - l0 < kList ? total - l0 : kList;
-        list_rows<kWarps>(marks, w0, k.rows, l0, l0 + have, list);
-        for (int s0 = 0; s0 < have; s0 += 32) {
-            const int s = s0 + half * 16;
-            float x[16];
+    const int first = k.start[a], have = k.start[a + 1] - first;
+    const int *order = k.order + first;
+    for (int s0 = 0; s0 < have; s0 += 32) {
+        const int s = s0 + half * 16;
+        float x[16];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                x[u] = 0.0f;
-                if (s + u < have && c < J.x.bcols) {
-                    const uint32_t t = list[s + u], b = t / (uint32_t)J.x.brows;
-                    const int64_t at = (int64_t)(t - b * (uint32_t)J.x.brows) * J.x.bcols + c;
-                    if (in_bounds(k.status, at, 1, J.x.brows * J.x.bcols))
-                        x[u] = as_float(((const TX *)J.x.at[b * J.x.b1 + blk])[at]);
-                }
+        for (int u = 0; u < 16; ++u) {
+            x[u] = 0.0f;
+            if (s + u < have && c < J.x.bcols) {
+                const uint32_t t = order[s + u], b = t / (uint32_t)J.x.brows;
+                const int64_t at = (int64_t)(t - b * (uint32_t)J.x.brows) * J.x.bcols + c;
+                if (in_bounds(k.status, at, 1, J.x.brows * J.x.bcols))
+                    x[u] = as_float(((const TX *)J.x.at[b * J.x.b1 + blk])[at]);
             }
-            __syncthreads();
-            for (int i = th; i < 16 * 16; i += 128) {
-                const int u = i / 16, r = r0 + i % 16;
-                ss[half][u][i % 16] = s + u < have && r < k.R ? J.s[(int64_t)list[s + u] * k.R + r] : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[half][u][i], x[u], acc[i]);
         }
-    }
+        __syncthreads();
+        for (int i = th; i < 16 * 16; i += 128) {
+            const int u = i / 16, r = r0 + i % 16;
+            ss[half][u][i % 16] = s + u < have && r < k.R ? J.s[(int64_t)order[s + u] * k.R + r] : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[half][u][i], x[u], acc[i]);
     }
     if (half)
 #pragma unroll
@@ -1726,9 +1756,22 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     // Shares of an adapter's rows until the card is full or a share is down to
     // four groups of rows.
     int cs = 1;
-    while (cs < 8 && tiles * k.n * cs * 2 <= 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
+    while (cs < 8 && tiles * k.n * cs * 2 <= 4 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kOuterThreads),
                               Shape::kSmem, s, k);
+}
+
+int padded(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // adapter rows of a product
+
+cudaError_t arrange(const ArrangeK &k, cudaStream_t s) {
+    shmm::count_launch();
+    // CTAs for a wave of two per SM, of 64 rows and more.
+    int64_t y = 2 * sms() / k.n, most = k.rows / k.n / 64;
+    if (y > most) y = most;
+    const dim3 g((unsigned)k.n, (unsigned)(y > 1 ? y : 1));
+    if (k.R <= 16) return launch_pdl(arrange_kernel<16>, g, dim3(512), 0, s, k);
+    if (k.R <= 32) return launch_pdl(arrange_kernel<32>, g, dim3(512), 0, s, k);
+    return launch_pdl(arrange_kernel<64>, g, dim3(512), 0, s, k);
 }
 
 // One or both gradient products (job[1].cols == 0: one) of one type.
@@ -1743,7 +1786,7 @@ cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     bool vec = true;
     for (OuterJob &j : k.job) {
         if (!j.cols) continue;
-        j.tiles = (int)((j.x.bcols + 255) / 256 * j.x.b1);
+        j.tiles = (int)((j.x.bcols + kOuterCols - 1) / kOuterCols * j.x.b1);
         vec = vec && j.x.bcols % 8 == 0;
     }
     if (k.R <= 16) return vec ? outer_tc<16, true>(k, s) : outer_tc<16, false>(k, s);
@@ -1770,7 +1813,23 @@ void fill_expand(ExpandK *k, const shmm::AdapterArgs &a, const shmm::RankBoxes &
 
 namespace shmm {
 
-size_t adapters_workspace_bytes(int64_t rows, int R) { return (size_t)((rows * R * 4 + 255) / 256 * 256); }
+// Workspace of the backward call: the gradient of the low values, then the
+// rows' arrangement.
+struct Rooms {
+    size_t start, order, parts[2], all;
+};
+static Rooms rooms(int64_t rows, int n, int R, bool tc) {
+    auto up = [](int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); };
+    Rooms r;
+    r.start = up(rows * R * 4);
+    r.order = r.start + up(((int64_t)n + 1) * 4);
+    r.parts[0] = r.order + up(rows * 4);
+    r.parts[1] = r.parts[0] + (tc ? up(rows * 6 * padded(R)) : 0);
+    r.all = rows ? r.parts[1] + (tc ? up(rows * 6 * padded(R)) : 0) : 0;
+    return r;
+}
+
+size_t adapters_workspace_bytes(int64_t rows, int n, int R, bool tc) { return rooms(rows, n, R, tc).all; }
 
 int launch_adapters_forward(const AdapterArgs &a, const BlockGrid &A, const RankBoxes &C, shmm_dtype_t in_dt,
                             shmm_dtype_t out_dt, int *status, void *stream) {
@@ -1802,44 +1861,64 @@ int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const Bl
                              shmm_dtype_t in_dt, shmm_dtype_t out_dt, int *status, void *stream) {
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (a.rows) {
-        ProjK p = {};
-        fill(&p.x, dC);
-        p.w = a.up;
-        p.ids = a.ids;
-        p.scale = a.scale;
-        p.out = a.dlow;
-        p.n = a.n;
-        p.R = a.R;
-        p.rows = a.rows;
-        p.cols = a.K;
-        p.status = status;
-        if ((e = project(p, out_dt, in_dt, s)) != cudaSuccess) return (int)e;
+    if (a.rows == 0) {  // nothing to read, and no workspace
+        const size_t factor = (size_t)a.n * a.R * 4;
+        e = cudaMemsetAsync(a.ddown, 0, factor * a.J, s);
+        return (int)(e != cudaSuccess ? e : cudaMemsetAsync(a.dup, 0, factor * a.K, s));
     }
+    ProjK p = {};
+    fill(&p.x, dC);
+    p.w = a.up;
+    p.ids = a.ids;
+    p.scale = a.scale;
+    p.out = a.dlow;
+    p.n = a.n;
+    p.R = a.R;
+    p.rows = a.rows;
+    p.cols = a.K;
+    p.status = status;
+    if ((e = project(p, out_dt, in_dt, s)) != cudaSuccess) return (int)e;
+    const bool tc[2] = {out_dt == SHMM_BF16, in_dt == SHMM_BF16};  // dup, ddown
+    const Rooms at = rooms(a.rows, a.n, a.R, tc[0] || tc[1]);
+    char *ws = reinterpret_cast<char *>(a.dlow);
     OuterK o = {};
-    fill(&o.job[0].x, dC);
-    o.job[0].s = a.low;
-    o.job[0].scale = a.scale;
-    o.job[0].out = a.dup;
-    o.job[0].cols = a.K;
-    OuterJob down = {};
-    fill(&down.x, A);
-    down.s = a.dlow;
-    down.out = a.ddown;
-    down.cols = a.J;
-    o.ids = a.ids;
+    o.order = reinterpret_cast<int *>(ws + at.order);
+    o.start = reinterpret_cast<int *>(ws + at.start);
     o.n = a.n;
     o.R = a.R;
     o.rows = a.rows;
     o.status = status;
-    const bool both = in_dt == SHMM_BF16 && out_dt == SHMM_BF16;
-    if (both) o.job[1] = down;
+    OuterJob up = {}, down = {};
+    fill(&up.x, dC);
+    up.s = a.low;
+    up.parts = reinterpret_cast<bf16 *>(ws + at.parts[0]);
+    up.scale = a.scale;
+    up.out = a.dup;
+    up.cols = a.K;
+    fill(&down.x, A);
+    down.s = a.dlow;
+    down.parts = reinterpret_cast<bf16 *>(ws + at.parts[1]);
+    down.out = a.ddown;
+    down.cols = a.J;
+    ArrangeK g = {};
+    g.ids = a.ids;
+    g.order = reinterpret_cast<int *>(ws + at.order);
+    g.start = reinterpret_cast<int *>(ws + at.start);
+    g.s[0] = tc[0] ? a.low : nullptr;
+    g.s[1] = tc[1] ? a.dlow : nullptr;
+    for (int j = 0; j < 2; ++j) g.parts[j] = reinterpret_cast<bf16 *>(ws + at.parts[j]);
+    g.n = a.n;
+    g.R = a.R;
+    g.rows = a.rows;
+    g.status = status;
+    if ((e = arrange(g, s)) != cudaSuccess) return (int)e;
+    o.job[0] = up;
+    if (tc[0] && tc[1]) o.job[1] = down;
     if ((e = outer(o, out_dt, s)) != cudaSuccess) return (int)e;
-    if (!both) {
+    if (!(tc[0] && tc[1])) {
         o.job[0] = down;
         if ((e = outer(o, in_dt, s)) != cudaSuccess) return (int)e;
     }
-    if (!a.rows) return 0;
     ExpandK x = {};
     fill_expand(&x, a, dA);
     x.w = a.down;

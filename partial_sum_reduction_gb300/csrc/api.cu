@@ -1031,7 +1031,7 @@ shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *p, int n_adapters,
         if (!p || !bytes) return fail(SHMM_ERR_NULL, std::string(fn) + ": NULL argument");
         const shmm_status_t st = check_adapter_shape(fn, n_adapters, rank);
         if (st != SHMM_OK) return st;
-        *bytes = shmm::adapters_workspace_bytes(p->I, rank);
+        *bytes = shmm::adapters_workspace_bytes(p->I, n_adapters, rank, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
         return SHMM_OK;
     });
 }
@@ -1053,7 +1053,7 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int r
             (st = check_ptr(fn, ddown, "ddown", 4)) != SHMM_OK || (st = check_ptr(fn, dup, "dup", 4)) != SHMM_OK)
             return st;
         if (base_r && (st = check_ptrs(p, base_r, SHMM_TENSOR_A, fn, "base_r")) != SHMM_OK) return st;
-        const size_t need = shmm::adapters_workspace_bytes(p->I, rank);
+        const size_t need = shmm::adapters_workspace_bytes(p->I, n_adapters, rank, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
         if (workspace_bytes < need)
             return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(workspace_bytes) +
                                             " bytes, " + std::to_string(need) + " needed");

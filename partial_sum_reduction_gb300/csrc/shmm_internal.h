@@ -218,7 +218,7 @@ struct AdapterArgs {
     float *ddown = nullptr, *dup = nullptr;     // [n][R][J], [n][R][K]
 };
 constexpr int kMaxAdapterRank = 64;
-size_t adapters_workspace_bytes(int64_t rows, int R);
+size_t adapters_workspace_bytes(int64_t rows, int n, int R, bool tc);  // tc: a bf16 matrix takes part
 int launch_adapters_forward(const AdapterArgs &a, const BlockGrid &A, const RankBoxes &C, shmm_dtype_t in_dt,
                             shmm_dtype_t out_dt, int *status, void *stream);
 int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const BlockGrid &A, const RankBoxes &dA,

@@ -43,10 +43,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_
            (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128, N = n, A
-// K-major, B K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128, N = n; A
+// and B K-major or (a_mn, b_mn) MN-major.
+__host__ __device__ constexpr uint32_t instruction(int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
 
