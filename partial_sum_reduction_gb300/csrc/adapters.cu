@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
 // shared memory in order.  Beside the warp instructions above it: the factor
 // is read once per 128 rows instead of per 32, and no thread spends
 // instructions on addresses, which bounded them.
-constexpr int kTcThreads = 320, kTcStages = 6;
+constexpr int kTcThreads = 320, kTcStages = 3;
 // Chunks summed in the tensor memory before their sum is added in registers:
 // 16 instructions.  The tensor core's own fp32 additions cut instead of
 // rounding, so their error grows with their number (some 4e-8 of the sum per
@@ -440,7 +440,7 @@ constexpr size_t kTcSmem = kTcRing + 1024;
 static_assert(128 * kTcSum * 4 <= kTcRing, "the sums take the ring's memory");
 
 template <int RP>
-__global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_constant__ ProjTcK k) {
+__global__ void __launch_bounds__(kTcThreads, 2) project_tc_kernel(const __grid_constant__ ProjTcK k) {
     pdl_wait();
     constexpr int ROWS = 128, PER = kTcCols / RP, S = kTcStages, MINE = kTcCols / 2;  // MINE: of a reading warp
     __shared__ int ids[ROWS], list[ROWS], count, abort_flag;
@@ -584,49 +584,35 @@ __global__ void __launch_bounds__(kTcThreads) project_tc_kernel(const __grid_con
 #pragma unroll
             for (int c = 0; c < MINE; c += 16) {
                 if (c0 + c >= na * RP) continue;
-                const int i = (c0 + c) / RP, r = (c0 + c) % RP;
-                if (cs > 1) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<float4 *>(sums + row * kTcSum + c0 + c + j) =
-                            make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
-                } else if (ids[row] == list[p0 + i] && in_bounds(k.status, (t0 + row) * k.R, k.R, k.rows * k.R)) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (r + j < k.R) k.out[(t0 + row) * k.R + r + j] = k.scale ? acc[c + j] * scales[i] : acc[c + j];
-                }
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<float4 *>(sums + row * kTcSum + c0 + c + j) =
+                        make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
             }
         }
-        if (cs > 1) {
-            cluster.sync();
-            const int r0 = ROWS * cr / cs, r1 = ROWS * (cr + 1) / cs;
-            const int vecs = na * RP / 4;
-            for (int e = threadIdx.x; e < (r1 - r0) * vecs; e += kTcThreads) {
-                const int row = r0 + e / vecs, c = e % vecs * 4, i = c / RP, r = c % RP;
-                if (r >= k.R || ids[row] != list[p0 + i]) continue;
-                float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int b = 0; b < 8; ++b)
-                    if (b < cs) v[b] = *cluster.map_shared_rank(reinterpret_cast<float4 *>(sums + row * kTcSum + c), b);
-#pragma unroll
-                for (int b = 0; b < 8; ++b)
-                    if (b < cs) {
-                        t.x += v[b].x;
-                        t.y += v[b].y;
-                        t.z += v[b].z;
-                        t.w += v[b].w;
-                    }
-                const float *u = &t.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r + j < k.R && in_bounds(k.status, (t0 + row) * k.R + r + j, 1, k.rows * k.R))
-                        k.out[(t0 + row) * k.R + r + j] = k.scale ? u[j] * scales[i] : u[j];
+        cluster.sync();
+        const int r0 = ROWS * cr / cs, r1 = ROWS * (cr + 1) / cs;
+        const int vecs = na * RP / 4;
+        for (int e = threadIdx.x; e < (r1 - r0) * vecs; e += kTcThreads) {
+            const int row = r0 + e / vecs, c = e % vecs * 4, i = c / RP, r = c % RP;
+            if (r >= k.R || ids[row] != list[p0 + i]) continue;
+            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1  // at 96 registers a thread
+            for (int b = 0; b < cs; ++b) {
+                const float4 v = *cluster.map_shared_rank(reinterpret_cast<float4 *>(sums + row * kTcSum + c), b);
+                t.x += v.x;
+                t.y += v.y;
+                t.z += v.z;
+                t.w += v.w;
             }
-            shmm_tc::fence_async();
-            cluster.sync();  // the sums are read: the stages may be filled again
-        } else {
-            __syncthreads();
+            const float *u = &t.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r + j < k.R && in_bounds(k.status, (t0 + row) * k.R + r + j, 1, k.rows * k.R))
+                    k.out[(t0 + row) * k.R + r + j] = k.scale ? u[j] * scales[i] : u[j];
         }
+        shmm_tc::fence_async();
+        cluster.sync();  // the sums are read: the stages may be filled again
         shmm_tc::fence_after();
     }
     // Never leave a load into shared memory in flight.
@@ -1173,7 +1159,6 @@ __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_
 // the ids alone, so that they need nothing of one another.
 template <int RP>
 __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ ArrangeK k) {
-    pdl_enter();
     __shared__ Marks marks;
     __shared__ int list[kList], sum[16];
     const int a = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -1199,13 +1184,18 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
         const int total = mark_rows<16>(k.ids, w0, k.rows, a, marks, k.status);
         const int lo = (int)((int64_t)total * blockIdx.y / gridDim.y), hi = (int)((int64_t)total * (blockIdx.y + 1) / gridDim.y);
-        for (int l0 = lo; l0 < hi; l0 += kList) {
-            const int have = hi - l0 < kList ? hi - l0 : kList;
-            list_rows<16>(marks, w0, k.rows, l0, l0 + have, list);
-            for (int i = threadIdx.x; i < have; i += 512)
-                if (in_bounds(k.status, at + l0 + i, 1, k.rows)) k.order[at + l0 + i] = list[i];
+        // The ids and the forward call's values are from before the kernel that
+        // this one follows (which has itself waited for what was before it);
+        // the gradient of the low values is that kernel's.
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j) {
+            if (j == 1) pdl_wait();
+            for (int l0 = lo; l0 < hi; l0 += kList) {
+                const int have = hi - l0 < kList ? hi - l0 : kList;
+                if (j == 0 || hi - lo > kList) list_rows<16>(marks, w0, k.rows, l0, l0 + have, list);
+                if (j == 0)
+                    for (int i = threadIdx.x; i < have; i += 512)
+                        if (in_bounds(k.status, at + l0 + i, 1, k.rows)) k.order[at + l0 + i] = list[i];
                 if (!k.s[j]) continue;
 #pragma unroll 2
                 for (int e = threadIdx.x; e < have * (RP / 2); e += 512) {
@@ -1222,6 +1212,7 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
         }
         at += total;
     }
+    pdl_release();
     if (threadIdx.x == 0 && blockIdx.y == 0) {
         k.start[a] = below;
         if (a == k.n - 1) k.start[k.n] = at;
@@ -1656,7 +1647,7 @@ cudaError_t project_tc(const ProjK &k, int b0, cudaStream_t s) {
     t.status = k.status;
     const int64_t tiles = (int64_t)t.row_tiles * b0;
     int c, z;
-    spread(tiles, sms(), 1, t.chunks / 4, false, &c, &z);
+    spread(tiles, 2 * sms(), 1, t.chunks / 4, false, &c, &z);
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, c), dim3(1, c, 1), dim3(kTcThreads), kTcSmem, s, t);
 }
 
