@@ -635,7 +635,8 @@ template <typename TX, typename TW, int NR>
 __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_constant__ ProjK k) {
     pdl_enter();
     constexpr int ROWS = 32, RP = 16 * NR;
-    __shared__ int ids[ROWS], list[ROWS], count;
+    __shared__ int ids[ROWS], list[ROWS], count, block_row[ROWS];
+    __shared__ int64_t row_at[ROWS];  // in its row of blocks
     __shared__ float xs[ROWS][33], ws[RP][33], part[ROWS * RP];
     cg::cluster_group cluster = cg::this_cluster();
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
@@ -645,30 +646,46 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
     if (blockIdx.z == 0 && cr == 0)
         for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
             if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows) k.out[t0 * k.R + i] = 0.0f;
-    const int64_t per_block = (k.x.bcols + 31) / 32, chunks = per_block * k.x.b1;
+    if (threadIdx.x < ROWS) {
+        block_row[threadIdx.x] = (int)((t0 + threadIdx.x) / k.x.brows);
+        row_at[threadIdx.x] = (t0 + threadIdx.x) % k.x.brows * k.x.bcols;
+    }
+    __syncthreads();
+    const int bcols = (int)k.x.bcols, per_block = (bcols + 31) / 32, chunks = per_block * k.x.b1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     for (int d = blockIdx.z; d < nd; d += gridDim.z) {
         const int a = list[d];
         const TW *w = (const TW *)k.w + (int64_t)a * k.R * k.cols;
         float acc[2][NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) acc[0][i] = acc[1][i] = 0.0f;
-        for (int64_t ch = cr; ch < chunks; ch += cs) {
-            const int blk = (int)(ch / per_block);
-            const int64_t c = (ch - blk * per_block) * 32 + (threadIdx.x & 31);
-            for (int row = threadIdx.x / 32; row < ROWS; row += kWarps) {
-                const int64_t t = t0 + row;
-                float v = 0.0f;
-                if (ids[row] == a && c < k.x.bcols) {
-                    const int64_t at = (t % k.x.brows) * k.x.bcols + c;
-                    if (in_bounds(k.status, at, 1, k.x.brows * k.x.bcols))
-                        v = as_float(((const TX *)k.x.at[(t / k.x.brows) * k.x.b1 + blk])[at]);
-                }
-                xs[row][threadIdx.x & 31] = v;
+        // A chunk's values, asked for while the one before it is computed.
+        float xv[ROWS / kWarps], wv[RP / kWarps];
+        auto fetch = [&](int ch) {
+            const int blk = ch / per_block, c = (ch - blk * per_block) * 32 + lane;
+            const bool in = ch < chunks && c < bcols;
+#pragma unroll
+            for (int i = 0; i < ROWS / kWarps; ++i) {
+                const int row = warp + i * kWarps;
+                const int64_t at = row_at[row] + c;
+                xv[i] = in && ids[row] == a && in_bounds(k.status, at, 1, k.x.brows * k.x.bcols)
+                            ? as_float(((const TX *)k.x.at[block_row[row] * k.x.b1 + blk])[at])
+                            : 0.0f;
             }
-            for (int r = threadIdx.x / 32; r < RP; r += kWarps)
-                ws[r][threadIdx.x & 31] =
-                    r < k.R && c < k.x.bcols ? as_float(w[r * k.cols + blk * k.x.bcols + c]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < RP / kWarps; ++i) {
+                const int r = warp + i * kWarps;
+                wv[i] = in && r < k.R ? as_float(w[r * k.cols + (int64_t)blk * bcols + c]) : 0.0f;
+            }
+        };
+        fetch(cr);
+        for (int ch = cr; ch < chunks; ch += cs) {
+#pragma unroll
+            for (int i = 0; i < ROWS / kWarps; ++i) xs[warp + i * kWarps][lane] = xv[i];
+#pragma unroll
+            for (int i = 0; i < RP / kWarps; ++i) ws[warp + i * kWarps][lane] = wv[i];
             __syncthreads();
+            fetch(ch + cs);
 #pragma unroll
             for (int c2 = 0; c2 < 32; ++c2) {
                 const float x0 = xs[ty][c2], x1 = xs[ty + 16][c2];
@@ -1459,40 +1476,49 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
 }
 
 // Any types, on CUDA cores: one adapter, 128 columns and 16 adapter rows per
-// CTA; the halves of the CTA take every other group of 16 rows.
+// CTA, a cluster along z sharing the adapter's rows; the halves of a CTA take
+// every other group of 16 of them.
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
     __shared__ float ss[2][16][16];
-    __shared__ float sums[16][128];
-    const OuterJob &J = k.job[0];
-    const int r0 = blockIdx.z * 16, a = blockIdx.y, half = threadIdx.x / 128, th = threadIdx.x % 128;
-    const int per_block = (int)((J.x.bcols + 127) / 128);
-    const int blk = blockIdx.x / per_block;
-    const int64_t c = (int64_t)(blockIdx.x - blk * per_block) * 128 + th;
+    __shared__ float sums[16 * 128];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    const int which = (int)blockIdx.x >= k.job[0].tiles;
+    const OuterJob &J = k.job[which];
+    const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y, r0 = blockIdx.z / cs * 16;
+    const int half = threadIdx.x / 128, th = threadIdx.x % 128;
+    const int bcols = (int)J.x.bcols, per_block = (bcols + 127) / 128, blk = tile / per_block;
+    const int c0 = (tile - blk * per_block) * 128, c = c0 + th;
+    const int first = k.start[a], total = k.start[a + 1] - first, groups = (total + 31) / 32;
+    const int lo = (int)((int64_t)groups * cr / cs) * 32, end = (int)((int64_t)groups * (cr + 1) / cs) * 32;
+    const int have = (end < total ? end : total) - lo;
+    const int *order = k.order + first + lo;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    const int first = k.start[a], have = k.start[a + 1] - first;
-    const int *order = k.order + first;
     for (int s0 = 0; s0 < have; s0 += 32) {
         const int s = s0 + half * 16;
-        float x[16];
+        float x[16], v[2];
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
             x[u] = 0.0f;
-            if (s + u < have && c < J.x.bcols) {
+            if (s + u < have && c < bcols) {
                 const uint32_t t = order[s + u], b = t / (uint32_t)J.x.brows;
-                const int64_t at = (int64_t)(t - b * (uint32_t)J.x.brows) * J.x.bcols + c;
-                if (in_bounds(k.status, at, 1, J.x.brows * J.x.bcols))
+                const int64_t at = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols + c;
+                if (in_bounds(k.status, at, 1, J.x.brows * bcols))
                     x[u] = as_float(((const TX *)J.x.at[b * J.x.b1 + blk])[at]);
             }
         }
-        __syncthreads();
-        for (int i = th; i < 16 * 16; i += 128) {
-            const int u = i / 16, r = r0 + i % 16;
-            ss[half][u][i % 16] = s + u < have && r < k.R ? J.s[(int64_t)order[s + u] * k.R + r] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int u = th / 16 + i * 8, r = r0 + th % 16;
+            v[i] = s + u < have && r < k.R ? J.s[(int64_t)order[s + u] * k.R + r] : 0.0f;
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ss[half][th / 16 + i * 8][th % 16] = v[i];
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < 16; ++u)
@@ -1501,16 +1527,21 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
     }
     if (half)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sums[i][th] = acc[i];
+        for (int i = 0; i < 16; ++i) sums[i * 128 + th] = acc[i];
     __syncthreads();
-    if (half || c >= J.x.bcols) return;
-    const float scale = J.scale ? J.scale[a] : 1.0f;
+    if (!half)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t at = ((int64_t)a * k.R + r0 + i) * J.cols + blk * J.x.bcols + c;
-        if (r0 + i < k.R && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols))
-            J.out[at] = (acc[i] + sums[i][th]) * scale;
+        for (int i = 0; i < 16; ++i) sums[i * 128 + th] += acc[i];
+    if (cs > 1) cluster.sync();
+    else __syncthreads();
+    const float scale = J.scale ? J.scale[a] : 1.0f;
+    for (int e = cr * kThreads + threadIdx.x; e < 16 * 128; e += cs * kThreads) {
+        const float v = cs > 1 ? sum_cluster(cluster, sums + e, cs) : sums[e];
+        const int r = r0 + e / 128, col = c0 + e % 128;
+        const int64_t at = ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + col;
+        if (r < k.R && col < bcols && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols)) J.out[at] = v * scale;
     }
+    if (cs > 1) cluster.sync();  // nobody leaves with what another CTA still reads
 }
 
 // ---- launches --------------------------------------------------------------
@@ -1769,10 +1800,18 @@ cudaError_t arrange(const ArrangeK &k, cudaStream_t s) {
 cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     shmm::count_launch();
     if (xt == SHMM_F32) {
-        const OuterJob &j = k.job[0];
-        return launch_pdl(outer_simt_kernel<float>,
-                          dim3((unsigned)((j.x.bcols + 127) / 128 * j.x.b1), (unsigned)k.n, (unsigned)((k.R + 15) / 16)),
-                          dim3(kThreads), 0, s, k);
+        int64_t tiles = 0;
+        for (OuterJob &j : k.job) {
+            j.tiles = j.cols ? (int)((j.x.bcols + 127) / 128 * j.x.b1) : 0;
+            tiles += j.tiles;
+        }
+        // Shares of an adapter's rows until the card is full or a share is
+        // down to 32 rows.
+        const int z = (k.R + 15) / 16;
+        int cs = 1;
+        while (cs < 8 && tiles * k.n * z * cs * 2 <= 4 * sms() && k.rows / k.n >= 64 * cs) cs *= 2;
+        return launch_pdl_cluster(outer_simt_kernel<float>, dim3((unsigned)tiles, (unsigned)k.n, z * cs), dim3(1, 1, cs),
+                                  dim3(kThreads), 0, s, k);
     }
     bool vec = true;
     for (OuterJob &j : k.job) {
@@ -1904,9 +1943,9 @@ int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const Bl
     g.status = status;
     if ((e = arrange(g, s)) != cudaSuccess) return (int)e;
     o.job[0] = up;
-    if (tc[0] && tc[1]) o.job[1] = down;
+    if (in_dt == out_dt) o.job[1] = down;
     if ((e = outer(o, out_dt, s)) != cudaSuccess) return (int)e;
-    if (!(tc[0] && tc[1])) {
+    if (in_dt != out_dt) {
         o.job[0] = down;
         if ((e = outer(o, in_dt, s)) != cudaSuccess) return (int)e;
     }
