@@ -1778,7 +1778,7 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     // Shares of an adapter's rows until the card is full or a share is down to
     // four groups of rows.
     int cs = 1;
-    while (cs < 8 && tiles * k.n * cs * 2 <= 4 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
+    while (cs < 8 && tiles * k.n * cs * 2 <= 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
     return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kOuterThreads),
                               Shape::kSmem, s, k);
 }
