@@ -244,7 +244,7 @@ __device__ __forceinline__ int col_of(int j) {
 // gradient; copying warp i (one thread of it) takes entries i, i + COPIERS, ...
 // With the rows in registers instead, what was in flight fell with every
 // register the running sums took: 63 us forward and 81 us backward at 8192 x
-// 4096 bf16 with a residual, where this takes FWD_US and BWD_US.
+// 4096 bf16 with a residual, where this takes 49 and 61 us.
 constexpr int kMaxStages = 16;
 // Forward, one block: three CTAs per SM under one another's chains of sums and
 // barriers (54 -> 49 us at 8192 x 4096 bf16 with a residual; with a second
@@ -324,8 +324,12 @@ __device__ __forceinline__ void ring_end(Ring &ring, int first, int64_t put, int
 __device__ __forceinline__ void ring_wait(Ring &ring, const Turn &turn, int *status) {
     shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[turn.stage]), turn.phase, &ring.abort_flag, status);
 }
-// ... and has been read.
+// ... and has been read.  The fence: the next copy into the entry goes through
+// the async proxy, and a warp's shared-memory loads may still be in their
+// queue when its arrival is counted (without it, one call in 25 had a first
+// row with a piece of the third's).
 __device__ __forceinline__ void ring_free(Ring &ring, Turn &turn, int stages) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if ((threadIdx.x & 31) == 0) shmm_dev::mbar_arrive(shmm_dev::smem_u32(&ring.empty[turn.stage]));
     turn.next(stages);
@@ -677,7 +681,10 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
         int s, g;
         int64_t rr, grow;
         locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-        const float mean = k.mean[s][rr], rstd = k.rstd[s][rr], shift = -mean * rstd;  // xh = x rstd + shift
+        // x - mean before anything else, not x rstd - mean rstd: in a row whose
+        // values differ little the second's own rounding would be the result.
+        const bool known = in_bounds(k.status, rr, 1, k.brows);
+        const float mean = known ? k.mean[s][rr] : 0.0f, rstd = known ? k.rstd[s][rr] : 0.0f;
         float dy[NV][VW];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -706,21 +713,20 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
             if (col_of<VW, ONEWARP>(j) < cols)
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
-                    const float xh = fmaf(x[j].get(i), rstd, shift), w = dy[j][i] * ga[j][i];
+                    const float xh = (x[j].get(i) - mean) * rstd, w = dy[j][i] * ga[j][i];
                     sum.x += w;
                     sum.y = fmaf(w, xh, sum.y);
                     dg[j][i] = fmaf(dy[j][i], xh, dg[j][i]);
                     db[j][i] += dy[j][i];
                 }
         sum = row_sum<ONEWARP>(sum, scratch, turn);
-        const float k1 = -rstd * (sum.x * inv_n), k2 = -rstd * (sum.y * inv_n);
+        const float k1 = -rstd * (sum.x * inv_n), k2 = -rstd * rstd * (sum.y * inv_n);
         float o[NV][VW];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
-                const float xh = fmaf(x[j].get(i), rstd, shift);
-                o[j][i] = fmaf(xh, k2, fmaf(dy[j][i] * ga[j][i], rstd, k1));
+                o[j][i] = fmaf(x[j].get(i) - mean, k2, fmaf(dy[j][i] * ga[j][i], rstd, k1));
             }
         if (t + step < k.rows) load_row(t + step);
 #pragma unroll
@@ -852,6 +858,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
         int s, g;
         int64_t rr, grow;
         locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
+        if (!in_bounds(k.status, rr, 1, k.brows)) return;
         mean = k.mean[s][rr];
         rstd = k.rstd[s][rr];
     };
@@ -892,16 +899,17 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
             if (col[j] < cols) from_ring(x[j], entries + turn.stage * entry, col[j]);
         }
         ring_free(ring, turn, stages);
-        const float rs = rstd, shift = -mean * rstd;  // xh = x rstd + shift
+        const float rs = rstd;
+        const F2 minus = both(-mean);  // x - mean first (see ln_backward_kernel)
         if (t + gridDim.x < k.rows) read_stats(t + gridDim.x);
-        const F2 rs2 = both(rs), shift2 = both(shift);
+        const F2 rs2 = both(rs);
         F2 sw = both(0.0f), swx = both(0.0f);  // of w and of w xh
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (col[j] < cols)
 #pragma unroll
                 for (int i = 0; i < VW / 2; ++i) {
-                    const F2 d = dy(j, i), xh = fma(x[j].get2(i), rs2, shift2), w = d * ga(j, i);
+                    const F2 d = dy(j, i), xh = (x[j].get2(i) + minus) * rs2, w = d * ga(j, i);
                     sw = sw + w;
                     swx = fma(w, xh, swx);
                     dg[j][i] = fma(d, xh, dg[j][i]);
@@ -909,7 +917,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
                 }
         const float2 pw = split(sw), px = split(swx);
         const float2 sum = stream_sum(make_float2(pw.x + pw.y, px.x + px.y), scratch, sum_turn, work);
-        const F2 k1 = both(-rs * (sum.x * inv_n)), k2 = both(-rs * (sum.y * inv_n));
+        const F2 k1 = both(-rs * (sum.x * inv_n)), k2 = both(-rs * rs * (sum.y * inv_n));
         if (has_res) ring_wait(ring, turn, k.status);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -917,7 +925,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
             F2 o[VW / 2];
 #pragma unroll
             for (int i = 0; i < VW / 2; ++i)
-                o[i] = fma(fma(x[j].get2(i), rs2, shift2), k2, fma(dy(j, i) * ga(j, i), rs2, k1));
+                o[i] = fma(x[j].get2(i) + minus, k2, fma(dy(j, i) * ga(j, i), rs2, k1));
             if constexpr (N == 1) {
                 if (has_res) {
                     Raw<T, VW> r;
@@ -964,7 +972,8 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_wide_kernel(const __g
             !in_bounds(k.status, grow * k.cols, k.cols, k.G * k.brows * k.cols))
             continue;  // the same for the whole CTA
         const T *x = (const T *)k.src[s] + rr * k.cols;
-        const float mean = k.mean[s][rr], rstd = k.rstd[s][rr];
+        const bool known = in_bounds(k.status, rr, 1, k.brows);
+        const float mean = known ? k.mean[s][rr] : 0.0f, rstd = known ? k.rstd[s][rr] : 0.0f;
         auto grad = [&](int64_t c) {
             float dy = (float)((const GT *)k.grad[g * k.G])[grow * k.cols + c];
             for (int m = 1; m < k.G; ++m) dy += (float)((const GT *)k.grad[g * k.G + m])[grow * k.cols + c];
@@ -1115,7 +1124,7 @@ cudaError_t forward_vec(const FwdK<N> &k, cudaStream_t s) {
     const int64_t cap = (int64_t)sms() * (1024 / h.threads > 0 ? 1024 / h.threads : 1);
     if (grid > cap) grid = cap;
     const dim3 g((unsigned)grid), b((unsigned)h.threads);
-constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
+    constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
     if (h.onewarp) return launch_pdl(ln_forward_kernel<T, VW, kMost, N, true>, g, b, 0, s, k);
     if (h.nv == kMost) return launch_pdl(ln_forward_kernel<T, VW, kMost, N, false>, g, b, 0, s, k);
     if (h.nv == kMost / 2 && VW > 1) return launch_pdl(ln_forward_kernel<T, VW, (VW > 1 ? kMost / 2 : kMost), N, false>, g, b, 0, s, k);
@@ -1146,7 +1155,7 @@ cudaError_t backward_vec(const BwdK<N> &k, int *parts, cudaStream_t s) {
     if (grid > cap) grid = cap;
     *parts = (int)grid;
     const dim3 g((unsigned)grid), b((unsigned)h.threads);
-constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
+    constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
     if (h.onewarp) return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, true>, g, b, 0, s, k);
     if (h.nv == kMost) return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, false>, g, b, 0, s, k);
     if (h.nv == kMost / 2 && VW > 1) return launch_pdl(ln_backward_kernel<T, GT, VW, (VW > 1 ? kMost / 2 : kMost), N, false>, g, b, 0, s, k);

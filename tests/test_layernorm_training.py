@@ -105,6 +105,24 @@ def test_forward(s, rows, cols, dtype, residual):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_in_flight_do_not_meet(s, dtype):
+    """Many calls on freshly copied inputs, whose first rows arrive late and
+    their followers early: every row is its own, forward and backward."""
+    rows, cols = 1003, 4096
+    x, gamma, beta, r = inputs(rows, cols, dtype)
+    res, dy = (r(rows, cols).to(DT[dtype]) for _ in range(2))
+    want = (x.float() + res.float()).to(DT[dtype]).cuda()
+    first = None
+    for _ in range(150):
+        y, mean, rstd, total = forward(s, x, gamma, beta, res)
+        assert torch.equal(total, want)
+        got = (y, mean, rstd) + backward(s, dy, total, mean, rstd, gamma, res)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+@pytest.mark.gpu
 def test_forward_equals_the_inference_call_within_a_step(s):
     """shmm_layernorm and shmm_layernorm_forward compute the same function;
     the sums' order may differ, so bf16 results differ by a step at most."""
@@ -185,6 +203,25 @@ def test_backward(s, rows, cols, dtype, residual):
     within(dx, wx, 128 * E * amp * sx + HALF[DT[dtype]] * (wx.abs() + 128 * E * amp * sx), "dx")
     within(dg, wg, (rows + 64) * E * amp * (sg + sb), "dgamma")
     within(db, wb, (rows + 64) * E * sb, "dbeta")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(37, 512), (37, 4096), (37, 1001), (37, 9000), (1301, 4096), (1301, 8192)])
+def test_backward_of_constant_rows(s, rows, cols, dtype):
+    """Rows of one value far from zero: xh is exactly 0 (the sum of `cols`
+    times 1000 = 125 * 8 is exact below 2^24 * 8, so is its division, so is
+    x - mean), and so is dgamma, however large rstd = 316 is."""
+    x = torch.full((rows, cols), 1000.0).to(DT[dtype])
+    _, gamma, beta, r = inputs(rows, cols, dtype)
+    dy = r(rows, cols).to(DT[dtype])
+    y, mean, rstd, _ = forward(s, x, gamma, beta)
+    assert (mean == 1000.0).all() and torch.equal(y.cpu(), beta.to(DT[dtype]).expand(rows, cols))
+    dx, dg, db = backward(s, dy.cuda(), x.cuda(), mean, rstd, gamma.cuda())
+    assert (dg == 0).all()
+    w, _, wb, scale, _, sb = formula_grad(x, dy, mean.cpu(), rstd.cpu(), gamma)
+    within(dx, w, 128 * E * scale + HALF[DT[dtype]] * (w.abs() + 128 * E * scale), "dx")
+    within(db, wb, E * (rows + 64) * sb, "dbeta")
 
 
 @pytest.mark.gpu
