@@ -523,14 +523,18 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_d
  * cores.  One row of the batch: one launch of few CTAs per factor, the same
  * kernels.  A plan whose result GeLU finishes is refused: the adapters' part
  * belongs before it.
- * Errors: NULL, ALIGN, SHAPE (n_adapters, rank, an empty J or K, a size of
- * 2^31 or more), UNSUPPORTED (rank > 64, SHMM_FLAG_GELU), CUDA. */
+ * An infinity in a row's own A, base or factors makes that row's results
+ * infinite or NaN (a part of the split may be 0, and 0 times infinity is
+ * NaN), never another adapter's or another row's.
+ * Errors: NULL, ALIGN, SHAPE (n_adapters, rank, an empty J or K, I of 2^31 or
+ * more, J or K of 2^23 or more), UNSUPPORTED (rank > 64, SHMM_FLAG_GELU),
+ * CUDA. */
 shmm_status_t shmm_adapters_forward(const shmm_plan_t *plan, int n_adapters, int rank, const void *const *A_r,
                                     const int32_t *row_adapter, const void *down, const void *up, const float *scale,
                                     const void *const *base_r, void *const *C_r, float *low, void *stream);
 
 /* Workspace of shmm_adapters_backward in bytes.  Host only.
- * Errors: NULL, SHAPE (n_adapters, rank), UNSUPPORTED (rank > 64). */
+ * Errors: NULL, SHAPE (n_adapters, rank, I, J, K), UNSUPPORTED (rank > 64). */
 shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *plan, int n_adapters, int rank,
                                            size_t *bytes);
 

@@ -1412,7 +1412,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
     __syncthreads();
     // Result through shared memory, the parts' rows added there; the cluster's
     // sums then meet.
-    const float scale = J.scale ? J.scale[a] : 1.0f;
+    const float scale = J.scale && total > 0 ? J.scale[a] : 1.0f;  // no rows: zeros whatever it is
     float *out = J.out + (int64_t)a * k.R * J.cols + (int64_t)blk * bcols + c0;
     const bool whole = (J.cols & 3) == 0 && (bcols & 3) == 0 && (reinterpret_cast<uintptr_t>(J.out) & 15) == 0;
     auto put = [&](int r, int c, float4 v) {  // four columns from c of row r
@@ -1498,8 +1498,8 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (int s0 = 0; s0 < have; s0 += 32) {
-        const int s = s0 + half * 16;
+    for (int64_t s0 = 0; s0 < have; s0 += 32) {
+        const int64_t s = s0 + half * 16;
         float x[16], v[2];
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
@@ -1534,7 +1534,7 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
         for (int i = 0; i < 16; ++i) sums[i * 128 + th] += acc[i];
     if (cs > 1) cluster.sync();
     else __syncthreads();
-    const float scale = J.scale ? J.scale[a] : 1.0f;
+    const float scale = J.scale && total > 0 ? J.scale[a] : 1.0f;  // no rows: zeros whatever it is
     for (int e = cr * kThreads + threadIdx.x; e < 16 * 128; e += cs * kThreads) {
         const float v = cs > 1 ? sum_cluster(cluster, sums + e, cs) : sums[e];
         const int r = r0 + e / 128, col = c0 + e % 128;

@@ -962,6 +962,15 @@ static shmm_status_t check_adapter_shape(const char *fn, int n, int R) {
     return SHMM_OK;
 }
 
+// Rows are counted in 31 bits; 2^23 columns keep the launches' second grid
+// dimension (of 256 columns and more) within its 65535.
+static shmm_status_t check_adapter_sizes(const char *fn, const shmm_plan_t *p) {
+    if (p->I >= (int64_t)1 << 31) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": I must be below 2^31");
+    if (p->J >= (int64_t)1 << 23 || p->K >= (int64_t)1 << 23)
+        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": J and K must be below 2^23");
+    return SHMM_OK;
+}
+
 // What the adapters' calls share: the plan and the adapters' shape.
 static shmm_status_t check_adapters(const char *fn, const shmm_plan_t *p, int n, int R, const int *ids,
                                     const void *down, const void *up, const float *scale, const float *low) {
@@ -972,15 +981,17 @@ static shmm_status_t check_adapters(const char *fn, const shmm_plan_t *p, int n,
     shmm_status_t st;
     if ((st = check_adapter_shape(fn, n, R)) != SHMM_OK) return st;
     if (p->J == 0 || p->K == 0) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": the plan's J or K is 0");
-    const int64_t most = (int64_t)1 << 31;
-    if (p->I >= most || p->J >= most || p->K >= most)
-        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": I, J and K must be below 2^31");
+    if ((st = check_adapter_sizes(fn, p)) != SHMM_OK) return st;
     if ((st = check_ptr(fn, down, "down", 16)) != SHMM_OK || (st = check_ptr(fn, up, "up", 16)) != SHMM_OK) return st;
     if (scale && (st = check_ptr(fn, scale, "scale", 4)) != SHMM_OK) return st;
     if (p->I == 0) return SHMM_OK;
     if ((st = check_ptr(fn, ids, "row_adapter", 4)) != SHMM_OK || (st = check_ptr(fn, low, "low", 4)) != SHMM_OK)
         return st;
     return SHMM_OK;
+}
+
+static size_t adapters_workspace(const shmm_plan_t *p, int n, int R) {
+    return shmm::adapters_workspace_bytes(p->I, n, R, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
 }
 
 static shmm::AdapterArgs adapter_args(const shmm_plan_t *p, int n, int R, const int *ids, const void *down,
@@ -1029,9 +1040,10 @@ shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *p, int n_adapters,
     return guarded([&]() -> shmm_status_t {
         shmm::clear_error();
         if (!p || !bytes) return fail(SHMM_ERR_NULL, std::string(fn) + ": NULL argument");
-        const shmm_status_t st = check_adapter_shape(fn, n_adapters, rank);
-        if (st != SHMM_OK) return st;
-        *bytes = shmm::adapters_workspace_bytes(p->I, n_adapters, rank, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
+        shmm_status_t st;
+        if ((st = check_adapter_shape(fn, n_adapters, rank)) != SHMM_OK || (st = check_adapter_sizes(fn, p)) != SHMM_OK)
+            return st;
+        *bytes = adapters_workspace(p, n_adapters, rank);
         return SHMM_OK;
     });
 }
@@ -1053,7 +1065,7 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int r
             (st = check_ptr(fn, ddown, "ddown", 4)) != SHMM_OK || (st = check_ptr(fn, dup, "dup", 4)) != SHMM_OK)
             return st;
         if (base_r && (st = check_ptrs(p, base_r, SHMM_TENSOR_A, fn, "base_r")) != SHMM_OK) return st;
-        const size_t need = shmm::adapters_workspace_bytes(p->I, n_adapters, rank, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
+        const size_t need = adapters_workspace(p, n_adapters, rank);
         if (workspace_bytes < need)
             return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(workspace_bytes) +
                                             " bytes, " + std::to_string(need) + " needed");

@@ -225,6 +225,26 @@ def test_refusals(monkeypatch):
 
 # ---- GPU -----------------------------------------------------------------------
 
+
+def test_refusals_of_sizes():
+    import partial_sum_reduction_gb300 as s
+    from partial_sum_reduction_gb300 import build
+    build.build()
+    L, m, P = s.lib(), s.shmm, ctypes.c_void_p
+    one, a, n = (P * 1)(0x10000), P(0x30000), ctypes.c_size_t()
+    for I, J, K, ok in ((1 << 31, 8, 8, False), (8, 1 << 23, 8, False), (8, 8, 1 << 23, False),
+                        ((1 << 31) - 1, 8, 8, True), (8, (1 << 23) - 8, (1 << 23) - 8, True)):
+        p = s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K)
+        st = L.shmm_adapters_workspace_size(p.handle, 2, 8, ctypes.byref(n))
+        assert st == (m.OK if ok else m.ERR_SHAPE)
+        if ok:
+            assert n.value >= I * 8 * 4
+            continue
+        assert L.shmm_adapters_forward(p.handle, 2, 8, one, a, a, a, None, None, one, a, None) == m.ERR_SHAPE
+        assert L.shmm_adapters_backward(p.handle, 2, 8, one, one, a, a, a, None, a, None, one, a, a, a, 1 << 40,
+                                        None) == m.ERR_SHAPE
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("layout", list(LAYOUTS))
 @pytest.mark.parametrize("in_dt,out_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
@@ -293,6 +313,35 @@ def test_tall_batches(s, layout, I, J, K, R, n, kind):
     g = torch.Generator().manual_seed(I)
     ids = torch.arange(I) // 211 % (n + 1) - 1 if kind == "runs" else torch.randint(-1, n, (I,), generator=g)
     Case(s, layout, I, J, K, R, n, ids=ids).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("I,R,n,kind", [(33000, 8, 3, "any"), (40001, 20, 2, "any"), (5000, 16, 400, "one"),
+                                        (17000, 40, 305, "one")])
+def test_long_and_lopsided_batches(s, I, R, n, kind, dt):
+    """More rows than one pass over the row adapters marks, and one adapter
+    with nearly all rows among many without any."""
+    ids = None
+    if kind == "one":
+        ids = torch.full((I,), 7)
+        ids[::611] = n - 1
+        ids[5::977] = -1
+    c = Case(s, "whole", I, 72, 40, R, n, dt, dt, ids=ids)
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_an_adapter_without_rows_has_zero_gradients_whatever_its_scale(s, dt):
+    c = Case(s, "whole", 70, 136, 72, 12, 4, dt, dt, ids=torch.arange(70) % 2)
+    c.scale[2], c.scale[3] = float("nan"), float("inf")
+    c.dev["scale"] = c.scale.cuda()
+    C, low = c.forward()
+    dA, dd, du = c.backward(low)
+    assert all(torch.isfinite(t.float()).all() for t in C + dA + [low, dd, du])
+    assert (dd[2:] == 0).all() and (du[2:] == 0).all()
+    assert (dd[:2] != 0).any() and (du[:2] != 0).any()
 
 
 @pytest.mark.gpu
