@@ -267,6 +267,10 @@ def prepare(case, seed):
         import partial_sum_reduction_gb300 as s
         mesh, sa, sb, sc, _ = LAYOUTS[case["layout"]]
         st["plan"] = s.Plan(mesh, sa, sb, sc, T, J, K, case["dtype"], case["dtype"])
+        # a rank's shard is a buffer of its own, which a view of the whole at an odd offset is not
+        for k in ("A", "base", "dC"):
+            if k in st:
+                st[k] = [t.clone() if t.data_ptr() % 16 else t for t in st[k]]
         st["out"] = [torch.empty_like(t) for t in st["base"]]
         if grad:
             st["ddown"] = torch.empty(n, R, J, device="cuda")
