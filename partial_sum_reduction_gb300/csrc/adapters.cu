@@ -96,6 +96,7 @@ struct ExpandK {
     const float *scale;   // or NULL
     const float *s;       // [rows][R]
     int n, R, row_tiles, mt;  // CTAs per box's rows; 16-row tiles of a CTA
+    int beside;           // runs beside the kernel before it (see ExpandEnd)
     int64_t rows, cols;
     int *status;
 };
@@ -795,10 +796,24 @@ struct ExpandShape {
     static size_t smem(int row_tiles) { return kQueue + (size_t)kParts * 16 * row_tiles * kPitch * 2; }
 };
 
+// The backward call's expand comes after the factor gradients' kernel, of
+// which it needs nothing: what it reads was complete before that one's first
+// CTA got past its own wait, and it writes none of that one's inputs (dA is
+// neither A nor dC).  So its CTAs work on the SMs that kernel's last ones
+// leave empty, and wait for it at their end: the end of this kernel is the
+// end of both.
+__device__ __forceinline__ void expand_begin(const ExpandK &k) {
+    if (!k.beside) pdl_wait();
+    pdl_release();
+}
+__device__ __forceinline__ void expand_end(const ExpandK &k) {
+    if (k.beside) pdl_wait();
+}
+
 template <bool FEW, int KT, bool VEC, typename TO>
 __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     expand_mma_kernel(const __grid_constant__ ExpandK k) {
-    pdl_enter();
+    expand_begin(k);
     using Shape = ExpandShape<FEW, KT, TO>;
     constexpr int RP = 16 * KT, PITCH = Shape::kPitch, PARTS = Shape::kParts;
     constexpr int RING = Shape::kRing, WORDS = Shape::kWords;
@@ -867,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     __syncthreads();
     if (c0 >= k.bcols) {
         queue_wait<0>();
+        expand_end(k);
         return;
     }
     const int64_t col = k.col0[rank] * k.bcols;  // of the box in the factor
@@ -1009,6 +1025,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
         slot = slot + 1 == RING ? 0 : slot + 1;
     }
     queue_wait<0>();
+    expand_end(k);
 }
 
 // Rows of the tile without an adapter: base as it is.
@@ -1036,7 +1053,7 @@ __device__ __forceinline__ void copy_rows(const ExpandK &k, int rank, const int 
 // Any types, on CUDA cores: 16 rows x 256 columns, a column per thread.
 template <typename TW, typename TO>
 __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_constant__ ExpandK k) {
-    pdl_enter();
+    expand_begin(k);
     constexpr int ROWS = 16, RMAX = 64;
     __shared__ int ids[ROWS], list[ROWS], count;
     __shared__ float ss[RMAX][ROWS];
@@ -1051,7 +1068,10 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
     }
     __syncthreads();
     const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
-    if (c >= k.bcols) return;
+    if (c >= k.bcols) {
+        expand_end(k);
+        return;
+    }
     const TO *base = (const TO *)k.base[rank];
     TO *out = (TO *)k.out[rank];
     for (int d = blockIdx.z; d < nd; d += gridDim.z) {
@@ -1084,6 +1104,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
             if (ids[i] == a && in_bounds(k.status, at, 1, k.brows * k.bcols)) out[at] = TO(old[i] + acc[i] * scale);
         }
     }
+    expand_end(k);
 }
 
 // ---- outer -----------------------------------------------------------------
@@ -1951,6 +1972,7 @@ int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const Bl
     }
     ExpandK x = {};
     fill_expand(&x, a, dA);
+    x.beside = 1;
     x.w = a.down;
     x.s = a.dlow;
     x.cols = a.J;

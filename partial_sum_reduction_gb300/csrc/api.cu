@@ -1070,6 +1070,10 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int r
             return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(workspace_bytes) +
                                             " bytes, " + std::to_string(need) + " needed");
         if (need && (st = check_ptr(fn, workspace, "workspace", 256)) != SHMM_OK) return st;
+        for (int r = 0; r < p->nranks; ++r)
+            if (dA_r[r] && (dA_r[r] == A_r[r] || dA_r[r] == dC_r[r]))
+                return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": dA_r[" + std::to_string(r) +
+                                                      "] is also an A_r or dC_r, which is read while dA is written");
         std::string err;
         int *status = status_ptr(&err);
         if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);

@@ -226,6 +226,19 @@ def test_refusals(monkeypatch):
 # ---- GPU -----------------------------------------------------------------------
 
 
+def test_refusal_of_a_gradient_over_its_inputs():
+    import partial_sum_reduction_gb300 as s
+    from partial_sum_reduction_gb300 import build
+    build.build()
+    L, m, P = s.lib(), s.shmm, ctypes.c_void_p
+    p = s.Plan("{X:2}", "I_X,J", "J,K", "I_X,K", 8, 16, 16)
+    PP, a = P * 2, P(0x30000)
+    for A, dC, dA in (((1, 2), (3, 4), (5, 2)), ((1, 2), (3, 4), (3, 5)), ((1, 2), (3, 4), (1, 2))):
+        A, dC, dA = (PP(*(0x10000 * v for v in t)) for t in (A, dC, dA))
+        assert L.shmm_adapters_backward(p.handle, 3, 8, dC, A, a, a, a, None, a, None, dA, a, a, P(0x40000), 1 << 40,
+                                        None) == m.ERR_UNSUPPORTED
+
+
 def test_refusals_of_sizes():
     import partial_sum_reduction_gb300 as s
     from partial_sum_reduction_gb300 import build
