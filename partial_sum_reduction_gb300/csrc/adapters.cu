@@ -630,15 +630,27 @@ __global__ void __launch_bounds__(kTcThreads, 2) project_tc_kernel(const __grid_
 template <typename T>
 __device__ __forceinline__ float as_float(T v) { return (float)v; }
 
+// acc += s[0..3] x, the four values of s (in shared memory) in one load.
+__device__ __forceinline__ void fma4(float *acc, const float *s, float x) {
+    const float4 v = *reinterpret_cast<const float4 *>(s);
+    acc[0] = fmaf(v.x, x, acc[0]);
+    acc[1] = fmaf(v.y, x, acc[1]);
+    acc[2] = fmaf(v.z, x, acc[2]);
+    acc[3] = fmaf(v.w, x, acc[3]);
+}
+
 // Any types, on CUDA cores: 32 rows x 16 NR adapter rows per CTA, columns in
-// chunks of 32 through shared memory, the cluster sharing the chunks.
+// chunks of 32 through shared memory, the cluster sharing the chunks.  Shared
+// memory is read four columns at a time (pitch 36: no bank conflicts): one
+// load per value made its reads the bound.
 template <typename TX, typename TW, int NR>
 __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_constant__ ProjK k) {
     pdl_enter();
     constexpr int ROWS = 32, RP = 16 * NR;
     __shared__ int ids[ROWS], list[ROWS], count, block_row[ROWS];
     __shared__ int64_t row_at[ROWS];  // in its row of blocks
-    __shared__ float xs[ROWS][33], ws[RP][33], part[ROWS * RP];
+    __shared__ __align__(16) float xs[ROWS][36], ws[RP][36];
+    __shared__ float part[ROWS * RP];
     cg::cluster_group cluster = cg::this_cluster();
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -688,13 +700,14 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
             __syncthreads();
             fetch(ch + cs);
 #pragma unroll
-            for (int c2 = 0; c2 < 32; ++c2) {
-                const float x0 = xs[ty][c2], x1 = xs[ty + 16][c2];
+            for (int c2 = 0; c2 < 32; c2 += 4) {
+                const float4 x0 = *reinterpret_cast<const float4 *>(&xs[ty][c2]);
+                const float4 x1 = *reinterpret_cast<const float4 *>(&xs[ty + 16][c2]);
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    const float v = ws[tx + 16 * i][c2];
-                    acc[0][i] = fmaf(x0, v, acc[0][i]);
-                    acc[1][i] = fmaf(x1, v, acc[1][i]);
+                    const float4 v = *reinterpret_cast<const float4 *>(&ws[tx + 16 * i][c2]);
+                    acc[0][i] = fmaf(x0.w, v.w, fmaf(x0.z, v.z, fmaf(x0.y, v.y, fmaf(x0.x, v.x, acc[0][i]))));
+                    acc[1][i] = fmaf(x1.w, v.w, fmaf(x1.z, v.z, fmaf(x1.y, v.y, fmaf(x1.x, v.x, acc[1][i]))));
                 }
             }
             __syncthreads();
@@ -1056,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
     expand_begin(k);
     constexpr int ROWS = 16, RMAX = 64;
     __shared__ int ids[ROWS], list[ROWS], count;
-    __shared__ float ss[RMAX][ROWS];
+    __shared__ __align__(16) float ss[RMAX][ROWS];
     const int rank = blockIdx.x / k.row_tiles;
     const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;
     const int64_t t0 = k.row0[rank] * k.brows + l0, t1 = (k.row0[rank] + 1) * k.brows;
@@ -1088,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
             for (int r = 0; r < 8; ++r) {
                 if (r0 + r >= k.R) break;
 #pragma unroll
-                for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(ss[r0 + r][i], v[r], acc[i]);
+                for (int i = 0; i < ROWS; i += 4) fma4(acc + i, &ss[r0 + r][i], v[r]);
             }
         }
         const float scale = k.scale ? k.scale[a] : 1.0f;
@@ -1502,7 +1515,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
-    __shared__ float ss[2][16][16];
+    __shared__ __align__(16) float ss[2][16][16];
     __shared__ float sums[16 * 128];
     cg::cluster_group cluster = cg::this_cluster();
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
@@ -1544,7 +1557,7 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
 #pragma unroll
         for (int u = 0; u < 16; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmaf(ss[half][u][i], x[u], acc[i]);
+            for (int i = 0; i < 16; i += 4) fma4(acc + i, &ss[half][u][i], x[u]);
     }
     if (half)
 #pragma unroll
