@@ -70,12 +70,15 @@
  *                      pairs idle, its tiles run as 256-column halves, one
  *                      round on twice as many pairs.  Both give the same
  *                      bits.
- *   SHMM_PDL=0         the GEMMs and the collective kernels launch in
- *                      plain stream order.  By default each is a
- *                      programmatic dependent of the kernel before it in
- *                      the stream: its set-up may run while that kernel
- *                      finishes, and it touches no global memory until
- *                      that kernel has completed.
+ *   SHMM_PDL=0         the GEMMs, the collective kernels and those of
+ *                      layer normalisation for training and of the
+ *                      adapters launch in plain stream order.  By default
+ *                      each is a programmatic dependent of the kernel
+ *                      before it in the stream: its set-up may run while
+ *                      that kernel finishes, and it touches no global
+ *                      memory until that kernel has completed (within one
+ *                      shmm_adapters_backward: what that kernel neither
+ *                      reads nor writes).  Same bits.
  *   SHMM_LN_BULK=0     LayerNorm (+ all-gather) reads each row with
  *                      per-thread loads instead of staging several rows
  *                      in shared memory through the bulk-copy engine.

@@ -6,17 +6,25 @@
 //   dlow[t]  = scale[a] dC[t] . up[a]^T,   dA[t] = base[t] + dlow[t] . down[a]
 //   dup[a]   = scale[a] sum over a's rows of low[t]^T dC[t]
 //   ddown[a] = sum over a's rows of dlow[t]^T A[t]
-// Both factors lie as [n][R][columns], so three kernels make all of it:
+// Both factors lie as [n][R][columns], so three kernels make all of it (and a
+// fourth sorts the rows by adapter for the last one):
 //   project  out[t] = X[t] . W[a]^T     (low, dlow)
 //   expand   O[t] = base[t] + S[t] . W[a]   (C, dA)
 //   outer    G[a] = sum S[t]^T X[t]     (dup, ddown)
 // R is at most 64, so a row's X and O move 2 bytes per 2 R operations and all
 // three are HBM-bound (64 operations per byte at R = 64, against 280 at the
-// card's tensor rate).  They use warp matrix instructions (mma.sync, bf16
-// operands, fp32 accumulators) whose operands come straight from global
-// memory in 16-byte loads: the order of the summed index is free, so each
-// thread takes eight consecutive values where the instruction's own layout
-// would give it scattered pairs.  fp32 operands take CUDA-core kernels.
+// card's tensor rate).  What each is made of follows from where its operands
+// come from:
+//   project of few rows, and expand: warp matrix instructions (mma.sync, bf16
+//   operands, fp32 accumulators) whose operands come straight from global
+//   memory in 16-byte pieces.  The order of the summed index is free, so each
+//   thread takes eight consecutive values where the instruction's own layout
+//   would give it scattered pairs.  Every byte is used by one thread, once.
+//   project of many rows, and outer: tcgen05.  Both operands go through shared
+//   memory as they lie (one needs a row tile against all its adapters' factors,
+//   the other a group of rows against 128 columns), the sums stay in the TMEM
+//   for 16 instructions and then go on in registers.
+//   fp32 operands: CUDA cores.
 //
 // The low-rank rows stay fp32 between the kernels.  Where they are matrix
 // operands they are split into two bf16 parts (three where the result is
@@ -275,6 +283,9 @@ __device__ __forceinline__ float sum_cluster(cg::cluster_group &cluster, float *
 // through distributed shared memory, so no partial sum goes to HBM).
 // blockIdx.z strides over the tile's distinct adapters.  X and W pieces run
 // ST - 1 chunks ahead through the threads' queues, across adapters too.
+// 96 rows of 64 adapters, 8192 columns, rank 16: 9.3 us for 27 MB; a launch,
+// two dependent reads (the row adapters, then the first chunk) and the join of
+// warps and cluster are some 5 of them.
 template <int MT, int NT>
 struct ProjShape {
     static constexpr int kPieces = 2 * MT + NT;  // per thread and chunk
@@ -425,6 +436,10 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
 // shared memory in order.  Beside the warp instructions above it: the factor
 // is read once per 128 rows instead of per 32, and no thread spends
 // instructions on addresses, which bounded them.
+// 8192 rows: 61 us at 16384 columns, rank 32 (268 MB, 4.4 TB/s); 88 us at 28672
+// columns, rank 16 (470 MB, 5.3 TB/s).  What is left is the start and the join of
+// each cluster (5 us of 15 at 4096 rows of 4096 columns) and the places that
+// clusters of a power of two leave empty (256 of 304 taken in these).
 constexpr int kTcThreads = 320, kTcStages = 3;
 // Chunks summed in the tensor memory before their sum is added in registers:
 // 16 instructions.  The tensor core's own fp32 additions cut instead of
@@ -432,10 +447,11 @@ constexpr int kTcThreads = 320, kTcStages = 3;
 // instruction: 1e-5 over a 7168-column share); in registers they round.
 constexpr int kTcSegment = 4;
 constexpr int kTcSum = 132;  // fp32 of a row of sums: whole 16-byte vectors
-// One CTA per SM: the reading warps' sums of a pass take 64 registers a
-// thread, and a smaller pass would make the tile with the most adapters, which
-// then streams X twice, the one that ends last.
-constexpr int kTcCols = 128;  // factor rows of a pass
+// Two CTAs per SM (61 us against 72 with one and twice the stages, at 8192 x
+// 16384, rank 32).  A pass takes 128 factor rows, whose sums are 64 registers a
+// thread: a smaller one would make the tile with the most adapters, which then
+// streams X twice, the one that ends last.
+constexpr int kTcCols = 128;
 constexpr uint32_t kTcStage = 16384 + kTcCols * 128, kTcRing = kTcStages * kTcStage;
 constexpr size_t kTcSmem = kTcRing + 1024;
 static_assert(128 * kTcSum * 4 <= kTcRing, "the sums take the ring's memory");
@@ -793,6 +809,9 @@ struct Out8 {
 // threads with 64 bytes of a row side by side: base and output move in whole
 // sectors.  The base of up to kRing row tiles is in flight through the
 // threads' queues from the start.
+// 182 us for 8192 x 4096 to each of 8 ranks at rank 32 (1.07 GB, 5.9 TB/s), 82
+// us for 537 MB at rank 16 (6.5 TB/s): HBM.  Few rows (96, 8192 columns, 64
+// adapters): 11.8 us, latency as in project_mma_kernel.
 // blockIdx.x: rank x row tile; blockIdx.z strides over a row tile's adapters
 // (and z = 0 copies the rows without one).
 constexpr int kMaxRowTiles = 16;
@@ -1207,7 +1226,9 @@ __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_
 // and lays their low-rank values down in that order as those kernels' operand:
 // three bf16 parts of RP values each (zeros past R), per row.  A CTA takes one
 // adapter, and CTAs along y share its rows; every CTA counts for itself, from
-// the ids alone, so that they need nothing of one another.
+// the ids alone, so that they need nothing of one another.  Latency: 6 us by
+// itself for 4096 rows, 10 for 8192 at rank 32, all but 3 to 4 of it beside the
+// projection.
 template <int RP>
 __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ ArrangeK k) {
     __shared__ Marks marks;
@@ -1279,6 +1300,12 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
 // parts' rows are added at the end.  The factor side, 3 RP columns, would be
 // the bound of warp matrix instructions at RP = 32 and above (about half their
 // rate), and its operands of their shared-memory reads.
+// 80 us for 8192 rows of 20480 columns at rank 32 (336 MB, 4.2 TB/s), 23 us for
+// 4096 of 8192 at rank 16.  The bytes in flight bound it: 64 KB of X per SM,
+// which come back in some 2.3 us.  With the low values split and the rows listed
+// in every column tile instead (256 columns, one CTA per SM) it was 124 us; with
+// barriers between copying and issuing warps only where a stage changes hands,
+// 85.
 constexpr int kOuterThreads = 256, kOuterCols = 128;  // two CTAs per SM
 template <int RP>
 struct OuterShape {
