@@ -77,6 +77,7 @@ struct ProjK {
     const int *ids;
     const float *scale;   // multiplies the result, or NULL
     float *out;           // [rows][R]
+    int *clear;           // set to 0 (for arrange_kernel), or NULL
     int n, R;
     int64_t rows, cols;
     int *status;
@@ -89,6 +90,7 @@ struct ProjTcK {
     const int *ids;
     const float *scale;
     float *out;
+    int *clear;
     int n, R, b1, row_tiles, per_block, chunks;  // row tiles of a block; 64-column chunks of a block, of X
     int64_t brows, bcols, rows;
     int *status;
@@ -118,8 +120,27 @@ struct OuterJob {
     int64_t cols;
     int tiles;            // column tiles of the launch
 };
+// How the CTAs of a column tile share the rows of an adapter that has more of
+// them than one CTA's part of all the work: the shares have places, numbered
+// over all such adapters, whose CTAs come after those of the n adapters.  The
+// host knows the rows, not whose they are, and one adapter with all of them is
+// a common batch: 6540 rows of one of 17 adapters, 160 x 544, took 298 us with
+// CTAs counted for equal adapters, 66 with these.  (Clusters large enough for
+// that, whose idle CTAs leave at once, cost equal adapters 32 us instead of 23:
+// they have to find room together.)
+struct Shares {
+    int2 *of;             // [n]: the adapter's first place and its number of CTAs (1: no places)
+    int2 *at;             // [most]: adapter and share of a place (adapter -1: none)
+    int *taken;           // places given out
+    int *arrived;         // [tiles][most]: CTAs done, counted at the adapter's first place
+    float *sums;          // [tiles][most]: their sums
+    int most, tiles;      // places and column tiles (times the pieces of R, where CTAs share that too)
+    int group, least;     // rows of a group; groups of a CTA
+    int64_t room;         // CTAs that the card holds at once
+};
 struct OuterK {
     OuterJob job[2];
+    Shares sh;
     const int *order;     // [rows]: the rows with an adapter, by adapter, each one's ascending
     const int *start;     // [n + 1]: adapter a's are order[start[a]] .. order[start[a + 1] - 1]
     int n, R;
@@ -127,6 +148,7 @@ struct OuterK {
     int *status;
 };
 struct ArrangeK {
+    Shares sh;
     const int *ids;
     const float *s[2];    // either may be NULL
     bf16 *parts[2];
@@ -309,6 +331,7 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
     const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+    if (k.clear && threadIdx.x == 0) *k.clear = 0;
     const int nd = distinct<ROWS>(k.ids, t0, k.rows, k.n, ids, list, &count, k.status);
     // rows without an adapter: zeros
     if (blockIdx.z == 0 && cr == 0)
@@ -486,6 +509,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) project_tc_kernel(const __grid_
     shmm_tc::fence_before();
     const int brow = blockIdx.x / k.row_tiles, l0 = (int)(blockIdx.x % k.row_tiles) * ROWS;
     const int64_t t0 = brow * k.brows + l0, t1 = (brow + 1) * k.brows;
+    if (k.clear && threadIdx.x == 0) *k.clear = 0;
     const int nd = distinct<ROWS>(k.ids, t0, t1, k.n, ids, list, &count, k.status);
     shmm_tc::fence_after();
     // Only now may the next kernel's CTAs come: one that takes all of an SM's
@@ -671,6 +695,7 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
     const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+    if (k.clear && threadIdx.x == 0) *k.clear = 0;
     const int nd = distinct<ROWS>(k.ids, t0, k.rows, k.n, ids, list, &count, k.status);
     if (blockIdx.z == 0 && cr == 0)
         for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
@@ -1145,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 // kWindow rows (one read of the row adapters), with how many lie before each
 // 32-row word, then turns the marks into lists of up to kList rows, ascending.
 constexpr int kWindow = 16384, kList = 1024;
+constexpr int kMostShares = 16;  // CTAs of one adapter and column tile
 struct Marks {
     uint32_t bits[kWindow / 32];
     int before[kWindow / 32];
@@ -1232,26 +1258,39 @@ __device__ __forceinline__ void list_rows(const Marks &marks, int64_t w0, int64_
 template <int RP>
 __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ ArrangeK k) {
     __shared__ Marks marks;
-    __shared__ int list[kList], sum[16];
+    __shared__ int list[kList], sum[16], valid_sum[16];
     const int a = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    // rows of the adapters below this one: where its own begin
-    int below = 0;
-    if (a > 0) {
-        const int64_t n4 = (reinterpret_cast<uintptr_t>(k.ids) & 15) ? 0 : k.rows / 4;
+    // rows of the adapters below this one, where its own begin, and of all
+    int below = 0, valid = 0;
+    const int64_t n4 = (reinterpret_cast<uintptr_t>(k.ids) & 15) ? 0 : k.rows / 4;
+    auto count = [&](int id) {
+        below += (unsigned)id < (unsigned)a;
+        valid += (unsigned)id < (unsigned)k.n;
+    };
 #pragma unroll 4
-        for (int64_t i = threadIdx.x; i < n4; i += 512) {
-            const int4 v = in_bounds(k.status, i * 4, 4, k.rows) ? reinterpret_cast<const int4 *>(k.ids)[i] : make_int4(a, a, a, a);
-            below += ((unsigned)v.x < (unsigned)a) + ((unsigned)v.y < (unsigned)a) + ((unsigned)v.z < (unsigned)a) +
-                     ((unsigned)v.w < (unsigned)a);
-        }
-        for (int64_t i = n4 * 4 + threadIdx.x; i < k.rows; i += 512) below += (unsigned)k.ids[i] < (unsigned)a;
-        below = __reduce_add_sync(0xffffffffu, below);
+    for (int64_t i = threadIdx.x; i < n4; i += 512) {
+        const int4 v = in_bounds(k.status, i * 4, 4, k.rows) ? reinterpret_cast<const int4 *>(k.ids)[i] : make_int4(-1, -1, -1, -1);
+        count(v.x);
+        count(v.y);
+        count(v.z);
+        count(v.w);
     }
-    if (lane == 0) sum[warp] = below;
+    for (int64_t i = n4 * 4 + threadIdx.x; i < k.rows; i += 512) count(k.ids[i]);
+    below = __reduce_add_sync(0xffffffffu, below);
+    valid = __reduce_add_sync(0xffffffffu, valid);
+    if (lane == 0) {
+        sum[warp] = below;
+        valid_sum[warp] = valid;
+    }
     __syncthreads();
-    below = 0;
+    below = valid = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) below += sum[i];
+    for (int i = 0; i < 16; ++i) {
+        below += sum[i];
+        valid += valid_sum[i];
+    }
+    if (a == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < k.sh.tiles * k.sh.most; i += 512) k.sh.arrived[i] = 0;
     int at = below;  // place of the window's first row
     for (int64_t w0 = 0; w0 < k.rows; w0 += kWindow) {
         const int total = mark_rows<16>(k.ids, w0, k.rows, a, marks, k.status);
@@ -1288,11 +1327,54 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
     if (threadIdx.x == 0 && blockIdx.y == 0) {
         k.start[a] = below;
         if (a == k.n - 1) k.start[k.n] = at;
+        // A CTA's part of all the work, and how many of them this adapter is.
+        // Which places it gets depends on who asks first; the sums do not.
+        int first = 0, want = 1;
+        if (k.sh.most) {
+            const int64_t groups = (at - below + k.sh.group - 1) / k.sh.group, all = (valid + k.sh.group - 1) / k.sh.group;
+            int64_t each = (all * k.sh.tiles + k.sh.room - 1) / k.sh.room;
+            if (each < k.sh.least) each = k.sh.least;
+            const int64_t w = groups / each;  // whole parts only: all CTAs still fit the card at once
+            want = (int)(w < 1 ? 1 : w > kMostShares ? kMostShares : w);
+            if (want > 1) {
+                first = atomicAdd(k.sh.taken, want);
+                const bool fits = first + want <= k.sh.most;  // always (see Grain)
+                for (int i = 0; i < want && first + i < k.sh.most; ++i) k.sh.at[first + i] = make_int2(fits ? a : -1, i);
+                if (!fits) want = 1;
+            }
+        }
+        k.sh.of[a] = make_int2(first, want);
     }
 }
 
-// A CTA takes one adapter and 128 columns, and a cluster along z shares the
-// adapter's rows (its sums meet through distributed shared memory, in order).
+// What the CTAs of a factor gradient's kernel do at the start: which adapter
+// and share blockIdx.y is (false: none) ...
+__device__ __forceinline__ bool take_share(const OuterK &k, int *a, int *share, int2 *of) {
+    *a = blockIdx.y;
+    *share = 0;
+    if (*a >= k.n) {
+        const int place = *a - k.n;
+        if (place >= *k.sh.taken) return false;
+        const int2 at = k.sh.at[place];
+        if (at.x < 0 || at.y == 0) return false;
+        *a = at.x;
+        *share = at.y;
+    }
+    *of = k.sh.of[*a];
+    return true;
+}
+// ... and at the end, with their own sums of `values` floats in memory: true
+// for the last of an adapter's CTAs, which then adds all of them in order.
+__device__ __forceinline__ bool last_share(const OuterK &k, int tile, int2 of, int *flag) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) *flag = atomicAdd(&k.sh.arrived[tile * k.sh.most + of.x], 1) == of.y - 1;
+    __syncthreads();
+    __threadfence();
+    return *flag;
+}
+
+// A CTA takes one adapter, or a share of its rows, and 128 columns.
 // Rows go in groups of 64, on tcgen05.  Both operands are MN-major, as their
 // rows lie in memory: X's, gathered by index, 64 x 128; and the arranged low
 // values', whose three parts stand beside one another, 64 x 3 RP, so that one
@@ -1300,7 +1382,7 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
 // parts' rows are added at the end.  The factor side, 3 RP columns, would be
 // the bound of warp matrix instructions at RP = 32 and above (about half their
 // rate), and its operands of their shared-memory reads.
-// 80 us for 8192 rows of 20480 columns at rank 32 (336 MB, 4.2 TB/s), 23 us for
+// 80 us for 8192 rows of 20480 columns at rank 32 (336 MB, 4.2 TB/s), 24 us for
 // 4096 of 8192 at rank 16.  The bytes in flight bound it: 64 KB of X per SM,
 // which come back in some 2.3 us.  With the low values split and the rows listed
 // in every column tile instead (256 columns, one CTA per SM) it was 124 us; with
@@ -1319,7 +1401,7 @@ struct OuterShape {
     static constexpr uint32_t kRing = kStages * kStage;
     static constexpr uint32_t kZeros = RP == 64 ? 8192 : 0;  // the lower half of the third part's product
     static constexpr int kPitch = 132;                       // fp32
-    static constexpr size_t kResult = (size_t)kRows * kPitch * 4 + (size_t)RP * kOuterCols * 4;  // product, sum
+    static constexpr size_t kResult = (size_t)kRows * kPitch * 4;
     static constexpr size_t kSmem = (kResult > kRing + kZeros ? kResult : kRing + kZeros) + 1024;
 };
 constexpr int kOuterSegment = 4;  // groups summed in the tensor memory before registers take them (see kTcSegment)
@@ -1331,18 +1413,20 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
     using Shape = OuterShape<RP>;
     constexpr int S = Shape::kStages;
     constexpr int AHEAD = S - 1;  // groups asked for early
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, last;
     __shared__ const bf16 *row_at[kOuterList];  // rows' first values of this tile's block, by place in the share
     __shared__ uint32_t tmem_at;
     __shared__ __align__(8) uint64_t bars[S];  // a stage's products are done
     extern __shared__ uint8_t raw_smem[];
     uint8_t *smem = raw_smem + (1024 - (shmm_dev::smem_u32(raw_smem) & 1023)) % 1024;
     const uint32_t smem_at = shmm_dev::smem_u32(smem);
-    cg::cluster_group cluster = cg::this_cluster();
-    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    int a, cr;  // share cr of the adapter's
+    int2 of;
+    if (!take_share(k, &a, &cr, &of)) return;
+    const int cs = of.y;
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
-    const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y;
+    const int tile = blockIdx.x - (which ? k.job[0].tiles : 0);
     const int bcols = (int)J.x.bcols, per_block = (bcols + kOuterCols - 1) / kOuterCols, blk = tile / per_block;
     const int c0 = (tile - blk * per_block) * kOuterCols;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -1493,7 +1577,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
         }
     };
     float *piece = reinterpret_cast<float *>(smem);                // [kRows][kPitch]
-    float *sums = piece + Shape::kRows * Shape::kPitch;            // [RP][128]
+    float *sums = k.sh.sums + ((int64_t)blockIdx.x * k.sh.most + of.x) * (RP * kOuterCols);  // the first share's
     auto add = [](float4 &t, const float4 &v) {
         t.x += v.x;
         t.y += v.y;
@@ -1513,23 +1597,17 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
 #pragma unroll
         for (int h = Shape::kBands - 1; h >= 0; --h)
             add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
-        if (cs > 1) *reinterpret_cast<float4 *>(sums + r * kOuterCols + j) = t;
+        if (cs > 1) __stcg(reinterpret_cast<float4 *>(sums + (int64_t)cr * RP * kOuterCols + r * kOuterCols + j), t);
         else put(r, j, t);
     }
-    if (cs > 1) {
-        cluster.sync();
-        for (int e = cr * kOuterThreads + threadIdx.x; e < k.R * 32; e += cs * kOuterThreads) {
-            float4 v[8], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-                if (b < cs) v[b] = *cluster.map_shared_rank(reinterpret_cast<float4 *>(sums) + e, b);
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-                if (b < cs) add(t, v[b]);
+    if (cs > 1 && last_share(k, blockIdx.x, of, &last))
+        for (int e = threadIdx.x; e < k.R * 32; e += kOuterThreads) {
+            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int b = 0; b < cs; ++b)
+                add(t, __ldcg(reinterpret_cast<const float4 *>(sums + (int64_t)b * RP * kOuterCols + e * 4)));
             put(e / 32, e % 32 * 4, t);
         }
-        cluster.sync();  // nobody leaves with what another CTA still reads
-    }
     shmm_tc::fence_before();
     __syncthreads();
     shmm_tc::fence_after();
@@ -1537,18 +1615,21 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
 }
 
 // Any types, on CUDA cores: one adapter, 128 columns and 16 adapter rows per
-// CTA, a cluster along z sharing the adapter's rows; the halves of a CTA take
-// every other group of 16 of them.
+// CTA, or a share of the adapter's rows; the halves of a CTA take every other
+// group of 16 of them.
 template <typename TX>
 __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_constant__ OuterK k) {
     pdl_enter();
     __shared__ __align__(16) float ss[2][16][16];
     __shared__ float sums[16 * 128];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int cr = (int)cluster.block_rank(), cs = (int)cluster.num_blocks();
+    __shared__ int last;
+    int a, cr;  // share cr of the adapter's
+    int2 of;
+    if (!take_share(k, &a, &cr, &of)) return;
+    const int cs = of.y;
     const int which = (int)blockIdx.x >= k.job[0].tiles;
     const OuterJob &J = k.job[which];
-    const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), a = blockIdx.y, r0 = blockIdx.z / cs * 16;
+    const int tile = blockIdx.x - (which ? k.job[0].tiles : 0), r0 = blockIdx.z * 16;
     const int half = threadIdx.x / 128, th = threadIdx.x % 128;
     const int bcols = (int)J.x.bcols, per_block = (bcols + 127) / 128, blk = tile / per_block;
     const int c0 = (tile - blk * per_block) * 128, c = c0 + th;
@@ -1593,16 +1674,23 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
     if (!half)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sums[i * 128 + th] += acc[i];
-    if (cs > 1) cluster.sync();
-    else __syncthreads();
+    __syncthreads();
     const float scale = J.scale && total > 0 ? J.scale[a] : 1.0f;  // no rows: zeros whatever it is
-    for (int e = cr * kThreads + threadIdx.x; e < 16 * 128; e += cs * kThreads) {
-        const float v = cs > 1 ? sum_cluster(cluster, sums + e, cs) : sums[e];
+    const int piece = blockIdx.z * gridDim.x + blockIdx.x;  // a tile's 16 adapter rows
+    float *shared_sums = k.sh.sums + ((int64_t)piece * k.sh.most + of.x) * (16 * 128);
+    if (cs > 1) {
+        for (int e = threadIdx.x; e < 16 * 128; e += kThreads) __stcg(shared_sums + cr * (16 * 128) + e, sums[e]);
+        if (!last_share(k, piece, of, &last)) return;
+    }
+    for (int e = threadIdx.x; e < 16 * 128; e += kThreads) {
+        float v = cs > 1 ? 0.0f : sums[e];
+        if (cs > 1)
+#pragma unroll 4
+            for (int b = 0; b < cs; ++b) v += __ldcg(shared_sums + b * (16 * 128) + e);
         const int r = r0 + e / 128, col = c0 + e % 128;
         const int64_t at = ((int64_t)a * k.R + r) * J.cols + (int64_t)blk * bcols + col;
         if (r < k.R && col < bcols && in_bounds(k.status, at, 1, (int64_t)k.n * k.R * J.cols)) J.out[at] = v * scale;
     }
-    if (cs > 1) cluster.sync();  // nobody leaves with what another CTA still reads
 }
 
 // ---- launches --------------------------------------------------------------
@@ -1727,6 +1815,7 @@ cudaError_t project_tc(const ProjK &k, int b0, cudaStream_t s) {
     t.ids = k.ids;
     t.scale = k.scale;
     t.out = k.out;
+    t.clear = k.clear;
     t.n = k.n;
     t.R = k.R;
     t.b1 = k.x.b1;
@@ -1835,13 +1924,8 @@ cudaError_t outer_tc(const OuterK &k, cudaStream_t s) {
     static shmm::PerDevice<int> done;
     cudaError_t e = opt_in(kern, Shape::kSmem, &done);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = k.job[0].tiles + k.job[1].tiles;
-    // Shares of an adapter's rows until the card is full or a share is down to
-    // four groups of rows.
-    int cs = 1;
-    while (cs < 8 && tiles * k.n * cs * 2 <= 2 * sms() && k.rows / k.n >= 512 * cs) cs *= 2;
-    return launch_pdl_cluster(kern, dim3((unsigned)tiles, (unsigned)k.n, cs), dim3(1, 1, cs), dim3(kOuterThreads),
-                              Shape::kSmem, s, k);
+    return launch_pdl(kern, dim3((unsigned)(k.job[0].tiles + k.job[1].tiles), (unsigned)(k.n + k.sh.most)),
+                      dim3(kOuterThreads), Shape::kSmem, s, k);
 }
 
 int padded(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // adapter rows of a product
@@ -1849,7 +1933,7 @@ int padded(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // adapter rows 
 cudaError_t arrange(const ArrangeK &k, cudaStream_t s) {
     shmm::count_launch();
     // CTAs for a wave of two per SM, of 64 rows and more.
-    int64_t y = 2 * sms() / k.n, most = k.rows / k.n / 64;
+    int64_t y = 2 * sms() / k.n, most = k.rows / 64;
     if (y > most) y = most;
     const dim3 g((unsigned)k.n, (unsigned)(y > 1 ? y : 1));
     if (k.R <= 16) return launch_pdl(arrange_kernel<16>, g, dim3(512), 0, s, k);
@@ -1860,26 +1944,13 @@ cudaError_t arrange(const ArrangeK &k, cudaStream_t s) {
 // One or both gradient products (job[1].cols == 0: one) of one type.
 cudaError_t outer(OuterK k, shmm_dtype_t xt, cudaStream_t s) {
     shmm::count_launch();
-    if (xt == SHMM_F32) {
-        int64_t tiles = 0;
-        for (OuterJob &j : k.job) {
-            j.tiles = j.cols ? (int)((j.x.bcols + 127) / 128 * j.x.b1) : 0;
-            tiles += j.tiles;
-        }
-        // Shares of an adapter's rows until the card is full or a share is
-        // down to 32 rows.
-        const int z = (k.R + 15) / 16;
-        int cs = 1;
-        while (cs < 8 && tiles * k.n * z * cs * 2 <= 4 * sms() && k.rows / k.n >= 64 * cs) cs *= 2;
-        return launch_pdl_cluster(outer_simt_kernel<float>, dim3((unsigned)tiles, (unsigned)k.n, z * cs), dim3(1, 1, cs),
-                                  dim3(kThreads), 0, s, k);
-    }
+    if (xt == SHMM_F32)
+        return launch_pdl(outer_simt_kernel<float>,
+                          dim3((unsigned)(k.job[0].tiles + k.job[1].tiles), (unsigned)(k.n + k.sh.most), (k.R + 15) / 16),
+                          dim3(kThreads), 0, s, k);
     bool vec = true;
-    for (OuterJob &j : k.job) {
-        if (!j.cols) continue;
-        j.tiles = (int)((j.x.bcols + kOuterCols - 1) / kOuterCols * j.x.b1);
-        vec = vec && j.x.bcols % 8 == 0;
-    }
+    for (const OuterJob &j : k.job)
+        if (j.cols) vec = vec && j.x.bcols % 8 == 0;
     if (k.R <= 16) return vec ? outer_tc<16, true>(k, s) : outer_tc<16, false>(k, s);
     if (k.R <= 32) return vec ? outer_tc<32, true>(k, s) : outer_tc<32, false>(k, s);
     return vec ? outer_tc<64, true>(k, s) : outer_tc<64, false>(k, s);
@@ -1904,17 +1975,41 @@ void fill_expand(ExpandK *k, const shmm::AdapterArgs &a, const shmm::RankBoxes &
 
 namespace shmm {
 
+// Places for shares (see Shares).  An adapter with w >= 2 of them has w parts'
+// worth of groups, the last one perhaps of a single row: at most twice as many
+// as its rows fill.  So all places together are at most 2 (room / tiles) per
+// column tile.  None when half the card's CTAs or more have a column tile of
+// their own, or for few rows.
+struct Grain {
+    int per_sm, group, least;  // CTAs per SM, rows of a group, groups of a CTA
+    int64_t room() const { return (int64_t)per_sm * sms(); }
+    bool shared(int64_t rows) const { return rows > (int64_t)group * least; }
+    int most(int64_t rows, int64_t n, int64_t tiles) const {
+        if (tiles * 2 > room() || !shared(rows)) return 0;
+        const int64_t most = 2 * room() / tiles + 2;
+        return n + most > 65535 ? 0 : (int)most;
+    }
+};
+static Grain grain(bool tc) { return tc ? Grain{2, 64, 4} : Grain{4, 32, 1}; }
+
 // Workspace of the backward call: the gradient of the low values, then the
-// rows' arrangement.
+// rows' arrangement and the shares'.
 struct Rooms {
-    size_t start, order, parts[2], all;
+    size_t start, order, of, at, taken, arrived, sums, parts[2], all;
 };
 static Rooms rooms(int64_t rows, int n, int R, bool tc) {
     auto up = [](int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); };
+    const Grain g = grain(tc);
+    const int64_t room = g.room(), places = g.shared(rows) ? 3 * room : 0;  // over all tiles: most * tiles <= 3 room
     Rooms r;
     r.start = up(rows * R * 4);
     r.order = r.start + up(((int64_t)n + 1) * 4);
-    r.parts[0] = r.order + up(rows * 4);
+    r.of = r.order + up(rows * 4);
+    r.at = r.of + up((int64_t)n * 8);
+    r.taken = r.at + (places ? up((2 * room + 2) * 8) : 0);
+    r.arrived = r.taken + 256;
+    r.sums = r.arrived + up(places * 4);
+    r.parts[0] = r.sums + up(places * (tc ? padded(R) : 16) * 128 * 4);
     r.parts[1] = r.parts[0] + (tc ? up(rows * 6 * padded(R)) : 0);
     r.all = rows ? r.parts[1] + (tc ? up(rows * 6 * padded(R)) : 0) : 0;
     return r;
@@ -1968,10 +2063,11 @@ int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const Bl
     p.rows = a.rows;
     p.cols = a.K;
     p.status = status;
-    if ((e = project(p, out_dt, in_dt, s)) != cudaSuccess) return (int)e;
     const bool tc[2] = {out_dt == SHMM_BF16, in_dt == SHMM_BF16};  // dup, ddown
     const Rooms at = rooms(a.rows, a.n, a.R, tc[0] || tc[1]);
     char *ws = reinterpret_cast<char *>(a.dlow);
+    p.clear = reinterpret_cast<int *>(ws + at.taken);
+    if ((e = project(p, out_dt, in_dt, s)) != cudaSuccess) return (int)e;
     OuterK o = {};
     o.order = reinterpret_cast<int *>(ws + at.order);
     o.start = reinterpret_cast<int *>(ws + at.start);
@@ -1991,7 +2087,28 @@ int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const Bl
     down.parts = reinterpret_cast<bf16 *>(ws + at.parts[1]);
     down.out = a.ddown;
     down.cols = a.J;
+    const bool one = in_dt == out_dt;  // one launch for both
+    for (int j = 0; j < 2; ++j) {
+        OuterJob &J = j ? down : up;
+        J.tiles = (int)((J.x.bcols + kOuterCols - 1) / kOuterCols * J.x.b1);
+    }
+    Shares &sh = o.sh;
+    sh.of = reinterpret_cast<int2 *>(ws + at.of);
+    sh.at = reinterpret_cast<int2 *>(ws + at.at);
+    sh.taken = reinterpret_cast<int *>(ws + at.taken);
+    sh.arrived = reinterpret_cast<int *>(ws + at.arrived);
+    sh.sums = reinterpret_cast<float *>(ws + at.sums);
+    if (one) {
+        const int64_t tiles = (int64_t)(up.tiles + down.tiles) * (tc[0] ? 1 : (a.R + 15) / 16);
+        const Grain g = grain(tc[0]);
+        sh.room = g.room();
+        sh.group = g.group;
+        sh.least = g.least;
+        sh.most = g.most(a.rows, a.n, tiles);
+        sh.tiles = (int)tiles;
+    }
     ArrangeK g = {};
+    g.sh = sh;
     g.ids = a.ids;
     g.order = reinterpret_cast<int *>(ws + at.order);
     g.start = reinterpret_cast<int *>(ws + at.start);
@@ -2004,9 +2121,9 @@ int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const Bl
     g.status = status;
     if ((e = arrange(g, s)) != cudaSuccess) return (int)e;
     o.job[0] = up;
-    if (in_dt == out_dt) o.job[1] = down;
+    if (one) o.job[1] = down;
     if ((e = outer(o, out_dt, s)) != cudaSuccess) return (int)e;
-    if (in_dt != out_dt) {
+    if (!one) {
         o.job[0] = down;
         if ((e = outer(o, in_dt, s)) != cudaSuccess) return (int)e;
     }

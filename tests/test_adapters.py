@@ -346,6 +346,19 @@ def test_long_and_lopsided_batches(s, I, R, n, kind, dt):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("layout,I,J,K,R,n,few", [("columns", 6540, 160, 272, 32, 17, 0), ("whole", 9000, 264, 520, 16, 3, 200),
+                                                  ("rows", 4100, 136, 72, 64, 9, 1300), ("whole", 2600, 40, 24, 5, 2, 65)])
+def test_an_adapter_with_most_rows(s, layout, I, J, K, R, n, few, dt):
+    """One adapter's rows shared by many CTAs; `few` rows among the others."""
+    g = torch.Generator().manual_seed(I)
+    ids = torch.full((I,), n - 1)
+    at = torch.randperm(I, generator=g)[:few]
+    ids[at] = torch.randint(0, n - 1, (few,), generator=g)
+    Case(s, layout, I, J, K, R, n, dt, dt, ids=ids).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_an_adapter_without_rows_has_zero_gradients_whatever_its_scale(s, dt):
     c = Case(s, "whole", 70, 136, 72, 12, 4, dt, dt, ids=torch.arange(70) % 2)
     c.scale[2], c.scale[3] = float("nan"), float("inf")
@@ -456,6 +469,40 @@ def test_no_rows(s):
         plan.adapters_backward([e(0, 200)], [e(0, 40)], ids, d, u, None, low, None, [e(0, 40)], dd, du, None)
         s.shmm_sync_status()
         assert (dd == 0).all() and (du == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("I,J,K,R,n,dt", [(130, 96, 96, 12, 300, "f32"), (97, 40, 36, 3, 2, "f32"), (191, 24, 8, 64, 7, "f32"),
+                                          (257, 136, 72, 16, 2, "bf16"), (900, 264, 136, 32, 5, "bf16"),
+                                          (2600, 72, 520, 64, 3, "bf16"), (2, 8, 8, 1, 9, "bf16")])
+def test_nothing_outside_its_buffers(s, I, J, K, R, n, dt):
+    """Every buffer, the workspace to the byte, lies between guard bytes."""
+    c = Case(s, "whole", I, J, K, R, n, dt, dt, ids=(torch.arange(I) % 29 == 3).int() * (n - 1))
+    pool = torch.full((64 << 20,), 0x5a, dtype=torch.uint8, device="cuda")
+    guard = torch.ones(pool.numel(), dtype=torch.bool, device="cuda")
+    end = [4096]
+
+    def take(nbytes):
+        lo, end[0] = end[0], end[0] + (nbytes + 8191) // 256 * 256
+        guard[lo:lo + nbytes] = False
+        return pool[lo:lo + nbytes]
+
+    def put(t, fill=None):
+        d = take(t.numel() * t.element_size()).view(t.dtype).view(t.shape)
+        return d.copy_(t) if fill is None else d.fill_(fill)
+
+    nan = float("nan")
+    A, dC, base, dbase, down, up, scale, ids = (put(t) for t in (c.A, c.dC, c.base, c.dbase, c.down, c.up, c.scale, c.ids))
+    C, dA, low = put(c.base, nan), put(c.dbase, nan), put(torch.empty(I, R), nan)
+    dd, du = put(torch.empty(n, R, J), nan), put(torch.empty(n, R, K), nan)
+    ws = take(c.plan.adapters_workspace_size(n, R))
+    assert end[0] < pool.numel()
+    c.plan.adapters_forward([A], ids, down, up, scale, [base], [C], low)
+    c.plan.adapters_backward([dC], [A], ids, down, up, scale, low, [dbase], [dA], dd, du, ws)
+    s.shmm_sync_status()
+    assert (pool[guard] == 0x5a).all()
+    c.check_forward([C], low)
+    c.check_backward(low, [dA], dd, du)
 
 
 @pytest.mark.gpu
