@@ -1555,8 +1555,8 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
     for (int f = ngroups > S ? ngroups - S : 0; f < ngroups; ++f)
         shmm_dev::mbar_wait(shmm_dev::smem_u32(&bars[f % S]), (f / S) & 1, &abort_flag, k.status, false);
     __syncthreads();
-    // Result through shared memory, the parts' rows added there; the cluster's
-    // sums then meet.
+    // Result through shared memory, the parts' rows added there; then the
+    // shares' sums.
     const float scale = J.scale && total > 0 ? J.scale[a] : 1.0f;  // no rows: zeros whatever it is
     float *out = J.out + (int64_t)a * k.R * J.cols + (int64_t)blk * bcols + c0;
     const bool whole = (J.cols & 3) == 0 && (bcols & 3) == 0 && (reinterpret_cast<uintptr_t>(J.out) & 15) == 0;
