@@ -472,6 +472,20 @@ def test_no_rows(s):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [64900, 65535])
+def test_as_many_adapters_as_there_may_be(s, n, dt):
+    """The launches' second grid dimension is one adapter each; few of them
+    have rows, one has most."""
+    ids = torch.full((900,), n - 1)
+    ids[::3] = torch.arange(300) * 211
+    c = Case(s, "whole", 900, 24, 16, 2, n, dt, dt, ids=ids)
+    used = torch.unique(c.ids).tolist()
+    c.rows_of = lambda: [(a, (c.ids == a).nonzero().flatten()) for a in used]
+    c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("I,J,K,R,n,dt", [(130, 96, 96, 12, 300, "f32"), (97, 40, 36, 3, 2, "f32"), (191, 24, 8, 64, 7, "f32"),
                                           (257, 136, 72, 16, 2, "bf16"), (900, 264, 136, 32, 5, "bf16"),
                                           (2600, 72, 520, 64, 3, "bf16"), (2, 8, 8, 1, 9, "bf16")])
