@@ -77,8 +77,8 @@
  *                      before it in the stream: its set-up may run while
  *                      that kernel finishes, and it touches no global
  *                      memory until that kernel has completed (within one
- *                      shmm_adapters_backward: what that kernel neither
- *                      reads nor writes).  Same bits.
+ *                      call of the adapters' entry points: none that
+ *                      that kernel writes).  Same bits.
  *   SHMM_LN_BULK=0     LayerNorm (+ all-gather) reads each row with
  *                      per-thread loads instead of staging several rows
  *                      in shared memory through the bulk-copy engine.

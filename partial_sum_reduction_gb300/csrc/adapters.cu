@@ -836,7 +836,7 @@ struct Out8 {
 // threads' queues from the start.
 // 182 us for 8192 x 4096 to each of 8 ranks at rank 32 (1.07 GB, 5.9 TB/s), 82
 // us for 537 MB at rank 16 (6.5 TB/s): HBM.  Few rows (96, 8192 columns, 64
-// adapters): 11.8 us, latency as in project_mma_kernel.
+// adapters): 12 us, one of them beside the projection; latency as in project_mma_kernel.
 // blockIdx.x: rank x row tile; blockIdx.z strides over a row tile's adapters
 // (and z = 0 copies the rows without one).
 constexpr int kMaxRowTiles = 16;
@@ -853,15 +853,17 @@ struct ExpandShape {
     static size_t smem(int row_tiles) { return kQueue + (size_t)kParts * 16 * row_tiles * kPitch * 2; }
 };
 
-// The backward call's expand comes after the factor gradients' kernel, of
-// which it needs nothing: what it reads was complete before that one's first
-// CTA got past its own wait, and it writes none of that one's inputs (dA is
-// neither A nor dC).  So its CTAs work on the SMs that kernel's last ones
-// leave empty, and wait for it at their end: the end of this kernel is the
+// What may be done before the kernel in front of this one is over.  In both
+// calls that kernel has itself waited for everything that the call was given,
+// so row adapters, factors and base can be read, and factors and base are on
+// their way when it ends; the forward call's is the projection, whose low rows
+// are waited for.  The backward call's is the factor gradients' kernel, of
+// which expand needs nothing, while it writes none of that one's inputs (dA is
+// neither A nor dC): its CTAs work on the SMs that kernel's last ones leave
+// empty, and wait for it at their end, so that the end of this kernel is the
 // end of both.
-__device__ __forceinline__ void expand_begin(const ExpandK &k) {
+__device__ __forceinline__ void expand_low(const ExpandK &k) {
     if (!k.beside) pdl_wait();
-    pdl_release();
 }
 __device__ __forceinline__ void expand_end(const ExpandK &k) {
     if (k.beside) pdl_wait();
@@ -870,7 +872,7 @@ __device__ __forceinline__ void expand_end(const ExpandK &k) {
 template <bool FEW, int KT, bool VEC, typename TO>
 __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     expand_mma_kernel(const __grid_constant__ ExpandK k) {
-    expand_begin(k);
+    pdl_release();
     using Shape = ExpandShape<FEW, KT, TO>;
     constexpr int RP = 16 * KT, PITCH = Shape::kPitch, PARTS = Shape::kParts;
     constexpr int RING = Shape::kRing, WORDS = Shape::kWords;
@@ -916,21 +918,28 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     };
 #pragma unroll
     for (int m = 0; m < RING; ++m) ask(m, m);
-    int my_id = -1;  // of row threadIdx.x; on its way while the low rows are split
+    int my_id = -1;  // of row threadIdx.x
     if ((int)threadIdx.x < nrows && in_bounds(k.status, t0 + threadIdx.x, 1, k.rows)) my_id = k.ids[t0 + threadIdx.x];
+    auto low_rows = [&] {  // their parts into shared memory
+        expand_low(k);
 #pragma unroll 4
-    for (int i = threadIdx.x; i < ROWS * RP / 2; i += kThreads) {
-        const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
-        float lo = 0.0f, hi = 0.0f;
-        if (row < nrows) {
-            if (r < k.R) lo = k.s[(t0 + row) * k.R + r];
-            if (r + 1 < k.R) hi = k.s[(t0 + row) * k.R + r + 1];
-        }
-        uint32_t p[PARTS];
-        split<PARTS>(lo, hi, p);
+        for (int i = threadIdx.x; i < ROWS * RP / 2; i += kThreads) {
+            const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
+            float lo = 0.0f, hi = 0.0f;
+            if (row < nrows) {
+                if (r < k.R) lo = k.s[(t0 + row) * k.R + r];
+                if (r + 1 < k.R) hi = k.s[(t0 + row) * k.R + r + 1];
+            }
+            uint32_t p[PARTS];
+            split<PARTS>(lo, hi, p);
 #pragma unroll
-        for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(ss + (h * ROWS + row) * PITCH + r) = p[h];
-    }
+            for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint32_t *>(ss + (h * ROWS + row) * PITCH + r) = p[h];
+        }
+    };
+    // FEW: waited for after the first factor pieces are on their way.  Else at
+    // once, while the row adapters are (after them it costs a start of its own:
+    // 192 against 182 us in the longest case above).
+    if constexpr (!FEW) low_rows();
     if ((int)threadIdx.x < ROWS) {
         my_id = my_id >= 0 && my_id < k.n ? my_id : -1;
         ids[threadIdx.x] = my_id;
@@ -938,6 +947,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     }
     __syncthreads();
     if (c0 >= k.bcols) {
+        if constexpr (FEW) {
+            low_rows();
+            __syncthreads();
+        }
         queue_wait<0>();
         expand_end(k);
         return;
@@ -1000,6 +1013,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
         if constexpr (AHEAD > 0) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) ask_w(i);
+        }
+        if constexpr (FEW) {  // one row tile
+            low_rows();
+            __syncthreads();
         }
         queue_wait<RING - 1 + AHEAD>();
         Out8<TO, VEC> now[4];
@@ -1110,7 +1127,7 @@ __device__ __forceinline__ void copy_rows(const ExpandK &k, int rank, const int 
 // Any types, on CUDA cores: 16 rows x 256 columns, a column per thread.
 template <typename TW, typename TO>
 __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_constant__ ExpandK k) {
-    expand_begin(k);
+    pdl_release();
     constexpr int ROWS = 16, RMAX = 64;
     __shared__ int ids[ROWS], list[ROWS], count;
     __shared__ __align__(16) float ss[RMAX][ROWS];
@@ -1118,6 +1135,7 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
     const int64_t l0 = (int64_t)(blockIdx.x % k.row_tiles) * ROWS;
     const int64_t t0 = k.row0[rank] * k.brows + l0, t1 = (k.row0[rank] + 1) * k.brows;
     const int nd = distinct<ROWS>(k.ids, t0, t1 < k.rows ? t1 : k.rows, k.n, ids, list, &count, k.status);
+    expand_low(k);
     if (blockIdx.z == 0) copy_rows<TO, ROWS>(k, rank, ids, l0, k.brows, (int64_t)blockIdx.y * 256);
     for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads) {
         const int row = i / k.R, r = i % k.R;
