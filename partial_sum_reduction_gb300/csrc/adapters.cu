@@ -1401,11 +1401,13 @@ __device__ __forceinline__ bool last_share(const OuterK &k, int tile, int2 of, i
 // the bound of warp matrix instructions at RP = 32 and above (about half their
 // rate), and its operands of their shared-memory reads.
 // 80 us for 8192 rows of 20480 columns at rank 32 (336 MB, 4.2 TB/s), 24 us for
-// 4096 of 8192 at rank 16.  The bytes in flight bound it: 64 KB of X per SM,
-// which come back in some 2.3 us.  With the low values split and the rows listed
-// in every column tile instead (256 columns, one CTA per SM) it was 124 us; with
-// barriers between copying and issuing warps only where a stage changes hands,
-// 85.
+// 4096 of 8192 at rank 16.  What bounds it is a group's own chain, some 2400
+// cycles in each of two CTAs: waiting for its copies, its products, asking for
+// the next, reading sums.  Not HBM (rows brought into the L2 six groups early:
+// 84 us), not the L2 (22 % busy), issue slots (33 %) or the CTA's barrier (only
+// the issuing warp waiting for the others: 85).  Other copies were slower: the
+// low values split and the rows listed in every column tile (256 columns, one
+// CTA per SM), 124 us; TMA gathers of four rows, 131 (65 cycles each).
 constexpr int kOuterThreads = 256, kOuterCols = 128;  // two CTAs per SM
 template <int RP>
 struct OuterShape {
