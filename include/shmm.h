@@ -522,7 +522,7 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_d
  *   C_r[N]       out: box SHMM_TENSOR_C
  *   low          out: fp32 [I, rank], for shmm_adapters_backward
  * bf16 plans use the tensor cores: products of bf16 values in fp32, low split
- * into bf16 parts worth 16 bits (24 where C is fp32).  fp32 plans use the CUDA
+ * into three bf16 parts that hold all of its 24 bits.  fp32 plans use the CUDA
  * cores.  One row of the batch: one launch of few CTAs per factor, the same
  * kernels.  A plan whose result GeLU finishes is refused: the adapters' part
  * belongs before it.

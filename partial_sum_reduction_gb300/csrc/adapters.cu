@@ -27,9 +27,10 @@
 //   fp32 operands: CUDA cores.
 //
 // The low-rank rows stay fp32 between the kernels.  Where they are matrix
-// operands they are split into two bf16 parts (three where the result is
-// stored in fp32), high bits first, so a product loses 2^-17 (2^-24) of
-// itself, not the 2^-9 that rounding them to bf16 would.
+// operands they are split into three bf16 parts, high bits first: 8 + 8 + 8
+// bits, all of an fp32 value's 24, so a product with a bf16 factor loses
+// nothing before it is added.  (Two parts would lose up to 2^-16 of it,
+// rounding to bf16 2^-8.)
 //
 // Rows of other adapters never mix: a row's result takes only products with
 // its own adapter, and rows of an adapter are gathered by index for its
@@ -842,7 +843,7 @@ struct Out8 {
 constexpr int kMaxRowTiles = 16;
 template <bool FEW, int KT, typename TO>
 struct ExpandShape {
-    static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
+    static constexpr int kParts = 3;  // of the low values: all their bits (see the top)
     static constexpr int kPitch = 16 * KT + 8;  // bf16: a row's start moves by 4 banks, fragments do not conflict
     static constexpr int kWords = sizeof(TO) / 2;  // 16-byte pieces of eight outputs
     static constexpr int kRing = FEW ? 1 : kWords == 1 ? 3 : 2;

@@ -1,0 +1,56 @@
+"""What the adapters' sums keep: every bit of the low-rank values that are
+operands of the next product.
+
+The cases need no tolerance.  Their sums are exact in fp32 in any order: all
+terms are multiples of 2^-20 and no partial sum exceeds 4."""
+import pytest
+import torch
+
+from parity_util import lib
+
+E = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def s():
+    return lib()
+
+
+def repeated(row, rows, dt):
+    return torch.tensor(row).expand(rows, len(row)).contiguous().to(DT[dt]).cuda()
+
+
+def padded(values, width):
+    return values + [0.0] * (width - len(values))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_dt,out_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,J,K", [(1, 8, 8), (5, 3, 5), (40, 16, 1032), (300, 24, 520), (9900, 8, 136)])
+def test_low_values_keep_their_bits(s, rows, J, K, in_dt, out_dt):
+    """low = (1 + 2^-8 + 2^-20, 1, 2^-8) times up = (1, -1, -1): the result is
+    2^-20, which every type holds, and 0 if the first value lost its last bit.
+    The same for the gradient of A, with dlow in low's place."""
+    from partial_sum_reduction_gb300 import helpers as H
+    parts = [1.0, 2.0 ** -8, 2.0 ** -20]
+    narrow = torch.zeros(1, 3, max(J, K))
+    narrow[0, 0, :3], narrow[0, 1, 0], narrow[0, 2, 1] = 1.0, 1.0, 1.0
+    spread = torch.tensor([1.0, -1.0, -1.0]).reshape(1, 3, 1)
+    ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    low = torch.empty(rows, 3, device="cuda")
+    plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", rows, J, K, in_dt, out_dt)
+    down, up = narrow[:, :, :J].to(DT[in_dt]).cuda().contiguous(), spread.expand(1, 3, K).to(DT[in_dt]).cuda().contiguous()
+    C = H.alloc(plan, s.TENSOR_C, fill=float("nan"))
+    plan.adapters_forward([repeated(padded(parts, J), rows, in_dt)], ids, down, up, None, None, C, low)
+    s.shmm_sync_status()
+    assert (low == torch.tensor([1 + 2.0 ** -8 + 2.0 ** -20, 1.0, 2.0 ** -8], device="cuda")).all()
+    assert (C[0].float() == 2.0 ** -20).all()
+    up, down = narrow[:, :, :K].to(DT[in_dt]).cuda().contiguous(), spread.expand(1, 3, J).to(DT[in_dt]).cuda().contiguous()
+    dA = H.alloc(plan, s.TENSOR_A, fill=float("nan"))
+    dd, du = torch.empty(1, 3, J, device="cuda"), torch.empty(1, 3, K, device="cuda")
+    A = torch.zeros(rows, J, dtype=DT[in_dt], device="cuda")
+    plan.adapters_backward([repeated(padded(parts, K), rows, out_dt)], [A], ids, down, up, None, low, None, dA, dd, du,
+                           H.adapters_workspace(plan, 1, 3))
+    s.shmm_sync_status()
+    assert (dA[0].float() == 2.0 ** -20).all()
