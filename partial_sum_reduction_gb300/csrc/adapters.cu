@@ -653,8 +653,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) project_tc_kernel(const __grid_
                 if (r + j < k.R && in_bounds(k.status, (t0 + row) * k.R + r + j, 1, k.rows * k.R))
                     k.out[(t0 + row) * k.R + r + j] = k.scale ? u[j] * scales[i] : u[j];
         }
-        shmm_tc::fence_async();
-        cluster.sync();  // the sums are read: the stages may be filled again
+        // The sums are read, by other CTAs too: after this barrier the stages
+        // may be filled again.  That is the async proxy's writing, so every
+        // reader orders its loads, remote ones among them, before the barrier
+        // and the copying thread its copies after it; a fence of the CTA's own
+        // shared memory would say nothing about a peer's.
+        shmm_tc::fence_async_cluster();
+        cluster.sync();
+        shmm_tc::fence_async_cluster();
         shmm_tc::fence_after();
     }
     // Never leave a load into shared memory in flight.

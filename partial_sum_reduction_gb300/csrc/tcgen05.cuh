@@ -25,6 +25,8 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 // Orders this thread's ordinary shared-memory accesses before later ones of
 // the async proxy (TMA, tcgen05.mma) that a barrier orders after it.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// The same for accesses of any address, another CTA's shared memory included.
+__device__ __forceinline__ void fence_async_cluster() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 

@@ -1,0 +1,35 @@
+"""The order of the training and adapter operators' accesses, within a kernel
+and between calls: repeated calls on freshly copied inputs, early starts
+against plain stream order, other streams than the current one."""
+import pytest
+import torch
+
+from parity_util import lib
+from test_adapters import Case
+
+
+@pytest.fixture(scope="module")
+def s():
+    return lib()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,n", [(16, 40), (32, 23), (64, 9)])
+def test_passes_over_a_row_tile_do_not_meet(s, R, n):
+    """128-row tiles of dozens of adapters, 2048 columns shared by clusters of
+    eight CTAs: every pass but the last is followed by copies into the memory
+    that held its sums, which the other CTAs have read.  Many calls on freshly
+    copied inputs give one result, within its bounds."""
+    c = Case(s, "whole", 2048, 2048, 2048, R, n)
+    host = {k: v.cpu().pin_memory() for k, v in (("down", c.down), ("up", c.up), ("A", c.A))}
+    C0, low0 = c.forward()
+    c.check_forward(C0, low0)
+    g0 = c.backward(low0)
+    c.check_backward(low0, *g0)
+    for _ in range(60):
+        c.dev["down"], c.dev["up"] = host["down"].cuda(), host["up"].cuda()
+        c.A_r = [host["A"].cuda()]
+        C, low = c.forward()
+        assert torch.equal(low, low0) and torch.equal(C[0], C0[0])
+        g = c.backward(low)
+        assert torch.equal(g[0][0], g0[0][0]) and torch.equal(g[1], g0[1]) and torch.equal(g[2], g0[2])
