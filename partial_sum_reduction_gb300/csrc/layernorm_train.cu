@@ -24,6 +24,7 @@
 #include "checked.cuh"
 #include "device_wait.cuh"
 #include "pdl.cuh"
+#include "ring_order.h"
 #include "shmm_internal.h"
 
 namespace {
@@ -252,9 +253,10 @@ constexpr int kMaxStages = 16;
 // copying warp they do not fit); gathered: two (98 against 101 us, 8 ranks).
 // Backward: two, the third's registers would spill (57 against 77 us), and a
 // second copying warp for its three entries a row.
-constexpr int kForwardCopiers = 1, kBackwardCopiers = 2;
+constexpr int kForwardCopiers = 1, kBackwardCopiers = 2, kMaxCopiers = 2;
 struct Ring {
     uint64_t full[kMaxStages], empty[kMaxStages];
+    int64_t put[kMaxCopiers];  // entries of each copying thread, once it is done
     int abort_flag;
 };
 
@@ -305,18 +307,19 @@ __device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uin
 }
 
 // The end, for every thread.  The working warps have waited for every entry,
-// unless a wait was given up: then a copying thread (`put` > 0, its n-th entry
-// number `first` + n COPIERS) waits, again with a limit, for its entries of
-// the last lap, so that no copy into shared memory stays in flight.
+// unless a wait was given up: then one thread waits, again with a limit, for
+// every stage's last entry, so that no copy into shared memory stays in flight.
+// (An older entry of a stage was read before the last one was put.)
 template <int COPIERS>
-__device__ __forceinline__ void ring_end(Ring &ring, int first, int64_t put, int stages, int *status) {
+__device__ __forceinline__ void ring_end(Ring &ring, int stages, int *status) {
     __syncwarp();
     __syncthreads();
-    if (put && *(volatile int *)&ring.abort_flag)
-        for (int64_t i = put > stages / COPIERS ? put - stages / COPIERS : 0; i < put; ++i) {
-            const int64_t u = first + i * COPIERS;
-            shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[u % stages]), (uint32_t)(u / stages) & 1,
-                                &ring.abort_flag, status, false);
+    if (threadIdx.x == 0 && *(volatile int *)&ring.abort_flag)
+        for (int i = 0; i < stages; ++i) {
+            const int64_t u = shmm_ring::last_entry(i, stages, COPIERS, ring.put);
+            if (u >= 0)
+                shmm_dev::mbar_wait(shmm_dev::smem_u32(&ring.full[i]), (uint32_t)(u / stages) & 1, &ring.abort_flag,
+                                    status, false);
         }
 }
 
@@ -483,13 +486,12 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kForwardCopie
     const bool has_res = N == 1 && k.res;
     ring_init(ring, stages, work / 32);
     if ((int)threadIdx.x >= work) {
-        int64_t put = 0;
         const int first = ((int)threadIdx.x - work) / 32;
         if ((threadIdx.x & 31) == 0) {
             // entries of a row: x, then the residual
             const uint32_t at = shmm_dev::smem_u32(entries);
             Turn turn{first, 0};
-            int64_t t = blockIdx.x;
+            int64_t t = blockIdx.x, put = 0;
             int e = first;
             for (bool ok = true; ok;) {
                 const int per_row = has_res ? 2 : 1;
@@ -506,8 +508,9 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kForwardCopie
                 put += ok;
                 e += kForwardCopiers;
             }
+            ring.put[first] = put;
         }
-        ring_end<kForwardCopiers>(ring, first, put, stages, k.status);
+        ring_end<kForwardCopiers>(ring, stages, k.status);
         return;
     }
     Turn turn{0, 0};
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kForwardCopie
             for (int m = 0; m < k.G; ++m) y.store((T *)k.dst[g * k.G + m] + grow * cols + col[j]);
         }
     }
-    ring_end<kForwardCopiers>(ring, 0, 0, stages, k.status);
+    ring_end<kForwardCopiers>(ring, stages, k.status);
 }
 
 // Rows of any width: the row is read three times (from L2 after the first).
@@ -802,13 +805,12 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
     F2 gr[N == 1 ? NV : 1][VW / 2];
     ring_init(ring, stages, work / 32);
     if ((int)threadIdx.x >= work) {
-        int64_t put = 0;
         const int first = ((int)threadIdx.x - work) / 32;
         if ((threadIdx.x & 31) == 0) {
             const int per_row = k.G + 1 + (has_res ? 1 : 0);
             const uint32_t at = shmm_dev::smem_u32(entries);
             Turn turn{first, 0};
-            int64_t t = blockIdx.x;
+            int64_t t = blockIdx.x, put = 0;
             int e = first, s, g;  // the next entry: number e of row t
             int64_t rr, grow;
             if (t < k.rows) locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
@@ -829,8 +831,9 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
                 put += ok;
                 e += kBackwardCopiers;
             }
+            ring.put[first] = put;
         }
-        ring_end<kBackwardCopiers>(ring, first, put, stages, k.status);
+        ring_end<kBackwardCopiers>(ring, stages, k.status);
         return;
     }
     Turn turn{0, 0};
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
             *reinterpret_cast<float2 *>(part + cols + col[j] + 2 * i) = split(db[j][i]);
         }
     }
-    ring_end<kBackwardCopiers>(ring, 0, 0, stages, k.status);
+    ring_end<kBackwardCopiers>(ring, stages, k.status);
 }
 
 // Rows of any width: the row is read twice, and each thread adds its columns

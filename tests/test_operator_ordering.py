@@ -1,11 +1,17 @@
 """The order of the training and adapter operators' accesses, within a kernel
 and between calls: repeated calls on freshly copied inputs, early starts
 against plain stream order, other streams than the current one."""
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
 from parity_util import lib
 from test_adapters import Case
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -33,3 +39,18 @@ def test_passes_over_a_row_tile_do_not_meet(s, R, n):
         assert torch.equal(low, low0) and torch.equal(C[0], C0[0])
         g = c.backward(low)
         assert torch.equal(g[0][0], g0[0][0]) and torch.equal(g[1], g0[1]) and torch.equal(g[2], g0[2])
+
+
+def test_a_stopped_ring_is_waited_for(tmp_path):
+    """The row rings of the training LayerNorm, stopped after a given-up wait:
+    every copy in flight is a stage's last entry, which the end waits for, with
+    any number of stages and one or two copying threads (host arithmetic)."""
+    if not shutil.which("g++"):
+        pytest.skip("g++ not available")
+    exe = str(tmp_path / "ring_order")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-I",
+                        os.path.join(ROOT, "partial_sum_reduction_gb300", "csrc"),
+                        os.path.join(ROOT, "tests", "c", "ring_order.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout == "ok\n", r.stdout
