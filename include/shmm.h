@@ -555,8 +555,9 @@ shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *plan, int n_adapte
  *   A_r, row_adapter, down, up, scale  in: as in the forward call
  *   low          in: as the forward call left it
  *   base_r[N]    in: box SHMM_TENSOR_A, in_dtype, or NULL for 0; may be dA_r
- *   dA_r[N]      out: box SHMM_TENSOR_A, in_dtype, every rank's; no A_r or dC_r
- *                (UNSUPPORTED): they may still be read while it is written
+ *   dA_r[N]      out: box SHMM_TENSOR_A, in_dtype, every rank's; shares no byte
+ *                with any rank's A_r or dC_r (UNSUPPORTED), which may still be
+ *                read while it is written
  *   ddown, dup   out: fp32, the shapes of down and up, overwritten; zeros for
  *                an adapter without rows
  *   workspace    device memory of >= shmm_adapters_workspace_size() bytes,

@@ -990,6 +990,41 @@ static shmm_status_t check_adapters(const char *fn, const shmm_plan_t *p, int n,
     return SHMM_OK;
 }
 
+// The bytes of the ranks' boxes of one tensor.
+struct Span {
+    uintptr_t lo, hi;
+    int rank;
+};
+static std::vector<Span> spans(const shmm_plan_t *p, const void *const *arr, int tensor, shmm_dtype_t dt) {
+    std::vector<Span> v;
+    for (int r = 0; r < p->nranks; ++r) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(arr[r]);
+        const int64_t bytes = p->boxes[tensor][r].numel() * (dt == SHMM_F32 ? 4 : 2);
+        if (bytes) v.push_back({at, at + (uintptr_t)bytes, r});
+    }
+    return v;
+}
+
+// Refuses an output that shares bytes with an input: of any rank, since a
+// block that several ranks hold is read from one of them for all.
+static shmm_status_t check_apart(const char *fn, const std::vector<Span> &out, const char *out_name,
+                                 std::vector<Span> in, const char *in_name) {
+    std::sort(in.begin(), in.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
+    std::vector<Span> reach(in);  // of in[0..i], the one that ends last
+    for (size_t i = 1; i < reach.size(); ++i)
+        if (reach[i - 1].hi > reach[i].hi) reach[i] = reach[i - 1];
+    for (const Span &o : out) {
+        const size_t before = std::lower_bound(in.begin(), in.end(), o.hi,
+                                               [](const Span &a, uintptr_t hi) { return a.lo < hi; }) - in.begin();
+        if (before && reach[before - 1].hi > o.lo)
+            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
+                                                  "] overlaps " + in_name + "[" +
+                                                  std::to_string(reach[before - 1].rank) +
+                                                  "], which is read while it is written");
+    }
+    return SHMM_OK;
+}
+
 static size_t adapters_workspace(const shmm_plan_t *p, int n, int R) {
     return shmm::adapters_workspace_bytes(p->I, n, R, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
 }
@@ -1070,10 +1105,10 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int r
             return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(workspace_bytes) +
                                             " bytes, " + std::to_string(need) + " needed");
         if (need && (st = check_ptr(fn, workspace, "workspace", 256)) != SHMM_OK) return st;
-        for (int r = 0; r < p->nranks; ++r)
-            if (dA_r[r] && (dA_r[r] == A_r[r] || dA_r[r] == dC_r[r]))
-                return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": dA_r[" + std::to_string(r) +
-                                                      "] is also an A_r or dC_r, which is read while dA is written");
+        const std::vector<Span> dA = spans(p, (const void *const *)dA_r, SHMM_TENSOR_A, p->in_dt);
+        if ((st = check_apart(fn, dA, "dA_r", spans(p, A_r, SHMM_TENSOR_A, p->in_dt), "A_r")) != SHMM_OK ||
+            (st = check_apart(fn, dA, "dA_r", spans(p, dC_r, SHMM_TENSOR_C, p->out_dt), "dC_r")) != SHMM_OK)
+            return st;
         std::string err;
         int *status = status_ptr(&err);
         if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
