@@ -518,7 +518,8 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_d
  *   down, up     in: [n_adapters, rank, J] and [n_adapters, rank, K], row-major,
  *                in_dtype, 16-byte aligned (whole: the factors are not sharded)
  *   scale        in: fp32 array of n_adapters, or NULL for 1
- *   base_r[N]    in: box SHMM_TENSOR_C, out_dtype, or NULL for 0; may be C_r
+ *   base_r[N]    in: box SHMM_TENSOR_C, out_dtype, or NULL for 0; a rank's may
+ *                be its own C_r; no other overlap with a C_r (UNSUPPORTED)
  *   C_r[N]       out: box SHMM_TENSOR_C
  *   low          out: fp32 [I, rank], for shmm_adapters_backward
  * bf16 plans use the tensor cores: products of bf16 values in fp32, low split
@@ -530,8 +531,8 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_d
  * infinite or NaN (a part of the split may be 0, and 0 times infinity is
  * NaN), never another adapter's or another row's.
  * Errors: NULL, ALIGN, SHAPE (n_adapters, rank, an empty J or K, I of 2^31 or
- * more, J or K of 2^23 or more), UNSUPPORTED (rank > 64, SHMM_FLAG_GELU),
- * CUDA. */
+ * more, J or K of 2^23 or more), UNSUPPORTED (rank > 64, SHMM_FLAG_GELU, an
+ * overlap), CUDA. */
 shmm_status_t shmm_adapters_forward(const shmm_plan_t *plan, int n_adapters, int rank, const void *const *A_r,
                                     const int32_t *row_adapter, const void *down, const void *up, const float *scale,
                                     const void *const *base_r, void *const *C_r, float *low, void *stream);
@@ -554,7 +555,8 @@ shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *plan, int n_adapte
  *                once
  *   A_r, row_adapter, down, up, scale  in: as in the forward call
  *   low          in: as the forward call left it
- *   base_r[N]    in: box SHMM_TENSOR_A, in_dtype, or NULL for 0; may be dA_r
+ *   base_r[N]    in: box SHMM_TENSOR_A, in_dtype, or NULL for 0; a rank's may
+ *                be its own dA_r; no other overlap with a dA_r (UNSUPPORTED)
  *   dA_r[N]      out: box SHMM_TENSOR_A, in_dtype, every rank's; shares no byte
  *                with any rank's A_r or dC_r (UNSUPPORTED), which may still be
  *                read while it is written

@@ -1025,6 +1025,48 @@ static shmm_status_t check_apart(const char *fn, const std::vector<Span> &out, c
     return SHMM_OK;
 }
 
+// Refuses an output that shares bytes with another rank's part of the array
+// that it is added to or made from, or with a part of its own that is not the
+// same one: every rank reads its own while the others write.
+static shmm_status_t check_in_place(const char *fn, const std::vector<Span> &out, const char *out_name,
+                                    std::vector<Span> in, const char *in_name) {
+    std::sort(in.begin(), in.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
+    // Of in[0..i]: the one that ends last, and the last of another rank.
+    std::vector<std::pair<Span, Span>> reach;
+    std::pair<Span, Span> top{{0, 0, -1}, {0, 0, -1}};
+    for (const Span &s : in) {
+        if (s.hi > top.first.hi) {
+            if (s.rank != top.first.rank) top.second = top.first;
+            top.first = s;
+        } else if (s.rank != top.first.rank && s.hi > top.second.hi) {
+            top.second = s;
+        }
+        reach.push_back(top);
+    }
+    std::vector<const Span *> own;
+    for (const Span &s : in) {
+        if ((int)own.size() <= s.rank) own.resize(s.rank + 1, nullptr);
+        own[s.rank] = &s;
+    }
+    for (const Span &o : out) {
+        const Span *bad = nullptr;
+        const size_t before = std::lower_bound(in.begin(), in.end(), o.hi,
+                                               [](const Span &a, uintptr_t hi) { return a.lo < hi; }) - in.begin();
+        if (before) {
+            const std::pair<Span, Span> &r = reach[before - 1];
+            const Span &other = r.first.rank == o.rank ? r.second : r.first;
+            if (other.hi > o.lo) bad = &other;
+        }
+        const Span *mine = o.rank < (int)own.size() ? own[o.rank] : nullptr;
+        if (mine && mine->lo != o.lo && mine->lo < o.hi && o.lo < mine->hi) bad = mine;
+        if (bad)
+            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
+                                                  "] overlaps " + in_name + "[" + std::to_string(bad->rank) +
+                                                  "], which is read while it is written");
+    }
+    return SHMM_OK;
+}
+
 static size_t adapters_workspace(const shmm_plan_t *p, int n, int R) {
     return shmm::adapters_workspace_bytes(p->I, n, R, p->in_dt == SHMM_BF16 || p->out_dt == SHMM_BF16);
 }
@@ -1056,7 +1098,12 @@ shmm_status_t shmm_adapters_forward(const shmm_plan_t *p, int n_adapters, int ra
             (st = check_ptrs(p, A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK ||
             (st = check_ptrs(p, (const void *const *)C_r, SHMM_TENSOR_C, fn, "C_r")) != SHMM_OK)
             return st;
-        if (base_r && (st = check_ptrs(p, base_r, SHMM_TENSOR_C, fn, "base_r")) != SHMM_OK) return st;
+        if (base_r) {
+            if ((st = check_ptrs(p, base_r, SHMM_TENSOR_C, fn, "base_r")) != SHMM_OK ||
+                (st = check_in_place(fn, spans(p, (const void *const *)C_r, SHMM_TENSOR_C, p->out_dt), "C_r",
+                                     spans(p, base_r, SHMM_TENSOR_C, p->out_dt), "base_r")) != SHMM_OK)
+                return st;
+        }
         std::string err;
         int *status = status_ptr(&err);
         if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
@@ -1108,6 +1155,8 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int r
         const std::vector<Span> dA = spans(p, (const void *const *)dA_r, SHMM_TENSOR_A, p->in_dt);
         if ((st = check_apart(fn, dA, "dA_r", spans(p, A_r, SHMM_TENSOR_A, p->in_dt), "A_r")) != SHMM_OK ||
             (st = check_apart(fn, dA, "dA_r", spans(p, dC_r, SHMM_TENSOR_C, p->out_dt), "dC_r")) != SHMM_OK)
+            return st;
+        if (base_r && (st = check_in_place(fn, dA, "dA_r", spans(p, base_r, SHMM_TENSOR_A, p->in_dt), "base_r")) != SHMM_OK)
             return st;
         std::string err;
         int *status = status_ptr(&err);

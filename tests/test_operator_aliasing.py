@@ -52,3 +52,37 @@ def test_input_gradient_over_any_rank_s_inputs(s, mesh, sa, sb, sc):
     if not torch.cuda.is_available():
         assert backward(s, plan, dC, [A[0]] * n, free) == s.shmm.ERR_CUDA
         assert backward(s, plan, dC, A, [a + size for a in A]) == s.shmm.ERR_CUDA
+
+
+def forward(s, plan, base, C):
+    a = P(0x7000000)
+    return s.lib().shmm_adapters_forward(plan.handle, 3, 8, table(apart(plan.nranks, 0x1000000)), a, a, a, None,
+                                         None if base is None else table(base), table(C), a, None)
+
+
+@pytest.mark.parametrize("mesh,sa,sb,sc", [("{X:4}", "I,J", "J,K_X", "I,K_X"), ("{X:2,Y:2}", "I_X,J_Y", "J_Y,K", "I_X,K")])
+def test_base_shared_by_ranks_and_written_in_place(s, mesh, sa, sb, sc):
+    """A rank's base may be its own output, as the same buffer; nothing else
+    of what any rank adds to may be written by another."""
+    import torch
+    plan = s.Plan(mesh, sa, sb, sc, 8, 32, 32)
+    n = plan.nranks
+    calls = {s.TENSOR_A: lambda base, out: backward(s, plan, apart(n, 0x2000000), apart(n, 0x1000000), out, base),
+             s.TENSOR_C: lambda base, out: forward(s, plan, base, out)}
+    for tensor, call in calls.items():
+        rows, cols = plan.rank_box(tensor, 0)[1]
+        size = rows * cols * 2
+        free, other = apart(n, 0x3000000), apart(n, 0x4000000)
+        for q in range(n):
+            for r in range(n):
+                for shift in (0, 16 - size, size - 16):
+                    if q == r and shift == 0:
+                        continue
+                    base, out = list(other), list(free)
+                    out[r] = base[q] + shift
+                    assert call(base, out) == s.shmm.ERR_UNSUPPORTED, (tensor, q, r, shift)
+        # one base for all ranks, written in place by one of them
+        assert call([free[1]] * n, free) == s.shmm.ERR_UNSUPPORTED
+        if not torch.cuda.is_available():  # these pass every check and end at the device
+            assert call(free, free) == call([other[0]] * n, free) == call([o + size for o in free], free) == s.shmm.ERR_CUDA
+            assert call(None, free) == s.shmm.ERR_CUDA
