@@ -487,11 +487,12 @@ shmm_status_t shmm_layernorm_all_gather_forward(const shmm_plan_t *plan, const v
  *                leaves them) or the plan's out_dtype
  *   dfull_r[N]   in: box SHMM_TENSOR_C
  *   shard_r[N]   in: box SHMM_TENSOR_C_REDUCED, the rows that were normalised
- *   dshard_r[N]  out: box SHMM_TENSOR_C_REDUCED, out_dtype; may be shard_r
+ *   dshard_r[N]  out: box SHMM_TENSOR_C_REDUCED, out_dtype; a rank's may be its
+ *                own shard_r; no other overlap with a shard_r (UNSUPPORTED)
  *   workspace    shmm_layernorm_backward_workspace_size(nranks * block rows,
  *                cols) bytes
  * Errors: NULL, ALIGN, SHAPE, DTYPE (grad_dtype), NOMEM, UNSUPPORTED (no row
- * all-gather), CUDA. */
+ * all-gather, an overlap), CUDA. */
 shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *plan, shmm_dtype_t grad_dtype,
                                                  const void *const *dfull_r, const void *const *shard_r,
                                                  const float *const *mean_r, const float *const *rstd_r,

@@ -667,6 +667,83 @@ static shmm_status_t check_ptr(const char *fn, const void *p, const char *what, 
     return SHMM_OK;
 }
 
+// The bytes of the ranks' boxes of one tensor.
+struct Span {
+    uintptr_t lo, hi;
+    int rank;
+};
+static std::vector<Span> spans(const shmm_plan_t *p, const void *const *arr, int tensor, shmm_dtype_t dt) {
+    std::vector<Span> v;
+    for (int r = 0; r < p->nranks; ++r) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(arr[r]);
+        const int64_t bytes = p->boxes[tensor][r].numel() * (dt == SHMM_F32 ? 4 : 2);
+        if (bytes) v.push_back({at, at + (uintptr_t)bytes, r});
+    }
+    return v;
+}
+
+// Refuses an output that shares bytes with an input: of any rank, since a
+// block that several ranks hold is read from one of them for all.
+static shmm_status_t check_apart(const char *fn, const std::vector<Span> &out, const char *out_name,
+                                 std::vector<Span> in, const char *in_name) {
+    std::sort(in.begin(), in.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
+    std::vector<Span> reach(in);  // of in[0..i], the one that ends last
+    for (size_t i = 1; i < reach.size(); ++i)
+        if (reach[i - 1].hi > reach[i].hi) reach[i] = reach[i - 1];
+    for (const Span &o : out) {
+        const size_t before = std::lower_bound(in.begin(), in.end(), o.hi,
+                                               [](const Span &a, uintptr_t hi) { return a.lo < hi; }) - in.begin();
+        if (before && reach[before - 1].hi > o.lo)
+            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
+                                                  "] overlaps " + in_name + "[" +
+                                                  std::to_string(reach[before - 1].rank) +
+                                                  "], which is read while it is written");
+    }
+    return SHMM_OK;
+}
+
+// Refuses an output that shares bytes with another rank's part of the array
+// that it is added to or made from, or with a part of its own that is not the
+// same one: every rank reads its own while the others write.
+static shmm_status_t check_in_place(const char *fn, const std::vector<Span> &out, const char *out_name,
+                                    std::vector<Span> in, const char *in_name) {
+    std::sort(in.begin(), in.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
+    // Of in[0..i]: the one that ends last, and the last of another rank.
+    std::vector<std::pair<Span, Span>> reach;
+    std::pair<Span, Span> top{{0, 0, -1}, {0, 0, -1}};
+    for (const Span &s : in) {
+        if (s.hi > top.first.hi) {
+            if (s.rank != top.first.rank) top.second = top.first;
+            top.first = s;
+        } else if (s.rank != top.first.rank && s.hi > top.second.hi) {
+            top.second = s;
+        }
+        reach.push_back(top);
+    }
+    std::vector<const Span *> own;
+    for (const Span &s : in) {
+        if ((int)own.size() <= s.rank) own.resize(s.rank + 1, nullptr);
+        own[s.rank] = &s;
+    }
+    for (const Span &o : out) {
+        const Span *bad = nullptr;
+        const size_t before = std::lower_bound(in.begin(), in.end(), o.hi,
+                                               [](const Span &a, uintptr_t hi) { return a.lo < hi; }) - in.begin();
+        if (before) {
+            const std::pair<Span, Span> &r = reach[before - 1];
+            const Span &other = r.first.rank == o.rank ? r.second : r.first;
+            if (other.hi > o.lo) bad = &other;
+        }
+        const Span *mine = o.rank < (int)own.size() ? own[o.rank] : nullptr;
+        if (mine && mine->lo != o.lo && mine->lo < o.hi && o.lo < mine->hi) bad = mine;
+        if (bad)
+            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
+                                                  "] overlaps " + in_name + "[" + std::to_string(bad->rank) +
+                                                  "], which is read while it is written");
+    }
+    return SHMM_OK;
+}
+
 // Statistics of a row gather's blocks: one fp32 array per rank.
 static shmm_status_t check_stats(const shmm_plan_t *p, const float *const *arr, const char *fn, const char *what) {
     if (!arr) return fail(SHMM_ERR_NULL, std::string(fn) + ": " + what + " array is NULL");
@@ -898,7 +975,10 @@ shmm_status_t shmm_layernorm_all_gather_backward(const shmm_plan_t *p, shmm_dtyp
         a.cols = p->boxes[SHMM_TENSOR_C_REDUCED][0].ext[1];
         const int64_t rows = a.brows * g.size * g.count;
         if ((st = norm_sizes(fn, rows, a.cols, p->out_dt)) != SHMM_OK) return st;
-        if ((st = check_norm_workspace(fn, rows, a.cols, workspace, workspace_bytes)) != SHMM_OK) return st;
+        if ((st = check_norm_workspace(fn, rows, a.cols, workspace, workspace_bytes)) != SHMM_OK ||
+            (st = check_in_place(fn, spans(p, (const void *const *)dshard_r, SHMM_TENSOR_C_REDUCED, p->out_dt),
+                                 "dshard_r", spans(p, shard_r, SHMM_TENSOR_C_REDUCED, p->out_dt), "shard_r")) != SHMM_OK)
+            return st;
         a.dt = p->out_dt;
         a.grad_dt = grad_dtype;
         a.gamma = gamma;
@@ -987,83 +1067,6 @@ static shmm_status_t check_adapters(const char *fn, const shmm_plan_t *p, int n,
     if (p->I == 0) return SHMM_OK;
     if ((st = check_ptr(fn, ids, "row_adapter", 4)) != SHMM_OK || (st = check_ptr(fn, low, "low", 4)) != SHMM_OK)
         return st;
-    return SHMM_OK;
-}
-
-// The bytes of the ranks' boxes of one tensor.
-struct Span {
-    uintptr_t lo, hi;
-    int rank;
-};
-static std::vector<Span> spans(const shmm_plan_t *p, const void *const *arr, int tensor, shmm_dtype_t dt) {
-    std::vector<Span> v;
-    for (int r = 0; r < p->nranks; ++r) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(arr[r]);
-        const int64_t bytes = p->boxes[tensor][r].numel() * (dt == SHMM_F32 ? 4 : 2);
-        if (bytes) v.push_back({at, at + (uintptr_t)bytes, r});
-    }
-    return v;
-}
-
-// Refuses an output that shares bytes with an input: of any rank, since a
-// block that several ranks hold is read from one of them for all.
-static shmm_status_t check_apart(const char *fn, const std::vector<Span> &out, const char *out_name,
-                                 std::vector<Span> in, const char *in_name) {
-    std::sort(in.begin(), in.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
-    std::vector<Span> reach(in);  // of in[0..i], the one that ends last
-    for (size_t i = 1; i < reach.size(); ++i)
-        if (reach[i - 1].hi > reach[i].hi) reach[i] = reach[i - 1];
-    for (const Span &o : out) {
-        const size_t before = std::lower_bound(in.begin(), in.end(), o.hi,
-                                               [](const Span &a, uintptr_t hi) { return a.lo < hi; }) - in.begin();
-        if (before && reach[before - 1].hi > o.lo)
-            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
-                                                  "] overlaps " + in_name + "[" +
-                                                  std::to_string(reach[before - 1].rank) +
-                                                  "], which is read while it is written");
-    }
-    return SHMM_OK;
-}
-
-// Refuses an output that shares bytes with another rank's part of the array
-// that it is added to or made from, or with a part of its own that is not the
-// same one: every rank reads its own while the others write.
-static shmm_status_t check_in_place(const char *fn, const std::vector<Span> &out, const char *out_name,
-                                    std::vector<Span> in, const char *in_name) {
-    std::sort(in.begin(), in.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
-    // Of in[0..i]: the one that ends last, and the last of another rank.
-    std::vector<std::pair<Span, Span>> reach;
-    std::pair<Span, Span> top{{0, 0, -1}, {0, 0, -1}};
-    for (const Span &s : in) {
-        if (s.hi > top.first.hi) {
-            if (s.rank != top.first.rank) top.second = top.first;
-            top.first = s;
-        } else if (s.rank != top.first.rank && s.hi > top.second.hi) {
-            top.second = s;
-        }
-        reach.push_back(top);
-    }
-    std::vector<const Span *> own;
-    for (const Span &s : in) {
-        if ((int)own.size() <= s.rank) own.resize(s.rank + 1, nullptr);
-        own[s.rank] = &s;
-    }
-    for (const Span &o : out) {
-        const Span *bad = nullptr;
-        const size_t before = std::lower_bound(in.begin(), in.end(), o.hi,
-                                               [](const Span &a, uintptr_t hi) { return a.lo < hi; }) - in.begin();
-        if (before) {
-            const std::pair<Span, Span> &r = reach[before - 1];
-            const Span &other = r.first.rank == o.rank ? r.second : r.first;
-            if (other.hi > o.lo) bad = &other;
-        }
-        const Span *mine = o.rank < (int)own.size() ? own[o.rank] : nullptr;
-        if (mine && mine->lo != o.lo && mine->lo < o.hi && o.lo < mine->hi) bad = mine;
-        if (bad)
-            return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
-                                                  "] overlaps " + in_name + "[" + std::to_string(bad->rank) +
-                                                  "], which is read while it is written");
-    }
     return SHMM_OK;
 }
 

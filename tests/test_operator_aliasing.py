@@ -86,3 +86,33 @@ def test_base_shared_by_ranks_and_written_in_place(s, mesh, sa, sb, sc):
         if not torch.cuda.is_available():  # these pass every check and end at the device
             assert call(free, free) == call([other[0]] * n, free) == call([o + size for o in free], free) == s.shmm.ERR_CUDA
             assert call(None, free) == s.shmm.ERR_CUDA
+
+
+@pytest.mark.parametrize("mesh,sa,sc", [("{X:4}", "I_X,J", "I,K"), ("{X:2,Y:2}", "I_X,J", "I,K")])
+def test_rows_gradient_over_another_rank_s_rows(s, mesh, sa, sc):
+    """Ranks that hold copies of an owner block may share its rows, unless one
+    of them is written in place."""
+    import torch
+    plan = s.Plan(mesh, sa, "J,K", sc, 8, 8, 64)
+    n = plan.nranks
+    rows, cols = plan.rank_box(s.TENSOR_C_REDUCED, 0)[1]
+    size = rows * cols * 2
+    a, stats = P(0x7000000), table(apart(n, 0x5000000))
+
+    def call(shard, dshard):
+        return s.lib().shmm_layernorm_all_gather_backward(
+            plan.handle, 0, table(apart(n, 0x2000000)), table(shard), stats, stats, a, table(dshard), a, a,
+            P(0x8000000), 1 << 40, None)
+
+    free, other = apart(n, 0x3000000), apart(n, 0x4000000)
+    for q in range(n):
+        for r in range(n):
+            for shift in (0, 16 - size, size - 16):
+                if q == r and shift == 0:
+                    continue
+                out = list(free)
+                out[r] = other[q] + shift
+                assert call(other, out) == s.shmm.ERR_UNSUPPORTED, (q, r, shift)
+    assert call([free[1]] * n, free) == s.shmm.ERR_UNSUPPORTED
+    if not torch.cuda.is_available():  # these pass every check and end at the device
+        assert call(free, free) == call([other[0]] * n, free) == call([o + size for o in free], free) == s.shmm.ERR_CUDA
