@@ -422,10 +422,15 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    float *s = acc + (m * NT + j) * 4;
+                    // A chunk's own sum first, then added: the matrix
+                    // instructions cut what they add to (see kTcSegment),
+                    // this addition rounds.
+                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     const Raw8 &lo = x[2 * m], &hi = x[2 * m + 1];
                     mma(s, lo.w[0], hi.w[0], lo.w[1], hi.w[1], b.w[0], b.w[1]);
                     mma(s, lo.w[2], hi.w[2], lo.w[3], hi.w[3], b.w[2], b.w[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[(m * NT + j) * 4 + i] += s[i];
                 }
             }
             stage = stage + 1 == ST ? 0 : stage + 1;

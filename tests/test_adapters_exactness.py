@@ -1,7 +1,8 @@
 """What the adapters' sums keep: every bit of the low-rank values that are
-operands of the next product.
+operands of the next product, and a rounding (not a cut) per step of a long
+sum.
 
-The cases need no tolerance.  Their sums are exact in fp32 in any order: all
+The first cases need no tolerance.  Their sums are exact in fp32 in any order: all
 terms are multiples of 2^-20 and no partial sum exceeds 4."""
 import pytest
 import torch
@@ -54,3 +55,33 @@ def test_low_values_keep_their_bits(s, rows, J, K, in_dt, out_dt):
                            H.adapters_workspace(plan, 1, 3))
     s.shmm_sync_status()
     assert (dA[0].float() == 2.0 ** -20).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [4, 40])
+def test_long_sums_round(s, R):
+    """28671 positive products per value, 8192 rows: too many rows for a
+    cluster to share the columns, and a width that no TMA load takes, so a
+    thread sums 112 chunks of 32.  With E = 2^-24: a chunk is two matrix
+    instructions, each off by at most 2 E of their sum (they cut); each of the
+    112 additions rounds by at most E of what it has so far, half of the whole
+    on average (56 E); three more join the warps.  So a value is off by at most
+    4 + 56 + 3 = 63 E.  The mean over many values keeps only what does not
+    average out: the cuts' 4 E, and of the roundings, 3.7 E of deviation per
+    value (variance E^2 / 3 times 112 / 3 + 3), eight deviations of the mean of
+    1024 values, 1 E.  6 E bounds both.  (Cutting at every one of the 224
+    instructions is off by some 80 E, all to one side.)"""
+    I, J, K = 8192, 28671, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    A = (torch.rand(I, J, generator=g, device="cuda") + 0.5).bfloat16()
+    down = (torch.rand(1, R, J, generator=g, device="cuda") + 0.5).bfloat16()
+    up = torch.zeros(1, R, K, device="cuda").bfloat16()
+    plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K)
+    low, C = torch.empty(I, R, device="cuda"), torch.empty(I, K, device="cuda").bfloat16()
+    plan.adapters_forward([A], torch.zeros(I, dtype=torch.int32, device="cuda"), down, up, None, None, [C], low)
+    s.shmm_sync_status()
+    some = torch.arange(0, I, 32, device="cuda")
+    want = A[some].double() @ down[0].double().T
+    off = (low[some].double() - want) / want
+    assert off.abs().max().item() <= 63 * E
+    assert abs(off.mean().item()) <= 6 * E
