@@ -307,14 +307,15 @@ __device__ __forceinline__ bool ring_put(Ring &ring, Turn &turn, int stages, uin
 }
 
 // The end, for every thread.  The working warps have waited for every entry,
-// unless a wait was given up: then one thread waits, again with a limit, for
-// every stage's last entry, so that no copy into shared memory stays in flight.
-// (An older entry of a stage was read before the last one was put.)
+// unless a wait was given up: then one thread (`waits`; a copying one, whose
+// warp has the registers for it) waits, again with a limit, for every stage's
+// last entry, so that no copy into shared memory stays in flight.  (An older
+// entry of a stage was read before the last one was put.)
 template <int COPIERS>
-__device__ __forceinline__ void ring_end(Ring &ring, int stages, int *status) {
+__device__ __forceinline__ void ring_end(Ring &ring, bool waits, int stages, int *status) {
     __syncwarp();
     __syncthreads();
-    if (threadIdx.x == 0 && *(volatile int *)&ring.abort_flag)
+    if (waits && *(volatile int *)&ring.abort_flag)
         for (int i = 0; i < stages; ++i) {
             const int64_t u = shmm_ring::last_entry(i, stages, COPIERS, ring.put);
             if (u >= 0)
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kForwardCopie
             }
             ring.put[first] = put;
         }
-        ring_end<kForwardCopiers>(ring, stages, k.status);
+        ring_end<kForwardCopiers>(ring, (int)threadIdx.x == work, stages, k.status);
         return;
     }
     Turn turn{0, 0};
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kForwardCopie
             for (int m = 0; m < k.G; ++m) y.store((T *)k.dst[g * k.G + m] + grow * cols + col[j]);
         }
     }
-    ring_end<kForwardCopiers>(ring, stages, k.status);
+    ring_end<kForwardCopiers>(ring, false, stages, k.status);
 }
 
 // Rows of any width: the row is read three times (from L2 after the first).
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
             }
             ring.put[first] = put;
         }
-        ring_end<kBackwardCopiers>(ring, stages, k.status);
+        ring_end<kBackwardCopiers>(ring, (int)threadIdx.x == work, stages, k.status);
         return;
     }
     Turn turn{0, 0};
@@ -955,7 +956,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
             *reinterpret_cast<float2 *>(part + cols + col[j] + 2 * i) = split(db[j][i]);
         }
     }
-    ring_end<kBackwardCopiers>(ring, stages, k.status);
+    ring_end<kBackwardCopiers>(ring, false, stages, k.status);
 }
 
 // Rows of any width: the row is read twice, and each thread adds its columns
