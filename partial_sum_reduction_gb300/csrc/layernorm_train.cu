@@ -725,13 +725,15 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
                     db[j][i] += dy[j][i];
                 }
         sum = row_sum<ONEWARP>(sum, scratch, turn);
-        const float k1 = -rstd * (sum.x * inv_n), k2 = -rstd * rstd * (sum.y * inv_n);
+        // xh before its factor, not (x - mean) times rstd^2, which overflows where
+        // rows are small and eps is 0 (rstd above 2^64), though the result does not.
+        const float k1 = -rstd * (sum.x * inv_n), k2 = -rstd * (sum.y * inv_n);
         float o[NV][VW];
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
-                o[j][i] = fmaf(x[j].get(i) - mean, k2, fmaf(dy[j][i] * ga[j][i], rstd, k1));
+                o[j][i] = fmaf((x[j].get(i) - mean) * rstd, k2, fmaf(dy[j][i] * ga[j][i], rstd, k1));
             }
         if (t + step < k.rows) load_row(t + step);
 #pragma unroll
@@ -922,7 +924,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
                 }
         const float2 pw = split(sw), px = split(swx);
         const float2 sum = stream_sum(make_float2(pw.x + pw.y, px.x + px.y), scratch, sum_turn, work);
-        const F2 k1 = both(-rs * (sum.x * inv_n)), k2 = both(-rs * rs * (sum.y * inv_n));
+        const F2 k1 = both(-rs * (sum.x * inv_n)), k2 = both(-rs * (sum.y * inv_n));  // (see ln_backward_kernel)
         if (has_res) ring_wait(ring, turn, k.status);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
             F2 o[VW / 2];
 #pragma unroll
             for (int i = 0; i < VW / 2; ++i)
-                o[i] = fma(x[j].get2(i) + minus, k2, fma(dy(j, i) * ga(j, i), rs2, k1));
+                o[i] = fma((x[j].get2(i) + minus) * rs2, k2, fma(dy(j, i) * ga(j, i), rs2, k1));
             if constexpr (N == 1) {
                 if (has_res) {
                     Raw<T, VW> r;
