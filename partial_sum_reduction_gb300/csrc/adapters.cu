@@ -107,7 +107,7 @@ struct ExpandK {
     const float *scale;   // or NULL
     const float *s;       // [rows][R]
     int n, R, row_tiles, mt;  // CTAs per box's rows; 16-row tiles of a CTA
-    int beside;           // runs beside the kernel before it (see ExpandEnd)
+    int beside;           // runs beside the kernel before it (see expand_end)
     int64_t rows, cols;
     int *status;
 };

@@ -1164,10 +1164,7 @@ cudaError_t backward_vec(const BwdK<N> &k, int *parts, cudaStream_t s) {
     const dim3 g((unsigned)grid), b((unsigned)h.threads);
     constexpr int kMost = kCols / VW;  // accesses of a thread that holds kCols columns
     if (h.onewarp) return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, true>, g, b, 0, s, k);
-    if (h.nv == kMost) return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, false>, g, b, 0, s, k);
-    if (h.nv == kMost / 2 && VW > 1) return launch_pdl(ln_backward_kernel<T, GT, VW, (VW > 1 ? kMost / 2 : kMost), N, false>, g, b, 0, s, k);
-    if (h.nv == kMost / 4 && VW < 8) return launch_pdl(ln_backward_kernel<T, GT, VW, (VW < 8 ? kMost / 4 : kMost), N, false>, g, b, 0, s, k);
-    return cudaErrorInvalidValue;
+    return launch_pdl(ln_backward_kernel<T, GT, VW, kMost, N, false>, g, b, 0, s, k);
 }
 
 template <typename T, typename GT, int N>
@@ -1230,9 +1227,14 @@ cudaError_t run_backward(const shmm::NormBackwardArgs &a, int *status, cudaStrea
     cudaError_t e = cudaSuccess;
     if (k.rows > 0) {
         shmm::count_launch();
-        if (a.dt == SHMM_F32) e = backward<float, float, N>(k, &parts, s);
-        else if (a.grad_dt == SHMM_F32) e = backward<__nv_bfloat16, float, N>(k, &parts, s);
-        else e = backward<__nv_bfloat16, __nv_bfloat16, N>(k, &parts, s);
+        if (a.dt == SHMM_F32) {
+            e = backward<float, float, N>(k, &parts, s);
+        } else if (a.grad_dt == SHMM_BF16) {
+            e = backward<__nv_bfloat16, __nv_bfloat16, N>(k, &parts, s);
+        } else {  // partial sums of several members
+            if constexpr (N > 1) e = backward<__nv_bfloat16, float, N>(k, &parts, s);
+            else e = cudaErrorInvalidValue;
+        }
         if (e != cudaSuccess) return e;
     }
     shmm::count_launch();

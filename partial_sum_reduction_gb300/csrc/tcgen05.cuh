@@ -18,10 +18,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, u
         : "memory");
 }
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
 // Orders this thread's ordinary shared-memory accesses before later ones of
 // the async proxy (TMA, tcgen05.mma) that a barrier orders after it.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
