@@ -538,7 +538,7 @@ shmm_status_t shmm_adapters_forward(const shmm_plan_t *plan, int n_adapters, int
                                     const int32_t *row_adapter, const void *down, const void *up, const float *scale,
                                     const void *const *base_r, void *const *C_r, float *low, void *stream);
 
-/* Workspace of shmm_adapters_backward in bytes.  Host only.
+/* Workspace of shmm_adapters_backward in bytes.  Host only: no device is asked.
  * Errors: NULL, SHAPE (n_adapters, rank, I, J, K), UNSUPPORTED (rank > 64). */
 shmm_status_t shmm_adapters_workspace_size(const shmm_plan_t *plan, int n_adapters, int rank,
                                            size_t *bytes);

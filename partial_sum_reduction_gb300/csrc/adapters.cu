@@ -2012,9 +2012,13 @@ namespace shmm {
 // as its rows fill.  So all places together are at most 2 (room / tiles) per
 // column tile.  None when half the card's CTAs or more have a column tile of
 // their own, or for few rows.
+// The card's SMs are a constant here, not asked of the current device: the
+// workspace's size follows from them, and it is the same wherever it is asked
+// for.  (Nothing waits for all CTAs to be there at once.)
 struct Grain {
+    static constexpr int kSms = 152;
     int per_sm, group, least;  // CTAs per SM, rows of a group, groups of a CTA
-    int64_t room() const { return (int64_t)per_sm * sms(); }
+    int64_t room() const { return (int64_t)per_sm * kSms; }
     bool shared(int64_t rows) const { return rows > (int64_t)group * least; }
     int most(int64_t rows, int64_t n, int64_t tiles) const {
         if (tiles * 2 > room() || !shared(rows)) return 0;

@@ -4,6 +4,7 @@ against plain stream order, other streams than the current one."""
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -54,3 +55,23 @@ def test_a_stopped_ring_is_waited_for(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout
+
+
+SIZES = """
+import partial_sum_reduction_gb300 as s
+for dt in ("bf16", "f32"):
+    for I, J, K, n, R in ((1, 8, 8, 1, 1), (97, 40, 36, 2, 3), (6540, 160, 544, 17, 32), (8192, 4096, 16384, 8, 64)):
+        print(s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K, dt, dt).adapters_workspace_size(n, R))
+    print(s.shmm_layernorm_backward_workspace_size(8192, 4096))
+"""
+
+
+@pytest.mark.gpu
+def test_workspace_sizes_ask_no_device(s):
+    """What a process without a device allocates for is what the calls of one
+    with a device ask for."""
+    got = [subprocess.run([sys.executable, "-c", touch + SIZES], cwd=ROOT, env=env, capture_output=True, text=True)
+           for touch, env in (("", dict(os.environ, CUDA_VISIBLE_DEVICES="")),
+                              ("import torch; torch.zeros(1, device='cuda')\n", dict(os.environ)))]
+    assert all(r.returncode == 0 for r in got), got
+    assert got[0].stdout == got[1].stdout and len(got[0].stdout.split()) == 10
