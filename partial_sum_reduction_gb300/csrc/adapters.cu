@@ -55,6 +55,7 @@ namespace {
 namespace cg = cooperative_groups;
 using bf16 = __nv_bfloat16;
 using shmm_dev::in_bounds;
+using shmm_dev::piece_in_bounds;
 using shmm_pdl::launch_pdl;
 using shmm_pdl::launch_pdl_cluster;
 using shmm_pdl::pdl_enter;
@@ -337,7 +338,8 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
     // rows without an adapter: zeros
     if (blockIdx.z == 0 && cr == 0)
         for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
-            if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows) k.out[t0 * k.R + i] = 0.0f;
+            if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows && in_bounds(k.status, t0 * k.R + i, 1, k.rows * k.R))
+                k.out[t0 * k.R + i] = 0.0f;
     int br[2 * MT], id[2 * MT];
     int64_t off[2 * MT];  // of the row in its block
 #pragma unroll
@@ -353,13 +355,13 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
     // Piece i of X (row i % 2 MT) and j of W for columns c.. of block blk:
     // its address, and whether it exists.
     auto x_piece = [&](int i, int a, int blk, int c, bool *ok) {
-        *ok = id[i] == a && c < bcols && in_bounds(k.status, off[i] + c, 1, k.x.brows * k.x.bcols);
+        *ok = id[i] == a && c < bcols && piece_in_bounds<VEC>(k.status, off[i] + c, bcols - c, k.x.brows * k.x.bcols);
         return (const bf16 *)k.x.at[br[i] + blk] + off[i];
     };
     auto w_piece = [&](int j, int a, int blk, int c, bool *ok) {
         const int r = j * 8 + g;
         const int64_t at = ((int64_t)a * k.R + r) * k.cols + (int64_t)blk * bcols;
-        *ok = r < k.R && c < bcols && in_bounds(k.status, at + c, 1, (int64_t)k.n * k.R * k.cols);
+        *ok = r < k.R && c < bcols && piece_in_bounds<VEC>(k.status, at + c, bcols - c, (int64_t)k.n * k.R * k.cols);
         return (const bf16 *)k.w + at;
     };
     int ask_d = blockIdx.z, ask_ch = ch0;  // the next chunk to ask for
@@ -524,7 +526,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) project_tc_kernel(const __grid_
     const uint32_t tmem = tmem_at;
     if (cr == 0)  // rows without an adapter: zeros
         for (int i = threadIdx.x; i < ROWS * k.R; i += kTcThreads)
-            if (ids[i / k.R] < 0 && t0 + i / k.R < t1) k.out[t0 * k.R + i] = 0.0f;
+            if (ids[i / k.R] < 0 && t0 + i / k.R < t1 && in_bounds(k.status, t0 * k.R + i, 1, k.rows * k.R))
+                k.out[t0 * k.R + i] = 0.0f;
     const int lo = (int)((int64_t)k.chunks * cr / cs), hi = (int)((int64_t)k.chunks * (cr + 1) / cs);
     // Producer and issuer are one thread each, so their own instructions are
     // what a chunk costs them (a division or two each made it 1500 cycles):
@@ -711,7 +714,8 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
     const int nd = distinct<ROWS>(k.ids, t0, k.rows, k.n, ids, list, &count, k.status);
     if (blockIdx.z == 0 && cr == 0)
         for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads)
-            if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows) k.out[t0 * k.R + i] = 0.0f;
+            if (ids[i / k.R] < 0 && t0 + i / k.R < k.rows && in_bounds(k.status, t0 * k.R + i, 1, k.rows * k.R))
+                k.out[t0 * k.R + i] = 0.0f;
     if (threadIdx.x < ROWS) {
         block_row[threadIdx.x] = (int)((t0 + threadIdx.x) / k.x.brows);
         row_at[threadIdx.x] = (t0 + threadIdx.x) % k.x.brows * k.x.bcols;
@@ -721,7 +725,8 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     for (int d = blockIdx.z; d < nd; d += gridDim.z) {
         const int a = list[d];
-        const TW *w = (const TW *)k.w + (int64_t)a * k.R * k.cols;
+        const int64_t w_at = (int64_t)a * k.R * k.cols;
+        const TW *w = (const TW *)k.w + w_at;
         float acc[2][NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) acc[0][i] = acc[1][i] = 0.0f;
@@ -741,7 +746,9 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < RP / kWarps; ++i) {
                 const int r = warp + i * kWarps;
-                wv[i] = in && r < k.R ? as_float(w[r * k.cols + (int64_t)blk * bcols + c]) : 0.0f;
+                const int64_t at = r * k.cols + (int64_t)blk * bcols + c;
+                wv[i] = in && r < k.R && in_bounds(k.status, w_at + at, 1, (int64_t)k.n * k.R * k.cols) ? as_float(w[at])
+                                                                                                        : 0.0f;
             }
         };
         fetch(cr);
@@ -911,7 +918,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     auto has = [&](int m, int i, int64_t *at, int *left) {
         *at = at0 + (int64_t)(m * 16 + (i >> 1) * 8) * k.bcols + 32 * (i & 1);
         *left = left0 - 32 * (i & 1);
-        return m * 16 + (i >> 1) * 8 + g < nrows && *left > 0 && in_bounds(k.status, *at, 1, k.brows * k.bcols);
+        return m * 16 + (i >> 1) * 8 + g < nrows && *left > 0 &&
+               piece_in_bounds<VEC>(k.status, *at, *left, k.brows * k.bcols);
     };
     auto ask = [&](int m, int slot) {  // row tile m into a slot of the queue
         if (VEC && m < MT) {
@@ -939,8 +947,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
             const int row = i / (RP / 2), r = (i % (RP / 2)) * 2;
             float lo = 0.0f, hi = 0.0f;
             if (row < nrows) {
-                if (r < k.R) lo = k.s[(t0 + row) * k.R + r];
-                if (r + 1 < k.R) hi = k.s[(t0 + row) * k.R + r + 1];
+                const int64_t at = (t0 + row) * k.R + r;
+                if (r < k.R && in_bounds(k.status, at, 1, k.rows * k.R)) lo = k.s[at];
+                if (r + 1 < k.R && in_bounds(k.status, at + 1, 1, k.rows * k.R)) hi = k.s[at + 1];
             }
             uint32_t p[PARTS];
             split<PARTS>(lo, hi, p);
@@ -983,8 +992,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
                 const int r = kt * 16 + 2 * q + (i & 1) + (i >> 1) * 8;
                 const int64_t c = c0 + 32 * (g & 1) + 8 * (g >> 1);  // product column j of lane group g: this one + j
                 const bool ok = r < k.R && c < k.bcols &&
-                                in_bounds(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, 1,
-                                          (int64_t)k.n * k.R * k.cols);
+                                piece_in_bounds<VEC>(k.status, ((int64_t)a * k.R + r) * k.cols + col + c, k.bcols - c,
+                                                     (int64_t)k.n * k.R * k.cols);
                 if (AHEAD && to >= 0) {
                     queue16(queue_at + (uint32_t)Shape::kBase + (uint32_t)((to * KT + kt) * 4 + i) * kThreads * 16,
                             ok ? (const void *)(w + r * k.cols + c) : k.w, ok);
@@ -1151,7 +1160,8 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
     if (blockIdx.z == 0) copy_rows<TO, ROWS>(k, rank, ids, l0, k.brows, (int64_t)blockIdx.y * 256);
     for (int i = threadIdx.x; i < ROWS * k.R; i += kThreads) {
         const int row = i / k.R, r = i % k.R;
-        ss[r][row] = ids[row] >= 0 ? k.s[(t0 + row) * k.R + r] : 0.0f;
+        const int64_t at = (t0 + row) * k.R + r;
+        ss[r][row] = ids[row] >= 0 && in_bounds(k.status, at, 1, k.rows * k.R) ? k.s[at] : 0.0f;
     }
     __syncthreads();
     const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
@@ -1163,14 +1173,18 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
     TO *out = (TO *)k.out[rank];
     for (int d = blockIdx.z; d < nd; d += gridDim.z) {
         const int a = list[d];
-        const TW *w = (const TW *)k.w + (int64_t)a * k.R * k.cols + k.col0[rank] * k.bcols + c;
+        const int64_t w_at = (int64_t)a * k.R * k.cols + k.col0[rank] * k.bcols + c;
+        const TW *w = (const TW *)k.w + w_at;
         float acc[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) acc[i] = 0.0f;
         for (int r0 = 0; r0 < k.R; r0 += 8) {
             float v[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] = r0 + r < k.R ? as_float(w[(r0 + r) * k.cols]) : 0.0f;
+            for (int r = 0; r < 8; ++r)
+                v[r] = r0 + r < k.R && in_bounds(k.status, w_at + (r0 + r) * k.cols, 1, (int64_t)k.n * k.R * k.cols)
+                           ? as_float(w[(r0 + r) * k.cols])
+                           : 0.0f;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 if (r0 + r >= k.R) break;
@@ -1305,7 +1319,8 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
         count(v.z);
         count(v.w);
     }
-    for (int64_t i = n4 * 4 + threadIdx.x; i < k.rows; i += 512) count(k.ids[i]);
+    for (int64_t i = n4 * 4 + threadIdx.x; i < k.rows; i += 512)
+        if (in_bounds(k.status, i, 1, k.rows)) count(k.ids[i]);
     below = __reduce_add_sync(0xffffffffu, below);
     valid = __reduce_add_sync(0xffffffffu, valid);
     if (lane == 0) {
@@ -1341,11 +1356,13 @@ __global__ void __launch_bounds__(512) arrange_kernel(const __grid_constant__ Ar
 #pragma unroll 2
                 for (int e = threadIdx.x; e < have * (RP / 2); e += 512) {
                     const int i = e / (RP / 2), r = e % (RP / 2) * 2;
-                    const float *v = k.s[j] + (int64_t)list[i] * k.R;
+                    const int64_t from = (int64_t)list[i] * k.R;
+                    if (!in_bounds(k.status, from, k.R, k.rows * k.R)) continue;
+                    const float *v = k.s[j] + from;
                     uint32_t p[3];
                     split<3>(r < k.R ? v[r] : 0.0f, r + 1 < k.R ? v[r + 1] : 0.0f, p);
                     const int64_t to = ((int64_t)at + l0 + i) * (3 * RP) + r;
-                    if (!in_bounds(k.status, to, 2 * RP + 2, k.rows * 3 * RP)) continue;
+                    if (!in_bounds(k.status, to, 2 * RP + 2, k.rows * 3 * RP)) continue;  // the three parts' places
 #pragma unroll
                     for (int h = 0; h < 3; ++h) *reinterpret_cast<uint32_t *>(k.parts[j] + to + h * RP) = p[h];
                 }
@@ -1537,7 +1554,9 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
                 *reinterpret_cast<uint4 *>(smem + x_to + at0 + i * 2048) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
             }
         }
-        const bool real = (int)f * 64 + pr < have;
+        const bool real = (int)f * 64 + pr < have &&
+                          in_bounds(k.status, (int64_t)(first + lo + (int)f * 64 + pr) * Shape::kWidth, Shape::kWidth,
+                                    k.rows * Shape::kWidth);
         const bf16 *from = parts + (int64_t)(real ? f * 64 + pr : 0) * Shape::kWidth + pc * 8;
 #pragma unroll
         for (int i = 0; i < (Shape::kWidth + 31) / 32; ++i) {
@@ -1629,8 +1648,10 @@ __global__ void __launch_bounds__(kOuterThreads, 2) outer_tc_kernel(const __grid
 #pragma unroll
         for (int h = Shape::kBands - 1; h >= 0; --h)
             add(t, *reinterpret_cast<const float4 *>(piece + (h * RP + r) * Shape::kPitch + j));
-        if (cs > 1) __stcg(reinterpret_cast<float4 *>(sums + (int64_t)cr * RP * kOuterCols + r * kOuterCols + j), t);
-        else put(r, j, t);
+        if (cs == 1) put(r, j, t);
+        else if (in_bounds(k.status, (sums - k.sh.sums) + (int64_t)cr * RP * kOuterCols + r * kOuterCols + j, 4,
+                           (int64_t)k.sh.tiles * k.sh.most * RP * kOuterCols))
+            __stcg(reinterpret_cast<float4 *>(sums + (int64_t)cr * RP * kOuterCols + r * kOuterCols + j), t);
     }
     if (cs > 1 && last_share(k, blockIdx.x, of, &last))
         for (int e = threadIdx.x; e < k.R * 32; e += kOuterThreads) {
@@ -1678,7 +1699,7 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
             x[u] = 0.0f;
-            if (s + u < have && c < bcols) {
+            if (s + u < have && c < bcols && in_bounds(k.status, first + lo + s + u, 1, k.rows)) {
                 const uint32_t t = order[s + u], b = t / (uint32_t)J.x.brows;
                 const int64_t at = (int64_t)(t - b * (uint32_t)J.x.brows) * bcols + c;
                 if (in_bounds(k.status, at, 1, J.x.brows * bcols))
@@ -1688,7 +1709,11 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int u = th / 16 + i * 8, r = r0 + th % 16;
-            v[i] = s + u < have && r < k.R ? J.s[(int64_t)order[s + u] * k.R + r] : 0.0f;
+            v[i] = 0.0f;
+            if (s + u < have && r < k.R && in_bounds(k.status, first + lo + s + u, 1, k.rows)) {
+                const int64_t at = (int64_t)order[s + u] * k.R + r;
+                if (in_bounds(k.status, at, 1, k.rows * k.R)) v[i] = J.s[at];
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -1711,7 +1736,10 @@ __global__ void __launch_bounds__(kThreads) outer_simt_kernel(const __grid_const
     const int piece = blockIdx.z * gridDim.x + blockIdx.x;  // a tile's 16 adapter rows
     float *shared_sums = k.sh.sums + ((int64_t)piece * k.sh.most + of.x) * (16 * 128);
     if (cs > 1) {
-        for (int e = threadIdx.x; e < 16 * 128; e += kThreads) __stcg(shared_sums + cr * (16 * 128) + e, sums[e]);
+        for (int e = threadIdx.x; e < 16 * 128; e += kThreads)
+            if (in_bounds(k.status, (shared_sums - k.sh.sums) + cr * (16 * 128) + e, 1,
+                          (int64_t)k.sh.tiles * k.sh.most * (16 * 128)))
+                __stcg(shared_sums + cr * (16 * 128) + e, sums[e]);
         if (!last_share(k, piece, of, &last)) return;
     }
     for (int e = threadIdx.x; e < 16 * 128; e += kThreads) {

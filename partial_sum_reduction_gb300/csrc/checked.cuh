@@ -29,4 +29,11 @@ __device__ __forceinline__ bool in_bounds(int *status, int64_t first, int64_t co
 #endif
 }
 
+// The same for eight consecutive values that one access moves (VEC), or that
+// are moved one by one while `left` of them remain in the row.
+template <bool VEC>
+__device__ __forceinline__ bool piece_in_bounds(int *status, int64_t first, int64_t left, int64_t extent) {
+    return in_bounds(status, first, VEC || left > 8 ? 8 : left, extent);
+}
+
 }  // namespace shmm_dev

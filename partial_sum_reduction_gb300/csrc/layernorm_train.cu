@@ -67,6 +67,7 @@ struct BwdK {
     const void *res;      // N == 1: gradient added to dt, or NULL
     const float *gamma;
     float *part;          // [gridDim.x][2][cols]
+    int64_t part_floats;  // of them the workspace holds
     int G;
     int64_t brows, cols, rows;
     int *status;
@@ -605,7 +606,9 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_wide_kernel(const __gr
         int s, g;
         int64_t rr, grow;
         locate<N>(t, k.brows, k.G, &s, &g, &rr, &grow);
-        if (!in_bounds(k.status, rr * k.cols, k.cols, k.brows * k.cols)) continue;  // the same for the whole CTA
+        if (!in_bounds(k.status, rr * k.cols, k.cols, k.brows * k.cols) ||
+            !in_bounds(k.status, grow * k.cols, k.cols, k.G * k.brows * k.cols))
+            continue;  // the same for the whole CTA
         const T *x = (const T *)k.src[s] + rr * k.cols;
         float2 sum = make_float2(0.0f, 0.0f);
         for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) {
@@ -754,6 +757,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_kernel(const __grid_c
         }
     }
     // This CTA's rows' sums.  One warp per row: the warps' sums in order.
+    if (!in_bounds(k.status, (int64_t)blockIdx.x * 2 * cols, 2 * cols, k.part_floats)) return;
     float *part = k.part + (int64_t)blockIdx.x * 2 * cols;
     if constexpr (ONEWARP) {
         __shared__ float sh[(kMaxThreads / 32) * 32 * NV * VW];
@@ -949,9 +953,10 @@ __global__ void __launch_bounds__((BIG ? kMaxThreads : 256) + 32 * kBackwardCopi
         if (has_res) ring_free(ring, turn, stages);
     }
     float *part = k.part + (int64_t)blockIdx.x * 2 * cols;
+    const bool room = in_bounds(k.status, (int64_t)blockIdx.x * 2 * cols, 2 * cols, k.part_floats);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if (col[j] >= cols) continue;
+        if (col[j] >= cols || !room) continue;
 #pragma unroll
         for (int i = 0; i < VW / 2; ++i) {
             *reinterpret_cast<float2 *>(part + col[j] + 2 * i) = split(dg[j][i]);
@@ -969,6 +974,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_wide_kernel(const __g
     __shared__ float2 scratch[2 * kMaxThreads / 32];
     int turn = 0;
     const float inv_n = 1.0f / (float)k.cols;
+    if (!in_bounds(k.status, (int64_t)blockIdx.x * 2 * k.cols, 2 * k.cols, k.part_floats)) return;
     float *part = k.part + (int64_t)blockIdx.x * 2 * k.cols;
     for (int64_t c = threadIdx.x; c < k.cols; c += blockDim.x) part[c] = part[k.cols + c] = 0.0f;
     for (int64_t t = blockIdx.x; t < k.rows; t += gridDim.x) {
@@ -1011,8 +1017,8 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_wide_kernel(const __g
 // columns of the [parts][2 cols] array; warp y adds rows y, y + 32, ... and
 // the 32 sums are added in order: a fixed order, so one input gives one
 // result.  parts == 0 (no rows) writes zeros.
-__global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, int parts, int64_t cols, float *dgamma,
-                                                           float *dbeta) {
+__global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, int parts, int64_t part_floats, int64_t cols,
+                                                           float *dgamma, float *dbeta, int *status) {
     pdl_enter();
     __shared__ float sh[32][33];
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
@@ -1022,7 +1028,10 @@ __global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, in
         for (int p0 = threadIdx.y; p0 < parts; p0 += 32 * U) {
             float v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = p0 + 32 * u < parts ? part[(int64_t)(p0 + 32 * u) * 2 * cols + c] : 0.0f;
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = (int64_t)(p0 + 32 * u) * 2 * cols + c;
+                v[u] = p0 + 32 * u < parts && in_bounds(status, at, 1, part_floats) ? part[at] : 0.0f;
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) a += v[u];
         }
@@ -1218,6 +1227,7 @@ cudaError_t run_backward(const shmm::NormBackwardArgs &a, int *status, cudaStrea
     k.res = a.res;
     k.gamma = a.gamma;
     k.part = a.workspace;
+    k.part_floats = (int64_t)(shmm::norm_workspace_bytes((int64_t)a.ngroups * a.G * a.brows, a.cols) / sizeof(float));
     k.G = a.G;
     k.brows = a.brows;
     k.cols = a.cols;
@@ -1239,7 +1249,7 @@ cudaError_t run_backward(const shmm::NormBackwardArgs &a, int *status, cudaStrea
     }
     shmm::count_launch();
     return launch_pdl(ln_grad_sum_kernel, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(32, 32), 0, s,
-                      (const float *)a.workspace, parts, a.cols, a.dgamma, a.dbeta);
+                      (const float *)a.workspace, parts, k.part_floats, a.cols, a.dgamma, a.dbeta, status);
 }
 
 }  // namespace
