@@ -1014,9 +1014,11 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_wide_kernel(const __g
 }
 
 // dgamma and dbeta: the CTAs' partial rows, column by column.  A CTA takes 32
-// columns of the [parts][2 cols] array; warp y adds rows y, y + 32, ... and
-// the 32 sums are added in order: a fixed order, so one input gives one
-// result.  parts == 0 (no rows) writes zeros.
+// columns of the [parts][2 cols] array; warp y adds rows y, y + 32, ..., ten at
+// a time in pairs, and the 32 sums are added in pairs: a fixed order, so one
+// input gives one result, and few additions deep (in a row they were off by
+// 1.5e-7 at 1031 rows, more than the sums that made them).  parts == 0 (no
+// rows) writes zeros.
 __global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, int parts, int64_t part_floats, int64_t cols,
                                                            float *dgamma, float *dbeta, int *status) {
     pdl_enter();
@@ -1032,18 +1034,21 @@ __global__ void __launch_bounds__(1024) ln_grad_sum_kernel(const float *part, in
                 const int64_t at = (int64_t)(p0 + 32 * u) * 2 * cols + c;
                 v[u] = p0 + 32 * u < parts && in_bounds(status, at, 1, part_floats) ? part[at] : 0.0f;
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) a += v[u];
+            a += (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]))) + (v[8] + v[9]);
         }
     }
     sh[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
     if (threadIdx.y == 0 && c < 2 * cols) {
-        float t = 0.0f;
+        float t[32];
 #pragma unroll
-        for (int y = 0; y < 32; ++y) t += sh[y][threadIdx.x];
-        if (c < cols) dgamma[c] = t;
-        else dbeta[c - cols] = t;
+        for (int y = 0; y < 32; ++y) t[y] = sh[y][threadIdx.x];
+#pragma unroll
+        for (int h = 16; h > 0; h /= 2)
+#pragma unroll
+            for (int y = 0; y < h; ++y) t[y] += t[y + h];
+        if (c < cols) dgamma[c] = t[0];
+        else dbeta[c - cols] = t[0];
     }
 }
 
