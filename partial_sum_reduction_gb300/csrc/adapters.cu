@@ -697,7 +697,8 @@ __device__ __forceinline__ void fma4(float *acc, const float *s, float x) {
 // Any types, on CUDA cores: 32 rows x 16 NR adapter rows per CTA, columns in
 // chunks of 32 through shared memory, the cluster sharing the chunks.  Shared
 // memory is read four columns at a time (pitch 36: no bank conflicts): one
-// load per value made its reads the bound.
+// load per value made its reads the bound.  A chunk is summed by itself and
+// then added, so a long share's rounding grows with its chunks, not its columns.
 template <typename TX, typename TW, int NR>
 __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_constant__ ProjK k) {
     pdl_enter();
@@ -759,6 +760,9 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
             for (int i = 0; i < RP / kWarps; ++i) ws[warp + i * kWarps][lane] = wv[i];
             __syncthreads();
             fetch(ch + cs);
+            float sum[2][NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) sum[0][i] = sum[1][i] = 0.0f;
 #pragma unroll
             for (int c2 = 0; c2 < 32; c2 += 4) {
                 const float4 x0 = *reinterpret_cast<const float4 *>(&xs[ty][c2]);
@@ -766,9 +770,14 @@ __global__ void __launch_bounds__(kThreads) project_simt_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
                     const float4 v = *reinterpret_cast<const float4 *>(&ws[tx + 16 * i][c2]);
-                    acc[0][i] = fmaf(x0.w, v.w, fmaf(x0.z, v.z, fmaf(x0.y, v.y, fmaf(x0.x, v.x, acc[0][i]))));
-                    acc[1][i] = fmaf(x1.w, v.w, fmaf(x1.z, v.z, fmaf(x1.y, v.y, fmaf(x1.x, v.x, acc[1][i]))));
+                    sum[0][i] = fmaf(x0.w, v.w, fmaf(x0.z, v.z, fmaf(x0.y, v.y, fmaf(x0.x, v.x, sum[0][i]))));
+                    sum[1][i] = fmaf(x1.w, v.w, fmaf(x1.z, v.z, fmaf(x1.y, v.y, fmaf(x1.x, v.x, sum[1][i]))));
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                acc[0][i] += sum[0][i];
+                acc[1][i] += sum[1][i];
             }
             __syncthreads();
         }

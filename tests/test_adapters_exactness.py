@@ -85,3 +85,25 @@ def test_long_sums_round(s, R):
     off = (low[some].double() - want) / want
     assert off.abs().max().item() <= 63 * E
     assert abs(off.mean().item()) <= 6 * E
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [4, 40])
+def test_long_fp32_sums(s, R):
+    """8192 positive fp32 products per value, 40000 rows: a thread sums them
+    all, in 256 chunks of 32.  The i-th of n additions is off by i / n of E =
+    2^-24 of the result at most, evenly spread: a variance of E^2 n / 9 for all.
+    256 chunks: (16 / 3 E)^2, and their own sums a 256th of E^2 32 / 9 each,
+    nothing beside it.  The root of the mean over 1000 values is within 1.2 of
+    that.  (8192 additions in a row: 30 E.)"""
+    I, J, K = 40000, 8192, 8
+    g = torch.Generator(device="cuda").manual_seed(4)
+    A = torch.rand(I, J, generator=g, device="cuda") + 0.5
+    down, up = torch.rand(1, R, J, generator=g, device="cuda") + 0.5, torch.zeros(1, R, K, device="cuda")
+    plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K, "f32", "f32")
+    low, C = torch.empty(I, R, device="cuda"), torch.empty(I, K, device="cuda")
+    plan.adapters_forward([A], torch.zeros(I, dtype=torch.int32, device="cuda"), down, up, None, None, [C], low)
+    s.shmm_sync_status()
+    some = torch.arange(0, I, 160, device="cuda")
+    want = A[some].double() @ down[0].double().T
+    assert ((low[some].double() - want) / want).square().mean().sqrt().item() <= 1.2 * 16 / 3 * E
