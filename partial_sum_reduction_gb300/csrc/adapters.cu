@@ -11,10 +11,12 @@
 //   project  out[t] = X[t] . W[a]^T     (low, dlow)
 //   expand   O[t] = base[t] + S[t] . W[a]   (C, dA)
 //   outer    G[a] = sum S[t]^T X[t]     (dup, ddown)
-// R is at most 64, so a row's X and O move 2 bytes per 2 R operations and all
-// three are HBM-bound (64 operations per byte at R = 64, against 280 at the
-// card's tensor rate).  What each is made of follows from where its operands
-// come from:
+// R is at most 64, so a row's X and O move 2 bytes per 2 R operations, or per
+// 6 R where the low values go in three parts: 64 to 192 operations per byte at
+// R = 64, against 280 at the rate of tcgen05 and about half of that at that of
+// warp instructions.  So all three are bound by HBM up to R = 16; expand, on
+// warp instructions, by those too at R = 32 and above.  What each is made of
+// follows from where its operands come from:
 //   project of few rows, and expand: warp matrix instructions (mma.sync, bf16
 //   operands, fp32 accumulators) whose operands come straight from global
 //   memory in 16-byte pieces.  The order of the summed index is free, so each
@@ -307,9 +309,10 @@ __device__ __forceinline__ float sum_cluster(cg::cluster_group &cluster, float *
 // through distributed shared memory, so no partial sum goes to HBM).
 // blockIdx.z strides over the tile's distinct adapters.  X and W pieces run
 // ST - 1 chunks ahead through the threads' queues, across adapters too.
-// 96 rows of 64 adapters, 8192 columns, rank 16: 9.3 us for 27 MB; a launch,
+// 96 rows of 64 adapters, 8192 columns, rank 16: 9.9 us for 27 MB; a launch,
 // two dependent reads (the row adapters, then the first chunk) and the join of
-// warps and cluster are some 5 of them.
+// warps and cluster are some 5 of them.  A factor that several row tiles use is
+// read, and its sums joined, once in each.
 template <int MT, int NT>
 struct ProjShape {
     static constexpr int kPieces = 2 * MT + NT;  // per thread and chunk
@@ -467,10 +470,11 @@ __global__ void __launch_bounds__(kThreads) project_mma_kernel(const __grid_cons
 // shared memory in order.  Beside the warp instructions above it: the factor
 // is read once per 128 rows instead of per 32, and no thread spends
 // instructions on addresses, which bounded them.
-// 8192 rows: 61 us at 16384 columns, rank 32 (268 MB, 4.4 TB/s); 88 us at 28672
-// columns, rank 16 (470 MB, 5.3 TB/s).  What is left is the start and the join of
-// each cluster (5 us of 15 at 4096 rows of 4096 columns) and the places that
-// clusters of a power of two leave empty (256 of 304 taken in these).
+// 8192 rows: 64 us at 16384 columns, rank 32 (268 MB, 4.2 TB/s); 90 us at 28672
+// columns, rank 16 (470 MB, 5.2 TB/s).  What is left is the start and the join of
+// each cluster (5 us of 17 at 4096 rows of 4096 columns) and the places that
+// clusters of a power of two leave empty (256 of 304 taken in these).  Ranks to
+// 32 spill 16 bytes a thread.
 constexpr int kTcThreads = 320, kTcStages = 3;
 // Chunks summed in the tensor memory before their sum is added in registers:
 // 16 instructions.  The tensor core's own fp32 additions cut instead of
@@ -862,9 +866,11 @@ struct Out8 {
 // threads with 64 bytes of a row side by side: base and output move in whole
 // sectors.  The base of up to kRing row tiles is in flight through the
 // threads' queues from the start.
-// 182 us for 8192 x 4096 to each of 8 ranks at rank 32 (1.07 GB, 5.9 TB/s), 82
-// us for 537 MB at rank 16 (6.5 TB/s): HBM.  Few rows (96, 8192 columns, 64
-// adapters): 12 us, one of them beside the projection; latency as in project_mma_kernel.
+// 86 us for 537 MB at rank 16 (6.2 TB/s): HBM.  205 us for 8192 x 4096 to each of
+// 8 ranks at rank 32 (1.07 GB, 5.2 TB/s): HBM and the matrix instructions of
+// three parts (two would take 182, and 82 at rank 16, and lose 2^-16 of the low
+// values).  Few rows (96, 8192 columns, 64 adapters): 13 us, one of them beside
+// the projection; latency as in project_mma_kernel.
 // blockIdx.x: rank x row tile; blockIdx.z strides over a row tile's adapters
 // (and z = 0 copies the rows without one).
 constexpr int kMaxRowTiles = 16;
@@ -968,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(TO) == 4 || KT > 2 ? 1 : 2)
     };
     // FEW: waited for after the first factor pieces are on their way.  Else at
     // once, while the row adapters are (after them it costs a start of its own:
-    // 192 against 182 us in the longest case above).
+    // 10 us of the longest case above).
     if constexpr (!FEW) low_rows();
     if ((int)threadIdx.x < ROWS) {
         my_id = my_id >= 0 && my_id < k.n ? my_id : -1;
@@ -1223,7 +1229,10 @@ __global__ void __launch_bounds__(kThreads) expand_simt_kernel(const __grid_cons
 // kWindow rows (one read of the row adapters), with how many lie before each
 // 32-row word, then turns the marks into lists of up to kList rows, ascending.
 constexpr int kWindow = 16384, kList = 1024;
-constexpr int kMostShares = 16;  // CTAs of one adapter and column tile
+// CTAs of one adapter and column tile.  One adapter, rank 16, with at most 16
+// and 32 of them: 36.9 and 38.4 us for 8192 rows of 512 + 512 columns, 71.6 and
+// 62.7 for 32768 of 256 + 256 (the whole gradient).
+constexpr int kMostShares = 16;
 struct Marks {
     uint32_t bits[kWindow / 32];
     int before[kWindow / 32];
@@ -1441,7 +1450,8 @@ __device__ __forceinline__ bool last_share(const OuterK &k, int tile, int2 of, i
 // 80 us for 8192 rows of 20480 columns at rank 32 (336 MB, 4.2 TB/s), 24 us for
 // 4096 of 8192 at rank 16.  What bounds it is a group's own chain, some 2400
 // cycles in each of two CTAs: waiting for its copies, its products, asking for
-// the next, reading sums.  Not HBM (rows brought into the L2 six groups early:
+// the next (800 of them: ten copies a thread, whose addresses spill: 84 bytes a
+// thread, 148 to 188 in the element form), reading sums.  Not HBM (rows brought into the L2 six groups early:
 // 84 us), not the L2 (22 % busy), issue slots (33 %) or the CTA's barrier (only
 // the issuing warp waiting for the others: 85).  Other copies were slower: the
 // low values split and the rows listed in every column tile (256 columns, one
@@ -1808,7 +1818,10 @@ int64_t slots_for(size_t smem) {
 // then its columns over a cluster of c (at most `split`).  One wave of equal
 // CTAs ends together; two leave the second part empty.
 // `few`: a batch of single tokens, most rows with an adapter of their own, so
-// the adapters come first; in longer ones a tile has one or two.
+// the adapters come first (96 rows of 64 adapters at random, 8192 columns, rank
+// 16: 14.2 us forward against 15.2 columns first; 256 rows 22.4 against 28.3).
+// In longer ones a tile is meant to have one or two; where it has many all the
+// same, columns first costs (512 rows of 64 adapters: 49.6 us against 35.9).
 void spread(int64_t tiles, int64_t slots, int64_t most, int64_t split, bool few, int *c, int *z) {
     *c = *z = 1;
     auto adapters = [&] {
@@ -1903,7 +1916,11 @@ cudaError_t project_tc(const ProjK &k, int b0, cudaStream_t s) {
 
 template <bool VEC>
 cudaError_t project_vec(const ProjK &k, cudaStream_t s) {
-    // tcgen05 from 2048 rows on: 16 row tiles, whose clusters of 8 reach most SMs.
+    // tcgen05 from 2048 rows on: 16 row tiles, whose clusters of 8 reach most
+    // SMs.  Forward, 4096 x 64, four adapters, tcgen05 and warp instructions:
+    // rank 64 18.6 and 16.8 us at 1024 rows, 20.6 and 25.7 at 2048, 32.6 and
+    // 64.3 at 8192; rank 16 15.6 and 12.2 at 2048, 16.7 and 15.3 at 4096, 20.9
+    // and 24.7 at 8192: one border for all ranks, late for high, early for low.
     const int b0 = (int)(k.rows / k.x.brows);
     if (VEC && k.rows >= 2048 && k.x.brows >= 128 && b0 * k.x.b1 <= kMaxMaps && k.cols >= 512) {
         if (k.R <= 16) return project_tc<16>(k, b0, s);
@@ -1954,7 +1971,10 @@ cudaError_t expand_vec(ExpandK k, int nranks, cudaStream_t s) {
     // A CTA of more row tiles reads a factor's piece and the low rows' split
     // less often (its start costs some 3 us), while the last wave of CTAs
     // leaves less of the card empty the more of them there are: 16 row tiles
-    // where that makes six waves of two CTAs per SM, 8 for three, else 4.
+    // where that makes six waves of two CTAs per SM, 8 for three, else 4, and
+    // one below half a wave.  Forward, 64 x 4096, rank 16, at the borders: 58368
+    // rows 190 us with 16 and 196 with 8; 14592 rows 50.8 with 8, 56.5 with 4 (56.4
+    // with 16); 1216 rows 9.0 with 4, 9.7 with 1.
     auto waves = [&](int mt) {
         return (double)((k.brows + 16 * mt - 1) / (16 * mt) * nranks * ((k.bcols + 511) / 512)) / (2 * sms());
     };

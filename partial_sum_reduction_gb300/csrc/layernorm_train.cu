@@ -247,7 +247,8 @@ __device__ __forceinline__ int col_of(int j) {
 // With the rows in registers instead, what was in flight fell with every
 // register the running sums took: 63 us forward and 81 us backward at 8192 x
 // 4096 bf16 with a residual, where this takes 50 and 63 us (49 and 61 without the
-// fence of ring_free).
+// fence of ring_free).  Some of the gradient's kernels spill: fp32 rows of one
+// block 84 to 156 bytes a thread, rows above 4096 columns up to 76.
 constexpr int kMaxStages = 16;
 // Forward, one block: three CTAs per SM under one another's chains of sums and
 // barriers (54 -> 49 us at 8192 x 4096 bf16 with a residual; with a second
