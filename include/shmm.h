@@ -45,7 +45,7 @@
  * that exceeded its time limit) are recorded in a device status word read by
  * shmm_sync_status().
  *
- * Numerics.  Inputs are bf16 or fp32.  Products accumulate in fp32; partial
+ * Numerics.  Inputs are bf16 or fp32 (8-bit operands: shmm_run_scaled).  Products accumulate in fp32; partial
  * sums are stored in fp32 (unless SHMM_FLAG_PARTIAL_OUT_DTYPE); the sum over a
  * reduction group is formed in fp32 in ascending rank order, one rounding per
  * addition, then rounded once to the output type (bf16: round to nearest
@@ -126,7 +126,19 @@ typedef enum {
                                     see shmm_bounds_checked) */
 } shmm_status_t;
 
-typedef enum { SHMM_F32 = 0, SHMM_BF16 = 1 } shmm_dtype_t;
+/* SHMM_E4M3: 8-bit values (1 sign, 4 exponent, 3 fraction bits, largest 448,
+ * no infinities) held in blocks that share a scale; see shmm_quantize. */
+typedef enum { SHMM_F32 = 0, SHMM_BF16 = 1, SHMM_E4M3 = 2 } shmm_dtype_t;
+
+/* Values that share a scale: this many consecutive columns of a row, or this
+ * many rows and columns. */
+#define SHMM_SCALE_BLOCK 128
+
+/* The gate's activation of a gated MLP block. */
+typedef enum {
+    SHMM_SILU = 0,      /* x / (1 + e^-x) */
+    SHMM_GELU_TANH = 1  /* the tanh form, as SHMM_FLAG_GELU */
+} shmm_activation_t;
 
 #define SHMM_MAX_AXES 8
 #define SHMM_AXIS_NAME_LEN 8
@@ -241,7 +253,11 @@ typedef struct shmm_plan shmm_plan_t;
  *   mesh, spec_A, spec_B, spec_C  in: the mesh and the three shardings
  *                                     (spec_C = the consumer's ownership)
  *   I, J, K                       in: global sizes; every split must be even
- *   in_dtype                      in: dtype of A and B
+ *   in_dtype                      in: dtype of A and B; a plan of SHMM_E4M3
+ *                                     serves shmm_run_scaled and
+ *                                     shmm_scaled_backward, and the calls on
+ *                                     results and partials (the calls that
+ *                                     read its operands otherwise: DTYPE)
  *   out_dtype                     in: dtype of C
  *   flags                         in: SHMM_FLAG_*
  *   plan                          out: new plan, owned by the caller
@@ -573,6 +589,159 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *plan, int n_adapters, in
                                      const void *up, const float *scale, const float *low, const void *const *base_r,
                                      void *const *dA_r, float *ddown, float *dup, void *workspace,
                                      size_t workspace_bytes, void *stream);
+
+/* ---- 8-bit operands, and the gated MLP block ------------------------------
+ *
+ * Blocks.  A [rows, cols] array in 8 bits is its e4m3 values [rows, cols] (one
+ * byte each) and fp32 scales, one for each block: SHMM_SCALE_BLOCK columns of a
+ * row (block_rows = 1; scales [rows, ceil(cols / 128)]) or 128 x 128 values
+ * (block_rows = 128; scales [ceil(rows / 128), ceil(cols / 128)]).  A value
+ * stands for itself times its block's scale.  Blocks are counted from the
+ * array's first row and column (a rank's box: from the box's), and end at its
+ * last.
+ *
+ * shmm_quantize makes them: with amax the block's largest finite magnitude,
+ * its scale is 2^e, e the smallest integer >= -126 with 448 * 2^e >= amax (1
+ * for a block of zeros), and its values are x / 2^e rounded to nearest even:
+ * that rounding is the only one.  Infinities and NaN become NaN.  The calls
+ * that read blocks take any finite scale.
+ *   x        [rows, cols], dtype F32 or BF16, 16-byte aligned
+ *   codes    out: [rows, cols] bytes, 16-byte aligned; shares no byte with x
+ *            (UNSUPPORTED)
+ *   scales   out: fp32
+ * No rows or no columns: nothing is written.
+ * Errors: NULL, ALIGN, SHAPE (negative sizes, rows of 2^31 or more, cols of
+ * 2^26 or more, block_rows), DTYPE, UNSUPPORTED, CUDA. */
+shmm_status_t shmm_quantize(int64_t rows, int64_t cols, shmm_dtype_t dtype, int block_rows, const void *x, void *codes,
+                            float *scales, void *stream);
+
+/* The way back: y = value * scale in fp32, rounded once to dtype (F32 or BF16;
+ * exact for scales that are powers of two, as shmm_quantize's are).  Same
+ * arguments and errors; y shares no byte with codes. */
+shmm_status_t shmm_dequantize(int64_t rows, int64_t cols, shmm_dtype_t dtype, int block_rows, const void *codes,
+                              const float *scales, void *y, void *stream);
+
+/* The sharded matmul of 8-bit operands: C = A . B for a plan of SHMM_E4M3, all
+ * four cases.  A has a scale for each 128 columns of a row, B one for each
+ * 128 x 128 values:
+ *   C[i,k] = sum over blocks b of J of
+ *            A_scale[i,b] * B_scale[b,k/128] * sum over j in b of A[i,j] * B[j,k]
+ * A block's products are summed by the tensor cores, the blocks' sums in fp32
+ * by the CUDA cores, so the scales cost no precision and long sums lose none;
+ * rounded once to out_dtype.  Every rank's shard is quantised on its own
+ * (shmm_quantize of its box), so blocks start at the box's corner.  Operands
+ * are read in place, a block that several ranks hold from the lowest one, and
+ * every rank's C is written: the collectives of the plan need no pass and no
+ * workspace of their own.
+ *   A_r[N], B_r[N]  in: boxes SHMM_TENSOR_A / SHMM_TENSOR_B, one byte a value
+ *   A_scale_r[N]    in: fp32 [box rows, ceil(box cols / 128)]
+ *   B_scale_r[N]    in: fp32 [ceil(box rows / 128), ceil(box cols / 128)]
+ *   C_r[N]          out: box SHMM_TENSOR_C, out_dtype; shares no byte with an
+ *                   operand (UNSUPPORTED)
+ * The tensor cores take shards whose rows are whole 16-byte pieces (columns of
+ * the boxes of A and B multiples of 16, of C whole 16-byte pieces too) and, where a dim is
+ * split, multiples of 128 along it, up to 16 ranks; other plans run on the
+ * CUDA cores (SHMM_FLAG_SIMT: all).  Other flags do not matter, but for
+ * SHMM_FLAG_GELU, which is refused.
+ * One input gives one result.
+ * Errors: NULL, ALIGN, DTYPE (not an E4M3 plan), SHAPE (I of 2^31 or more, J or
+ * K of 2^22 or more), UNSUPPORTED, CUDA. */
+shmm_status_t shmm_run_scaled(const shmm_plan_t *plan, const void *const *A_r, const float *const *A_scale_r,
+                              const void *const *B_r, const float *const *B_scale_r, void *const *C_r, void *stream);
+
+/* Workspace of shmm_scaled_backward in bytes: dC in 8 bits and A in bf16.  Host
+ * only.  Errors: NULL, DTYPE. */
+shmm_status_t shmm_scaled_backward_workspace_size(const shmm_plan_t *plan, size_t *bytes);
+
+/* Gradient of shmm_run_scaled, for the gradient dC of its C and operands as
+ * the forward call read them (A in 8 bits is the activation checkpoint):
+ *   dA = Q(dC) . B^T   Q(dC): each rank's box of dC in 8 bits, a scale for each
+ *                      128 columns of a row, as shmm_quantize makes them
+ *   dB = A^T . dC      A as it is held, dC as it came
+ * both rounded once to out_dtype, which must be BF16.  (The gradients of values
+ * before they were quantised: the rounding counts as the identity.)
+ *   dC_r[N]   in: box SHMM_TENSOR_C; a block that several ranks hold is read
+ *             from the lowest one and counts once
+ *   dA_r[N]   out: box SHMM_TENSOR_A, BF16, every rank's, or NULL (the whole
+ *             array): not wanted
+ *   dB_r[N]   out: box SHMM_TENSOR_B, BF16, every rank's, or NULL
+ *   workspace device memory of >= shmm_scaled_backward_workspace_size() bytes,
+ *             256-byte aligned; nothing in it needs to start at zero, and
+ *             calls that overlap on the GPU need one each
+ * The outputs share no byte with an input (UNSUPPORTED).  No rows: dB is zero.
+ * Errors: those of shmm_run_scaled, and NOMEM (workspace). */
+shmm_status_t shmm_scaled_backward(const shmm_plan_t *plan, const void *const *dC_r, const void *const *A_r,
+                                   const float *const *A_scale_r, const void *const *B_r,
+                                   const float *const *B_scale_r, void *const *dA_r, void *const *dB_r,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* What shmm_gated_forward keeps of the two projections for
+ * shmm_gated_backward: per rank, box SHMM_TENSOR_C, before the activation. */
+typedef struct {
+    shmm_dtype_t dtype;       /* the plan's in_dtype (rounded once), or
+                                 SHMM_E4M3: blocks of 128 columns of a row, half
+                                 (a quarter) of the bytes */
+    void *const *gate;        /* [N] */
+    void *const *up;          /* [N] */
+    float *const *gate_scale; /* [N], SHMM_E4M3: fp32 [box rows,
+                                 ceil(box cols / 128)]; else not read */
+    float *const *up_scale;
+} shmm_gated_saved_t;
+
+/* The gated first half of an MLP block ("GLU Variants Improve Transformer",
+ * Shazeer 2020): both projections, the activation and the product in one
+ * pass,
+ *   C = act(A . gate) * (A . up)
+ * for the plan's A and two operands of B's shape and sharding, all four
+ * cases; sums and products in fp32, rounded once.  Beside shmm_run with
+ * SHMM_FLAG_GELU, its form without a gate; the block's second half is
+ * shmm_run.  Operands are read in place, a block that several ranks hold from
+ * the lowest one, and every rank's C is written.
+ *   plan        in_dtype = out_dtype (F32 or BF16)
+ *   A_r[N]      in: box SHMM_TENSOR_A
+ *   gate_r[N], up_r[N]  in: box SHMM_TENSOR_B
+ *   C_r[N]      out: box SHMM_TENSOR_C
+ *   saved       out: what the backward call needs, or NULL
+ * The outputs share no byte with an input (UNSUPPORTED).  bf16 plans run on the
+ * tensor cores where shmm_run_scaled's sizes would (columns of the boxes
+ * multiples of 8; of C 16 to keep 8 bits), fp32 and other plans on the CUDA
+ * cores.  Flags: as there.
+ * Errors: NULL, ALIGN, DTYPE (in_dtype not out_dtype, E4M3; saved->dtype),
+ * SHAPE (I of 2^31 or more, J or K of 2^22 or more), UNSUPPORTED (activation,
+ * SHMM_FLAG_GELU, an overlap), CUDA. */
+shmm_status_t shmm_gated_forward(const shmm_plan_t *plan, int activation, const void *const *A_r,
+                                 const void *const *gate_r, const void *const *up_r, void *const *C_r,
+                                 const shmm_gated_saved_t *saved, void *stream);
+
+/* Workspace of shmm_gated_backward in bytes: the gradients of the two
+ * projections' results.  Host only.  Errors: NULL, DTYPE. */
+shmm_status_t shmm_gated_backward_workspace_size(const shmm_plan_t *plan, size_t *bytes);
+
+/* Gradient of shmm_gated_forward, for the gradient dC of its C.  With G and U
+ * as kept (restored in fp32):
+ *   dG = dC * U * act'(G), dU = dC * act(G)   in fp32, rounded once to the
+ *        plan's type: they are the next products' operands
+ *   dA    = dG . gate^T + dU . up^T
+ *   dgate = A^T . dG, dup = A^T . dU
+ *   dC_r[N]         in: box SHMM_TENSOR_C; a block that several ranks hold is
+ *                   read from the lowest one and counts once; so are `saved`'s
+ *   dA_r[N]         out: box SHMM_TENSOR_A, every rank's, or NULL: not wanted
+ *   dgate_r[N], dup_r[N]  out: box SHMM_TENSOR_B, every rank's; both or
+ *                   neither (NULL)
+ *   C_r[N]          out: C again, from G and U as kept (the operand of the
+ *                   second matmul's weight gradient: it need not be stored), or
+ *                   NULL
+ *   workspace       device memory of >= shmm_gated_backward_workspace_size()
+ *                   bytes, 256-byte aligned; nothing in it needs to start at
+ *                   zero, and calls that overlap on the GPU need one each
+ * All in the plan's type, rounded once.  The outputs share no byte with an
+ * input (UNSUPPORTED).  No rows: dgate and dup are zero.
+ * Errors: those of shmm_gated_forward, and NOMEM (workspace). */
+shmm_status_t shmm_gated_backward(const shmm_plan_t *plan, int activation, const void *const *dC_r,
+                                  const void *const *A_r, const void *const *gate_r, const void *const *up_r,
+                                  const shmm_gated_saved_t *saved, void *const *dA_r, void *const *dgate_r,
+                                  void *const *dup_r, void *const *C_r, void *workspace, size_t workspace_bytes,
+                                  void *stream);
 
 /* ---- planner: which operand to move ("Sharded matmuls and collectives on
  * a torus", Which operand to move: the ICI roofline) ---------------------- */

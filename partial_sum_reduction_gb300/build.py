@@ -26,7 +26,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
-SOURCES = ["planner.cpp", "adapters.cu", "api.cu", "collectives.cu", "gemm_simt.cu", "gemm_tcgen05.cu",
+SOURCES = ["planner.cpp", "adapters.cu", "api.cu", "blocks8.cu", "collectives.cu", "contract_simt.cu", "gemm_simt.cu", "gemm_tcgen05.cu",
            "layernorm_train.cu"]
 
 

@@ -124,6 +124,13 @@ shmm_status_t check_ptrs(const shmm_plan_t *p, const void *const *arr, int tenso
     return SHMM_OK;
 }
 
+// The calls that read a plan's operands as bf16 or fp32.
+shmm_status_t check_wide(const shmm_plan_t *p, const char *fn) {
+    if (p->in_dt == SHMM_E4M3)
+        return fail(SHMM_ERR_DTYPE, std::string(fn) + ": the plan's operands are E4M3 (shmm_run_scaled)");
+    return SHMM_OK;
+}
+
 shmm_status_t check_workspace(const shmm_plan_t *p, const void *workspace, size_t workspace_bytes,
                               const char *fn) {
     size_t need = 0;
@@ -366,6 +373,7 @@ shmm_status_t shmm_local_matmul(const shmm_plan_t *p, const void *const *A_r, co
     if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
     if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
     shmm_status_t st;
+    if ((st = check_wide(p, fn)) != SHMM_OK) return st;
     if ((st = check_ptrs(p, A_r, SHMM_TENSOR_A_LOCAL, fn, "A_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, B_r, SHMM_TENSOR_B_LOCAL, fn, "B_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, (const void *const *)P_r, SHMM_TENSOR_P, fn, "P_r")) != SHMM_OK) return st;
@@ -456,6 +464,7 @@ shmm_status_t shmm_all_gather(const shmm_plan_t *p, int tensor, const void *cons
     if (g->size == 1)
         return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": the plan gathers nothing for this tensor");
     shmm_status_t st;
+    if (tensor != SHMM_TENSOR_C && (st = check_wide(p, fn)) != SHMM_OK) return st;
     if ((st = check_ptrs(p, shard_r, src_t, fn, "shard_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, (const void *const *)full_r, dst_t, fn, "full_r")) != SHMM_OK) return st;
     std::string err;
@@ -474,6 +483,7 @@ shmm_status_t shmm_run(const shmm_plan_t *p, const void *const *A_r, const void 
     if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
     if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
     shmm_status_t st;
+    if ((st = check_wide(p, fn)) != SHMM_OK) return st;
     if ((st = check_ptrs(p, A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, B_r, SHMM_TENSOR_B, fn, "B_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, (const void *const *)C_r, SHMM_TENSOR_C, fn, "C_r")) != SHMM_OK) return st;
@@ -676,7 +686,7 @@ static std::vector<Span> spans(const shmm_plan_t *p, const void *const *arr, int
     std::vector<Span> v;
     for (int r = 0; r < p->nranks; ++r) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(arr[r]);
-        const int64_t bytes = p->boxes[tensor][r].numel() * (dt == SHMM_F32 ? 4 : 2);
+        const int64_t bytes = p->boxes[tensor][r].numel() * shmm::elem_bytes(dt);
         if (bytes) v.push_back({at, at + (uintptr_t)bytes, r});
     }
     return v;
@@ -1059,7 +1069,7 @@ static shmm_status_t check_adapters(const char *fn, const shmm_plan_t *p, int n,
     if (p->flags & SHMM_FLAG_GELU)
         return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": the adapters' product joins before the GeLU");
     shmm_status_t st;
-    if ((st = check_adapter_shape(fn, n, R)) != SHMM_OK) return st;
+    if ((st = check_wide(p, fn)) != SHMM_OK || (st = check_adapter_shape(fn, n, R)) != SHMM_OK) return st;
     if (p->J == 0 || p->K == 0) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": the plan's J or K is 0");
     if ((st = check_adapter_sizes(fn, p)) != SHMM_OK) return st;
     if ((st = check_ptr(fn, down, "down", 16)) != SHMM_OK || (st = check_ptr(fn, up, "up", 16)) != SHMM_OK) return st;
@@ -1177,6 +1187,518 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *p, int n_adapters, int r
     });
 }
 
+// ---- 8-bit operands, and the gated MLP block -------------------------------
+
+static int64_t scale_blocks(int64_t n) { return (n + SHMM_SCALE_BLOCK - 1) / SHMM_SCALE_BLOCK; }
+
+// A global array held as rank boxes of `tensor`, as a grid of blocks; a block
+// that several ranks hold is read from the lowest.  scale: with `scale_rows`,
+// the scales of 8-bit blocks, else NULL.
+static shmm::GridOperand grid_operand(const shmm_plan_t *p, int tensor, int64_t rows, int64_t cols,
+                                      const void *const *ptrs, shmm_dtype_t dt, const float *const *scale = nullptr,
+                                      int scale_rows = 1) {
+    shmm::GridOperand g;
+    const shmm::Box &b = p->boxes[tensor][0];
+    g.brows = b.ext[0];
+    g.bcols = g.ld = b.ext[1];
+    g.b0 = g.brows ? (int)(rows / g.brows) : 1;
+    g.b1 = g.bcols ? (int)(cols / g.bcols) : 1;
+    g.dt = dt;
+    g.at.assign((size_t)g.b0 * g.b1, nullptr);
+    if (scale) g.scale.assign(g.at.size(), nullptr);
+    g.scale_rows = scale_rows;
+    g.scale_ld = scale_blocks(g.bcols);
+    for (int r = p->nranks - 1; r >= 0; --r) {
+        const shmm::Box &q = p->boxes[tensor][r];
+        const size_t at = (size_t)((g.brows ? q.off[0] / g.brows : 0) * g.b1 + (g.bcols ? q.off[1] / g.bcols : 0));
+        g.at[at] = ptrs[r];
+        if (scale) g.scale[at] = scale[r];
+    }
+    return g;
+}
+
+static shmm::GridResult grid_result(const shmm_plan_t *p, int tensor, int64_t rows, int64_t cols, void *const *ptrs,
+                                    shmm_dtype_t dt, float *const *scale = nullptr) {
+    shmm::GridResult g;
+    const shmm::Box &b = p->boxes[tensor][0];
+    g.brows = b.ext[0];
+    g.bcols = b.ext[1];
+    g.b0 = g.brows ? (int)(rows / g.brows) : 1;
+    g.b1 = g.bcols ? (int)(cols / g.bcols) : 1;
+    g.dt = dt;
+    g.holders.resize((size_t)g.b0 * g.b1);
+    if (scale) g.scale_holders.resize(g.holders.size());
+    g.scale_ld = scale_blocks(g.bcols);
+    for (int r = 0; r < p->nranks; ++r) {
+        const shmm::Box &q = p->boxes[tensor][r];
+        const size_t at = (size_t)((g.brows ? q.off[0] / g.brows : 0) * g.b1 + (g.bcols ? q.off[1] / g.bcols : 0));
+        g.holders[at].push_back(ptrs[r]);
+        if (scale) g.scale_holders[at].push_back(scale[r]);
+    }
+    return g;
+}
+
+// A dense array of the workspace as a grid of one block; with the blocks' 8-bit
+// scales, as a grid of block columns `bcols` wide (a scale block starts at each).
+static shmm::GridOperand whole_operand(const void *at, int64_t rows, int64_t cols, shmm_dtype_t dt,
+                                       const float *scale = nullptr, int64_t bcols = 0) {
+    shmm::GridOperand g;
+    g.brows = rows;
+    g.ld = cols;
+    g.dt = dt;
+    g.bcols = scale ? bcols : cols;
+    g.b1 = g.bcols ? (int)(cols / g.bcols) : 1;
+    const int64_t per = scale_blocks(g.bcols);
+    for (int j = 0; j < g.b1; ++j) {
+        g.at.push_back(static_cast<const char *>(at) + j * g.bcols * shmm::elem_bytes(dt));
+        if (scale) g.scale.push_back(scale + j * per);
+    }
+    g.scale_ld = per * g.b1;
+    return g;
+}
+
+// Scales of the ranks' boxes of `tensor`: one fp32 array per rank.
+static shmm_status_t check_scales(const shmm_plan_t *p, const float *const *arr, int tensor, const char *fn,
+                                  const char *what) {
+    if (!arr) return fail(SHMM_ERR_NULL, std::string(fn) + ": " + what + " array is NULL");
+    for (int r = 0; r < p->nranks; ++r) {
+        if (p->boxes[tensor][r].numel() == 0) continue;
+        const shmm_status_t st = check_ptr(fn, arr[r], (std::string(what) + "[" + std::to_string(r) + "]").c_str(), 4);
+        if (st != SHMM_OK) return st;
+    }
+    return SHMM_OK;
+}
+
+static std::vector<Span> scale_spans(const shmm_plan_t *p, const float *const *arr, int tensor, int scale_rows) {
+    std::vector<Span> v;
+    for (int r = 0; r < p->nranks; ++r) {
+        const shmm::Box &b = p->boxes[tensor][r];
+        const uintptr_t at = reinterpret_cast<uintptr_t>(arr[r]);
+        const int64_t n = (b.ext[0] + scale_rows - 1) / scale_rows * scale_blocks(b.ext[1]);
+        if (n) v.push_back({at, at + (uintptr_t)(4 * n), r});
+    }
+    return v;
+}
+
+// A named set of buffers; every output of a call is compared with every input.
+struct NamedSpans {
+    const char *name;
+    std::vector<Span> at;
+};
+static shmm_status_t check_all_apart(const char *fn, const std::vector<NamedSpans> &outs, const std::vector<NamedSpans> &ins) {
+    for (const NamedSpans &o : outs)
+        for (const NamedSpans &i : ins) {
+            const shmm_status_t st = check_apart(fn, o.at, o.name, i.at, i.name);
+            if (st != SHMM_OK) return st;
+        }
+    return SHMM_OK;
+}
+
+static size_t up256(int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); }
+
+static shmm_status_t check_need(const char *fn, const void *workspace, size_t have, size_t need) {
+    if (have < need)
+        return fail(SHMM_ERR_NOMEM, std::string(fn) + ": workspace of " + std::to_string(have) + " bytes, " +
+                                        std::to_string(need) + " needed");
+    return need ? check_ptr(fn, workspace, "workspace", 256) : SHMM_OK;
+}
+
+// What these calls share: the plan, its flags and its sizes (the launches'
+// grids hold 2^31 rows and 2^22 columns of every product).
+static shmm_status_t check_block_plan(const char *fn, const shmm_plan_t *p) {
+    if (p->flags & SHMM_FLAG_GELU)
+        return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": not for a plan with SHMM_FLAG_GELU");
+    if (p->I >= (int64_t)1 << 31) return fail(SHMM_ERR_SHAPE, std::string(fn) + ": I must be below 2^31");
+    if (p->J >= (int64_t)1 << 22 || p->K >= (int64_t)1 << 22)
+        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": J and K must be below 2^22");
+    return SHMM_OK;
+}
+
+static shmm::ContractArgs contract_args(const shmm_plan_t *p, int64_t M, int64_t N, int64_t Kd) {
+    shmm::ContractArgs a;
+    a.M = M;
+    a.N = N;
+    a.Kd = Kd;
+    a.tensor_core = !(p->flags & SHMM_FLAG_SIMT);
+    a.max_sms = p->max_sms;
+    return a;
+}
+
+// Sizes and pointers of the two block conversions.
+static shmm_status_t check_blocks(const char *fn, int64_t rows, int64_t cols, shmm_dtype_t dtype, int block_rows,
+                                  const void *wide, const char *wide_name, const void *codes, const float *scales) {
+    if (dtype != SHMM_F32 && dtype != SHMM_BF16) return fail(SHMM_ERR_DTYPE, std::string(fn) + ": dtype must be F32 or BF16");
+    if (block_rows != 1 && block_rows != SHMM_SCALE_BLOCK)
+        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": block_rows must be 1 or 128");
+    if (rows < 0 || cols < 0 || rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 26)
+        return fail(SHMM_ERR_SHAPE, std::string(fn) + ": rows must be in [0, 2^31), cols in [0, 2^26)");
+    if (!rows || !cols) return SHMM_OK;
+    shmm_status_t st;
+    if ((st = check_ptr(fn, wide, wide_name, 16)) != SHMM_OK || (st = check_ptr(fn, codes, "codes", 16)) != SHMM_OK ||
+        (st = check_ptr(fn, scales, "scales", 4)) != SHMM_OK)
+        return st;
+    return SHMM_OK;
+}
+
+static std::vector<Span> one_span(const void *p, int64_t bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return {{at, at + (uintptr_t)bytes, 0}};
+}
+
+shmm_status_t shmm_quantize(int64_t rows, int64_t cols, shmm_dtype_t dtype, int block_rows, const void *x, void *codes,
+                            float *scales, void *stream) {
+    static const char *fn = "shmm_quantize";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+        shmm_status_t st;
+        if ((st = check_blocks(fn, rows, cols, dtype, block_rows, x, "x", codes, scales)) != SHMM_OK) return st;
+        if (!rows || !cols) return SHMM_OK;
+        const int64_t ns = (rows + block_rows - 1) / block_rows * scale_blocks(cols);
+        if ((st = check_all_apart(fn, {{"codes", one_span(codes, rows * cols)}, {"scales", one_span(scales, 4 * ns)}},
+                                  {{"x", one_span(x, rows * cols * shmm::elem_bytes(dtype))}})) != SHMM_OK)
+            return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        shmm::GridOperand src = whole_operand(x, rows, cols, dtype);
+        src.scale_rows = block_rows;
+        const int e = shmm::launch_quantize(src, codes, cols, scales, scale_blocks(cols), status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_dequantize(int64_t rows, int64_t cols, shmm_dtype_t dtype, int block_rows, const void *codes,
+                              const float *scales, void *y, void *stream) {
+    static const char *fn = "shmm_dequantize";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+        shmm_status_t st;
+        if ((st = check_blocks(fn, rows, cols, dtype, block_rows, y, "y", codes, scales)) != SHMM_OK) return st;
+        if (!rows || !cols) return SHMM_OK;
+        const int64_t ns = (rows + block_rows - 1) / block_rows * scale_blocks(cols);
+        if ((st = check_all_apart(fn, {{"y", one_span(y, rows * cols * shmm::elem_bytes(dtype))}},
+                                  {{"codes", one_span(codes, rows * cols)}, {"scales", one_span(scales, 4 * ns)}})) != SHMM_OK)
+            return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        shmm::GridOperand src = whole_operand(codes, rows, cols, SHMM_E4M3, scales, cols);
+        src.scale_rows = block_rows;
+        const int e = shmm::launch_dequantize(src, y, cols, dtype, status, stream);
+        if (e) return cuda_fail(fn, e);
+        return SHMM_OK;
+    });
+}
+
+// What the two calls on 8-bit operands share.
+static shmm_status_t check_scaled(const char *fn, const shmm_plan_t *p, const void *const *A_r,
+                                  const float *const *A_scale_r, const void *const *B_r, const float *const *B_scale_r) {
+    if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
+    if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+    if (p->in_dt != SHMM_E4M3) return fail(SHMM_ERR_DTYPE, std::string(fn) + ": the plan's operands are not E4M3");
+    shmm_status_t st;
+    if ((st = check_block_plan(fn, p)) != SHMM_OK || (st = check_ptrs(p, A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK ||
+        (st = check_scales(p, A_scale_r, SHMM_TENSOR_A, fn, "A_scale_r")) != SHMM_OK ||
+        (st = check_ptrs(p, B_r, SHMM_TENSOR_B, fn, "B_r")) != SHMM_OK ||
+        (st = check_scales(p, B_scale_r, SHMM_TENSOR_B, fn, "B_scale_r")) != SHMM_OK)
+        return st;
+    return SHMM_OK;
+}
+
+static std::vector<NamedSpans> scaled_inputs(const shmm_plan_t *p, const void *const *A_r, const float *const *A_scale_r,
+                                             const void *const *B_r, const float *const *B_scale_r) {
+    return {{"A_r", spans(p, A_r, SHMM_TENSOR_A, SHMM_E4M3)},
+            {"A_scale_r", scale_spans(p, A_scale_r, SHMM_TENSOR_A, 1)},
+            {"B_r", spans(p, B_r, SHMM_TENSOR_B, SHMM_E4M3)},
+            {"B_scale_r", scale_spans(p, B_scale_r, SHMM_TENSOR_B, SHMM_SCALE_BLOCK)}};
+}
+
+shmm_status_t shmm_run_scaled(const shmm_plan_t *p, const void *const *A_r, const float *const *A_scale_r,
+                              const void *const *B_r, const float *const *B_scale_r, void *const *C_r, void *stream) {
+    static const char *fn = "shmm_run_scaled";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_scaled(fn, p, A_r, A_scale_r, B_r, B_scale_r)) != SHMM_OK ||
+            (st = check_ptrs(p, (const void *const *)C_r, SHMM_TENSOR_C, fn, "C_r")) != SHMM_OK ||
+            (st = check_all_apart(fn, {{"C_r", spans(p, (const void *const *)C_r, SHMM_TENSOR_C, p->out_dt)}},
+                                  scaled_inputs(p, A_r, A_scale_r, B_r, B_scale_r))) != SHMM_OK)
+            return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        shmm::ContractArgs a = contract_args(p, p->I, p->K, p->J);
+        a.X[0] = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, SHMM_E4M3, A_scale_r);
+        a.Y[0] = grid_operand(p, SHMM_TENSOR_B, p->J, p->K, B_r, SHMM_E4M3, B_scale_r, SHMM_SCALE_BLOCK);
+        a.D[0] = grid_result(p, SHMM_TENSOR_C, p->I, p->K, C_r, p->out_dt);
+        const int e = shmm::launch_contract(a, status, stream, &err);
+        if (e) return cuda_fail(fn, e, err);
+        return SHMM_OK;
+    });
+}
+
+// The workspace of the two calls below: dC's values in 8 bits, their scales,
+// and A in bf16, each on a 256-byte boundary.
+struct ScaledScratch {
+    size_t codes, scales, wide;
+    int64_t scale_ld;
+    size_t bytes() const { return codes + scales + wide; }
+};
+static ScaledScratch scaled_scratch(const shmm_plan_t *p) {
+    const int64_t bcols = p->boxes[SHMM_TENSOR_C][0].ext[1];
+    const int64_t ld = bcols ? p->K / bcols * scale_blocks(bcols) : 0;
+    return {up256(p->I * p->K), up256(4 * p->I * ld), up256(2 * p->I * p->J), ld};
+}
+
+shmm_status_t shmm_scaled_backward_workspace_size(const shmm_plan_t *p, size_t *bytes) {
+    static const char *fn = "shmm_scaled_backward_workspace_size";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        if (!p || !bytes) return fail(SHMM_ERR_NULL, std::string(fn) + ": NULL argument");
+        if (p->in_dt != SHMM_E4M3) return fail(SHMM_ERR_DTYPE, std::string(fn) + ": the plan's operands are not E4M3");
+        *bytes = scaled_scratch(p).bytes();
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_scaled_backward(const shmm_plan_t *p, const void *const *dC_r, const void *const *A_r,
+                                   const float *const *A_scale_r, const void *const *B_r,
+                                   const float *const *B_scale_r, void *const *dA_r, void *const *dB_r,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    static const char *fn = "shmm_scaled_backward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_scaled(fn, p, A_r, A_scale_r, B_r, B_scale_r)) != SHMM_OK) return st;
+        if (p->out_dt != SHMM_BF16) return fail(SHMM_ERR_DTYPE, std::string(fn) + ": gradients are BF16, the plan's result is not");
+        if ((st = check_ptrs(p, dC_r, SHMM_TENSOR_C, fn, "dC_r")) != SHMM_OK) return st;
+        std::vector<NamedSpans> outs, ins = scaled_inputs(p, A_r, A_scale_r, B_r, B_scale_r);
+        ins.push_back({"dC_r", spans(p, dC_r, SHMM_TENSOR_C, p->out_dt)});
+        if (dA_r) {
+            if ((st = check_ptrs(p, (const void *const *)dA_r, SHMM_TENSOR_A, fn, "dA_r")) != SHMM_OK) return st;
+            outs.push_back({"dA_r", spans(p, (const void *const *)dA_r, SHMM_TENSOR_A, SHMM_BF16)});
+        }
+        if (dB_r) {
+            if ((st = check_ptrs(p, (const void *const *)dB_r, SHMM_TENSOR_B, fn, "dB_r")) != SHMM_OK) return st;
+            outs.push_back({"dB_r", spans(p, (const void *const *)dB_r, SHMM_TENSOR_B, SHMM_BF16)});
+        }
+        const ScaledScratch w = scaled_scratch(p);
+        if ((st = check_need(fn, workspace, workspace_bytes, w.bytes())) != SHMM_OK ||
+            (st = check_all_apart(fn, outs, ins)) != SHMM_OK)
+            return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        char *codes = static_cast<char *>(workspace);
+        float *scales = reinterpret_cast<float *>(codes + w.codes);
+        char *wide = codes + w.codes + w.scales;
+        int e = 0;
+        if (dA_r) {
+            const shmm::GridOperand dC = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, dC_r, p->out_dt);
+            e = shmm::launch_quantize(dC, codes, p->K, scales, w.scale_ld, status, stream);
+            if (e) return cuda_fail(fn, e);
+            shmm::ContractArgs a = contract_args(p, p->I, p->J, p->K);
+            a.y_t = true;
+            a.X[0] = whole_operand(codes, p->I, p->K, SHMM_E4M3, scales, dC.bcols);
+            a.Y[0] = grid_operand(p, SHMM_TENSOR_B, p->J, p->K, B_r, SHMM_E4M3, B_scale_r, SHMM_SCALE_BLOCK);
+            a.D[0] = grid_result(p, SHMM_TENSOR_A, p->I, p->J, dA_r, SHMM_BF16);
+            e = shmm::launch_contract(a, status, stream, &err);
+            if (e) return cuda_fail(fn, e, err);
+        }
+        if (dB_r) {
+            const shmm::GridOperand A = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, SHMM_E4M3, A_scale_r);
+            e = shmm::launch_dequantize(A, wide, p->J, SHMM_BF16, status, stream);
+            if (e) return cuda_fail(fn, e);
+            shmm::ContractArgs a = contract_args(p, p->J, p->K, p->I);
+            a.x_t = true;
+            a.X[0] = whole_operand(wide, p->I, p->J, SHMM_BF16);
+            a.Y[0] = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, dC_r, p->out_dt);
+            a.D[0] = grid_result(p, SHMM_TENSOR_B, p->J, p->K, dB_r, SHMM_BF16);
+            e = shmm::launch_contract(a, status, stream, &err);
+            if (e) return cuda_fail(fn, e, err);
+        }
+        return SHMM_OK;
+    });
+}
+
+// What the two calls of the gated block share.
+static shmm_status_t check_gated(const char *fn, const shmm_plan_t *p, int activation, const void *const *A_r,
+                                 const void *const *gate_r, const void *const *up_r, const shmm_gated_saved_t *saved) {
+    if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
+    if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
+    if (p->in_dt == SHMM_E4M3 || p->in_dt != p->out_dt)
+        return fail(SHMM_ERR_DTYPE, std::string(fn) + ": operands and result must be of one type, F32 or BF16");
+    if (activation != SHMM_SILU && activation != SHMM_GELU_TANH)
+        return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": unknown activation");
+    shmm_status_t st;
+    if ((st = check_block_plan(fn, p)) != SHMM_OK || (st = check_ptrs(p, A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK ||
+        (st = check_ptrs(p, gate_r, SHMM_TENSOR_B, fn, "gate_r")) != SHMM_OK ||
+        (st = check_ptrs(p, up_r, SHMM_TENSOR_B, fn, "up_r")) != SHMM_OK)
+        return st;
+    if (!saved) return SHMM_OK;
+    if (saved->dtype != p->in_dt && saved->dtype != SHMM_E4M3)
+        return fail(SHMM_ERR_DTYPE, std::string(fn) + ": saved values are of the plan's type or E4M3");
+    if ((st = check_ptrs(p, (const void *const *)saved->gate, SHMM_TENSOR_C, fn, "saved gate")) != SHMM_OK ||
+        (st = check_ptrs(p, (const void *const *)saved->up, SHMM_TENSOR_C, fn, "saved up")) != SHMM_OK)
+        return st;
+    if (saved->dtype == SHMM_E4M3 &&
+        ((st = check_scales(p, saved->gate_scale, SHMM_TENSOR_C, fn, "saved gate_scale")) != SHMM_OK ||
+         (st = check_scales(p, saved->up_scale, SHMM_TENSOR_C, fn, "saved up_scale")) != SHMM_OK))
+        return st;
+    return SHMM_OK;
+}
+
+static void add_saved_spans(const shmm_plan_t *p, const shmm_gated_saved_t *s, std::vector<NamedSpans> *to) {
+    to->push_back({"saved gate", spans(p, (const void *const *)s->gate, SHMM_TENSOR_C, s->dtype)});
+    to->push_back({"saved up", spans(p, (const void *const *)s->up, SHMM_TENSOR_C, s->dtype)});
+    if (s->dtype != SHMM_E4M3) return;
+    to->push_back({"saved gate_scale", scale_spans(p, s->gate_scale, SHMM_TENSOR_C, 1)});
+    to->push_back({"saved up_scale", scale_spans(p, s->up_scale, SHMM_TENSOR_C, 1)});
+}
+
+shmm_status_t shmm_gated_forward(const shmm_plan_t *p, int activation, const void *const *A_r,
+                                 const void *const *gate_r, const void *const *up_r, void *const *C_r,
+                                 const shmm_gated_saved_t *saved, void *stream) {
+    static const char *fn = "shmm_gated_forward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_gated(fn, p, activation, A_r, gate_r, up_r, saved)) != SHMM_OK ||
+            (st = check_ptrs(p, (const void *const *)C_r, SHMM_TENSOR_C, fn, "C_r")) != SHMM_OK)
+            return st;
+        std::vector<NamedSpans> outs = {{"C_r", spans(p, (const void *const *)C_r, SHMM_TENSOR_C, p->out_dt)}};
+        if (saved) add_saved_spans(p, saved, &outs);
+        if ((st = check_all_apart(fn, outs, {{"A_r", spans(p, A_r, SHMM_TENSOR_A, p->in_dt)},
+                                             {"gate_r", spans(p, gate_r, SHMM_TENSOR_B, p->in_dt)},
+                                             {"up_r", spans(p, up_r, SHMM_TENSOR_B, p->in_dt)}})) != SHMM_OK)
+            return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        shmm::ContractArgs a = contract_args(p, p->I, p->K, p->J);
+        a.gated = true;
+        a.act = activation;
+        a.X[0] = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, p->in_dt);
+        a.Y[0] = grid_operand(p, SHMM_TENSOR_B, p->J, p->K, gate_r, p->in_dt);
+        a.Y[1] = grid_operand(p, SHMM_TENSOR_B, p->J, p->K, up_r, p->in_dt);
+        a.D[0] = grid_result(p, SHMM_TENSOR_C, p->I, p->K, C_r, p->out_dt);
+        if (saved) {
+            const bool e8 = saved->dtype == SHMM_E4M3;
+            a.keep = true;
+            a.kept[0] = grid_result(p, SHMM_TENSOR_C, p->I, p->K, saved->gate, saved->dtype, e8 ? saved->gate_scale : nullptr);
+            a.kept[1] = grid_result(p, SHMM_TENSOR_C, p->I, p->K, saved->up, saved->dtype, e8 ? saved->up_scale : nullptr);
+        }
+        const int e = shmm::launch_contract(a, status, stream, &err);
+        if (e) return cuda_fail(fn, e, err);
+        return SHMM_OK;
+    });
+}
+
+static size_t gated_half(const shmm_plan_t *p) { return up256(p->I * p->K * shmm::elem_bytes(p->in_dt)); }
+
+shmm_status_t shmm_gated_backward_workspace_size(const shmm_plan_t *p, size_t *bytes) {
+    static const char *fn = "shmm_gated_backward_workspace_size";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        if (!p || !bytes) return fail(SHMM_ERR_NULL, std::string(fn) + ": NULL argument");
+        if (p->in_dt == SHMM_E4M3 || p->in_dt != p->out_dt)
+            return fail(SHMM_ERR_DTYPE, std::string(fn) + ": operands and result must be of one type, F32 or BF16");
+        *bytes = 2 * gated_half(p);
+        return SHMM_OK;
+    });
+}
+
+shmm_status_t shmm_gated_backward(const shmm_plan_t *p, int activation, const void *const *dC_r,
+                                  const void *const *A_r, const void *const *gate_r, const void *const *up_r,
+                                  const shmm_gated_saved_t *saved, void *const *dA_r, void *const *dgate_r,
+                                  void *const *dup_r, void *const *C_r, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    static const char *fn = "shmm_gated_backward";
+    return guarded([&]() -> shmm_status_t {
+        shmm::clear_error();
+        shmm::Range range(fn);
+        shmm_status_t st;
+        if ((st = check_gated(fn, p, activation, A_r, gate_r, up_r, saved)) != SHMM_OK) return st;
+        if (!saved) return fail(SHMM_ERR_NULL, std::string(fn) + ": saved is NULL");
+        if ((st = check_ptrs(p, dC_r, SHMM_TENSOR_C, fn, "dC_r")) != SHMM_OK) return st;
+        if (!dgate_r != !dup_r) return fail(SHMM_ERR_NULL, std::string(fn) + ": dgate_r and dup_r go together");
+        std::vector<NamedSpans> outs, ins = {{"dC_r", spans(p, dC_r, SHMM_TENSOR_C, p->out_dt)},
+                                             {"A_r", spans(p, A_r, SHMM_TENSOR_A, p->in_dt)},
+                                             {"gate_r", spans(p, gate_r, SHMM_TENSOR_B, p->in_dt)},
+                                             {"up_r", spans(p, up_r, SHMM_TENSOR_B, p->in_dt)}};
+        add_saved_spans(p, saved, &ins);
+        const struct {
+            void *const *at;
+            int tensor;
+            const char *name;
+        } out[4] = {{dA_r, SHMM_TENSOR_A, "dA_r"}, {dgate_r, SHMM_TENSOR_B, "dgate_r"}, {dup_r, SHMM_TENSOR_B, "dup_r"},
+                    {C_r, SHMM_TENSOR_C, "C_r"}};
+        for (const auto &o : out) {
+            if (!o.at) continue;
+            if ((st = check_ptrs(p, (const void *const *)o.at, o.tensor, fn, o.name)) != SHMM_OK) return st;
+            outs.push_back({o.name, spans(p, (const void *const *)o.at, o.tensor, p->in_dt)});
+        }
+        const size_t half = gated_half(p);
+        if ((st = check_need(fn, workspace, workspace_bytes, 2 * half)) != SHMM_OK ||
+            (st = check_all_apart(fn, outs, ins)) != SHMM_OK)
+            return st;
+        std::string err;
+        int *status = status_ptr(&err);
+        if (!status) return fail(SHMM_ERR_CUDA, std::string(fn) + ": " + err);
+        const bool e8 = saved->dtype == SHMM_E4M3;
+        shmm::GatedSlopeArgs s;
+        s.act = activation;
+        s.rows = p->I;
+        s.cols = p->K;
+        s.dH = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, dC_r, p->out_dt);
+        s.G = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, (const void *const *)saved->gate, saved->dtype,
+                           e8 ? saved->gate_scale : nullptr);
+        s.U = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, (const void *const *)saved->up, saved->dtype,
+                           e8 ? saved->up_scale : nullptr);
+        s.dG = workspace;
+        s.dU = static_cast<char *>(workspace) + half;
+        s.dt = p->in_dt;
+        s.want_H = C_r != nullptr;
+        if (C_r) s.H = grid_result(p, SHMM_TENSOR_C, p->I, p->K, C_r, p->out_dt);
+        int e = shmm::launch_gated_slopes(s, status, stream);
+        if (e) return cuda_fail(fn, e);
+        const shmm::GridOperand dG = whole_operand(s.dG, p->I, p->K, p->in_dt), dU = whole_operand(s.dU, p->I, p->K, p->in_dt);
+        if (dA_r) {
+            shmm::ContractArgs a = contract_args(p, p->I, p->J, p->K);
+            a.terms = 2;
+            a.y_t = true;
+            a.X[0] = dG;
+            a.X[1] = dU;
+            a.Y[0] = grid_operand(p, SHMM_TENSOR_B, p->J, p->K, gate_r, p->in_dt);
+            a.Y[1] = grid_operand(p, SHMM_TENSOR_B, p->J, p->K, up_r, p->in_dt);
+            a.D[0] = grid_result(p, SHMM_TENSOR_A, p->I, p->J, dA_r, p->in_dt);
+            e = shmm::launch_contract(a, status, stream, &err);
+            if (e) return cuda_fail(fn, e, err);
+        }
+        if (dgate_r) {
+            shmm::ContractArgs a = contract_args(p, p->J, p->K, p->I);
+            a.x_t = true;
+            a.two = true;
+            a.X[0] = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, p->in_dt);
+            a.Y[0] = dG;
+            a.Y[1] = dU;
+            a.D[0] = grid_result(p, SHMM_TENSOR_B, p->J, p->K, dgate_r, p->in_dt);
+            a.D[1] = grid_result(p, SHMM_TENSOR_B, p->J, p->K, dup_r, p->in_dt);
+            e = shmm::launch_contract(a, status, stream, &err);
+            if (e) return cuda_fail(fn, e, err);
+        }
+        return SHMM_OK;
+    });
+}
+
 shmm_status_t shmm_run_static_workspace(const shmm_plan_t *p, const void *const *A_r,
                                         const void *const *B_r, void *const *C_r, void *stream) {
     static const char *fn = "shmm_run_static_workspace";
@@ -1216,6 +1738,7 @@ shmm_status_t shmm_run_batch(int n, const shmm_plan_t *const *plans, const void 
         const std::string at = std::string(fn) + " (plan " + std::to_string(i) + ")";
         if (!p) return fail(SHMM_ERR_NULL, at + ": plan is NULL");
         shmm_status_t st;
+        if ((st = check_wide(p, at.c_str())) != SHMM_OK) return st;
         if ((st = check_ptrs(p, A_r[i], SHMM_TENSOR_A, at.c_str(), "A_r")) != SHMM_OK) return st;
         if ((st = check_ptrs(p, B_r[i], SHMM_TENSOR_B, at.c_str(), "B_r")) != SHMM_OK) return st;
         if ((st = check_ptrs(p, (const void *const *)C_r[i], SHMM_TENSOR_C, at.c_str(), "C_r")) != SHMM_OK)
@@ -1275,6 +1798,7 @@ shmm_status_t shmm_run_host(const shmm_plan_t *p, const void *A_host, const void
     if (!p) return fail(SHMM_ERR_NULL, std::string(fn) + ": plan is NULL");
     if (injected(fn)) return fail(SHMM_ERR_INJECTED, std::string(fn) + ": injected failure");
     shmm_status_t st;
+    if ((st = check_wide(p, fn)) != SHMM_OK) return st;
     if ((st = check_ptrs(p, (const void *const *)A_r, SHMM_TENSOR_A, fn, "A_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, (const void *const *)B_r, SHMM_TENSOR_B, fn, "B_r")) != SHMM_OK) return st;
     if ((st = check_ptrs(p, (const void *const *)C_r, SHMM_TENSOR_C, fn, "C_r")) != SHMM_OK) return st;

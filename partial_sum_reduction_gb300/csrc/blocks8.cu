@@ -1,0 +1,466 @@
+// 8-bit blocks (e4m3 values with a power-of-two scale for each 128 columns of
+// a row, or each 128 x 128 values) and the element-wise gradient of the gated
+// MLP block that reads them.
+//
+// A block's scale is the smallest 2^e (e >= -126) with 448 * 2^e at or above
+// its largest finite magnitude, 1 for a block of zeros.  e4m3's relative step
+// is the same in every binade, so a power of two gives up nothing but a part
+// of one binade of range, and the arithmetic around it is exact: x * 2^-e is
+// exact in fp32, the only rounding is the one to e4m3 (to nearest even), and a
+// restored value (four significant bits times 2^e) is exact in bf16 and fp32.
+// Infinities and NaN become NaN and leave the rest of the block as it is.
+//
+// All three kernels are bound by HBM: one read and one write of every value.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <vector>
+
+#include "checked.cuh"
+#include "e4m3.cuh"
+#include "gated_act.cuh"
+#include "pdl.cuh"
+#include "shmm_internal.h"
+
+namespace {
+
+using namespace shmm_dev;
+
+constexpr int kBlock = 128;
+constexpr int kShards = SHMM_MAX_RANKS;  // blocks of a grid
+constexpr int kThreads = 256;
+// A warp takes this many columns of one row, kPieces pieces of 256: enough
+// loads in flight per lane to cover the memory's latency.
+constexpr int kPieces = 4;
+constexpr int kChunk = 256 * kPieces;
+
+// Eight consecutive values of a row, `left` of which exist.
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int64_t left, float *v) {
+    if (VEC) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.0f;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *p, int64_t left, float *v) {
+    if (VEC) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+    }
+}
+// ... of 8-bit values.
+template <bool VEC>
+__device__ __forceinline__ void load8(const uint8_t *p, int64_t left, float *v) {
+    uint32_t w[2] = {0, 0};
+    if (VEC) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        w[0] = q.x, w[1] = q.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = from_e4m3x2(w[i / 2] >> (16 * (i % 2)));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, int64_t left, const float *v) {
+    if (VEC) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float *p, int64_t left, const float *v) {
+    if (VEC) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = v[i];
+    }
+}
+// Eight values times `inv` as e4m3.
+template <bool VEC>
+__device__ __forceinline__ void store8_e4m3(uint8_t *p, int64_t left, const float *v, float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = to_e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) | to_e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    if (VEC) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+// ---- to 8 bits ------------------------------------------------------------
+
+// One block of the source grid per blockIdx.z, read at src[z].
+struct ToK {
+    const void *src[kShards];
+    uint8_t *codes;
+    float *scale;
+    int64_t brows, bcols, src_ld, ld, scale_ld;
+    int64_t codes_n, scale_n;  // extents (bounds-checked build)
+    int b1;                    // blocks along the columns
+    int per;                   // scale blocks along a block's columns
+    int *status;
+};
+
+// A scale for each 128 columns of a row: a warp takes a row's chunk of
+// columns, 16 lanes a block, so the largest magnitude takes four shuffles.
+// 8192 x 16384 bf16: 67 us, 6.1 TB/s.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant__ ToK k) {
+    shmm_pdl::pdl_enter();
+    const int lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (row >= k.brows) return;
+    const int bi = blockIdx.z / k.b1, bj = blockIdx.z % k.b1;
+    const T *src = static_cast<const T *>(k.src[blockIdx.z]) + row * k.src_ld;
+    const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
+    const int64_t s_at = (bi * k.brows + row) * k.scale_ld + (int64_t)bj * k.per;
+    for (int64_t c0 = (int64_t)blockIdx.y * kChunk; c0 < k.bcols; c0 += (int64_t)gridDim.y * kChunk) {
+        float v[kPieces][8];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int64_t c = c0 + i * 256 + lane * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            if (c < k.bcols && piece_in_bounds<VEC>(k.status, row * k.src_ld + c, k.bcols - c, k.brows * k.src_ld))
+                load8<VEC>(src + c, k.bcols - c, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int64_t c = c0 + i * 256 + lane * 8;
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[i][j]));
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            const int e = scale_exp(amax);
+            if (c >= k.bcols) continue;
+            if (piece_in_bounds<VEC>(k.status, at + c, k.bcols - c, k.codes_n))
+                store8_e4m3<VEC>(k.codes + at + c, k.bcols - c, v[i], pow2(-e));
+            if (lane % 16 == 0 && in_bounds(k.status, s_at + c / kBlock, 1, k.scale_n)) k.scale[s_at + c / kBlock] = pow2(e);
+        }
+    }
+}
+
+// A scale for each 128 x 128 values: a CTA takes a block, which stays in its
+// registers between the largest magnitude and the rounding.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_constant__ ToK k) {
+    shmm_pdl::pdl_enter();
+    __shared__ float part[kThreads / 32];
+    const int bi = blockIdx.z / k.b1, bj = blockIdx.z % k.b1;
+    const int x = threadIdx.x % 16, y = threadIdx.x / 16;
+    const T *src = static_cast<const T *>(k.src[blockIdx.z]);
+    const int64_t rb = blockIdx.x;
+    for (int64_t cb = blockIdx.y; cb < k.per; cb += gridDim.y) {
+        const int64_t c = cb * kBlock + x * 8, r0 = rb * kBlock + y;
+        float v[8][8];
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 16 * i;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            if (r < k.brows && c < k.bcols &&
+                piece_in_bounds<VEC>(k.status, r * k.src_ld + c, k.bcols - c, k.brows * k.src_ld))
+                load8<VEC>(src + r * k.src_ld + c, k.bcols - c, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[i][j]));
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        __syncthreads();  // the last block's partial maxima have been read
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) amax = fmaxf(amax, part[i]);
+        const int e = scale_exp(amax);
+        const int64_t s_at = (bi * ((k.brows + kBlock - 1) / kBlock) + rb) * k.scale_ld + (int64_t)bj * k.per + cb;
+        if (threadIdx.x == 0 && in_bounds(k.status, s_at, 1, k.scale_n)) k.scale[s_at] = pow2(e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 16 * i, at = (bi * k.brows + r) * k.ld + bj * k.bcols + c;
+            if (r < k.brows && c < k.bcols && piece_in_bounds<VEC>(k.status, at, k.bcols - c, k.codes_n))
+                store8_e4m3<VEC>(k.codes + at, k.bcols - c, v[i], pow2(-e));
+        }
+    }
+}
+
+// ---- and back -------------------------------------------------------------
+
+struct BackK {
+    const void *src[kShards];
+    const float *scale[kShards];
+    void *dst;
+    int64_t brows, bcols, src_ld, ld, scale_ld, dst_n;
+    int b1, scale_rows;
+    int *status;
+};
+
+// 8192 x 4096 to bf16: 17 us, 6.0 TB/s.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ BackK k) {
+    shmm_pdl::pdl_enter();
+    const int lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (row >= k.brows) return;
+    const int bi = blockIdx.z / k.b1, bj = blockIdx.z % k.b1;
+    const uint8_t *src = static_cast<const uint8_t *>(k.src[blockIdx.z]) + row * k.src_ld;
+    const int64_t s_row = row / k.scale_rows * k.scale_ld;
+    const int64_t s_n = (k.brows + k.scale_rows - 1) / k.scale_rows * k.scale_ld;
+    const float *scale = k.scale[blockIdx.z] + s_row;
+    const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
+    for (int64_t c0 = (int64_t)blockIdx.y * kChunk; c0 < k.bcols; c0 += (int64_t)gridDim.y * kChunk) {
+        float v[kPieces][8], s[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int64_t c = c0 + i * 256 + lane * 8;
+            s[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            if (c < k.bcols && piece_in_bounds<VEC>(k.status, row * k.src_ld + c, k.bcols - c, k.brows * k.src_ld) &&
+                in_bounds(k.status, s_row + c / kBlock, 1, s_n)) {
+                load8<VEC>(src + c, k.bcols - c, v[i]);
+                s[i] = scale[c / kBlock];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int64_t c = c0 + i * 256 + lane * 8;
+            if (c >= k.bcols || !piece_in_bounds<VEC>(k.status, at + c, k.bcols - c, k.dst_n)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] *= s[i];
+            store8<VEC>(static_cast<T *>(k.dst) + at + c, k.bcols - c, v[i]);
+        }
+    }
+}
+
+// ---- the gated block's gradient, element by element ------------------------
+
+struct SlopeK {
+    const void *dH[kShards], *G[kShards], *U[kShards];
+    const float *g_scale[kShards], *u_scale[kShards];
+    void *H[kShards];              // holders of every block, block by block
+    uint16_t h_first[kShards + 1]; // block z's holders: H[h_first[z]] .. H[h_first[z + 1] - 1]
+    void *dG, *dU;
+    int64_t brows, bcols, ld, scale_ld, out_n;
+    int b1;
+    int *status;
+};
+
+// T: the gradients' type; S: the kept pre-activations' (uint8_t: 8 bits).
+// Pieces of eight values, two in flight per lane.
+template <typename T, typename S, int ACT, bool VEC>
+__global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__ SlopeK k) {
+    constexpr bool E8 = sizeof(S) == 1;
+    constexpr int PIECES = 2;
+    shmm_pdl::pdl_enter();
+    const int lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (row >= k.brows) return;
+    const int z = blockIdx.z, bi = z / k.b1, bj = z % k.b1;
+    const int64_t in = row * k.bcols, n = k.brows * k.bcols;
+    const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
+    for (int64_t c0 = (int64_t)blockIdx.y * (256 * PIECES); c0 < k.bcols; c0 += (int64_t)gridDim.y * (256 * PIECES)) {
+        float d[PIECES][8], g[PIECES][8], u[PIECES][8], gs[PIECES], us[PIECES];
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int64_t c = c0 + i * 256 + lane * 8, left = k.bcols - c;
+            gs[i] = us[i] = 1.0f;
+            if (left <= 0 || !piece_in_bounds<VEC>(k.status, in + c, left, n)) continue;
+            load8<VEC>(static_cast<const T *>(k.dH[z]) + in + c, left, d[i]);
+            load8<VEC>(static_cast<const S *>(k.G[z]) + in + c, left, g[i]);
+            load8<VEC>(static_cast<const S *>(k.U[z]) + in + c, left, u[i]);
+            const int64_t s = row * k.scale_ld + c / kBlock;
+            if (E8 && in_bounds(k.status, s, 1, k.brows * k.scale_ld)) {
+                gs[i] = k.g_scale[z][s];
+                us[i] = k.u_scale[z][s];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int64_t c = c0 + i * 256 + lane * 8, left = k.bcols - c;
+            if (left <= 0 || !piece_in_bounds<VEC>(k.status, at + c, left, k.out_n)) continue;
+            float h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float gj = E8 ? g[i][j] * gs[i] : g[i][j], uj = E8 ? u[i][j] * us[i] : u[i][j];
+                float slope;
+                const float a = gate_act_slope<ACT>(gj, &slope);
+                h[j] = a * uj;
+                g[i][j] = d[i][j] * uj * slope;
+                u[i][j] = d[i][j] * a;
+            }
+            store8<VEC>(static_cast<T *>(k.dG) + at + c, left, g[i]);
+            store8<VEC>(static_cast<T *>(k.dU) + at + c, left, u[i]);
+            for (int q = k.h_first[z]; q < k.h_first[z + 1]; ++q)
+                if (piece_in_bounds<VEC>(k.status, in + c, left, n)) store8<VEC>(static_cast<T *>(k.H[q]) + in + c, left, h);
+        }
+    }
+}
+
+// ---- host side --------------------------------------------------------------
+
+bool aligned(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
+// Whole 8-value pieces of rows `ld` apart (and blocks bcols wide) start on
+// their own boundaries.
+bool pieces_fit(int64_t bcols, int64_t ld) { return bcols % 8 == 0 && ld % 8 == 0; }
+
+dim3 rows_grid(int64_t brows, int64_t bcols, int64_t chunk, int blocks) {
+    const int64_t y = (bcols + chunk - 1) / chunk;
+    return dim3((unsigned)((brows + kThreads / 32 - 1) / (kThreads / 32)), (unsigned)(y < 65535 ? y : 65535),
+                (unsigned)blocks);
+}
+
+}  // namespace
+
+namespace shmm {
+
+int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scale, int64_t scale_ld, int *status,
+                    void *stream) {
+    const int blocks = src.b0 * src.b1;
+    if (src.brows == 0 || src.bcols == 0) return 0;
+    ToK k = {};
+    for (int i = 0; i < blocks; ++i) k.src[i] = src.at[i];
+    k.codes = static_cast<uint8_t *>(codes);
+    k.scale = scale;
+    k.brows = src.brows;
+    k.bcols = src.bcols;
+    k.src_ld = src.ld;
+    k.ld = ld;
+    k.scale_ld = scale_ld;
+    k.b1 = src.b1;
+    k.per = (int)((src.bcols + kBlock - 1) / kBlock);
+    k.codes_n = src.b0 * src.brows * ld;
+    k.scale_n = src.b0 * ((src.brows + src.scale_rows - 1) / src.scale_rows) * scale_ld;
+    k.status = status;
+    bool vec = pieces_fit(src.bcols, src.ld) && ld % 8 == 0 && aligned(codes, 8);
+    for (int i = 0; i < blocks; ++i) vec = vec && aligned(src.at[i], 16);
+    const bool f32 = src.dt == SHMM_F32, squares = src.scale_rows == kBlock;
+    dim3 grid = rows_grid(src.brows, src.bcols, kChunk, blocks);
+    if (squares)
+        grid = dim3((unsigned)((src.brows + kBlock - 1) / kBlock), (unsigned)(k.per < 65535 ? k.per : 65535), (unsigned)blocks);
+    cudaStream_t s = (cudaStream_t)stream;
+    count_launch();
+#define GO(KERN, T) (int)(vec ? shmm_pdl::launch_pdl(KERN<T, true>, grid, dim3(kThreads), 0, s, k) \
+                              : shmm_pdl::launch_pdl(KERN<T, false>, grid, dim3(kThreads), 0, s, k))
+    if (squares) return f32 ? GO(to_squares_kernel, float) : GO(to_squares_kernel, __nv_bfloat16);
+    return f32 ? GO(to_rows_kernel, float) : GO(to_rows_kernel, __nv_bfloat16);
+#undef GO
+}
+
+int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream) {
+    const int blocks = src.b0 * src.b1;
+    if (src.brows == 0 || src.bcols == 0) return 0;
+    BackK k = {};
+    bool vec = pieces_fit(src.bcols, src.ld) && ld % 8 == 0 && aligned(dst, 16);
+    for (int i = 0; i < blocks; ++i) {
+        k.src[i] = src.at[i];
+        k.scale[i] = src.scale[i];
+        vec = vec && aligned(src.at[i], 8);
+    }
+    k.dst = dst;
+    k.brows = src.brows;
+    k.bcols = src.bcols;
+    k.src_ld = src.ld;
+    k.ld = ld;
+    k.scale_ld = src.scale_ld;
+    k.dst_n = src.b0 * src.brows * ld;
+    k.b1 = src.b1;
+    k.scale_rows = src.scale_rows;
+    k.status = status;
+    const dim3 grid = rows_grid(src.brows, src.bcols, kChunk, blocks);
+    cudaStream_t s = (cudaStream_t)stream;
+    count_launch();
+    if (dt == SHMM_F32)
+        return (int)(vec ? shmm_pdl::launch_pdl(back_kernel<float, true>, grid, dim3(kThreads), 0, s, k)
+                         : shmm_pdl::launch_pdl(back_kernel<float, false>, grid, dim3(kThreads), 0, s, k));
+    return (int)(vec ? shmm_pdl::launch_pdl(back_kernel<__nv_bfloat16, true>, grid, dim3(kThreads), 0, s, k)
+                     : shmm_pdl::launch_pdl(back_kernel<__nv_bfloat16, false>, grid, dim3(kThreads), 0, s, k));
+}
+
+int launch_gated_slopes(const GatedSlopeArgs &a, int *status, void *stream) {
+    const int blocks = a.dH.b0 * a.dH.b1;
+    if (a.dH.brows == 0 || a.dH.bcols == 0) return 0;
+    const bool e8 = a.G.dt == SHMM_E4M3;
+    SlopeK k = {};
+    bool vec = pieces_fit(a.dH.bcols, a.cols) && aligned(a.dG, 16) && aligned(a.dU, 16);
+    int h = 0;
+    for (int i = 0; i < blocks; ++i) {
+        k.dH[i] = a.dH.at[i];
+        k.G[i] = a.G.at[i];
+        k.U[i] = a.U.at[i];
+        vec = vec && aligned(k.dH[i], 16) && aligned(k.G[i], e8 ? 8 : 16) && aligned(k.U[i], e8 ? 8 : 16);
+        if (e8) {
+            k.g_scale[i] = a.G.scale[i];
+            k.u_scale[i] = a.U.scale[i];
+        }
+        k.h_first[i] = (uint16_t)h;
+        if (a.want_H)
+            for (void *p : a.H.holders[i]) {
+                k.H[h++] = p;
+                vec = vec && aligned(p, 16);
+            }
+    }
+    k.h_first[blocks] = (uint16_t)h;
+    k.dG = a.dG;
+    k.dU = a.dU;
+    k.brows = a.dH.brows;
+    k.bcols = a.dH.bcols;
+    k.ld = a.cols;
+    k.scale_ld = a.G.scale_ld;
+    k.out_n = a.rows * a.cols;
+    k.b1 = a.dH.b1;
+    k.status = status;
+    const dim3 grid = rows_grid(k.brows, k.bcols, 512, blocks);
+    cudaStream_t s = (cudaStream_t)stream;
+    count_launch();
+#define GO(T, S, ACT) (int)(vec ? shmm_pdl::launch_pdl(slope_kernel<T, S, ACT, true>, grid, dim3(kThreads), 0, s, k) \
+                                : shmm_pdl::launch_pdl(slope_kernel<T, S, ACT, false>, grid, dim3(kThreads), 0, s, k))
+#define GO_ACT(T, S) (a.act == SHMM_SILU ? GO(T, S, SHMM_SILU) : GO(T, S, SHMM_GELU_TANH))
+    if (a.dt == SHMM_F32) return e8 ? GO_ACT(float, uint8_t) : GO_ACT(float, float);
+    return e8 ? GO_ACT(__nv_bfloat16, uint8_t) : GO_ACT(__nv_bfloat16, __nv_bfloat16);
+#undef GO_ACT
+#undef GO
+}
+
+}  // namespace shmm

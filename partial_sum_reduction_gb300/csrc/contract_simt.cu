@@ -1,0 +1,342 @@
+// The products of the gated MLP block and of 8-bit operands on the CUDA cores:
+// any type, size and sharding, for fp32 operands and for shapes that the tensor
+// cores' loads cannot address.
+//
+// A CTA computes 32 rows by 128 columns of the result, the columns counted from
+// a result block's left edge, so a 128-column scale block of a kept 8-bit
+// result lies in one warp: warp w has rows 4w .. 4w+3, lane l columns 4l ..
+// 4l+3.  The contracted dim goes through shared memory 32 at a time, the next
+// piece's loads in flight while one is used.  Everything is fp32; sums of 256
+// products are added to a second sum, so an element's error grows with the
+// number of pieces and not of products.
+//
+// Bound by the FMA pipe's operand reads (two or three 16-byte shared reads per
+// 16 or 32 FMAs).
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <vector>
+
+#include "checked.cuh"
+#include "e4m3.cuh"
+#include "gated_act.cuh"
+#include "pdl.cuh"
+#include "shmm_internal.h"
+
+namespace {
+
+using namespace shmm_dev;
+
+constexpr int TM = 32, TN = 128, TK = 32;
+constexpr int kThreads = 256;
+constexpr int kFlush = 8;   // pieces of TK in the first sum
+constexpr int XS = TM + 4, YS = TN + 4;  // shared rows of the pieces, whole 16-byte vectors
+
+// An operand: at most CAP blocks.
+template <int CAP>
+struct Op {
+    const void *at[CAP];
+    const float *scale[CAP];
+    int64_t brows, bcols, ld, scale_ld;
+    int b0, b1, dt, scale_rows;
+};
+
+template <int CAP>
+struct Res {
+    void *to[CAP];
+    float *scale[CAP];
+    uint16_t first[CAP + 1];  // block p's holders: to[first[p]] .. to[first[p + 1] - 1]
+    int64_t brows, bcols, scale_ld;
+    int b0, b1, dt;
+};
+
+template <int CAP>
+struct SimtK {
+    Op<CAP> X[2], Y[2];
+    Res<CAP> D, kept[2];
+    int64_t M, N, Kd;
+    int terms, x_t, y_t, keep, act;
+    int n_per;  // column tiles of a result block
+    int *status;
+};
+
+template <int CAP>
+__device__ __forceinline__ float fetch(const Op<CAP> &o, int64_t r, int64_t c, int *status) {
+    int p = 0;
+    if (o.b0 > 1) {
+        const int64_t b = r / o.brows;
+        r -= b * o.brows;
+        p = (int)b * o.b1;
+    }
+    if (o.b1 > 1) {
+        const int64_t b = c / o.bcols;
+        c -= b * o.bcols;
+        p += (int)b;
+    }
+    const int64_t i = r * o.ld + c;
+    if (!in_bounds(status, i, 1, (o.brows - 1) * o.ld + o.bcols)) return 0.0f;
+    if (o.dt == SHMM_F32) return static_cast<const float *>(o.at[p])[i];
+    if (o.dt == SHMM_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(o.at[p])[i]);
+    const int64_t s = r / o.scale_rows * o.scale_ld + c / 128;
+    if (!in_bounds(status, s, 1, (o.brows + o.scale_rows - 1) / o.scale_rows * o.scale_ld)) return 0.0f;
+    return from_e4m3x2(static_cast<const uint8_t *>(o.at[p])[i]).x * o.scale[p][s];
+}
+
+// Element (m, k) of X or (k, n) of Y, each stored as it is or transposed.
+template <int CAP>
+__device__ __forceinline__ float fetch_at(const Op<CAP> &o, int64_t r, int64_t c, int t, int *status) {
+    return t ? fetch(o, c, r, status) : fetch(o, r, c, status);
+}
+
+__device__ __forceinline__ void store_as(void *p, int64_t i, int dt, float v) {
+    if (dt == SHMM_F32) static_cast<float *>(p)[i] = v;
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// Four values of global row `row`, columns cl .. cl + 3 of block column cb, to
+// every holder.
+template <int CAP>
+__device__ __forceinline__ void put4(const Res<CAP> &d, int64_t row, int cb, int64_t cl, const float *v, int *status) {
+    const int64_t br = row / d.brows, at = (row - br * d.brows) * d.bcols + cl;
+    const int p = (int)br * d.b1 + cb;
+    for (int q = d.first[p]; q < d.first[p + 1]; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (cl + j < d.bcols && in_bounds(status, at + j, 1, d.brows * d.bcols)) store_as(d.to[q], at + j, d.dt, v[j]);
+}
+
+// The same in 8 bits: the warp holds the row's block of 128 columns.
+template <int CAP>
+__device__ __forceinline__ void put4_e4m3(const Res<CAP> &d, int64_t row, bool row_ok, int cb, int64_t cl, const float *v,
+                                          int lane, int *status) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (cl + j < d.bcols) amax = fmaxf(amax, finite_abs(v[j]));
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, s));
+    if (!row_ok) return;
+    const int e = scale_exp(amax);
+    const float inv = pow2(-e);
+    const int64_t br = row / d.brows, rl = row - br * d.brows, at = rl * d.bcols + cl, s = rl * d.scale_ld + cl / 128;
+    const int p = (int)br * d.b1 + cb;
+    const uint32_t w = to_e4m3x2(v[0] * inv, v[1] * inv) | to_e4m3x2(v[2] * inv, v[3] * inv) << 16;
+    for (int q = d.first[p]; q < d.first[p + 1]; ++q) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (cl + j < d.bcols && in_bounds(status, at + j, 1, d.brows * d.bcols))
+                static_cast<uint8_t *>(d.to[q])[at + j] = (uint8_t)(w >> (8 * j));
+        if (lane == 0 && in_bounds(status, s, 1, d.brows * d.scale_ld)) d.scale[q][s] = pow2(e);
+    }
+}
+
+template <int CAP, bool GATED>
+__global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_constant__ SimtK<CAP> k) {
+    constexpr int NY = GATED ? 2 : 1;
+    constexpr int PX = TM * TK / kThreads, PY = TK * TN / kThreads;
+    __shared__ __align__(16) float xs[TK][XS];
+    __shared__ __align__(16) float ys[NY][TK][YS];
+    shmm_pdl::pdl_enter();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t m0 = (int64_t)blockIdx.x * TM;
+    const int cb = blockIdx.y / k.n_per;                                    // result block column
+    const int64_t n0l = (int64_t)(blockIdx.y % k.n_per) * TN;               // first column in it
+    const int64_t n0 = cb * k.D.bcols + n0l, n1 = (cb + 1) * k.D.bcols;     // ... of the whole array, and the block's end
+    const int64_t per_term = (k.Kd + TK - 1) / TK, pieces = k.terms * per_term;
+
+    float xr[PX], yr[NY][PY];
+    auto ask = [&](int64_t piece) {
+        const int t = piece >= per_term ? 1 : 0;
+        const int64_t k0 = (piece - t * per_term) * TK;
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            const int64_t kk = k0 + (k.x_t ? at / TM : at % TK), m = m0 + (k.x_t ? at % TM : at / TK);
+            xr[i] = kk < k.Kd && m < k.M ? fetch_at(k.X[t], m, kk, k.x_t, k.status) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < PY; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            const int64_t kk = k0 + (k.y_t ? at % TK : at / TN), n = n0 + (k.y_t ? at / TK : at % TN);
+            const bool in = kk < k.Kd && n < n1;
+            if (GATED) {
+                yr[0][i] = in ? fetch_at(k.Y[0], kk, n, k.y_t, k.status) : 0.0f;
+                yr[NY - 1][i] = in ? fetch_at(k.Y[1], kk, n, k.y_t, k.status) : 0.0f;
+            } else {
+                yr[0][i] = in ? fetch_at(k.Y[t], kk, n, k.y_t, k.status) : 0.0f;
+            }
+        }
+    };
+
+    float sum[NY][4][4] = {}, acc[NY][4][4] = {};
+    if (pieces) ask(0);
+    for (int64_t piece = 0; piece < pieces; ++piece) {
+        __syncthreads();  // the last piece has been used
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            if (k.x_t) xs[at / TM][at % TM] = xr[i];
+            else xs[at % TK][at / TK] = xr[i];
+        }
+#pragma unroll
+        for (int y = 0; y < NY; ++y)
+#pragma unroll
+            for (int i = 0; i < PY; ++i) {
+                const int at = threadIdx.x + i * kThreads;
+                if (k.y_t) ys[y][at % TK][at / TK] = yr[y][i];
+                else ys[y][at / TN][at % TN] = yr[y][i];
+            }
+        __syncthreads();
+        if (piece + 1 < pieces) ask(piece + 1);
+#pragma unroll
+        for (int kk = 0; kk < TK; ++kk) {
+            const float4 x4 = *reinterpret_cast<const float4 *>(&xs[kk][warp * 4]);
+            const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+            for (int y = 0; y < NY; ++y) {
+                const float4 y4 = *reinterpret_cast<const float4 *>(&ys[y][kk][lane * 4]);
+                const float v[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[y][i][j] = fmaf(x[i], v[j], acc[y][i][j]);
+            }
+        }
+        if (piece % kFlush == kFlush - 1 || piece + 1 == pieces) {
+#pragma unroll
+            for (int y = 0; y < NY; ++y)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sum[y][i][j] += acc[y][i][j];
+                        acc[y][i][j] = 0.0f;
+                    }
+        }
+    }
+
+    const int64_t cl = n0l + lane * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = m0 + warp * 4 + i;
+        const bool row_ok = row < k.M;
+        if (GATED) {
+            if (k.keep) {
+#pragma unroll
+                for (int y = 0; y < NY; ++y) {
+                    if (k.kept[y].dt == SHMM_E4M3) put4_e4m3(k.kept[y], row, row_ok, cb, cl, sum[y][i], lane, k.status);
+                    else if (row_ok) put4(k.kept[y], row, cb, cl, sum[y][i], k.status);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float g = sum[0][i][j];
+                sum[0][i][j] = (k.act == SHMM_SILU ? gate_act<SHMM_SILU>(g) : gate_act<SHMM_GELU_TANH>(g)) * sum[NY - 1][i][j];
+            }
+        }
+        if (row_ok) put4(k.D, row, cb, cl, sum[0][i], k.status);
+    }
+}
+
+// ---- host side --------------------------------------------------------------
+
+template <int CAP>
+void set_op(Op<CAP> *o, const shmm::GridOperand &g) {
+    for (size_t i = 0; i < g.at.size(); ++i) {
+        o->at[i] = g.at[i];
+        if (!g.scale.empty()) o->scale[i] = g.scale[i];
+    }
+    o->brows = g.brows;
+    o->bcols = g.bcols;
+    o->ld = g.ld;
+    o->scale_ld = g.scale_ld;
+    o->b0 = g.b0;
+    o->b1 = g.b1;
+    o->dt = g.dt;
+    o->scale_rows = g.scale_rows;
+}
+
+template <int CAP>
+void set_res(Res<CAP> *d, const shmm::GridResult &g) {
+    int n = 0;
+    for (size_t p = 0; p < g.holders.size(); ++p) {
+        d->first[p] = (uint16_t)n;
+        for (size_t q = 0; q < g.holders[p].size(); ++q, ++n) {
+            d->to[n] = g.holders[p][q];
+            if (!g.scale_holders.empty()) d->scale[n] = g.scale_holders[p][q];
+        }
+    }
+    d->first[g.holders.size()] = (uint16_t)n;
+    d->brows = g.brows;
+    d->bcols = g.bcols;
+    d->scale_ld = g.scale_ld;
+    d->b0 = g.b0;
+    d->b1 = g.b1;
+    d->dt = g.dt;
+}
+
+// Blocks, and holders, of the largest table.
+size_t entries(const shmm::ContractArgs &a) {
+    size_t n = 1;
+    for (int i = 0; i < 2; ++i) {
+        n = n > a.X[i].at.size() ? n : a.X[i].at.size();
+        n = n > a.Y[i].at.size() ? n : a.Y[i].at.size();
+        for (const shmm::GridResult *d : {&a.D[i], &a.kept[i]}) {
+            size_t h = 0;
+            for (const auto &b : d->holders) h += b.size();
+            n = n > h ? n : h;
+        }
+    }
+    return n;
+}
+
+template <int CAP>
+cudaError_t launch(const shmm::ContractArgs &a, int which, int *status, cudaStream_t s) {
+    static_assert(sizeof(SimtK<CAP>) <= 32764, "kernel parameters");
+    SimtK<CAP> k = {};
+    for (int i = 0; i < 2; ++i) {
+        set_op(&k.X[i], a.X[i]);
+        set_op(&k.Y[i], a.two ? a.Y[which] : a.Y[i]);
+        if (a.keep) set_res(&k.kept[i], a.kept[i]);
+    }
+    set_res(&k.D, a.D[which]);
+    k.M = a.M;
+    k.N = a.N;
+    k.Kd = a.Kd;
+    k.terms = a.terms;
+    k.x_t = a.x_t;
+    k.y_t = a.y_t;
+    k.keep = a.keep;
+    k.act = a.act;
+    k.n_per = (int)((k.D.bcols + TN - 1) / TN);
+    k.status = status;
+    const dim3 grid((unsigned)((a.M + TM - 1) / TM), (unsigned)(k.n_per * k.D.b1));
+    shmm::count_launch();
+    return a.gated ? shmm_pdl::launch_pdl(contract_simt_kernel<CAP, true>, grid, dim3(kThreads), 0, s, k)
+                   : shmm_pdl::launch_pdl(contract_simt_kernel<CAP, false>, grid, dim3(kThreads), 0, s, k);
+}
+
+}  // namespace
+
+namespace shmm {
+
+int launch_contract_simt(const ContractArgs &a, int *status, void *stream) {
+    if (a.M == 0 || a.N == 0) return 0;
+    const bool small = entries(a) <= 16;
+    for (int w = 0; w < (a.two ? 2 : 1); ++w) {
+        const cudaError_t e = small ? launch<16>(a, w, status, (cudaStream_t)stream)
+                                    : launch<SHMM_MAX_RANKS>(a, w, status, (cudaStream_t)stream);
+        if (e != cudaSuccess) return (int)e;
+    }
+    return 0;
+}
+
+int launch_contract(const ContractArgs &a, int *status, void *stream, std::string *msg) {
+    (void)msg;
+    return launch_contract_simt(a, status, stream);
+}
+
+}  // namespace shmm

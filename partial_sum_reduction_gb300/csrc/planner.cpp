@@ -38,7 +38,7 @@ bool injected(const char *fn) {
     return list.find(std::string(",") + fn + ",") != std::string::npos;
 }
 
-int64_t elem_bytes(shmm_dtype_t t) { return t == SHMM_F32 ? 4 : 2; }
+int64_t elem_bytes(shmm_dtype_t t) { return t == SHMM_F32 ? 4 : t == SHMM_E4M3 ? 1 : 2; }
 
 static std::atomic<uint64_t> g_launches{0};
 void count_launch(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
@@ -173,8 +173,8 @@ shmm_status_t shmm_plan(const shmm_mesh_t *mesh, const shmm_spec_t *spec_A,
     *plan_out = nullptr;
     if (mesh->naxes < 0 || mesh->naxes > SHMM_MAX_AXES)
         return fail(SHMM_ERR_SHAPE, "shmm_plan: mesh axis count out of range");
-    if (in_dtype != SHMM_F32 && in_dtype != SHMM_BF16)
-        return fail(SHMM_ERR_DTYPE, "shmm_plan: input dtype must be F32 or BF16");
+    if (in_dtype != SHMM_F32 && in_dtype != SHMM_BF16 && in_dtype != SHMM_E4M3)
+        return fail(SHMM_ERR_DTYPE, "shmm_plan: input dtype must be F32, BF16 or E4M3");
     if (out_dtype != SHMM_F32 && out_dtype != SHMM_BF16)
         return fail(SHMM_ERR_DTYPE, "shmm_plan: output dtype must be F32 or BF16");
     if (I < 0 || J < 0 || K < 0)

@@ -224,6 +224,76 @@ int launch_adapters_forward(const AdapterArgs &a, const BlockGrid &A, const Rank
 int launch_adapters_backward(const AdapterArgs &a, const BlockGrid &dC, const BlockGrid &A, const RankBoxes &dA,
                              shmm_dtype_t in_dt, shmm_dtype_t out_dt, int *status, void *stream);
 
+// ---- 8-bit blocks and the products of the gated MLP block ----------------
+
+// A global array held as a b0 x b1 grid of equal blocks, read in place: block
+// p (row-major grid) at at[p], rows `ld` elements apart.  8-bit blocks have a
+// scale for each 128 columns of a row (scale_rows = 1) or each 128 x 128
+// values (128), counted from the block's corner: scale[p], rows scale_ld apart.
+struct GridOperand {
+    int b0 = 1, b1 = 1;
+    int64_t brows = 0, bcols = 0, ld = 0;
+    shmm_dtype_t dt = SHMM_BF16;
+    std::vector<const void *> at;
+    std::vector<const float *> scale;
+    int scale_rows = 1;
+    int64_t scale_ld = 0;
+};
+
+// A global array written to every rank that holds a block of it: holders[p]
+// are the buffers of block p, each dense.  Scales (8-bit results) likewise.
+struct GridResult {
+    int b0 = 1, b1 = 1;
+    int64_t brows = 0, bcols = 0;
+    shmm_dtype_t dt = SHMM_BF16;
+    std::vector<std::vector<void *>> holders;
+    std::vector<std::vector<float *>> scale_holders;
+    int64_t scale_ld = 0;
+};
+
+// A contraction over global arrays.  X is [M, Kd] ([Kd, M] with x_t), Y is
+// [Kd, N] ([N, Kd] with y_t):
+//   plain:  D[0] = sum over the terms t of X[t] . Y[t]
+//   two:    D[0] = X[0] . Y[0], D[1] = X[0] . Y[1]
+//   gated:  G = X[0] . Y[0], U = X[0] . Y[1], D[0] = act(G) * U;
+//           kept[0] = G, kept[1] = U where `keep`
+struct ContractArgs {
+    int64_t M = 0, N = 0, Kd = 0;
+    int terms = 1;
+    bool x_t = false, y_t = false, two = false, gated = false, keep = false;
+    int act = SHMM_SILU;
+    bool tensor_core = true;  // may run on the tensor cores
+    int max_sms = 0;
+    GridOperand X[2], Y[2];
+    GridResult D[2], kept[2];
+};
+// Sizes below which the launches' grids hold: M below 2^31, N below 2^22.
+int launch_contract(const ContractArgs &a, int *status, void *stream, std::string *msg);
+int launch_contract_simt(const ContractArgs &a, int *status, void *stream);
+
+// Every block of src in 8 bits: its values into the [rows, cols] array `codes`
+// (row pitch ld), its scales into `scale`, scale_ld apart by row blocks; block
+// (i, j) of the grid starts at row i * brows, column j * bcols and scale
+// column j * ceil(bcols / 128).  src.scale_rows says which blocks.
+int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scale, int64_t scale_ld, int *status,
+                    void *stream);
+// The way back, into a [rows, cols] array of dtype dt (row pitch ld).
+int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream);
+
+// Gradient of act(G) * U by its elements, for the gradient dH of the product:
+//   dG = dH * U * act'(G), dU = dH * act(G), rounded to dt, into [rows, cols]
+//   arrays; H (NULL holders: not wanted) = act(G) * U to every holder.
+struct GatedSlopeArgs {
+    int act = SHMM_SILU;
+    int64_t rows = 0, cols = 0;
+    GridOperand dH, G, U;  // one grid
+    void *dG = nullptr, *dU = nullptr;
+    shmm_dtype_t dt = SHMM_BF16;
+    bool want_H = false;
+    GridResult H;
+};
+int launch_gated_slopes(const GatedSlopeArgs &a, int *status, void *stream);
+
 // Copies rectangles between row-major buffers: rectangle i moves h[i] rows of
 // w[i] elements of `elem` bytes from src[i] (row pitch src_ld[i] elements) to
 // dst[i] (pitch dst_ld[i]).  The reshard (all-to-all) collective.

@@ -7,9 +7,8 @@ from typing import List, Optional
 
 import torch
 
-from .shmm import F32, TENSOR_P, Plan, shmm_layernorm_backward_workspace_size
-
-TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+from .shmm import (F32, SCALE_BLOCK, TENSOR_A, TENSOR_B, TENSOR_C, TENSOR_P, TORCH_DTYPES, GatedSaved, Plan, scale_shape,
+                   shmm_layernorm_backward_workspace_size, shmm_quantize)
 
 
 def tensor_dtype(plan: Plan, tensor: int) -> torch.dtype:
@@ -67,4 +66,43 @@ def layernorm_workspace(rows: int, cols: int, device="cuda") -> Optional[torch.T
 def adapters_workspace(plan: Plan, n_adapters: int, rank: int, device="cuda") -> Optional[torch.Tensor]:
     """Workspace of plan.adapters_backward for adapters of the given rank."""
     n = plan.adapters_workspace_size(n_adapters, rank)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def quantize(x: torch.Tensor, block_rows: int = 1):
+    """(codes, scales) of a 2-D CUDA tensor in 8 bits (shmm_quantize)."""
+    codes = torch.empty(x.shape, dtype=TORCH_DTYPES["e4m3"], device=x.device)
+    scales = torch.empty(scale_shape(x.shape[0], x.shape[1], block_rows), dtype=torch.float32, device=x.device)
+    shmm_quantize(x, codes, scales, block_rows)
+    return codes, scales
+
+
+def shard_scaled(plan: Plan, tensor: int, full: torch.Tensor):
+    """Each rank's box of operand A or B of an "e4m3" plan, quantised on its
+    own: (codes per rank, scales per rank)."""
+    block_rows = {TENSOR_A: 1, TENSOR_B: SCALE_BLOCK}[tensor]
+    pairs = [quantize(t, block_rows) for t in shard(plan, tensor, full)]
+    return [c for c, _ in pairs], [s for _, s in pairs]
+
+
+def scaled_workspace(plan: Plan, device="cuda") -> Optional[torch.Tensor]:
+    """Workspace of plan.scaled_backward."""
+    n = plan.scaled_workspace_size()
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def gated_saved(plan: Plan, dtype: Optional[str] = None, device="cuda") -> GatedSaved:
+    """Buffers for what plan.gated_forward keeps: dtype "e4m3" (8 bits), or the
+    plan's own type."""
+    dtype = dtype or plan.in_dtype
+    gate, up = (alloc(plan, TENSOR_C, device, TORCH_DTYPES[dtype]) for _ in range(2))
+    if dtype != "e4m3":
+        return GatedSaved(dtype, gate, up)
+    gs, us = ([torch.empty(scale_shape(*t.shape), dtype=torch.float32, device=device) for t in ts] for ts in (gate, up))
+    return GatedSaved(dtype, gate, up, gs, us)
+
+
+def gated_workspace(plan: Plan, device="cuda") -> Optional[torch.Tensor]:
+    """Workspace of plan.gated_backward."""
+    n = plan.gated_workspace_size()
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None

@@ -33,14 +33,17 @@ MAX_RANKS = 256
 # status codes
 OK, ERR_INVALID_SPEC, ERR_ILLEGAL_OUTPUT, ERR_SHAPE, ERR_DTYPE, ERR_NULL, ERR_ALIGN, ERR_CUDA, \
     ERR_TIMEOUT, ERR_NOMEM, ERR_UNSUPPORTED, ERR_INJECTED, ERR_BOUNDS = range(13)
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
+SCALE_BLOCK = 128
+SILU, GELU_TANH = 0, 1
 FLAG_FUSED, FLAG_GELU, FLAG_TREE, FLAG_PARTIAL_OUT_DTYPE, FLAG_SIMT = 0x1, 0x2, 0x4, 0x8, 0x10
 FLAG_RANK_ORDER = 0x20
 TENSOR_A, TENSOR_B, TENSOR_C, TENSOR_P, TENSOR_A_LOCAL, TENSOR_B_LOCAL, TENSOR_C_REDUCED = range(7)
 COLL_NONE, COLL_REDUCE_SCATTER, COLL_ALL_REDUCE = range(3)
 COLLECTIVE_NAMES = {COLL_NONE: "none", COLL_REDUCE_SCATTER: "reduce_scatter",
                     COLL_ALL_REDUCE: "all_reduce"}
-DTYPE_CODES = {"f32": F32, "bf16": BF16}
+DTYPE_CODES = {"f32": F32, "bf16": BF16, "e4m3": E4M3}
+ACTIVATIONS = {"silu": SILU, "gelu": GELU_TANH}
 
 
 class shmm_mesh_t(ctypes.Structure):
@@ -76,6 +79,11 @@ class shmm_operand_choice_t(ctypes.Structure):
                 ("t_gather", ctypes.c_double), ("t_reduce", ctypes.c_double)]
 
 
+class shmm_gated_saved_t(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("gate_scale", ctypes.c_void_p), ("up_scale", ctypes.c_void_p)]
+
+
 class ShmmError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__("%s: %s" % (_status_name(status), message))
@@ -90,7 +98,10 @@ EXPORTS = ["shmm_plan", "shmm_plan_destroy", "shmm_plan_query", "shmm_plan_rank_
            "shmm_layernorm_all_gather", "shmm_run_host", "shmm_bounds_checked", "shmm_run_batch",
            "shmm_layernorm_forward", "shmm_layernorm_backward_workspace_size", "shmm_layernorm_backward",
            "shmm_layernorm_all_gather_forward", "shmm_layernorm_all_gather_backward",
-           "shmm_adapters_forward", "shmm_adapters_workspace_size", "shmm_adapters_backward"]
+           "shmm_adapters_forward", "shmm_adapters_workspace_size", "shmm_adapters_backward",
+           "shmm_quantize", "shmm_dequantize", "shmm_run_scaled", "shmm_scaled_backward_workspace_size",
+           "shmm_scaled_backward", "shmm_gated_forward", "shmm_gated_backward_workspace_size",
+           "shmm_gated_backward"]
 
 _lib = None
 
@@ -144,6 +155,15 @@ def lib():
         L.shmm_adapters_workspace_size.argtypes = [P, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
         L.shmm_adapters_backward.argtypes = [P, ctypes.c_int, ctypes.c_int, P, P, P, P, P, P, P, P, P, P, P, P,
                                              ctypes.c_size_t, P]
+        L.shmm_quantize.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, P, P, P, P]
+        L.shmm_dequantize.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, P, P, P, P]
+        L.shmm_run_scaled.argtypes = [P, P, P, P, P, P, P]
+        L.shmm_scaled_backward_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        L.shmm_scaled_backward.argtypes = [P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.shmm_gated_forward.argtypes = [P, ctypes.c_int, P, P, P, P, ctypes.POINTER(shmm_gated_saved_t), P]
+        L.shmm_gated_backward_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        L.shmm_gated_backward.argtypes = [P, ctypes.c_int, P, P, P, P, ctypes.POINTER(shmm_gated_saved_t), P, P, P, P, P,
+                                          ctypes.c_size_t, P]
         L.shmm_reshard.argtypes = [ctypes.POINTER(shmm_mesh_t), ctypes.POINTER(shmm_spec_t),
                                    ctypes.POINTER(shmm_spec_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                    PP, PP, P]
@@ -282,7 +302,7 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
-TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
 
 
 def _refuse(t, what: str, shape, dtype):
@@ -359,6 +379,26 @@ def _workspace(ws, dev: int):
     if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a dense CUDA tensor of the current device")
     return ws.data_ptr(), ws.nbytes
+
+
+def scale_shape(rows: int, cols: int, block_rows: int = 1) -> Tuple[int, int]:
+    """Shape of the scales of a [rows, cols] array in 8 bits."""
+    return (-(-rows // block_rows), -(-cols // SCALE_BLOCK))
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError("activation %r, expected one of %s" % (name, sorted(ACTIVATIONS)))
+    return ACTIVATIONS[name]
+
+
+class GatedSaved:
+    """What gated_forward keeps for gated_backward: per-rank lists of the two
+    projections' values before the activation, in the plan's type or (dtype
+    "e4m3") in 8 bits with a scale for each 128 columns of a row."""
+
+    def __init__(self, dtype: str, gate, up, gate_scale=None, up_scale=None):
+        self.dtype, self.gate, self.up, self.gate_scale, self.up_scale = dtype, gate, up, gate_scale, up_scale
 
 
 class Plan:
@@ -548,6 +588,107 @@ class Plan:
             _tensor(ddown, "ddown", (n, rank, J), f32, dev), _tensor(dup, "dup", (n, rank, K), f32, dev), ws, ws_bytes,
             _stream_handle(stream)))
 
+    def _scale_shapes(self, tensor: int, block_rows: int = 1):
+        """Per-rank shapes of the scales of `tensor`'s boxes in 8 bits (kept)."""
+        key = (tensor, block_rows)
+        got = self._box_shapes.get(key)
+        if got is None:
+            got = self._box_shapes[key] = [scale_shape(e[0], e[1], block_rows) for e in self._shapes(tensor)]
+        return got
+
+    def _scaled(self, A_r, A_scale_r, B_r, B_scale_r, dev):
+        f32, e4m3 = torch.float32, TORCH_DTYPES[self.in_dtype]
+        return (_tensors(A_r, "A", self._shapes(TENSOR_A), e4m3, dev),
+                _tensors(A_scale_r, "A_scale", self._scale_shapes(TENSOR_A), f32, dev),
+                _tensors(B_r, "B", self._shapes(TENSOR_B), e4m3, dev),
+                _tensors(B_scale_r, "B_scale", self._scale_shapes(TENSOR_B, SCALE_BLOCK), f32, dev))
+
+    def run_scaled(self, A_r, A_scale_r, B_r, B_scale_r, C_r, stream=None):
+        """The sharded matmul of 8-bit operands (a plan of in_dtype "e4m3"):
+        A with a scale for each 128 columns of a row, B one for each 128 x
+        128 values, every rank's box quantised on its own (see
+        include/shmm.h)."""
+        dev = _device()
+        ops = self._scaled(A_r, A_scale_r, B_r, B_scale_r, dev)
+        C = _tensors(C_r, "C", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev)
+        _check(lib().shmm_run_scaled(self._h, *map(_at, ops), _at(C), _stream_handle(stream)))
+
+    def scaled_workspace_size(self) -> int:
+        n = ctypes.c_size_t()
+        _check(lib().shmm_scaled_backward_workspace_size(self._h, ctypes.byref(n)))
+        return n.value
+
+    def scaled_backward(self, dC_r, A_r, A_scale_r, B_r, B_scale_r, dA_r, dB_r, workspace, stream=None):
+        """Gradient of run_scaled: dA = Q(dC) . B^T with dC in 8 bits too,
+        dB = A^T . dC from the 8-bit A that was kept (see include/shmm.h);
+        dA_r or dB_r may be None.  workspace: helpers.scaled_workspace."""
+        dev, bf16 = _device(), torch.bfloat16
+        ops = self._scaled(A_r, A_scale_r, B_r, B_scale_r, dev)
+        ws, ws_bytes = _workspace(workspace, dev)
+        dC = _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev)
+        dA = None if dA_r is None else _tensors(dA_r, "dA", self._shapes(TENSOR_A), bf16, dev)
+        dB = None if dB_r is None else _tensors(dB_r, "dB", self._shapes(TENSOR_B), bf16, dev)
+        _check(lib().shmm_scaled_backward(self._h, _at(dC), *map(_at, ops), _at(dA), _at(dB), ws, ws_bytes,
+                                          _stream_handle(stream)))
+
+    def _saved(self, saved, dev):
+        """(structure, what it points to) of a GatedSaved, checked."""
+        if saved is None:
+            return None, None
+        box, f32 = self._shapes(TENSOR_C), torch.float32
+        if saved.dtype not in TORCH_DTYPES:
+            raise ValueError("saved.dtype is %r, expected one of %s" % (saved.dtype, sorted(TORCH_DTYPES)))
+        dt = TORCH_DTYPES[saved.dtype]
+        keep = [_tensors(saved.gate, "saved.gate", box, dt, dev), _tensors(saved.up, "saved.up", box, dt, dev)]
+        if saved.dtype == "e4m3":
+            if saved.gate_scale is None or saved.up_scale is None:
+                raise ValueError("saved values in 8 bits need gate_scale and up_scale")
+            scales = self._scale_shapes(TENSOR_C)
+            keep += [_tensors(saved.gate_scale, "saved.gate_scale", scales, f32, dev),
+                     _tensors(saved.up_scale, "saved.up_scale", scales, f32, dev)]
+        return shmm_gated_saved_t(DTYPE_CODES[saved.dtype], *[_at(k) for k in keep]), keep
+
+    def _gated(self, A_r, gate_r, up_r, dev):
+        dt, box = TORCH_DTYPES[self.in_dtype], self._shapes(TENSOR_B)
+        return (_tensors(A_r, "A", self._shapes(TENSOR_A), dt, dev), _tensors(gate_r, "gate", box, dt, dev),
+                _tensors(up_r, "up", box, dt, dev))
+
+    def gated_forward(self, A_r, gate_r, up_r, C_r, activation: str = "silu", saved: "Optional[GatedSaved]" = None,
+                      stream=None):
+        """The gated first half of an MLP block, C = act(A . gate) * (A .
+        up), in one pass; `saved` (helpers.gated_saved) receives both
+        projections for gated_backward (see include/shmm.h).  activation:
+        "silu" or "gelu" (tanh form)."""
+        dev = _device()
+        ops = self._gated(A_r, gate_r, up_r, dev)
+        C = _tensors(C_r, "C", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev)
+        st, keep = self._saved(saved, dev)
+        _check(lib().shmm_gated_forward(self._h, _activation(activation), *map(_at, ops), _at(C),
+                                        None if st is None else ctypes.byref(st), _stream_handle(stream)))
+
+    def gated_workspace_size(self) -> int:
+        n = ctypes.c_size_t()
+        _check(lib().shmm_gated_backward_workspace_size(self._h, ctypes.byref(n)))
+        return n.value
+
+    def gated_backward(self, dC_r, A_r, gate_r, up_r, saved, dA_r, dgate_r, dup_r, workspace, activation: str = "silu",
+                       C_r=None, stream=None):
+        """Gradient of gated_forward from what it saved: dA, dgate, dup, and C
+        again where C_r is given (see include/shmm.h).  dA_r, or dgate_r and
+        dup_r, may be None.  workspace: helpers.gated_workspace."""
+        dev = _device()
+        dt, B = TORCH_DTYPES[self.in_dtype], self._shapes(TENSOR_B)
+        ops = self._gated(A_r, gate_r, up_r, dev)
+        st, keep = self._saved(saved, dev)
+        ws, ws_bytes = _workspace(workspace, dev)
+        dC = _tensors(dC_r, "dC", self._shapes(TENSOR_C), TORCH_DTYPES[self.out_dtype], dev)
+        outs = [None if t is None else _tensors(t, what, box, dt, dev)
+                for t, what, box in ((dA_r, "dA", self._shapes(TENSOR_A)), (dgate_r, "dgate", B), (dup_r, "dup", B),
+                                     (C_r, "C", self._shapes(TENSOR_C)))]
+        _check(lib().shmm_gated_backward(self._h, _activation(activation), _at(dC), *map(_at, ops),
+                                         None if st is None else ctypes.byref(st), *map(_at, outs), ws, ws_bytes,
+                                         _stream_handle(stream)))
+
     def run_host(self, A_host, B_host, C_host, A_r, B_r, C_r, workspace=None, stream=None):
         """shmm_run_host: global A [I,J], B [J,K] (CPU tensors, pinned for
         overlap, or None when A_r / B_r already hold the shards) in, global C
@@ -692,6 +833,32 @@ def shmm_layernorm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, workspa
         None if residual_grad is None else _tensor(residual_grad, "residual_grad", shape, dt, dev),
         _tensor(dx, "dx", shape, dt, dev), _tensor(dgamma, "dgamma", (cols,), f32, dev),
         _tensor(dbeta, "dbeta", (cols,), f32, dev), ws, ws_bytes, _stream_handle(stream)))
+
+
+def shmm_quantize(x, codes, scales, block_rows: int = 1, stream=None):
+    """x [rows, cols] in 8 bits: codes (float8_e4m3fn) and fp32 scales, one for
+    each 128 columns of a row (block_rows=1) or 128 x 128 values (128); see
+    include/shmm.h.  scale_shape gives the scales' shape."""
+    rows, cols, dt, code = _rows_dtype(x)
+    dev = _device()
+    if block_rows not in (1, SCALE_BLOCK):
+        raise ValueError("block_rows must be 1 or %d" % SCALE_BLOCK)
+    _check(lib().shmm_quantize(
+        rows, cols, code, block_rows, _tensor(x, "x", (rows, cols), dt, dev),
+        _tensor(codes, "codes", (rows, cols), TORCH_DTYPES["e4m3"], dev),
+        _tensor(scales, "scales", scale_shape(rows, cols, block_rows), torch.float32, dev), _stream_handle(stream)))
+
+
+def shmm_dequantize(codes, scales, y, block_rows: int = 1, stream=None):
+    """The way back: y (fp32 or bf16) = codes * scales."""
+    rows, cols, dt, code = _rows_dtype(y, "y")
+    dev = _device()
+    if block_rows not in (1, SCALE_BLOCK):
+        raise ValueError("block_rows must be 1 or %d" % SCALE_BLOCK)
+    _check(lib().shmm_dequantize(
+        rows, cols, code, block_rows, _tensor(codes, "codes", (rows, cols), TORCH_DTYPES["e4m3"], dev),
+        _tensor(scales, "scales", scale_shape(rows, cols, block_rows), torch.float32, dev),
+        _tensor(y, "y", (rows, cols), dt, dev), _stream_handle(stream)))
 
 
 def shmm_reshard(mesh, spec_from, spec_to, rows: int, cols: int, dtype: str, src_r, dst_r, stream=None):
