@@ -1,0 +1,170 @@
+// Which kernel takes a contraction of the gated MLP block or of 8-bit operands,
+// and the tensor-core kernels' tables.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+#include <string>
+#include <vector>
+
+#include "contract_tc.cuh"
+#include "shmm_internal.h"
+#include "tensor_map.h"
+
+namespace {
+
+using namespace shmm_tcn;
+using shmm::ContractArgs;
+using shmm::GridOperand;
+using shmm::GridResult;
+
+bool on16(int64_t n, shmm_dtype_t dt) { return n * shmm::elem_bytes(dt) % 16 == 0; }
+
+// Tiles cross no block's edge: where a dim is split, blocks are whole tiles of
+// 128; rows are whole 16-byte pieces for TMA.
+bool edges_fit(int b0, int b1, int64_t brows, int64_t bcols) {
+    return (b0 == 1 || brows % 128 == 0) && (b1 == 1 || bcols % 128 == 0);
+}
+bool operand_fits(const GridOperand &o) {
+    if (o.at.size() > (size_t)kSlots || !edges_fit(o.b0, o.b1, o.brows, o.bcols) || !on16(o.ld, o.dt)) return false;
+    for (const void *p : o.at)
+        if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+    return true;
+}
+size_t holders_of(const GridResult &d) {
+    size_t n = 0;
+    for (const auto &b : d.holders) n += b.size();
+    return n;
+}
+bool result_fits(const GridResult &d) {
+    return d.holders.size() <= (size_t)kSlots && holders_of(d) <= (size_t)kSlots &&
+           edges_fit(d.b0, d.b1, d.brows, d.bcols) && on16(d.bcols, d.dt);
+}
+
+// The tensor-core form of a contraction, or -1.
+int form_of(const ContractArgs &a) {
+    if (!a.tensor_core || a.M <= 0 || a.N <= 0 || a.Kd <= 0) return -1;
+    if (a.M > (int64_t)1 << 30 || a.Kd > (int64_t)1 << 30) return -1;  // coordinates are 32-bit
+    const int ny = a.gated || a.two || a.terms == 2 ? 2 : 1, nx = a.terms;
+    for (int i = 0; i < nx; ++i)
+        if (!operand_fits(a.X[i])) return -1;
+    for (int i = 0; i < ny; ++i)
+        if (!operand_fits(a.Y[i])) return -1;
+    for (int i = 0; i < (a.two ? 2 : 1); ++i)
+        if (!result_fits(a.D[i])) return -1;
+    for (int i = 0; a.keep && i < 2; ++i)
+        if (!result_fits(a.kept[i])) return -1;
+    const shmm_dtype_t in = a.X[0].dt;
+    if (in == SHMM_BF16 && a.D[0].dt == SHMM_BF16) {
+        if (a.gated) return kGated;
+        if (!a.x_t && a.y_t) return kNT;
+        if (a.x_t && !a.y_t) return kTN;
+    }
+    if (in == SHMM_E4M3 && !a.x_t && a.terms == 1) return a.y_t ? kNT8 : kNN8;
+    return -1;
+}
+
+struct Maps {
+    ContractK *k;
+    shmm::EncodeTiledFn fn;
+    int n = 0;
+    bool ok = true;
+    void add(const void *base, int64_t rows, int64_t cols, int64_t ld, shmm_dtype_t dt, uint32_t bx, uint32_t by,
+             CUtensorMapSwizzle sw) {
+        if (n >= kMaps) ok = false;
+        if (!ok) return;
+        const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)(ld * shmm::elem_bytes(dt))};
+        const cuuint32_t box[2] = {bx, by}, estr[2] = {1, 1};
+        const CUtensorMapDataType type = dt == SHMM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : dt == SHMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        ok = fn(&k->maps[n++], type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    // mn: the contracted dim runs along the rows.
+    void operand(OpK *o, const GridOperand &g, bool mn) {
+        *o = {n, g.b0, g.b1, g.brows, g.bcols};
+        const uint32_t row = 128 / (uint32_t)shmm::elem_bytes(g.dt);  // values of a 128-byte swizzled row
+        for (const void *p : g.at)
+            add(p, g.brows, g.bcols, g.ld, g.dt, row, mn ? row : 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    // Result boxes: 32 x 32 (fp32: 128-byte rows, bf16: 64), bytes 32 x 64.
+    int holders(const GridResult &d) {
+        const int at = n;
+        const bool e8 = d.dt == SHMM_E4M3;
+        for (const auto &b : d.holders)
+            for (void *p : b)
+                add(p, d.brows, d.bcols, d.bcols, d.dt, e8 ? 64 : 32, 32,
+                    d.dt == SHMM_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+        return at;
+    }
+    void result(ResK *o, const GridResult &d) {
+        o->b0 = d.b0;
+        o->b1 = d.b1;
+        o->brows = d.brows;
+        o->bcols = d.bcols;
+        int h = 0;
+        for (size_t p = 0; p < d.holders.size(); ++p) {
+            o->first[p] = (uint8_t)h;
+            h += (int)d.holders[p].size();
+        }
+        o->first[d.holders.size()] = (uint8_t)h;
+        o->map0 = holders(d);
+    }
+};
+
+void set_scales(ScalesK *t, const GridOperand &g) {
+    for (size_t i = 0; i < g.scale.size(); ++i) t->at[i] = g.scale[i];
+    t->ld = g.scale_ld;
+    t->n = (g.brows + g.scale_rows - 1) / g.scale_rows * g.scale_ld;
+}
+
+}  // namespace
+
+namespace shmm {
+
+int launch_contract(const ContractArgs &a, int *status, void *stream, std::string *msg) {
+    const int form = form_of(a);
+    if (form < 0) return launch_contract_simt(a, status, stream);
+    const EncodeTiledFn fn = encode_fn(msg);
+    if (!fn) return (int)cudaErrorNotSupported;
+    static_assert(sizeof(ContractK) <= 32764, "kernel parameters");
+    ContractK k;
+    memset(&k, 0, sizeof k);
+    Maps m = {&k, fn};
+    const bool x_mn = form == kTN, y_mn = form == kGated || form == kTN || form == kNN8;
+    for (int i = 0; i < a.terms; ++i) m.operand(&k.X[i], a.X[i], x_mn);
+    for (int i = 0; i < (a.gated || a.two ? 2 : a.terms); ++i) m.operand(&k.Y[i], a.Y[i], y_mn);
+    for (int i = 0; i < (a.two ? 2 : 1); ++i) m.result(&k.D[i], a.D[i]);
+    if (a.keep) {
+        k.keep = a.kept[0].dt == SHMM_E4M3 ? 2 : 1;
+        k.kept_ld = a.kept[0].scale_ld;
+        for (int y = 0; y < 2; ++y) {
+            k.kept_map[y] = m.holders(a.kept[y]);
+            int h = 0;
+            for (const auto &b : a.kept[y].scale_holders)
+                for (float *p : b) k.kept_scale[y][h++] = p;
+        }
+    }
+    if (!m.ok) {
+        *msg = "cuTensorMapEncodeTiled rejected an operand or a result";
+        return (int)cudaErrorInvalidValue;
+    }
+    if (form == kNN8 || form == kNT8) {
+        set_scales(&k.x_scale, a.X[0]);
+        set_scales(&k.y_scale, a.Y[0]);
+    }
+    k.M = a.M;
+    k.N = a.N;
+    k.Kd = a.Kd;
+    k.terms = a.terms;
+    k.two = a.two;
+    k.act = a.act;
+    k.out_f32 = a.D[0].dt == SHMM_F32;
+    k.status = status;
+    return launch_pair(k, form, a.max_sms, (cudaStream_t)stream);
+}
+
+}  // namespace shmm

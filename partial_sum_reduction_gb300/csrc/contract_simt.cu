@@ -334,9 +334,4 @@ int launch_contract_simt(const ContractArgs &a, int *status, void *stream) {
     return 0;
 }
 
-int launch_contract(const ContractArgs &a, int *status, void *stream, std::string *msg) {
-    (void)msg;
-    return launch_contract_simt(a, status, stream);
-}
-
 }  // namespace shmm

@@ -81,7 +81,8 @@ def shard_scaled(plan: Plan, tensor: int, full: torch.Tensor):
     """Each rank's box of operand A or B of an "e4m3" plan, quantised on its
     own: (codes per rank, scales per rank)."""
     block_rows = {TENSOR_A: 1, TENSOR_B: SCALE_BLOCK}[tensor]
-    pairs = [quantize(t, block_rows) for t in shard(plan, tensor, full)]
+    # a row slice of a contiguous array is a view, which may start off a 16-byte boundary
+    pairs = [quantize(t.clone() if t.data_ptr() % 16 else t, block_rows) for t in shard(plan, tensor, full)]
     return [c for c, _ in pairs], [s for _, s in pairs]
 
 

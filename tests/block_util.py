@@ -69,9 +69,11 @@ def gate_act(name, x):
     if name == "silu":
         s = torch.sigmoid(x)
         return x * s, s + x * s * (1 - s)
-    c = math.sqrt(2 / math.pi)
-    t = torch.tanh(c * (x + 0.044715 * x ** 3))
-    return 0.5 * x * (1 + t), 0.5 * (1 + t) + 0.5 * x * (1 - t * t) * c * (1 + 3 * 0.044715 * x * x)
+    # (1 + tanh v) / 2 is the logistic function of 2 v, which does not cancel where v is far below zero
+    c = 2 * math.sqrt(2 / math.pi)
+    p = torch.sigmoid(c * (x + 0.044715 * x ** 3))
+    q = torch.sigmoid(-c * (x + 0.044715 * x ** 3))
+    return x * p, p + x * p * q * c * (1 + 3 * 0.044715 * x * x)
 
 
 def box(plan, tensor, rank, full):
