@@ -63,8 +63,18 @@ using namespace shmm_pair;
 using namespace shmm_tcn;
 
 constexpr int kStagingBytes = 32 * 1024;  // epilogue boxes, 4 KB per warp
+// Warps 0-3: TMA, MMA, and two that fetch the scales of the 8-bit forms; warps
+// 4-11: the epilogue.
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+// 8-bit forms: registers that the first warpgroup hands to the other two, whose
+// threads hold 128 sums each.  A launch gives every thread 168 (65536 / 384,
+// rounded down to a multiple of 8): 128 * 72 + 256 * 216 = 384 * 168.
+constexpr int kFewRegs = 72, kManyRegs = 216;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "no more registers than the launch has");
+// 8-bit forms: k-blocks whose scales wait in shared memory (1 KB each: the
+// product of the row's and the 128 columns' scale, for both column halves).
+constexpr int kScaleSlots = 8;
 
 template <int FORM>
 struct Cfg {
@@ -75,8 +85,8 @@ struct Cfg {
     static constexpr int BK = F8 ? 128 : 64;   // values of a k-block: 128 bytes
     static constexpr int BOX = 16384;          // 128 rows or columns of a k-block
     static constexpr int STAGE = BOX * (1 + NH);
-    static constexpr int S = F8 ? 6 : 4;
-    static constexpr int SMEM = S * STAGE + kStagingBytes + 1024 /*align*/ + 1024 /*barriers*/;
+    static constexpr int S = F8 ? 5 : 4;
+    static constexpr int SMEM = S * STAGE + kStagingBytes + (F8 ? kScaleSlots * 1024 : 0) + 1024 /*align*/ + 1024 /*barriers*/;
 };
 
 // MMA of the pair: M = 256, N = 256, fp32 accumulator.
@@ -275,13 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *tiles = smem;
     uint8_t *staging = smem + S * C::STAGE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + kStagingBytes);
-    // bars: full[S], empty[S], acc_full[2], acc_empty[2], drain, hand-off
-    uint32_t *words = reinterpret_cast<uint32_t *>(bars + 2 * S + 6);
+    float *scales = reinterpret_cast<float *>(staging + kStagingBytes);  // [kScaleSlots][2][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + kStagingBytes + (C::F8 ? kScaleSlots * 1024 : 0));
+    // bars: full[S], empty[S], acc_full[2], acc_empty[2], drain, hand-off, scales_full[], scales_empty[]
+    uint32_t *words = reinterpret_cast<uint32_t *>(bars + 2 * S + 6 + 2 * kScaleSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
     volatile uint32_t *peer_issued = words + 2;  // the peer's load count, and its bytes of each of its last S stages
     volatile uint32_t *peer_bytes = words + 4;
-    static_assert(2 * 8 * 8 + 6 * 8 + (4 + 8) * 4 <= 1024, "barriers and words");
+    static_assert((2 * S + 6 + 2 * kScaleSlots) * 8 + (4 + S) * 4 <= 1024, "barriers and words");
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t cr = cluster_ctarank();  // 0: leader, 1: peer
@@ -292,6 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     auto accf_bar = [&](int s) { return smem_u32(&bars[2 * S + s]); };
     auto acce_bar = [&](int s) { return smem_u32(&bars[2 * S + 2 + s]); };
     const uint32_t drain_bar = smem_u32(&bars[2 * S + 4]), handoff_bar = smem_u32(&bars[2 * S + 5]);
+    auto scalesf_bar = [&](int s) { return smem_u32(&bars[2 * S + 6 + s]); };
+    auto scalese_bar = [&](int s) { return smem_u32(&bars[2 * S + 6 + kScaleSlots + s]); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -301,6 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
         for (int s = 0; s < 2; ++s) {
             mbar_init(accf_bar(s), 1);
             mbar_init(acce_bar(s), 2 * kEpiWarps);  // both CTAs' epilogue warps
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            mbar_init(scalesf_bar(s), 2);  // the two warps that fetch scales
+            mbar_init(scalese_bar(s), kEpiWarps);
         }
         mbar_init(drain_bar, 1);
         mbar_init(handoff_bar, 1);
@@ -323,157 +340,192 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     grid_dependency_wait();
     grid_launch_dependents();
 
-    if (warp == 0) {
-        // ---------------- TMA producer (both CTAs) ----------------
-        if (lane == 0) {
-            uint32_t it = 0;  // stages loaded
-            uint32_t stage_bytes[S];
+    if (warp < 4) {
+        if constexpr (C::F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            if (lane == 0) {
+                uint32_t it = 0;  // stages loaded
+                uint32_t stage_bytes[S];
+                bool ok = true;
+                for (int t = pair; t < k.total && ok; t += npairs) {
+                    int mt, nt, hh;
+                    item_coords(k, t, &mt, &nt, &hh);
+                    const int nh = hh >= 0 ? 1 : NH;
+                    const uint32_t bytes = (uint32_t)(C::BOX * (1 + nh));
+                    for (int term = 0; term < k.terms && ok; ++term) {
+                        Cursor x, y[NH];
+                        x.template start<!C::X_MN>(k.X[term], (int64_t)mt * 256 + (int)cr * 128);
+    #pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
+                            if (FORM == kGated) y[h].template start<!C::Y_MN>(k.Y[cr], hc);
+                            else y[h].template start<!C::Y_MN>(k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
+                        }
+                        for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
+                            const int s = it % S;
+                            if (!mbar_wait(empty_bar(s), ((it / S) & 1) ^ 1, abort_flag, k.status)) {
+                                ok = false;
+                                break;
+                            }
+                            if (cr == 0) mbar_expect_tx(full_bar(s), 2 * bytes);
+                            stage_bytes[s] = bytes;
+                            const uint32_t bar = mapa_shared(full_bar(s), 0);
+                            const uint32_t dst = smem_u32(tiles + s * C::STAGE);
+                            load_box<C::X_MN, C::F8>(k, x, dst, bar);
+                            x.advance(C::BK);
+    #pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                if (h < nh) load_box<C::Y_MN, C::F8>(k, y[h], dst + (uint32_t)(C::BOX * (1 + h)), bar);
+                                y[h].advance(C::BK);
+                            }
+                        }
+                    }
+                }
+                // Both CTAs' loads of a stage complete on the leader's barrier, so the
+                // leader waits for all of them; the peer hands over how many stages
+                // it loaded, and their bytes.  After an abort the counts may differ by
+                // up to S stages: the leader arms the peer's extra stages for the
+                // peer's half, and stands in for the half the peer never loaded.
+                if (cr == 1) {
+                    for (int s = 0; s < S; ++s)
+                        if ((uint32_t)s < it) st_cluster_u32(mapa_shared(smem_u32((const void *)(peer_bytes + s)), 0), stage_bytes[s]);
+                    st_cluster_u32(mapa_shared(smem_u32((const void *)peer_issued), 0), it);
+                    mbar_arrive_cluster(mapa_shared(handoff_bar, 0));
+                } else {
+                    uint32_t it_peer = it;
+                    if (mbar_wait_cluster(handoff_bar, 0, k.status)) it_peer = *peer_issued;
+                    const uint32_t it_max = it_peer > it ? it_peer : it;
+                    for (uint32_t i = it_peer < it ? it_peer : it; i < it_max; ++i) {
+                        const int s = (int)(i % S);
+                        if (i >= it) mbar_expect_tx(full_bar(s), peer_bytes[s]);  // the peer's half only
+                        else mbar_complete_tx(full_bar(s), stage_bytes[s]);       // the half never loaded
+                    }
+                    for (uint32_t i = it_max > (uint32_t)S ? it_max - S : 0; i < it_max; ++i)
+                        mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status, false);
+                }
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (leader CTA only) ----------------
+            if (lane == 0 && cr == 0) {
+                const int k_total = k.terms * k.k_blocks;
+                uint32_t it = 0;
+                uint32_t fills[2] = {0, 0};
+                bool ok = true;
+                // The four MMAs of the k-block in stage s, half h of its Y, into buffer buf.
+                auto issue = [&](int s, int buf, int h, bool first) {
+                    const uint32_t a = smem_u32(tiles + s * C::STAGE), b = a + (uint32_t)(C::BOX * (1 + h));
+    #pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        pair_mma<FORM>(tmem_base + (uint32_t)(buf * 256), operand_step<C::X_MN, C::F8>(a, kk),
+                                       operand_step<C::Y_MN, C::F8>(b, kk), !first || kk > 0);
+                };
+                auto wait_free = [&](int buf) -> bool {
+                    if (!mbar_wait(acce_bar(buf), (fills[buf] & 1) ^ 1, abort_flag, k.status)) return false;
+                    fence_after();
+                    return true;
+                };
+                auto wait_stage = [&](uint32_t i) -> bool {
+                    if (!mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status)) return false;
+                    fence_after();
+                    return true;
+                };
+                for (int t = pair; t < k.total && ok; t += npairs) {
+                    if (C::F8) {
+                        // every k-block is an accumulator of its own
+                        for (int kb = 0; kb < k_total; ++kb, ++it) {
+                            const int buf = it & 1;
+                            if (!wait_free(buf) || !wait_stage(it)) {
+                                ok = false;
+                                break;
+                            }
+                            issue(it % S, buf, 0, true);
+                            umma2_commit_both(empty_bar(it % S));
+                            umma2_commit_both(accf_bar(buf));
+                            ++fills[buf];
+                        }
+                        continue;
+                    }
+                    // Half 0 runs ahead over the first R loaded stages while the
+                    // epilogue still reads half 1 of the previous tile, then half 1
+                    // catches up on the same stages.
+                    const bool half = t >= k.half_from;
+                    const int R = k_total < S ? k_total : S;
+                    if (!wait_free(0)) break;
+                    for (int kb = 0; kb < R; ++kb) {
+                        if (!wait_stage(it + (uint32_t)kb)) {
+                            ok = false;
+                            break;
+                        }
+                        issue((int)((it + (uint32_t)kb) % S), 0, 0, kb == 0);
+                        if (half) umma2_commit_both(empty_bar((int)((it + (uint32_t)kb) % S)));
+                    }
+                    if (!ok) break;
+                    if (!half) {
+                        if (!wait_free(1)) break;
+                        for (int kb = 0; kb < R; ++kb) {
+                            const int s = (int)((it + (uint32_t)kb) % S);
+                            issue(s, 1, NH - 1, kb == 0);
+                            umma2_commit_both(empty_bar(s));
+                        }
+                    }
+                    it += (uint32_t)R;
+                    for (int kb = R; kb < k_total; ++kb, ++it) {
+                        if (!wait_stage(it)) {
+                            ok = false;
+                            break;
+                        }
+                        issue(it % S, 0, 0, false);
+                        if (!half) issue(it % S, 1, NH - 1, false);
+                        umma2_commit_both(empty_bar(it % S));
+                    }
+                    if (!ok) break;
+                    umma2_commit_both(accf_bar(0));
+                    ++fills[0];
+                    if (!half) {
+                        umma2_commit_both(accf_bar(1));
+                        ++fills[1];
+                    }
+                }
+                umma2_commit_both(drain_bar);
+                mbar_wait(drain_bar, 0, abort_flag, k.status, false);
+            }
+        } else if constexpr (C::F8) {
+            // ---------------- scales (both CTAs): thread i of 64 has rows i and i + 64 ----------------
+            const int i = threadIdx.x - 64;
+            uint32_t it = 0;
             bool ok = true;
             for (int t = pair; t < k.total && ok; t += npairs) {
                 int mt, nt, hh;
                 item_coords(k, t, &mt, &nt, &hh);
-                const int nh = hh >= 0 ? 1 : NH;
-                const uint32_t bytes = (uint32_t)(C::BOX * (1 + nh));
-                for (int term = 0; term < k.terms && ok; ++term) {
-                    Cursor x, y[NH];
-                    x.start<!C::X_MN>(k.X[term], (int64_t)mt * 256 + (int)cr * 128);
-#pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
-                        if (FORM == kGated) y[h].start<!C::Y_MN>(k.Y[cr], hc);
-                        else y[h].start<!C::Y_MN>(k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
-                    }
-                    for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
-                        const int s = it % S;
-                        if (!mbar_wait(empty_bar(s), ((it / S) & 1) ^ 1, abort_flag, k.status)) {
-                            ok = false;
-                            break;
-                        }
-                        if (cr == 0) mbar_expect_tx(full_bar(s), 2 * bytes);
-                        stage_bytes[s] = bytes;
-                        const uint32_t bar = mapa_shared(full_bar(s), 0);
-                        const uint32_t dst = smem_u32(tiles + s * C::STAGE);
-                        load_box<C::X_MN, C::F8>(k, x, dst, bar);
-                        x.advance(C::BK);
-#pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            if (h < nh) load_box<C::Y_MN, C::F8>(k, y[h], dst + (uint32_t)(C::BOX * (1 + h)), bar);
-                            y[h].advance(C::BK);
-                        }
-                    }
-                }
-            }
-            // Both CTAs' loads of a stage complete on the leader's barrier, so the
-            // leader waits for all of them; the peer hands over how many stages
-            // it loaded, and their bytes.  After an abort the counts may differ by
-            // up to S stages: the leader arms the peer's extra stages for the
-            // peer's half, and stands in for the half the peer never loaded.
-            if (cr == 1) {
-                for (int s = 0; s < S; ++s)
-                    if ((uint32_t)s < it) st_cluster_u32(mapa_shared(smem_u32((const void *)(peer_bytes + s)), 0), stage_bytes[s]);
-                st_cluster_u32(mapa_shared(smem_u32((const void *)peer_issued), 0), it);
-                mbar_arrive_cluster(mapa_shared(handoff_bar, 0));
-            } else {
-                uint32_t it_peer = it;
-                if (mbar_wait_cluster(handoff_bar, 0, k.status)) it_peer = *peer_issued;
-                const uint32_t it_max = it_peer > it ? it_peer : it;
-                for (uint32_t i = it_peer < it ? it_peer : it; i < it_max; ++i) {
-                    const int s = (int)(i % S);
-                    if (i >= it) mbar_expect_tx(full_bar(s), peer_bytes[s]);  // the peer's half only
-                    else mbar_complete_tx(full_bar(s), stage_bytes[s]);       // the half never loaded
-                }
-                for (uint32_t i = it_max > (uint32_t)S ? it_max - S : 0; i < it_max; ++i)
-                    mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status, false);
-            }
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (leader CTA only) ----------------
-        if (lane == 0 && cr == 0) {
-            const int k_total = k.terms * k.k_blocks;
-            uint32_t it = 0;
-            uint32_t fills[2] = {0, 0};
-            bool ok = true;
-            // The four MMAs of the k-block in stage s, half h of its Y, into buffer buf.
-            auto issue = [&](int s, int buf, int h, bool first) {
-                const uint32_t a = smem_u32(tiles + s * C::STAGE), b = a + (uint32_t)(C::BOX * (1 + h));
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    pair_mma<FORM>(tmem_base + (uint32_t)(buf * 256), operand_step<C::X_MN, C::F8>(a, kk),
-                                   operand_step<C::Y_MN, C::F8>(b, kk), !first || kk > 0);
-            };
-            auto wait_free = [&](int buf) -> bool {
-                if (!mbar_wait(acce_bar(buf), (fills[buf] & 1) ^ 1, abort_flag, k.status)) return false;
-                fence_after();
-                return true;
-            };
-            auto wait_stage = [&](uint32_t i) -> bool {
-                if (!mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status)) return false;
-                fence_after();
-                return true;
-            };
-            for (int t = pair; t < k.total && ok; t += npairs) {
-                if (C::F8) {
-                    // every k-block is an accumulator of its own
-                    for (int kb = 0; kb < k_total; ++kb, ++it) {
-                        const int buf = it & 1;
-                        if (!wait_free(buf) || !wait_stage(it)) {
-                            ok = false;
-                            break;
-                        }
-                        issue(it % S, buf, 0, true);
-                        umma2_commit_both(empty_bar(it % S));
-                        umma2_commit_both(accf_bar(buf));
-                        ++fills[buf];
-                    }
-                    continue;
-                }
-                // Half 0 runs ahead over the first R loaded stages while the
-                // epilogue still reads half 1 of the previous tile, then half 1
-                // catches up on the same stages.
-                const bool half = t >= k.half_from;
-                const int R = k_total < S ? k_total : S;
-                if (!wait_free(0)) break;
-                for (int kb = 0; kb < R; ++kb) {
-                    if (!wait_stage(it + (uint32_t)kb)) {
+                const int row = mt * 256 + (int)cr * 128 + i, col = nt * 256;
+                ScaleCursor x0, x1, y0, y1;
+                x0.template start<true>(k.X[0], k.x_scale, row, 1, row < k.M);
+                x1.template start<true>(k.X[0], k.x_scale, row + 64, 1, row + 64 < k.M);
+                y0.template start<!C::Y_MN>(k.Y[0], k.y_scale, col, 128, col < k.N);
+                y1.template start<!C::Y_MN>(k.Y[0], k.y_scale, col + 128, 128, col + 128 < k.N);
+                for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
+                    const int s = it % kScaleSlots;
+                    const float a = x0.next(k.status), b = x1.next(k.status), c = y0.next(k.status), d = y1.next(k.status);
+                    ok = mbar_wait(scalese_bar(s), ((it / kScaleSlots) & 1) ^ 1, abort_flag, k.status);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
-                    issue((int)((it + (uint32_t)kb) % S), 0, 0, kb == 0);
-                    if (half) umma2_commit_both(empty_bar((int)((it + (uint32_t)kb) % S)));
-                }
-                if (!ok) break;
-                if (!half) {
-                    if (!wait_free(1)) break;
-                    for (int kb = 0; kb < R; ++kb) {
-                        const int s = (int)((it + (uint32_t)kb) % S);
-                        issue(s, 1, NH - 1, kb == 0);
-                        umma2_commit_both(empty_bar(s));
-                    }
-                }
-                it += (uint32_t)R;
-                for (int kb = R; kb < k_total; ++kb, ++it) {
-                    if (!wait_stage(it)) {
-                        ok = false;
-                        break;
-                    }
-                    issue(it % S, 0, 0, false);
-                    if (!half) issue(it % S, 1, NH - 1, false);
-                    umma2_commit_both(empty_bar(it % S));
-                }
-                if (!ok) break;
-                umma2_commit_both(accf_bar(0));
-                ++fills[0];
-                if (!half) {
-                    umma2_commit_both(accf_bar(1));
-                    ++fills[1];
+                    float *to = scales + s * 256;
+                    to[i] = a * c;
+                    to[i + 64] = b * c;
+                    to[128 + i] = a * d;
+                    to[128 + i + 64] = b * d;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(scalesf_bar(s));  // releases the warp's stores, which the sync orders before it
                 }
             }
-            umma2_commit_both(drain_bar);
-            mbar_wait(drain_bar, 0, abort_flag, k.status, false);
         }
     } else {
-        // ---------------- epilogue (warps 2.., both CTAs) ----------------
-        const int ew = warp - 2, quad = warp % 4, set = ew / 4;
+        // ---------------- epilogue (both CTAs) ----------------
+        if constexpr (C::F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        const int ew = warp - 4, quad = warp % 4, set = ew / 4;
         const uint32_t lanes = tmem_base + ((uint32_t)(quad * 32) << 16);
         Stager st = {&k, smem_u32(staging) + (uint32_t)ew * 4096u, 0, lane};
         uint32_t used[2] = {0, 0};
@@ -509,34 +561,35 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                 }
             } else {
                 const int col0 = nt * 256 + set * 128;
-                ScaleCursor xs, ys;
-                xs.start<true>(k.X[0], k.x_scale, row0 + lane, 1, row0 + lane < k.M);
-                ys.start<!C::Y_MN>(k.Y[0], k.y_scale, col0, 128, col0 < k.N);
                 float acc[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-                float sx = xs.next(k.status), sy = ys.next(k.status);
                 for (int kb = 0; kb < k.k_blocks; ++kb, ++fill) {
-                    const int b = fill & 1;
-                    const float s = sx * sy;
-                    if (kb + 1 < k.k_blocks) {  // the next k-block's scales, while this one is waited for
-                        sx = xs.next(k.status);
-                        sy = ys.next(k.status);
-                    }
-                    if (!wait_full(b)) {
+                    const int b = fill & 1, s = fill % kScaleSlots;
+                    int got = 1;
+                    if (lane == 0)
+                        got = mbar_wait(scalesf_bar(s), (fill / kScaleSlots) & 1, abort_flag, k.status) &&
+                              mbar_wait(accf_bar(b), (fill >> 1) & 1, abort_flag, k.status);
+                    if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
                         ok = false;
                         break;
                     }
+                    fence_after();
                     const uint32_t at = lanes + (uint32_t)(b * 256 + set * 128);
-                    uint32_t r[2][16];
-                    tmem_ask16(at, r[0]);
+                    uint32_t r[2][32];
+                    tmem_ask32(at, r[0]);
+                    const float sc = reinterpret_cast<volatile float *>(scales)[s * 256 + set * 128 + quad * 32 + lane];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        tmem_got16(r[c & 1]);
-                        if (c < 7) tmem_ask16(at + (uint32_t)((c + 1) * 16), r[(c + 1) & 1]);
-                        else release(b);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_got32(r[c & 1]);
+                        if (c < 3) {
+                            tmem_ask32(at + (uint32_t)((c + 1) * 32), r[(c + 1) & 1]);
+                        } else {
+                            release(b);
+                            if (lane == 0) mbar_arrive(scalese_bar(s));
+                        }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[c * 16 + i] = fmaf(__uint_as_float(r[c & 1][i]), s, acc[c * 16 + i]);
+                        for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(r[c & 1][j]), sc, acc[c * 32 + j]);
                     }
                 }
                 if (!ok) break;
