@@ -28,10 +28,14 @@
 // 8-bit forms: a k-block is 128 values, the scales' block.  Its four MMAs (K =
 // 32) fill one of two 256 x 256 accumulators; the epilogue warps read it and
 // add it times the two scales to fp32 sums in their registers (128 per thread)
-// while the next k-block fills the other.  Per k-block and SM the tensor cores
-// take 512 cycles, the reads 256 of TMEM's 128 lanes x 4 bytes and the FMAs
-// 256.  No sum is longer than 128 products in the tensor cores' adders, whose
-// additions truncate.
+// while the next k-block fills the other.  No sum is longer than 128 products
+// in the tensor cores' adders, whose additions truncate.  Measured: 8192 x 8192
+// x 28672 in 1.84 ms, 2.09 PFLOP/s, 1.08 of the measured bf16 rate; 950 cycles
+// per k-block, where its MMAs take 512.  What bounds it is the way round one
+// accumulator, which two k-blocks share: MMAs, their commit and the signal (some
+// 1150 cycles from the first MMA), the epilogue's reads (570), the hand-back
+// (200).  TMEM has no room for a third; reading two or four pieces at a time,
+// packed FMAs and other splits of the reads changed nothing (1.84 to 1.87 ms).
 //
 // Every wait is bounded; on expiry the kernel records SHMM_ERR_TIMEOUT, drains
 // its own loads and MMAs, frees TMEM and returns.
@@ -63,8 +67,8 @@ using namespace shmm_pair;
 using namespace shmm_tcn;
 
 constexpr int kStagingBytes = 32 * 1024;  // epilogue boxes, 4 KB per warp
-// Warps 0-3: TMA, MMA, and two that fetch the scales of the 8-bit forms; warps
-// 4-11: the epilogue.
+// Warps 0-3: TMA, MMA, and for the 8-bit forms a second MMA issuer and one that
+// fetches the scales; warps 4-11: the epilogue.
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 // 8-bit forms: registers that the first warpgroup hands to the other two, whose
@@ -316,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
             mbar_init(acce_bar(s), 2 * kEpiWarps);  // both CTAs' epilogue warps
         }
         for (int s = 0; s < kScaleSlots; ++s) {
-            mbar_init(scalesf_bar(s), 2);  // the two warps that fetch scales
+            mbar_init(scalesf_bar(s), 1);
             mbar_init(scalese_bar(s), kEpiWarps);
         }
-        mbar_init(drain_bar, 1);
+        mbar_init(drain_bar, C::F8 ? 2 : 1);  // the MMA issuers
         mbar_init(handoff_bar, 1);
         *abort_flag = 0;
         *peer_issued = 0;
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                     for (int term = 0; term < k.terms && ok; ++term) {
                         Cursor x, y[NH];
                         x.template start<!C::X_MN>(k.X[term], (int64_t)mt * 256 + (int)cr * 128);
-    #pragma unroll
+#pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
                             if (FORM == kGated) y[h].template start<!C::Y_MN>(k.Y[cr], hc);
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                             const uint32_t dst = smem_u32(tiles + s * C::STAGE);
                             load_box<C::X_MN, C::F8>(k, x, dst, bar);
                             x.advance(C::BK);
-    #pragma unroll
+#pragma unroll
                             for (int h = 0; h < NH; ++h) {
                                 if (h < nh) load_box<C::Y_MN, C::F8>(k, y[h], dst + (uint32_t)(C::BOX * (1 + h)), bar);
                                 y[h].advance(C::BK);
@@ -405,7 +409,40 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                         mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status, false);
                 }
             }
-        } else if (warp == 1) {
+        } else if (C::F8 && warp < 3) {
+            // ---------------- MMA issuers (leader CTA only): warp 1 fills the even accumulator, warp 2 the odd one ----
+            // One thread's waits and commits for one accumulator would hold up the
+            // other's MMAs (1.86 ms with one issuer, 1.84 with two).
+            if (lane == 0 && cr == 0) {
+                const int buf = warp - 1;
+                const uint32_t mine = pair < k.total ? (uint32_t)((k.total - 1 - pair) / npairs + 1) : 0;
+                const uint32_t total = mine * (uint32_t)k.k_blocks;  // k-blocks of this pair's tiles
+                // Descriptors hold addresses in units of 16 bytes.
+                const uint64_t a0 = operand_step<C::X_MN, true>(smem_u32(tiles), 0);
+                const uint64_t b0 = operand_step<C::Y_MN, true>(smem_u32(tiles) + C::BOX, 0);
+                constexpr uint32_t A_STEP = 2, B_STEP = C::Y_MN ? 256 : 2;
+                const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+                uint32_t stage = (uint32_t)buf, phase = 0;
+                for (uint32_t it = (uint32_t)buf; it < total; it += 2) {
+                    if (!mbar_wait(full_bar((int)stage), phase, abort_flag, k.status) ||
+                        !mbar_wait(acce_bar(buf), ((it >> 1) & 1) ^ 1, abort_flag, k.status))
+                        break;
+                    fence_after();
+                    const uint64_t a = a0 + stage * (C::STAGE / 16), b = b0 + stage * (C::STAGE / 16);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) pair_mma<FORM>(d, a + kk * A_STEP, b + kk * B_STEP, kk > 0);
+                    umma2_commit_both(accf_bar(buf));
+                    umma2_commit_both(empty_bar((int)stage));
+                    stage += 2;
+                    if (stage >= (uint32_t)S) {
+                        stage -= S;
+                        phase ^= 1;
+                    }
+                }
+                umma2_commit_both(drain_bar);
+                mbar_wait(drain_bar, 0, abort_flag, k.status, false);
+            }
+        } else if (!C::F8 && warp == 1) {
             // ---------------- MMA issuer (leader CTA only) ----------------
             if (lane == 0 && cr == 0) {
                 const int k_total = k.terms * k.k_blocks;
@@ -415,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                 // The four MMAs of the k-block in stage s, half h of its Y, into buffer buf.
                 auto issue = [&](int s, int buf, int h, bool first) {
                     const uint32_t a = smem_u32(tiles + s * C::STAGE), b = a + (uint32_t)(C::BOX * (1 + h));
-    #pragma unroll
+#pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         pair_mma<FORM>(tmem_base + (uint32_t)(buf * 256), operand_step<C::X_MN, C::F8>(a, kk),
                                        operand_step<C::Y_MN, C::F8>(b, kk), !first || kk > 0);
@@ -431,21 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                     return true;
                 };
                 for (int t = pair; t < k.total && ok; t += npairs) {
-                    if (C::F8) {
-                        // every k-block is an accumulator of its own
-                        for (int kb = 0; kb < k_total; ++kb, ++it) {
-                            const int buf = it & 1;
-                            if (!wait_free(buf) || !wait_stage(it)) {
-                                ok = false;
-                                break;
-                            }
-                            issue(it % S, buf, 0, true);
-                            umma2_commit_both(empty_bar(it % S));
-                            umma2_commit_both(accf_bar(buf));
-                            ++fills[buf];
-                        }
-                        continue;
-                    }
                     // Half 0 runs ahead over the first R loaded stages while the
                     // epilogue still reads half 1 of the previous tile, then half 1
                     // catches up on the same stages.
@@ -491,34 +513,48 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                 mbar_wait(drain_bar, 0, abort_flag, k.status, false);
             }
         } else if constexpr (C::F8) {
-            // ---------------- scales (both CTAs): thread i of 64 has rows i and i + 64 ----------------
-            const int i = threadIdx.x - 64;
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = pair; t < k.total && ok; t += npairs) {
-                int mt, nt, hh;
-                item_coords(k, t, &mt, &nt, &hh);
-                const int row = mt * 256 + (int)cr * 128 + i, col = nt * 256;
-                ScaleCursor x0, x1, y0, y1;
-                x0.template start<true>(k.X[0], k.x_scale, row, 1, row < k.M);
-                x1.template start<true>(k.X[0], k.x_scale, row + 64, 1, row + 64 < k.M);
-                y0.template start<!C::Y_MN>(k.Y[0], k.y_scale, col, 128, col < k.N);
-                y1.template start<!C::Y_MN>(k.Y[0], k.y_scale, col + 128, 128, col + 128 < k.N);
-                for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
-                    const int s = it % kScaleSlots;
-                    const float a = x0.next(k.status), b = x1.next(k.status), c = y0.next(k.status), d = y1.next(k.status);
-                    ok = mbar_wait(scalese_bar(s), ((it / kScaleSlots) & 1) ^ 1, abort_flag, k.status);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
+            // ---------------- scales (both CTAs): a lane has rows lane + 0, 32, 64, 96 ----------------
+            if (warp == 3) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int t = pair; t < k.total && ok; t += npairs) {
+                    int mt, nt, hh;
+                    item_coords(k, t, &mt, &nt, &hh);
+                    const int row = mt * 256 + (int)cr * 128 + lane, col = nt * 256;
+                    ScaleCursor x, y;  // the rows of a tile are in one block, and its columns in one or two
+                    x.template start<true>(k.X[0], k.x_scale, mt * 256 + (int)cr * 128, 1, true);
+                    int64_t at[4];
+                    bool in[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        in[q] = row + 32 * q < k.M;
+                        at[q] = (int64_t)(lane + 32 * q) * k.x_scale.ld;
                     }
-                    float *to = scales + s * 256;
-                    to[i] = a * c;
-                    to[i + 64] = b * c;
-                    to[128 + i] = a * d;
-                    to[128 + i + 64] = b * d;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(scalesf_bar(s));  // releases the warp's stores, which the sync orders before it
+                    // lanes 0-15 fetch the first 128 columns' scale, the others the second's
+                    const int yc = col + (lane / 16) * 128;
+                    y.template start<!C::Y_MN>(k.Y[0], k.y_scale, yc, 128, yc < k.N);
+                    for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
+                        const int s = it % kScaleSlots;
+                        float v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = in[q] ? x.peek(at[q], k.status) : 0.0f;
+                        x.step_on();
+                        const float w = y.next(k.status);
+                        const float w0 = __shfl_sync(0xFFFFFFFFu, w, 0), w1 = __shfl_sync(0xFFFFFFFFu, w, 16);
+                        ok = mbar_wait(scalese_bar(s), ((it / kScaleSlots) & 1) ^ 1, abort_flag, k.status);
+                        if (!__all_sync(0xFFFFFFFFu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        float *to = scales + s * 256 + lane;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            to[32 * q] = v[q] * w0;
+                            to[128 + 32 * q] = v[q] * w1;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(scalesf_bar(s));  // releases the warp's stores, which the sync orders before it
+                    }
                 }
             }
         }
@@ -576,20 +612,17 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                     }
                     fence_after();
                     const uint32_t at = lanes + (uint32_t)(b * 256 + set * 128);
-                    uint32_t r[2][32];
-                    tmem_ask32(at, r[0]);
                     const float sc = reinterpret_cast<volatile float *>(scales)[s * 256 + set * 128 + quad * 32 + lane];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_got32(r[c & 1]);
-                        if (c < 3) {
-                            tmem_ask32(at + (uint32_t)((c + 1) * 32), r[(c + 1) & 1]);
-                        } else {
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t r[64];
+                        tmem_read64(at + (uint32_t)(c * 64), r);
+                        if (c == 1) {
                             release(b);
                             if (lane == 0) mbar_arrive(scalese_bar(s));
                         }
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(r[c & 1][j]), sc, acc[c * 32 + j]);
+                        for (int j = 0; j < 64; ++j) acc[c * 64 + j] = fmaf(__uint_as_float(r[j]), sc, acc[c * 64 + j]);
                     }
                 }
                 if (!ok) break;

@@ -131,15 +131,23 @@ struct ScaleCursor {
         i = 0;
         p = s.at[blk];
     }
-    __device__ __forceinline__ float next(int *status) {
-        const int64_t at = first + i * inc;
-        const float v = in && in_bounds(status, at, 1, t->n) ? __ldg(p + at) : 0.0f;
+    // The scale `off` places from the next one (another row's), and on to the
+    // next k-block.
+    __device__ __forceinline__ float peek(int64_t off, int *status) const {
+        const int64_t at = first + i * inc + off;
+        return in && in_bounds(status, at, 1, t->n) ? __ldg(p + at) : 0.0f;
+    }
+    __device__ __forceinline__ void step_on() {
         if (++i == n && left > 0) {
             i = 0;
             blk += step;
             --left;
             p = t->at[blk];
         }
+    }
+    __device__ __forceinline__ float next(int *status) {
+        const float v = peek(0, status);
+        step_on();
         return v;
     }
 };
@@ -194,20 +202,26 @@ __device__ __forceinline__ void tmem_got32(uint32_t *r) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ask16(uint32_t at, uint32_t *r) {
+// 64 columns, read and waited for at once: no copies of the registers, which the
+// two-step form makes one of each.
+__device__ __forceinline__ void tmem_read64(uint32_t at, uint32_t *r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at));
-}
-__device__ __forceinline__ void tmem_got16(uint32_t *r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+        " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31,"
+        " %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47,"
+        " %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        "\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(at)
+        : "memory");
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t *w) {
