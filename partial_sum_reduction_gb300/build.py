@@ -27,7 +27,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 SOURCES = ["planner.cpp", "adapters.cu", "api.cu", "blocks8.cu", "collectives.cu", "contract.cu",
-           "contract_pair.cu", "contract_simt.cu", "gemm_simt.cu", "gemm_tcgen05.cu", "layernorm_train.cu"]
+           "contract_pair.cu", "contract_simt.cu", "contract_small.cu", "gemm_simt.cu", "gemm_tcgen05.cu", "layernorm_train.cu"]
 
 
 def _nvcc():

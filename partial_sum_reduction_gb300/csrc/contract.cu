@@ -26,8 +26,9 @@ bool on16(int64_t n, shmm_dtype_t dt) { return n * shmm::elem_bytes(dt) % 16 == 
 bool edges_fit(int b0, int b1, int64_t brows, int64_t bcols) {
     return (b0 == 1 || brows % 128 == 0) && (b1 == 1 || bcols % 128 == 0);
 }
-bool operand_fits(const GridOperand &o) {
-    if (o.at.size() > (size_t)kSlots || !edges_fit(o.b0, o.b1, o.brows, o.bcols) || !on16(o.ld, o.dt)) return false;
+bool operand_fits(const GridOperand &o, bool few_rows = false) {
+    if (o.at.size() > (size_t)kSlots || !on16(o.ld, o.dt)) return false;
+    if (!edges_fit(few_rows ? 1 : o.b0, o.b1, o.brows, o.bcols)) return false;
     for (const void *p : o.at)
         if (reinterpret_cast<uintptr_t>(p) % 16) return false;
     return true;
@@ -37,9 +38,27 @@ size_t holders_of(const GridResult &d) {
     for (const auto &b : d.holders) n += b.size();
     return n;
 }
-bool result_fits(const GridResult &d) {
+bool result_fits(const GridResult &d, bool few_rows = false) {
     return d.holders.size() <= (size_t)kSlots && holders_of(d) <= (size_t)kSlots &&
-           edges_fit(d.b0, d.b1, d.brows, d.bcols) && on16(d.bcols, d.dt);
+           edges_fit(few_rows ? 1 : d.b0, d.b1, d.brows, d.bcols) && on16(d.bcols, d.dt);
+}
+
+int num_sms() {
+    static shmm::PerDevice<int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= shmm::kMaxDevices) return 148;
+    int n = cache.get(dev);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    cache.set(dev, n);
+    return n;
+}
+
+// Up to 128 rows, split over the ranks in whole groups of 8: the kernel for few
+// rows puts the ranks' rows below one another (groups of 8 are what the
+// swizzle of a tile repeats over).
+bool rows_stack(const ContractArgs &a) {
+    return !a.x_t && a.M <= 128 && a.X[0].b0 > 1 && a.X[0].brows % 8 == 0 && a.terms == 1;
 }
 
 // The tensor-core form of a contraction, or -1.
@@ -47,14 +66,15 @@ int form_of(const ContractArgs &a) {
     if (!a.tensor_core || a.M <= 0 || a.N <= 0 || a.Kd <= 0) return -1;
     if (a.M > (int64_t)1 << 30 || a.Kd > (int64_t)1 << 30) return -1;  // coordinates are 32-bit
     const int ny = a.gated || a.two || a.terms == 2 ? 2 : 1, nx = a.terms;
+    const bool stack = rows_stack(a) && !(a.keep && a.kept[0].dt == SHMM_E4M3);
     for (int i = 0; i < nx; ++i)
-        if (!operand_fits(a.X[i])) return -1;
+        if (!operand_fits(a.X[i], stack)) return -1;
     for (int i = 0; i < ny; ++i)
         if (!operand_fits(a.Y[i])) return -1;
     for (int i = 0; i < (a.two ? 2 : 1); ++i)
-        if (!result_fits(a.D[i])) return -1;
+        if (!result_fits(a.D[i], stack)) return -1;
     for (int i = 0; a.keep && i < 2; ++i)
-        if (!result_fits(a.kept[i])) return -1;
+        if (!result_fits(a.kept[i], stack)) return -1;
     const shmm_dtype_t in = a.X[0].dt;
     if (in == SHMM_BF16 && a.D[0].dt == SHMM_BF16) {
         if (a.gated) return kGated;
@@ -63,6 +83,17 @@ int form_of(const ContractArgs &a) {
     }
     if (in == SHMM_E4M3 && !a.x_t && a.terms == 1) return a.y_t ? kNT8 : kNN8;
     return -1;
+}
+
+// The kernel for few rows and small shapes, or CTA pairs.  Pairs need 256 rows
+// by 256 accumulator columns each to be busy; below one such half tile per pair
+// the small kernel's 128 x 128 tiles, split along the contracted dim, spread the
+// work further.  (Kept 8-bit blocks of 128 columns need the pairs' tiles.)
+bool use_small(const ContractArgs &a, int form, int sms) {
+    if (a.keep && a.kept[0].dt == SHMM_E4M3) return false;
+    if (a.M <= 128) return true;
+    const int64_t halves = (a.M + 255) / 256 * ((a.N + (form == kGated ? 127 : 255)) / (form == kGated ? 128 : 256)) * (a.two ? 2 : 1);
+    return halves <= sms / 2;
 }
 
 struct Maps {
@@ -84,11 +115,11 @@ struct Maps {
                 sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
     // mn: the contracted dim runs along the rows.
-    void operand(OpK *o, const GridOperand &g, bool mn) {
+    void operand(OpK *o, const GridOperand &g, bool mn, uint32_t rows = 128) {
         *o = {n, g.b0, g.b1, g.brows, g.bcols};
         const uint32_t row = 128 / (uint32_t)shmm::elem_bytes(g.dt);  // values of a 128-byte swizzled row
         for (const void *p : g.at)
-            add(p, g.brows, g.bcols, g.ld, g.dt, row, mn ? row : 128, CU_TENSOR_MAP_SWIZZLE_128B);
+            add(p, g.brows, g.bcols, g.ld, g.dt, row, mn ? row : rows, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     // Result boxes: 32 x 32 (fp32: 128-byte rows, bf16: 64), bytes 32 x 64.
     int holders(const GridResult &d) {
@@ -100,7 +131,7 @@ struct Maps {
                     d.dt == SHMM_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
         return at;
     }
-    void result(ResK *o, const GridResult &d) {
+    void result(ResK *o, const GridResult &d, bool maps) {
         o->b0 = d.b0;
         o->b1 = d.b1;
         o->brows = d.brows;
@@ -111,7 +142,7 @@ struct Maps {
             h += (int)d.holders[p].size();
         }
         o->first[d.holders.size()] = (uint8_t)h;
-        o->map0 = holders(d);
+        if (maps) o->map0 = holders(d);
     }
 };
 
@@ -135,14 +166,34 @@ int launch_contract(const ContractArgs &a, int *status, void *stream, std::strin
     memset(&k, 0, sizeof k);
     Maps m = {&k, fn};
     const bool x_mn = form == kTN, y_mn = form == kGated || form == kTN || form == kNN8;
-    for (int i = 0; i < a.terms; ++i) m.operand(&k.X[i], a.X[i], x_mn);
+    int sms = num_sms();
+    if (a.max_sms > 0 && a.max_sms < sms) sms = a.max_sms;
+    const bool small = use_small(a, form, sms);
+    k.x_boxes = 1;
+    k.x_rows = 128;
+    if (small && !x_mn && a.M < 128) k.x_rows = (int)((a.M + 7) / 8 * 8);
+    uint32_t box_rows = (uint32_t)k.x_rows;
+    if (small && rows_stack(a)) {
+        k.x_boxes = a.X[0].b0;
+        box_rows = (uint32_t)a.X[0].brows;
+    }
+    for (int i = 0; i < a.terms; ++i) m.operand(&k.X[i], a.X[i], x_mn, box_rows);
     for (int i = 0; i < (a.gated || a.two ? 2 : a.terms); ++i) m.operand(&k.Y[i], a.Y[i], y_mn);
-    for (int i = 0; i < (a.two ? 2 : 1); ++i) m.result(&k.D[i], a.D[i]);
+    auto buffers = [&](int at, const GridResult &d) {
+        int h = 0;
+        for (const auto &b : d.holders)
+            for (void *p : b) k.out[at][h++] = p;
+    };
+    for (int i = 0; i < (a.two ? 2 : 1); ++i) {
+        m.result(&k.D[i], a.D[i], !small);
+        buffers(i, a.D[i]);
+    }
     if (a.keep) {
         k.keep = a.kept[0].dt == SHMM_E4M3 ? 2 : 1;
         k.kept_ld = a.kept[0].scale_ld;
         for (int y = 0; y < 2; ++y) {
-            k.kept_map[y] = m.holders(a.kept[y]);
+            if (!small) k.kept_map[y] = m.holders(a.kept[y]);
+            buffers(2 + y, a.kept[y]);
             int h = 0;
             for (const auto &b : a.kept[y].scale_holders)
                 for (float *p : b) k.kept_scale[y][h++] = p;
@@ -164,7 +215,7 @@ int launch_contract(const ContractArgs &a, int *status, void *stream, std::strin
     k.act = a.act;
     k.out_f32 = a.D[0].dt == SHMM_F32;
     k.status = status;
-    return launch_pair(k, form, a.max_sms, (cudaStream_t)stream);
+    return small ? launch_small(k, form, sms, (cudaStream_t)stream) : launch_pair(k, form, a.max_sms, (cudaStream_t)stream);
 }
 
 }  // namespace shmm

@@ -51,6 +51,10 @@ struct ContractK {
     int total, half_from;  // work items; from half_from on they are half tiles
     int two, act, out_f32;
     int *status;
+    // the kernel for few rows: buffers of the results (D[0], D[1], kept), rows of X
+    // in a stage, its boxes there, stages, their bytes, parts of the contracted dim
+    void *out[4][kSlots];
+    int x_rows, x_boxes, stages, ring_bytes, parts;
 };
 
 // Which block of `blocks` along a dim holds coordinate x, and the coordinate in
@@ -90,6 +94,15 @@ struct Cursor {
             step = o.b1, left = o.b0 - 1, extent = o.brows;
         }
         at = 0;
+    }
+    // From the start to contracted coordinate `to`.
+    __device__ __forceinline__ void seek(int64_t to) {
+        while (left > 0 && to >= extent) {
+            to -= extent;
+            map += step;
+            --left;
+        }
+        at = (int32_t)to;
     }
     __device__ __forceinline__ void advance(int by) {
         at += by;
@@ -136,6 +149,16 @@ struct ScaleCursor {
     __device__ __forceinline__ float peek(int64_t off, int *status) const {
         const int64_t at = first + i * inc + off;
         return in && in_bounds(status, at, 1, t->n) ? __ldg(p + at) : 0.0f;
+    }
+    // From the start to k-block kb.
+    __device__ __forceinline__ void seek(int kb) {
+        while (left > 0 && kb >= n) {
+            kb -= n;
+            blk += step;
+            --left;
+        }
+        p = t->at[blk];
+        i = kb;
     }
     __device__ __forceinline__ void step_on() {
         if (++i == n && left > 0) {
@@ -253,5 +276,6 @@ __device__ __forceinline__ void stage_f32_row(uint32_t at, int r, const float *v
 }
 
 int launch_pair(ContractK &k, int form, int max_sms, cudaStream_t s);
+int launch_small(ContractK &k, int form, int sms, cudaStream_t s);
 
 }  // namespace shmm_tcn

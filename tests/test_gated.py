@@ -83,6 +83,15 @@ def test_sizes(I, J, K, act, kept):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kept", kinds("bf16"))
+@pytest.mark.parametrize("layout,I,J,K", [("rows", 32, 1024, 512), ("rows", 96, 4096, 768), ("rows", 12, 512, 256), ("all_reduce", 48, 1024, 512),
+                                          ("scatter_rows", 64, 2048, 256), ("columns", 24, 512, 2048), ("whole", 128, 16384, 128)])
+def test_few_rows_of_many_ranks(layout, I, J, K, kept):
+    """Rows split over the ranks in groups of 8 (and not), long sums shared by several CTAs."""
+    forward_and_check(layout, I, J, K, "bf16", "silu", kept)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("I,J,K", [(301, 1000, 1157), (1, 1, 1), (5, 37, 300), (64, 4096, 128)])
 def test_fp32_sizes(I, J, K, act):
@@ -236,7 +245,8 @@ def test_nan_stays_where_it_is(where):
     plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", 300, 512, 512, "bf16", "bf16")
     A, gate, up = inputs(4, 300, 512, 512, "bf16")
     clean, C = s.helpers.alloc(plan, s.TENSOR_C), s.helpers.alloc(plan, s.TENSOR_C)
-    plan.gated_forward([A], [gate], [up], clean)
+    # the same call as below: what is kept may choose the kernel, and with it how a sum is split
+    plan.gated_forward([A], [gate], [up], clean, saved=s.helpers.gated_saved(plan, "e4m3"))
     (A if where == "A" else gate)[7, 100] = float("nan")
     saved = s.helpers.gated_saved(plan, "e4m3")
     plan.gated_forward([A], [gate], [up], C, saved=saved)

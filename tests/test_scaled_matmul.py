@@ -75,6 +75,15 @@ def test_odd_sizes_on_the_cuda_cores(layout, I, J, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout,I,J,K", [("rows", 32, 1024, 512), ("rows", 96, 4096, 768), ("rows", 12, 512, 256), ("all_reduce", 48, 1024, 512),
+                                          ("scatter_rows", 64, 2048, 256), ("columns", 24, 512, 2048), ("whole", 128, 16384, 128)])
+def test_few_rows_of_many_ranks(layout, I, J, K):
+    """Rows split over the ranks in groups of 8 (and not), long sums shared by several CTAs."""
+    run_and_check(layout, I, J, K, "f32", scale_seed=2)
+    run_and_check(layout, I, J, K, "bf16")
+
+
+@pytest.mark.gpu
 def test_many_ranks():
     mesh = "{X:32}"
     plan = s.Plan(mesh, "I_X,J", "J,K", "I_X,K", 4096, 256, 256, "e4m3", "bf16")
