@@ -35,49 +35,90 @@ constexpr int kThreads = 256;
 // loads in flight per lane to cover the memory's latency.
 constexpr int kPieces = 4;
 constexpr int kChunk = 256 * kPieces;
+constexpr int kBackPieces = 8, kBackChunk = 256 * kBackPieces;  // of 8-byte loads
 
-// Eight consecutive values of a row, `left` of which exist.
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int64_t left, float *v) {
-    if (VEC) {
+// Eight consecutive values of a row as they are stored, and widened: loads are
+// kept apart from their use, so that all of a warp's are in flight at once.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void vec(const __nv_bfloat16 *p) {
         const uint4 q = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    }
+    __device__ __forceinline__ void one(int i, __nv_bfloat16 v) {
+        w[i / 2] |= (uint32_t)__bfloat16_as_ushort(v) << (16 * (i % 2));
+    }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
+    __device__ __forceinline__ void get(float *v) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(w[i] << 16);
             v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.0f;
     }
-}
-template <bool VEC>
-__device__ __forceinline__ void load8(const float *p, int64_t left, float *v) {
-    if (VEC) {
+    // The largest magnitude's bits as fp32 (infinities and NaN above all others).
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi = max(hi, w[i] & 0x7FFF0000u);
+            lo = max(lo, w[i] << 16 & 0x7FFF0000u);
+        }
+        return max(hi, lo);
+    }
+};
+template <>
+struct Raw8<float> {
+    float f[8];
+    __device__ __forceinline__ void vec(const float *p) {
         const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
     }
-}
-// ... of 8-bit values.
-template <bool VEC>
-__device__ __forceinline__ void load8(const uint8_t *p, int64_t left, float *v) {
-    uint32_t w[2] = {0, 0};
-    if (VEC) {
+    __device__ __forceinline__ void one(int i, float v) { f[i] = v; }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+    }
+    __device__ __forceinline__ void get(float *v) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[i];
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        return m;
+    }
+};
+template <>
+struct Raw8<uint8_t> {
+    uint32_t w[2];
+    __device__ __forceinline__ void vec(const uint8_t *p) {
         const uint2 q = *reinterpret_cast<const uint2 *>(p);
         w[0] = q.x, w[1] = q.y;
+    }
+    __device__ __forceinline__ void one(int i, uint8_t v) { w[i / 4] |= (uint32_t)v << (8 * (i % 4)); }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = 0; }
+    __device__ __forceinline__ void get(float *v) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = from_e4m3x2(w[i / 2] >> (16 * (i % 2)));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+    }
+};
+// `left` of the eight exist.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T *p, int64_t left, Raw8<T> *r) {
+    if (VEC) {
+        r->vec(p);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = from_e4m3x2(w[i / 2] >> (16 * (i % 2)));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            if (i < left) r->one(i, p[i]);
     }
 }
 
@@ -108,13 +149,21 @@ __device__ __forceinline__ void store8(float *p, int64_t left, const float *v) {
             if (i < left) p[i] = v[i];
     }
 }
-// Eight values times `inv` as e4m3.
+// Eight values times `inv` as e4m3; `finite`: the block has no infinity (NaN
+// stays NaN either way).
 template <bool VEC>
-__device__ __forceinline__ void store8_e4m3(uint8_t *p, int64_t left, const float *v, float inv) {
+__device__ __forceinline__ void store8_e4m3(uint8_t *p, int64_t left, const float *v, float inv, bool finite) {
     uint32_t w[2];
+    if (finite) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w[i] = to_e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) | to_e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+        for (int i = 0; i < 2; ++i)
+            w[i] = finite_to_e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) |
+                   finite_to_e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = to_e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) | to_e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    }
     if (VEC) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     } else {
@@ -152,27 +201,36 @@ __global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant
     const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
     const int64_t s_at = (bi * k.brows + row) * k.scale_ld + (int64_t)bj * k.per;
     for (int64_t c0 = (int64_t)blockIdx.y * kChunk; c0 < k.bcols; c0 += (int64_t)gridDim.y * kChunk) {
-        float v[kPieces][8];
+        Raw8<T> raw[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            raw[i].clear();
             if (c < k.bcols && piece_in_bounds<VEC>(k.status, row * k.src_ld + c, k.bcols - c, k.brows * k.src_ld))
-                load8<VEC>(src + c, k.bcols - c, v[i]);
+                load8<VEC>(src + c, k.bcols - c, &raw[i]);
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8;
-            float amax = 0.0f;
+            uint32_t top = raw[i].top();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[i][j]));
+            for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            float v[8];
+            raw[i].get(v);
+            const bool finite = top < 0x7F800000u;
+            float amax = __uint_as_float(top);
+            if (__any_sync(0xFFFFFFFFu, !finite)) {  // the largest finite one, then
+                float m = 0.0f;
 #pragma unroll
-            for (int d = 1; d < 16; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[j]));
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                amax = m;
+            }
             const int e = scale_exp(amax);
             if (c >= k.bcols) continue;
             if (piece_in_bounds<VEC>(k.status, at + c, k.bcols - c, k.codes_n))
-                store8_e4m3<VEC>(k.codes + at + c, k.bcols - c, v[i], pow2(-e));
+                store8_e4m3<VEC>(k.codes + at + c, k.bcols - c, v, pow2(-e), finite);
             if (lane % 16 == 0 && in_bounds(k.status, s_at + c / kBlock, 1, k.scale_n)) k.scale[s_at + c / kBlock] = pow2(e);
         }
     }
@@ -190,21 +248,23 @@ __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_const
     const int64_t rb = blockIdx.x;
     for (int64_t cb = blockIdx.y; cb < k.per; cb += gridDim.y) {
         const int64_t c = cb * kBlock + x * 8, r0 = rb * kBlock + y;
-        float v[8][8];
+        Raw8<T> raw[8];
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 16 * i;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            raw[i].clear();
             if (r < k.brows && c < k.bcols &&
                 piece_in_bounds<VEC>(k.status, r * k.src_ld + c, k.bcols - c, k.brows * k.src_ld))
-                load8<VEC>(src + r * k.src_ld + c, k.bcols - c, v[i]);
+                load8<VEC>(src + r * k.src_ld + c, k.bcols - c, &raw[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+            float v[8];
+            raw[i].get(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[i][j]));
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[j]));
+        }
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
         __syncthreads();  // the last block's partial maxima have been read
@@ -219,7 +279,11 @@ __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_const
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 16 * i, at = (bi * k.brows + r) * k.ld + bj * k.bcols + c;
             if (r < k.brows && c < k.bcols && piece_in_bounds<VEC>(k.status, at, k.bcols - c, k.codes_n))
-                store8_e4m3<VEC>(k.codes + at, k.bcols - c, v[i], pow2(-e));
+            {
+                float v[8];
+                raw[i].get(v);
+                store8_e4m3<VEC>(k.codes + at, k.bcols - c, v, pow2(-e), false);
+            }
         }
     }
 }
@@ -248,27 +312,29 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ 
     const int64_t s_n = (k.brows + k.scale_rows - 1) / k.scale_rows * k.scale_ld;
     const float *scale = k.scale[blockIdx.z] + s_row;
     const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
-    for (int64_t c0 = (int64_t)blockIdx.y * kChunk; c0 < k.bcols; c0 += (int64_t)gridDim.y * kChunk) {
-        float v[kPieces][8], s[kPieces];
+    for (int64_t c0 = (int64_t)blockIdx.y * kBackChunk; c0 < k.bcols; c0 += (int64_t)gridDim.y * kBackChunk) {
+        Raw8<uint8_t> raw[kBackPieces];
+        float s[kBackPieces];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < kBackPieces; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8;
             s[i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            raw[i].clear();
             if (c < k.bcols && piece_in_bounds<VEC>(k.status, row * k.src_ld + c, k.bcols - c, k.brows * k.src_ld) &&
                 in_bounds(k.status, s_row + c / kBlock, 1, s_n)) {
-                load8<VEC>(src + c, k.bcols - c, v[i]);
+                load8<VEC>(src + c, k.bcols - c, &raw[i]);
                 s[i] = scale[c / kBlock];
             }
         }
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < kBackPieces; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8;
             if (c >= k.bcols || !piece_in_bounds<VEC>(k.status, at + c, k.bcols - c, k.dst_n)) continue;
+            float v[8];
+            raw[i].get(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= s[i];
-            store8<VEC>(static_cast<T *>(k.dst) + at + c, k.bcols - c, v[i]);
+            for (int j = 0; j < 8; ++j) v[j] *= s[i];
+            store8<VEC>(static_cast<T *>(k.dst) + at + c, k.bcols - c, v);
         }
     }
 }
@@ -300,15 +366,18 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
     const int64_t in = row * k.bcols, n = k.brows * k.bcols;
     const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
     for (int64_t c0 = (int64_t)blockIdx.y * (256 * PIECES); c0 < k.bcols; c0 += (int64_t)gridDim.y * (256 * PIECES)) {
-        float d[PIECES][8], g[PIECES][8], u[PIECES][8], gs[PIECES], us[PIECES];
+        Raw8<T> dr[PIECES];
+        Raw8<S> gr[PIECES], ur[PIECES];
+        float gs[PIECES], us[PIECES];
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8, left = k.bcols - c;
             gs[i] = us[i] = 1.0f;
+            dr[i].clear(), gr[i].clear(), ur[i].clear();
             if (left <= 0 || !piece_in_bounds<VEC>(k.status, in + c, left, n)) continue;
-            load8<VEC>(static_cast<const T *>(k.dH[z]) + in + c, left, d[i]);
-            load8<VEC>(static_cast<const S *>(k.G[z]) + in + c, left, g[i]);
-            load8<VEC>(static_cast<const S *>(k.U[z]) + in + c, left, u[i]);
+            load8<VEC>(static_cast<const T *>(k.dH[z]) + in + c, left, &dr[i]);
+            load8<VEC>(static_cast<const S *>(k.G[z]) + in + c, left, &gr[i]);
+            load8<VEC>(static_cast<const S *>(k.U[z]) + in + c, left, &ur[i]);
             const int64_t s = row * k.scale_ld + c / kBlock;
             if (E8 && in_bounds(k.status, s, 1, k.brows * k.scale_ld)) {
                 gs[i] = k.g_scale[z][s];
@@ -319,18 +388,19 @@ __global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__
         for (int i = 0; i < PIECES; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8, left = k.bcols - c;
             if (left <= 0 || !piece_in_bounds<VEC>(k.status, at + c, left, k.out_n)) continue;
-            float h[8];
+            float d[8], g[8], u[8], h[8];
+            dr[i].get(d), gr[i].get(g), ur[i].get(u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float gj = E8 ? g[i][j] * gs[i] : g[i][j], uj = E8 ? u[i][j] * us[i] : u[i][j];
+                const float gj = E8 ? g[j] * gs[i] : g[j], uj = E8 ? u[j] * us[i] : u[j];
                 float slope;
                 const float a = gate_act_slope<ACT>(gj, &slope);
                 h[j] = a * uj;
-                g[i][j] = d[i][j] * uj * slope;
-                u[i][j] = d[i][j] * a;
+                g[j] = d[j] * uj * slope;
+                u[j] = d[j] * a;
             }
-            store8<VEC>(static_cast<T *>(k.dG) + at + c, left, g[i]);
-            store8<VEC>(static_cast<T *>(k.dU) + at + c, left, u[i]);
+            store8<VEC>(static_cast<T *>(k.dG) + at + c, left, g);
+            store8<VEC>(static_cast<T *>(k.dU) + at + c, left, u);
             for (int q = k.h_first[z]; q < k.h_first[z + 1]; ++q)
                 if (piece_in_bounds<VEC>(k.status, in + c, left, n)) store8<VEC>(static_cast<T *>(k.H[q]) + in + c, left, h);
         }
@@ -408,7 +478,7 @@ int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_
     k.b1 = src.b1;
     k.scale_rows = src.scale_rows;
     k.status = status;
-    const dim3 grid = rows_grid(src.brows, src.bcols, kChunk, blocks);
+    const dim3 grid = rows_grid(src.brows, src.bcols, kBackChunk, blocks);
     cudaStream_t s = (cudaStream_t)stream;
     count_launch();
     if (dt == SHMM_F32)

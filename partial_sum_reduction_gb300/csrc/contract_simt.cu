@@ -41,7 +41,7 @@ struct Op {
     const void *at[CAP];
     const float *scale[CAP];
     int64_t brows, bcols, ld, scale_ld;
-    int b0, b1, dt, scale_rows;
+    int b0, b1, scale_rows;
 };
 
 template <int CAP>
@@ -63,32 +63,60 @@ struct SimtK {
     int *status;
 };
 
-template <int CAP>
+__device__ __forceinline__ float wide(float v) { return v; }
+__device__ __forceinline__ float wide(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float wide(uint8_t v) { return from_e4m3x2(v).x; }
+
+// Stored element (r, c) of an operand of several blocks.  T: uint8_t for 8 bits.
+template <typename T, int CAP>
 __device__ __forceinline__ float fetch(const Op<CAP> &o, int64_t r, int64_t c, int *status) {
-    int p = 0;
-    if (o.b0 > 1) {
-        const int64_t b = r / o.brows;
-        r -= b * o.brows;
-        p = (int)b * o.b1;
-    }
-    if (o.b1 > 1) {
-        const int64_t b = c / o.bcols;
-        c -= b * o.bcols;
-        p += (int)b;
-    }
+    const int64_t b = r / o.brows, d = c / o.bcols;
+    const int p = (int)b * o.b1 + (int)d;
+    r -= b * o.brows;
+    c -= d * o.bcols;
     const int64_t i = r * o.ld + c;
     if (!in_bounds(status, i, 1, (o.brows - 1) * o.ld + o.bcols)) return 0.0f;
-    if (o.dt == SHMM_F32) return static_cast<const float *>(o.at[p])[i];
-    if (o.dt == SHMM_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(o.at[p])[i]);
+    const float v = wide(static_cast<const T *>(o.at[p])[i]);
+    if (sizeof(T) > 1) return v;
     const int64_t s = r / o.scale_rows * o.scale_ld + c / 128;
     if (!in_bounds(status, s, 1, (o.brows + o.scale_rows - 1) / o.scale_rows * o.scale_ld)) return 0.0f;
-    return from_e4m3x2(static_cast<const uint8_t *>(o.at[p])[i]).x * o.scale[p][s];
+    return v * o.scale[p][s];
 }
 
-// Element (m, k) of X or (k, n) of Y, each stored as it is or transposed.
-template <int CAP>
-__device__ __forceinline__ float fetch_at(const Op<CAP> &o, int64_t r, int64_t c, int t, int *status) {
-    return t ? fetch(o, c, r, status) : fetch(o, r, c, status);
+// N elements of one thread's part of a piece: element i at result index a0 + i *
+// da, contracted index k0 + i * dk (0 past the ends), stored as [result,
+// contracted] or, MAJOR_K, the other way round.  One block: the addresses are
+// independent of one another and of any table, so the loads go out together.
+template <typename T, int CAP, int N>
+__device__ __forceinline__ void fetch_part(const Op<CAP> &o, bool major_k, int64_t a0, int da, int64_t a_end, int64_t k0,
+                                           int dk, int64_t k_end, float *v, int *status) {
+    if (o.b0 * o.b1 == 1) {
+        const T *base = static_cast<const T *>(o.at[0]);
+        const int64_t n = (o.brows - 1) * o.ld + o.bcols;
+        T raw[N];
+        float sc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t a = a0 + (int64_t)i * da, kk = k0 + (int64_t)i * dk;
+            const int64_t r = major_k ? kk : a, c = major_k ? a : kk, at = r * o.ld + c;
+            const bool in = a < a_end && kk < k_end && in_bounds(status, at, 1, n);
+            raw[i] = T(0);
+            sc[i] = 0.0f;
+            if (in) raw[i] = base[at];
+            if (sizeof(T) == 1 && in) {
+                const int64_t s = (o.scale_rows == 1 ? r : r / 128) * o.scale_ld + c / 128;
+                if (in_bounds(status, s, 1, (o.brows + o.scale_rows - 1) / o.scale_rows * o.scale_ld)) sc[i] = o.scale[0][s];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = sizeof(T) == 1 ? wide(raw[i]) * sc[i] : wide(raw[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t a = a0 + (int64_t)i * da, kk = k0 + (int64_t)i * dk;
+            v[i] = a < a_end && kk < k_end ? fetch<T>(o, major_k ? kk : a, major_k ? a : kk, status) : 0.0f;
+        }
+    }
 }
 
 __device__ __forceinline__ void store_as(void *p, int64_t i, int dt, float v) {
@@ -133,7 +161,7 @@ __device__ __forceinline__ void put4_e4m3(const Res<CAP> &d, int64_t row, bool r
     }
 }
 
-template <int CAP, bool GATED>
+template <typename T, int CAP, bool GATED>
 __global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_constant__ SimtK<CAP> k) {
     constexpr int NY = GATED ? 2 : 1;
     constexpr int PX = TM * TK / kThreads, PY = TK * TN / kThreads;
@@ -151,23 +179,13 @@ __global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_co
     auto ask = [&](int64_t piece) {
         const int t = piece >= per_term ? 1 : 0;
         const int64_t k0 = (piece - t * per_term) * TK;
+        if (k.x_t) fetch_part<T, CAP, PX>(k.X[t], true, m0 + lane, 0, k.M, k0 + warp, kThreads / TM, k.Kd, xr, k.status);
+        else fetch_part<T, CAP, PX>(k.X[t], false, m0 + warp, kThreads / TK, k.M, k0 + lane, 0, k.Kd, xr, k.status);
 #pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int at = threadIdx.x + i * kThreads;
-            const int64_t kk = k0 + (k.x_t ? at / TM : at % TK), m = m0 + (k.x_t ? at % TM : at / TK);
-            xr[i] = kk < k.Kd && m < k.M ? fetch_at(k.X[t], m, kk, k.x_t, k.status) : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < PY; ++i) {
-            const int at = threadIdx.x + i * kThreads;
-            const int64_t kk = k0 + (k.y_t ? at % TK : at / TN), n = n0 + (k.y_t ? at / TK : at % TN);
-            const bool in = kk < k.Kd && n < n1;
-            if (GATED) {
-                yr[0][i] = in ? fetch_at(k.Y[0], kk, n, k.y_t, k.status) : 0.0f;
-                yr[NY - 1][i] = in ? fetch_at(k.Y[1], kk, n, k.y_t, k.status) : 0.0f;
-            } else {
-                yr[0][i] = in ? fetch_at(k.Y[t], kk, n, k.y_t, k.status) : 0.0f;
-            }
+        for (int y = 0; y < NY; ++y) {
+            const Op<CAP> &o = k.Y[GATED ? y : t];
+            if (k.y_t) fetch_part<T, CAP, PY>(o, false, n0 + warp, kThreads / TK, n1, k0 + lane, 0, k.Kd, yr[y], k.status);
+            else fetch_part<T, CAP, PY>(o, true, n0 + threadIdx.x % TN, 0, n1, k0 + threadIdx.x / TN, kThreads / TN, k.Kd, yr[y], k.status);
         }
     };
 
@@ -255,7 +273,6 @@ void set_op(Op<CAP> *o, const shmm::GridOperand &g) {
     o->scale_ld = g.scale_ld;
     o->b0 = g.b0;
     o->b1 = g.b1;
-    o->dt = g.dt;
     o->scale_rows = g.scale_rows;
 }
 
@@ -315,8 +332,11 @@ cudaError_t launch(const shmm::ContractArgs &a, int which, int *status, cudaStre
     k.status = status;
     const dim3 grid((unsigned)((a.M + TM - 1) / TM), (unsigned)(k.n_per * k.D.b1));
     shmm::count_launch();
-    return a.gated ? shmm_pdl::launch_pdl(contract_simt_kernel<CAP, true>, grid, dim3(kThreads), 0, s, k)
-                   : shmm_pdl::launch_pdl(contract_simt_kernel<CAP, false>, grid, dim3(kThreads), 0, s, k);
+#define GO(T, G) shmm_pdl::launch_pdl(contract_simt_kernel<T, CAP, G>, grid, dim3(kThreads), 0, s, k)
+    if (a.X[0].dt == SHMM_E4M3) return GO(uint8_t, false);
+    if (a.X[0].dt == SHMM_BF16) return a.gated ? GO(__nv_bfloat16, true) : GO(__nv_bfloat16, false);
+    return a.gated ? GO(float, true) : GO(float, false);
+#undef GO
 }
 
 }  // namespace

@@ -22,11 +22,15 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Two values to e4m3 (the first in the low byte); infinities become NaN.
+// Two values to e4m3 (the first in the low byte), no infinities among them.
+__device__ __forceinline__ uint32_t finite_to_e4m3x2(float a, float b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// ... any values: infinities become NaN.
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
     if (fabsf(a) == INFINITY) a = NAN;
     if (fabsf(b) == INFINITY) b = NAN;
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    return finite_to_e4m3x2(a, b);
 }
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
