@@ -180,8 +180,8 @@ struct Stager {
         stage_f32_row(at, lane, v);
         send(d, map0, at, row0, col0);
     }
-    // 64 values times inv as e4m3
-    __device__ __forceinline__ void bytes(const ResK &d, int map0, const float *v, float inv, int row0, int col0) {
+    // 64 values times inv as e4m3; `finite`: no infinity among them
+    __device__ __forceinline__ void bytes(const ResK &d, int map0, const float *v, float inv, bool finite, int row0, int col0) {
         const uint32_t at = next(2048);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -189,7 +189,8 @@ struct Stager {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float *x = v + 16 * j + 4 * i;
-                w[i] = to_e4m3x2(x[0] * inv, x[1] * inv) | to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+                w[i] = finite_to_e4m3x2(x[0] * inv, x[1] * inv) | finite_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+                if (!finite) w[i] = to_e4m3x2(x[0] * inv, x[1] * inv) | to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
             }
             st_shared_v4(at + (uint32_t)(lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)), w);
         }
@@ -205,29 +206,41 @@ __device__ __forceinline__ void finish_half(const ContractK &k, Stager &st, uint
                                             int h, int lane, Release release) {
     const bool rows_in = row0 < k.M;
     if (FORM == kGated) {
-        float amax[2] = {0.0f, 0.0f};
+        float amax[2] = {0.0f, 0.0f};  // NaN apart: fmaxf leaves it out
+        uint32_t r[2][64];
         if (k.keep == 2) {  // the block's largest magnitudes: the other warp's columns, too
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                tmem_read64(acc + (uint32_t)(y * 128 + (1 - set) * 64), r[y]);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) amax[y] = fmaxf(amax[y], fabsf(__uint_as_float(r[y][i])));
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) tmem_read64(acc + (uint32_t)(y * 128 + set * 64), r[y]);
+        bool finite = true;
+        if (k.keep == 2) {
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t r[32];
-                    tmem_ask32(acc + (uint32_t)(y * 128 + (1 - set) * 64 + c * 32), r);
-                    tmem_got32(r);
+                for (int i = 0; i < 64; ++i) amax[y] = fmaxf(amax[y], fabsf(__uint_as_float(r[y][i])));
+            finite = amax[0] < INFINITY && amax[1] < INFINITY;
+            if (__any_sync(0xFFFFFFFFu, !finite)) {  // an infinity somewhere: the largest finite ones, then
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) amax[y] = fmaxf(amax[y], finite_abs(__uint_as_float(r[i])));
+                for (int y = 0; y < 2; ++y) {
+                    float m = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) m = fmaxf(m, finite_abs(__uint_as_float(r[y][i])));
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[8];
+                        tmem_read8(acc + (uint32_t)(y * 128 + (1 - set) * 64 + c * 8), o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(__uint_as_float(o[i])));
+                    }
+                    amax[y] = m;
                 }
-        }
-        uint32_t r[2][64];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            tmem_ask32(acc + (uint32_t)(y * 128 + set * 64), r[y]);
-            tmem_ask32(acc + (uint32_t)(y * 128 + set * 64 + 32), r[y] + 32);
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            tmem_got32(r[y]);
-            tmem_got32(r[y] + 32);
+            }
         }
         release();
         if (!rows_in || col >= k.N) return;
@@ -237,10 +250,8 @@ __device__ __forceinline__ void finish_half(const ContractK &k, Stager &st, uint
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 float *v = y ? u : g;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) amax[y] = fmaxf(amax[y], finite_abs(v[i]));
                 const int e = scale_exp(amax[y]);
-                if (c0 < k.N) st.bytes(k.D[0], k.kept_map[y], v, pow2(-e), row0, c0);
+                if (c0 < k.N) st.bytes(k.D[0], k.kept_map[y], v, pow2(-e), finite, row0, c0);
                 if (y == set && row0 + lane < k.M) {  // warp 0 of the two writes the gate's scales, warp 1 the up's
                     int32_t rl, cl;
                     const int p = block_of(k.D[0], row0 + lane, col, &rl, &cl);
@@ -265,10 +276,8 @@ __device__ __forceinline__ void finish_half(const ContractK &k, Stager &st, uint
         }
     } else {
         uint32_t r[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ask32(acc + (uint32_t)(set * 128 + c * 32), r + c * 32);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_got32(r + c * 32);
+        tmem_read64(acc + (uint32_t)(set * 128), r);
+        tmem_read64(acc + (uint32_t)(set * 128 + 64), r + 64);
         release();
         if (!rows_in) return;
         const ResK &d = k.D[k.two ? h : 0];
