@@ -85,15 +85,17 @@ int form_of(const ContractArgs &a) {
     return -1;
 }
 
-// The kernel for few rows and small shapes, or CTA pairs.  Pairs need 256 rows
-// by 256 accumulator columns each to be busy; below one such half tile per pair
-// the small kernel's 128 x 128 tiles, split along the contracted dim, spread the
-// work further.  (Kept 8-bit blocks of 128 columns need the pairs' tiles.)
+// The kernel for few rows and small shapes, or CTA pairs.  (Kept 8-bit blocks of
+// 128 columns need the pairs' tiles.)  Up to 128 rows would fill half a pair's
+// tile at most.  Above, the small kernel's 128 x 128 tiles win where they leave
+// at least half of its places free, so that two or more CTAs share a tile's
+// contracted dim.  Measured, us, pairs / small: 515 x 1024 rows by 2 x 2816
+// products (dA) 32 / 19 in four parts; 512 x 4096 by 2 x 4096 51 / 42 in two;
+// 1024 x 4096 by 2 x 4096 54 / 71 in one; 8 bits, 256 x 4096 x 4096 23 / 17 in
+// two, 512 x 4096 x 4096 23 / 25 in one.
 bool use_small(const ContractArgs &a, int form, int sms) {
     if (a.keep && a.kept[0].dt == SHMM_E4M3) return false;
-    if (a.M <= 128) return true;
-    const int64_t halves = (a.M + 255) / 256 * ((a.N + (form == kGated ? 127 : 255)) / (form == kGated ? 128 : 256)) * (a.two ? 2 : 1);
-    return halves <= sms / 2;
+    return a.M <= 128 || small_parts(form, a.M, a.N, a.Kd, a.terms, a.two, sms) > 1;
 }
 
 struct Maps {

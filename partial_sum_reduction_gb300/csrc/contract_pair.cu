@@ -360,6 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
             if (lane == 0) {
                 uint32_t it = 0;  // stages loaded
                 uint32_t stage_bytes[S];
+                // One thread feeds the pair: what its loop computes is time between loads.
+                const uint32_t full0 = full_bar(0), empty0 = empty_bar(0), leader_full0 = mapa_shared(full0, 0);
+                const uint32_t tiles0 = smem_u32(tiles);
+                uint32_t stage = 0, phase = 0;
                 bool ok = true;
                 for (int t = pair; t < k.total && ok; t += npairs) {
                     int mt, nt, hh;
@@ -368,30 +372,29 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                     const uint32_t bytes = (uint32_t)(C::BOX * (1 + nh));
                     for (int term = 0; term < k.terms && ok; ++term) {
                         Cursor x, y[NH];
-                        x.template start<!C::X_MN>(k.X[term], (int64_t)mt * 256 + (int)cr * 128);
+                        x.template start<!C::X_MN>(k.maps, k.X[term], (int64_t)mt * 256 + (int)cr * 128);
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
-                            if (FORM == kGated) y[h].template start<!C::Y_MN>(k.Y[cr], hc);
-                            else y[h].template start<!C::Y_MN>(k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
+                            if (FORM == kGated) y[h].template start<!C::Y_MN>(k.maps, k.Y[cr], hc);
+                            else y[h].template start<!C::Y_MN>(k.maps, k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
                         }
                         for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
-                            const int s = it % S;
-                            if (!mbar_wait(empty_bar(s), ((it / S) & 1) ^ 1, abort_flag, k.status)) {
+                            if (!mbar_wait(empty0 + stage * 8, phase ^ 1, abort_flag, k.status)) {
                                 ok = false;
                                 break;
                             }
-                            if (cr == 0) mbar_expect_tx(full_bar(s), 2 * bytes);
-                            stage_bytes[s] = bytes;
-                            const uint32_t bar = mapa_shared(full_bar(s), 0);
-                            const uint32_t dst = smem_u32(tiles + s * C::STAGE);
-                            load_box<C::X_MN, C::F8>(k, x, dst, bar);
+                            if (cr == 0) mbar_expect_tx(full0 + stage * 8, 2 * bytes);
+                            stage_bytes[stage] = bytes;
+                            const uint32_t bar = leader_full0 + stage * 8, dst = tiles0 + stage * C::STAGE;
+                            load_box<C::X_MN, C::F8>(x, dst, bar);
                             x.advance(C::BK);
 #pragma unroll
                             for (int h = 0; h < NH; ++h) {
-                                if (h < nh) load_box<C::Y_MN, C::F8>(k, y[h], dst + (uint32_t)(C::BOX * (1 + h)), bar);
+                                if (h < nh) load_box<C::Y_MN, C::F8>(y[h], dst + (uint32_t)(C::BOX * (1 + h)), bar);
                                 y[h].advance(C::BK);
                             }
+                            if (++stage == (uint32_t)S) stage = 0, phase ^= 1;
                         }
                     }
                 }

@@ -194,50 +194,53 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
             int term = kb0 / k.k_blocks, kb = kb0 % k.k_blocks;
             auto start = [&](int at) {
                 if (term >= k.terms) return;
-                x.template start<!C::X_MN>(k.X[term], row0);
-                x.seek((int64_t)at * C::BK);
+                x.template start<!C::X_MN>(k.maps, k.X[term], row0);
+                x.seek(at * C::BK);
                 if (FORM == kGated) {
-                    y[0].template start<false>(k.Y[0], col0);
-                    y[1].template start<false>(k.Y[1], col0);
-                    y[1].seek((int64_t)at * C::BK);
+                    y[0].template start<false>(k.maps, k.Y[0], col0);
+                    y[1].template start<false>(k.maps, k.Y[1], col0);
+                    y[1].seek(at * C::BK);
                 } else {
-                    y[0].template start<!C::Y_MN>(k.Y[k.two ? which : term], col0);
+                    y[0].template start<!C::Y_MN>(k.maps, k.Y[k.two ? which : term], col0);
                 }
-                y[0].seek((int64_t)at * C::BK);
+                y[0].seek(at * C::BK);
             };
             start(kb);
             const int n = kb1 - kb0;
             int it = 0;
+            uint32_t stage = 0, phase = 0, dst = smem_u32(tiles);
+            const uint32_t full0 = full_bar(0), empty0 = empty_bar(0);
+            const uint32_t row_bytes = (uint32_t)k.X[0].brows * 128;
             for (; it < n; ++it) {
-                const int s = it % S;
-                if (!mbar_wait(empty_bar(s), ((it / S) & 1) ^ 1, abort_flag, k.status)) break;
-                const uint32_t bar = full_bar(s), dst = smem_u32(tiles) + (uint32_t)s * stage_bytes;
+                if (!mbar_wait(empty0 + stage * 8, phase ^ 1, abort_flag, k.status)) break;
+                const uint32_t bar = full0 + stage * 8;
                 mbar_expect_tx(bar, stage_bytes);
-                const CUtensorMap *mx = &k.maps[x.map];
                 if (C::X_MN) {
-                    tma_load_2d(dst, mx, bar, x.fixed, x.at);
-                    tma_load_2d(dst + 8192, mx, bar, x.fixed + 64, x.at);
+                    tma_load_2d(dst, x.map, bar, x.fixed, x.at);
+                    tma_load_2d(dst + 8192, x.map, bar, x.fixed + 64, x.at);
                 } else if (k.x_boxes == 1) {
-                    tma_load_2d(dst, mx, bar, x.at, x.fixed);
+                    tma_load_2d(dst, x.map, bar, x.at, x.fixed);
                 } else {  // few rows, split over the ranks: a box from each
                     for (int b = 0; b < k.x_boxes; ++b)
-                        tma_load_2d(dst + (uint32_t)(b * (int)k.X[0].brows * 128), &k.maps[x.map + b * k.X[0].b1], bar, x.at, 0);
+                        tma_load_2d(dst + (uint32_t)b * row_bytes, x.map + b * k.X[0].b1, bar, x.at, 0);
                 }
                 const uint32_t to = dst + x_bytes;
                 if (FORM == kGated) {
-                    tma_load_2d(to, &k.maps[y[0].map], bar, y[0].fixed, y[0].at);
-                    tma_load_2d(to + 8192, &k.maps[y[1].map], bar, y[1].fixed, y[1].at);
+                    tma_load_2d(to, y[0].map, bar, y[0].fixed, y[0].at);
+                    tma_load_2d(to + 8192, y[1].map, bar, y[1].fixed, y[1].at);
                     y[1].advance(C::BK);
                 } else if (!C::Y_MN) {
-                    tma_load_2d(to, &k.maps[y[0].map], bar, y[0].at, y[0].fixed);
+                    tma_load_2d(to, y[0].map, bar, y[0].at, y[0].fixed);
                 } else if (C::F8) {
-                    tma_load_2d(to, &k.maps[y[0].map], bar, y[0].fixed, y[0].at);
+                    tma_load_2d(to, y[0].map, bar, y[0].fixed, y[0].at);
                 } else {
-                    tma_load_2d(to, &k.maps[y[0].map], bar, y[0].fixed, y[0].at);
-                    tma_load_2d(to + 8192, &k.maps[y[0].map], bar, y[0].fixed + 64, y[0].at);
+                    tma_load_2d(to, y[0].map, bar, y[0].fixed, y[0].at);
+                    tma_load_2d(to + 8192, y[0].map, bar, y[0].fixed + 64, y[0].at);
                 }
                 x.advance(C::BK);
                 y[0].advance(C::BK);
+                dst += stage_bytes;
+                if (++stage == (uint32_t)S) stage = 0, phase ^= 1, dst = smem_u32(tiles);
                 if (++kb == k.k_blocks) {
                     kb = 0;
                     ++term;
@@ -253,18 +256,25 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
         // ---------------- MMA ----------------
         if (lane == 0) {
             const int n = kb1 - kb0;
+            uint32_t stage = 0, phase = 0;
+            // descriptors hold addresses in units of 16 bytes
+            uint64_t a = operand_step<C::X_MN, C::F8>(smem_u32(tiles), 0);
+            uint64_t b = operand_step<C::Y_MN, C::F8>(smem_u32(tiles) + x_bytes, 0);
+            constexpr uint32_t A_STEP = C::X_MN ? 128 : 2, B_STEP = !C::Y_MN ? 2 : C::F8 ? 256 : 128;
+            const uint64_t a0 = a, b0 = b;
             for (int it = 0; it < n; ++it) {
-                const int s = it % S, buf = C::F8 ? it % C::BUFS : 0;
-                if (!mbar_wait(full_bar(s), (it / S) & 1, abort_flag, k.status)) break;
+                const int buf = C::F8 ? it % C::BUFS : 0;
+                if (!mbar_wait(full_bar((int)stage), phase, abort_flag, k.status)) break;
                 if (C::F8 && !mbar_wait(acce_bar(buf), ((it / C::BUFS) & 1) ^ 1, abort_flag, k.status)) break;
                 fence_after();
-                const uint32_t a = smem_u32(tiles) + (uint32_t)s * stage_bytes, b = a + x_bytes;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma<FORM>(tmem_base + (uint32_t)(buf * 128), operand_step<C::X_MN, C::F8>(a, kk),
-                              operand_step<C::Y_MN, C::F8>(b, kk), kk > 0 || (!C::F8 && it > 0));
+                    mma<FORM>(tmem_base + (uint32_t)(buf * 128), a + kk * A_STEP, b + kk * B_STEP, kk > 0 || (!C::F8 && it > 0));
                 if (C::F8) commit(accf_bar(buf));
-                commit(empty_bar(s));
+                commit(empty_bar((int)stage));
+                a += stage_bytes / 16;
+                b += stage_bytes / 16;
+                if (++stage == (uint32_t)S) stage = 0, phase ^= 1, a = a0, b = b0;
             }
             if (!C::F8) commit(accf_bar(0));
             commit(drain_bar);
@@ -281,18 +291,39 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
         }
         y.template start<!C::Y_MN>(k.Y[0], k.y_scale, col0, 128, true);
         y.seek(kb0);
-        for (int it = 0; it < kb1 - kb0; ++it) {
-            const int s = it % kScaleSlots;
-            float v[4];
+        // Four k-blocks' scales at a time, the next four asked for before these are
+        // waited for a place: one at a time, each k-block would take a read's latency.
+        const int n = kb1 - kb0;
+        float v[4][4], w[4], nv[4][4], nw[4];
+        auto ask = [&](int it) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = x[q].next(k.status);
-            const float w = y.next(k.status);
-            ok = mbar_wait(scalese_bar(s), ((it / kScaleSlots) & 1) ^ 1, abort_flag, k.status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) scales[s * 128 + lane + 32 * q] = v[q] * w;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(scalesf_bar(s));
+                for (int q = 0; q < 4; ++q) nv[i][q] = it + i < n ? x[q].next(k.status) : 0.0f;
+                nw[i] = it + i < n ? y.next(k.status) : 0.0f;
+            }
+        };
+        ask(0);
+        for (int it = 0; it < n && ok; it += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = nw[i];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[i][q] = nv[i][q];
+            }
+            if (it + 4 < n) ask(it + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (it + i >= n) break;
+                const int s = (it + i) % kScaleSlots;
+                ok = mbar_wait(scalese_bar(s), (((it + i) / kScaleSlots) & 1) ^ 1, abort_flag, k.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) scales[s * 128 + lane + 32 * q] = v[i][q] * w[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scalesf_bar(s));
+            }
         }
     } else if (warp >= 4 && (warp % 4) < active) {
         // ---------------- partial sums into shared memory ----------------
@@ -422,11 +453,7 @@ int launch_form(ContractK &k, int sms, cudaStream_t s) {
     k.ring_bytes = k.stages * stage;
     if (k.ring_bytes < k.x_rows * kPitch * 4) k.ring_bytes = (k.x_rows * kPitch * 4 + 1023) / 1024 * 1024;
     const int64_t tiles = (int64_t)k.m_tiles * k.n_tiles * (k.two ? 2 : 1);
-    // As many parts as there are places for, with four k-blocks each at least.
-    const int all = k.terms * k.k_blocks;
-    int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= (int64_t)sms * C::CTAS && all >= parts * 2 * 4) parts *= 2;
-    k.parts = parts;
+    const int parts = k.parts = small_parts(FORM, k.M, k.N, k.Kd, k.terms, k.two, sms);
     shmm::count_launch();
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -449,6 +476,17 @@ int launch_form(ContractK &k, int sms, cudaStream_t s) {
 }  // namespace
 
 namespace shmm_tcn {
+
+// As many parts as there are places for, with four k-blocks each at least.
+int small_parts(int form, int64_t M, int64_t N, int64_t Kd, int terms, bool two, int sms) {
+    const bool f8 = form == kNN8 || form == kNT8;
+    const int64_t width = form == kGated ? 64 : 128, bk = f8 ? 128 : 64;
+    const int64_t tiles = (M + 127) / 128 * ((N + width - 1) / width) * (two ? 2 : 1), all = terms * ((Kd + bk - 1) / bk);
+    const int64_t places = (int64_t)sms * (f8 ? Cfg<kNN8>::CTAS : Cfg<kGated>::CTAS);
+    int parts = 1;
+    while (parts < 8 && tiles * parts * 2 <= places && all >= parts * 2 * 4) parts *= 2;
+    return parts;
+}
 
 int launch_small(ContractK &k, int form, int sms, cudaStream_t s) {
     switch (form) {

@@ -81,33 +81,33 @@ __device__ __forceinline__ int block_of(const ResK &d, int row, int col, int32_t
 // the tile's row or column in it, `at` the contracted coordinate in it.
 // K_MAJOR: stored [rows or columns of the result, contracted].
 struct Cursor {
-    int map, step, left;  // shards still to come
-    int32_t fixed, at;
-    int64_t extent;
+    const CUtensorMap *map;
+    int step, left;  // from shard to shard, and those still to come
+    int32_t fixed, at, extent;
     template <bool K_MAJOR>
-    __device__ __forceinline__ void start(const OpK &o, int64_t fixed_at) {
+    __device__ __forceinline__ void start(const CUtensorMap *maps, const OpK &o, int64_t fixed_at) {
         if (K_MAJOR) {
-            map = o.map0 + split(o.b0, o.brows, fixed_at, &fixed) * o.b1;
-            step = 1, left = o.b1 - 1, extent = o.bcols;
+            map = maps + o.map0 + split(o.b0, o.brows, fixed_at, &fixed) * o.b1;
+            step = 1, left = o.b1 - 1, extent = (int32_t)o.bcols;
         } else {
-            map = o.map0 + split(o.b1, o.bcols, fixed_at, &fixed);
-            step = o.b1, left = o.b0 - 1, extent = o.brows;
+            map = maps + o.map0 + split(o.b1, o.bcols, fixed_at, &fixed);
+            step = o.b1, left = o.b0 - 1, extent = (int32_t)o.brows;
         }
         at = 0;
     }
     // From the start to contracted coordinate `to`.
-    __device__ __forceinline__ void seek(int64_t to) {
+    __device__ __forceinline__ void seek(int32_t to) {
         while (left > 0 && to >= extent) {
             to -= extent;
             map += step;
             --left;
         }
-        at = (int32_t)to;
+        at = to;
     }
     __device__ __forceinline__ void advance(int by) {
         at += by;
-        if (left > 0 && at >= extent) {
-            at -= (int32_t)extent;
+        if (at >= extent && left > 0) {
+            at -= extent;
             map += step;
             --left;
         }
@@ -179,16 +179,15 @@ struct ScaleCursor {
 // into shared memory.  K-major: one box, a row of 128 bytes per row of the
 // result.  MN-major: a row per contracted index, 128 bytes of the result's dim
 // per box (two boxes of 64 bf16 values, one of 128 bytes).
-template <bool MN, bool F8, typename Params>
-__device__ __forceinline__ void load_box(const Params &k, const Cursor &c, uint32_t dst, uint32_t bar) {
-    const CUtensorMap *map = &k.maps[c.map];
+template <bool MN, bool F8>
+__device__ __forceinline__ void load_box(const Cursor &c, uint32_t dst, uint32_t bar) {
     if (!MN) {
-        shmm_pair::tma_load_2d_pair(dst, map, bar, c.at, c.fixed);
+        shmm_pair::tma_load_2d_pair(dst, c.map, bar, c.at, c.fixed);
     } else if (F8) {
-        shmm_pair::tma_load_2d_pair(dst, map, bar, c.fixed, c.at);
+        shmm_pair::tma_load_2d_pair(dst, c.map, bar, c.fixed, c.at);
     } else {
-        shmm_pair::tma_load_2d_pair(dst, map, bar, c.fixed, c.at);
-        shmm_pair::tma_load_2d_pair(dst + 8192, map, bar, c.fixed + 64, c.at);
+        shmm_pair::tma_load_2d_pair(dst, c.map, bar, c.fixed, c.at);
+        shmm_pair::tma_load_2d_pair(dst + 8192, c.map, bar, c.fixed + 64, c.at);
     }
 }
 
@@ -262,5 +261,6 @@ __device__ __forceinline__ void stage_f32_row(uint32_t at, int r, const float *v
 
 int launch_pair(ContractK &k, int form, int max_sms, cudaStream_t s);
 int launch_small(ContractK &k, int form, int sms, cudaStream_t s);
+int small_parts(int form, int64_t M, int64_t N, int64_t Kd, int terms, bool two, int sms);
 
 }  // namespace shmm_tcn
