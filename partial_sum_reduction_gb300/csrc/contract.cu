@@ -77,7 +77,7 @@ int form_of(const ContractArgs &a) {
         if (!result_fits(a.kept[i], stack)) return -1;
     const shmm_dtype_t in = a.X[0].dt;
     if (in == SHMM_BF16 && a.D[0].dt == SHMM_BF16) {
-        if (a.gated) return kGated;
+        if (a.gated) return a.keep && a.kept[0].dt == SHMM_E4M3 ? kGated8 : kGated;
         if (!a.x_t && a.y_t) return kNT;
         if (a.x_t && !a.y_t) return kTN;
     }
@@ -94,7 +94,7 @@ int form_of(const ContractArgs &a) {
 // 1024 x 4096 by 2 x 4096 54 / 71 in one; 8 bits, 256 x 4096 x 4096 23 / 17 in
 // two, 512 x 4096 x 4096 23 / 25 in one.
 bool use_small(const ContractArgs &a, int form, int sms) {
-    if (a.keep && a.kept[0].dt == SHMM_E4M3) return false;
+    if (form == kGated8) return false;
     return a.M <= 128 || small_parts(form, a.M, a.N, a.Kd, a.terms, a.two, sms) > 1;
 }
 
@@ -167,7 +167,7 @@ int launch_contract(const ContractArgs &a, int *status, void *stream, std::strin
     ContractK k;
     memset(&k, 0, sizeof k);
     Maps m = {&k, fn};
-    const bool x_mn = form == kTN, y_mn = form == kGated || form == kTN || form == kNN8;
+    const bool x_mn = form == kTN, y_mn = form == kGated || form == kGated8 || form == kTN || form == kNN8;
     int sms = num_sms();
     if (a.max_sms > 0 && a.max_sms < sms) sms = a.max_sms;
     const bool small = use_small(a, form, sms);

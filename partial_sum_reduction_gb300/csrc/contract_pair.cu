@@ -84,13 +84,17 @@ template <int FORM>
 struct Cfg {
     static constexpr bool F8 = FORM == kNN8 || FORM == kNT8;
     static constexpr bool X_MN = FORM == kTN;                                       // X stored [Kd, M]
-    static constexpr bool Y_MN = FORM == kGated || FORM == kTN || FORM == kNN8;     // Y stored [Kd, N]
-    static constexpr int NH = F8 ? 1 : 2;      // 256-column halves of a tile
+    static constexpr bool GATED = FORM == kGated || FORM == kGated8;
+    static constexpr bool Y_MN = GATED || FORM == kTN || FORM == kNN8;              // Y stored [Kd, N]
+    static constexpr bool REGS = F8 || FORM == kGated8;  // long sums in registers
+    static constexpr int RUN = F8 ? 1 : 4;     // k-blocks of an accumulator, with REGS
+    static constexpr int ISSUERS = F8 ? 2 : 1;
+    static constexpr int NH = REGS ? 1 : 2;    // 256-column halves of a tile
     static constexpr int BK = F8 ? 128 : 64;   // values of a k-block: 128 bytes
     static constexpr int BOX = 16384;          // 128 rows or columns of a k-block
     static constexpr int STAGE = BOX * (1 + NH);
-    static constexpr int S = F8 ? 5 : 4;
-    static constexpr int SMEM = S * STAGE + kStagingBytes + (F8 ? kScaleSlots * 1024 : 0) + 1024 /*align*/ + 1024 /*barriers*/;
+    static constexpr int S = REGS ? 5 : 4;
+    static constexpr int SMEM = S * STAGE + kStagingBytes + (REGS ? kScaleSlots * 1024 : 0) + 1024 /*align*/ + 1024 /*barriers*/;
 };
 
 // MMA of the pair: M = 256, N = 256, fp32 accumulator.
@@ -139,6 +143,7 @@ __device__ __forceinline__ void item_coords(const ContractK &k, int t, int *mt, 
 template <int FORM>
 __device__ __forceinline__ int half_col(const ContractK &k, int nt, int h) {
     if (FORM == kGated) return nt * 256 + h * 128;
+    if (FORM == kGated8) return nt * 128;
     if (Cfg<FORM>::F8 || k.two) return nt * 256;
     return nt * 512 + h * 256;
 }
@@ -198,82 +203,112 @@ struct Stager {
     }
 };
 
-// One half of a finished tile of a bf16 form, for one epilogue warp: the half's
-// accumulator (256 columns from `acc`) into registers, `release`, then the rest.
-// The two warps of a lane quadrant (set 0 and 1) share the columns.
+// act(g) * u of one warp's 32 rows and 64 columns from c0.
+template <int ACT>
+__device__ __forceinline__ void store_product(const ContractK &k, Stager &st, const float *g, const float *u, int row0, int c0) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (c0 + c * 32 >= k.N) break;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = gate_act<ACT>(g[c * 32 + i]) * u[c * 32 + i];
+        st.bf16(k.D[0], k.D[0].map0, v, row0, c0 + c * 32);
+    }
+}
+
+// What the two warps of a lane quadrant tell each other of their rows: two
+// exponents per row, in turn in two places.  A warp writes a place again only
+// after the other has arrived at the next exchange, having read this one.
+constexpr int kNoValue = -127;  // a block of zeros, below every exponent
+struct Exchange {
+    volatile int16_t *at;  // [2][2 warps][32 rows]
+    uint32_t bar;          // both warps arrive
+    uint32_t turn;
+    volatile int *abort_flag;
+    int *status;
+    __device__ __forceinline__ void give(int set, const int *e, int lane) {
+        at[((turn & 1) * 2 + set) * 32 + lane] = (int16_t)((e[0] & 0xFF) | (e[1] << 8));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);  // releases the warp's writes
+    }
+    // The larger ones; false: the wait ran out.
+    __device__ __forceinline__ bool take(int set, int *e, int lane) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(bar, turn & 1, abort_flag, status) ? 1 : 0;
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        const int o = at[((turn & 1) * 2 + (set ^ 1)) * 32 + lane];
+        e[0] = max(e[0], (int)(int8_t)(o & 0xFF));
+        e[1] = max(e[1], o >> 8);
+        ++turn;
+        return ok != 0;
+    }
+};
+
+// A finished tile whose pre-activations are kept in 8 bits: this warp's 64 of a
+// block's 128 columns, the scales from both warps.
+template <int ACT>
+__device__ __forceinline__ bool store_kept8(const ContractK &k, Stager &st, Exchange &ex, const float *g, const float *u, int set,
+                                            int row0, int col, int lane) {
+    const int c0 = col + set * 64;
+    bool finite = true;
+    int e[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const float *v = y ? u : g;
+        float m = 0.0f;  // fmaxf leaves NaN out
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(v[i]));
+        const bool inf = m == INFINITY;
+        finite = finite && !inf;
+        if (__any_sync(0xFFFFFFFFu, inf)) {  // the largest finite one, then
+            m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) m = fmaxf(m, finite_abs(v[i]));
+        }
+        e[y] = m == 0.0f ? kNoValue : scale_exp(m);
+    }
+    ex.give(set, e, lane);
+    store_product<ACT>(k, st, g, u, row0, c0);
+    if (!ex.take(set, e, lane)) return false;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int ey = e[y] == kNoValue ? 0 : e[y];
+        if (c0 < k.N) st.bytes(k.D[0], k.kept_map[y], y ? u : g, pow2(-ey), finite, row0, c0);
+        if (y == set && row0 + lane < k.M) {  // one of the two warps writes the gate's scales, the other the up's
+            int32_t rl, cl;
+            const int p = block_of(k.D[0], row0 + lane, col, &rl, &cl);
+            const int64_t at = (int64_t)rl * k.kept_ld + cl / 128;
+            if (in_bounds(k.status, at, 1, k.D[0].brows * k.kept_ld))
+                for (int q = k.D[0].first[p]; q < k.D[0].first[p + 1]; ++q) k.kept_scale[y][q][at] = pow2(ey);
+        }
+    }
+    return true;
+}
+
+// One half of a finished tile of a form that sums in TMEM, for one epilogue warp:
+// the half's accumulator (256 columns from `acc`) into registers, `release`,
+// then the rest.  The two warps of a lane quadrant (set 0 and 1) share the
+// columns.
 template <int FORM, int ACT, typename Release>
 __device__ __forceinline__ void finish_half(const ContractK &k, Stager &st, uint32_t acc, int set, int row0, int col,
-                                            int h, int lane, Release release) {
+                                            int h, Release release) {
     const bool rows_in = row0 < k.M;
     if (FORM == kGated) {
-        float amax[2] = {0.0f, 0.0f};  // NaN apart: fmaxf leaves it out
         uint32_t r[2][64];
-        if (k.keep == 2) {  // the block's largest magnitudes: the other warp's columns, too
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                tmem_read64(acc + (uint32_t)(y * 128 + (1 - set) * 64), r[y]);
-#pragma unroll
-                for (int i = 0; i < 64; ++i) amax[y] = fmaxf(amax[y], fabsf(__uint_as_float(r[y][i])));
-            }
-        }
 #pragma unroll
         for (int y = 0; y < 2; ++y) tmem_read64(acc + (uint32_t)(y * 128 + set * 64), r[y]);
-        bool finite = true;
-        if (k.keep == 2) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int i = 0; i < 64; ++i) amax[y] = fmaxf(amax[y], fabsf(__uint_as_float(r[y][i])));
-            finite = amax[0] < INFINITY && amax[1] < INFINITY;
-            if (__any_sync(0xFFFFFFFFu, !finite)) {  // an infinity somewhere: the largest finite ones, then
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float m = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) m = fmaxf(m, finite_abs(__uint_as_float(r[y][i])));
-#pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t o[8];
-                        tmem_read8(acc + (uint32_t)(y * 128 + (1 - set) * 64 + c * 8), o);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(__uint_as_float(o[i])));
-                    }
-                    amax[y] = m;
-                }
-            }
-        }
         release();
         if (!rows_in || col >= k.N) return;
-        float *g = reinterpret_cast<float *>(r[0]), *u = reinterpret_cast<float *>(r[1]);
+        const float *g = reinterpret_cast<float *>(r[0]), *u = reinterpret_cast<float *>(r[1]);
         const int c0 = col + set * 64;
-        if (k.keep == 2) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                float *v = y ? u : g;
-                const int e = scale_exp(amax[y]);
-                if (c0 < k.N) st.bytes(k.D[0], k.kept_map[y], v, pow2(-e), finite, row0, c0);
-                if (y == set && row0 + lane < k.M) {  // warp 0 of the two writes the gate's scales, warp 1 the up's
-                    int32_t rl, cl;
-                    const int p = block_of(k.D[0], row0 + lane, col, &rl, &cl);
-                    const int64_t at = (int64_t)rl * k.kept_ld + cl / 128;
-                    if (in_bounds(k.status, at, 1, k.D[0].brows * k.kept_ld))
-                        for (int q = k.D[0].first[p]; q < k.D[0].first[p + 1]; ++q) k.kept_scale[y][q][at] = pow2(e);
-                }
-            }
-        } else if (k.keep == 1) {
+        if (k.keep) {
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (c0 + c * 32 < k.N) st.bf16(k.D[0], k.kept_map[y], (y ? u : g) + c * 32, row0, c0 + c * 32);
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (c0 + c * 32 >= k.N) break;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) g[c * 32 + i] = gate_act<ACT>(g[c * 32 + i]) * u[c * 32 + i];
-            st.bf16(k.D[0], k.D[0].map0, g + c * 32, row0, c0 + c * 32);
-        }
+        store_product<ACT>(k, st, g, u, row0, c0);
     } else {
         uint32_t r[128];
         tmem_read64(acc + (uint32_t)(set * 128), r);
@@ -298,16 +333,17 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *tiles = smem;
     uint8_t *staging = smem + S * C::STAGE;
-    float *scales = reinterpret_cast<float *>(staging + kStagingBytes);  // [kScaleSlots][2][128]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + kStagingBytes + (C::F8 ? kScaleSlots * 1024 : 0));
-    // bars: full[S], empty[S], acc_full[2], acc_empty[2], drain, hand-off, scales_full[], scales_empty[]
+    // 8-bit forms: scales [kScaleSlots][2][128]; kGated8: what pairs of epilogue warps exchange, 256 bytes a pair
+    float *scales = reinterpret_cast<float *>(staging + kStagingBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + kStagingBytes + (C::REGS ? kScaleSlots * 1024 : 0));
+    // bars: full[S], empty[S], acc_full[2], acc_empty[2], drain, hand-off, scales_full[] (kGated8: exchanges), scales_empty[]
     uint32_t *words = reinterpret_cast<uint32_t *>(bars + 2 * S + 6 + 2 * kScaleSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
     volatile uint32_t *peer_issued = words + 2;  // the peer's load count, and its bytes of each of its last S stages
     volatile uint32_t *peer_bytes = words + 4;
     static_assert((2 * S + 6 + 2 * kScaleSlots) * 8 + (4 + S) * 4 <= 1024, "barriers and words");
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // warp: known to be uniform
     const uint32_t cr = cluster_ctarank();  // 0: leader, 1: peer
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
@@ -329,10 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
             mbar_init(acce_bar(s), 2 * kEpiWarps);  // both CTAs' epilogue warps
         }
         for (int s = 0; s < kScaleSlots; ++s) {
-            mbar_init(scalesf_bar(s), 1);
+            mbar_init(scalesf_bar(s), C::F8 ? 1 : 2);  // the warp that fetches them; an exchange's two warps
             mbar_init(scalese_bar(s), kEpiWarps);
         }
-        mbar_init(drain_bar, C::F8 ? 2 : 1);  // the MMA issuers
+        mbar_init(drain_bar, C::ISSUERS);
         mbar_init(handoff_bar, 1);
         *abort_flag = 0;
         *peer_issued = 0;
@@ -354,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     grid_launch_dependents();
 
     if (warp < 4) {
-        if constexpr (C::F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if constexpr (C::REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
             if (lane == 0) {
@@ -376,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
-                            if (FORM == kGated) y[h].template start<!C::Y_MN>(k.maps, k.Y[cr], hc);
+                            if (C::GATED) y[h].template start<!C::Y_MN>(k.maps, k.Y[cr], hc);
                             else y[h].template start<!C::Y_MN>(k.maps, k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
                         }
                         for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
@@ -421,40 +457,69 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                         mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status, false);
                 }
             }
-        } else if (C::F8 && warp < 3) {
-            // ---------------- MMA issuers (leader CTA only): warp 1 fills the even accumulator, warp 2 the odd one ----
-            // One thread's waits and commits for one accumulator would hold up the
-            // other's MMAs (1.86 ms with one issuer, 1.84 with two).
-            if (lane == 0 && cr == 0) {
-                const int buf = warp - 1;
+        } else if (C::REGS && warp <= C::ISSUERS) {
+            // ---------------- MMA issuers (leader CTA only) ----------------
+            // 8-bit forms: warp 1 fills the even accumulator, warp 2 the odd one; one
+            // thread's waits and commits for one would hold up the other's MMAs (1.86
+            // ms with one issuer, 1.84 with two).  A stage's barrier tells only the
+            // last two fills apart, so nobody may wait for one before the fill before
+            // it (S k-blocks back) is complete: with a k-block to an accumulator that
+            // one belongs to an accumulator that the epilogue has handed back before.
+            // With four it may be the other issuer's present one, so there is one
+            // issuer, which takes all in order.
+            if (cr == 0) {
+                const bool chosen = elect_one();
+                const int runs = (k.k_blocks + C::RUN - 1) / C::RUN;  // accumulators filled per tile
                 const uint32_t mine = pair < k.total ? (uint32_t)((k.total - 1 - pair) / npairs + 1) : 0;
-                const uint32_t total = mine * (uint32_t)k.k_blocks;  // k-blocks of this pair's tiles
+                const uint32_t total = mine * (uint32_t)runs;
                 // Descriptors hold addresses in units of 16 bytes.
-                const uint64_t a0 = operand_step<C::X_MN, true>(smem_u32(tiles), 0);
-                const uint64_t b0 = operand_step<C::Y_MN, true>(smem_u32(tiles) + C::BOX, 0);
-                constexpr uint32_t A_STEP = 2, B_STEP = C::Y_MN ? 256 : 2;
-                const uint32_t d = tmem_base + (uint32_t)(buf * 256);
-                uint32_t stage = (uint32_t)buf, phase = 0;
-                for (uint32_t it = (uint32_t)buf; it < total; it += 2) {
-                    if (!mbar_wait(full_bar((int)stage), phase, abort_flag, k.status) ||
-                        !mbar_wait(acce_bar(buf), ((it >> 1) & 1) ^ 1, abort_flag, k.status))
-                        break;
-                    fence_after();
-                    const uint64_t a = a0 + stage * (C::STAGE / 16), b = b0 + stage * (C::STAGE / 16);
+                const uint64_t a0 = operand_step<C::X_MN, C::F8>(smem_u32(tiles), 0);
+                const uint64_t b0 = operand_step<C::Y_MN, C::F8>(smem_u32(tiles) + C::BOX, 0);
+                constexpr uint32_t A_STEP = 2, B_STEP = !C::Y_MN ? 2 : C::F8 ? 256 : 128;
+                uint32_t stage = 0, phase = 0, in_tile = 0;  // of run `it`
+                auto skip = [&](int n) {
+                    stage += (uint32_t)n;
+                    while (stage >= (uint32_t)S) stage -= S, phase ^= 1;
+                };
+                auto length = [&]() -> int {
+                    const int left = k.k_blocks - (int)in_tile * C::RUN;
+                    return left < C::RUN ? left : C::RUN;
+                };
+                bool ok = true;
+                for (uint32_t it = 0; it < total && ok; ++it) {
+                    const int n = length();
+                    const int buf = (int)(it & 1);
+                    if (C::ISSUERS == 1 || buf == warp - 1) {
+                        const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+                        if (!warp_wait(acce_bar(buf), ((it >> 1) & 1) ^ 1, abort_flag, k.status)) break;
+                        uint32_t s = stage, p = phase;
+                        for (int kb = 0; kb < n; ++kb) {
+                            if (!warp_wait(full_bar((int)s), p, abort_flag, k.status)) {
+                                ok = false;
+                                break;
+                            }
+                            fence_after();
+                            const uint64_t a = a0 + s * (C::STAGE / 16), b = b0 + s * (C::STAGE / 16);
+                            if (chosen) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) pair_mma<FORM>(d, a + kk * A_STEP, b + kk * B_STEP, kk > 0);
-                    umma2_commit_both(accf_bar(buf));
-                    umma2_commit_both(empty_bar((int)stage));
-                    stage += 2;
-                    if (stage >= (uint32_t)S) {
-                        stage -= S;
-                        phase ^= 1;
+                                for (int kk = 0; kk < 4; ++kk) pair_mma<FORM>(d, a + kk * A_STEP, b + kk * B_STEP, kb > 0 || kk > 0);
+                                if (kb == n - 1) umma2_commit_both(accf_bar(buf));
+                                umma2_commit_both(empty_bar((int)s));
+                            }
+                            __syncwarp();
+                            if (++s == (uint32_t)S) s = 0, p ^= 1;
+                        }
                     }
+                    skip(n);
+                    if (++in_tile == (uint32_t)runs) in_tile = 0;
                 }
-                umma2_commit_both(drain_bar);
-                mbar_wait(drain_bar, 0, abort_flag, k.status, false);
+                if (chosen) {
+                    umma2_commit_both(drain_bar);
+                    mbar_wait(drain_bar, 0, abort_flag, k.status, false);
+                }
+                __syncwarp();
             }
-        } else if (!C::F8 && warp == 1) {
+        } else if (!C::REGS && warp == 1) {
             // ---------------- MMA issuer (leader CTA only) ----------------
             if (lane == 0 && cr == 0) {
                 const int k_total = k.terms * k.k_blocks;
@@ -572,10 +637,11 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
         }
     } else {
         // ---------------- epilogue (both CTAs) ----------------
-        if constexpr (C::F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        if constexpr (C::REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int ew = warp - 4, quad = warp % 4, set = ew / 4;
         const uint32_t lanes = tmem_base + ((uint32_t)(quad * 32) << 16);
         Stager st = {&k, smem_u32(staging) + (uint32_t)ew * 4096u, 0, lane};
+        Exchange ex = {reinterpret_cast<volatile int16_t *>(scales) + quad * 128, scalesf_bar(quad), 0, abort_flag, k.status};
         uint32_t used[2] = {0, 0};
         auto wait_full = [&](int b) -> bool {
             int ok = 1;
@@ -596,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
             int mt, nt, hh;
             item_coords(k, t, &mt, &nt, &hh);
             const int row0 = mt * 256 + (int)cr * 128 + quad * 32;
-            if constexpr (!C::F8) {
+            if constexpr (!C::REGS) {
                 const int nh = hh >= 0 ? 1 : NH;
                 for (int h = 0; h < nh; ++h) {
                     if (!wait_full(h)) {
@@ -605,33 +671,36 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                     }
                     const int half = hh >= 0 ? hh : h;
                     finish_half<FORM, ACT>(k, st, lanes + (uint32_t)(h * 256), set, row0, half_col<FORM>(k, nt, half), half,
-                                           lane, [&] { release(h); });
+                                           [&] { release(h); });
                 }
             } else {
-                const int col0 = nt * 256 + set * 128;
+                const int col0 = C::F8 ? nt * 256 + set * 128 : nt * 128;
+                // the warp's columns: 128 in a row, or 64 of the gate and the same 64 of the up projection
+                const uint32_t first = C::F8 ? set * 128 : set * 64, second = C::F8 ? first + 64 : first + 128;
                 float acc[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-                for (int kb = 0; kb < k.k_blocks; ++kb, ++fill) {
+                for (int kb = 0; kb < k.k_blocks; kb += C::RUN, ++fill) {
                     const int b = fill & 1, s = fill % kScaleSlots;
                     int got = 1;
                     if (lane == 0)
-                        got = mbar_wait(scalesf_bar(s), (fill / kScaleSlots) & 1, abort_flag, k.status) &&
+                        got = (!C::F8 || mbar_wait(scalesf_bar(s), (fill / kScaleSlots) & 1, abort_flag, k.status)) &&
                               mbar_wait(accf_bar(b), (fill >> 1) & 1, abort_flag, k.status);
                     if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint32_t at = lanes + (uint32_t)(b * 256 + set * 128);
-                    const float sc = reinterpret_cast<volatile float *>(scales)[s * 256 + set * 128 + quad * 32 + lane];
+                    const uint32_t at = lanes + (uint32_t)(b * 256);
+                    const float sc =
+                        C::F8 ? reinterpret_cast<volatile float *>(scales)[s * 256 + set * 128 + quad * 32 + lane] : 1.0f;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t r[64];
-                        tmem_read64(at + (uint32_t)(c * 64), r);
+                        tmem_read64(at + (c ? second : first), r);
                         if (c == 1) {
                             release(b);
-                            if (lane == 0) mbar_arrive(scalese_bar(s));
+                            if (C::F8 && lane == 0) mbar_arrive(scalese_bar(s));
                         }
 #pragma unroll
                         for (int j = 0; j < 64; ++j) acc[c * 64 + j] = fmaf(__uint_as_float(r[j]), sc, acc[c * 64 + j]);
@@ -639,12 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                 }
                 if (!ok) break;
                 if (row0 >= k.M) continue;
+                if constexpr (FORM == kGated8) {
+                    ok = store_kept8<ACT>(k, st, ex, acc, acc + 64, set, row0, col0, lane);
+                } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int c0 = col0 + c * 32;
-                    if (c0 >= k.N) break;
-                    if (k.out_f32) st.f32(k.D[0], k.D[0].map0, acc + c * 32, row0, c0);
-                    else st.bf16(k.D[0], k.D[0].map0, acc + c * 32, row0, c0);
+                    for (int c = 0; c < 4; ++c) {
+                        const int c0 = col0 + c * 32;
+                        if (c0 >= k.N) break;
+                        if (k.out_f32) st.f32(k.D[0], k.D[0].map0, acc + c * 32, row0, c0);
+                        else st.bf16(k.D[0], k.D[0].map0, acc + c * 32, row0, c0);
+                    }
                 }
             }
         }
@@ -708,12 +781,12 @@ int launch_form(ContractK &k, int max_sms, cudaStream_t s) {
     if (e != cudaSuccess) return (int)e;
     if (cap < 1) return (int)cudaErrorNotSupported;
     if (max_sms > 0 && max_sms / 2 < cap) cap = max_sms / 2 > 0 ? max_sms / 2 : 1;
-    const int width = FORM == kGated || C::F8 || k.two ? 256 : 512;
+    const int width = FORM == kGated8 ? 128 : FORM == kGated || C::F8 || k.two ? 256 : 512;
     k.m_tiles = (int)((k.M + 255) / 256);
     k.n_tiles = (int)((k.N + width - 1) / width);
     k.k_blocks = (int)((k.Kd + C::BK - 1) / C::BK);
     k.total = k.half_from = k.m_tiles * k.n_tiles;
-    if (!C::F8) {
+    if (!C::REGS) {
         // A last wave that would leave at least half of the pairs idle runs as
         // halves on twice as many.
         const int r = k.total % cap;
@@ -751,6 +824,9 @@ int launch_pair(ContractK &k, int form, int max_sms, cudaStream_t s) {
         case kGated:
             return k.act == SHMM_SILU ? launch_form<kGated, SHMM_SILU>(k, max_sms, s)
                                       : launch_form<kGated, SHMM_GELU_TANH>(k, max_sms, s);
+        case kGated8:
+            return k.act == SHMM_SILU ? launch_form<kGated8, SHMM_SILU>(k, max_sms, s)
+                                      : launch_form<kGated8, SHMM_GELU_TANH>(k, max_sms, s);
         case kNT: return launch_form<kNT, SHMM_SILU>(k, max_sms, s);
         case kTN: return launch_form<kTN, SHMM_SILU>(k, max_sms, s);
         case kNN8: return launch_form<kNN8, SHMM_SILU>(k, max_sms, s);

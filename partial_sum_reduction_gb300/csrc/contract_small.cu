@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
     static_assert((2 * MS + 8 + 2 * kScaleSlots + 1) * 8 + 8 <= 1024, "barriers and words");
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // warp: known to be uniform
     const int parts = k.parts, part = (int)cluster_ctarank(), S = k.stages;
     auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
     auto empty_bar = [&](int s) { return smem_u32(&bars[MS + s]); };
@@ -254,28 +254,30 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA ----------------
-        if (lane == 0) {
-            const int n = kb1 - kb0;
-            uint32_t stage = 0, phase = 0;
-            // descriptors hold addresses in units of 16 bytes
-            uint64_t a = operand_step<C::X_MN, C::F8>(smem_u32(tiles), 0);
-            uint64_t b = operand_step<C::Y_MN, C::F8>(smem_u32(tiles) + x_bytes, 0);
-            constexpr uint32_t A_STEP = C::X_MN ? 128 : 2, B_STEP = !C::Y_MN ? 2 : C::F8 ? 256 : 128;
-            const uint64_t a0 = a, b0 = b;
-            for (int it = 0; it < n; ++it) {
-                const int buf = C::F8 ? it % C::BUFS : 0;
-                if (!mbar_wait(full_bar((int)stage), phase, abort_flag, k.status)) break;
-                if (C::F8 && !mbar_wait(acce_bar(buf), ((it / C::BUFS) & 1) ^ 1, abort_flag, k.status)) break;
-                fence_after();
+        const bool chosen = elect_one();
+        const int n = kb1 - kb0;
+        uint32_t stage = 0, phase = 0;
+        // descriptors hold addresses in units of 16 bytes
+        const uint64_t a0 = operand_step<C::X_MN, C::F8>(smem_u32(tiles), 0);
+        const uint64_t b0 = operand_step<C::Y_MN, C::F8>(smem_u32(tiles) + x_bytes, 0);
+        constexpr uint32_t A_STEP = C::X_MN ? 128 : 2, B_STEP = !C::Y_MN ? 2 : C::F8 ? 256 : 128;
+        for (int it = 0; it < n; ++it) {
+            const int buf = C::F8 ? it % C::BUFS : 0;
+            if (!warp_wait(full_bar((int)stage), phase, abort_flag, k.status)) break;
+            if (C::F8 && !warp_wait(acce_bar(buf), ((it / C::BUFS) & 1) ^ 1, abort_flag, k.status)) break;
+            fence_after();
+            const uint64_t a = a0 + stage * (stage_bytes / 16), b = b0 + stage * (stage_bytes / 16);
+            if (chosen) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma<FORM>(tmem_base + (uint32_t)(buf * 128), a + kk * A_STEP, b + kk * B_STEP, kk > 0 || (!C::F8 && it > 0));
                 if (C::F8) commit(accf_bar(buf));
                 commit(empty_bar((int)stage));
-                a += stage_bytes / 16;
-                b += stage_bytes / 16;
-                if (++stage == (uint32_t)S) stage = 0, phase ^= 1, a = a0, b = b0;
             }
+            __syncwarp();
+            if (++stage == (uint32_t)S) stage = 0, phase ^= 1;
+        }
+        if (chosen) {
             if (!C::F8) commit(accf_bar(0));
             commit(drain_bar);
             mbar_wait(drain_bar, 0, abort_flag, k.status, false);

@@ -15,7 +15,7 @@ namespace shmm_tcn {
 
 using shmm_dev::in_bounds;
 
-enum Form { kGated, kNT, kTN, kNN8, kNT8 };
+enum Form { kGated, kNT, kTN, kNN8, kNT8, kGated8 };  // kGated8: the pre-activations kept in 8 bits
 
 constexpr int kSlots = 16;  // blocks of an operand, holders of a result
 constexpr int kMaps = 96;
@@ -202,13 +202,6 @@ __device__ __forceinline__ uint64_t operand_step(uint32_t addr, int kk) {
     return shmm_pair::smem_desc(addr + (uint32_t)(kk * 2048), 8192, 1024);
 }
 
-__device__ __forceinline__ void tmem_read8(uint32_t at, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(at)
-        : "memory");
-}
 // TMEM columns of this warp's 32 lanes, read and waited for in one statement:
 // nothing that uses the registers can move before the wait.
 __device__ __forceinline__ void tmem_read64(uint32_t at, uint32_t *r) {
@@ -229,6 +222,19 @@ __device__ __forceinline__ void tmem_read64(uint32_t at, uint32_t *r) {
           "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
         : "r"(at)
         : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// A wait by a whole warp, with an answer that is the same for all its lanes (and
+// known to be): an MMA issuer's loop stays uniform, its descriptors in uniform
+// registers, where tcgen05.mma takes them from.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+    return __all_sync(0xFFFFFFFFu, shmm_dev::mbar_wait(bar, parity, abort_flag, status));
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t at, const uint32_t *w) {
