@@ -87,7 +87,16 @@ struct Cfg {
     static constexpr bool GATED = FORM == kGated || FORM == kGated8;
     static constexpr bool Y_MN = GATED || FORM == kTN || FORM == kNN8;              // Y stored [Kd, N]
     static constexpr bool REGS = F8 || FORM == kGated8;  // long sums in registers
-    static constexpr int RUN = F8 ? 1 : 4;     // k-blocks of an accumulator, with REGS
+    // k-blocks of an accumulator, with REGS: of a tile's first two, and of the others.
+    // The first two are filled while the epilogue still works on the last tile.
+    // (kGated8, 8192 x 4096 x 16384: 1282 us with runs of 4, 1186 of 8, 1105 of 16;
+    // what is kept then differs from the 64-bit form by 1.1e-4, 2.0e-4 and 2.7 to
+    // 3.6e-4, with fp32 products by 1.4 to 2.5e-4.)
+    static constexpr int LEAD = F8 ? 1 : 8, RUN = F8 ? 1 : 4;
+    static __device__ __forceinline__ int run(int r, int left) {
+        const int n = r < 2 ? LEAD : RUN;
+        return left < n ? left : n;
+    }
     static constexpr int ISSUERS = F8 ? 2 : 1;
     static constexpr int NH = REGS ? 1 : 2;    // 256-column halves of a tile
     static constexpr int BK = F8 ? 128 : 64;   // values of a k-block: 128 bytes
@@ -393,69 +402,71 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
         if constexpr (C::REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
-            if (lane == 0) {
-                uint32_t it = 0;  // stages loaded
-                uint32_t stage_bytes[S];
-                // One thread feeds the pair: what its loop computes is time between loads.
-                const uint32_t full0 = full_bar(0), empty0 = empty_bar(0), leader_full0 = mapa_shared(full0, 0);
-                const uint32_t tiles0 = smem_u32(tiles);
-                uint32_t stage = 0, phase = 0;
-                bool ok = true;
-                for (int t = pair; t < k.total && ok; t += npairs) {
-                    int mt, nt, hh;
-                    item_coords(k, t, &mt, &nt, &hh);
-                    const int nh = hh >= 0 ? 1 : NH;
-                    const uint32_t bytes = (uint32_t)(C::BOX * (1 + nh));
-                    for (int term = 0; term < k.terms && ok; ++term) {
-                        Cursor x, y[NH];
-                        x.template start<!C::X_MN>(k.maps, k.X[term], (int64_t)mt * 256 + (int)cr * 128);
+            const bool chosen = elect_one();
+            uint32_t it = 0;  // stages loaded
+            uint32_t stage_bytes[S];
+            // One warp feeds the pair: what its loop computes is time between loads.
+            const uint32_t full0 = full_bar(0), empty0 = empty_bar(0), leader_full0 = mapa_shared(full0, 0);
+            const uint32_t tiles0 = smem_u32(tiles);
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (int t = pair; t < k.total && ok; t += npairs) {
+                int mt, nt, hh;
+                item_coords(k, t, &mt, &nt, &hh);
+                const int nh = hh >= 0 ? 1 : NH;
+                const uint32_t bytes = (uint32_t)(C::BOX * (1 + nh));
+                for (int term = 0; term < k.terms && ok; ++term) {
+                    Cursor x, y[NH];
+                    x.template start<!C::X_MN>(k.maps, k.X[term], (int64_t)mt * 256 + (int)cr * 128);
 #pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
-                            if (C::GATED) y[h].template start<!C::Y_MN>(k.maps, k.Y[cr], hc);
-                            else y[h].template start<!C::Y_MN>(k.maps, k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
+                    for (int h = 0; h < NH; ++h) {
+                        const int hc = half_col<FORM>(k, nt, hh >= 0 ? hh : h);
+                        if (C::GATED) y[h].template start<!C::Y_MN>(k.maps, k.Y[cr], hc);
+                        else y[h].template start<!C::Y_MN>(k.maps, k.Y[k.two ? (hh >= 0 ? hh : h) : term], hc + (int)cr * 128);
+                    }
+                    for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
+                        if (!warp_wait(empty0 + stage * 8, phase ^ 1, abort_flag, k.status)) {
+                            ok = false;
+                            break;
                         }
-                        for (int kb = 0; kb < k.k_blocks; ++kb, ++it) {
-                            if (!mbar_wait(empty0 + stage * 8, phase ^ 1, abort_flag, k.status)) {
-                                ok = false;
-                                break;
-                            }
+                        stage_bytes[stage] = bytes;
+                        const uint32_t bar = leader_full0 + stage * 8, dst = tiles0 + stage * C::STAGE;
+                        if (chosen) {
                             if (cr == 0) mbar_expect_tx(full0 + stage * 8, 2 * bytes);
-                            stage_bytes[stage] = bytes;
-                            const uint32_t bar = leader_full0 + stage * 8, dst = tiles0 + stage * C::STAGE;
                             load_box<C::X_MN, C::F8>(x, dst, bar);
-                            x.advance(C::BK);
 #pragma unroll
-                            for (int h = 0; h < NH; ++h) {
+                            for (int h = 0; h < NH; ++h)
                                 if (h < nh) load_box<C::Y_MN, C::F8>(y[h], dst + (uint32_t)(C::BOX * (1 + h)), bar);
-                                y[h].advance(C::BK);
-                            }
-                            if (++stage == (uint32_t)S) stage = 0, phase ^= 1;
                         }
+                        __syncwarp();
+                        x.advance(C::BK);
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) y[h].advance(C::BK);
+                        if (++stage == (uint32_t)S) stage = 0, phase ^= 1;
                     }
                 }
-                // Both CTAs' loads of a stage complete on the leader's barrier, so the
-                // leader waits for all of them; the peer hands over how many stages
-                // it loaded, and their bytes.  After an abort the counts may differ by
-                // up to S stages: the leader arms the peer's extra stages for the
-                // peer's half, and stands in for the half the peer never loaded.
-                if (cr == 1) {
-                    for (int s = 0; s < S; ++s)
-                        if ((uint32_t)s < it) st_cluster_u32(mapa_shared(smem_u32((const void *)(peer_bytes + s)), 0), stage_bytes[s]);
-                    st_cluster_u32(mapa_shared(smem_u32((const void *)peer_issued), 0), it);
-                    mbar_arrive_cluster(mapa_shared(handoff_bar, 0));
-                } else {
-                    uint32_t it_peer = it;
-                    if (mbar_wait_cluster(handoff_bar, 0, k.status)) it_peer = *peer_issued;
-                    const uint32_t it_max = it_peer > it ? it_peer : it;
-                    for (uint32_t i = it_peer < it ? it_peer : it; i < it_max; ++i) {
-                        const int s = (int)(i % S);
-                        if (i >= it) mbar_expect_tx(full_bar(s), peer_bytes[s]);  // the peer's half only
-                        else mbar_complete_tx(full_bar(s), stage_bytes[s]);       // the half never loaded
-                    }
-                    for (uint32_t i = it_max > (uint32_t)S ? it_max - S : 0; i < it_max; ++i)
-                        mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status, false);
+            }
+            // Both CTAs' loads of a stage complete on the leader's barrier, so the
+            // leader waits for all of them; the peer hands over how many stages
+            // it loaded, and their bytes.  After an abort the counts may differ by
+            // up to S stages: the leader arms the peer's extra stages for the
+            // peer's half, and stands in for the half the peer never loaded.
+            if (chosen && cr == 1) {
+                for (int s = 0; s < S; ++s)
+                    if ((uint32_t)s < it) st_cluster_u32(mapa_shared(smem_u32((const void *)(peer_bytes + s)), 0), stage_bytes[s]);
+                st_cluster_u32(mapa_shared(smem_u32((const void *)peer_issued), 0), it);
+                mbar_arrive_cluster(mapa_shared(handoff_bar, 0));
+            } else if (chosen) {
+                uint32_t it_peer = it;
+                if (mbar_wait_cluster(handoff_bar, 0, k.status)) it_peer = *peer_issued;
+                const uint32_t it_max = it_peer > it ? it_peer : it;
+                for (uint32_t i = it_peer < it ? it_peer : it; i < it_max; ++i) {
+                    const int s = (int)(i % S);
+                    if (i >= it) mbar_expect_tx(full_bar(s), peer_bytes[s]);  // the peer's half only
+                    else mbar_complete_tx(full_bar(s), stage_bytes[s]);       // the half never loaded
                 }
+                for (uint32_t i = it_max > (uint32_t)S ? it_max - S : 0; i < it_max; ++i)
+                    mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status, false);
             }
         } else if (C::REGS && warp <= C::ISSUERS) {
             // ---------------- MMA issuers (leader CTA only) ----------------
@@ -469,49 +480,45 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
             // issuer, which takes all in order.
             if (cr == 0) {
                 const bool chosen = elect_one();
-                const int runs = (k.k_blocks + C::RUN - 1) / C::RUN;  // accumulators filled per tile
-                const uint32_t mine = pair < k.total ? (uint32_t)((k.total - 1 - pair) / npairs + 1) : 0;
-                const uint32_t total = mine * (uint32_t)runs;
+                const uint32_t mine = pair < k.total ? (uint32_t)((k.total - 1 - pair) / npairs + 1) : 0;  // tiles
                 // Descriptors hold addresses in units of 16 bytes.
                 const uint64_t a0 = operand_step<C::X_MN, C::F8>(smem_u32(tiles), 0);
                 const uint64_t b0 = operand_step<C::Y_MN, C::F8>(smem_u32(tiles) + C::BOX, 0);
                 constexpr uint32_t A_STEP = 2, B_STEP = !C::Y_MN ? 2 : C::F8 ? 256 : 128;
-                uint32_t stage = 0, phase = 0, in_tile = 0;  // of run `it`
-                auto skip = [&](int n) {
-                    stage += (uint32_t)n;
-                    while (stage >= (uint32_t)S) stage -= S, phase ^= 1;
-                };
-                auto length = [&]() -> int {
-                    const int left = k.k_blocks - (int)in_tile * C::RUN;
-                    return left < C::RUN ? left : C::RUN;
-                };
+                uint32_t stage = 0, phase = 0, it = 0;  // `it`: accumulators filled so far
                 bool ok = true;
-                for (uint32_t it = 0; it < total && ok; ++it) {
-                    const int n = length();
-                    const int buf = (int)(it & 1);
-                    if (C::ISSUERS == 1 || buf == warp - 1) {
-                        const uint32_t d = tmem_base + (uint32_t)(buf * 256);
-                        if (!warp_wait(acce_bar(buf), ((it >> 1) & 1) ^ 1, abort_flag, k.status)) break;
-                        uint32_t s = stage, p = phase;
-                        for (int kb = 0; kb < n; ++kb) {
-                            if (!warp_wait(full_bar((int)s), p, abort_flag, k.status)) {
+                for (uint32_t t = 0; t < mine && ok; ++t) {
+                    int n = 0;
+                    for (int r = 0, kb0 = 0; kb0 < k.k_blocks && ok; ++r, kb0 += n, ++it) {
+                        n = C::run(r, k.k_blocks - kb0);
+                        const int buf = (int)(it & 1);
+                        if (C::ISSUERS == 1 || buf == warp - 1) {
+                            const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+                            if (!warp_wait(acce_bar(buf), ((it >> 1) & 1) ^ 1, abort_flag, k.status)) {
                                 ok = false;
                                 break;
                             }
-                            fence_after();
-                            const uint64_t a = a0 + s * (C::STAGE / 16), b = b0 + s * (C::STAGE / 16);
-                            if (chosen) {
+                            uint32_t s = stage, p = phase;
+                            for (int kb = 0; kb < n; ++kb) {
+                                if (!warp_wait(full_bar((int)s), p, abort_flag, k.status)) {
+                                    ok = false;
+                                    break;
+                                }
+                                fence_after();
+                                const uint64_t a = a0 + s * (C::STAGE / 16), b = b0 + s * (C::STAGE / 16);
+                                if (chosen) {
 #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) pair_mma<FORM>(d, a + kk * A_STEP, b + kk * B_STEP, kb > 0 || kk > 0);
-                                if (kb == n - 1) umma2_commit_both(accf_bar(buf));
-                                umma2_commit_both(empty_bar((int)s));
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        pair_mma<FORM>(d, a + kk * A_STEP, b + kk * B_STEP, kb > 0 || kk > 0);
+                                    if (kb == n - 1) umma2_commit_both(accf_bar(buf));
+                                    umma2_commit_both(empty_bar((int)s));
+                                }
+                                __syncwarp();
+                                if (++s == (uint32_t)S) s = 0, p ^= 1;
                             }
-                            __syncwarp();
-                            if (++s == (uint32_t)S) s = 0, p ^= 1;
                         }
+                        for (stage += (uint32_t)n; stage >= (uint32_t)S; stage -= S) phase ^= 1;
                     }
-                    skip(n);
-                    if (++in_tile == (uint32_t)runs) in_tile = 0;
                 }
                 if (chosen) {
                     umma2_commit_both(drain_bar);
@@ -521,26 +528,33 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
             }
         } else if (!C::REGS && warp == 1) {
             // ---------------- MMA issuer (leader CTA only) ----------------
-            if (lane == 0 && cr == 0) {
+            if (cr == 0) {
+                const bool chosen = elect_one();
                 const int k_total = k.terms * k.k_blocks;
-                uint32_t it = 0;
-                uint32_t fills[2] = {0, 0};
+                uint32_t it = 0, fills0 = 0, fills1 = 0;
                 bool ok = true;
-                // The four MMAs of the k-block in stage s, half h of its Y, into buffer buf.
-                auto issue = [&](int s, int buf, int h, bool first) {
-                    const uint32_t a = smem_u32(tiles + s * C::STAGE), b = a + (uint32_t)(C::BOX * (1 + h));
+                const uint64_t a0 = operand_step<C::X_MN, false>(smem_u32(tiles), 0);
+                const uint64_t b0 = operand_step<C::Y_MN, false>(smem_u32(tiles) + C::BOX, 0);
+                constexpr uint32_t A_STEP = C::X_MN ? 128 : 2, B_STEP = C::Y_MN ? 128 : 2;
+                // The four MMAs of the k-block in stage s, half h of its Y, into buffer
+                // h; `done`: and the stage may be filled again.
+                auto issue = [&](uint32_t s, int h, bool first, bool done) {
+                    const uint64_t a = a0 + s * (C::STAGE / 16), b = b0 + s * (C::STAGE / 16) + (uint32_t)(h * (C::BOX / 16));
+                    if (chosen) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        pair_mma<FORM>(tmem_base + (uint32_t)(buf * 256), operand_step<C::X_MN, C::F8>(a, kk),
-                                       operand_step<C::Y_MN, C::F8>(b, kk), !first || kk > 0);
+                        for (int kk = 0; kk < 4; ++kk)
+                            pair_mma<FORM>(tmem_base + (uint32_t)(h * 256), a + kk * A_STEP, b + kk * B_STEP, !first || kk > 0);
+                        if (done) umma2_commit_both(empty_bar((int)s));
+                    }
+                    __syncwarp();
                 };
-                auto wait_free = [&](int buf) -> bool {
-                    if (!mbar_wait(acce_bar(buf), (fills[buf] & 1) ^ 1, abort_flag, k.status)) return false;
+                auto wait_free = [&](int buf, uint32_t fills) -> bool {
+                    if (!warp_wait(acce_bar(buf), (fills & 1) ^ 1, abort_flag, k.status)) return false;
                     fence_after();
                     return true;
                 };
                 auto wait_stage = [&](uint32_t i) -> bool {
-                    if (!mbar_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status)) return false;
+                    if (!warp_wait(full_bar((int)(i % S)), (i / S) & 1, abort_flag, k.status)) return false;
                     fence_after();
                     return true;
                 };
@@ -550,23 +564,18 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                     // catches up on the same stages.
                     const bool half = t >= k.half_from;
                     const int R = k_total < S ? k_total : S;
-                    if (!wait_free(0)) break;
+                    if (!wait_free(0, fills0)) break;
                     for (int kb = 0; kb < R; ++kb) {
                         if (!wait_stage(it + (uint32_t)kb)) {
                             ok = false;
                             break;
                         }
-                        issue((int)((it + (uint32_t)kb) % S), 0, 0, kb == 0);
-                        if (half) umma2_commit_both(empty_bar((int)((it + (uint32_t)kb) % S)));
+                        issue((it + (uint32_t)kb) % S, 0, kb == 0, half);
                     }
                     if (!ok) break;
                     if (!half) {
-                        if (!wait_free(1)) break;
-                        for (int kb = 0; kb < R; ++kb) {
-                            const int s = (int)((it + (uint32_t)kb) % S);
-                            issue(s, 1, NH - 1, kb == 0);
-                            umma2_commit_both(empty_bar(s));
-                        }
+                        if (!wait_free(1, fills1)) break;
+                        for (int kb = 0; kb < R; ++kb) issue((it + (uint32_t)kb) % S, NH - 1, kb == 0, true);
                     }
                     it += (uint32_t)R;
                     for (int kb = R; kb < k_total; ++kb, ++it) {
@@ -574,20 +583,23 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                             ok = false;
                             break;
                         }
-                        issue(it % S, 0, 0, false);
-                        if (!half) issue(it % S, 1, NH - 1, false);
-                        umma2_commit_both(empty_bar(it % S));
+                        issue(it % S, 0, false, half);
+                        if (!half) issue(it % S, NH - 1, false, true);
                     }
                     if (!ok) break;
-                    umma2_commit_both(accf_bar(0));
-                    ++fills[0];
-                    if (!half) {
-                        umma2_commit_both(accf_bar(1));
-                        ++fills[1];
+                    if (chosen) {
+                        umma2_commit_both(accf_bar(0));
+                        if (!half) umma2_commit_both(accf_bar(1));
                     }
+                    __syncwarp();
+                    ++fills0;
+                    if (!half) ++fills1;
                 }
-                umma2_commit_both(drain_bar);
-                mbar_wait(drain_bar, 0, abort_flag, k.status, false);
+                if (chosen) {
+                    umma2_commit_both(drain_bar);
+                    mbar_wait(drain_bar, 0, abort_flag, k.status, false);
+                }
+                __syncwarp();
             }
         } else if constexpr (C::F8) {
             // ---------------- scales (both CTAs): a lane has rows lane + 0, 32, 64, 96 ----------------
@@ -680,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
                 float acc[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-                for (int kb = 0; kb < k.k_blocks; kb += C::RUN, ++fill) {
+                for (int kb = 0, run = 0; kb < k.k_blocks; kb += C::run(run, k.k_blocks), ++run, ++fill) {
                     const int b = fill & 1, s = fill % kScaleSlots;
                     int got = 1;
                     if (lane == 0)

@@ -189,31 +189,33 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
 
     if (warp == 0) {
         // ---------------- TMA ----------------
-        if (lane == 0) {
-            Cursor x, y[2];
-            int term = kb0 / k.k_blocks, kb = kb0 % k.k_blocks;
-            auto start = [&](int at) {
-                if (term >= k.terms) return;
-                x.template start<!C::X_MN>(k.maps, k.X[term], row0);
-                x.seek(at * C::BK);
-                if (FORM == kGated) {
-                    y[0].template start<false>(k.maps, k.Y[0], col0);
-                    y[1].template start<false>(k.maps, k.Y[1], col0);
-                    y[1].seek(at * C::BK);
-                } else {
-                    y[0].template start<!C::Y_MN>(k.maps, k.Y[k.two ? which : term], col0);
-                }
-                y[0].seek(at * C::BK);
-            };
-            start(kb);
-            const int n = kb1 - kb0;
-            int it = 0;
-            uint32_t stage = 0, phase = 0, dst = smem_u32(tiles);
-            const uint32_t full0 = full_bar(0), empty0 = empty_bar(0);
-            const uint32_t row_bytes = (uint32_t)k.X[0].brows * 128;
-            for (; it < n; ++it) {
-                if (!mbar_wait(empty0 + stage * 8, phase ^ 1, abort_flag, k.status)) break;
-                const uint32_t bar = full0 + stage * 8;
+        const bool chosen = elect_one();
+        Cursor x, y[2];
+        int term = kb0 / k.k_blocks, kb = kb0 % k.k_blocks;
+        auto start = [&](int at) {
+            if (term >= k.terms) return;
+            x.template start<!C::X_MN>(k.maps, k.X[term], row0);
+            x.seek(at * C::BK);
+            if (FORM == kGated) {
+                y[0].template start<false>(k.maps, k.Y[0], col0);
+                y[1].template start<false>(k.maps, k.Y[1], col0);
+                y[1].seek(at * C::BK);
+            } else {
+                y[0].template start<!C::Y_MN>(k.maps, k.Y[k.two ? which : term], col0);
+            }
+            y[0].seek(at * C::BK);
+        };
+        start(kb);
+        const int n = kb1 - kb0;
+        int it = 0;
+        uint32_t stage = 0, phase = 0, dst = smem_u32(tiles);
+        const uint32_t full0 = full_bar(0), empty0 = empty_bar(0);
+        const uint32_t row_bytes = (uint32_t)k.X[0].brows * 128;
+        for (; it < n; ++it) {
+            if (!warp_wait(empty0 + stage * 8, phase ^ 1, abort_flag, k.status)) break;
+            const uint32_t bar = full0 + stage * 8;
+            const uint32_t to = dst + x_bytes;
+            if (chosen) {
                 mbar_expect_tx(bar, stage_bytes);
                 if (C::X_MN) {
                     tma_load_2d(dst, x.map, bar, x.fixed, x.at);
@@ -224,11 +226,9 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
                     for (int b = 0; b < k.x_boxes; ++b)
                         tma_load_2d(dst + (uint32_t)b * row_bytes, x.map + b * k.X[0].b1, bar, x.at, 0);
                 }
-                const uint32_t to = dst + x_bytes;
                 if (FORM == kGated) {
                     tma_load_2d(to, y[0].map, bar, y[0].fixed, y[0].at);
                     tma_load_2d(to + 8192, y[1].map, bar, y[1].fixed, y[1].at);
-                    y[1].advance(C::BK);
                 } else if (!C::Y_MN) {
                     tma_load_2d(to, y[0].map, bar, y[0].at, y[0].fixed);
                 } else if (C::F8) {
@@ -237,20 +237,22 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
                     tma_load_2d(to, y[0].map, bar, y[0].fixed, y[0].at);
                     tma_load_2d(to + 8192, y[0].map, bar, y[0].fixed + 64, y[0].at);
                 }
-                x.advance(C::BK);
-                y[0].advance(C::BK);
-                dst += stage_bytes;
-                if (++stage == (uint32_t)S) stage = 0, phase ^= 1, dst = smem_u32(tiles);
-                if (++kb == k.k_blocks) {
-                    kb = 0;
-                    ++term;
-                    start(0);
-                }
             }
-            // never leave with a load in flight
-            for (int i = it > S ? it - S : 0; i < it; ++i)
-                mbar_wait(full_bar(i % S), (i / S) & 1, abort_flag, k.status, false);
+            __syncwarp();
+            x.advance(C::BK);
+            y[0].advance(C::BK);
+            if (FORM == kGated) y[1].advance(C::BK);
+            dst += stage_bytes;
+            if (++stage == (uint32_t)S) stage = 0, phase ^= 1, dst = smem_u32(tiles);
+            if (++kb == k.k_blocks) {
+                kb = 0;
+                ++term;
+                start(0);
+            }
         }
+        // never leave with a load in flight
+        for (int i = it > S ? it - S : 0; chosen && i < it; ++i)
+            mbar_wait(full_bar(i % S), (i / S) & 1, abort_flag, k.status, false);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA ----------------
