@@ -43,6 +43,7 @@ template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
+    static constexpr bool kHalf = true;  // a value's bits are the upper half of an fp32 value's
     uint32_t w[4];
     __device__ __forceinline__ void vec(const __nv_bfloat16 *p) {
         const uint4 q = *reinterpret_cast<const uint4 *>(p);
@@ -61,17 +62,14 @@ struct Raw8<__nv_bfloat16> {
     }
     // The largest magnitude's bits as fp32 (infinities and NaN above all others).
     __device__ __forceinline__ uint32_t top() const {
-        uint32_t hi = 0, lo = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hi = max(hi, w[i] & 0x7FFF0000u);
-            lo = max(lo, w[i] << 16 & 0x7FFF0000u);
-        }
-        return max(hi, lo);
+        const uint32_t m = 0x7FFF7FFFu;
+        const uint32_t both = __vmaxu2(__vmaxu2(w[0] & m, w[1] & m), __vmaxu2(w[2] & m, w[3] & m));
+        return max(both & 0xFFFF0000u, both << 16);
     }
 };
 template <>
 struct Raw8<float> {
+    static constexpr bool kHalf = false;
     float f[8];
     __device__ __forceinline__ void vec(const float *p) {
         const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
@@ -209,17 +207,38 @@ __global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant
             if (c < k.bcols && piece_in_bounds<VEC>(k.status, row * k.src_ld + c, k.bcols - c, k.brows * k.src_ld))
                 load8<VEC>(src + c, k.bcols - c, &raw[i]);
         }
+        // The blocks' largest magnitudes over 16 lanes; those of bf16 values two to a
+        // register.
+        uint32_t top[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) top[i] = raw[i].top();
+        if (Raw8<T>::kHalf) {
+#pragma unroll
+            for (int i = 0; i < kPieces; i += 2) {
+                uint32_t two = top[i] | top[i + 1] >> 16;
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) two = __vmaxu2(two, __shfl_xor_sync(0xFFFFFFFFu, two, d));
+                top[i] = two & 0xFFFF0000u;
+                top[i + 1] = two << 16;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) top[i] = max(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
+        }
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) most = max(most, top[i]);
+        const bool all_finite = !__any_sync(0xFFFFFFFFu, most >= 0x7F800000u);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int64_t c = c0 + i * 256 + lane * 8;
-            uint32_t top = raw[i].top();
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
             float v[8];
             raw[i].get(v);
-            const bool finite = top < 0x7F800000u;
-            float amax = __uint_as_float(top);
-            if (__any_sync(0xFFFFFFFFu, !finite)) {  // the largest finite one, then
+            const bool finite = top[i] < 0x7F800000u;
+            float amax = __uint_as_float(top[i]);
+            if (!all_finite) {  // the largest finite one, where that is another
                 float m = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[j]));
@@ -241,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_constant__ ToK k) {
     shmm_pdl::pdl_enter();
-    __shared__ float part[kThreads / 32];
+    __shared__ uint32_t part[kThreads / 32];
     const int bi = blockIdx.z / k.b1, bj = blockIdx.z % k.b1;
     const int x = threadIdx.x % 16, y = threadIdx.x / 16;
     const T *src = static_cast<const T *>(k.src[blockIdx.z]);
@@ -249,7 +268,6 @@ __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_const
     for (int64_t cb = blockIdx.y; cb < k.per; cb += gridDim.y) {
         const int64_t c = cb * kBlock + x * 8, r0 = rb * kBlock + y;
         Raw8<T> raw[8];
-        float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 16 * i;
@@ -258,20 +276,35 @@ __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_const
                 piece_in_bounds<VEC>(k.status, r * k.src_ld + c, k.bcols - c, k.brows * k.src_ld))
                 load8<VEC>(src + r * k.src_ld + c, k.bcols - c, &raw[i]);
         }
+        // The largest magnitude's bits over the CTA; with an infinity or NaN among the
+        // values, those of the largest finite one.
+        auto over_cta = [&](uint32_t m) -> uint32_t {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float v[8];
-            raw[i].get(v);
+            for (int d = 1; d < 32; d *= 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            __syncthreads();  // the last values have been read
+            if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
+            __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[j]));
+            for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
+            return m;
+        };
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, raw[i].top());
+        top = over_cta(top);
+        const bool finite = top < 0x7F800000u;
+        if (!finite) {
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v[8];
+                raw[i].get(v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(finite_abs(v[j])));
+            }
+            top = over_cta(top);
         }
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        __syncthreads();  // the last block's partial maxima have been read
-        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = amax;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) amax = fmaxf(amax, part[i]);
+        const float amax = __uint_as_float(top);
         const int e = scale_exp(amax);
         const int64_t s_at = (bi * ((k.brows + kBlock - 1) / kBlock) + rb) * k.scale_ld + (int64_t)bj * k.per + cb;
         if (threadIdx.x == 0 && in_bounds(k.status, s_at, 1, k.scale_n)) k.scale[s_at] = pow2(e);
@@ -282,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_const
             {
                 float v[8];
                 raw[i].get(v);
-                store8_e4m3<VEC>(k.codes + at, k.bcols - c, v, pow2(-e), false);
+                store8_e4m3<VEC>(k.codes + at, k.bcols - c, v, pow2(-e), finite);
             }
         }
     }
