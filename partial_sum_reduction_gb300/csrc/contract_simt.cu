@@ -84,26 +84,31 @@ __device__ __forceinline__ float fetch(const Op<CAP> &o, int64_t r, int64_t c, i
 }
 
 // N elements of one thread's part of a piece: element i at result index a0 + i *
-// da, contracted index k0 + i * dk (0 past the ends), stored as [result,
-// contracted] or, MAJOR_K, the other way round.  One block: the addresses are
-// independent of one another and of any table, so the loads go out together.
-template <typename T, int CAP, int N>
-__device__ __forceinline__ void fetch_part(const Op<CAP> &o, bool major_k, int64_t a0, int da, int64_t a_end, int64_t k0,
-                                           int dk, int64_t k_end, float *v, int *status) {
+// DA, contracted index k0 + i * DK (one of the two is 0; 0 past the ends), stored
+// as [result, contracted] or, MAJOR_K, the other way round.  One block: addresses
+// a stride apart, so the loads go out together at an add or two each.
+template <typename T, int CAP, int N, bool MAJOR_K, int DA, int DK>
+__device__ __forceinline__ void fetch_part(const Op<CAP> &o, int64_t a0, int64_t a_end, int64_t k0, int64_t k_end, float *v,
+                                           int *status) {
+    static_assert((DA == 0) != (DK == 0), "one index moves");
     if (o.b0 * o.b1 == 1) {
-        const T *base = static_cast<const T *>(o.at[0]);
-        const int64_t n = (o.brows - 1) * o.ld + o.bcols;
+        // how many of the N exist
+        const int64_t room = DA ? (a_end - a0 + DA - 1) / (DA ? DA : 1) : (k_end - k0 + DK - 1) / (DK ? DK : 1);
+        const int count = (DA ? k0 < k_end : a0 < a_end) ? (room < N ? (int)room : N) : 0;
+        const int64_t r0 = MAJOR_K ? k0 : a0, c0 = MAJOR_K ? a0 : k0;
+        const uint32_t step = (uint32_t)(MAJOR_K ? (DA ? DA : DK * o.ld) : (DA ? DA * o.ld : DK));  // N of them: below 2^31
+        const int64_t at0 = r0 * o.ld + c0, n = (o.brows - 1) * o.ld + o.bcols;
+        const T *p = static_cast<const T *>(o.at[0]) + at0;
         T raw[N];
         float sc[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t a = a0 + (int64_t)i * da, kk = k0 + (int64_t)i * dk;
-            const int64_t r = major_k ? kk : a, c = major_k ? a : kk, at = r * o.ld + c;
-            const bool in = a < a_end && kk < k_end && in_bounds(status, at, 1, n);
+            const bool in = i < count && in_bounds(status, at0 + (int64_t)i * step, 1, n);
             raw[i] = T(0);
             sc[i] = 0.0f;
-            if (in) raw[i] = base[at];
+            if (in) raw[i] = p[(uint32_t)i * step];
             if (sizeof(T) == 1 && in) {
+                const int64_t r = r0 + i * (MAJOR_K ? DK : DA), c = c0 + i * (MAJOR_K ? DA : DK);
                 const int64_t s = (o.scale_rows == 1 ? r : r / 128) * o.scale_ld + c / 128;
                 if (in_bounds(status, s, 1, (o.brows + o.scale_rows - 1) / o.scale_rows * o.scale_ld)) sc[i] = o.scale[0][s];
             }
@@ -113,8 +118,8 @@ __device__ __forceinline__ void fetch_part(const Op<CAP> &o, bool major_k, int64
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t a = a0 + (int64_t)i * da, kk = k0 + (int64_t)i * dk;
-            v[i] = a < a_end && kk < k_end ? fetch<T>(o, major_k ? kk : a, major_k ? a : kk, status) : 0.0f;
+            const int64_t a = a0 + (int64_t)i * DA, kk = k0 + (int64_t)i * DK;
+            v[i] = a < a_end && kk < k_end ? fetch<T>(o, MAJOR_K ? kk : a, MAJOR_K ? a : kk, status) : 0.0f;
         }
     }
 }
@@ -179,13 +184,13 @@ __global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_co
     auto ask = [&](int64_t piece) {
         const int t = piece >= per_term ? 1 : 0;
         const int64_t k0 = (piece - t * per_term) * TK;
-        if (k.x_t) fetch_part<T, CAP, PX>(k.X[t], true, m0 + lane, 0, k.M, k0 + warp, kThreads / TM, k.Kd, xr, k.status);
-        else fetch_part<T, CAP, PX>(k.X[t], false, m0 + warp, kThreads / TK, k.M, k0 + lane, 0, k.Kd, xr, k.status);
+        if (k.x_t) fetch_part<T, CAP, PX, true, 0, kThreads / TM>(k.X[t], m0 + lane, k.M, k0 + warp, k.Kd, xr, k.status);
+        else fetch_part<T, CAP, PX, false, kThreads / TK, 0>(k.X[t], m0 + warp, k.M, k0 + lane, k.Kd, xr, k.status);
 #pragma unroll
         for (int y = 0; y < NY; ++y) {
             const Op<CAP> &o = k.Y[GATED ? y : t];
-            if (k.y_t) fetch_part<T, CAP, PY>(o, false, n0 + warp, kThreads / TK, n1, k0 + lane, 0, k.Kd, yr[y], k.status);
-            else fetch_part<T, CAP, PY>(o, true, n0 + threadIdx.x % TN, 0, n1, k0 + threadIdx.x / TN, kThreads / TN, k.Kd, yr[y], k.status);
+            if (k.y_t) fetch_part<T, CAP, PY, false, kThreads / TK, 0>(o, n0 + warp, n1, k0 + lane, k.Kd, yr[y], k.status);
+            else fetch_part<T, CAP, PY, true, 0, kThreads / TN>(o, n0 + threadIdx.x % TN, n1, k0 + threadIdx.x / TN, k.Kd, yr[y], k.status);
         }
     };
 
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_co
             }
         __syncthreads();
         if (piece + 1 < pieces) ask(piece + 1);
-#pragma unroll
+#pragma unroll 16
         for (int kk = 0; kk < TK; ++kk) {
             const float4 x4 = *reinterpret_cast<const float4 *>(&xs[kk][warp * 4]);
             const float x[4] = {x4.x, x4.y, x4.z, x4.w};
