@@ -606,9 +606,8 @@ shmm_status_t shmm_adapters_backward(const shmm_plan_t *plan, int n_adapters, in
  * that rounding is the only one.  Infinities and NaN become NaN.  The calls
  * that read blocks take any finite scale.
  *   x        [rows, cols], dtype F32 or BF16, 16-byte aligned
- *   codes    out: [rows, cols] bytes, 16-byte aligned; shares no byte with x
- *            (UNSUPPORTED)
- *   scales   out: fp32
+ *   codes    out: [rows, cols] bytes, 16-byte aligned
+ *   scales   out: fp32; x, codes and scales share no byte (UNSUPPORTED)
  * No rows or no columns: nothing is written.
  * Errors: NULL, ALIGN, SHAPE (negative sizes, rows of 2^31 or more, cols of
  * 2^26 or more, block_rows), DTYPE, UNSUPPORTED, CUDA. */
@@ -641,8 +640,10 @@ shmm_status_t shmm_dequantize(int64_t rows, int64_t cols, shmm_dtype_t dtype, in
  * The tensor cores take shards whose rows are whole 16-byte pieces (columns of
  * the boxes of A and B multiples of 16, of C whole 16-byte pieces too) and, where a dim is
  * split, multiples of 128 along it, up to 16 ranks; other plans run on the
- * CUDA cores (SHMM_FLAG_SIMT: all).  Other flags do not matter, but for
- * SHMM_FLAG_GELU, which is refused.
+ * CUDA cores (SHMM_FLAG_SIMT: all).  Up to 128 rows may also be split over the
+ * ranks in multiples of 8.  Other flags do not matter, but for SHMM_FLAG_GELU,
+ * which is refused; shmm_plan_set_sm_limit holds for products large enough for
+ * CTA pairs.
  * One input gives one result.
  * Errors: NULL, ALIGN, DTYPE (not an E4M3 plan), SHAPE (I of 2^31 or more, J or
  * K of 2^22 or more), UNSUPPORTED, CUDA. */
@@ -668,7 +669,8 @@ shmm_status_t shmm_scaled_backward_workspace_size(const shmm_plan_t *plan, size_
  *   workspace device memory of >= shmm_scaled_backward_workspace_size() bytes,
  *             256-byte aligned; nothing in it needs to start at zero, and
  *             calls that overlap on the GPU need one each
- * The outputs share no byte with an input (UNSUPPORTED).  No rows: dB is zero.
+ * The outputs share no byte with an input or one another (UNSUPPORTED).  No
+ * rows: dB is zero.
  * Errors: those of shmm_run_scaled, and NOMEM (workspace). */
 shmm_status_t shmm_scaled_backward(const shmm_plan_t *plan, const void *const *dC_r, const void *const *A_r,
                                    const float *const *A_scale_r, const void *const *B_r,
@@ -702,8 +704,8 @@ typedef struct {
  *   gate_r[N], up_r[N]  in: box SHMM_TENSOR_B
  *   C_r[N]      out: box SHMM_TENSOR_C
  *   saved       out: what the backward call needs, or NULL
- * The outputs share no byte with an input (UNSUPPORTED).  bf16 plans run on the
- * tensor cores where shmm_run_scaled's sizes would (columns of the boxes
+ * The outputs share no byte with an input or one another (UNSUPPORTED).  bf16
+ * plans run on the tensor cores where shmm_run_scaled's sizes would (columns of the boxes
  * multiples of 8; of C 16 to keep 8 bits), fp32 and other plans on the CUDA
  * cores.  Flags: as there.
  * Errors: NULL, ALIGN, DTYPE (in_dtype not out_dtype, E4M3; saved->dtype),
@@ -735,7 +737,7 @@ shmm_status_t shmm_gated_backward_workspace_size(const shmm_plan_t *plan, size_t
  *                   bytes, 256-byte aligned; nothing in it needs to start at
  *                   zero, and calls that overlap on the GPU need one each
  * All in the plan's type, rounded once.  The outputs share no byte with an
- * input (UNSUPPORTED).  No rows: dgate and dup are zero.
+ * input or one another (UNSUPPORTED).  No rows: dgate and dup are zero.
  * Errors: those of shmm_gated_forward, and NOMEM (workspace). */
 shmm_status_t shmm_gated_backward(const shmm_plan_t *plan, int activation, const void *const *dC_r,
                                   const void *const *A_r, const void *const *gate_r, const void *const *up_r,

@@ -707,7 +707,7 @@ static shmm_status_t check_apart(const char *fn, const std::vector<Span> &out, c
             return fail(SHMM_ERR_UNSUPPORTED, std::string(fn) + ": " + out_name + "[" + std::to_string(o.rank) +
                                                   "] overlaps " + in_name + "[" +
                                                   std::to_string(reach[before - 1].rank) +
-                                                  "], which is read while it is written");
+                                                  "], which is read or written at the same time");
     }
     return SHMM_OK;
 }
@@ -1280,7 +1280,8 @@ static std::vector<Span> scale_spans(const shmm_plan_t *p, const float *const *a
     return v;
 }
 
-// A named set of buffers; every output of a call is compared with every input.
+// A named set of buffers; every output of a call is compared with every input
+// and every other output.
 struct NamedSpans {
     const char *name;
     std::vector<Span> at;
@@ -1289,6 +1290,11 @@ static shmm_status_t check_all_apart(const char *fn, const std::vector<NamedSpan
     for (const NamedSpans &o : outs)
         for (const NamedSpans &i : ins) {
             const shmm_status_t st = check_apart(fn, o.at, o.name, i.at, i.name);
+            if (st != SHMM_OK) return st;
+        }
+    for (size_t i = 1; i < outs.size(); ++i)
+        for (size_t j = 0; j < i; ++j) {
+            const shmm_status_t st = check_apart(fn, outs[i].at, outs[i].name, outs[j].at, outs[j].name);
             if (st != SHMM_OK) return st;
         }
     return SHMM_OK;

@@ -168,8 +168,7 @@ int launch_contract(const ContractArgs &a, int *status, void *stream, std::strin
     memset(&k, 0, sizeof k);
     Maps m = {&k, fn};
     const bool x_mn = form == kTN, y_mn = form == kGated || form == kGated8 || form == kTN || form == kNN8;
-    int sms = num_sms();
-    if (a.max_sms > 0 && a.max_sms < sms) sms = a.max_sms;
+    const int sms = num_sms();  // whatever the plan's limit: which kernel and how many parts set the sums' order
     const bool small = use_small(a, form, sms);
     k.x_boxes = 1;
     k.x_rows = 128;

@@ -137,6 +137,7 @@ def test_refusals(name, args, status):
 def test_scales_over_the_values_are_refused():
     assert _call("shmm_quantize", scales=4096 + 64) == m.ERR_UNSUPPORTED
     assert _call("shmm_dequantize", scales=4096 + 64) == m.ERR_UNSUPPORTED
+    assert _call("shmm_quantize", scales=(1 << 20) + 1020) == m.ERR_UNSUPPORTED
 
 
 def test_injected_failure(monkeypatch):

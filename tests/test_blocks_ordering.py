@@ -1,0 +1,136 @@
+"""The order of the 8-bit and gated operators' accesses, within a kernel and
+between calls: repeated calls on freshly copied inputs, calls on several streams
+at once, early starts against plain stream order, a limit on the SMs."""
+import pytest
+import torch
+
+import partial_sum_reduction_gb300 as s
+from block_util import LAYOUTS, cut, gen, normal
+
+
+def gated_step(layout, I, J, K, kept, seed=0):
+    """(a call of the whole training step on fresh copies, its results)."""
+    mesh, sa, sb, sc = LAYOUTS[layout]
+    plan = s.Plan(mesh, sa, sb, sc, I, J, K, "bf16", "bf16")
+    g = gen(seed)
+    full = [(normal(g, *e) / d).bfloat16() for e, d in (((I, J), 1), ((J, K), J ** 0.5), ((J, K), J ** 0.5), ((I, K), 20))]
+    tensors = (s.TENSOR_A, s.TENSOR_B, s.TENSOR_B, s.TENSOR_C)
+    host = [[t.cpu().pin_memory() for t in cut(plan, k, f)] for k, f in zip(tensors, full)]
+
+    def call(stream=None):
+        A, gate, up, dC = ([t.cuda() for t in ts] for ts in host)
+        C, saved = s.helpers.alloc(plan, s.TENSOR_C), None if kept == "none" else s.helpers.gated_saved(plan, kept)
+        plan.gated_forward(A, gate, up, C, saved=saved, stream=stream)
+        if saved is None:
+            return C
+        outs = [s.helpers.alloc(plan, t) for t in tensors[:3]]
+        plan.gated_backward(dC, A, gate, up, saved, *outs, s.helpers.gated_workspace(plan), stream=stream)
+        return sum(outs, C)
+    return plan, call
+
+
+def scaled_step(layout, I, J, K, seed=0):
+    mesh, sa, sb, sc = LAYOUTS[layout]
+    plan = s.Plan(mesh, sa, sb, sc, I, J, K, "e4m3", "bf16")
+    g = gen(seed)
+    full = [(normal(g, *e) / d).bfloat16() for e, d in (((I, J), 1), ((J, K), J ** 0.5), ((I, K), 20))]
+    host = [[t.cpu().pin_memory() for t in cut(plan, k, f)] for k, f in zip((s.TENSOR_A, s.TENSOR_B, s.TENSOR_C), full)]
+
+    def call(stream=None):
+        A, B = ([s.helpers.quantize(t.cuda(), br) for t in ts] for ts, br in ((host[0], 1), (host[1], 128)))
+        ops = [[x[i] for x in ts] for ts in (A, B) for i in (0, 1)]
+        dC, C = [t.cuda() for t in host[2]], s.helpers.alloc(plan, s.TENSOR_C)
+        plan.run_scaled(*ops, C, stream=stream)
+        dA, dB = (s.helpers.alloc(plan, t, dtype=torch.bfloat16) for t in (s.TENSOR_A, s.TENSOR_B))
+        plan.scaled_backward(dC, *ops, dA, dB, s.helpers.scaled_workspace(plan), stream=stream)
+        return C + dA + dB
+    return plan, call
+
+
+STEPS = [("gated", "columns", 512, 1024, 2048, "e4m3"), ("gated", "all_reduce", 1024, 512, 1024, "bf16"),
+         ("gated", "whole", 16, 4096, 2048, "bf16"), ("gated", "rows", 32, 4096, 4096, "none"), ("gated", "whole", 515, 1024, 1408, "e4m3"),
+         ("scaled", "columns", 512, 1024, 2048), ("scaled", "whole", 16, 4096, 2048), ("scaled", "whole", 1000, 1040, 2032),
+         ("scaled", "grid", 2048, 2048, 2048)]
+
+
+def step(case, seed=0):
+    return (gated_step if case[0] == "gated" else scaled_step)(*case[1:], seed=seed)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(map(str, c)))
+def test_many_calls_give_one_result(case):
+    _, call = step(case)
+    first = call()
+    for _ in range(25):
+        assert all(torch.equal(a, b) for a, b in zip(call(), first))
+
+
+@pytest.mark.gpu
+def test_several_streams_at_once():
+    """Kernels of different shapes side by side: each step's results are those
+    of the step alone."""
+    made = [step(c, seed=i) for i, c in enumerate(STEPS[:8:2])]
+    alone = [call() for _, call in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(6):
+        got = []
+        for (_, call), st in zip(made, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                got.append(call())
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(map(str, c)))
+def test_early_starts_change_nothing(case, monkeypatch):
+    _, call = step(case)
+    first = call()
+    monkeypatch.setenv("SHMM_PDL", "0")
+    assert all(torch.equal(a, b) for a, b in zip(call(), first))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(map(str, c)))
+def test_a_limit_on_the_sms_changes_no_result(case):
+    plan, call = step(case)
+    first = call()
+    for limit in (2, 40):
+        plan.set_sm_limit(limit)
+        assert all(torch.equal(a, b) for a, b in zip(call(), first))
+
+
+@pytest.mark.gpu
+def test_beside_the_plans_own_matmuls():
+    """The gated half, the plan's own matmul and a LayerNorm in turn on one
+    stream, over the same buffers each time: nothing starts before what it reads
+    is there."""
+    T, D, F = 256, 512, 1024
+    first = s.Plan("{X:1}", "I,J", "J,K", "I,K", T, D, F, "bf16", "bf16")
+    second = s.Plan("{X:1}", "I,J", "J,K", "I,K", T, F, D, "bf16", "bf16")
+    g = gen(1)
+    x0 = normal(g, T, D).bfloat16()
+    gate, up = ((normal(g, D, F) / D ** 0.5).bfloat16() for _ in range(2))
+    down = (normal(g, F, D) / F ** 0.5).bfloat16()
+    gamma, beta = torch.ones(D, device="cuda"), torch.zeros(D, device="cuda")
+
+    def run(sync):
+        x, h, y = x0.clone(), torch.empty(T, F, device="cuda", dtype=torch.bfloat16), torch.empty_like(x0)
+        for _ in range(12):
+            first.gated_forward([x], [gate], [up], [h])
+            if sync:
+                torch.cuda.synchronize()
+            second.run([h], [down], [y])
+            if sync:
+                torch.cuda.synchronize()
+            s.shmm_layernorm(y, gamma, beta, x)
+            if sync:
+                torch.cuda.synchronize()
+        return x
+    want = run(True)
+    for _ in range(5):
+        assert torch.equal(run(False), want)

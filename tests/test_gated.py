@@ -441,6 +441,9 @@ def test_refused_overlaps_and_workspaces():
     for over in (1 << 27, 1 << 32, 1 << 35):
         assert _backward(p, dA=_arr(over)) == m.ERR_UNSUPPORTED
         assert _backward(p, C=_arr(over)) == m.ERR_UNSUPPORTED
+    assert _backward(p, dup=_arr(1 << 29)) == m.ERR_UNSUPPORTED and _backward(p, C=_arr(1 << 28)) == m.ERR_UNSUPPORTED
+    assert _forward(p, saved=_saved(up=1 << 32)) == m.ERR_UNSUPPORTED
+    assert _forward(p, saved=_saved(gs=1 << 27)) == m.ERR_UNSUPPORTED
     assert _backward(p, saved=None) == m.ERR_NULL
     assert _backward(p, dgate=None) == m.ERR_NULL and _backward(p, dup=None) == m.ERR_NULL
     need = p.gated_workspace_size()

@@ -310,6 +310,7 @@ def test_refused_results_and_workspaces():
         assert _backward(p, dA=_arr(over)) == m.ERR_UNSUPPORTED
         assert _backward(p, dB=_arr(over)) == m.ERR_UNSUPPORTED
     assert _backward(p, dA=_arr(1 << 27)) == m.ERR_UNSUPPORTED  # over dC
+    assert _backward(p, dB=_arr(1 << 28)) == m.ERR_UNSUPPORTED  # over dA
     need = p.scaled_workspace_size()
     assert need == 64 * 128 + 256 + 64 * 256 * 2
     assert _backward(p, n=need - 1) == m.ERR_NOMEM and _backward(p, ws=None) == m.ERR_NULL
