@@ -4,14 +4,24 @@
 //
 // A CTA computes 32 rows by 128 columns of the result, the columns counted from
 // a result block's left edge, so a 128-column scale block of a kept 8-bit
-// result lies in one warp: warp w has rows 4w .. 4w+3, lane l columns 4l ..
-// 4l+3.  The contracted dim goes through shared memory 32 at a time, the next
-// piece's loads in flight while one is used.  Everything is fp32; sums of 256
-// products are added to a second sum, so an element's error grows with the
-// number of pieces and not of products.
+// result lies in one warp.  The contracted dim goes through shared memory 64 at
+// a time.  Two groups of eight warps take 32 of the 64 each, a warp 4 rows and a
+// lane 4 columns (of both projections): 16 warps at 128 registers, where one
+// group's 8 warps left FMAs waiting for shared memory.  Two pieces lie in shared
+// memory and the loads of a third are in flight, with one barrier per piece.
+// Everything is fp32; sums of 256 products are added to a second sum (in shared
+// memory), so an element's error grows with the number of pieces and not of
+// products.
 //
-// Bound by the FMA pipe's operand reads (two or three 16-byte shared reads per
-// 16 or 32 FMAs).
+// Measured (fp32): gated forward 301 x 1000 x 1157 in 75 us (18 TFLOP/s; 87 with
+// one group of 8 warps and 32-deep pieces), dA of it in 119 with the slopes
+// (218), 1024 x 1024 x 1500 in 221 (247), 2048 x 2048 x 2048 in 1030 (33
+// TFLOP/s; 1115); the one-operand products of 2048 x 2048 x 2048 lose 5 to 7 %
+// (dA 1267 -> 1335 us).  A 64-deep piece takes 4.7 us of an SM, 2.2 of them FMAs;
+// shared-memory reads (9 to 10 cycles for 8 of FMAs) take half of the cycles and
+// issue slots 47 %, and what is left is waits for either and for the loads.
+// Packed FMAs (77 us), 8 rows to a thread with four groups (87; packed 78) were
+// no faster.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -30,9 +40,9 @@ namespace {
 
 using namespace shmm_dev;
 
-constexpr int TM = 32, TN = 128, TK = 32;
-constexpr int kThreads = 256;
-constexpr int kFlush = 8;   // pieces of TK in the first sum
+constexpr int TM = 32, TN = 128, TK = 64;
+constexpr int kThreads = 512, kGroups = 2;
+constexpr int kFlush = 8;   // pieces in the first sum, each TK / kGroups products of it
 constexpr int XS = TM + 4, YS = TN + 4;  // shared rows of the pieces, whole 16-byte vectors
 
 // An operand: at most CAP blocks.
@@ -166,61 +176,81 @@ __device__ __forceinline__ void put4_e4m3(const Res<CAP> &d, int64_t row, bool r
     }
 }
 
+// Shared memory: two pieces of X and Y, then every thread's second sums.
+struct __align__(16) XPiece { float v[TK][XS]; };
+struct __align__(16) YPiece { float v[TK][YS]; };
+constexpr size_t smem_bytes(int ny) { return 2 * (sizeof(XPiece) + ny * sizeof(YPiece)) + (size_t)ny * 4 * kThreads * sizeof(float4); }
+static_assert(smem_bytes(2) <= 227 * 1024, "a CTA's shared memory");
+
 template <typename T, int CAP, bool GATED>
-__global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_constant__ SimtK<CAP> k) {
+__global__ void __launch_bounds__(kThreads, 1) contract_simt_kernel(const __grid_constant__ SimtK<CAP> k) {
     constexpr int NY = GATED ? 2 : 1;
     constexpr int PX = TM * TK / kThreads, PY = TK * TN / kThreads;
-    __shared__ __align__(16) float xs[TK][XS];
-    __shared__ __align__(16) float ys[NY][TK][YS];
+    extern __shared__ __align__(16) uint8_t smem[];
+    XPiece *xs = reinterpret_cast<XPiece *>(smem);
+    YPiece *ys = reinterpret_cast<YPiece *>(xs + 2);  // [2][NY]
+    float4 *sums = reinterpret_cast<float4 *>(ys + 2 * NY);  // [NY * 4][kThreads]
     shmm_pdl::pdl_enter();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32 % 8, group = tid / 256;
     const int64_t m0 = (int64_t)blockIdx.x * TM;
     const int cb = blockIdx.y / k.n_per;                                    // result block column
     const int64_t n0l = (int64_t)(blockIdx.y % k.n_per) * TN;               // first column in it
     const int64_t n0 = cb * k.D.bcols + n0l, n1 = (cb + 1) * k.D.bcols;     // ... of the whole array, and the block's end
     const int64_t per_term = (k.Kd + TK - 1) / TK, pieces = k.terms * per_term;
 
+    // A thread's elements of a piece.  Stored with the contracted dim last, a warp
+    // takes 8 of it in 4 rows, which go to 32 banks of [contracted][row].
+    const int at_k = lane % 8 + warp * 8, at_r = lane / 8 + group * 4;
     float xr[PX], yr[NY][PY];
     auto ask = [&](int64_t piece) {
         const int t = piece >= per_term ? 1 : 0;
         const int64_t k0 = (piece - t * per_term) * TK;
-        if (k.x_t) fetch_part<T, CAP, PX, true, 0, kThreads / TM>(k.X[t], m0 + lane, k.M, k0 + warp, k.Kd, xr, k.status);
-        else fetch_part<T, CAP, PX, false, kThreads / TK, 0>(k.X[t], m0 + warp, k.M, k0 + lane, k.Kd, xr, k.status);
+        if (k.x_t) fetch_part<T, CAP, PX, true, 0, kThreads / TM>(k.X[t], m0 + lane, k.M, k0 + tid / TM, k.Kd, xr, k.status);
+        else fetch_part<T, CAP, PX, false, kThreads / TK, 0>(k.X[t], m0 + at_r, k.M, k0 + at_k, k.Kd, xr, k.status);
 #pragma unroll
         for (int y = 0; y < NY; ++y) {
             const Op<CAP> &o = k.Y[GATED ? y : t];
-            if (k.y_t) fetch_part<T, CAP, PY, false, kThreads / TK, 0>(o, n0 + warp, n1, k0 + lane, k.Kd, yr[y], k.status);
-            else fetch_part<T, CAP, PY, true, 0, kThreads / TN>(o, n0 + threadIdx.x % TN, n1, k0 + threadIdx.x / TN, k.Kd, yr[y], k.status);
+            if (k.y_t) fetch_part<T, CAP, PY, false, kThreads / TK, 0>(o, n0 + at_r, n1, k0 + at_k, k.Kd, yr[y], k.status);
+            else fetch_part<T, CAP, PY, true, 0, kThreads / TN>(o, n0 + tid % TN, n1, k0 + tid / TN, k.Kd, yr[y], k.status);
+        }
+    };
+    auto put = [&](int b) {
+        float (&x)[TK][XS] = xs[b].v;
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            if (k.x_t) x[tid / TM + i * (kThreads / TM)][tid % TM] = xr[i];
+            else x[at_k][at_r + i * (kThreads / TK)] = xr[i];
+        }
+#pragma unroll
+        for (int y = 0; y < NY; ++y) {
+            float (&v)[TK][YS] = ys[b * NY + y].v;
+#pragma unroll
+            for (int i = 0; i < PY; ++i) {
+                if (k.y_t) v[at_k][at_r + i * (kThreads / TK)] = yr[y][i];
+                else v[tid / TN + i * (kThreads / TN)][tid % TN] = yr[y][i];
+            }
         }
     };
 
-    float sum[NY][4][4] = {}, acc[NY][4][4] = {};
-    if (pieces) ask(0);
+    float acc[NY][4][4] = {};
+#pragma unroll
+    for (int i = 0; i < NY * 4; ++i) sums[i * kThreads + tid] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (pieces) {
+        ask(0);
+        put(0);
+    }
     for (int64_t piece = 0; piece < pieces; ++piece) {
-        __syncthreads();  // the last piece has been used
-#pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int at = threadIdx.x + i * kThreads;
-            if (k.x_t) xs[at / TM][at % TM] = xr[i];
-            else xs[at % TK][at / TK] = xr[i];
-        }
-#pragma unroll
-        for (int y = 0; y < NY; ++y)
-#pragma unroll
-            for (int i = 0; i < PY; ++i) {
-                const int at = threadIdx.x + i * kThreads;
-                if (k.y_t) ys[y][at % TK][at / TK] = yr[y][i];
-                else ys[y][at / TN][at % TN] = yr[y][i];
-            }
-        __syncthreads();
+        const int b = (int)(piece & 1);
+        __syncthreads();  // this piece is in place, and the one before has been used
         if (piece + 1 < pieces) ask(piece + 1);
-#pragma unroll 16
-        for (int kk = 0; kk < TK; ++kk) {
-            const float4 x4 = *reinterpret_cast<const float4 *>(&xs[kk][warp * 4]);
+        const int kk0 = group * (TK / kGroups);
+#pragma unroll 8
+        for (int kk = kk0; kk < kk0 + TK / kGroups; ++kk) {
+            const float4 x4 = *reinterpret_cast<const float4 *>(&xs[b].v[kk][warp * 4]);
             const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
             for (int y = 0; y < NY; ++y) {
-                const float4 y4 = *reinterpret_cast<const float4 *>(&ys[y][kk][lane * 4]);
+                const float4 y4 = *reinterpret_cast<const float4 *>(&ys[b * NY + y].v[kk][lane * 4]);
                 const float v[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -232,35 +262,53 @@ __global__ void __launch_bounds__(kThreads) contract_simt_kernel(const __grid_co
 #pragma unroll
             for (int y = 0; y < NY; ++y)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    float4 *p = &sums[(y * 4 + i) * kThreads + tid];
+                    float4 v = *p;
+                    v.x += acc[y][i][0];
+                    v.y += acc[y][i][1];
+                    v.z += acc[y][i][2];
+                    v.w += acc[y][i][3];
+                    *p = v;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        sum[y][i][j] += acc[y][i][j];
-                        acc[y][i][j] = 0.0f;
-                    }
+                    for (int j = 0; j < 4; ++j) acc[y][i][j] = 0.0f;
+                }
         }
+        if (piece + 1 < pieces) put(b ^ 1);
     }
+    __syncthreads();
 
+    // The groups' sums together; each group finishes two of a warp's four rows.
     const int64_t cl = n0l + lane * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int h = 0; h < 2; ++h) {
+        const int i = group * 2 + h;
         const int64_t row = m0 + warp * 4 + i;
         const bool row_ok = row < k.M;
+        float sum[NY][4];
+#pragma unroll
+        for (int y = 0; y < NY; ++y) {
+            const float4 a = sums[(y * 4 + i) * kThreads + tid % 256], c = sums[(y * 4 + i) * kThreads + tid % 256 + 256];
+            sum[y][0] = a.x + c.x;
+            sum[y][1] = a.y + c.y;
+            sum[y][2] = a.z + c.z;
+            sum[y][3] = a.w + c.w;
+        }
         if (GATED) {
             if (k.keep) {
 #pragma unroll
                 for (int y = 0; y < NY; ++y) {
-                    if (k.kept[y].dt == SHMM_E4M3) put4_e4m3(k.kept[y], row, row_ok, cb, cl, sum[y][i], lane, k.status);
-                    else if (row_ok) put4(k.kept[y], row, cb, cl, sum[y][i], k.status);
+                    if (k.kept[y].dt == SHMM_E4M3) put4_e4m3(k.kept[y], row, row_ok, cb, cl, sum[y], lane, k.status);
+                    else if (row_ok) put4(k.kept[y], row, cb, cl, sum[y], k.status);
                 }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float g = sum[0][i][j];
-                sum[0][i][j] = (k.act == SHMM_SILU ? gate_act<SHMM_SILU>(g) : gate_act<SHMM_GELU_TANH>(g)) * sum[NY - 1][i][j];
+                const float g = sum[0][j];
+                sum[0][j] = (k.act == SHMM_SILU ? gate_act<SHMM_SILU>(g) : gate_act<SHMM_GELU_TANH>(g)) * sum[NY - 1][j];
             }
         }
-        if (row_ok) put4(k.D, row, cb, cl, sum[0][i], k.status);
+        if (row_ok) put4(k.D, row, cb, cl, sum[0], k.status);
     }
 }
 
@@ -315,6 +363,22 @@ size_t entries(const shmm::ContractArgs &a) {
     return n;
 }
 
+template <typename T, int CAP, bool GATED>
+cudaError_t go(const SimtK<CAP> &k, dim3 grid, cudaStream_t s) {
+    constexpr size_t kSmem = smem_bytes(GATED ? 2 : 1);
+    static shmm::PerDevice<int> attr_set;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= shmm::kMaxDevices) return cudaErrorInvalidDevice;
+    if (!attr_set.get(dev)) {
+        e = cudaFuncSetAttribute(contract_simt_kernel<T, CAP, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set.set(dev, 1);
+    }
+    return shmm_pdl::launch_pdl(contract_simt_kernel<T, CAP, GATED>, grid, dim3(kThreads), kSmem, s, k);
+}
+
 template <int CAP>
 cudaError_t launch(const shmm::ContractArgs &a, int which, int *status, cudaStream_t s) {
     static_assert(sizeof(SimtK<CAP>) <= 32764, "kernel parameters");
@@ -337,11 +401,9 @@ cudaError_t launch(const shmm::ContractArgs &a, int which, int *status, cudaStre
     k.status = status;
     const dim3 grid((unsigned)((a.M + TM - 1) / TM), (unsigned)(k.n_per * k.D.b1));
     shmm::count_launch();
-#define GO(T, G) shmm_pdl::launch_pdl(contract_simt_kernel<T, CAP, G>, grid, dim3(kThreads), 0, s, k)
-    if (a.X[0].dt == SHMM_E4M3) return GO(uint8_t, false);
-    if (a.X[0].dt == SHMM_BF16) return a.gated ? GO(__nv_bfloat16, true) : GO(__nv_bfloat16, false);
-    return a.gated ? GO(float, true) : GO(float, false);
-#undef GO
+    if (a.X[0].dt == SHMM_E4M3) return go<uint8_t, CAP, false>(k, grid, s);
+    if (a.X[0].dt == SHMM_BF16) return a.gated ? go<__nv_bfloat16, CAP, true>(k, grid, s) : go<__nv_bfloat16, CAP, false>(k, grid, s);
+    return a.gated ? go<float, CAP, true>(k, grid, s) : go<float, CAP, false>(k, grid, s);
 }
 
 }  // namespace
