@@ -1505,11 +1505,21 @@ shmm_status_t shmm_scaled_backward(const shmm_plan_t *p, const void *const *dC_r
         char *codes = static_cast<char *>(workspace);
         float *scales = reinterpret_cast<float *>(codes + w.codes);
         char *wide = codes + w.codes + w.scales;
+        // dC in 8 bits and A restored, then the two products; of each two the second
+        // runs beside the first (with a dim of size 0 there may be no first).
+        const bool beside = dA_r && dB_r && p->I > 0 && p->J > 0 && p->K > 0;
         int e = 0;
+        const shmm::GridOperand dC = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, dC_r, p->out_dt);
         if (dA_r) {
-            const shmm::GridOperand dC = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, dC_r, p->out_dt);
             e = shmm::launch_quantize(dC, codes, p->K, scales, w.scale_ld, status, stream);
             if (e) return cuda_fail(fn, e);
+        }
+        if (dB_r) {
+            const shmm::GridOperand A = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, SHMM_E4M3, A_scale_r);
+            e = shmm::launch_dequantize(A, wide, p->J, SHMM_BF16, status, stream, beside);
+            if (e) return cuda_fail(fn, e);
+        }
+        if (dA_r) {
             shmm::ContractArgs a = contract_args(p, p->I, p->J, p->K);
             a.y_t = true;
             a.X[0] = whole_operand(codes, p->I, p->K, SHMM_E4M3, scales, dC.bcols);
@@ -1519,13 +1529,11 @@ shmm_status_t shmm_scaled_backward(const shmm_plan_t *p, const void *const *dC_r
             if (e) return cuda_fail(fn, e, err);
         }
         if (dB_r) {
-            const shmm::GridOperand A = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, SHMM_E4M3, A_scale_r);
-            e = shmm::launch_dequantize(A, wide, p->J, SHMM_BF16, status, stream);
-            if (e) return cuda_fail(fn, e);
             shmm::ContractArgs a = contract_args(p, p->J, p->K, p->I);
             a.x_t = true;
+            a.beside = beside;
             a.X[0] = whole_operand(wide, p->I, p->J, SHMM_BF16);
-            a.Y[0] = grid_operand(p, SHMM_TENSOR_C, p->I, p->K, dC_r, p->out_dt);
+            a.Y[0] = dC;
             a.D[0] = grid_result(p, SHMM_TENSOR_B, p->J, p->K, dB_r, SHMM_BF16);
             e = shmm::launch_contract(a, status, stream, &err);
             if (e) return cuda_fail(fn, e, err);
@@ -1693,6 +1701,7 @@ shmm_status_t shmm_gated_backward(const shmm_plan_t *p, int activation, const vo
             shmm::ContractArgs a = contract_args(p, p->J, p->K, p->I);
             a.x_t = true;
             a.two = true;
+            a.beside = dA_r && p->I > 0 && p->J > 0 && p->K > 0;  // dA is under way
             a.X[0] = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, p->in_dt);
             a.Y[0] = dG;
             a.Y[1] = dU;

@@ -328,24 +328,25 @@ struct BackK {
     const float *scale[kShards];
     void *dst;
     int64_t brows, bcols, src_ld, ld, scale_ld, dst_n;
-    int b1, scale_rows;
+    int b1, scale_rows, beside;
     int *status;
 };
 
 // 8192 x 4096 to bf16: 17 us, 6.0 TB/s.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ BackK k) {
-    shmm_pdl::pdl_enter();
+    if (!k.beside) shmm_pdl::pdl_wait();
+    shmm_pdl::pdl_release();
     const int lane = threadIdx.x % 32;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    if (row >= k.brows) return;
+    const int64_t cols = row < k.brows ? k.bcols : 0;
     const int bi = blockIdx.z / k.b1, bj = blockIdx.z % k.b1;
     const uint8_t *src = static_cast<const uint8_t *>(k.src[blockIdx.z]) + row * k.src_ld;
     const int64_t s_row = row / k.scale_rows * k.scale_ld;
     const int64_t s_n = (k.brows + k.scale_rows - 1) / k.scale_rows * k.scale_ld;
     const float *scale = k.scale[blockIdx.z] + s_row;
     const int64_t at = (bi * k.brows + row) * k.ld + bj * k.bcols;
-    for (int64_t c0 = (int64_t)blockIdx.y * kBackChunk; c0 < k.bcols; c0 += (int64_t)gridDim.y * kBackChunk) {
+    for (int64_t c0 = (int64_t)blockIdx.y * kBackChunk; c0 < cols; c0 += (int64_t)gridDim.y * kBackChunk) {
         Raw8<uint8_t> raw[kBackPieces];
         float s[kBackPieces];
 #pragma unroll
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ 
             store8<VEC>(static_cast<T *>(k.dst) + at + c, k.bcols - c, v);
         }
     }
+    if (k.beside) shmm_pdl::pdl_wait();
 }
 
 // ---- the gated block's gradient, element by element ------------------------
@@ -491,7 +493,8 @@ int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scal
 #undef GO
 }
 
-int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream) {
+int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream,
+                      bool beside) {
     const int blocks = src.b0 * src.b1;
     if (src.brows == 0 || src.bcols == 0) return 0;
     BackK k = {};
@@ -510,6 +513,7 @@ int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_
     k.dst_n = src.b0 * src.brows * ld;
     k.b1 = src.b1;
     k.scale_rows = src.scale_rows;
+    k.beside = beside;
     k.status = status;
     const dim3 grid = rows_grid(src.brows, src.bcols, kBackChunk, blocks);
     cudaStream_t s = (cudaStream_t)stream;

@@ -215,6 +215,7 @@ int launch_contract(const ContractArgs &a, int *status, void *stream, std::strin
     k.two = a.two;
     k.act = a.act;
     k.out_f32 = a.D[0].dt == SHMM_F32;
+    k.beside = a.beside;
     k.status = status;
     return small ? launch_small(k, form, sms, (cudaStream_t)stream) : launch_pair(k, form, a.max_sms, (cudaStream_t)stream);
 }

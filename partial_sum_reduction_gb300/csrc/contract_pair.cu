@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     const uint32_t tmem_base = *words;
     // The prologue above touches no global memory: it may overlap the end of
     // the kernel before in the stream.
-    grid_dependency_wait();
+    if (!k.beside) grid_dependency_wait();
     grid_launch_dependents();
 
     if (warp < 4) {
@@ -743,6 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
+    if (k.beside) grid_dependency_wait();
 }
 
 // ---- host side --------------------------------------------------------------

@@ -68,7 +68,7 @@ struct SimtK {
     Op<CAP> X[2], Y[2];
     Res<CAP> D, kept[2];
     int64_t M, N, Kd;
-    int terms, x_t, y_t, keep, act;
+    int terms, x_t, y_t, keep, act, beside;
     int n_per;  // column tiles of a result block
     int *status;
 };
@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) contract_simt_kernel(const __grid
     XPiece *xs = reinterpret_cast<XPiece *>(smem);
     YPiece *ys = reinterpret_cast<YPiece *>(xs + 2);  // [2][NY]
     float4 *sums = reinterpret_cast<float4 *>(ys + 2 * NY);  // [NY * 4][kThreads]
-    shmm_pdl::pdl_enter();
+    if (!k.beside) shmm_pdl::pdl_wait();
+    shmm_pdl::pdl_release();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32 % 8, group = tid / 256;
     const int64_t m0 = (int64_t)blockIdx.x * TM;
     const int cb = blockIdx.y / k.n_per;                                    // result block column
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_simt_kernel(const __grid
         }
         if (row_ok) put4(k.D, row, cb, cl, sum[0], k.status);
     }
+    if (k.beside) shmm_pdl::pdl_wait();
 }
 
 // ---- host side --------------------------------------------------------------
@@ -397,6 +399,7 @@ cudaError_t launch(const shmm::ContractArgs &a, int which, int *status, cudaStre
     k.y_t = a.y_t;
     k.keep = a.keep;
     k.act = a.act;
+    k.beside = a.beside || which == 1;  // the second of two products does not need the first
     k.n_per = (int)((k.D.bcols + TN - 1) / TN);
     k.status = status;
     const dim3 grid((unsigned)((a.M + TM - 1) / TM), (unsigned)(k.n_per * k.D.b1));

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
     __syncthreads();
     fence_after();
     const uint32_t tmem_base = *words;
-    grid_dependency_wait();
+    if (!k.beside) grid_dependency_wait();
     grid_launch_dependents();
 
     const uint32_t x_bytes = (uint32_t)k.x_rows * 128;  // of a stage; the 16 KB of Y follow
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
     fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kCols) : "memory");
+    if (k.beside) grid_dependency_wait();
 }
 
 // ---- host side --------------------------------------------------------------

@@ -49,7 +49,7 @@ struct ContractK {
     int64_t M, N, Kd;
     int m_tiles, n_tiles, k_blocks, terms;
     int total, half_from;  // work items; from half_from on they are half tiles
-    int two, act, out_f32;
+    int two, act, out_f32, beside;
     int *status;
     // the kernel for few rows: buffers of the results (D[0], D[1], kept), rows of X
     // in a stage, its boxes there, stages, their bytes, parts of the contracted dim

@@ -264,6 +264,11 @@ struct ContractArgs {
     int act = SHMM_SILU;
     bool tensor_core = true;  // may run on the tensor cores
     int max_sms = 0;
+    // The product neither needs nor overwrites anything of the launch before it in
+    // the stream, and that launch is one of this call's that waits for all before
+    // itself: this one then starts beside it, and waits for it before it ends, so
+    // that whatever waits for this one has waited for both.
+    bool beside = false;
     GridOperand X[2], Y[2];
     GridResult D[2], kept[2];
 };
@@ -277,8 +282,10 @@ int launch_contract_simt(const ContractArgs &a, int *status, void *stream);
 // column j * ceil(bcols / 128).  src.scale_rows says which blocks.
 int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scale, int64_t scale_ld, int *status,
                     void *stream);
-// The way back, into a [rows, cols] array of dtype dt (row pitch ld).
-int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream);
+// The way back, into a [rows, cols] array of dtype dt (row pitch ld).  beside: as
+// in ContractArgs.
+int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream,
+                      bool beside = false);
 
 // Gradient of act(G) * U by its elements, for the gradient dH of the product:
 //   dG = dH * U * act'(G), dU = dH * act(G), rounded to dt, into [rows, cols]

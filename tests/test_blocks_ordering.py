@@ -134,3 +134,82 @@ def test_beside_the_plans_own_matmuls():
     want = run(True)
     for _ in range(5):
         assert torch.equal(run(False), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f32", "scaled"])
+@pytest.mark.parametrize("I,J,K", [(8, 128, 16384), (640, 256, 1024), (24, 4096, 256), (2048, 2048, 1024)])
+def test_what_follows_a_backward_pass_waits_for_both_products(kind, I, J, K, monkeypatch):
+    """The two products of a backward pass run side by side.  Library calls that
+    read dA or overwrite what it is made of, right behind the pass, in a stream
+    and from a graph, give what they give in plain stream order."""
+    in_dt, dt = ("e4m3", "bf16") if kind == "scaled" else (kind, kind)
+    plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K, in_dt, dt)
+    tdt = torch.float32 if dt == "f32" else torch.bfloat16
+    g = gen(3)
+    sets = []
+    for _ in range(2):
+        A, gate, up, dC = ((normal(g, *e) / d).to(tdt) for e, d in (((I, J), 1), ((J, K), J ** 0.5), ((J, K), J ** 0.5), ((I, K), 20)))
+        if kind == "scaled":
+            a, b = s.helpers.quantize(A, 1), s.helpers.quantize(gate, 128)
+            sets.append(([dC], [a[0]], [a[1]], [b[0]], [b[1]]))
+        else:
+            saved = s.helpers.gated_saved(plan, dt)
+            plan.gated_forward([A], [gate], [up], s.helpers.alloc(plan, s.TENSOR_C), saved=saved)
+            sets.append(([dC], [A], [gate], [up], saved))
+    ws = s.helpers.scaled_workspace(plan) if kind == "scaled" else s.helpers.gated_workspace(plan)
+    back = plan.scaled_backward if kind == "scaled" else plan.gated_backward
+    out_dt = torch.bfloat16 if kind == "scaled" else tdt
+    outs = [[torch.empty(e, device="cuda", dtype=out_dt)] for e in ((I, J), (J, K), (J, K))][:2 if kind == "scaled" else 3]
+    codes = [torch.empty(o[0].shape, device="cuda", dtype=torch.float8_e4m3fn) for _ in range(4) for o in outs]
+    scales = [torch.empty(s.scale_shape(*c.shape), device="cuda") for c in codes]
+
+    def run():
+        for i in range(4):  # one workspace, one set of results, other operands each time
+            stream = torch.cuda.current_stream()
+            back(*sets[i % 2], *outs, ws, stream=stream)
+            for j, o in enumerate(outs):
+                s.shmm_quantize(o[0], codes[i * len(outs) + j], scales[i * len(outs) + j], stream=stream)
+
+    def result():
+        torch.cuda.synchronize()
+        return [c.view(torch.uint8).clone() for c in codes] + [x.clone() for x in scales]
+
+    def clear():
+        for c in codes:
+            c.view(torch.uint8).zero_()
+
+    monkeypatch.setenv("SHMM_PDL", "0")
+    run()
+    want = result()
+    monkeypatch.delenv("SHMM_PDL")
+    for _ in range(5):
+        clear()
+        run()
+        assert all(torch.equal(a, b) for a, b in zip(result(), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        clear()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(result(), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("I,J,K", [(0, 128, 256), (16, 0, 256), (16, 128, 0)])
+def test_a_backward_pass_with_an_empty_dim(I, J, K):
+    """Where a product is left out, the next one waits for what it needs."""
+    plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K, "bf16", "bf16")
+    new = lambda t: s.helpers.alloc(plan, t)
+    saved = s.helpers.gated_saved(plan, "bf16")
+    A, gate, up, dC, C = (new(t) for t in (s.TENSOR_A, s.TENSOR_B, s.TENSOR_B, s.TENSOR_C, s.TENSOR_C))
+    for t in (A, gate, up, dC):
+        t[0].normal_()
+    outs = [new(t) for t in (s.TENSOR_A, s.TENSOR_B, s.TENSOR_B)]
+    for o in outs:
+        o[0].fill_(7.0)
+    plan.gated_forward(A, gate, up, C, saved=saved)
+    plan.gated_backward(dC, A, gate, up, saved, *outs, s.helpers.gated_workspace(plan))
+    torch.cuda.synchronize()
+    assert all(not o[0].any() for o in outs)
