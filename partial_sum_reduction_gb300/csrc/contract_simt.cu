@@ -9,19 +9,21 @@
 // lane 4 columns (of both projections): 16 warps at 128 registers, where one
 // group's 8 warps left FMAs waiting for shared memory.  Two pieces lie in shared
 // memory and the loads of a third are in flight, with one barrier per piece.
-// Everything is fp32; sums of 256 products are added to a second sum (in shared
+// Everything is fp32; sums of 64 products are added to a second sum (in shared
 // memory), so an element's error grows with the number of pieces and not of
-// products.
+// products.  (Of a million values that are kept in 8 bits, sums of 256 leave 27
+// on another side of a rounding border than 64-bit sums do, these 13, and a
+// library's fp32 products 34; they cost 3 %.)
 //
-// Measured (fp32): gated forward 301 x 1000 x 1157 in 75 us (18 TFLOP/s; 87 with
-// one group of 8 warps and 32-deep pieces), dA of it in 119 with the slopes
-// (218), 1024 x 1024 x 1500 in 221 (247), 2048 x 2048 x 2048 in 1030 (33
-// TFLOP/s; 1115); the one-operand products of 2048 x 2048 x 2048 lose 5 to 7 %
-// (dA 1267 -> 1335 us).  A 64-deep piece takes 4.7 us of an SM, 2.2 of them FMAs;
+// Measured (fp32): gated forward 301 x 1000 x 1157 in 78 us (18 TFLOP/s; 87 with
+// one group of 8 warps and 32-deep pieces), its backward pass in 213 (248),
+// forward 1024 x 1024 x 1500 in 229 (247), 2048 x 2048 x 2048 in 1068 (32
+// TFLOP/s; 1115); the one-operand products of 2048 x 2048 x 2048 lose 8 to 9 %
+// (dA 1267 -> 1368 us).  A 64-deep piece takes 4.7 us of an SM, 2.2 of them FMAs;
 // shared-memory reads (9 to 10 cycles for 8 of FMAs) take half of the cycles and
 // issue slots 47 %, and what is left is waits for either and for the loads.
-// Packed FMAs (77 us), 8 rows to a thread with four groups (87; packed 78) were
-// no faster.
+// Packed FMAs (2 % slower), 8 rows to a thread with four groups (16 %; packed 3
+// %) gained nothing.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -42,7 +44,7 @@ using namespace shmm_dev;
 
 constexpr int TM = 32, TN = 128, TK = 64;
 constexpr int kThreads = 512, kGroups = 2;
-constexpr int kFlush = 8;   // pieces in the first sum, each TK / kGroups products of it
+constexpr int kFlush = 2;   // pieces in the first sum, each TK / kGroups products of it
 constexpr int XS = TM + 4, YS = TN + 4;  // shared rows of the pieces, whole 16-byte vectors
 
 // An operand: at most CAP blocks.
