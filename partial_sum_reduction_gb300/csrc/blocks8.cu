@@ -29,7 +29,9 @@ namespace {
 using namespace shmm_dev;
 
 constexpr int kBlock = 128;
-constexpr int kShards = SHMM_MAX_RANKS;  // blocks of a grid
+// Blocks of a grid, and holders of one, that a kernel's parameters have room for:
+// CAP in its structures, kFew or all.  With all, 2 to 14 KB go with each launch.
+constexpr int kFew = 16, kAll = SHMM_MAX_RANKS;
 constexpr int kThreads = 256;
 // A warp takes this many columns of one row, kPieces pieces of 256: enough
 // loads in flight per lane to cover the memory's latency.
@@ -174,8 +176,9 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *p, int64_t left, const floa
 // ---- to 8 bits ------------------------------------------------------------
 
 // One block of the source grid per blockIdx.z, read at src[z].
+template <int CAP>
 struct ToK {
-    const void *src[kShards];
+    const void *src[CAP];
     uint8_t *codes;
     float *scale;
     int64_t brows, bcols, src_ld, ld, scale_ld;
@@ -187,9 +190,10 @@ struct ToK {
 
 // A scale for each 128 columns of a row: a warp takes a row's chunk of
 // columns, 16 lanes a block, so the largest magnitude takes four shuffles.
-// 8192 x 16384 bf16: 67 us, 6.1 TB/s.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant__ ToK k) {
+// 8192 x 16384 bf16: 71 us, 5.7 TB/s, 66 % of the issue slots; 16 x 4096: 1.8 us
+// replayed from a graph.  Two pieces fewer or four more per lane: 88, 80 us.
+template <typename T, bool VEC, int CAP>
+__global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant__ ToK<CAP> k) {
     shmm_pdl::pdl_enter();
     const int lane = threadIdx.x % 32;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
@@ -256,9 +260,10 @@ __global__ void __launch_bounds__(kThreads) to_rows_kernel(const __grid_constant
 }
 
 // A scale for each 128 x 128 values: a CTA takes a block, which stays in its
-// registers between the largest magnitude and the rounding.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_constant__ ToK k) {
+// registers between the largest magnitude and the rounding.  8192 x 16384 bf16:
+// 70 us, 5.8 TB/s.
+template <typename T, bool VEC, int CAP>
+__global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_constant__ ToK<CAP> k) {
     shmm_pdl::pdl_enter();
     __shared__ uint32_t part[kThreads / 32];
     const int bi = blockIdx.z / k.b1, bj = blockIdx.z % k.b1;
@@ -323,9 +328,10 @@ __global__ void __launch_bounds__(kThreads) to_squares_kernel(const __grid_const
 
 // ---- and back -------------------------------------------------------------
 
+template <int CAP>
 struct BackK {
-    const void *src[kShards];
-    const float *scale[kShards];
+    const void *src[CAP];
+    const float *scale[CAP];
     void *dst;
     int64_t brows, bcols, src_ld, ld, scale_ld, dst_n;
     int b1, scale_rows, beside;
@@ -333,8 +339,8 @@ struct BackK {
 };
 
 // 8192 x 4096 to bf16: 17 us, 6.0 TB/s.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ BackK k) {
+template <typename T, bool VEC, int CAP>
+__global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ BackK<CAP> k) {
     if (!k.beside) shmm_pdl::pdl_wait();
     shmm_pdl::pdl_release();
     const int lane = threadIdx.x % 32;
@@ -376,11 +382,12 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ 
 
 // ---- the gated block's gradient, element by element ------------------------
 
+template <int CAP>
 struct SlopeK {
-    const void *dH[kShards], *G[kShards], *U[kShards];
-    const float *g_scale[kShards], *u_scale[kShards];
-    void *H[kShards];              // holders of every block, block by block
-    uint16_t h_first[kShards + 1]; // block z's holders: H[h_first[z]] .. H[h_first[z + 1] - 1]
+    const void *dH[CAP], *G[CAP], *U[CAP];
+    const float *g_scale[CAP], *u_scale[CAP];
+    void *H[CAP];              // holders of every block, block by block
+    uint16_t h_first[CAP + 1]; // block z's holders: H[h_first[z]] .. H[h_first[z + 1] - 1]
     void *dG, *dU;
     int64_t brows, bcols, ld, scale_ld, out_n;
     int b1;
@@ -388,9 +395,14 @@ struct SlopeK {
 };
 
 // T: the gradients' type; S: the kept pre-activations' (uint8_t: 8 bits).
-// Pieces of eight values, two in flight per lane.
-template <typename T, typename S, int ACT, bool VEC>
-__global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__ SlopeK k) {
+// Pieces of eight values, two in flight per lane.  Everything is fp32 up to dG
+// and dU, which are rounded to T: they are the next products' operands, and the
+// tensor cores' have no more bits.  (In bf16 half a step on each is 1.7e-3 of
+// their 2-norm, and what comes of them is that much less exact.)
+//
+// 8192 x 16384 bf16 from 8 bits: 184 us, 5.8 TB/s, and 72 % of the issue slots.
+template <typename T, typename S, int ACT, bool VEC, int CAP>
+__global__ void __launch_bounds__(kThreads) slope_kernel(const __grid_constant__ SlopeK<CAP> k) {
     constexpr bool E8 = sizeof(S) == 1;
     constexpr int PIECES = 2;
     shmm_pdl::pdl_enter();
@@ -456,15 +468,11 @@ dim3 rows_grid(int64_t brows, int64_t bcols, int64_t chunk, int blocks) {
                 (unsigned)blocks);
 }
 
-}  // namespace
-
-namespace shmm {
-
-int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scale, int64_t scale_ld, int *status,
-                    void *stream) {
+template <int CAP>
+int quantize(const shmm::GridOperand &src, void *codes, int64_t ld, float *scale, int64_t scale_ld, int *status,
+             void *stream) {
     const int blocks = src.b0 * src.b1;
-    if (src.brows == 0 || src.bcols == 0) return 0;
-    ToK k = {};
+    ToK<CAP> k = {};
     for (int i = 0; i < blocks; ++i) k.src[i] = src.at[i];
     k.codes = static_cast<uint8_t *>(codes);
     k.scale = scale;
@@ -485,19 +493,19 @@ int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scal
     if (squares)
         grid = dim3((unsigned)((src.brows + kBlock - 1) / kBlock), (unsigned)(k.per < 65535 ? k.per : 65535), (unsigned)blocks);
     cudaStream_t s = (cudaStream_t)stream;
-    count_launch();
-#define GO(KERN, T) (int)(vec ? shmm_pdl::launch_pdl(KERN<T, true>, grid, dim3(kThreads), 0, s, k) \
-                              : shmm_pdl::launch_pdl(KERN<T, false>, grid, dim3(kThreads), 0, s, k))
+    shmm::count_launch();
+#define GO(KERN, T) (int)(vec ? shmm_pdl::launch_pdl(KERN<T, true, CAP>, grid, dim3(kThreads), 0, s, k) \
+                              : shmm_pdl::launch_pdl(KERN<T, false, CAP>, grid, dim3(kThreads), 0, s, k))
     if (squares) return f32 ? GO(to_squares_kernel, float) : GO(to_squares_kernel, __nv_bfloat16);
     return f32 ? GO(to_rows_kernel, float) : GO(to_rows_kernel, __nv_bfloat16);
 #undef GO
 }
 
-int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream,
-                      bool beside) {
+template <int CAP>
+int dequantize(const shmm::GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream,
+               bool beside) {
     const int blocks = src.b0 * src.b1;
-    if (src.brows == 0 || src.bcols == 0) return 0;
-    BackK k = {};
+    BackK<CAP> k = {};
     bool vec = pieces_fit(src.bcols, src.ld) && ld % 8 == 0 && aligned(dst, 16);
     for (int i = 0; i < blocks; ++i) {
         k.src[i] = src.at[i];
@@ -517,19 +525,19 @@ int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_
     k.status = status;
     const dim3 grid = rows_grid(src.brows, src.bcols, kBackChunk, blocks);
     cudaStream_t s = (cudaStream_t)stream;
-    count_launch();
+    shmm::count_launch();
     if (dt == SHMM_F32)
-        return (int)(vec ? shmm_pdl::launch_pdl(back_kernel<float, true>, grid, dim3(kThreads), 0, s, k)
-                         : shmm_pdl::launch_pdl(back_kernel<float, false>, grid, dim3(kThreads), 0, s, k));
-    return (int)(vec ? shmm_pdl::launch_pdl(back_kernel<__nv_bfloat16, true>, grid, dim3(kThreads), 0, s, k)
-                     : shmm_pdl::launch_pdl(back_kernel<__nv_bfloat16, false>, grid, dim3(kThreads), 0, s, k));
+        return (int)(vec ? shmm_pdl::launch_pdl(back_kernel<float, true, CAP>, grid, dim3(kThreads), 0, s, k)
+                         : shmm_pdl::launch_pdl(back_kernel<float, false, CAP>, grid, dim3(kThreads), 0, s, k));
+    return (int)(vec ? shmm_pdl::launch_pdl(back_kernel<__nv_bfloat16, true, CAP>, grid, dim3(kThreads), 0, s, k)
+                     : shmm_pdl::launch_pdl(back_kernel<__nv_bfloat16, false, CAP>, grid, dim3(kThreads), 0, s, k));
 }
 
-int launch_gated_slopes(const GatedSlopeArgs &a, int *status, void *stream) {
+template <int CAP>
+int gated_slopes(const shmm::GatedSlopeArgs &a, int *status, void *stream) {
     const int blocks = a.dH.b0 * a.dH.b1;
-    if (a.dH.brows == 0 || a.dH.bcols == 0) return 0;
     const bool e8 = a.G.dt == SHMM_E4M3;
-    SlopeK k = {};
+    SlopeK<CAP> k = {};
     bool vec = pieces_fit(a.dH.bcols, a.cols) && aligned(a.dG, 16) && aligned(a.dU, 16);
     int h = 0;
     for (int i = 0; i < blocks; ++i) {
@@ -560,14 +568,40 @@ int launch_gated_slopes(const GatedSlopeArgs &a, int *status, void *stream) {
     k.status = status;
     const dim3 grid = rows_grid(k.brows, k.bcols, 512, blocks);
     cudaStream_t s = (cudaStream_t)stream;
-    count_launch();
-#define GO(T, S, ACT) (int)(vec ? shmm_pdl::launch_pdl(slope_kernel<T, S, ACT, true>, grid, dim3(kThreads), 0, s, k) \
-                                : shmm_pdl::launch_pdl(slope_kernel<T, S, ACT, false>, grid, dim3(kThreads), 0, s, k))
+    shmm::count_launch();
+#define GO(T, S, ACT) (int)(vec ? shmm_pdl::launch_pdl(slope_kernel<T, S, ACT, true, CAP>, grid, dim3(kThreads), 0, s, k) \
+                                : shmm_pdl::launch_pdl(slope_kernel<T, S, ACT, false, CAP>, grid, dim3(kThreads), 0, s, k))
 #define GO_ACT(T, S) (a.act == SHMM_SILU ? GO(T, S, SHMM_SILU) : GO(T, S, SHMM_GELU_TANH))
     if (a.dt == SHMM_F32) return e8 ? GO_ACT(float, uint8_t) : GO_ACT(float, float);
     return e8 ? GO_ACT(__nv_bfloat16, uint8_t) : GO_ACT(__nv_bfloat16, __nv_bfloat16);
 #undef GO_ACT
 #undef GO
+}
+
+}  // namespace
+
+namespace shmm {
+
+int launch_quantize(const GridOperand &src, void *codes, int64_t ld, float *scale, int64_t scale_ld, int *status,
+                    void *stream) {
+    if (src.brows == 0 || src.bcols == 0) return 0;
+    return src.b0 * src.b1 <= kFew ? quantize<kFew>(src, codes, ld, scale, scale_ld, status, stream)
+                                   : quantize<kAll>(src, codes, ld, scale, scale_ld, status, stream);
+}
+
+int launch_dequantize(const GridOperand &src, void *dst, int64_t ld, shmm_dtype_t dt, int *status, void *stream,
+                      bool beside) {
+    if (src.brows == 0 || src.bcols == 0) return 0;
+    return src.b0 * src.b1 <= kFew ? dequantize<kFew>(src, dst, ld, dt, status, stream, beside)
+                                   : dequantize<kAll>(src, dst, ld, dt, status, stream, beside);
+}
+
+int launch_gated_slopes(const GatedSlopeArgs &a, int *status, void *stream) {
+    if (a.dH.brows == 0 || a.dH.bcols == 0) return 0;
+    size_t n = (size_t)a.dH.b0 * a.dH.b1, h = 0;
+    if (a.want_H)
+        for (const auto &b : a.H.holders) h += b.size();
+    return (n > h ? n : h) <= kFew ? gated_slopes<kFew>(a, status, stream) : gated_slopes<kAll>(a, status, stream);
 }
 
 }  // namespace shmm

@@ -292,10 +292,11 @@ def _ptr_array(tensors: Sequence, what: str) -> ctypes.Array:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_handle(stream) -> Optional[int]:
+def _stream_handle(stream, dev: Optional[int] = None) -> Optional[int]:
+    """dev: the current device, where the caller has asked for it."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -365,11 +366,19 @@ def _rows_dtype(x, what: str = "x"):
     """(rows, cols, torch dtype, dtype code) of a 2-D fp32 or bf16 tensor."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("%s must be a 2-D CUDA tensor" % what)
-    if x.dtype is torch.bfloat16:
-        return x.shape[0], x.shape[1], x.dtype, BF16
-    if x.dtype is torch.float32:
-        return x.shape[0], x.shape[1], x.dtype, F32
-    raise ValueError("%s is %s, expected torch.float32 or torch.bfloat16" % (what, x.dtype))
+    (rows, cols), dtype = x.shape, x.dtype
+    if dtype is torch.bfloat16:
+        return rows, cols, dtype, BF16
+    if dtype is torch.float32:
+        return rows, cols, dtype, F32
+    raise ValueError("%s is %s, expected torch.float32 or torch.bfloat16" % (what, dtype))
+
+
+def _dense(x, what: str, dev: int) -> int:
+    """Address of a tensor of known shape and type: dense, on device `dev`."""
+    if x.get_device() == dev and x.is_contiguous():
+        return x.data_ptr()
+    return _refuse(x, what, x.shape, x.dtype)
 
 
 def _workspace(ws, dev: int):
@@ -844,9 +853,10 @@ def shmm_quantize(x, codes, scales, block_rows: int = 1, stream=None):
     if block_rows not in (1, SCALE_BLOCK):
         raise ValueError("block_rows must be 1 or %d" % SCALE_BLOCK)
     _check(lib().shmm_quantize(
-        rows, cols, code, block_rows, _tensor(x, "x", (rows, cols), dt, dev),
+        rows, cols, code, block_rows, _dense(x, "x", dev),
         _tensor(codes, "codes", (rows, cols), TORCH_DTYPES["e4m3"], dev),
-        _tensor(scales, "scales", scale_shape(rows, cols, block_rows), torch.float32, dev), _stream_handle(stream)))
+        _tensor(scales, "scales", scale_shape(rows, cols, block_rows), torch.float32, dev),
+        _stream_handle(stream, dev)))
 
 
 def shmm_dequantize(codes, scales, y, block_rows: int = 1, stream=None):
@@ -858,7 +868,7 @@ def shmm_dequantize(codes, scales, y, block_rows: int = 1, stream=None):
     _check(lib().shmm_dequantize(
         rows, cols, code, block_rows, _tensor(codes, "codes", (rows, cols), TORCH_DTYPES["e4m3"], dev),
         _tensor(scales, "scales", scale_shape(rows, cols, block_rows), torch.float32, dev),
-        _tensor(y, "y", (rows, cols), dt, dev), _stream_handle(stream)))
+        _dense(y, "y", dev), _stream_handle(stream, dev)))
 
 
 def shmm_reshard(mesh, spec_from, spec_to, rows: int, cols: int, dtype: str, src_r, dst_r, stream=None):
