@@ -3,12 +3,13 @@
 // shards in place, accumulators in TMEM, results by bulk tensor stores to every
 // rank that holds them.
 //
-// One kernel, five forms (X: the first operand, Y: the second):
+// One kernel, six forms (X: the first operand, Y: the second):
 //   kGated  X [M,Kd] . Y0, Y1 [Kd,N] bf16: both projections of a gated MLP
 //           block.  A 256-column accumulator is 128 columns of the gate's and the
 //           same 128 of the up projection's: the pair's even CTA loads Y0's
 //           columns, the odd one Y1's, so one MMA computes both and the product
 //           of the two needs no exchange.
+//   kGated8 the same where the projections are kept in 8 bits
 //   kNT     X [M,Kd] . Y [N,Kd]^T bf16, summed over terms: dA = dG . gate^T +
 //           dU . up^T is one contraction over both.
 //   kTN     X [Kd,M]^T . Y [Kd,N] bf16: a weight gradient.  With two Y (dG, dU),
@@ -18,24 +19,33 @@
 // Nothing is transposed in memory: the MMA reads either operand K-major or
 // MN-major from 128-byte-swizzled tiles.
 //
-// bf16 forms: 256 x 512 accumulators (two MMAs of N = 256 per K step, sharing
+// kGated, kNT, kTN: 256 x 512 accumulators (two MMAs of N = 256 per K step, sharing
 // X: the tile that moves fewest operand bytes per FLOP), all of TMEM.  The
 // contraction stays in one fp32 accumulator; results are bf16.  The epilogue
 // takes half a tile's accumulator into registers at once and hands the TMEM
 // back before it computes and stores, so the next tile's MMAs wait for a TMEM
-// read and not for the stores.
+// read and not for the stores.  8192 x 4096 by 2 x 4096 x 16384: kGated 1.05 to
+// 1.08 ms, 2.04 to 2.10 PFLOP/s (1.06 to 1.09 of the measured bf16 rate; 1.11 to
+// 1.16 ms where it keeps the projections in bf16), kNT and kTN 1.11 to 1.18 ms;
+// the tensor cores are busy for 93 to 96 % of the cycles, and the power cap sets
+// the clock of calls in a row.
 //
-// 8-bit forms: a k-block is 128 values, the scales' block.  Its four MMAs (K =
+// kNN8, kNT8: a k-block is 128 values, the scales' block.  Its four MMAs (K =
 // 32) fill one of two 256 x 256 accumulators; the epilogue warps read it and
 // add it times the two scales to fp32 sums in their registers (128 per thread)
 // while the next k-block fills the other.  No sum is longer than 128 products
 // in the tensor cores' adders, whose additions truncate.  Measured: 8192 x 8192
-// x 28672 in 1.84 ms, 2.09 PFLOP/s, 1.08 of the measured bf16 rate; 950 cycles
+// x 28672 in 1.84 ms, 2.09 PFLOP/s, 1.08 of the measured bf16 rate; 965 cycles
 // per k-block, where its MMAs take 512.  What bounds it is the way round one
-// accumulator, which two k-blocks share: MMAs, their commit and the signal (some
-// 1150 cycles from the first MMA), the epilogue's reads (570), the hand-back
-// (200).  TMEM has no room for a third; reading two or four pieces at a time,
-// packed FMAs and other splits of the reads changed nothing (1.84 to 1.87 ms).
+// accumulator, which two k-blocks share: 750 cycles from the issue of the MMAs to
+// the signal, some 900 until the last warp has read its part, 260 until the next
+// MMAs are issued.  TMEM has no room for a third; reading two or four pieces at a
+// time, packed FMAs and other splits of the reads changed nothing (1.84 to 1.87
+// ms), and 16 epilogue warps with half the columns each lose (1.97 ms; 8192 x
+// 8192 x 4096 285 us, with 8 warps 276).
+//
+// kGated8: 256 x 128 of either projection at a time, summed over several k-blocks
+// in TMEM and then in registers, as the 8-bit forms do (see Cfg::LEAD): 1.22 ms.
 //
 // Every wait is bounded; on expiry the kernel records SHMM_ERR_TIMEOUT, drains
 // its own loads and MMAs, frees TMEM and returns.

@@ -18,7 +18,10 @@
 // contract_pair.cu; four, because the way round one takes some 1000 cycles and a
 // k-block's MMAs of this width 128.
 //
-// Bound by HBM for few rows (each weight is read once).
+// Bound by HBM for few rows, where each weight is read once: gated, 4 rows, 4096 x
+// 2 x 16384 bf16 in 42 us (6.3 TB/s); 8 bits, 16 rows, 4096 x 16384 in 20 (128
+// tiles on 152 SMs).  Above that by the latency of a launch, a tile's loads and the
+// parts' join.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
