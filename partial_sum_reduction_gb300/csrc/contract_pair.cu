@@ -41,8 +41,9 @@
 // the signal, some 900 until the last warp has read its part, 260 until the next
 // MMAs are issued.  TMEM has no room for a third; reading two or four pieces at a
 // time, packed FMAs and other splits of the reads changed nothing (1.84 to 1.87
-// ms), and 16 epilogue warps with half the columns each lose (1.97 ms; 8192 x
-// 8192 x 4096 285 us, with 8 warps 276).
+// ms).  16 epilogue warps with half the columns each lose (1.97 ms; 8192 x 8192 x
+// 4096 285 us, with 8 warps 276), and so do four accumulators of 128 columns and
+// MMAs half as wide (2.30 ms; 355).
 //
 // kGated8: 256 x 128 of either projection at a time, summed over several k-blocks
 // in TMEM and then in registers, as the 8-bit forms do (see Cfg::LEAD): 1.22 ms.
