@@ -341,8 +341,7 @@ struct BackK {
 // 8192 x 4096 to bf16: 17 us, 6.0 TB/s.
 template <typename T, bool VEC, int CAP>
 __global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ BackK<CAP> k) {
-    if (!k.beside) shmm_pdl::pdl_wait();
-    shmm_pdl::pdl_release();
+    shmm_pdl::pdl_enter(k.beside);
     const int lane = threadIdx.x % 32;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     const int64_t cols = row < k.brows ? k.bcols : 0;
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(const __grid_constant__ 
             store8<VEC>(static_cast<T *>(k.dst) + at + c, k.bcols - c, v);
         }
     }
-    if (k.beside) shmm_pdl::pdl_wait();
+    shmm_pdl::pdl_end(k.beside);
 }
 
 // ---- the gated block's gradient, element by element ------------------------

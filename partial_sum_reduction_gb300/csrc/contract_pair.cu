@@ -68,6 +68,7 @@
 #include "e4m3.cuh"
 #include "gated_act.cuh"
 #include "pair.cuh"
+#include "pdl.cuh"
 #include "shmm_internal.h"
 #include "tensor_map.h"
 
@@ -406,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     const uint32_t tmem_base = *words;
     // The prologue above touches no global memory: it may overlap the end of
     // the kernel before in the stream.
-    if (!k.beside) grid_dependency_wait();
-    grid_launch_dependents();
+    shmm_pdl::pdl_enter(k.beside);
 
     if (warp < 4) {
         if constexpr (C::REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_pair_kernel(const __grid
     fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
-    if (k.beside) grid_dependency_wait();
+    shmm_pdl::pdl_end(k.beside);
 }
 
 // ---- host side --------------------------------------------------------------

@@ -192,8 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_simt_kernel(const __grid
     XPiece *xs = reinterpret_cast<XPiece *>(smem);
     YPiece *ys = reinterpret_cast<YPiece *>(xs + 2);  // [2][NY]
     float4 *sums = reinterpret_cast<float4 *>(ys + 2 * NY);  // [NY * 4][kThreads]
-    if (!k.beside) shmm_pdl::pdl_wait();
-    shmm_pdl::pdl_release();
+    shmm_pdl::pdl_enter(k.beside);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32 % 8, group = tid / 256;
     const int64_t m0 = (int64_t)blockIdx.x * TM;
     const int cb = blockIdx.y / k.n_per;                                    // result block column
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) contract_simt_kernel(const __grid
         }
         if (row_ok) put4(k.D, row, cb, cl, sum[0], k.status);
     }
-    if (k.beside) shmm_pdl::pdl_wait();
+    shmm_pdl::pdl_end(k.beside);
 }
 
 // ---- host side --------------------------------------------------------------

@@ -36,6 +36,7 @@
 #include "device_wait.cuh"
 #include "gated_act.cuh"
 #include "pair.cuh"
+#include "pdl.cuh"
 #include "shmm_internal.h"
 
 namespace {
@@ -183,8 +184,7 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
     __syncthreads();
     fence_after();
     const uint32_t tmem_base = *words;
-    if (!k.beside) grid_dependency_wait();
-    grid_launch_dependents();
+    shmm_pdl::pdl_enter(k.beside);
 
     const uint32_t x_bytes = (uint32_t)k.x_rows * 128;  // of a stage; the 16 KB of Y follow
     const uint32_t stage_bytes = x_bytes + 16384;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<FORM>::THREADS, Cfg<FORM>::CTAS)
     fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kCols) : "memory");
-    if (k.beside) grid_dependency_wait();
+    shmm_pdl::pdl_end(k.beside);
 }
 
 // ---- host side --------------------------------------------------------------

@@ -19,6 +19,18 @@ __device__ __forceinline__ void pdl_enter() {
     pdl_release();
 }
 
+// A kernel that may run beside the one before it, which waits for what both need
+// before it lets this one start: its start orders what this one reads, the fence
+// drops what an SM may still hold of it in L1.  pdl_end waits for the other.
+__device__ __forceinline__ void pdl_enter(bool beside) {
+    if (beside) __threadfence();
+    else pdl_wait();
+    pdl_release();
+}
+__device__ __forceinline__ void pdl_end(bool beside) {
+    if (beside) pdl_wait();
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {
