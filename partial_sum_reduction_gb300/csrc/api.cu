@@ -1531,7 +1531,7 @@ shmm_status_t shmm_scaled_backward(const shmm_plan_t *p, const void *const *dC_r
         if (dB_r) {
             shmm::ContractArgs a = contract_args(p, p->J, p->K, p->I);
             a.x_t = true;
-            a.beside = beside;
+            a.beside = beside && !p->max_sms;  // two products would take the limit twice
             a.X[0] = whole_operand(wide, p->I, p->J, SHMM_BF16);
             a.Y[0] = dC;
             a.D[0] = grid_result(p, SHMM_TENSOR_B, p->J, p->K, dB_r, SHMM_BF16);
@@ -1701,7 +1701,8 @@ shmm_status_t shmm_gated_backward(const shmm_plan_t *p, int activation, const vo
             shmm::ContractArgs a = contract_args(p, p->J, p->K, p->I);
             a.x_t = true;
             a.two = true;
-            a.beside = dA_r && p->I > 0 && p->J > 0 && p->K > 0;  // dA is under way
+            // dA is under way; with a limit on the SMs the two would take it twice
+            a.beside = dA_r && p->I > 0 && p->J > 0 && p->K > 0 && !p->max_sms;
             a.X[0] = grid_operand(p, SHMM_TENSOR_A, p->I, p->J, A_r, p->in_dt);
             a.Y[0] = dG;
             a.Y[1] = dU;

@@ -197,6 +197,41 @@ def test_what_follows_a_backward_pass_waits_for_both_products(kind, I, J, K, mon
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["gated", "scaled"])
+def test_two_products_take_an_sm_limit_once(kind):
+    """With a limit on the SMs a backward pass's products run one after the
+    other: both take as long as each alone, together.  (Side by side on SMs of
+    their own they would take the longer one's time, some half of it.)"""
+    I, J, K = 2048, 2048, 2048
+    scaled = kind == "scaled"
+    plan = s.Plan("{X:1}", "I,J", "J,K", "I,K", I, J, K, "e4m3" if scaled else "bf16", "bf16")
+    g = gen(5)
+    A, gate, up, dC = (normal(g, *e).bfloat16() for e in ((I, J), (J, K), (J, K), (I, K)))
+    new = lambda t: s.helpers.alloc(plan, t, dtype=torch.bfloat16)
+    dA, dgate, dup = new(s.TENSOR_A), new(s.TENSOR_B), new(s.TENSOR_B)
+    if scaled:
+        (a, a_s), (b, b_s), ws = s.helpers.quantize(A, 1), s.helpers.quantize(gate, 128), s.helpers.scaled_workspace(plan)
+        back = lambda x, w: plan.scaled_backward([dC], [a], [a_s], [b], [b_s], x, w, ws)
+    else:
+        saved, ws = s.helpers.gated_saved(plan, "bf16"), s.helpers.gated_workspace(plan)
+        plan.gated_forward([A], [gate], [up], new(s.TENSOR_C), saved=saved)
+        back = lambda x, w: plan.gated_backward([dC], [A], [gate], [up], saved, x, w, None if w is None else dup, ws)
+
+    def ms(x, w):
+        times = []
+        for _ in range(4):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            back(x, w)
+            e1.record()
+            e1.synchronize()
+            times.append(e0.elapsed_time(e1))
+        return min(times)
+    plan.set_sm_limit(8)
+    assert ms(dA, dgate) > 0.8 * (ms(dA, None) + ms(None, dgate))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("I,J,K", [(0, 128, 256), (16, 0, 256), (16, 128, 0)])
 def test_a_backward_pass_with_an_empty_dim(I, J, K):
     """Where a product is left out, the next one waits for what it needs."""
