@@ -669,8 +669,8 @@ shmm_status_t shmm_scaled_backward_workspace_size(const shmm_plan_t *plan, size_
  *   workspace device memory of >= shmm_scaled_backward_workspace_size() bytes,
  *             256-byte aligned; nothing in it needs to start at zero, and
  *             calls that overlap on the GPU need one each
- * The outputs share no byte with an input or one another (UNSUPPORTED).  No
- * rows: dB is zero.
+ * The outputs and the workspace share no byte with an input or one another
+ * (UNSUPPORTED).  No rows: dB is zero.
  * Errors: those of shmm_run_scaled, and NOMEM (workspace). */
 shmm_status_t shmm_scaled_backward(const shmm_plan_t *plan, const void *const *dC_r, const void *const *A_r,
                                    const float *const *A_scale_r, const void *const *B_r,
@@ -736,8 +736,9 @@ shmm_status_t shmm_gated_backward_workspace_size(const shmm_plan_t *plan, size_t
  *   workspace       device memory of >= shmm_gated_backward_workspace_size()
  *                   bytes, 256-byte aligned; nothing in it needs to start at
  *                   zero, and calls that overlap on the GPU need one each
- * All in the plan's type, rounded once.  The outputs share no byte with an
- * input or one another (UNSUPPORTED).  No rows: dgate and dup are zero.
+ * All in the plan's type, rounded once.  The outputs and the workspace share no
+ * byte with an input or one another (UNSUPPORTED).  No rows: dgate and dup are
+ * zero.
  * Errors: those of shmm_gated_forward, and NOMEM (workspace). */
 shmm_status_t shmm_gated_backward(const shmm_plan_t *plan, int activation, const void *const *dC_r,
                                   const void *const *A_r, const void *const *gate_r, const void *const *up_r,

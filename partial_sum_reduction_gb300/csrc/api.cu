@@ -1496,8 +1496,9 @@ shmm_status_t shmm_scaled_backward(const shmm_plan_t *p, const void *const *dC_r
             outs.push_back({"dB_r", spans(p, (const void *const *)dB_r, SHMM_TENSOR_B, SHMM_BF16)});
         }
         const ScaledScratch w = scaled_scratch(p);
-        if ((st = check_need(fn, workspace, workspace_bytes, w.bytes())) != SHMM_OK ||
-            (st = check_all_apart(fn, outs, ins)) != SHMM_OK)
+        if ((st = check_need(fn, workspace, workspace_bytes, w.bytes())) != SHMM_OK) return st;
+        if (w.bytes()) outs.push_back({"workspace", one_span(workspace, (int64_t)w.bytes())});
+        if ((st = check_all_apart(fn, outs, ins)) != SHMM_OK)
             return st;
         std::string err;
         int *status = status_ptr(&err);
@@ -1661,8 +1662,9 @@ shmm_status_t shmm_gated_backward(const shmm_plan_t *p, int activation, const vo
             outs.push_back({o.name, spans(p, (const void *const *)o.at, o.tensor, p->in_dt)});
         }
         const size_t half = gated_half(p);
-        if ((st = check_need(fn, workspace, workspace_bytes, 2 * half)) != SHMM_OK ||
-            (st = check_all_apart(fn, outs, ins)) != SHMM_OK)
+        if ((st = check_need(fn, workspace, workspace_bytes, 2 * half)) != SHMM_OK) return st;
+        if (half) outs.push_back({"workspace", one_span(workspace, (int64_t)(2 * half))});
+        if ((st = check_all_apart(fn, outs, ins)) != SHMM_OK)
             return st;
         std::string err;
         int *status = status_ptr(&err);

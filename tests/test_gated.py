@@ -430,6 +430,15 @@ def test_refused_pointers(call):
         assert call(p, saved=_saved(**kw)) == status
 
 
+def test_a_workspace_over_an_operand_or_a_result_is_refused():
+    p = _plan()
+    need = p.gated_workspace_size()
+    for at in (1 << 20, 1 << 24, 1 << 25, 1 << 27, 1 << 28, 1 << 29, 1 << 30, 1 << 32, 1 << 35):
+        assert _backward(p, ws=at) == m.ERR_UNSUPPORTED
+        assert _backward(p, ws=at - need + 256) == m.ERR_UNSUPPORTED
+    assert _backward(p, C=_arr((1 << 31) + need - 16)) == m.ERR_UNSUPPORTED
+
+
 def test_refused_overlaps_and_workspaces():
     p = _plan()
     for over in (1 << 20, 1 << 24, (1 << 25) + 256 * 128 * 2 - 16):

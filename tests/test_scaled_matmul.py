@@ -302,6 +302,15 @@ def test_refused_plans():
     assert e.value.status == m.ERR_DTYPE
 
 
+def test_a_workspace_over_an_operand_or_a_result_is_refused():
+    p = _plan()
+    need = p.scaled_workspace_size()
+    for at in (1 << 20, 1 << 24, 1 << 25, 1 << 26, 1 << 27, 1 << 28, 1 << 29):
+        assert _backward(p, ws=at) == m.ERR_UNSUPPORTED
+        assert _backward(p, ws=at - need + 256 & -256) == m.ERR_UNSUPPORTED
+    assert _backward(p, dB=_arr((1 << 30) + need - 16)) == m.ERR_UNSUPPORTED
+
+
 def test_refused_results_and_workspaces():
     p = _plan()
     assert _forward(p, C=None) == m.ERR_NULL and _forward(p, C=_arr((1 << 27) + 4)) == m.ERR_ALIGN
